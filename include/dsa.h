@@ -83,11 +83,18 @@ extern "C" {
 #define DSA_DEV_TIMEOUT 64         /* a bounded wait inside a kernel gave up             */
 #define DSA_DEV_BAD_PAGE 256      /* paged MLA: block past the table or page outside
                                       [0, n_pages); the row is skipped              */
+#define DSA_DEV_BAD_LENGTH 512    /* plan: negative or overflowing length, negative free_begin;
+                                      chunk: cu_new outside [0, T] or decreasing, or more new
+                                      tokens than seq_lens[b]                            */
+#define DSA_DEV_NO_PAGE 1024      /* plan: block past the table or free list used up; slot -1  */
+#define DSA_DEV_TOKEN_CAP 2048    /* plan: more new tokens than T; the rest wait               */
 #define DSA_DEV_HIST_MISMATCH 128  /* dsa_select: workspace histogram did not match the
                                       scores (workspace not zero-filled); exact fallback ran */
 
 #define DSA_KPOOL_MAX 8            /* module glm5next_dsa, Constants, KERNEL_MAX_KPOOL   */
 #define DSA_SELECT_K_MAX 4096
+#define DSA_PLAN_MAX_B 8192        /* sequences of one paged step                        */
+#define DSA_PLAN_MAX_T 1073741823  /* tokens of one dsa_paged_plan (2^30 - 1)            */
 
 /*
  * dsa_kpool_compress - LayerNorm the indexer keys and pool them kpool at a time.
@@ -274,6 +281,114 @@ int dsa_mla_paged_decode(const void* q_lat, const dsa_paged_kv* kv, const int32_
                          size_t ws_bytes, int32_t* status_dev, void* stream);
 size_t dsa_mla_paged_decode_workspace_size(int Q, int Hm, int L, int out_width, int dtype,
                                            int kv_dtype);
+
+/*
+ * The paged serving step.  A step of a serving loop holds B sequences with
+ * ctx_lens[b] tokens in the cache and new_lens[b] new ones (1 for a decode, more
+ * for a chunk of a prompt, 0 for one that waits).  dsa_paged_plan lays the step's
+ * token axis out and gives the new tokens their cache rows, dsa_paged_append
+ * writes their latent rows there, dsa_mla_paged_chunk attends to everything that
+ * they see (dsa_select and dsa_mla_paged_decode, with the plan's q_seq and q_pos,
+ * attend to a selection instead).  The pages have no counterpart: they read a
+ * block table that the engine around them keeps (module glm5next_dsa, Modules,
+ * attend: the paged decode).
+ *
+ * dsa_paged_plan - block table, lengths and slot maps of a step, on the GPU.
+ *
+ *   cu_new   [B+1]  sequence b's new tokens are rows cu_new[b] .. cu_new[b+1]-1
+ *                   of the step; their sum is cut at T (DSA_DEV_TOKEN_CAP), and
+ *                   the cut lengths n_b = cu_new[b+1] - cu_new[b] count below
+ *   seq_lens [B]    ctx_lens[b] + n_b (may be ctx_lens itself: in place)
+ *   block_table [B, max_pages]  blocks ceil(ctx_lens[b] / page_size) up to
+ *                   ceil(seq_lens[b] / page_size) - 1 get free_pages[free_begin[0]],
+ *                   free_pages[free_begin[0] + 1], ... in the order of b; every
+ *                   other entry is left as it was
+ *   free_end [1]    free_begin[0] + pages taken (may be free_begin itself)
+ *   q_seq, q_pos [T]  the sequence and the position of token t
+ *   kv_rows  [T]    its row in the paged cache: page * page_size + q_pos % page_size
+ *   key_rows [T]    row_base[b] + q_pos: its row in a contiguous cache whose
+ *                   sequence b begins at row_base[b] (the key and gate caches, as
+ *                   kv_rows of dsa_indexer_project); NULL with row_base NULL
+ * Rows at and behind cu_new[B]: q_seq 0, q_pos -1, kv_rows -1, key_rows -1 - they
+ * see no pool and no token, and are stored nowhere.
+ *
+ *   free_pages [n_free] distinct page numbers in [0, n_pages) that no sequence
+ *   holds; entries before free_begin[0] are taken.  A block without a page (list
+ *   used up, table too narrow) gets -1 where the table has the entry, its tokens
+ *   kv_rows -1, and the step DSA_DEV_NO_PAGE.
+ * Apart from the two in-place forms, no output may overlap an input or another
+ * output.  Supported: B <= DSA_PLAN_MAX_B, T <= DSA_PLAN_MAX_T.  One launch, no
+ * workspace.  B == 0 is a no-op that writes nothing.
+ * Device faults: DSA_DEV_BAD_LENGTH (a negative length, or one past 2^31 - 1
+ * tokens: no new tokens for that sequence, and 0 cached ones where ctx_lens[b] is
+ * negative; a negative free_begin: no free pages), DSA_DEV_TOKEN_CAP,
+ * DSA_DEV_NO_PAGE, DSA_DEV_BAD_PAGE (a page number outside [0, n_pages) in
+ * free_pages or in the table: as no page).
+ */
+int dsa_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* free_pages,
+                   const int32_t* free_begin, const int32_t* row_base, int B, int T, int n_free,
+                   int n_pages, int page_size, int max_pages, int32_t* block_table,
+                   int32_t* seq_lens, int32_t* cu_new, int32_t* q_seq, int32_t* q_pos,
+                   int32_t* kv_rows, int32_t* key_rows, int32_t* free_end, int32_t* status_dev,
+                   void* stream);
+
+/*
+ * dsa_paged_append - write new latent rows into the paged cache.
+ *
+ *   kv_new  [T, L] activation dtype;  kv_rows [T] int32 cache rows (from
+ *   dsa_paged_plan); a negative entry drops the row
+ *   pages   [n_pages * page_size, L] kv_dtype DSA_BF16, DSA_F32 or DSA_FP8_E4M3
+ *   row_scale [n_pages * page_size] fp32 (DSA_FP8_E4M3 only, else NULL)
+ * bf16 and fp32 rows are rounded to nearest; an E4M3 row is stored as
+ *   row_scale[r] = max|x| / 448 over the row's finite elements (1 if that is 0),
+ *   code = x / row_scale[r], rounded to nearest, at most 448 in magnitude; a
+ *   NaN or infinite element becomes the NaN code.
+ * Other rows of the cache are left as they were.  Two tokens with the same cache
+ * row leave it with elements of either and the scale of either.
+ * Supported: L a multiple of 8 up to 1024, any pairing of the dtypes.  16-byte
+ * aligned kv_new and pages.
+ * Device faults: DSA_DEV_BAD_PAGE (kv_rows[t] past the cache: the row is dropped).
+ */
+int dsa_paged_append(const void* kv_new, const int32_t* kv_rows, int T, int L, int dtype,
+                     void* pages, float* row_scale, int n_pages, int page_size, int kv_dtype,
+                     int32_t* status_dev, void* stream);
+
+/*
+ * dsa_mla_paged_chunk - NoPE MLA of a step's new tokens over the paged cache:
+ * causal, with an optional sliding window beside which the first tokens stay
+ * visible (sinks).
+ *
+ * Source: module glm5next_dsa, "Traps carried from Slice 8" (NoPE: no rotary
+ * slice) and Constants, MASKED_ATTN_MAX_KEYS (dense masked attention, there an
+ * oracle only).  Row cu_new[b] + i of q_lat (i < n_b = cu_new[b+1] - cu_new[b])
+ * is the token at position p = seq_lens[b] - n_b + i of sequence b: the new
+ * tokens are the last of their sequence, and their rows are in the cache.  It sees
+ * position t when t <= p and (window == 0 or t > p - window or t < sinks):
+ *   z_t = sm_scale * <q_lat[row, h, :], c_t>
+ *   out[row, h, :] = sum_t softmax(z)_t * c_t;  lse[row, h] = log(sum_t exp(z_t))
+ * Nothing seen gives out = 0 and lse = -inf.  What a token does not see does not
+ * reach its output, whatever the cache holds there.  Rows of out and lse behind
+ * cu_new[B] are left as they were.
+ *
+ *   q_lat [T, Hm, L] activation dtype; kv as for dsa_mla_paged_decode (seq_lens
+ *   counts the new tokens); cu_new [B+1] int32, not decreasing, within [0, T]
+ *   window >= 0 (0: no window), sinks >= 0 (without a window: no effect)
+ *   out [T, Hm, L] activation dtype; lse [T, Hm] fp32 (may be NULL)
+ *   workspace: dsa_mla_paged_chunk_workspace_size(...) bytes, 16-byte aligned, no
+ *   initial value; calls in flight at the same time must not share one
+ * The lengths are read on the GPU: a captured call follows them when replayed.
+ * Outputs are deterministic.
+ * Supported: L multiple of 8 up to 1024 and Hm up to 128 in both dtypes, with
+ * pages of any kv_dtype; T * Hm < 2^31, B <= DSA_PLAN_MAX_B.
+ * Device faults: DSA_DEV_BAD_PAGE (a visible position past the table or on a page
+ * outside [0, n_pages): skipped), DSA_DEV_BAD_LENGTH (rows without a position see
+ * nothing; cu_new is cut to [0, T] and taken as empty where it decreases).
+ */
+int dsa_mla_paged_chunk(const void* q_lat, const dsa_paged_kv* kv, const int32_t* cu_new, int T,
+                        int B, int Hm, int L, int window, int sinks, float sm_scale, int dtype,
+                        void* out, float* lse, void* workspace, size_t ws_bytes,
+                        int32_t* status_dev, void* stream);
+size_t dsa_mla_paged_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype);
 
 /*
  * dsa_select - index_scores -> topk_pools -> expand_selection in one call.

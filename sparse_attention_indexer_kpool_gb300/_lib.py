@@ -55,6 +55,12 @@ SIGNATURES = {
                              + [c_int] * 5 + [c_float, c_int] + [c_void_p] * 3 + [c_size_t]
                              + [c_void_p] * 2),
     "dsa_mla_paged_decode_workspace_size": (c_size_t, [c_int] * 6),
+    "dsa_paged_plan": (c_int, [c_void_p] * 5 + [c_int] * 6 + [c_void_p] * 10),
+    "dsa_paged_append": (c_int, [c_void_p] * 2 + [c_int] * 3 + [c_void_p] * 2 + [c_int] * 3
+                         + [c_void_p] * 2),
+    "dsa_mla_paged_chunk": (c_int, [c_void_p, ctypes.POINTER(PagedKv), c_void_p] + [c_int] * 6
+                            + [c_float, c_int] + [c_void_p] * 3 + [c_size_t] + [c_void_p] * 2),
+    "dsa_mla_paged_chunk_workspace_size": (c_size_t, [c_int] * 5),
     "dsa_select": (c_int, [c_void_p, c_void_p, c_float, c_void_p, c_int] + [c_void_p] * 6
                    + [c_int] * 9 + [c_void_p] * 4 + [c_size_t] + [c_void_p] * 2),
     "dsa_select_workspace_size": (c_size_t, [c_int, c_int, c_int]),

@@ -139,6 +139,69 @@ int check_mla_paged(const void* q_lat, const dsa_paged_kv* kv, const int32_t* q_
   return DSA_OK;
 }
 
+int check_plan(const dsa::PlanArgs& a) {
+  if (a.B < 0 || a.T < 0 || a.n_free < 0) return DSA_ERR_INVALID_ARG;
+  if (a.n_pages < 1 || a.page_size < 1 || a.max_pages < 1) return DSA_ERR_INVALID_ARG;
+  if (a.T > 0 && (a.row_base == nullptr) != (a.key_rows == nullptr)) return DSA_ERR_INVALID_ARG;
+  if ((long long)a.n_pages * a.page_size > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
+  if (a.B > DSA_PLAN_MAX_B || a.T > DSA_PLAN_MAX_T) return DSA_ERR_UNSUPPORTED;
+  if (a.B == 0) return kNoWork;
+  if (!a.ctx_lens || !a.new_lens || !a.free_begin || !a.block_table || !a.seq_lens || !a.cu_new ||
+      !a.free_end || (a.n_free > 0 && !a.free_pages))
+    return DSA_ERR_INVALID_ARG;
+  if (a.T > 0 && (!a.q_seq || !a.q_pos || !a.kv_rows)) return DSA_ERR_INVALID_ARG;
+  const void* p[] = {a.ctx_lens, a.new_lens, a.free_pages, a.free_begin, a.row_base,
+                     a.block_table, a.seq_lens, a.cu_new, a.q_seq, a.q_pos, a.kv_rows,
+                     a.key_rows, a.free_end, a.status};
+  for (const void* x : p)
+    if (!aligned(x, 4)) return DSA_ERR_MISALIGNED;
+  return DSA_OK;
+}
+
+int check_append(const void* kv_new, const int32_t* kv_rows, int T, int L, int dtype,
+                 int kv_dtype, const void* pages, const float* row_scale, int n_pages,
+                 int page_size, const int32_t* status_dev) {
+  if (T < 0 || L < 1 || n_pages < 1 || page_size < 1) return DSA_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype)) return DSA_ERR_INVALID_ARG;
+  if (!dtype_ok(kv_dtype) && kv_dtype != DSA_FP8_E4M3) return DSA_ERR_INVALID_ARG;
+  if ((kv_dtype == DSA_FP8_E4M3) != (row_scale != nullptr)) return DSA_ERR_INVALID_ARG;
+  if (L % 8 != 0 || L > 1024) return DSA_ERR_UNSUPPORTED;
+  if ((long long)n_pages * page_size > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
+  if (T == 0) return kNoWork;
+  if (!kv_new || !kv_rows || !pages) return DSA_ERR_INVALID_ARG;
+  if (!aligned(kv_new, 16) || !aligned(pages, 16) || !aligned(kv_rows, 4) ||
+      !aligned(row_scale, 4) || !aligned(status_dev, 4))
+    return DSA_ERR_MISALIGNED;
+  return DSA_OK;
+}
+
+int check_chunk(const void* q_lat, const dsa_paged_kv* kv, const int32_t* cu_new, int T, int B,
+                int Hm, int L, int window, int sinks, float sm_scale, int dtype, const void* out,
+                const float* lse, const void* workspace, size_t ws_bytes,
+                const int32_t* status_dev) {
+  if (!kv || T < 0 || B < 0 || Hm < 1 || L < 1 || window < 0 || sinks < 0)
+    return DSA_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || !isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+  const int kd = kv->kv_dtype;
+  if (kd != DSA_BF16 && kd != DSA_F32 && kd != DSA_FP8_E4M3) return DSA_ERR_INVALID_ARG;
+  if (kv->n_pages < 1 || kv->page_size < 1 || kv->max_pages < 1) return DSA_ERR_INVALID_ARG;
+  if ((kd == DSA_FP8_E4M3) != (kv->row_scale != nullptr)) return DSA_ERR_INVALID_ARG;
+  if (L % 8 != 0 || L > 1024 || Hm > 128) return DSA_ERR_UNSUPPORTED;
+  if ((long long)kv->n_pages * kv->page_size > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
+  if ((long long)T * Hm > 0x7fffffffLL || B > DSA_PLAN_MAX_B) return DSA_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0) return kNoWork;
+  if (!q_lat || !kv->pages || !kv->block_table || !kv->seq_lens || !cu_new || !out)
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned(q_lat, 16) || !aligned(kv->pages, 16) || !aligned(out, 16) ||
+      !aligned(kv->block_table, 4) || !aligned(kv->seq_lens, 4) || !aligned(cu_new, 4) ||
+      !aligned(kv->row_scale, 4) || !aligned(lse, 4) || !aligned(status_dev, 4))
+    return DSA_ERR_MISALIGNED;
+  const size_t need = dsa::mla_chunk_workspace_size(T, Hm, L, dtype, kd);
+  if (need > 0 && (!workspace || ws_bytes < need)) return DSA_ERR_WORKSPACE;
+  if (workspace && !aligned(workspace, 16)) return DSA_ERR_MISALIGNED;
+  return DSA_OK;
+}
+
 }  // namespace
 
 namespace dsa {
@@ -414,6 +477,49 @@ int dsa_decode_layer(const dsa_decode_layer_args* a, void* stream) {
                                          a->token_ids, a->Q, a->B, a->Hm, a->L, a->out_width,
                                          a->sm_scale, a->dtype, a->out, a->lse, a->ws_mla,
                                          a->ws_mla_bytes, a->status_dev, st, true);
+}
+
+int dsa_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* free_pages,
+                   const int32_t* free_begin, const int32_t* row_base, int B, int T, int n_free,
+                   int n_pages, int page_size, int max_pages, int32_t* block_table,
+                   int32_t* seq_lens, int32_t* cu_new, int32_t* q_seq, int32_t* q_pos,
+                   int32_t* kv_rows, int32_t* key_rows, int32_t* free_end, int32_t* status_dev,
+                   void* stream) {
+  const dsa::PlanArgs a{ctx_lens, new_lens, free_pages, free_begin, row_base, B, T, n_free,
+                        n_pages, page_size, max_pages, block_table, seq_lens, cu_new, q_seq,
+                        q_pos, kv_rows, key_rows, free_end, status_dev};
+  const int r = check_plan(a);
+  if (r != DSA_OK) return r == kNoWork ? DSA_OK : r;
+  return dsa::launch_paged_plan(a, as_stream(stream));
+}
+
+int dsa_paged_append(const void* kv_new, const int32_t* kv_rows, int T, int L, int dtype,
+                     void* pages, float* row_scale, int n_pages, int page_size, int kv_dtype,
+                     int32_t* status_dev, void* stream) {
+  const int r = check_append(kv_new, kv_rows, T, L, dtype, kv_dtype, pages, row_scale, n_pages,
+                             page_size, status_dev);
+  if (r != DSA_OK) return r == kNoWork ? DSA_OK : r;
+  return dsa::launch_paged_append(kv_new, kv_rows, T, L, dtype, kv_dtype, pages, row_scale,
+                                  n_pages * page_size, status_dev, as_stream(stream));
+}
+
+size_t dsa_mla_paged_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype) {
+  if (T <= 0 || Hm <= 0 || L <= 0 || !dtype_ok(dtype)) return 0;
+  return dsa::mla_chunk_workspace_size(T, Hm, L, dtype, kv_dtype);
+}
+
+int dsa_mla_paged_chunk(const void* q_lat, const dsa_paged_kv* kv, const int32_t* cu_new, int T,
+                        int B, int Hm, int L, int window, int sinks, float sm_scale, int dtype,
+                        void* out, float* lse, void* workspace, size_t ws_bytes,
+                        int32_t* status_dev, void* stream) {
+  const int r = check_chunk(q_lat, kv, cu_new, T, B, Hm, L, window, sinks, sm_scale, dtype, out,
+                            lse, workspace, ws_bytes, status_dev);
+  if (r != DSA_OK) return r == kNoWork ? DSA_OK : r;
+  const dsa::PagedKv pk{kv->pages,    kv->row_scale, kv->block_table, kv->seq_lens,
+                        kv->n_pages,  kv->page_size, kv->max_pages,   kv->kv_dtype};
+  const dsa::ChunkArgs a{q_lat, pk, cu_new, T, B, Hm, L, window, sinks, sm_scale, dtype, out,
+                         lse, status_dev};
+  return dsa::launch_mla_chunk(a, workspace, as_stream(stream));
 }
 
 }  // extern "C"

@@ -335,6 +335,31 @@ int launch_mla_selected_decode(const void* q_lat, const void* kv, const int32_t*
                                int Hm, int L, int out_width, float sm_scale, int dtype, void* out,
                                float* lse, void* workspace, size_t ws_bytes, int32_t* status_dev,
                                cudaStream_t stream, bool early = false);
+// ---- the paged serving step
+struct PlanArgs {  // dsa_paged_plan after validation
+  const int32_t *ctx_lens, *new_lens, *free_pages, *free_begin, *row_base;
+  int B, T, n_free, n_pages, page_size, max_pages;
+  int32_t *block_table, *seq_lens, *cu_new, *q_seq, *q_pos, *kv_rows, *key_rows, *free_end;
+  int32_t* status;
+};
+int launch_paged_plan(const PlanArgs& a, cudaStream_t stream);
+int launch_paged_append(const void* kv_new, const int32_t* kv_rows, int T, int L, int dtype,
+                        int kv_dtype, void* pages, float* row_scale, int n_rows,
+                        int32_t* status_dev, cudaStream_t stream);
+// attention of a chunk of new tokens over the paged cache
+struct ChunkArgs {
+  const void* q_lat;
+  PagedKv kv;
+  const int32_t* cu_new;
+  int T, B, Hm, L, window, sinks;
+  float sm_scale;
+  int dtype;
+  void* out;
+  float* lse;
+  int32_t* status;
+};
+size_t mla_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype);
+int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream);
 }  // namespace dsa
 
 #define DSA_LAUNCH_CHECK()                          \

@@ -17,6 +17,7 @@ DSA_BF16, DSA_F32, DSA_FP8_E4M3 = 0, 1, 2
 DEV_BAD_TOKEN, DEV_POOL_OVERFLOW, DEV_POOL_UNCOVERED = 1, 2, 4
 DEV_BAD_POOL_ID, DEV_BAD_QSEQ, DEV_POOL_RANGE, DEV_TIMEOUT = 8, 16, 32, 64
 DEV_HIST_MISMATCH, DEV_BAD_PAGE = 128, 256
+DEV_BAD_LENGTH, DEV_NO_PAGE, DEV_TOKEN_CAP = 512, 1024, 2048
 
 
 class DsaError(RuntimeError):
@@ -180,6 +181,93 @@ def dsa_mla_paged_decode(q_lat, pages, row_scale, block_table, seq_lens, page_si
         0 if workspace is None else workspace.numel(), _ptr(status, torch.int32, "status"),
         _stream(stream))
     _check("dsa_mla_paged_decode", code)
+
+
+def _numel(t, n, name):
+    """The buffer's length is part of the call's geometry: the library cannot see it."""
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    return t
+
+
+def dsa_paged_plan(ctx_lens, new_lens, free_pages, free_begin, n_pages, page_size, block_table,
+                   seq_lens, cu_new, q_seq, q_pos, kv_rows, free_end, row_base=None,
+                   key_rows=None, status=None, stream=None):
+    """Block table, lengths and slot maps of a step from the requests' lengths: ``ctx_lens`` and
+    ``new_lens`` [B], ``free_pages`` [n_free], ``free_begin`` [1], ``block_table`` [B, max_pages]
+    (extended in place), outputs ``seq_lens`` [B] (may be ``ctx_lens``), ``cu_new`` [B + 1],
+    ``q_seq``, ``q_pos``, ``kv_rows`` [T] (T fixes the step's capacity), ``free_end`` [1] (may be
+    ``free_begin``); ``row_base`` [B] with ``key_rows`` [T] as well, or neither.  All int32."""
+    i32 = torch.int32
+    B, T = ctx_lens.numel(), q_seq.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    for t, n, name in ((new_lens, B, "new_lens"), (free_begin, 1, "free_begin"),
+                       (row_base, B, "row_base"), (seq_lens, B, "seq_lens"),
+                       (cu_new, B + 1, "cu_new"), (q_pos, T, "q_pos"), (kv_rows, T, "kv_rows"),
+                       (key_rows, T, "key_rows"), (free_end, 1, "free_end")):
+        _numel(t, n, name)
+    code = _lib.load().dsa_paged_plan(
+        _ptr(ctx_lens, i32, "ctx_lens"), _ptr(new_lens, i32, "new_lens"),
+        _ptr(free_pages, i32, "free_pages"), _ptr(free_begin, i32, "free_begin"),
+        _ptr(row_base, i32, "row_base"), B, T, free_pages.numel(), int(n_pages), int(page_size),
+        block_table.shape[1], _ptr(block_table, i32, "block_table"),
+        _ptr(seq_lens, i32, "seq_lens"), _ptr(cu_new, i32, "cu_new"), _ptr(q_seq, i32, "q_seq"),
+        _ptr(q_pos, i32, "q_pos"), _ptr(kv_rows, i32, "kv_rows"), _ptr(key_rows, i32, "key_rows"),
+        _ptr(free_end, i32, "free_end"), _ptr(status, i32, "status"), _stream(stream))
+    _check("dsa_paged_plan", code)
+
+
+def dsa_paged_append(kv_new, kv_rows, pages, row_scale=None, status=None, stream=None):
+    """Write ``kv_new`` [T, L] to the rows ``kv_rows`` [T] (negative: dropped) of ``pages``
+    [n_pages * page_size, L] (bf16, fp32, or float8_e4m3fn / uint8 codes with ``row_scale``
+    [n_pages * page_size] fp32)."""
+    if kv_new.dim() != 2 or pages.dim() != 2 or pages.shape[1] != kv_new.shape[1]:
+        raise ValueError("kv_new must be [T, L] and pages [n_pages * page_size, L]")
+    T, L = kv_new.shape
+    _numel(kv_rows, T, "kv_rows")
+    _numel(row_scale, pages.shape[0], "row_scale")
+    code = _lib.load().dsa_paged_append(
+        _ptr(kv_new, kv_new.dtype, "kv_new"), _ptr(kv_rows, torch.int32, "kv_rows"), T, L,
+        _dtype_tag(kv_new), _ptr(pages, pages.dtype, "pages"),
+        _ptr(row_scale, torch.float32, "row_scale"), pages.shape[0], 1, _kv_tag(pages),
+        _ptr(status, torch.int32, "status"), _stream(stream))
+    _check("dsa_paged_append", code)
+
+
+def mla_paged_chunk_workspace_bytes(q_lat, pages) -> int:
+    T, Hm, L = q_lat.shape
+    return int(_lib.load().dsa_mla_paged_chunk_workspace_size(T, Hm, L, _dtype_tag(q_lat),
+                                                              _kv_tag(pages)))
+
+
+def dsa_mla_paged_chunk(q_lat, pages, row_scale, block_table, seq_lens, page_size, cu_new, window,
+                        sinks, sm_scale, out, lse, workspace=None, status=None, stream=None):
+    """Causal attention of the step's new tokens (rows ``cu_new[b]`` .. of ``q_lat`` [T, Hm, L],
+    the last tokens of sequence b) over the paged cache; ``window`` 0 sees everything before,
+    ``sinks`` first tokens stay visible beside a window.  ``pages``, ``row_scale``, ``block_table``
+    and ``seq_lens`` as for ``dsa_mla_paged_decode``."""
+    T, Hm, L = q_lat.shape
+    if pages.dim() != 2 or pages.shape[1] != L or pages.shape[0] % int(page_size) != 0:
+        raise ValueError("pages must be [n_pages * page_size, L]")
+    if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0]:
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    B = block_table.shape[0]
+    for t, n, name in ((row_scale, pages.shape[0], "row_scale"), (cu_new, B + 1, "cu_new"),
+                       (out, T * Hm * L, "out"), (lse, T * Hm, "lse")):
+        _numel(t, n, name)
+    act = q_lat.dtype
+    kv = _lib.PagedKv(_ptr(pages, pages.dtype, "pages"), _ptr(row_scale, torch.float32, "row_scale"),
+                      _ptr(block_table, torch.int32, "block_table"),
+                      _ptr(seq_lens, torch.int32, "seq_lens"), pages.shape[0] // int(page_size),
+                      int(page_size), block_table.shape[1], _kv_tag(pages))
+    code = _lib.load().dsa_mla_paged_chunk(
+        _ptr(q_lat, act, "q_lat"), ctypes.byref(kv), _ptr(cu_new, torch.int32, "cu_new"), T, B, Hm,
+        L, int(window), int(sinks), float(sm_scale), _dtype_tag(q_lat), _ptr(out, act, "out"),
+        _ptr(lse, torch.float32, "lse"), _ptr(workspace, torch.uint8, "workspace"),
+        0 if workspace is None else workspace.numel(), _ptr(status, torch.int32, "status"),
+        _stream(stream))
+    _check("dsa_mla_paged_chunk", code)
 
 
 def select_workspace_bytes(Q, P_ld, select_k) -> int:

@@ -1,0 +1,412 @@
+"""The paged serving step on the GPU: the plan against integers, the append against
+fp32 divisions, the chunk attention against 64 bits within the bounds of its
+roundings, and the three together with the selection that they feed."""
+import math
+import random
+
+import pytest
+import torch
+
+from sparse_attention_indexer_kpool_gb300 import ops
+from tests import _paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+# ---------------------------------------------------------------- plan
+def run_plan(ctx, new, free, begin, n_pages, ps, table, T, base=None, in_place=False):
+    c, fb = i32(ctx), i32([begin])
+    tab = i32(table)
+    B = len(ctx)
+    e = lambda n: torch.full((n,), -77, dtype=torch.int32, device=DEV)  # noqa: E731
+    lens, end = (c, fb) if in_place else (e(B), e(1))
+    out = dict(seq_lens=lens, cu_new=e(B + 1), q_seq=e(T), q_pos=e(T), kv_rows=e(T))
+    keys = e(T) if base is not None else None
+    st = i32([0])
+    ops.dsa_paged_plan(c, i32(new), i32(free), fb, n_pages, ps, tab, out["seq_lens"],
+                       out["cu_new"], out["q_seq"], out["q_pos"], out["kv_rows"], end,
+                       row_base=None if base is None else i32(base), key_rows=keys, status=st)
+    torch.cuda.synchronize()
+    got = {k: v.tolist() for k, v in out.items()}
+    got |= dict(table=tab.tolist(), free_end=end.item())
+    if keys is not None:
+        got["key_rows"] = keys.tolist()
+    return got, st.item()
+
+
+def check_plan(*args, **kw):
+    in_place = kw.pop("in_place", False)
+    ctx, new, free, begin, n_pages, ps, table, T = args
+    got, st = run_plan(*args, **kw, in_place=in_place)
+    want, want_st = ref.plan(ctx, new, free, begin, n_pages, ps, [list(r) for r in table], T, **kw)
+    for k in got:
+        assert got[k] == want[k], k
+    assert st == want_st
+
+
+def random_plan(seed, B, ps, new_hi, ctx_hi, slack, width_cut=0):
+    rng = random.Random(seed)
+    ctx = [rng.randint(0, ctx_hi) for _ in range(B)]
+    new = [rng.randint(0, new_hi) for _ in range(B)]
+    have = [-(-c // ps) for c in ctx]
+    after = [-(-(c + n) // ps) for c, n in zip(ctx, new)]
+    width = max(1, max(after) - width_cut)
+    n_pages = sum(have) + sum(after) + 50
+    ids = list(range(n_pages))
+    rng.shuffle(ids)
+    table, at = [], 0
+    for h in have:
+        table.append((ids[at:at + h] + [-1] * width)[:width])
+        at += h
+    free = ids[at:at + 3 + sum(after) - sum(have) + slack]
+    base = [rng.randint(0, 10 ** 6) for _ in range(B)]
+    return ctx, new, free, 3, n_pages, ps, table, sum(new), base
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,ps,new_hi,ctx_hi,T_off", [
+    (1, 1, 1, 0, 0), (1, 64, 5000, 300, 9), (3, 7, 40, 100, 0), (64, 64, 1, 65000, 0),
+    (255, 16, 3, 900, 100), (256, 5, 30, 60, -11), (1025, 16, 4, 200, 1), (8192, 48, 2, 100, 3),
+    (300, 16, 200, 50, 5000)])
+def test_plan(B, ps, new_hi, ctx_hi, T_off, in_place):
+    ctx, new, free, begin, n_pages, ps, table, T, base = random_plan(B, B, ps, new_hi, ctx_hi, 5)
+    T = max(0, T + T_off)
+    check_plan(ctx, new, free, begin, n_pages, ps, table, T, base=base, in_place=in_place)
+    check_plan(ctx, new, free, begin, n_pages, ps, table, T, in_place=in_place)
+
+
+def test_plan_with_nothing_new_and_no_room():
+    check_plan([5, 0, 9], [0, 0, 0], [], 0, 4, 4, [[0, 1, -1], [-1] * 3, [2, 3, 0]], 0)
+    check_plan([5, 0, 9], [0, 0, 0], [1], 0, 4, 4, [[0, 1, -1], [-1] * 3, [2, 3, 0]], 5)
+    check_plan([5, 0, 9], [3, 2, 2], [3], 0, 4, 4, [[0, 1, -1], [-1] * 3, [2, 3, 0]], 0)
+
+
+def test_plan_faults_are_flagged_and_contained():
+    ctx, new, free, begin, n_pages, ps, table, T, base = random_plan(5, 40, 8, 20, 60, -30)
+    check_plan(ctx, new, free, begin, n_pages, ps, table, T, base=base)          # list used up
+    check_plan(ctx, new, free, -4, n_pages, ps, table, T)                        # no list at all
+    check_plan(ctx, new, free, len(free) + 9, n_pages, ps, table, T)             # begins past it
+    ctx, new, free, begin, n_pages, ps, table, T, base = random_plan(6, 40, 8, 20, 60, 5, 3)
+    check_plan(ctx, new, free, begin, n_pages, ps, table, T, base=base)          # narrow table
+    ctx, new, free, begin, n_pages, ps, table, T, base = random_plan(7, 9, 8, 20, 60, 5)
+    bad = list(ctx), list(new)
+    bad[1][2], bad[0][4], bad[0][5], bad[1][6] = -3, -1, 2 ** 31 - 2, 2 ** 31 - 1
+    check_plan(bad[0], bad[1], free, begin, n_pages, ps, table, T)
+    for k in range(begin, len(free), 2):
+        free[k] = [-1, n_pages, -2 ** 31, 2 ** 31 - 1][k % 4]
+    for row in table[::2]:
+        row[0:2] = [n_pages + 3, -9][:len(row)]
+    check_plan(ctx, new, free, begin, n_pages, ps, table, T)
+
+
+# ---------------------------------------------------------------- append
+@pytest.mark.parametrize("L", [8, 64, 248, 512, 520, 1024])
+@pytest.mark.parametrize("act", [BF, F32])
+@pytest.mark.parametrize("kv", [BF, F32, F8])
+def test_append(L, act, kv):
+    g = torch.Generator(device=DEV).manual_seed(L)
+    for T, n_rows in ((1, 5), (77, 200)):
+        x = torch.randn((T, L), generator=g, device=DEV).to(act)
+        x *= torch.logspace(-30, 30, T, device=DEV)[:, None].to(act)   # every scale
+        if T > 1:
+            x[3] = 0
+            x[4, 1], x[5, 0], x[5, L - 1], x[6] = math.nan, math.inf, -math.inf, math.nan
+            x[7] = 1e-44 if act == F32 else 0
+            x[8, 2] = -x[8].abs().max() * 2                            # the largest is negative
+        rows = torch.randperm(n_rows, generator=g, device=DEV)[:T].to(torch.int32)
+        if T > 1:
+            rows[10:20] = -1
+            rows[30], rows[31] = n_rows, 2 ** 31 - 1                   # dropped and flagged
+        pages = torch.randn((n_rows, L), generator=g, device=DEV).to(kv)
+        scale = torch.rand(n_rows, generator=g, device=DEV) if kv == F8 else None
+        want, want_s = pages.clone(), None if scale is None else scale.clone()
+        live = (rows >= 0) & (rows < n_rows)
+        at = rows[live].long()
+        if kv == F8:
+            codes, s = ref.quantise(x[live])
+            want.view(torch.uint8)[at] = codes.view(torch.uint8)
+            want_s[at] = s
+        else:
+            want[at] = x[live].to(kv)
+        st = i32([0])
+        ops.dsa_paged_append(x, rows, pages, scale, status=st)
+        torch.cuda.synchronize()
+        assert st.item() == (ops.DEV_BAD_PAGE if T > 1 else 0)
+        assert torch.equal(torch.nan_to_num(pages.float(), nan=12345.0),
+                           torch.nan_to_num(want.float(), nan=12345.0))
+        if kv == F8:
+            assert torch.equal(scale, want_s)
+
+
+# ---------------------------------------------------------------- chunk attention
+def make(lens, new, *, Hm=64, L=512, act=BF, kv=BF, ps=64, seed=0, pad=3, q_std=1.0,
+         hidden=math.nan):
+    """A paged cache whose rows outside the sequences hold ``hidden``."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    blocks = [-(-max(t, 0) // ps) for t in lens]
+    n_pages = sum(blocks) + 2
+    perm = torch.randperm(n_pages, generator=g, device=DEV).to(torch.int32)
+    table = torch.full((len(lens), max(blocks + [1]) + 1), -1, dtype=torch.int32, device=DEV)
+    n = n_pages * ps
+    x = torch.randn((n, L), generator=g, device=DEV)
+    used = torch.zeros(n, dtype=torch.bool, device=DEV)
+    at = 0
+    for b, t in enumerate(lens):
+        table[b, :blocks[b]] = perm[at:at + blocks[b]]
+        at += blocks[b]
+        p = torch.arange(max(t, 0), device=DEV)
+        used[table[b].long()[p // ps] * ps + p % ps] = True
+    x[~used] = hidden
+    if kv == F8:
+        pages, scale = ref.quantise(x)
+        scale[~used] = hidden
+    else:
+        pages, scale = x.to(kv), None
+    T = sum(new) + pad
+    cu = [0]
+    for k in new:
+        cu.append(cu[-1] + k)
+    q = (torch.randn((T, Hm, L), generator=g, device=DEV) * q_std).to(act)
+    return dict(q=q, pages=pages, scale=scale, table=table, lens=i32(lens), cu=i32(cu), ps=ps,
+                sm=1.0 / math.sqrt(L), T=T)
+
+
+def attend(s, window=0, sinks=0, stream=None, ws=None, out=None, lse=None):
+    T, Hm, L = s["q"].shape
+    out = torch.full_like(s["q"], 7.0) if out is None else out
+    lse = torch.full((T, Hm), 7.0, dtype=F32, device=DEV) if lse is None else lse
+    st = i32([0])
+    n = ops.mla_paged_chunk_workspace_bytes(s["q"], s["pages"])
+    if ws is None:  # what a workspace held before does not matter
+        ws = torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device=DEV)
+    ops.dsa_mla_paged_chunk(s["q"], s["pages"], s["scale"], s["table"], s["lens"], s["ps"],
+                            s["cu"], window, sinks, s["sm"], out, lse, ws, st, stream)
+    torch.cuda.synchronize()
+    return out, lse, st.item()
+
+
+def reference(s, window=0, sinks=0):
+    return ref.attend(s["q"], ref.values(s["pages"], s["scale"]), s["table"], s["lens"], s["ps"],
+                      s["cu"], window, sinks, s["sm"])
+
+
+def check(s, window=0, sinks=0, status=0):
+    out, lse, st = attend(s, window, sinks)
+    assert st == status
+    live = s["cu"][-1].item()
+    r = reference(s, window, sinks)
+    ref.check_attend(out, lse, r, s["q"].dtype, s["q"].shape[2],
+                     rows=torch.arange(live, device=DEV))
+    assert bool((out[live:] == 7.0).all()) and bool((lse[live:] == 7.0).all())
+    return out, lse
+
+
+LENS = [([1], [1]), ([127, 128, 129, 1], [1, 1, 1, 1]), ([300], [300]), ([0, 5, 0], [0, 5, 0]),
+        ([1000, 3, 130, 700, 64], [1, 3, 2, 9, 64]), ([2500, 17], [130, 0]),
+        ([513, 256, 255], [3, 7, 1])]
+MASKS = [(0, 0), (0, 5), (1, 0), (64, 4), (100, 130), (700, 1), (128, 1000)]
+GEOS = [(64, 512, BF, BF), (64, 512, BF, F8), (16, 512, BF, BF), (128, 512, BF, F8),
+        (33, 512, BF, BF), (1, 512, BF, F8), (80, 512, BF, BF), (4, 64, F32, F32),
+        (5, 40, BF, F8), (3, 1024, F32, F8), (2, 512, F32, BF), (2, 512, BF, F32)]
+
+
+@pytest.mark.parametrize("Hm,L,act,kv", GEOS)
+@pytest.mark.parametrize("which", range(len(LENS)))
+def test_chunk(Hm, L, act, kv, which):
+    lens, new = LENS[which]
+    for j, (window, sinks) in enumerate(MASKS):
+        ps = (64, 16, 1, 48, 5, 128, 8)[(which + j) % 7]
+        s = make(lens, new, Hm=Hm, L=L, act=act, kv=kv, ps=ps, seed=which * 10 + j)
+        check(s, window, sinks)
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("B,hi,new", [(1, 9000, 1), (3, 20000, 1), (160, 700, 1), (40, 2000, 3)])
+def test_chunk_decode_split_over_the_card(B, hi, new, kv):
+    rng = random.Random(B)
+    lens = [rng.randint(new, hi) for _ in range(B)]
+    s = make(lens, [new] * B, kv=kv, seed=B, q_std=2.0)
+    check(s)
+    check(s, 512, 4)
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_chunk_many_tokens(kv):
+    s = make([900, 1500, 40], [300, 200, 40], kv=kv, seed=3, q_std=2.0)
+    check(s)
+    check(s, 200, 9)
+
+
+@pytest.mark.parametrize("act,kv,L", [(BF, BF, 512), (BF, F8, 512), (F32, F32, 64)])
+def test_chunk_rising_and_falling_logits(act, kv, L):
+    """Keys whose logits climb (and fall) by hundreds along the sequence: the running
+    maximum has to move, far apart tiles must not overflow or vanish."""
+    for sign in (1.0, -1.0):
+        s = make([1300], [4], Hm=16, L=L, act=act, kv=kv, seed=4)
+        ramp = torch.linspace(-6.0, 6.0, 1300, device=DEV) * sign
+        p = torch.arange(1300, device=DEV)
+        rows = s["table"][0].long()[p // s["ps"]] * s["ps"] + p % s["ps"]
+        direction = torch.randn(L, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV)
+        x = ramp[:, None] * direction[None, :] + 0.05 * torch.randn((1300, L), device=DEV)
+        if kv == F8:
+            codes, sc = ref.quantise(x)
+            s["pages"].view(torch.uint8)[rows] = codes.view(torch.uint8)
+            s["scale"][rows] = sc
+        else:
+            s["pages"][rows] = x.to(kv)
+        s["q"] = (direction * 2).to(act).expand(s["T"], 16, L).contiguous()
+        check(s)
+        check(s, 300, 7)
+
+
+@pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 16, 512), (F32, F32, 4, 64)])
+def test_chunk_later_tokens_do_not_reach_earlier_ones(act, kv, Hm, L):
+    """NaN, infinities and the type's largest values in the rows of later tokens, outside
+    the window and behind the sequence leave the others as they are."""
+    for fill in (math.nan, math.inf, -math.inf, torch.finfo(kv).max):
+        s = make([400], [6], Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=6, hidden=fill)
+        want, want_lse, _ = attend(s, 50, 3)
+        p = torch.arange(400, device=DEV)
+        rows = s["table"][0].long()[p // 16] * 16 + p % 16
+        hide = torch.zeros(400, dtype=torch.bool, device=DEV)
+        hide[397:] = True                    # tokens 3, 4, 5 of the chunk
+        hide[3:394 - 50 + 1] = True          # outside every window
+        s["pages"][rows[hide]] = torch.full((), fill, device=DEV).to(kv)
+        if kv == F8:
+            s["scale"][rows[hide]] = fill
+        out, lse, _ = attend(s, 50, 3)
+        assert torch.equal(out[:3], want[:3]) and torch.equal(lse[:3], want_lse[:3])
+        if math.isnan(fill):                 # and it reaches those that see it
+            assert torch.isnan(out[3:6].float()).all()
+
+
+@pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 64, 512), (F32, F32, 4, 64)])
+def test_chunk_faults_are_flagged_and_contained(act, kv, Hm, L):
+    s = make([500, 100, 60], [3, 100, 2], Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=7)
+    n_pages = s["pages"].shape[0] // 16
+    s["table"][0, 3], s["table"][0, 20], s["table"][1, 0] = -1, n_pages, 2 ** 31 - 1
+    s["table"][2, :] = -5                              # nothing at all
+    check(s, status=ops.DEV_BAD_PAGE)
+    s = make([500, 100], [3, 100], Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=8)
+    s["table"] = s["table"][:, :10].contiguous()       # too narrow for the first
+    check(s, status=ops.DEV_BAD_PAGE)
+    s = make([5, 9, -3], [8, 9, 2], Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=9)
+    check(s, status=ops.DEV_BAD_LENGTH)                # rows before position 0 see nothing
+    s = make([50, 60], [10, 20], Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=10, pad=0)
+    s["cu"] = i32([-4, 10, 1000])                      # cut to the rows that exist
+    out, lse, st = attend(s)
+    assert st & ops.DEV_BAD_LENGTH and torch.isfinite(out.float()).all()
+    s["cu"] = i32([20, 3, 7])
+    assert attend(s)[2] & ops.DEV_BAD_LENGTH
+
+
+def test_chunk_infinite_and_nan_queries_stay_in_their_rows():
+    s = make([300, 40], [5, 3], seed=11)
+    want, want_lse, _ = attend(s)
+    s["q"][1, 7] = math.nan
+    s["q"][6, 0, 3] = math.inf
+    out, lse, _ = attend(s)
+    keep = torch.ones((s["T"], 64), dtype=torch.bool, device=DEV)
+    keep[1, 7] = keep[6, 0] = False
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
+    assert torch.isnan(out[1, 7].float()).all() and torch.isnan(out[6, 0].float()).all()
+
+
+def test_chunk_same_bits_every_time_and_beside_other_calls():
+    a = make([3000, 20, 777], [5, 20, 300], seed=12)
+    b = make([90, 9000], [1, 1], kv=F8, seed=13)
+    want_a, want_b = attend(a), attend(b)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(3):
+        for x, st in zip((a, b), streams):
+            T, Hm, L = x["q"].shape
+            out, lse = torch.full_like(x["q"], 7.0), torch.full((T, Hm), 7.0, device=DEV)
+            ws = torch.empty(max(16, ops.mla_paged_chunk_workspace_bytes(x["q"], x["pages"])),
+                             dtype=torch.uint8, device=DEV)
+            torch.cuda.synchronize()
+            ops.dsa_mla_paged_chunk(x["q"], x["pages"], x["scale"], x["table"], x["lens"],
+                                    x["ps"], x["cu"], 0, 0, x["sm"], out, lse, ws, None, st)
+            got.append((out, lse, ws))
+    torch.cuda.synchronize()
+    for i, (out, lse, _) in enumerate(got):
+        want = (want_a, want_b)[i % 2]
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_step_captured_and_replayed(kv):
+    """plan -> append -> attention in one CUDA graph, lengths and free list in place: each
+    replay is the next decode step.  The steps one by one, uncaptured, give the same."""
+    L, Hm, ps, B = 512, 64, 16, 5
+    g = torch.Generator(device=DEV).manual_seed(14)
+    lens0 = [0, 31, 16, 200, 5]
+    x = torch.randn((4, B, L), generator=g, device=DEV).to(BF)
+    q = torch.randn((4, B, Hm, L), generator=g, device=DEV).to(BF)
+
+    def state():
+        s = make(lens0, [0] * B, kv=kv, ps=ps, seed=15, pad=B, hidden=0.0)
+        n_pages = s["pages"].shape[0] // ps + 40
+        grow = torch.zeros((40 * ps, L), dtype=kv, device=DEV)
+        s["pages"] = torch.cat([s["pages"].view(torch.uint8), grow.view(torch.uint8)]).view(kv)
+        if s["scale"] is not None:
+            s["scale"] = torch.cat([s["scale"], torch.zeros(40 * ps, device=DEV)])
+        s["free"] = torch.arange(n_pages - 40, n_pages, device=DEV).to(torch.int32)
+        s["begin"], s["one"] = i32([0]), i32([1] * B)
+        for k in ("q_seq", "q_pos", "rows"):
+            s[k] = i32([0] * B)
+        s["x"], s["out"] = torch.empty_like(x[0]), torch.empty_like(q[0])
+        s["lse"] = torch.empty((B, Hm), dtype=F32, device=DEV)
+        s["q"] = torch.empty_like(q[0])
+        s["ws"] = torch.empty(max(16, ops.mla_paged_chunk_workspace_bytes(s["q"], s["pages"])),
+                              dtype=torch.uint8, device=DEV)
+        s["st"] = i32([0])
+        return s
+
+    def step(s):
+        ops.dsa_paged_plan(s["lens"], s["one"], s["free"], s["begin"], s["pages"].shape[0] // ps,
+                           ps, s["table"], s["lens"], s["cu"], s["q_seq"], s["q_pos"], s["rows"],
+                           s["begin"], status=s["st"])
+        ops.dsa_paged_append(s["x"], s["rows"], s["pages"], s["scale"], status=s["st"])
+        ops.dsa_mla_paged_chunk(s["q"], s["pages"], s["scale"], s["table"], s["lens"], ps,
+                                s["cu"], 0, 0, s["sm"], s["out"], s["lse"], s["ws"], s["st"])
+
+    def outputs(s, i):
+        s["x"].copy_(x[i])
+        s["q"].copy_(q[i])
+
+    eager, want = state(), []
+    for i in range(4):
+        outputs(eager, i)
+        step(eager)
+        want.append((eager["out"].clone(), eager["lse"].clone()))
+    s = state()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(s)
+    assert s["lens"].tolist() == lens0                 # captured, not run
+    for i in range(4):
+        outputs(s, i)
+        graph.replay()
+        assert torch.equal(s["out"], want[i][0]) and torch.equal(s["lse"], want[i][1])
+    assert s["lens"].tolist() == [n + 4 for n in lens0] and s["st"].item() == 0
+    assert s["begin"].item() == sum(-(-(n + 4) // ps) - -(-n // ps) for n in lens0)
+    # the cache holds the appended rows, and the attention read them
+    p = torch.full((B,), 3, device=DEV) + i32(lens0)
+    rows = s["table"].gather(1, (p // ps).long()[:, None])[:, 0] * ps + p % ps
+    have = ref.values(s["pages"], s["scale"])[rows.long()]
+    tol = (2.0 ** -4 if kv == F8 else 2.0 ** -8) * x[3].double().abs()
+    if kv == F8:  # codes below 2^-6 are 2^-9 apart
+        tol = torch.maximum(tol, 2.0 ** -10 * s["scale"][rows.long()].double()[:, None]) * 1.001
+    assert bool(((have - x[3].double()).abs() <= tol).all())
+    chk = dict(s, T=B)
+    ref.check_attend(s["out"], s["lse"], reference(chk), BF, L)
