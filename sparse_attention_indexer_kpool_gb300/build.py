@@ -27,7 +27,7 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2"
                      "--expt-relaxed-constexpr", "-Xptxas", "-v", "-I", INCLUDE]
 SOURCES = ["dsa_abi.cu", "kpool_compress.cu", "index_scores.cu", "index_scores_umma.cu",
            "topk.cu", "mla_decode.cu", "mla_umma.cu", "select_noalloc.cu",
-           "indexer_proj.cu", "paged_step.cu", "mla_chunk.cu"]
+           "indexer_proj.cu", "paged_step.cu", "mla_chunk.cu", "mla_chunk_umma.cu"]
 
 
 def _nvcc() -> str:

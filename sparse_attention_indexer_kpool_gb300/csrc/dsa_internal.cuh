@@ -360,6 +360,10 @@ struct ChunkArgs {
 };
 size_t mla_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype);
 int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream);
+// its tcgen05 form: bf16 activations, latent 512, bf16 or E4M3 pages
+bool mla_chunk_umma_ok(int L, int dtype, int kv_dtype);
+size_t mla_chunk_umma_workspace_size(int Hm);
+int launch_mla_chunk_umma(const ChunkArgs& a, void* workspace, cudaStream_t stream);
 }  // namespace dsa
 
 #define DSA_LAUNCH_CHECK()                          \

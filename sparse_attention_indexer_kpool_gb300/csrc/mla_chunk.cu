@@ -167,12 +167,13 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
 }  // namespace
 
 size_t mla_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype) {
-  (void)T; (void)Hm; (void)L; (void)dtype; (void)kv_dtype;
-  return 0;
+  if (T < 1 || !mla_chunk_umma_ok(L, dtype, kv_dtype)) return 0;
+  return mla_chunk_umma_workspace_size(Hm);
 }
 
 int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
-  (void)workspace;
+  if (mla_chunk_umma_ok(a.L, a.dtype, a.kv.kv_dtype))
+    return launch_mla_chunk_umma(a, workspace, stream);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

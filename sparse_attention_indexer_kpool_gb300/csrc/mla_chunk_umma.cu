@@ -1,0 +1,1035 @@
+// NoPE MLA of a step's new tokens over the paged latent cache on the tcgen05
+// tensor cores (bf16 activations, latent 512, bf16 or E4M3 pages).
+//
+// Module glm5next_dsa, "Traps carried from Slice 8" (NoPE: a score is the plain
+// latent dot product) and Constants, MASKED_ATTN_MAX_KEYS (dense masked
+// attention).  In absorbed MLA the value of a latent row is the row itself, so
+// one tile of rows feeds both products.
+//
+// Work.  A row tile is one token and up to kN of its heads; its keys are 128-row
+// tiles of positions, the sinks' tiles first, then those from the window's first
+// position (0 without one) to the token's own.  A tile's rows share one mask, by
+// position alone: what a token does not see is zeroed in shared memory before
+// the second product reads it, so nothing there (NaN, infinity) reaches the
+// output.  One persistent CTA per SM takes an equal, contiguous share of the
+// (row tile, key tile) units of the whole batch, found from the lengths by a scan
+// in every CTA; a row tile whose units fall to several CTAs leaves partials (O
+// unnormalised, maximum, sum) that a second kernel joins in CTA order.  Units
+// are counted with the longest token's tiles for every token of a sequence and
+// scaled to the token's own; tokens are taken from both ends of the chunk in
+// turn, so that a share of long and short ones evens out.
+//
+// Per key tile, S^T = C q^T (M = 128 rows, N = kN heads, K = 512) goes to TMEM; a
+// thread holds one row's scores of kN / 2 heads, P = 2^(z - m) goes to shared
+// memory row by row, and O^T += C^T P^T (M = 128 latent columns, four chunks)
+// reads the same tile MN-major.  The reference m of a head is its maximum when
+// it was last raised; it is raised, and O^T and the sums rescaled, only when a
+// score passes it by more than kRaiseAt (base 2): bf16 and fp32 keep the same
+// relative precision at any scale, so a stale reference costs nothing, and no
+// tile but such a one needs a maximum across rows.
+//
+// What bounds it.  One 128 x 64 x 16 MMA reads 6 KB of shared memory at 128
+// bytes a cycle (measured 51 cycles; the tensor cores alone would take 32), the
+// next tile's rows are written through the same port (1,024 cycles), and the
+// softmax of a tile stands between its two products: rows 128 KB, queries 64 KB
+// and P 16 KB leave no room for a second tile, so the tile is handed on in four
+// column chunks, each refilled as soon as its part of O^T is done.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "dsa_internal.cuh"
+#include "umma.cuh"
+
+#include <cudaTypedefs.h>
+
+namespace dsa {
+namespace {
+
+constexpr int kL = 512, kKeys = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRaiseAt = 20.f;
+constexpr int kKvBlock = kKeys * 128;  // 128 rows x 64 latent columns, 16 KB
+constexpr int kSoftThreads = 256;      // warps 0..7
+
+// Row sources: TMA boxes of bf16 rows (page size a multiple of 8), or four warps
+// that copy bf16 rows of any page size, or convert E4M3 codes.
+constexpr int kSrcTma = 0, kSrcCopy = 1, kSrcE4M3 = 2;
+__host__ __device__ constexpr int load_warps(int src) { return src == kSrcTma ? 1 : 4; }
+__host__ __device__ constexpr int cta_threads(int src) {
+  return kSoftThreads + 32 * load_warps(src) + 32;
+}
+
+struct Header {        // what CTA g left for the join
+  int start_tile;      // row tile whose first units it holds but not its last (-1: none)
+  int cont_tile;       // row tile that an earlier CTA began (-1: none; -2: no share at all)
+  int cont_some;       // it has a partial of that
+  int cont_ends;       // and its last units
+};
+
+struct Ctl {
+  float m[64], alpha[64], l[64];  // per head; first: read as float4
+  float red[4][64];
+  float rs[kKeys];
+  int valid[kKeys];               // copied rows: the position is seen and has a page
+  int prow[2][kKeys];
+  uint64_t full[4], empty[4], s_full, p_full, o_full, q_full, q_empty, drain;
+  unsigned long long scan[32];
+  unsigned long long start_off;   // first unit within start_b
+  uint32_t tmem;
+  int start_b;
+  unsigned groups;                // TMA boxes of the tile that hold rows
+  int raise;
+  int soft_dead[2];
+  int dead;
+};
+
+template <int kN>
+struct Smem {
+  static constexpr int kQBlock = kN * 128;
+  static constexpr int kPRow = kN * 2;              // bytes of one key's probabilities
+  static constexpr size_t kKv = 0;
+  static constexpr size_t kQ = 8 * (size_t)kKvBlock;
+  static constexpr size_t kP = kQ + 8 * (size_t)kQBlock;
+  static constexpr size_t kCtl = kP + (size_t)kKeys * kPRow;
+  static constexpr size_t kBytes = 1024 + kCtl + sizeof(Ctl);
+};
+static_assert(Smem<64>::kBytes <= 227 * 1024, "shared memory budget");
+
+struct Params {
+  PagedKv kv;
+  const int32_t* cu_new;
+  int T, B, Hm, window, sinks;
+  float zscale;              // sm_scale in base 2
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_o;             // [2 CTAs][kN][kL]
+  float2* part_ml;           // [2 CTAs][kN]
+  Header* head;
+  int32_t* status;
+  int drill, prefetch;
+  int box_rows;
+};
+
+// ---- the batch as units ------------------------------------------------------
+struct Seq {
+  int c0, n, base;             // rows c0 .. c0 + n - 1 of the step; position of the first
+  unsigned long long u;        // units per row tile
+};
+__device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p) {
+  Seq s;
+  s.c0 = min(max(cu0, 0), p.T);
+  s.n = max(min(cu1, p.T) - s.c0, 0);
+  s.base = len < 0 ? -s.n : len - s.n;   // negative: rows before position 0
+  const int all = max(len, 0);
+  long long u = ((long long)all + kKeys - 1) / kKeys;
+  if (p.window > 0) {
+    const long long w = ((long long)p.window + kKeys - 2) / kKeys + 1 +
+                        ((long long)p.sinks + kKeys - 1) / kKeys;
+    if (w < u) u = w;
+  }
+  s.u = u > 1 ? (unsigned long long)u : 1ull;
+  return s;
+}
+
+// One token's visible positions [0, s0) and [lo, pos], as key tiles.
+struct Keys {
+  int pos, lo, s0, sink_tiles, first, n;
+  __device__ __forceinline__ int tile(int v) const {
+    return v < sink_tiles ? v : first + (v - sink_tiles);
+  }
+  __device__ __forceinline__ bool sees(int t) const { return t <= pos && (t >= lo || t < s0); }
+};
+__device__ __forceinline__ Keys keys_of(int pos, const Params& p) {
+  Keys k;
+  k.pos = pos;
+  k.lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  k.s0 = min(p.sinks, k.lo);
+  k.first = k.lo / kKeys;
+  k.sink_tiles = min((k.s0 + kKeys - 1) / kKeys, k.first);
+  k.n = pos < 0 ? 0 : k.sink_tiles + pos / kKeys - k.first + 1;
+  return k;
+}
+
+// A walk over the CTA's units, row tile by row tile.  Every role walks alone; the
+// next sequence's lengths are read one sequence ahead.
+struct Walk {
+  const Params& p;
+  int hb;                       // head blocks per token
+  unsigned long long left;      // units still to do
+  unsigned long long off;       // units done of the current sequence
+  int b;
+  Seq s;
+  int cu_next, len_next;        // of sequence b + 1 (its end, its length)
+  // the current segment
+  int token, h0, tile_id, ta, tb;
+  Keys k;
+
+  __device__ __forceinline__ Walk(const Params& pp, int hb_, int b0, unsigned long long off0,
+                                  unsigned long long n)
+      : p(pp), hb(hb_), left(n), off(off0), b(b0) {
+    if (left == 0) return;
+    const int cu0 = __ldg(p.cu_new + b), cu1 = __ldg(p.cu_new + b + 1);
+    s = seq_of(cu0, cu1, __ldg(p.kv.seq_lens + b), p);
+    ahead();
+  }
+  __device__ __forceinline__ void ahead() {
+    if (b + 1 < p.B) {
+      cu_next = __ldg(p.cu_new + b + 2);
+      len_next = __ldg(p.kv.seq_lens + b + 1);
+    }
+  }
+  // the next segment: a row tile and its key tiles [ta, tb) (none: ta == tb)
+  __device__ __forceinline__ bool next() {
+    if (left == 0) return false;
+    unsigned long long all = (unsigned long long)s.n * hb * s.u;
+    while (off >= all) {  // units remain, so a sequence with some follows
+      if (++b >= p.B) return false;  // (lengths that changed under the call)
+      const int cu0 = __ldg(p.cu_new + b);
+      s = seq_of(cu0, cu_next, len_next, p);
+      ahead();
+      off = 0;
+      all = (unsigned long long)s.n * hb * s.u;
+    }
+    const unsigned long long r = off / s.u;
+    const unsigned long long a = off - r * s.u;
+    const unsigned long long e = min(s.u, a + left);
+    const int kk = (int)(r / hb), hblk = (int)(r - (unsigned long long)kk * hb);
+    const int i = (kk & 1) ? s.n - 1 - (kk >> 1) : kk >> 1;  // from both ends in turn
+    token = s.c0 + i;
+    h0 = hblk;
+    tile_id = token * hb + hblk;
+    k = keys_of(s.base + i < 0 ? -1 : s.base + i, p);
+    ta = (int)(a * k.n / s.u);
+    tb = (int)(e * k.n / s.u);
+    off += e - a;
+    left -= e - a;
+    return true;
+  }
+};
+
+// ---- small pieces ------------------------------------------------------------
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// kW values per lane (one row, kW heads) reduced over the warp's 32 rows by
+// halving exchanges; lane l ends with head l mod kW.
+template <int kW, bool kMax>
+__device__ __forceinline__ float across_rows(float (&v)[kW], int lane) {
+  if (kW == 16) {
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      const float o = __shfl_xor_sync(0xffffffffu, v[i], 16);
+      v[i] = kMax ? fmaxf(v[i], o) : v[i] + o;
+    }
+  }
+#pragma unroll
+  for (int s = kW / 2; s >= 1; s >>= 1) {
+    const bool upper = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float send = upper ? v[i] : v[i + s];
+      const float keep = upper ? v[i + s] : v[i];
+      const float recv = __shfl_xor_sync(0xffffffffu, send, s);
+      v[i] = kMax ? fmaxf(keep, recv) : keep + recv;
+    }
+  }
+  return v[0];
+}
+
+__device__ __forceinline__ void fma2(float& a0, float& a1, float b, float c0, float c1) {
+  unsigned long long a, bb, c;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(bb) : "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a) : "l"(bb), "l"(c));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  unsigned long long a, b;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+}
+
+template <int kW>
+__device__ __forceinline__ void tmem_ldw(uint32_t ta, float (&v)[kW]) {
+  if constexpr (kW == 32) tmem_ld32(ta, v); else tmem_ld16(ta, v);
+}
+// Store 16 consecutive fp32 columns of the warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+      "r"(__float_as_uint(v[15]))
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+template <int kW>
+__device__ __forceinline__ void tmem_stw(uint32_t ta, const float (&v)[kW]) {
+  if constexpr (kW == 32) tmem_st32(ta, v); else tmem_st16(ta, v);
+}
+
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+// Barriers of one role's threads (barrier 0 is the CTA's).
+__device__ __forceinline__ void sync_soft() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
+}
+__device__ __forceinline__ bool vote_soft(bool v) {  // whether any of them says so
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "n"(kSoftThreads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void sync_load() {
+  asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
+}
+
+// A bounded wait that also ends when another role has given up.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* dead,
+                                        unsigned long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*dead) return false;
+    if (global_ns() - t0 > limit_ns) {
+      *dead = 1;
+      return false;
+    }
+  }
+}
+
+// ---- the kernel --------------------------------------------------------------
+template <int kN, int kSrc>
+__global__ void __launch_bounds__(cta_threads(kSrc), 1)
+    mla_chunk_kernel(const __grid_constant__ CUtensorMap q_map,
+                     const __grid_constant__ CUtensorMap kv_map, const Params p) {
+  using S = Smem<kN>;
+  constexpr int kW = kN / 2;  // heads per softmax thread
+  constexpr int kLoad0 = kSoftThreads / 32, kMmaWarp = kLoad0 + load_warps(kSrc);
+  constexpr int kTmemCols = kN == 64 ? 512 : 256;  // S^T (kN), O^T (4 kN)
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl& c = *reinterpret_cast<Ctl*>(sb + S::kCtl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hb = (p.Hm + kN - 1) / kN;
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&c.full[i], kSrc == kSrcTma ? 1 : load_warps(kSrc));
+      mbar_init(&c.empty[i], 1);
+    }
+    mbar_init(&c.s_full, 1);
+    mbar_init(&c.p_full, kSoftThreads / 32);
+    mbar_init(&c.o_full, 1);
+    mbar_init(&c.q_full, 1);
+    mbar_init(&c.q_empty, 1);
+    mbar_init(&c.drain, 1);
+    fence_mbar_init();
+    c.soft_dead[0] = c.soft_dead[1] = c.dead = 0;
+    c.start_b = p.B;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc<kTmemCols>(&c.tmem);
+    tc_fence_before();
+  }
+  if (tid < 64) c.m[tid] = -INFINITY;
+  pdl_wait();  // every input may come from the kernel just before
+  pdl_launch_dependents();
+
+  // ---- this CTA's share of the batch's units
+  unsigned long long v0, v1;
+  {
+    constexpr int kT = cta_threads(kSrc);
+    const int per = (p.B + kT - 1) / kT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    unsigned long long mine = 0;
+    bool odd = false;
+    for (int b = b0; b < b1; ++b) {
+      const int cu0 = p.cu_new[b], cu1 = p.cu_new[b + 1], len = p.kv.seq_lens[b];
+      const Seq s = seq_of(cu0, cu1, len, p);
+      odd |= cu0 < 0 || cu1 < cu0 || cu1 > p.T || (s.n > 0 && s.base < 0);
+      mine += (unsigned long long)s.n * hb * s.u;
+    }
+    if (odd && blockIdx.x == 0) flag(p.status, DSA_DEV_BAD_LENGTH);
+    unsigned long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) c.scan[warp] = inc;
+    __syncthreads();
+    unsigned long long before = inc - mine, total = 0;
+    for (int w = 0; w < kT / 32; ++w) {
+      if (w < warp) before += c.scan[w];
+      total += c.scan[w];
+    }
+    v0 = total * blockIdx.x / gridDim.x;
+    v1 = total * (blockIdx.x + 1) / gridDim.x;
+    if (v0 < v1 && v0 >= before && v0 < before + mine) {
+      unsigned long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        const Seq s = seq_of(p.cu_new[b], p.cu_new[b + 1], p.kv.seq_lens[b], p);
+        const unsigned long long all = (unsigned long long)s.n * hb * s.u;
+        if (v0 < at + all) {
+          c.start_b = b;
+          c.start_off = v0 - at;
+          break;
+        }
+        at += all;
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  const uint32_t tmem = c.tmem;
+  const bool any = c.start_b < p.B;
+  Walk w(p, hb, any ? c.start_b : 0, any ? c.start_off : 0ull, any ? v1 - v0 : 0ull);
+  // a failure drill loads nothing and issues no MMA: the first waits run out
+  const bool issue = p.drill == 0;
+  const unsigned long long wait_ns = p.drill ? kDrillWaitNs : kWaitNs;
+  const uint32_t kvb = smem_u32(sb + S::kKv), qb = smem_u32(sb + S::kQ);
+  const uint32_t pb = smem_u32(sb + S::kP);
+  volatile int* dead = &c.dead;
+
+  if (warp < kLoad0) {
+    // ================= softmax and epilogue =================
+    const int qw = warp & 3;      // TMEM lanes 32 qw ..: this thread's key row r
+    const int hq = warp >> 2;     // heads kW hq ..
+    const int r = qw * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16);
+    Header hd = {-1, any ? -1 : -2, 0, 0};
+    int tiles = 0, segs = 0;      // waits so far
+    bool ok = true;
+    while (ok && w.next()) {
+      float l[kW], nm[kW];        // this row's sums; minus the reference (0: none yet)
+      bool unset = true;
+#pragma unroll
+      for (int i = 0; i < kW; ++i) l[i] = nm[i] = 0.f;
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        const int t = w.k.tile(v) * kKeys + r;
+        if (!wait_on(&c.s_full, tiles & 1, dead, wait_ns)) c.soft_dead[tiles & 1] = 1;
+        tc_fence_after();
+        float e[kW];
+        tmem_ldw<kW>(tl + hq * kW, e);
+        bool valid;
+        float rs = 1.f;
+        if constexpr (kSrc == kSrcTma) {
+          valid = w.k.sees(t) && ((c.groups >> (r / p.box_rows)) & 1u);
+          if (!valid) {  // the half of this row that this thread clears
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+            for (int blk = 4 * hq; blk < 4 * hq + 4; ++blk)
+              for (int ch = 0; ch < 8; ++ch)
+                *reinterpret_cast<uint4*>(sb + S::kKv + blk * kKvBlock + r * 128 + ch * 16) = zero;
+          }
+        } else {
+          valid = c.valid[r] != 0;
+          if constexpr (kSrc == kSrcE4M3) rs = c.rs[r];
+        }
+        const float zs = kSrc == kSrcE4M3 ? p.zscale * rs : p.zscale;
+        bool high = unset;
+#pragma unroll
+        for (int i = 0; i < kW; i += 2) fma2(e[i], e[i + 1], zs, nm[i], nm[i + 1]);
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+          e[i] = valid ? e[i] : -INFINITY;
+          high |= e[i] > kRaiseAt;
+        }
+        // every thread takes the same branch; the flag of a failed wait was
+        // written before this barrier
+        const bool full = vote_soft(high);
+        if (c.soft_dead[tiles & 1]) {
+          ok = false;
+          break;
+        }
+        if (full) {
+          tmem_ldw<kW>(tl + hq * kW, e);
+#pragma unroll
+          for (int i = 0; i < kW; ++i) e[i] = valid ? e[i] * zs : -INFINITY;
+          const float m = across_rows<kW, true>(e, lane);
+          if (lane < kW) c.red[qw][hq * kW + lane] = m;
+          if (tid == 0) c.raise = 0;
+          sync_soft();
+          if (tid < kN) {
+            const float tm = fmaxf(fmaxf(c.red[0][tid], c.red[1][tid]),
+                                   fmaxf(c.red[2][tid], c.red[3][tid]));
+            const float m_old = c.m[tid];
+            float a = 1.f;
+            if (m_old == -INFINITY) {
+              c.m[tid] = tm;  // nothing accumulated for this head yet
+            } else if (tm > m_old + kRaiseAt) {
+              c.m[tid] = tm;
+              a = ex2_fast(m_old - tm);
+              c.raise = 1;
+            }
+            c.alpha[tid] = a;
+          }
+          sync_soft();
+          unset = false;
+#pragma unroll
+          for (int i = 0; i < kW; ++i) {
+            const float mm = c.m[hq * kW + i];
+            nm[i] = mm == -INFINITY ? 0.f : -mm;
+            unset |= mm == -INFINITY;
+          }
+          if (c.raise) {  // O^T of the tiles so far is complete: S^T came after it
+#pragma unroll
+            for (int i = 0; i < kW; ++i) l[i] *= c.alpha[hq * kW + i];
+            if (v > w.ta) {
+#pragma unroll 1
+              for (int mc = 0; mc < 4; ++mc) {
+                float o[kW];
+                const uint32_t ta = tl + (uint32_t)(kN + mc * kN + hq * kW);
+                tmem_ldw<kW>(ta, o);
+#pragma unroll
+                for (int i = 0; i < kW; ++i) o[i] *= c.alpha[hq * kW + i];
+                tmem_stw<kW>(ta, o);
+              }
+            }
+          }
+          tmem_ldw<kW>(tl + hq * kW, e);
+#pragma unroll
+          for (int i = 0; i < kW; ++i) e[i] = valid ? fmaf(e[i], zs, nm[i]) : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < kW; ++i) e[i] = ex2_fast(e[i]);
+        // P is rounded to bf16 for the tensor cores; the sums keep the unrounded
+        // weights.  An E4M3 row's scale goes to its weights, so the tile holds codes.
+#pragma unroll
+        for (int q = 0; q < kW / 8; ++q) {
+          const float sc = kSrc == kSrcE4M3 ? rs : 1.f;
+          const uint4 pk4 = make_uint4(pack_bf16(e[8 * q] * sc, e[8 * q + 1] * sc),
+                                 pack_bf16(e[8 * q + 2] * sc, e[8 * q + 3] * sc),
+                                 pack_bf16(e[8 * q + 4] * sc, e[8 * q + 5] * sc),
+                                 pack_bf16(e[8 * q + 6] * sc, e[8 * q + 7] * sc));
+          const int ch = hq * (kW / 8) + q;
+          const int at = kN == 64 ? r * 128 + ((ch ^ (r & 7)) << 4)
+                                  : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+          *reinterpret_cast<uint4*>(sb + S::kP + at) = pk4;
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&c.p_full);
+#pragma unroll
+        for (int i = 0; i < kW; i += 2) add2(l[i], l[i + 1], e[i], e[i + 1]);
+      }
+      if (!ok) break;
+      const bool some = w.tb > w.ta, whole = w.ta == 0 && w.tb == w.k.n;
+      const bool begins = some && w.ta == 0 && !whole;
+      if (begins) hd.start_tile = w.tile_id;
+      if (!whole && !begins && hd.cont_tile < 0) {
+        hd.cont_tile = w.tile_id;
+        hd.cont_some = some;
+        hd.cont_ends = w.tb == w.k.n;
+      }
+      if (!some && !whole) continue;
+      const int heads = min(kN, p.Hm - w.h0 * kN);
+      const long long row0 = (long long)w.token * p.Hm + w.h0 * kN;
+      if (!some) {  // a token that sees nothing
+        for (int i = tid; i < heads * (kL / 8); i += kSoftThreads)
+          *reinterpret_cast<uint4*>(p.out + row0 * kL + (long long)i * 8) =
+              make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse && tid < heads) p.lse[row0 + tid] = -INFINITY;
+        continue;
+      }
+      {
+        const float sum = across_rows<kW, false>(l, lane);
+        if (lane < kW) c.red[qw][hq * kW + lane] = sum;
+      }
+      if (!wait_on(&c.o_full, segs & 1, dead, wait_ns)) c.soft_dead[tiles & 1] = 1;
+      ++segs;
+      tc_fence_after();
+      sync_soft();
+      if (c.soft_dead[tiles & 1]) {
+        ok = false;
+        break;
+      }
+      if (tid < kN) {
+        const float sum = (c.red[0][tid] + c.red[1][tid]) + (c.red[2][tid] + c.red[3][tid]);
+        const float m = c.m[tid];
+        c.m[tid] = -INFINITY;
+        if (whole) {
+          c.l[tid] = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
+          if (p.lse && tid < heads)
+            p.lse[row0 + tid] = sum == 0.f ? -INFINITY : (m + log2f(sum)) / kLog2e;
+        } else {
+          const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
+          p.part_ml[slot * kN + tid] = make_float2(m, sum);
+        }
+      }
+      sync_soft();
+      if (whole) {
+        // a lane pair holds two latent columns of every head: each lane of the pair
+        // stores both columns of one of two heads
+        float inv[kW];
+#pragma unroll
+        for (int i = 0; i < kW; ++i) inv[i] = c.l[hq * kW + i];
+        const bool upper = lane & 1;
+#pragma unroll 1
+        for (int mc = 0; mc < 4; ++mc) {
+          float o[kW];
+          tmem_ldw<kW>(tl + (uint32_t)(kN + mc * kN + hq * kW), o);
+          __nv_bfloat16* dst =
+              p.out + (row0 + hq * kW + (upper ? 1 : 0)) * kL + mc * 128 + qw * 32 + (lane & ~1);
+#pragma unroll
+          for (int i = 0; i < kW; i += 2) {
+            const float a = o[i] * inv[i], b = o[i + 1] * inv[i + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, upper ? a : b, 1);
+            if (hq * kW + i + (upper ? 1 : 0) < heads)
+              *reinterpret_cast<uint32_t*>(dst + (long long)i * kL) =
+                  upper ? pack_bf16(got, b) : pack_bf16(a, got);
+          }
+        }
+      } else {
+        float* dst = p.part_o +
+                     ((long long)(2 * blockIdx.x + (begins ? 1 : 0)) * kN + hq * kW) * kL +
+                     qw * 32 + lane;
+#pragma unroll 1
+        for (int mc = 0; mc < 4; ++mc) {
+          float o[kW];
+          tmem_ldw<kW>(tl + (uint32_t)(kN + mc * kN + hq * kW), o);
+#pragma unroll
+          for (int i = 0; i < kW; ++i)
+            if (hq * kW + i < heads) dst[(long long)i * kL + mc * 128] = o[i];
+        }
+      }
+      tc_fence_before();  // O^T is read: the next segment's P releases it
+    }
+    if (!ok) hd = Header{-1, -1, 0, 0};
+    if (tid == 0 && p.head) p.head[blockIdx.x] = hd;
+  } else if (warp < kMmaWarp) {
+    // ================= rows =================
+    int tiles = 0, segs = 0;
+    bool ok = issue;
+    if constexpr (kSrc == kSrcTma) {
+      const int R = p.box_rows, ng = kKeys / R;
+      int issued = 0;  // chunks of tile `tiles` under way
+      // the cache row of this lane's box of a tile (-1: nothing seen, -2: no page)
+      auto box_row = [&](const Keys& k, int b, int kt) -> int {
+        if (lane >= ng) return -1;
+        const int t0 = kt * kKeys + lane * R;
+        if (t0 > k.pos || !(t0 + R > k.lo || t0 < k.s0)) return -1;
+        const int blk = t0 / p.kv.page_size;
+        if (blk >= p.kv.max_pages) return -2;
+        const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
+        if (page < 0 || page >= p.kv.n_pages) return -2;
+        return page * p.kv.page_size + t0 % p.kv.page_size;
+      };
+      while (ok && w.next()) {
+        if (w.ta == w.tb) continue;
+        // the queries, once the previous segment's last product with them is done
+        const bool free_q = segs == 0 || wait_on(&c.q_empty, (segs - 1) & 1, dead, wait_ns);
+        if (!__all_sync(0xffffffffu, free_q)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&c.q_full, 8 * S::kQBlock);
+          for (int blk = 0; blk < 8; ++blk)
+            tma_load_2d(sb + S::kQ + blk * S::kQBlock, &q_map, blk * 64,
+                        w.token * p.Hm + w.h0 * kN, &c.q_full);
+        }
+        ++segs;
+        int row = box_row(w.k, w.b, w.k.tile(w.ta));
+        for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+          const int row_next = v + 1 < w.tb ? box_row(w.k, w.b, w.k.tile(v + 1)) : -1;
+          if (row == -2) {
+            flag(p.status, DSA_DEV_BAD_PAGE);
+            row = -1;
+          }
+          const unsigned boxes = __ballot_sync(0xffffffffu, row >= 0);
+          const uint32_t bytes = __popc(boxes) * R * 256;
+#pragma unroll 1
+          for (int mc = 0; mc < 4; ++mc) {
+            const bool room = tiles == 0 || wait_on(&c.empty[mc], (tiles - 1) & 1, dead, wait_ns);
+            ok = __all_sync(0xffffffffu, room);
+            if (!ok) break;
+            if (lane == 0) {
+              if (mc == 0) c.groups = boxes;  // the last tile's softmax has read its own
+              mbar_arrive_expect_tx(&c.full[mc], bytes);
+            }
+            issued = mc + 1;
+            __syncwarp();
+            if (row >= 0) {
+              unsigned char* dst = sb + S::kKv + 2 * mc * kKvBlock + lane * R * 128;
+              tma_load_2d(dst, &kv_map, mc * 128, row, &c.full[mc]);
+              tma_load_2d(dst + kKvBlock, &kv_map, mc * 128 + 64, row, &c.full[mc]);
+            }
+            if (p.prefetch && row_next >= 0) {
+              tma_prefetch_2d(&kv_map, mc * 128, row_next);
+              tma_prefetch_2d(&kv_map, mc * 128 + 64, row_next);
+            }
+          }
+          if (!ok) break;
+          issued = 0;
+          row = row_next;
+        }
+      }
+      // after a give-up: no copy into this CTA's memory may be in flight at its end
+      if (*dead && lane == 0) {
+        for (int mc = 0; mc < 4; ++mc)
+          if (mc < issued || tiles > 0)
+            mbar_wait_bounded(&c.full[mc], (mc < issued ? tiles : tiles - 1) & 1);
+        if (segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
+      }
+    } else {
+      const int lt = tid - kSoftThreads;  // 0..127: its row of every tile
+      // the cache row of position t (-1: not seen or no page)
+      auto row_of = [&](const Keys& k, int b, int t) -> int {
+        if (!k.sees(t)) return -1;
+        const int blk = t / p.kv.page_size;
+        int page = -1;
+        if (blk < p.kv.max_pages)
+          page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
+        if (page < 0 || page >= p.kv.n_pages) {
+          flag(p.status, DSA_DEV_BAD_PAGE);
+          return -1;
+        }
+        return page * p.kv.page_size + t % p.kv.page_size;
+      };
+      constexpr int kPer = kSrc == kSrcE4M3 ? 8 : 16;  // 16-byte pieces a thread and chunk
+      constexpr int kPieces = kSrc == kSrcE4M3 ? 8 : 16;  // of a row's chunk
+      constexpr int kRowBytes = kSrc == kSrcE4M3 ? kL : 2 * kL;
+      const unsigned char* pages = static_cast<const unsigned char*>(p.kv.pages);
+      while (ok && w.next()) {
+        if (w.ta == w.tb) continue;
+        if (segs > 0 && !wait_on(&c.q_empty, (segs - 1) & 1, dead, wait_ns)) {
+          ok = false;
+        } else if (lt == 0) {
+          mbar_arrive_expect_tx(&c.q_full, 8 * S::kQBlock);
+          for (int blk = 0; blk < 8; ++blk)
+            tma_load_2d(sb + S::kQ + blk * S::kQBlock, &q_map, blk * 64,
+                        w.token * p.Hm + w.h0 * kN, &c.q_full);
+        }
+        ++segs;
+        int row = row_of(w.k, w.b, w.k.tile(w.ta) * kKeys + lt);
+        for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+          c.prow[tiles & 1][lt] = row;
+          float rs = 0.f;
+          if (kSrc == kSrcE4M3 && row >= 0) rs = __ldg(p.kv.row_scale + row);
+          const bool seen = row >= 0;
+          row = v + 1 < w.tb ? row_of(w.k, w.b, w.k.tile(v + 1) * kKeys + lt) : -1;
+          if (row >= 0) {
+            const unsigned char* nx = pages + (long long)row * kRowBytes;
+#pragma unroll
+            for (int o = 0; o < kRowBytes; o += 128)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(nx + o));
+          }
+          sync_load();  // prow of this tile; the previous tile's reads of the other slot
+          const int* pr = c.prow[tiles & 1];
+#pragma unroll 1
+          for (int mc = 0; mc < 4; ++mc) {
+            uint4 raw[kPer];
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+              const int i = u * 128 + lt, rr = i / kPieces, pc = i % kPieces;
+              const int prow = pr[rr];
+              raw[u] = prow >= 0 ? __ldg(reinterpret_cast<const uint4*>(
+                                       pages + (long long)prow * kRowBytes +
+                                       (mc * kPieces + pc) * 16))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (ok && tiles > 0 && !wait_on(&c.empty[mc], (tiles - 1) & 1, dead, wait_ns))
+              ok = false;
+            if (mc == 0) {  // the last tile's softmax has read its own
+              c.valid[lt] = seen;
+              c.rs[lt] = rs;
+            }
+            unsigned char* dst = sb + S::kKv + 2 * mc * kKvBlock;
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+              const int i = u * 128 + lt, rr = i / kPieces, pc = i % kPieces;
+              if (kSrc == kSrcE4M3) {
+                const uint32_t x[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                  const int ch = 2 * pc + hf;
+                  *reinterpret_cast<uint4*>(dst + (ch >> 3) * kKvBlock + rr * 128 +
+                                            (((ch & 7) ^ (rr & 7)) << 4)) =
+                      make_uint4(e4m3x2_to_bf16x2(x[2 * hf] & 0xffffu),
+                                 e4m3x2_to_bf16x2(x[2 * hf] >> 16),
+                                 e4m3x2_to_bf16x2(x[2 * hf + 1] & 0xffffu),
+                                 e4m3x2_to_bf16x2(x[2 * hf + 1] >> 16));
+                }
+              } else {
+                *reinterpret_cast<uint4*>(dst + (pc >> 3) * kKvBlock + rr * 128 +
+                                          (((pc & 7) ^ (rr & 7)) << 4)) = raw[u];
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(&c.full[mc]);
+          }
+          // after a give-up every thread leaves at the same tile (nobody waits for
+          // the others in sync_load)
+          int stop = !ok;
+          asm volatile(
+              "{\n .reg .pred p, q;\n setp.ne.u32 p, %0, 0;\n"
+              " barrier.cta.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+              : "+r"(stop)::"memory");
+          if (stop) {
+            ok = false;
+            break;
+          }
+        }
+        int stop = !ok;
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %0, 0;\n"
+            " barrier.cta.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+            : "+r"(stop)::"memory");
+        ok = !stop;
+      }
+      if (*dead && lt == 0 && segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
+    }
+  } else if (lane == 0 && issue) {
+    // ================= MMA =================
+    constexpr uint32_t id_s = umma_idesc_bf16(kKeys, kN, false);
+    constexpr uint32_t id_o = umma_idesc_bf16(128, kN, true, true);
+    int tiles = 0, segs = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      if (w.ta == w.tb) continue;
+      if (!wait_on(&c.q_full, segs & 1, dead, wait_ns)) { ok = false; break; }
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+#pragma unroll
+        for (int mc = 0; mc < 4; ++mc) {
+          if (!wait_on(&c.full[mc], tiles & 1, dead, wait_ns)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t blk = 2 * mc + (j >> 2), off = (j & 3) * 32;
+            umma_bf16(tmem, sw128_desc(kvb + blk * kKvBlock + off),
+                      sw128_desc(qb + blk * S::kQBlock + off), id_s, (mc | j) ? 1u : 0u);
+          }
+        }
+        if (!ok) break;
+        umma_commit(&c.s_full);
+        if (v + 1 == w.tb) umma_commit(&c.q_empty);
+        if (!wait_on(&c.p_full, tiles & 1, dead, wait_ns)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int mc = 0; mc < 4; ++mc) {
+#pragma unroll
+          for (int kr = 0; kr < 8; ++kr) {
+            const uint64_t a = umma_desc_sw128(kvb + 2 * mc * kKvBlock + kr * 2048, kKvBlock, 1024);
+            const uint64_t b = kN == 64 ? umma_desc_sw128(pb + kr * 2048, kKeys * 128, 1024)
+                                        : umma_desc_sw64(pb + kr * 1024, kKeys * 64, 512);
+            umma_bf16(tmem + kN + mc * kN, a, b, id_o, (v > w.ta || kr > 0) ? 1u : 0u);
+          }
+          umma_commit(&c.empty[mc]);
+        }
+      }
+      if (!ok) break;
+      umma_commit(&c.o_full);
+      ++segs;
+    }
+    if (!ok) {  // drain what was issued before the CTA's memory is given back
+      umma_commit(&c.drain);
+      mbar_wait_bounded(&c.drain, 0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && c.dead) flag(p.status, DSA_DEV_TIMEOUT);  // outputs unspecified
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc<kTmemCols>(tmem);
+  }
+}
+
+// Join the partials of the row tiles that were split over CTAs, in CTA order: block
+// (g, y) takes the tile that CTA g began, heads 8 y ... (one warp per head, four
+// 16-byte pieces of the latent row a lane).
+template <int kN>
+__global__ void __launch_bounds__(256)
+    mla_chunk_join_kernel(const Params p, int n_cta) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int g = blockIdx.x, lane = threadIdx.x & 31;
+  const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int tile = p.head[g].start_tile;
+  if (tile < 0) return;
+  const int hb = (p.Hm + kN - 1) / kN;
+  const int token = tile / hb, head = (tile - token * hb) * kN + h;
+  if (head >= p.Hm) return;
+  float mx = -INFINITY, den = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = g; s < n_cta; ++s) {
+    int slot = 2 * g + 1;
+    bool last = false;
+    if (s > g) {
+      const Header hd = p.head[s];
+      if (hd.cont_tile == -2) continue;
+      if (hd.cont_tile != tile) break;
+      last = hd.cont_ends;
+      slot = 2 * s;
+      if (!hd.cont_some) {
+        if (last) break;
+        continue;
+      }
+    }
+    const float2 ml = p.part_ml[slot * kN + h];
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + ((long long)slot * kN + h) * kL);
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __ldcs(src + i * 32 + lane);
+    if (ml.y != 0.f) {  // a part that saw no page has nothing to add
+      const float m = fmaxf(mx, ml.x), ref = m == -INFINITY ? 0.f : m;
+      const float a = ex2_fast(mx - ref), b = ex2_fast(ml.x == -INFINITY ? 0.f : ml.x - ref);
+      den = den * a + ml.y * b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i].x = acc[i].x * a + v[i].x * b;
+        acc[i].y = acc[i].y * a + v[i].y * b;
+        acc[i].z = acc[i].z * a + v[i].z * b;
+        acc[i].w = acc[i].w * a + v[i].w * b;
+      }
+      mx = m;
+    }
+    if (last) break;
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const long long row = (long long)token * p.Hm + head;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint2*>(p.out + row * kL + (i * 32 + lane) * 4) =
+        make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv),
+                   pack_bf16(acc[i].z * inv, acc[i].w * inv));
+  if (p.lse && lane == 0) p.lse[row] = den == 0.f ? -INFINITY : (mx + log2f(den)) / kLog2e;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// [rows, 512] bf16, boxes of 64 columns x box_rows rows, 128-byte swizzle; rows at
+// or beyond `rows` read as zeros.
+bool row_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)kL, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kL * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int box_rows_of(int page_size) {  // largest power of two that divides it, 128 at most
+  const int r = page_size & -page_size;
+  return r > kKeys ? kKeys : r;
+}
+
+template <int kN>
+size_t workspace_bytes(int n_cta) {
+  return (size_t)n_cta * 2 * kN * (kL * 4 + 8) + (size_t)n_cta * sizeof(Header);
+}
+
+template <int kN, int kSrc>
+int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
+  const int n_cta = num_sms();
+  Params p = {};
+  p.kv = a.kv;
+  p.cu_new = a.cu_new;
+  p.T = a.T;
+  p.B = a.B;
+  p.Hm = a.Hm;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.zscale = a.sm_scale * kLog2e;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.status = a.status;
+  p.drill = failure_drill();
+  // rows that few tokens share come from HBM: the tile after the next is brought
+  // into L2 meanwhile
+  p.prefetch = a.T <= 4 * a.B;
+  p.box_rows = box_rows_of(a.kv.page_size);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)n_cta * 2 * kN * kL);
+  p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)n_cta * 2 * kN);
+  CUtensorMap q_map, kv_map;
+  if (!row_map(&q_map, a.q_lat, (uint64_t)a.T * a.Hm, kN)) return DSA_ERR_CUDA;
+  kv_map = q_map;
+  if (kSrc == kSrcTma &&
+      !row_map(&kv_map, a.kv.pages, (uint64_t)a.kv.n_pages * a.kv.page_size, p.box_rows))
+    return DSA_ERR_CUDA;
+  auto kernel = mla_chunk_kernel<kN, kSrc>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)Smem<kN>::kBytes) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(n_cta, 1, 1);
+  cfg.blockDim = dim3(cta_threads(kSrc), 1, 1);
+  cfg.dynamicSmemBytes = Smem<kN>::kBytes;
+  if (launch_kernel(&cfg, kernel, q_map, kv_map, p) != cudaSuccess) return DSA_ERR_CUDA;
+  cfg.gridDim = dim3(n_cta, kN / 8, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return launch_kernel(&cfg, mla_chunk_join_kernel<kN>, p, n_cta) == cudaSuccess ? DSA_OK
+                                                                                 : DSA_ERR_CUDA;
+}
+
+template <int kN>
+int launch_src(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
+  if (a.kv.kv_dtype == DSA_FP8_E4M3) return launch<kN, kSrcE4M3>(a, workspace, stream);
+  if (a.kv.page_size % 8 == 0) return launch<kN, kSrcTma>(a, workspace, stream);
+  return launch<kN, kSrcCopy>(a, workspace, stream);
+}
+
+}  // namespace
+
+bool mla_chunk_umma_ok(int L, int dtype, int kv_dtype) {
+  return L == kL && dtype == DSA_BF16 && (kv_dtype == DSA_BF16 || kv_dtype == DSA_FP8_E4M3);
+}
+
+size_t mla_chunk_umma_workspace_size(int Hm) {
+  return Hm <= 32 ? workspace_bytes<32>(num_sms()) : workspace_bytes<64>(num_sms());
+}
+
+int launch_mla_chunk_umma(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
+  return a.Hm <= 32 ? launch_src<32>(a, workspace, stream)
+                    : launch_src<64>(a, workspace, stream);
+}
+
+}  // namespace dsa
