@@ -52,12 +52,17 @@ constexpr float kRaiseAt = 20.f;
 constexpr int kKvBlock = kKeys * 128;  // 128 rows x 64 latent columns, 16 KB
 constexpr int kSoftThreads = 256;      // warps 0..7
 
-// Row sources: TMA boxes of bf16 rows (page size a multiple of 8), or four warps
-// that copy bf16 rows of any page size, or convert E4M3 codes.
-constexpr int kSrcTma = 0, kSrcCopy = 1, kSrcE4M3 = 2;
-__host__ __device__ constexpr int load_warps(int src) { return src == kSrcTma ? 1 : 4; }
+// Row sources: TMA boxes of bf16 rows or of E4M3 codes, which four warps then widen
+// in place (page size a multiple of 8); or, for any page size, four warps that copy
+// bf16 rows or widen E4M3 rows from global memory.
+constexpr int kSrcTma = 0, kSrcCopy = 1, kSrcCopy8 = 2, kSrcTma8 = 3;
+__host__ __device__ constexpr bool is_tma(int src) { return src == kSrcTma || src == kSrcTma8; }
+__host__ __device__ constexpr bool is_e4m3(int src) { return src == kSrcCopy8 || src == kSrcTma8; }
+// warps 8..: the TMA warp, then the row warps, then the MMA warp
+__host__ __device__ constexpr int tma_warps(int src) { return is_tma(src) ? 1 : 0; }
+__host__ __device__ constexpr int row_warps(int src) { return src == kSrcTma ? 0 : 4; }
 __host__ __device__ constexpr int cta_threads(int src) {
-  return kSoftThreads + 32 * load_warps(src) + 32;
+  return kSoftThreads + 32 * (tma_warps(src) + row_warps(src) + 1);
 }
 
 struct Header {        // what CTA g left for the join
@@ -68,16 +73,16 @@ struct Header {        // what CTA g left for the join
 };
 
 struct Ctl {
-  float m[64], alpha[64], l[64];  // per head; first: read as float4
+  float m[64], nm[64], alpha[64], l[64];  // per head; first: read as float4
   float red[4][64];
   float rs[kKeys];
   int valid[kKeys];               // copied rows: the position is seen and has a page
   int prow[2][kKeys];
-  uint64_t full[4], empty[4], s_full, p_full, o_full, q_full, q_empty, drain;
+  uint64_t full[4], empty[4], raw[4], s_full, p_full, o_full, q_full, q_empty, drain;
   unsigned long long scan[32];
-  unsigned long long start_off;   // first unit within start_b
   uint32_t tmem;
-  int start_b;
+  int start_b;                    // the CTA's first unit: sequence (B: no share),
+  unsigned start_row, start_unit; // row tile of it, unit of that
   unsigned groups;                // TMA boxes of the tile that hold rows
   int raise;
   int soft_dead[2];
@@ -108,69 +113,83 @@ struct Params {
   Header* head;
   int32_t* status;
   int drill, prefetch;
-  int box_rows;
+  int box_log;               // rows of a TMA box, 2^box_log (copied rows: 1)
 };
 
 // ---- the batch as units ------------------------------------------------------
 struct Seq {
   int c0, n, base;             // rows c0 .. c0 + n - 1 of the step; position of the first
-  unsigned long long u;        // units per row tile
+  unsigned u;                  // units per row tile
 };
 __device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p) {
   Seq s;
   s.c0 = min(max(cu0, 0), p.T);
   s.n = max(min(cu1, p.T) - s.c0, 0);
   s.base = len < 0 ? -s.n : len - s.n;   // negative: rows before position 0
-  const int all = max(len, 0);
-  long long u = ((long long)all + kKeys - 1) / kKeys;
+  const unsigned all = (unsigned)max(len, 0);
+  s.u = (all + kKeys - 1) / kKeys;
   if (p.window > 0) {
-    const long long w = ((long long)p.window + kKeys - 2) / kKeys + 1 +
-                        ((long long)p.sinks + kKeys - 1) / kKeys;
-    if (w < u) u = w;
+    const long long R = 1 << p.box_log;
+    const long long keys = ((p.sinks + R - 1) / R + (p.window + R - 2) / R + 1) * R;
+    if ((keys + kKeys - 1) / kKeys < (long long)s.u) s.u = (unsigned)((keys + kKeys - 1) / kKeys);
   }
-  s.u = u > 1 ? (unsigned long long)u : 1ull;
+  s.u = max(s.u, 1u);
   return s;
 }
 
-// One token's visible positions [0, s0) and [lo, pos], as key tiles.
+// One token's visible positions [0, s0) and [lo, pos] as boxes of R = 2^log
+// positions (aligned; the window's first and last may reach past it), 128 / R to a
+// key tile.
 struct Keys {
-  int pos, lo, s0, sink_tiles, first, n;
-  __device__ __forceinline__ int tile(int v) const {
-    return v < sink_tiles ? v : first + (v - sink_tiles);
+  int pos, lo, s0, log, sink_boxes, first, boxes, n;
+  // position of row r of key tile v (past the last box: past pos)
+  __device__ __forceinline__ int at(int v, int r) const {
+    const int g = (v << (7 - log)) + (r >> log);
+    const int box = g < sink_boxes ? g : first + (g - sink_boxes);
+    return g < boxes ? (box << log) + (r & ((1 << log) - 1)) : 0x7fffffff;
   }
   __device__ __forceinline__ bool sees(int t) const { return t <= pos && (t >= lo || t < s0); }
 };
 __device__ __forceinline__ Keys keys_of(int pos, const Params& p) {
   Keys k;
   k.pos = pos;
+  k.log = p.box_log;
   k.lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
   k.s0 = min(p.sinks, k.lo);
-  k.first = k.lo / kKeys;
-  k.sink_tiles = min((k.s0 + kKeys - 1) / kKeys, k.first);
-  k.n = pos < 0 ? 0 : k.sink_tiles + pos / kKeys - k.first + 1;
+  k.first = k.lo >> k.log;
+  k.sink_boxes = min((k.s0 >> k.log) + ((k.s0 & ((1 << k.log) - 1)) != 0), k.first);
+  k.boxes = pos < 0 ? 0 : k.sink_boxes + (pos >> k.log) - k.first + 1;
+  k.n = (k.boxes + (1 << (7 - k.log)) - 1) >> (7 - k.log);
   return k;
+}
+
+// a n / u, rounded down
+__device__ __forceinline__ int share_of(unsigned a, unsigned n, unsigned u) {
+  if (a == 0) return 0;
+  if (a == u) return (int)n;
+  if ((a | n) < 65536u) return (int)(a * n / u);
+  return (int)((unsigned long long)a * n / u);
 }
 
 // A walk over the CTA's units, row tile by row tile.  Every role walks alone; the
 // next sequence's lengths are read one sequence ahead.
 struct Walk {
   const Params& p;
-  int hb;                       // head blocks per token
+  int hb;                       // head blocks per token: 1 or 2
   unsigned long long left;      // units still to do
-  unsigned long long off;       // units done of the current sequence
   int b;
+  unsigned row, unit;           // of sequence b: row tile, unit of it
   Seq s;
   int cu_next, len_next;        // of sequence b + 1 (its end, its length)
   // the current segment
   int token, h0, tile_id, ta, tb;
   Keys k;
 
-  __device__ __forceinline__ Walk(const Params& pp, int hb_, int b0, unsigned long long off0,
-                                  unsigned long long n)
-      : p(pp), hb(hb_), left(n), off(off0), b(b0) {
+  __device__ __forceinline__ Walk(const Params& pp, int hb_, const Ctl& c, unsigned long long n)
+      : p(pp), hb(hb_), left(c.start_b < pp.B ? n : 0), b(c.start_b), row(c.start_row),
+        unit(c.start_unit) {
     if (left == 0) return;
-    const int cu0 = __ldg(p.cu_new + b), cu1 = __ldg(p.cu_new + b + 1);
-    s = seq_of(cu0, cu1, __ldg(p.kv.seq_lens + b), p);
+    s = seq_of(__ldg(p.cu_new + b), __ldg(p.cu_new + b + 1), __ldg(p.kv.seq_lens + b), p);
     ahead();
   }
   __device__ __forceinline__ void ahead() {
@@ -182,28 +201,28 @@ struct Walk {
   // the next segment: a row tile and its key tiles [ta, tb) (none: ta == tb)
   __device__ __forceinline__ bool next() {
     if (left == 0) return false;
-    unsigned long long all = (unsigned long long)s.n * hb * s.u;
-    while (off >= all) {  // units remain, so a sequence with some follows
-      if (++b >= p.B) return false;  // (lengths that changed under the call)
+    while (row >= (unsigned)s.n * hb) {  // units remain, so a sequence with some follows
+      if (++b >= p.B) return false;      // (lengths that changed under the call)
       const int cu0 = __ldg(p.cu_new + b);
       s = seq_of(cu0, cu_next, len_next, p);
       ahead();
-      off = 0;
-      all = (unsigned long long)s.n * hb * s.u;
+      row = 0;
     }
-    const unsigned long long r = off / s.u;
-    const unsigned long long a = off - r * s.u;
-    const unsigned long long e = min(s.u, a + left);
-    const int kk = (int)(r / hb), hblk = (int)(r - (unsigned long long)kk * hb);
+    const unsigned e = left < s.u - unit ? unit + (unsigned)left : s.u;
+    const int kk = (int)(hb == 2 ? row >> 1 : row);
+    h0 = hb == 2 ? (int)(row & 1u) : 0;
     const int i = (kk & 1) ? s.n - 1 - (kk >> 1) : kk >> 1;  // from both ends in turn
     token = s.c0 + i;
-    h0 = hblk;
-    tile_id = token * hb + hblk;
+    tile_id = token * hb + h0;
     k = keys_of(s.base + i < 0 ? -1 : s.base + i, p);
-    ta = (int)(a * k.n / s.u);
-    tb = (int)(e * k.n / s.u);
-    off += e - a;
-    left -= e - a;
+    ta = share_of(unit, k.n, s.u);
+    tb = share_of(e, k.n, s.u);
+    left -= e - unit;
+    unit = e;
+    if (e == s.u) {
+      unit = 0;
+      ++row;
+    }
     return true;
   }
 };
@@ -328,7 +347,8 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
                      const __grid_constant__ CUtensorMap kv_map, const Params p) {
   using S = Smem<kN>;
   constexpr int kW = kN / 2;  // heads per softmax thread
-  constexpr int kLoad0 = kSoftThreads / 32, kMmaWarp = kLoad0 + load_warps(kSrc);
+  constexpr int kLoad0 = kSoftThreads / 32, kRow0 = kLoad0 + tma_warps(kSrc),
+                kMmaWarp = kRow0 + row_warps(kSrc);
   constexpr int kTmemCols = kN == 64 ? 512 : 256;  // S^T (kN), O^T (4 kN)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -338,7 +358,8 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&c.full[i], kSrc == kSrcTma ? 1 : load_warps(kSrc));
+      mbar_init(&c.full[i], kSrc == kSrcTma ? 1 : row_warps(kSrc));
+      mbar_init(&c.raw[i], 1);
       mbar_init(&c.empty[i], 1);
     }
     mbar_init(&c.s_full, 1);
@@ -355,7 +376,10 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
     tmem_alloc<kTmemCols>(&c.tmem);
     tc_fence_before();
   }
-  if (tid < 64) c.m[tid] = -INFINITY;
+  if (tid < 64) {
+    c.m[tid] = -INFINITY;
+    c.nm[tid] = 0.f;
+  }
   pdl_wait();  // every input may come from the kernel just before
   pdl_launch_dependents();
 
@@ -370,7 +394,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       const int cu0 = p.cu_new[b], cu1 = p.cu_new[b + 1], len = p.kv.seq_lens[b];
       const Seq s = seq_of(cu0, cu1, len, p);
       odd |= cu0 < 0 || cu1 < cu0 || cu1 > p.T || (s.n > 0 && s.base < 0);
-      mine += (unsigned long long)s.n * hb * s.u;
+      mine += (unsigned long long)s.n * (unsigned)hb * s.u;
     }
     if (odd && blockIdx.x == 0) flag(p.status, DSA_DEV_BAD_LENGTH);
     unsigned long long inc = mine;
@@ -386,16 +410,23 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       if (w < warp) before += c.scan[w];
       total += c.scan[w];
     }
-    v0 = total * blockIdx.x / gridDim.x;
-    v1 = total * (blockIdx.x + 1) / gridDim.x;
+    if (total < (1ull << 32) / 256) {  // (fewer than 256 CTAs: a product of 32 bits)
+      v0 = (unsigned)total * blockIdx.x / gridDim.x;
+      v1 = (unsigned)total * (blockIdx.x + 1) / gridDim.x;
+    } else {
+      v0 = total * blockIdx.x / gridDim.x;
+      v1 = total * (blockIdx.x + 1) / gridDim.x;
+    }
     if (v0 < v1 && v0 >= before && v0 < before + mine) {
       unsigned long long at = before;
       for (int b = b0; b < b1; ++b) {
         const Seq s = seq_of(p.cu_new[b], p.cu_new[b + 1], p.kv.seq_lens[b], p);
-        const unsigned long long all = (unsigned long long)s.n * hb * s.u;
+        const unsigned long long all = (unsigned long long)s.n * (unsigned)hb * s.u;
         if (v0 < at + all) {
+          const unsigned long long off = v0 - at;
           c.start_b = b;
-          c.start_off = v0 - at;
+          c.start_row = (unsigned)(off >> 32 ? off / s.u : (unsigned)off / s.u);
+          c.start_unit = (unsigned)(off - (unsigned long long)c.start_row * s.u);
           break;
         }
         at += all;
@@ -407,7 +438,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
   }
   const uint32_t tmem = c.tmem;
   const bool any = c.start_b < p.B;
-  Walk w(p, hb, any ? c.start_b : 0, any ? c.start_off : 0ull, any ? v1 - v0 : 0ull);
+  Walk w(p, hb, c, v1 - v0);
   // a failure drill loads nothing and issues no MMA: the first waits run out
   const bool issue = p.drill == 0;
   const unsigned long long wait_ns = p.drill ? kDrillWaitNs : kWaitNs;
@@ -425,35 +456,41 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
     int tiles = 0, segs = 0;      // waits so far
     bool ok = true;
     while (ok && w.next()) {
-      float l[kW], nm[kW];        // this row's sums; minus the reference (0: none yet)
-      bool unset = true;
+      float l[kW];                // this row's sums
+      bool unset = true;          // some head here has no reference yet
 #pragma unroll
-      for (int i = 0; i < kW; ++i) l[i] = nm[i] = 0.f;
+      for (int i = 0; i < kW; ++i) l[i] = 0.f;
       for (int v = w.ta; v < w.tb; ++v, ++tiles) {
-        const int t = w.k.tile(v) * kKeys + r;
+        const int t = w.k.at(v, r);
         if (!wait_on(&c.s_full, tiles & 1, dead, wait_ns)) c.soft_dead[tiles & 1] = 1;
         tc_fence_after();
         float e[kW];
         tmem_ldw<kW>(tl + hq * kW, e);
         bool valid;
         float rs = 1.f;
-        if constexpr (kSrc == kSrcTma) {
-          valid = w.k.sees(t) && ((c.groups >> (r / p.box_rows)) & 1u);
+        if constexpr (is_tma(kSrc)) {
+          valid = w.k.sees(t) && ((c.groups >> (r >> w.k.log)) & 1u);
           if (!valid) {  // the half of this row that this thread clears
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
             for (int blk = 4 * hq; blk < 4 * hq + 4; ++blk)
-              for (int ch = 0; ch < 8; ++ch)
-                *reinterpret_cast<uint4*>(sb + S::kKv + blk * kKvBlock + r * 128 + ch * 16) = zero;
+#pragma unroll
+              for (int ch = 0; ch < 8; ++ch)  // (neighbouring rows in different banks)
+                *reinterpret_cast<uint4*>(sb + S::kKv + blk * kKvBlock + r * 128 +
+                                          ((ch ^ (r & 7)) << 4)) = zero;
           }
         } else {
           valid = c.valid[r] != 0;
-          if constexpr (kSrc == kSrcE4M3) rs = c.rs[r];
         }
-        const float zs = kSrc == kSrcE4M3 ? p.zscale * rs : p.zscale;
+        if constexpr (is_e4m3(kSrc)) rs = valid ? c.rs[r] : 0.f;
+        const float zs = is_e4m3(kSrc) ? p.zscale * rs : p.zscale;
         bool high = unset;
 #pragma unroll
-        for (int i = 0; i < kW; i += 2) fma2(e[i], e[i + 1], zs, nm[i], nm[i + 1]);
+        for (int q = 0; q < kW / 4; ++q) {  // minus the references (0: none yet)
+          const float4 nm = reinterpret_cast<const float4*>(c.nm + hq * kW)[q];
+          fma2(e[4 * q], e[4 * q + 1], zs, nm.x, nm.y);
+          fma2(e[4 * q + 2], e[4 * q + 3], zs, nm.z, nm.w);
+        }
 #pragma unroll
         for (int i = 0; i < kW; ++i) {
           e[i] = valid ? e[i] : -INFINITY;
@@ -487,15 +524,12 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
               c.raise = 1;
             }
             c.alpha[tid] = a;
+            c.nm[tid] = c.m[tid] == -INFINITY ? 0.f : -c.m[tid];
           }
           sync_soft();
           unset = false;
 #pragma unroll
-          for (int i = 0; i < kW; ++i) {
-            const float mm = c.m[hq * kW + i];
-            nm[i] = mm == -INFINITY ? 0.f : -mm;
-            unset |= mm == -INFINITY;
-          }
+          for (int i = 0; i < kW; ++i) unset |= c.m[hq * kW + i] == -INFINITY;
           if (c.raise) {  // O^T of the tiles so far is complete: S^T came after it
 #pragma unroll
             for (int i = 0; i < kW; ++i) l[i] *= c.alpha[hq * kW + i];
@@ -513,7 +547,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
           }
           tmem_ldw<kW>(tl + hq * kW, e);
 #pragma unroll
-          for (int i = 0; i < kW; ++i) e[i] = valid ? fmaf(e[i], zs, nm[i]) : -INFINITY;
+          for (int i = 0; i < kW; ++i) e[i] = valid ? fmaf(e[i], zs, c.nm[hq * kW + i]) : -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < kW; ++i) e[i] = ex2_fast(e[i]);
@@ -521,7 +555,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         // weights.  An E4M3 row's scale goes to its weights, so the tile holds codes.
 #pragma unroll
         for (int q = 0; q < kW / 8; ++q) {
-          const float sc = kSrc == kSrcE4M3 ? rs : 1.f;
+          const float sc = is_e4m3(kSrc) ? rs : 1.f;
           const uint4 pk4 = make_uint4(pack_bf16(e[8 * q] * sc, e[8 * q + 1] * sc),
                                  pack_bf16(e[8 * q + 2] * sc, e[8 * q + 3] * sc),
                                  pack_bf16(e[8 * q + 4] * sc, e[8 * q + 5] * sc),
@@ -573,6 +607,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         const float sum = (c.red[0][tid] + c.red[1][tid]) + (c.red[2][tid] + c.red[3][tid]);
         const float m = c.m[tid];
         c.m[tid] = -INFINITY;
+        c.nm[tid] = 0.f;
         if (whole) {
           c.l[tid] = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
           if (p.lse && tid < heads)
@@ -622,18 +657,18 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
     }
     if (!ok) hd = Header{-1, -1, 0, 0};
     if (tid == 0 && p.head) p.head[blockIdx.x] = hd;
-  } else if (warp < kMmaWarp) {
-    // ================= rows =================
+  } else if (warp < kRow0) {
+    // ================= TMA =================
     int tiles = 0, segs = 0;
     bool ok = issue;
-    if constexpr (kSrc == kSrcTma) {
-      const int R = p.box_rows, ng = kKeys / R;
+    {
+      const int R = 1 << p.box_log, ng = kKeys >> p.box_log;
       int issued = 0;  // chunks of tile `tiles` under way
       // the cache row of this lane's box of a tile (-1: nothing seen, -2: no page)
-      auto box_row = [&](const Keys& k, int b, int kt) -> int {
+      auto box_row = [&](const Keys& k, int b, int v) -> int {
         if (lane >= ng) return -1;
-        const int t0 = kt * kKeys + lane * R;
-        if (t0 > k.pos || !(t0 + R > k.lo || t0 < k.s0)) return -1;
+        const int t0 = k.at(v, lane * R);
+        if (t0 > k.pos) return -1;
         const int blk = t0 / p.kv.page_size;
         if (blk >= p.kv.max_pages) return -2;
         const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
@@ -642,6 +677,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       };
       while (ok && w.next()) {
         if (w.ta == w.tb) continue;
+        int row = box_row(w.k, w.b, w.ta);
         // the queries, once the previous segment's last product with them is done
         const bool free_q = segs == 0 || wait_on(&c.q_empty, (segs - 1) & 1, dead, wait_ns);
         if (!__all_sync(0xffffffffu, free_q)) break;
@@ -652,15 +688,15 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
                         w.token * p.Hm + w.h0 * kN, &c.q_full);
         }
         ++segs;
-        int row = box_row(w.k, w.b, w.k.tile(w.ta));
         for (int v = w.ta; v < w.tb; ++v, ++tiles) {
-          const int row_next = v + 1 < w.tb ? box_row(w.k, w.b, w.k.tile(v + 1)) : -1;
+          const int row_next = v + 1 < w.tb ? box_row(w.k, w.b, v + 1) : -1;
           if (row == -2) {
             flag(p.status, DSA_DEV_BAD_PAGE);
             row = -1;
           }
           const unsigned boxes = __ballot_sync(0xffffffffu, row >= 0);
-          const uint32_t bytes = __popc(boxes) * R * 256;
+          const uint32_t bytes = __popc(boxes) * R * (kSrc == kSrcTma ? 256 : 128);
+          uint64_t* land = kSrc == kSrcTma ? c.full : c.raw;
 #pragma unroll 1
           for (int mc = 0; mc < 4; ++mc) {
             const bool room = tiles == 0 || wait_on(&c.empty[mc], (tiles - 1) & 1, dead, wait_ns);
@@ -668,18 +704,19 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
             if (!ok) break;
             if (lane == 0) {
               if (mc == 0) c.groups = boxes;  // the last tile's softmax has read its own
-              mbar_arrive_expect_tx(&c.full[mc], bytes);
+              mbar_arrive_expect_tx(&land[mc], bytes);
             }
             issued = mc + 1;
             __syncwarp();
             if (row >= 0) {
               unsigned char* dst = sb + S::kKv + 2 * mc * kKvBlock + lane * R * 128;
-              tma_load_2d(dst, &kv_map, mc * 128, row, &c.full[mc]);
-              tma_load_2d(dst + kKvBlock, &kv_map, mc * 128 + 64, row, &c.full[mc]);
+              tma_load_2d(dst, &kv_map, mc * 128, row, &land[mc]);
+              if (kSrc == kSrcTma)
+                tma_load_2d(dst + kKvBlock, &kv_map, mc * 128 + 64, row, &land[mc]);
             }
             if (p.prefetch && row_next >= 0) {
               tma_prefetch_2d(&kv_map, mc * 128, row_next);
-              tma_prefetch_2d(&kv_map, mc * 128 + 64, row_next);
+              if (kSrc == kSrcTma) tma_prefetch_2d(&kv_map, mc * 128 + 64, row_next);
             }
           }
           if (!ok) break;
@@ -691,14 +728,79 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       if (*dead && lane == 0) {
         for (int mc = 0; mc < 4; ++mc)
           if (mc < issued || tiles > 0)
-            mbar_wait_bounded(&c.full[mc], (mc < issued ? tiles : tiles - 1) & 1);
+            mbar_wait_bounded(&(kSrc == kSrcTma ? c.full : c.raw)[mc],
+                              (mc < issued ? tiles : tiles - 1) & 1);
         if (segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
       }
+    }
+  } else if (warp < kMmaWarp) {
+    // ================= rows =================
+    int tiles = 0, segs = 0;
+    bool ok = issue;
+    const int lt = tid - 32 * kRow0;  // 0..127: its row of every tile
+    if constexpr (kSrc == kSrcTma8) {
+      // Widen a chunk of codes in place: 128 rows of 128 codes land in its first
+      // block, every thread takes 8 of their 16-byte pieces into registers, and once
+      // all have, both blocks take the bf16 rows.
+      auto scale_of = [&](const Keys& k, int b, int v) -> float {
+        const int t = k.at(v, lt);
+        if (!k.sees(t)) return 0.f;
+        const int blk = t / p.kv.page_size;
+        if (blk >= p.kv.max_pages) return 0.f;
+        const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
+        if (page < 0 || page >= p.kv.n_pages) return 0.f;
+        return __ldg(p.kv.row_scale + (long long)page * p.kv.page_size + t % p.kv.page_size);
+      };
+      while (ok && w.next()) {
+        float rs = w.ta < w.tb ? scale_of(w.k, w.b, w.ta) : 0.f;
+        for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+          const float rs_next = v + 1 < w.tb ? scale_of(w.k, w.b, v + 1) : 0.f;
+#pragma unroll 1
+          for (int mc = 0; mc < 4; ++mc) {
+            // (the codes' landing implies that the chunk was free)
+            ok = ok && wait_on(&c.raw[mc], tiles & 1, dead, wait_ns);
+            unsigned char* dst = sb + S::kKv + 2 * mc * kKvBlock;
+            uint4 raw[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              raw[u] = *reinterpret_cast<const uint4*>(dst + (u * 128 + lt) * 16);
+            int stop = !ok;  // every thread leaves at the same chunk
+            asm volatile(
+                "{\n .reg .pred p, q;\n setp.ne.u32 p, %0, 0;\n"
+                " barrier.cta.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+                : "+r"(stop)::"memory");
+            if (stop) {
+              ok = false;
+              break;
+            }
+            if (mc == 0) c.rs[lt] = rs;  // the last tile's softmax has read its own
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int i = u * 128 + lt, rr = i >> 3, pc = i & 7;
+              const uint32_t x[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const int ch = 2 * pc + hf;
+                *reinterpret_cast<uint4*>(dst + (ch >> 3) * kKvBlock + rr * 128 +
+                                          (((ch & 7) ^ (rr & 7)) << 4)) =
+                    make_uint4(e4m3x2_to_bf16x2(x[2 * hf] & 0xffffu),
+                               e4m3x2_to_bf16x2(x[2 * hf] >> 16),
+                               e4m3x2_to_bf16x2(x[2 * hf + 1] & 0xffffu),
+                               e4m3x2_to_bf16x2(x[2 * hf + 1] >> 16));
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(&c.full[mc]);
+          }
+          if (!ok) break;
+          rs = rs_next;
+        }
+      }
     } else {
-      const int lt = tid - kSoftThreads;  // 0..127: its row of every tile
       // the cache row of position t (-1: not seen or no page)
       auto row_of = [&](const Keys& k, int b, int t) -> int {
-        if (!k.sees(t)) return -1;
+        if (t > k.pos) return -1;  // (single positions: none but visible ones)
         const int blk = t / p.kv.page_size;
         int page = -1;
         if (blk < p.kv.max_pages)
@@ -709,9 +811,9 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         }
         return page * p.kv.page_size + t % p.kv.page_size;
       };
-      constexpr int kPer = kSrc == kSrcE4M3 ? 8 : 16;  // 16-byte pieces a thread and chunk
-      constexpr int kPieces = kSrc == kSrcE4M3 ? 8 : 16;  // of a row's chunk
-      constexpr int kRowBytes = kSrc == kSrcE4M3 ? kL : 2 * kL;
+      constexpr int kPer = kSrc == kSrcCopy8 ? 8 : 16;  // 16-byte pieces a thread and chunk
+      constexpr int kPieces = kSrc == kSrcCopy8 ? 8 : 16;  // of a row's chunk
+      constexpr int kRowBytes = kSrc == kSrcCopy8 ? kL : 2 * kL;
       const unsigned char* pages = static_cast<const unsigned char*>(p.kv.pages);
       while (ok && w.next()) {
         if (w.ta == w.tb) continue;
@@ -724,33 +826,39 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
                         w.token * p.Hm + w.h0 * kN, &c.q_full);
         }
         ++segs;
-        int row = row_of(w.k, w.b, w.k.tile(w.ta) * kKeys + lt);
+        int row = row_of(w.k, w.b, w.k.at(w.ta, lt));
         for (int v = w.ta; v < w.tb; ++v, ++tiles) {
-          c.prow[tiles & 1][lt] = row;
+          // this tile's rows (in its slot since the tile before, but for the first)
+          // and the next one's
+          if (v == w.ta) c.prow[tiles & 1][lt] = row;
           float rs = 0.f;
-          if (kSrc == kSrcE4M3 && row >= 0) rs = __ldg(p.kv.row_scale + row);
+          if (kSrc == kSrcCopy8 && row >= 0) rs = __ldg(p.kv.row_scale + row);
           const bool seen = row >= 0;
-          row = v + 1 < w.tb ? row_of(w.k, w.b, w.k.tile(v + 1) * kKeys + lt) : -1;
+          row = v + 1 < w.tb ? row_of(w.k, w.b, w.k.at(v + 1, lt)) : -1;
           if (row >= 0) {
             const unsigned char* nx = pages + (long long)row * kRowBytes;
 #pragma unroll
             for (int o = 0; o < kRowBytes; o += 128)
               asm volatile("prefetch.global.L2 [%0];" ::"l"(nx + o));
           }
-          sync_load();  // prow of this tile; the previous tile's reads of the other slot
-          const int* pr = c.prow[tiles & 1];
-#pragma unroll 1
-          for (int mc = 0; mc < 4; ++mc) {
-            uint4 raw[kPer];
+          c.prow[(tiles + 1) & 1][lt] = row;
+          sync_load();
+          uint4 raw[kPer];
+          auto fetch = [&](int mc) {
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
               const int i = u * 128 + lt, rr = i / kPieces, pc = i % kPieces;
-              const int prow = pr[rr];
+              const int prow = c.prow[tiles & 1][rr];
               raw[u] = prow >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                       pages + (long long)prow * kRowBytes +
-                                       (mc * kPieces + pc) * 16))
-                                 : make_uint4(0u, 0u, 0u, 0u);
+                                     pages + (long long)prow * kRowBytes +
+                                     (mc * kPieces + pc) * 16))
+                               : make_uint4(0u, 0u, 0u, 0u);
             }
+          };
+          fetch(0);
+#pragma unroll 1
+          for (int mc = 0; mc < 4; ++mc) {
+            if (mc > 0) fetch(mc);
             if (ok && tiles > 0 && !wait_on(&c.empty[mc], (tiles - 1) & 1, dead, wait_ns))
               ok = false;
             if (mc == 0) {  // the last tile's softmax has read its own
@@ -761,7 +869,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
               const int i = u * 128 + lt, rr = i / kPieces, pc = i % kPieces;
-              if (kSrc == kSrcE4M3) {
+              if (kSrc == kSrcCopy8) {
                 const uint32_t x[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
@@ -803,31 +911,38 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       }
       if (*dead && lt == 0 && segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
     }
-  } else if (lane == 0 && issue) {
+  } else if (issue) {
     // ================= MMA =================
+    // The whole warp runs the loop and one elected lane issues: the descriptors
+    // stay in uniform registers (one lane alone: 73 instead of 51 cycles a step).
     constexpr uint32_t id_s = umma_idesc_bf16(kKeys, kN, false);
     constexpr uint32_t id_o = umma_idesc_bf16(128, kN, true, true);
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_on(bar, parity, dead, wait_ns)) != 0;
+    };
     int tiles = 0, segs = 0;
     bool ok = true;
     while (ok && w.next()) {
       if (w.ta == w.tb) continue;
-      if (!wait_on(&c.q_full, segs & 1, dead, wait_ns)) { ok = false; break; }
-      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+      ok = wait_all(&c.q_full, segs & 1);
+      for (int v = w.ta; ok && v < w.tb; ++v, ++tiles) {
 #pragma unroll
         for (int mc = 0; mc < 4; ++mc) {
-          if (!wait_on(&c.full[mc], tiles & 1, dead, wait_ns)) { ok = false; break; }
+          ok = ok && wait_all(&c.full[mc], tiles & 1);
+          if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const uint32_t blk = 2 * mc + (j >> 2), off = (j & 3) * 32;
-            umma_bf16(tmem, sw128_desc(kvb + blk * kKvBlock + off),
-                      sw128_desc(qb + blk * S::kQBlock + off), id_s, (mc | j) ? 1u : 0u);
+            umma_bf16_elect(tmem, sw128_desc(kvb + blk * kKvBlock + off),
+                            sw128_desc(qb + blk * S::kQBlock + off), id_s, (mc | j) ? 1u : 0u);
           }
         }
         if (!ok) break;
-        umma_commit(&c.s_full);
-        if (v + 1 == w.tb) umma_commit(&c.q_empty);
-        if (!wait_on(&c.p_full, tiles & 1, dead, wait_ns)) { ok = false; break; }
+        umma_commit_elect(&c.s_full);
+        if (v + 1 == w.tb) umma_commit_elect(&c.q_empty);
+        ok = wait_all(&c.p_full, tiles & 1);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int mc = 0; mc < 4; ++mc) {
@@ -836,17 +951,17 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
             const uint64_t a = umma_desc_sw128(kvb + 2 * mc * kKvBlock + kr * 2048, kKvBlock, 1024);
             const uint64_t b = kN == 64 ? umma_desc_sw128(pb + kr * 2048, kKeys * 128, 1024)
                                         : umma_desc_sw64(pb + kr * 1024, kKeys * 64, 512);
-            umma_bf16(tmem + kN + mc * kN, a, b, id_o, (v > w.ta || kr > 0) ? 1u : 0u);
+            umma_bf16_elect(tmem + kN + mc * kN, a, b, id_o, (v > w.ta || kr > 0) ? 1u : 0u);
           }
-          umma_commit(&c.empty[mc]);
+          umma_commit_elect(&c.empty[mc]);
         }
       }
       if (!ok) break;
-      umma_commit(&c.o_full);
+      umma_commit_elect(&c.o_full);
       ++segs;
     }
     if (!ok) {  // drain what was issued before the CTA's memory is given back
-      umma_commit(&c.drain);
+      umma_commit_elect(&c.drain);
       mbar_wait_bounded(&c.drain, 0);
     }
   }
@@ -937,21 +1052,25 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // [rows, 512] bf16, boxes of 64 columns x box_rows rows, 128-byte swizzle; rows at
 // or beyond `rows` read as zeros.
-bool row_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
+// codes: [rows, 512] bytes, boxes of 128 columns, no swizzle.
+bool row_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows,
+             bool codes = false) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)kL, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)kL * 2};
-  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kL * (codes ? 1 : 2)};
+  const cuuint32_t box[2] = {codes ? 128u : 64u, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int box_rows_of(int page_size) {  // largest power of two that divides it, 128 at most
-  const int r = page_size & -page_size;
-  return r > kKeys ? kKeys : r;
+int box_log_of(int page_size) {  // largest power of two that divides it, 128 at most
+  int log = 0;
+  while (log < 7 && page_size % (2 << log) == 0) ++log;
+  return log;
 }
 
 template <int kN>
@@ -978,15 +1097,15 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   // rows that few tokens share come from HBM: the tile after the next is brought
   // into L2 meanwhile
   p.prefetch = a.T <= 4 * a.B;
-  p.box_rows = box_rows_of(a.kv.page_size);
+  p.box_log = is_tma(kSrc) ? box_log_of(a.kv.page_size) : 0;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)n_cta * 2 * kN * kL);
   p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)n_cta * 2 * kN);
   CUtensorMap q_map, kv_map;
   if (!row_map(&q_map, a.q_lat, (uint64_t)a.T * a.Hm, kN)) return DSA_ERR_CUDA;
   kv_map = q_map;
-  if (kSrc == kSrcTma &&
-      !row_map(&kv_map, a.kv.pages, (uint64_t)a.kv.n_pages * a.kv.page_size, p.box_rows))
+  if (is_tma(kSrc) && !row_map(&kv_map, a.kv.pages, (uint64_t)a.kv.n_pages * a.kv.page_size,
+                               1u << p.box_log, kSrc == kSrcTma8))
     return DSA_ERR_CUDA;
   auto kernel = mla_chunk_kernel<kN, kSrc>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1012,9 +1131,12 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
 
 template <int kN>
 int launch_src(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
-  if (a.kv.kv_dtype == DSA_FP8_E4M3) return launch<kN, kSrcE4M3>(a, workspace, stream);
-  if (a.kv.page_size % 8 == 0) return launch<kN, kSrcTma>(a, workspace, stream);
-  return launch<kN, kSrcCopy>(a, workspace, stream);
+  const bool codes = a.kv.kv_dtype == DSA_FP8_E4M3;
+  if (a.kv.page_size % 8 == 0)
+    return codes ? launch<kN, kSrcTma8>(a, workspace, stream)
+                 : launch<kN, kSrcTma>(a, workspace, stream);
+  return codes ? launch<kN, kSrcCopy8>(a, workspace, stream)
+               : launch<kN, kSrcCopy>(a, workspace, stream);
 }
 
 }  // namespace
