@@ -27,7 +27,8 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2"
                      "--expt-relaxed-constexpr", "-Xptxas", "-v", "-I", INCLUDE]
 SOURCES = ["dsa_abi.cu", "kpool_compress.cu", "index_scores.cu", "index_scores_umma.cu",
            "topk.cu", "mla_decode.cu", "mla_umma.cu", "select_noalloc.cu",
-           "indexer_proj.cu", "paged_step.cu", "mla_chunk.cu", "mla_chunk_umma.cu"]
+           "indexer_proj.cu", "paged_step.cu", "mla_chunk.cu", "mla_chunk_umma.cu",
+           "mla_chunk_pair.cu"]
 
 
 def _nvcc() -> str:

@@ -168,12 +168,16 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
 
 size_t mla_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype) {
   if (T < 1 || !mla_chunk_umma_ok(L, dtype, kv_dtype)) return 0;
-  return mla_chunk_umma_workspace_size(Hm);
+  const size_t one = mla_chunk_umma_workspace_size(Hm);
+  const size_t two = Hm > 32 ? mla_chunk_pair_workspace_size() : 0;
+  return one > two ? one : two;
 }
 
 int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   if (mla_chunk_umma_ok(a.L, a.dtype, a.kv.kv_dtype))
-    return launch_mla_chunk_umma(a, workspace, stream);
+    return mla_chunk_pair_ok(a.T, a.B, a.Hm, a.kv.page_size)
+               ? launch_mla_chunk_pair(a, workspace, stream)
+               : launch_mla_chunk_umma(a, workspace, stream);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

@@ -1,0 +1,401 @@
+// What the tensor-core kernels of the chunk attention share: the batch as units of
+// work, a walk over a CTA's (or CTA pair's) share of them, the join of partials.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "dsa_internal.cuh"
+#include "umma.cuh"
+
+#include <cudaTypedefs.h>
+
+namespace dsa {
+namespace chunk {
+
+constexpr int kL = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+// A head's reference is raised when a score passes it by more than this (base 2).
+constexpr float kRaiseAt = 20.f;
+
+struct Header {        // what a worker (CTA or CTA pair) left for the join
+  int start_tile;      // row tile whose first units it holds but not its last (-1: none)
+  int cont_tile;       // row tile that an earlier worker began (-1: none; -2: no share at all)
+  int cont_some;       // it has a partial of that
+  int cont_ends;       // and its last units
+};
+
+struct Params {
+  PagedKv kv;
+  const int32_t* cu_new;
+  int T, B, Hm, window, sinks;
+  float zscale;              // sm_scale in base 2
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_o;             // [2 workers][rows of a tile][kL]
+  float2* part_ml;           // [2 workers][rows of a tile]
+  Header* head;
+  int32_t* status;
+  int drill, prefetch;
+  int box_log;               // positions of a box, 2^box_log (copied rows: 1)
+};
+
+// ---- the batch as units ------------------------------------------------------
+// A unit is one key tile of kT positions for one row tile.  kPair: a row tile is two
+// tokens and a block of 64 heads, or one token and two such blocks (Hm > 64);
+// otherwise one token and a block of heads.
+struct Seq {
+  int c0, n, base;             // rows c0 .. c0 + n - 1 of the step; position of the first
+  unsigned u;                  // units per row tile
+};
+template <int kT, bool kPair>
+__device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p) {
+  Seq s;
+  s.c0 = min(max(cu0, 0), p.T);
+  s.n = max(min(cu1, p.T) - s.c0, 0);
+  s.base = len < 0 ? -s.n : len - s.n;   // negative: rows before position 0
+  const unsigned all = (unsigned)max(len, 0);
+  s.u = (all + kT - 1) / kT;
+  if (p.window > 0) {
+    const long long R = 1 << p.box_log;
+    const long long keys =
+        ((p.sinks + R - 1) / R + (p.window + (kPair ? 1 : 0) + R - 2) / R + 1) * R;
+    if ((keys + kT - 1) / kT < (long long)s.u) s.u = (unsigned)((keys + kT - 1) / kT);
+  }
+  s.u = max(s.u, 1u);
+  return s;
+}
+
+// Visible positions [0, s0) and [lo, pos] as boxes of R = 2^log positions (aligned;
+// the window's first and last may reach past it), kT / R to a key tile.  A row tile of
+// two tokens holds the union of theirs.
+template <int kT>
+struct Keys {
+  int pos, lo, s0, log, sink_boxes, first, boxes, n;
+  // position of row r of key tile v (past the last box: past pos)
+  __device__ __forceinline__ int at(int v, int r) const {
+    const int g = v * (kT >> log) + (r >> log);
+    const int box = g < sink_boxes ? g : first + (g - sink_boxes);
+    return g < boxes ? (box << log) + (r & ((1 << log) - 1)) : 0x7fffffff;
+  }
+  __device__ __forceinline__ bool sees(int t) const { return t <= pos && (t >= lo || t < s0); }
+};
+// pos0: the first token's position (the window begins there), pos: the last one's
+template <int kT>
+__device__ __forceinline__ Keys<kT> keys_of(int pos0, int pos, const Params& p) {
+  Keys<kT> k;
+  k.pos = pos;
+  k.log = p.box_log;
+  k.lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+  k.s0 = min(p.sinks, k.lo);
+  k.first = k.lo >> k.log;
+  k.sink_boxes = min((k.s0 >> k.log) + ((k.s0 & ((1 << k.log) - 1)) != 0), k.first);
+  k.boxes = pos < 0 ? 0 : k.sink_boxes + (pos >> k.log) - k.first + 1;
+  const int per = kT >> k.log;
+  k.n = (k.boxes + per - 1) / per;
+  return k;
+}
+
+// a n / u, rounded down
+__device__ __forceinline__ int share_of(unsigned a, unsigned n, unsigned u) {
+  if (a == 0) return 0;
+  if (a == u) return (int)n;
+  if ((a | n) < 65536u) return (int)(a * n / u);
+  return (int)((unsigned long long)a * n / u);
+}
+
+// Where a worker's share begins (in shared memory).
+struct Start {
+  unsigned long long scan[32];
+  int b;                       // sequence (B: no share)
+  unsigned row, unit;          // row tile of it, unit of that
+};
+
+template <int kT, bool kPair>
+__device__ __forceinline__ unsigned row_tiles(const Seq& s, int hb) {
+  return kPair ? (hb == 2 ? (unsigned)s.n : ((unsigned)s.n + 1) / 2) : (unsigned)s.n * hb;
+}
+
+// The share of worker `me` of `workers`: returns its number of units, and fills
+// *st.  Run by all kThreads threads of a CTA; ends with a barrier.
+template <int kT, bool kPair, int kThreads>
+__device__ __forceinline__ unsigned long long find_share(const Params& p, int hb, unsigned me,
+                                                         unsigned workers, Start* st,
+                                                         bool reports) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per),
+            b1 = min(p.B, b0 + per);
+  if (tid == 0) st->b = p.B;
+  unsigned long long mine = 0;
+  bool odd = false;
+  for (int b = b0; b < b1; ++b) {
+    const int cu0 = p.cu_new[b], cu1 = p.cu_new[b + 1], len = p.kv.seq_lens[b];
+    const Seq s = seq_of<kT, kPair>(cu0, cu1, len, p);
+    odd |= cu0 < 0 || cu1 < cu0 || cu1 > p.T || (s.n > 0 && s.base < 0);
+    mine += (unsigned long long)row_tiles<kT, kPair>(s, hb) * s.u;
+  }
+  if (odd && reports) flag(p.status, DSA_DEV_BAD_LENGTH);
+  unsigned long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) st->scan[warp] = inc;
+  __syncthreads();
+  unsigned long long before = inc - mine, total = 0, v0, v1;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += st->scan[w];
+    total += st->scan[w];
+  }
+  if (total < (1ull << 32) / 256) {  // (fewer than 256 workers: a product of 32 bits)
+    v0 = (unsigned)total * me / workers;
+    v1 = (unsigned)total * (me + 1) / workers;
+  } else {
+    v0 = total * me / workers;
+    v1 = total * (me + 1) / workers;
+  }
+  if (v0 < v1 && v0 >= before && v0 < before + mine) {
+    unsigned long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = seq_of<kT, kPair>(p.cu_new[b], p.cu_new[b + 1], p.kv.seq_lens[b], p);
+      const unsigned long long all = (unsigned long long)row_tiles<kT, kPair>(s, hb) * s.u;
+      if (v0 < at + all) {
+        const unsigned long long off = v0 - at;
+        st->b = b;
+        st->row = (unsigned)(off >> 32 ? off / s.u : (unsigned)off / s.u);
+        st->unit = (unsigned)(off - (unsigned long long)st->row * s.u);
+        break;
+      }
+      at += all;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  return v1 - v0;
+}
+
+// A walk over a worker's units, row tile by row tile.  Every role walks alone; the
+// next sequence's lengths are read one sequence ahead.
+template <int kT, bool kPair>
+struct Walk {
+  const Params& p;
+  int hb;                       // head blocks per token: 1 or 2
+  unsigned long long left;      // units still to do
+  int b;
+  unsigned row, unit;           // of sequence b: row tile, unit of it
+  Seq s;
+  int cu_next, len_next;        // of sequence b + 1 (its end, its length)
+  // the current segment: a row tile and its key tiles [ta, tb) (none: ta == tb)
+  int token, h0, tile_id, ta, tb;
+  int pos0;                     // the (first) token's position; -1 and below: sees nothing
+  bool two;                     // kPair: a second token follows the first
+  Keys<kT> k;
+
+  __device__ __forceinline__ Walk(const Params& pp, int hb_, const Start& st,
+                                  unsigned long long n)
+      : p(pp), hb(hb_), left(st.b < pp.B ? n : 0), b(st.b), row(st.row), unit(st.unit) {
+    if (left == 0) return;
+    s = seq_of<kT, kPair>(__ldg(p.cu_new + b), __ldg(p.cu_new + b + 1),
+                          __ldg(p.kv.seq_lens + b), p);
+    ahead();
+  }
+  __device__ __forceinline__ void ahead() {
+    if (b + 1 < p.B) {
+      cu_next = __ldg(p.cu_new + b + 2);
+      len_next = __ldg(p.kv.seq_lens + b + 1);
+    }
+  }
+  __device__ __forceinline__ bool next() {
+    if (left == 0) return false;
+    while (row >= row_tiles<kT, kPair>(s, hb)) {  // units remain: a sequence with some follows
+      if (++b >= p.B) return false;               // (lengths that changed under the call)
+      const int cu0 = __ldg(p.cu_new + b);
+      s = seq_of<kT, kPair>(cu0, cu_next, len_next, p);
+      ahead();
+      row = 0;
+    }
+    const unsigned e = left < s.u - unit ? unit + (unsigned)left : s.u;
+    const int kk = (int)(!kPair && hb == 2 ? row >> 1 : row);
+    h0 = !kPair && hb == 2 ? (int)(row & 1u) : 0;
+    // row tiles are taken from both ends in turn
+    const int n = kPair && hb == 1 ? (s.n + 1) / 2 : s.n;
+    int i = (kk & 1) ? n - 1 - (kk >> 1) : kk >> 1;
+    two = false;
+    if (kPair && hb == 1) {
+      i *= 2;
+      two = i + 1 < s.n;
+    }
+    token = s.c0 + i;
+    tile_id = kPair ? 2 * token + (two ? 1 : 0) : token * hb + h0;
+    pos0 = s.base + i;
+    const int last = pos0 + (two ? 1 : 0);
+    k = keys_of<kT>(pos0, last < 0 ? -1 : last, p);
+    ta = share_of(unit, k.n, s.u);
+    tb = share_of(e, k.n, s.u);
+    left -= e - unit;
+    unit = e;
+    if (e == s.u) {
+      unit = 0;
+      ++row;
+    }
+    return true;
+  }
+};
+
+// ---- small pieces ------------------------------------------------------------
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void fma2(float& a0, float& a1, float b, float c0, float c1) {
+  unsigned long long a, bb, c;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(bb) : "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a) : "l"(bb), "l"(c));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  unsigned long long a, b;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+}
+
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+// A bounded wait that also ends when another role has given up.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* dead,
+                                        unsigned long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*dead) return false;
+    if (global_ns() - t0 > limit_ns) {
+      *dead = 1;
+      return false;
+    }
+  }
+}
+
+// Join the partials of the row tiles that were split over workers, in their order:
+// block (g, y) takes the tile that worker g began, rows 8 y ... (one warp per row,
+// four 16-byte pieces of the latent row a lane).
+template <int kRows, bool kPair>
+__global__ void __launch_bounds__(256)
+    mla_chunk_join_kernel(const Params p, int workers) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int g = blockIdx.x, lane = threadIdx.x & 31;
+  const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int tile = p.head[g].start_tile;
+  if (tile < 0) return;
+  int token, head;
+  if (kPair) {
+    token = tile >> 1;
+    head = h;
+    if (p.Hm <= 64 && h >= 64) {  // the second token's rows
+      if (!(tile & 1)) return;
+      ++token;
+      head = h - 64;
+    }
+  } else {
+    const int hb = (p.Hm + kRows - 1) / kRows;
+    token = tile / hb;
+    head = (tile - token * hb) * kRows + h;
+  }
+  if (head >= p.Hm) return;
+  float mx = -INFINITY, den = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = g; s < workers; ++s) {
+    int slot = 2 * g + 1;
+    bool last = false;
+    if (s > g) {
+      const Header hd = p.head[s];
+      if (hd.cont_tile == -2) continue;
+      if (hd.cont_tile != tile) break;
+      last = hd.cont_ends;
+      slot = 2 * s;
+      if (!hd.cont_some) {
+        if (last) break;
+        continue;
+      }
+    }
+    const float2 ml = p.part_ml[slot * kRows + h];
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + ((long long)slot * kRows + h) * kL);
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __ldcs(src + i * 32 + lane);
+    if (ml.y != 0.f) {  // a part that saw no page has nothing to add
+      const float m = fmaxf(mx, ml.x), ref = m == -INFINITY ? 0.f : m;
+      const float a = ex2_fast(mx - ref), b = ex2_fast(ml.x == -INFINITY ? 0.f : ml.x - ref);
+      den = den * a + ml.y * b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i].x = acc[i].x * a + v[i].x * b;
+        acc[i].y = acc[i].y * a + v[i].y * b;
+        acc[i].z = acc[i].z * a + v[i].z * b;
+        acc[i].w = acc[i].w * a + v[i].w * b;
+      }
+      mx = m;
+    }
+    if (last) break;
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const long long row = (long long)token * p.Hm + head;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint2*>(p.out + row * kL + (i * 32 + lane) * 4) =
+        make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv),
+                   pack_bf16(acc[i].z * inv, acc[i].w * inv));
+  if (p.lse && lane == 0) p.lse[row] = den == 0.f ? -INFINITY : (mx + log2f(den)) / kLog2e;
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// [rows, 512] bf16, boxes of 64 columns x box_rows rows, 128-byte swizzle; rows at
+// or beyond `rows` read as zeros.
+// codes: [rows, 512] bytes, boxes of 128 columns, no swizzle.
+inline bool row_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows,
+             bool codes = false) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)kL, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kL * (codes ? 1 : 2)};
+  const cuuint32_t box[2] = {codes ? 128u : 64u, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace chunk
+}  // namespace dsa

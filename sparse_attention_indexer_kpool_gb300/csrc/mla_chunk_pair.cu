@@ -1,0 +1,961 @@
+// The chunk attention on pairs of CTAs (bf16 activations, latent 512, more than 32
+// heads, bf16 or E4M3 pages of a multiple of 8 rows): two row blocks of 64 (two
+// tokens, or one token's two blocks of heads) share every key row.
+//
+// Why pairs.  One CTA cannot hold more than 64 rows: the fp32 output of a row takes
+// 512 TMEM columns over 128 lanes, and with 64 rows every MMA reads 6 KB of shared
+// memory for 32 cycles' work, and every key row is fetched for one token.  A cluster
+// of two CTAs splits the latent axis instead: CTA c holds latent columns 256 c .. of
+// the queries (64 KB), of the keys (40 KB for a tile of 80, three stages), and of the
+// output (256 TMEM columns for all 128 rows).
+//   S_c = Q_c K_c^T      M = 128 rows, N = 80 keys, K = 256: a partial sum
+//   S   = S_0 + S_1      each CTA sends the partials of the other one's 64 rows
+//                        through distributed shared memory and adds its own
+//   P                    softmax weights of its 64 rows, written to its own TMEM and
+//                        sent (bf16) to the other's
+//   O_c += P V_c         A = P from TMEM, V_c = K_c read MN-major, N = 256, K = 80
+// An MMA then reads 6.5 KB for 40 cycles' work (QK) or 8 KB for 128 (PV), a key row is
+// fetched once for two tokens, and no product is done twice.  The exchange and the
+// softmax stand between a tile's two products (about 2,000 cycles); three tiles are in
+// flight, so the tensor cores work on the others meanwhile.
+//
+// The two tokens of a pair see the same keys but for the last one and the first of a
+// window.  A key that neither sees is zeroed in shared memory before PV; one that only
+// one of them sees is zeroed if it holds a NaN or an infinity (its logit is then one,
+// too, which makes the seeing token's sums NaN), so that nothing masked reaches a row.
+//
+// Every wait is bounded; both CTAs meet at a cluster barrier before either ends.
+#include "mla_chunk.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace chunk;
+
+constexpr int kKT = 80;                      // keys of a tile
+constexpr int kGroups = kKT / 8;             // of 8 rows: 4 KB, [64-column block][row][128 B]
+constexpr int kStageBytes = kGroups * 4096;  // 40 KB
+constexpr int kStages = 3;
+constexpr int kQBlock = 128 * 128;           // 128 rows x 64 latent columns
+constexpr int kSoftThreads = 256;
+constexpr int kW = kKT / 2;                  // scores of a softmax thread
+constexpr int kWidenWarps = 5;               // E4M3: two groups each
+constexpr size_t kOffQ = 0;
+constexpr size_t kOffK = 4 * (size_t)kQBlock;
+constexpr size_t kOffS = kOffK + (size_t)kStages * kStageBytes;   // [20][64 rows] x 16 B
+constexpr size_t kOffP = kOffS + (size_t)(kKT / 4) * 64 * 16;     // [10][64 rows] x 16 B
+constexpr uint32_t kSBytes = kKT * 64 * 4, kPBytes = kKT * 64 * 2 + 64 * 4;
+
+struct Ctl {
+  float rs[kStages][kKT];          // E4M3: the keys' row scales (first: read as float4)
+  float alpha[64];                 // from the other CTA: its rows' rescale of this tile
+  float inv[128];                  // 1 / sum of every row (the other CTA's rows: sent)
+  float mx[2][64], sum[2][64];     // own rows: the two threads of a row
+  uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], raw[kStages];
+  uint64_t s_full[kStages], p_full[kStages], o_full, drain;
+  uint64_t in_s, in_p, in_l;       // data from the other CTA
+  uint64_t free_s, free_p;         // the other CTA has read what was sent
+  uint64_t epi;                    // the sums of a segment's rows are there
+  Start start;
+  uint32_t tmem;
+  unsigned groups[kStages];        // groups of the tile that have a page
+  int own_dead[2], send_dead[2];
+  int dead;
+};
+constexpr size_t kOffCtl = kOffP + (size_t)(kKT / 8) * 64 * 16;
+constexpr size_t kSmem = 1024 + kOffCtl + sizeof(Ctl);
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+static_assert(256 + kStages * kKT <= 512, "TMEM columns");
+
+__host__ __device__ constexpr int pair_threads(bool codes) {
+  return kSoftThreads + 32 * (2 + (codes ? kWidenWarps : 0));
+}
+
+// ---- cluster pieces ------------------------------------------------------------
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+// the address of this CTA's shared-memory location in CTA `rank`
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// 16 / 4 bytes to the other CTA; counted on its barrier
+__device__ __forceinline__ void send16(uint32_t addr, uint4 v, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4},"
+      " [%5];" ::"r"(addr),
+      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void send4(uint32_t addr, float v, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+      "r"(__float_as_uint(v)), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* dead,
+                                             unsigned long long limit_ns) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (try_wait_cluster(bar, parity)) return true;
+    if (*dead) return false;
+    if (global_ns() - t0 > limit_ns) {
+      *dead = 1;
+      return false;
+    }
+  }
+}
+// whether the phase has completed, without waiting
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// barriers of the four warps that own rows (1) and of the four that send (2)
+__device__ __forceinline__ bool vote4(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n"
+      " barrier.cta.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// 40 consecutive fp32 columns of the warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld40(uint32_t ta, float (&v)[40]) {
+  uint32_t r[40];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(ta));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]),
+                 "=r"(r[38]), "=r"(r[39])
+               : "r"(ta + 32));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 40; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 20 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_st20(uint32_t ta, const uint32_t (&v)[20]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(ta),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ta + 16),
+               "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19])
+               : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// O += P V with P (the A operand) in TMEM; one elected lane of a converged warp.
+__device__ __forceinline__ void umma_tmem_a_elect(uint32_t d, uint32_t a, uint64_t b,
+                                                  uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+// What one row block (token) of the tile sees.
+struct Sight {
+  int pos, lo, sinks;
+  __device__ __forceinline__ bool operator()(int t) const {
+    return t <= pos && (t >= lo || t < sinks);
+  }
+};
+__device__ __forceinline__ Sight sight_of(int pos, const Params& p) {
+  return Sight{pos, p.window > 0 ? max(0, pos - p.window + 1) : 0, p.sinks};
+}
+
+using PairWalk = Walk<kKT, true>;
+using PairKeys = Keys<kKT>;
+
+template <bool kCodes>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes), 1)
+    mla_chunk_pair_kernel(const __grid_constant__ CUtensorMap q_map,
+                          const __grid_constant__ CUtensorMap kv_map, const Params p) {
+  constexpr int kTmaWarp = kSoftThreads / 32, kMmaWarp = kTmaWarp + 1, kWiden0 = kMmaWarp + 1;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl& c = *reinterpret_cast<Ctl*>(sb + kOffCtl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cta_rank(), other = rank ^ 1u;
+  const int hb = (p.Hm + 63) / 64;
+  const unsigned me = blockIdx.x >> 1, workers = gridDim.x >> 1;
+
+  if (tid == 0) {
+    mbar_init(&c.q_full, 1);
+    mbar_init(&c.q_empty, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&c.k_full[i], kCodes ? kWidenWarps : 1);
+      mbar_init(&c.k_empty[i], 1);
+      mbar_init(&c.raw[i], 1);
+      mbar_init(&c.s_full[i], 1);
+      mbar_init(&c.p_full[i], kSoftThreads / 32);
+    }
+    mbar_init(&c.o_full, 1);
+    mbar_init(&c.drain, 1);
+    mbar_init(&c.in_s, 1);
+    mbar_init(&c.in_p, 1);
+    mbar_init(&c.in_l, 1);
+    mbar_init(&c.free_s, 4);
+    mbar_init(&c.free_p, 4);
+    mbar_init(&c.epi, kSoftThreads / 32);
+    fence_mbar_init();
+    c.own_dead[0] = c.own_dead[1] = c.send_dead[0] = c.send_dead[1] = c.dead = 0;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc<512>(&c.tmem);
+    tc_fence_before();
+  }
+  pdl_wait();  // every input may come from the kernel just before
+  pdl_launch_dependents();
+  const unsigned long long units = find_share<kKT, true, pair_threads(kCodes)>(
+      p, hb, me, workers, &c.start, blockIdx.x == 0);
+  cluster_sync();  // the other CTA's barriers exist
+  const uint32_t tmem = c.tmem;
+  const bool any = c.start.b < p.B;
+  PairWalk w(p, hb, c.start, units);
+  // a failure drill loads nothing and issues no MMA: the first waits run out
+  const bool issue = p.drill == 0;
+  const unsigned long long wait_ns = p.drill ? kDrillWaitNs : kWaitNs;
+  volatile int* dead = &c.dead;
+
+  if (warp < kTmaWarp) {
+    // ================= softmax, exchange, epilogue =================
+    const int qw = warp & 3, h = warp >> 2;  // TMEM lanes 32 qw .., keys 40 h ..
+    const int g = qw >> 1;                   // row block of these lanes
+    const bool own = g == (int)rank;
+    const int r = (qw & 1) * 32 + lane;      // row of the block
+    const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16);
+    const uint32_t to_s = map_to(smem_u32(sb + kOffS) + (h * 10 * 64 + r) * 16, other);
+    const uint32_t to_p = map_to(smem_u32(sb + kOffP) + (h * 5 * 64 + r) * 16, other);
+    const uint32_t bar_s = map_to(smem_u32(&c.in_s), other),
+                   bar_p = map_to(smem_u32(&c.in_p), other),
+                   bar_l = map_to(smem_u32(&c.in_l), other),
+                   bar_free_s = map_to(smem_u32(&c.free_s), other),
+                   bar_free_p = map_to(smem_u32(&c.free_p), other);
+    const uint4* in_s = reinterpret_cast<const uint4*>(sb + kOffS) + h * 10 * 64 + r;
+    const uint4* in_p = reinterpret_cast<const uint4*>(sb + kOffP) + h * 5 * 64 + r;
+    Header hd = {-1, any ? -1 : -2, 0, 0};
+    int tiles = 0, segs = 0, sums = 0;
+    bool ok = true;
+    // the phases of the data from the other CTA are armed one ahead
+    if (any) {
+      if (own && tid == 64 * (int)rank) {
+        mbar_arrive_expect_tx(&c.in_s, kSBytes);
+        mbar_arrive_expect_tx(&c.in_l, 64 * 4);
+      }
+      if (!own && tid == 64 * (int)other) mbar_arrive_expect_tx(&c.in_p, kPBytes);
+    }
+    while (ok && w.next()) {
+      // this thread's row block: its token, its heads, what it sees
+      const bool there = p.Hm > 64 || g == 0 || w.two;
+      const int token = p.Hm > 64 ? w.token : w.token + (there ? g : 0);
+      const int head = p.Hm > 64 ? g * 64 + r : r;
+      const bool live = there && head < p.Hm;
+      const int pos_a = w.pos0 < 0 ? -1 : w.pos0;
+      // (a missing second token sees what the first one does, for nobody)
+      const int pos_b = w.two ? (w.pos0 + 1 < 0 ? -1 : w.pos0 + 1) : pos_a;
+      const Sight sa = sight_of(pos_a, p), sbt = sight_of(pos_b, p);
+      const Sight mine = g == 0 ? sa : sbt;
+      float m = -INFINITY, l = 0.f;
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        const int st = tiles % kStages, ph = (tiles / kStages) & 1;
+        const uint32_t tS = tl + 256 + (uint32_t)(st * kKT);
+        bool fine = wait_on(&c.s_full[st], ph, dead, wait_ns);
+        tc_fence_after();
+        float e[kW];
+        tmem_ld40(tS + h * kW, e);
+        // is every key of the tile seen by both blocks?
+        const int t0 = w.k.at(v, 0), t1 = w.k.at(v, kKT - 1);
+        const bool plain = c.groups[st] == (1u << kGroups) - 1 && t1 - t0 == kKT - 1 &&
+                           t0 >= max(sa.lo, sbt.lo) && t1 <= min(sa.pos, sbt.pos);
+        if (!plain && (tid >> 1) < kKT) {
+          // clear what neither sees, and what one does not see if it is not finite
+          const int key = tid >> 1;
+          const int t = w.k.at(v, key);
+          const bool paged = (c.groups[st] >> (key >> 3)) & 1u;
+          const bool ina = paged && sa(t), inb = paged && sbt(t);
+          if (!(ina && inb)) {
+            unsigned char* kr = sb + kOffK + st * kStageBytes + (key >> 3) * 4096 +
+                                (tid & 1) * 2048 + (key & 7) * 128;
+            bool odd = !(ina || inb);
+            if (!odd) {
+              for (int i = 0; i < 16; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4*>(
+                    kr + (i >> 3) * 1024 + (((i & 7) ^ (key & 7)) << 4));
+                const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+                for (int j = 0; j < 4; ++j)
+                  odd |= (wd[j] & 0x7f80u) == 0x7f80u || (wd[j] & 0x7f800000u) == 0x7f800000u;
+              }
+            }
+            if (odd)
+              for (int i = 0; i < 16; ++i)
+                *reinterpret_cast<uint4*>(kr + (i >> 3) * 1024 +
+                                          (((i & 7) ^ (key & 7)) << 4)) =
+                    make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        if (own) {
+          fine = fine && wait_cluster(&c.in_s, tiles & 1, dead, wait_ns);
+#pragma unroll
+          for (int j = 0; j < 10; ++j) {
+            const uint4 x = in_s[j * 64];
+            e[4 * j] += __uint_as_float(x.x);
+            e[4 * j + 1] += __uint_as_float(x.y);
+            e[4 * j + 2] += __uint_as_float(x.z);
+            e[4 * j + 3] += __uint_as_float(x.w);
+          }
+          __syncwarp();
+          if (lane == 0) arrive_remote(bar_free_s);
+          // the keys this block sees, 40 bits
+          uint32_t see_lo = 0xffffffffu, see_hi = 0xffu;
+          if (!plain) {
+            const int ta = w.k.at(v, h * kW + lane);
+            see_lo = __ballot_sync(
+                0xffffffffu, mine(ta) && ((c.groups[st] >> ((h * kW + lane) >> 3)) & 1u));
+            const int tb = w.k.at(v, h * kW + 32 + (lane & 7));
+            see_hi = __ballot_sync(0xffffffffu,
+                                   lane < 8 && mine(tb) &&
+                                       ((c.groups[st] >> ((h * kW + 32 + (lane & 7)) >> 3)) & 1u));
+          }
+          const float nm = m == -INFINITY ? 0.f : -m;
+          if constexpr (kCodes) {
+#pragma unroll
+            for (int q = 0; q < 10; ++q) {
+              const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + h * kW)[q];
+              e[4 * q] = fmaf(e[4 * q], p.zscale * rs.x, nm);
+              e[4 * q + 1] = fmaf(e[4 * q + 1], p.zscale * rs.y, nm);
+              e[4 * q + 2] = fmaf(e[4 * q + 2], p.zscale * rs.z, nm);
+              e[4 * q + 3] = fmaf(e[4 * q + 3], p.zscale * rs.w, nm);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kW; i += 2) fma2(e[i], e[i + 1], p.zscale, nm, nm);
+          }
+          if (!plain) {
+#pragma unroll
+            for (int i = 0; i < kW; ++i)
+              if (!((i < 32 ? see_lo >> i : see_hi >> (i - 32)) & 1u)) e[i] = -INFINITY;
+          }
+          float top = e[0];
+#pragma unroll
+          for (int i = 1; i < kW; ++i) top = fmaxf(top, e[i]);
+          if (!fine) c.own_dead[tiles & 1] = 1;
+          c.mx[h][r] = top;  // relative to the reference
+          const bool full = vote4(1, live && (m == -INFINITY || top > kRaiseAt));
+          if (c.own_dead[tiles & 1]) {
+            ok = false;
+            break;
+          }
+          if (tid == 64 * (int)rank) mbar_arrive_expect_tx(&c.in_s, kSBytes);  // the next tile's
+          float alpha = 1.f;
+          if (full) {
+            const float both = fmaxf(c.mx[0][r], c.mx[1][r]);  // of the row, relative
+            float step = 0.f;
+            if (m == -INFINITY) {
+              if (both > -INFINITY) {  // the first key that this row sees
+                m = both;              // (nothing accumulated: no rescale)
+                step = -both;
+              }
+            } else if (both > kRaiseAt) {
+              m += both;
+              step = -both;
+              alpha = ex2_fast(-both);
+              l *= alpha;
+            }
+            // (an infinite maximum: its key's weight is NaN, as in the formula)
+#pragma unroll
+            for (int i = 0; i < kW; ++i) e[i] += step;
+          }
+#pragma unroll
+          for (int i = 0; i < kW; ++i) e[i] = ex2_fast(e[i]);
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < kW; i += 4) {
+            add2(s4[0], s4[1], e[i], e[i + 1]);
+            add2(s4[2], s4[3], e[i + 2], e[i + 3]);
+          }
+          l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          // P is rounded to bf16 for the tensor cores; the sums keep the unrounded
+          // weights.  An E4M3 row's scale goes to its weights.
+          uint32_t pk[20];
+          if constexpr (kCodes) {
+#pragma unroll
+            for (int q = 0; q < 10; ++q) {
+              const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + h * kW)[q];
+              e[4 * q] *= rs.x;
+              e[4 * q + 1] *= rs.y;
+              e[4 * q + 2] *= rs.z;
+              e[4 * q + 3] *= rs.w;
+            }
+            if (!plain) {  // (a hidden key's scale may be anything)
+#pragma unroll
+              for (int i = 0; i < kW; ++i)
+                if (!((i < 32 ? see_lo >> i : see_hi >> (i - 32)) & 1u)) e[i] = 0.f;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 20; ++i) pk[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+          // the other CTA has taken the last tile's weights
+          if (tiles > 0 && !wait_cluster(&c.free_p, (tiles - 1) & 1, dead, wait_ns)) {
+            c.own_dead[(tiles + 1) & 1] = 1;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 5; ++j)
+              send16(to_p + j * 64 * 16, make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2],
+                                                    pk[4 * j + 3]), bar_p);
+            if (h == 0)
+              send4(map_to(smem_u32(&c.alpha[r]), other), alpha, bar_p);
+          }
+          if (v > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // O of the tiles so far, once the last of them is in it
+            wait_on(&c.k_empty[(tiles - 1) % kStages], ((tiles - 1) / kStages) & 1, dead, wait_ns);
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              float o[32];
+              const uint32_t ta = tl + h * 128 + cc * 32;
+              tmem_ld32(ta, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32(ta, o);
+            }
+          }
+          tmem_st20(tS + h * 20, pk);
+        } else {
+          // ---- this block's partial scores go to the CTA that owns it
+          if (tiles > 0 && fine)
+            fine = wait_cluster(&c.free_s, (tiles - 1) & 1, dead, wait_ns);
+          if (fine) {
+#pragma unroll
+            for (int j = 0; j < 10; ++j)
+              send16(to_s + j * 64 * 16,
+                     make_uint4(__float_as_uint(e[4 * j]), __float_as_uint(e[4 * j + 1]),
+                                __float_as_uint(e[4 * j + 2]), __float_as_uint(e[4 * j + 3])),
+                     bar_s);
+          }
+          // ---- and its weights come back
+          fine = fine && wait_cluster(&c.in_p, tiles & 1, dead, wait_ns);
+          uint32_t pk[20];
+#pragma unroll
+          for (int j = 0; j < 5; ++j) {
+            const uint4 x = in_p[j * 64];
+            pk[4 * j] = x.x;
+            pk[4 * j + 1] = x.y;
+            pk[4 * j + 2] = x.z;
+            pk[4 * j + 3] = x.w;
+          }
+          const float alpha = c.alpha[r];
+          if (!fine) c.send_dead[tiles & 1] = 1;
+          // (also: both halves of the row have read their scores, which P overlays)
+          vote4(2, false);
+          if (c.send_dead[tiles & 1]) {
+            ok = false;
+            break;
+          }
+          if (tid == 64 * (int)other) mbar_arrive_expect_tx(&c.in_p, kPBytes);  // the next tile's
+          if (lane == 0) arrive_remote(bar_free_p);
+          if (v > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) {
+            wait_on(&c.k_empty[(tiles - 1) % kStages], ((tiles - 1) / kStages) & 1, dead, wait_ns);
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              float o[32];
+              const uint32_t ta = tl + h * 128 + cc * 32;
+              tmem_ld32(ta, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32(ta, o);
+            }
+          }
+          tmem_st20(tS + h * 20, pk);
+        }
+        fence_proxy_async_smem();  // cleared keys
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&c.p_full[st]);
+      }
+      if (!ok) break;
+      const bool some = w.tb > w.ta, whole = w.ta == 0 && w.tb == w.k.n;
+      const bool begins = some && w.ta == 0 && !whole;
+      if (begins) hd.start_tile = w.tile_id;
+      if (!whole && !begins && hd.cont_tile < 0) {
+        hd.cont_tile = w.tile_id;
+        hd.cont_some = some;
+        hd.cont_ends = w.tb == w.k.n;
+      }
+      if (!some && !whole) continue;
+      const long long row = (long long)token * p.Hm + head;
+      if (!some) {  // tokens that see nothing
+        if (own && live) {
+          __nv_bfloat16* dst = p.out + row * kL + h * 256;
+          for (int i = 0; i < 32; ++i)
+            *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0u, 0u, 0u, 0u);
+          if (p.lse && h == 0) p.lse[row] = -INFINITY;
+        }
+        continue;
+      }
+      bool fine = wait_on(&c.o_full, segs & 1, dead, wait_ns);
+      ++segs;
+      tc_fence_after();
+      const int slot = 2 * (int)me + (begins ? 1 : 0);
+      if (own) {
+        c.sum[h][r] = l;
+        vote4(1, false);
+        const float sum = c.sum[0][r] + c.sum[1][r];
+        if (h == 0) {
+          if (whole) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
+            c.inv[64 * rank + r] = inv;
+            send4(map_to(smem_u32(&c.inv[64 * rank + r]), other), inv, bar_l);
+            if (p.lse && live) p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) / kLog2e;
+          } else {
+            p.part_ml[slot * 128 + 64 * rank + r] = make_float2(m, sum);
+          }
+        }
+      }
+      if (whole) {
+        fine = fine && wait_cluster(&c.in_l, sums & 1, dead, wait_ns);
+        ++sums;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&c.epi);
+      fine = wait_on(&c.epi, (segs - 1) & 1, dead, wait_ns) && fine;
+      if (vote4(own ? 1 : 2, !fine)) {  // the four warps leave together
+        ok = false;
+        break;
+      }
+      if (whole && own && tid == 64 * (int)rank) mbar_arrive_expect_tx(&c.in_l, 64 * 4);
+      // a thread holds its row's 128 latent columns 256 rank + 128 h ..
+      if (whole) {
+        const float inv = c.inv[64 * g + r];
+        __nv_bfloat16* dst = p.out + row * kL + 256 * rank + 128 * h;
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          float o[32];
+          tmem_ld32(tl + h * 128 + cc * 32, o);
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(dst + cc * 32 + q * 8) = make_uint4(
+                  pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv),
+                  pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                  pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
+                  pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+          }
+        }
+      } else {
+        float* dst = p.part_o + ((long long)slot * 128 + 64 * g + r) * kL + 256 * rank + 128 * h;
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          float o[32];
+          tmem_ld32(tl + h * 128 + cc * 32, o);
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(dst + cc * 32 + q * 4) =
+                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+        }
+      }
+      // O, c.inv and c.sum are read: this warp's next P, which every next write of
+      // them waits for, says so
+      tc_fence_before();
+    }
+    if (!ok) hd = Header{-1, -1, 0, 0};
+    if (tid == 0 && rank == 0) p.head[me] = hd;
+  } else if (warp == kTmaWarp) {
+    // ================= TMA =================
+    int tiles = 0, segs = 0;
+    bool ok = issue, armed = false;
+    // the cache row of this lane's group of a tile (-1: nothing seen, -2: no page)
+    auto group_row = [&](const PairKeys& k, int b, int v) -> int {
+      if (lane >= kGroups) return -1;
+      const int t0 = k.at(v, lane * 8);
+      if (t0 > k.pos) return -1;
+      const int blk = t0 / p.kv.page_size;
+      if (blk >= p.kv.max_pages) return -2;
+      const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
+      if (page < 0 || page >= p.kv.n_pages) return -2;
+      return page * p.kv.page_size + t0 % p.kv.page_size;
+    };
+    uint64_t* land = kCodes ? c.raw : c.k_full;
+    while (ok && w.next()) {
+      if (w.ta == w.tb) continue;
+      int row = group_row(w.k, w.b, w.ta);
+      const bool free_q = segs == 0 || wait_on(&c.q_empty, (segs - 1) & 1, dead, wait_ns);
+      if (!__all_sync(0xffffffffu, free_q)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&c.q_full, 4 * kQBlock);
+        for (int g = 0; g < 2; ++g) {
+          // (a missing second token: the first one's rows again, never used)
+          const int y = p.Hm > 64 ? w.token * p.Hm + g * 64 : (w.token + (w.two ? g : 0)) * p.Hm;
+          for (int blk = 0; blk < 4; ++blk)
+            tma_load_2d(sb + kOffQ + blk * kQBlock + g * 8192, &q_map, 256 * rank + blk * 64, y,
+                        &c.q_full);
+        }
+      }
+      ++segs;
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        const int row_next = v + 1 < w.tb ? group_row(w.k, w.b, v + 1) : -1;
+        if (row == -2) {
+          flag(p.status, DSA_DEV_BAD_PAGE);
+          row = -1;
+        }
+        const int st = tiles % kStages;
+        const unsigned groups = __ballot_sync(0xffffffffu, row >= 0);
+        const bool room = tiles < kStages ||
+                          wait_on(&c.k_empty[st], (tiles / kStages - 1) & 1, dead, wait_ns);
+        ok = __all_sync(0xffffffffu, room);
+        if (!ok) break;
+        if (lane == 0) {
+          c.groups[st] = groups;
+          mbar_arrive_expect_tx(&land[st], __popc(groups) * (kCodes ? 2048 : 4096));
+        }
+        armed = true;
+        __syncwarp();
+        if (row >= 0)
+          tma_load_3d(sb + kOffK + st * kStageBytes + lane * 4096, &kv_map, 0, row,
+                      (kCodes ? 2 : 4) * (int)rank, &land[st]);
+        if (p.prefetch && row_next >= 0)
+          tma_prefetch_3d(&kv_map, 0, row_next, (kCodes ? 2 : 4) * (int)rank);
+        row = row_next;
+      }
+    }
+    // after a give-up: no copy into this CTA's memory may be in flight at its end
+    if (*dead && lane == 0) {
+      for (int i = 1; i <= kStages; ++i)
+        if (armed && tiles - i >= 0)
+          mbar_wait_bounded(&land[(tiles - i) % kStages], ((tiles - i) / kStages) & 1);
+      if (segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ================= MMA =================
+    if (issue) {
+      constexpr uint32_t id_s = umma_idesc_bf16(128, kKT, false);
+      constexpr uint32_t id_o = umma_idesc_bf16(128, 256, false, true);
+      const uint32_t qb = smem_u32(sb + kOffQ), kb = smem_u32(sb + kOffK);
+      // Two streams over the same tiles: scores as soon as a stage holds keys, outputs
+      // as soon as a tile's weights are there; whichever is ready goes next (outputs
+      // first: they free the stage).
+      PairWalk wo(p, hb, c.start, units);
+      auto segment = [](PairWalk& x) {
+        while (x.next())
+          if (x.tb > x.ta) return true;
+        return false;
+      };
+      auto ready = [](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0;
+      };
+      bool ok = true, left_s = segment(w), left_o = segment(wo), have_q = false;
+      int ns = 0, no = 0, vs = w.ta, vo = wo.ta, seg = 0;
+      unsigned long long since = 0;  // time of the first idle look
+      while (left_o) {
+        if (no < ns && ready(&c.p_full[no % kStages], (no / kStages) & 1)) {
+          const int st = no % kStages;
+          const uint32_t k0 = kb + st * kStageBytes, a0 = tmem + 256 + st * kKT;
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < kKT / 16; ++s)
+            umma_tmem_a_elect(tmem, a0 + s * 8, umma_desc_sw128(k0 + s * 8192, 1024, 4096), id_o,
+                              (vo > wo.ta || s > 0) ? 1u : 0u);
+          umma_commit_elect(&c.k_empty[st]);
+          ++no;
+          if (++vo == wo.tb) {
+            umma_commit_elect(&c.o_full);
+            left_o = segment(wo);
+            vo = wo.ta;
+          }
+          since = 0;
+          continue;
+        }
+        if (left_s && ns - no < kStages) {
+          have_q = have_q || ready(&c.q_full, seg & 1);
+          // (the stage's keys imply that its last PV is done: its scores are free)
+          if (have_q && ready(&c.k_full[ns % kStages], (ns / kStages) & 1)) {
+            const int st = ns % kStages;
+            const uint32_t k0 = kb + st * kStageBytes;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t blk = j >> 2, off = (j & 3) * 32;
+              umma_bf16_elect(tmem + 256 + st * kKT, sw128_desc(qb + blk * kQBlock + off),
+                              umma_desc_sw128(k0 + blk * 1024 + off, 16, 4096), id_s,
+                              j ? 1u : 0u);
+            }
+            umma_commit_elect(&c.s_full[st]);
+            ++ns;
+            if (++vs == w.tb) {
+              umma_commit_elect(&c.q_empty);
+              ++seg;
+              left_s = segment(w);
+              vs = w.ta;
+              have_q = false;
+            }
+            since = 0;
+            continue;
+          }
+        }
+        const unsigned long long now = global_ns();
+        if (since == 0) since = now;
+        const bool late = now - since > wait_ns;
+        if (late) *dead = 1;
+        if (__any_sync(0xffffffffu, late || *dead)) {
+          ok = false;
+          break;
+        }
+      }
+      if (!ok) {  // drain what was issued before the CTA's memory is given back
+        umma_commit_elect(&c.drain);
+        mbar_wait_bounded(&c.drain, 0);
+      }
+    }
+  } else if constexpr (kCodes) {
+    // ================= E4M3 rows, widened in place =================
+    // A group's codes (8 rows of 256, two swizzled blocks) land in the first half of
+    // its 4 KB; one warp takes them into registers and writes the bf16 rows.
+    const int wi = warp - kWiden0;  // groups wi, wi + 5
+    int tiles = 0;
+    bool ok = issue;
+    auto scale_of = [&](const PairKeys& k, int b, int v) -> float {
+      // lanes 0..15: the rows of this warp's two groups
+      if (lane >= 16) return 0.f;
+      const int t = k.at(v, (wi + kWidenWarps * (lane >> 3)) * 8 + (lane & 7));
+      if (t > k.pos) return 0.f;
+      const int blk = t / p.kv.page_size;
+      if (blk >= p.kv.max_pages) return 0.f;
+      const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
+      if (page < 0 || page >= p.kv.n_pages) return 0.f;
+      return __ldg(p.kv.row_scale + (long long)page * p.kv.page_size + t % p.kv.page_size);
+    };
+    while (ok && w.next()) {
+      float rs = w.ta < w.tb ? scale_of(w.k, w.b, w.ta) : 0.f;
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        const float rs_next = v + 1 < w.tb ? scale_of(w.k, w.b, v + 1) : 0.f;
+        const int st = tiles % kStages;
+        const bool here = wait_on(&c.raw[st], (tiles / kStages) & 1, dead, wait_ns);
+        ok = __all_sync(0xffffffffu, here);
+        if (!ok) break;
+        if (lane < 16) c.rs[st][(wi + kWidenWarps * (lane >> 3)) * 8 + (lane & 7)] = rs;
+        const int rr = lane & 7;
+#pragma unroll
+        for (int gi = 0; gi < 2; ++gi) {
+          unsigned char* gp = sb + kOffK + st * kStageBytes + (wi + kWidenWarps * gi) * 4096;
+          uint4 raw[4];
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int pc = (lane >> 3) + 4 * it;
+            raw[it] = *reinterpret_cast<const uint4*>(gp + (pc >> 3) * 1024 + rr * 128 +
+                                                      (((pc & 7) ^ rr) << 4));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int pc = (lane >> 3) + 4 * it;
+            const uint32_t x[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              *reinterpret_cast<uint4*>(gp + (pc >> 2) * 1024 + rr * 128 +
+                                        (((2 * (pc & 3) + hf) ^ rr) << 4)) =
+                  make_uint4(e4m3x2_to_bf16x2(x[2 * hf] & 0xffffu),
+                             e4m3x2_to_bf16x2(x[2 * hf] >> 16),
+                             e4m3x2_to_bf16x2(x[2 * hf + 1] & 0xffffu),
+                             e4m3x2_to_bf16x2(x[2 * hf + 1] >> 16));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&c.k_full[st]);
+        rs = rs_next;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && c.dead) flag(p.status, DSA_DEV_TIMEOUT);  // outputs unspecified
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc<512>(tmem);
+  }
+  __syncwarp();
+  cluster_sync();  // neither CTA's memory goes while the other may write to it
+}
+
+// [rows, 512] as 64-column (codes: 128-byte) blocks: boxes of 8 rows of this CTA's
+// half of the latent columns, 128-byte swizzle.
+bool group_map(CUtensorMap* m, const void* base, uint64_t rows, bool codes) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {codes ? 128u : 64u, (cuuint64_t)rows, codes ? 4u : 8u};
+  const cuuint64_t strides[2] = {(cuuint64_t)kL * (codes ? 1 : 2), 128};
+  const cuuint32_t box[3] = {codes ? 128u : 64u, 8, codes ? 2u : 4u};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTA pairs that the current device holds at once (0: none; asked once per device).
+int max_pairs() {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];  // pairs + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return 0;
+  }
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n - 1;
+  n = 1 << 30;
+  for (int codes = 0; codes < 2; ++codes) {
+    auto kernel = codes ? mla_chunk_pair_kernel<true> : mla_chunk_pair_kernel<false>;
+    int got = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) ==
+        cudaSuccess) {
+      cudaLaunchAttribute a;
+      a.id = cudaLaunchAttributeClusterDimension;
+      a.val.clusterDim.x = 2;
+      a.val.clusterDim.y = a.val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(num_sms() / 2 * 2, 1, 1);
+      cfg.blockDim = dim3(pair_threads(codes), 1, 1);
+      cfg.dynamicSmemBytes = kSmem;
+      cfg.attrs = &a;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess) got = 0;
+    }
+    n = got < n ? got : n;
+  }
+  cudaGetLastError();  // a refused query leaves no error behind
+  if (n > num_sms() / 2) n = num_sms() / 2;
+  known[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+template <bool kCodes>
+int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
+  const int pairs = max_pairs();
+  Params p = {};
+  p.kv = a.kv;
+  p.cu_new = a.cu_new;
+  p.T = a.T;
+  p.B = a.B;
+  p.Hm = a.Hm;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.zscale = a.sm_scale * kLog2e;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.status = a.status;
+  p.drill = failure_drill();
+  p.prefetch = a.T <= 4 * a.B;
+  p.box_log = 3;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)pairs * 2 * 128 * kL);
+  p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)pairs * 2 * 128);
+  CUtensorMap q_map, kv_map;
+  if (!row_map(&q_map, a.q_lat, (uint64_t)a.T * a.Hm, 64) ||
+      !group_map(&kv_map, a.kv.pages, (uint64_t)a.kv.n_pages * a.kv.page_size, kCodes))
+    return DSA_ERR_CUDA;
+  auto kernel = mla_chunk_pair_kernel<kCodes>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) !=
+      cudaSuccess)
+    return DSA_ERR_CUDA;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(2 * pairs, 1, 1);
+  cfg.blockDim = dim3(pair_threads(kCodes), 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  if (launch_kernel(&cfg, kernel, q_map, kv_map, p) != cudaSuccess) return DSA_ERR_CUDA;
+  cfg.gridDim = dim3(pairs, 16, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return launch_kernel(&cfg, mla_chunk_join_kernel<128, true>, p, pairs) == cudaSuccess
+             ? DSA_OK
+             : DSA_ERR_CUDA;
+}
+
+}  // namespace
+
+bool mla_chunk_pair_ok(int T, int B, int Hm, int page_size) {
+  (void)T;
+  (void)B;
+  return Hm > 32 && page_size % 8 == 0 && max_pairs() > 0;
+}
+
+size_t mla_chunk_pair_workspace_size() {
+  const size_t pairs = num_sms() / 2;
+  return pairs * 2 * 128 * (kL * 4 + 8) + pairs * sizeof(Header);
+}
+
+int launch_mla_chunk_pair(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
+  return a.kv.kv_dtype == DSA_FP8_E4M3 ? launch<true>(a, workspace, stream)
+                                       : launch<false>(a, workspace, stream);
+}
+
+}  // namespace dsa

@@ -34,21 +34,14 @@
 // softmax of a tile stands between its two products: rows 128 KB, queries 64 KB
 // and P 16 KB leave no room for a second tile, so the tile is handed on in four
 // column chunks, each refilled as soon as its part of O^T is done.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-#include <math.h>
-
-#include "dsa_internal.cuh"
-#include "umma.cuh"
-
-#include <cudaTypedefs.h>
+#include "mla_chunk.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kL = 512, kKeys = 128;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRaiseAt = 20.f;
+using namespace chunk;
+
+constexpr int kKeys = 128;
 constexpr int kKvBlock = kKeys * 128;  // 128 rows x 64 latent columns, 16 KB
 constexpr int kSoftThreads = 256;      // warps 0..7
 
@@ -65,13 +58,6 @@ __host__ __device__ constexpr int cta_threads(int src) {
   return kSoftThreads + 32 * (tma_warps(src) + row_warps(src) + 1);
 }
 
-struct Header {        // what CTA g left for the join
-  int start_tile;      // row tile whose first units it holds but not its last (-1: none)
-  int cont_tile;       // row tile that an earlier CTA began (-1: none; -2: no share at all)
-  int cont_some;       // it has a partial of that
-  int cont_ends;       // and its last units
-};
-
 struct Ctl {
   float m[64], nm[64], alpha[64], l[64];  // per head; first: read as float4
   float red[4][64];
@@ -79,10 +65,8 @@ struct Ctl {
   int valid[kKeys];               // copied rows: the position is seen and has a page
   int prow[2][kKeys];
   uint64_t full[4], empty[4], raw[4], s_full, p_full, o_full, q_full, q_empty, drain;
-  unsigned long long scan[32];
+  Start start;
   uint32_t tmem;
-  int start_b;                    // the CTA's first unit: sequence (B: no share),
-  unsigned start_row, start_unit; // row tile of it, unit of that
   unsigned groups;                // TMA boxes of the tile that hold rows
   int raise;
   int soft_dead[2];
@@ -101,140 +85,7 @@ struct Smem {
 };
 static_assert(Smem<64>::kBytes <= 227 * 1024, "shared memory budget");
 
-struct Params {
-  PagedKv kv;
-  const int32_t* cu_new;
-  int T, B, Hm, window, sinks;
-  float zscale;              // sm_scale in base 2
-  __nv_bfloat16* out;
-  float* lse;
-  float* part_o;             // [2 CTAs][kN][kL]
-  float2* part_ml;           // [2 CTAs][kN]
-  Header* head;
-  int32_t* status;
-  int drill, prefetch;
-  int box_log;               // rows of a TMA box, 2^box_log (copied rows: 1)
-};
-
-// ---- the batch as units ------------------------------------------------------
-struct Seq {
-  int c0, n, base;             // rows c0 .. c0 + n - 1 of the step; position of the first
-  unsigned u;                  // units per row tile
-};
-__device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p) {
-  Seq s;
-  s.c0 = min(max(cu0, 0), p.T);
-  s.n = max(min(cu1, p.T) - s.c0, 0);
-  s.base = len < 0 ? -s.n : len - s.n;   // negative: rows before position 0
-  const unsigned all = (unsigned)max(len, 0);
-  s.u = (all + kKeys - 1) / kKeys;
-  if (p.window > 0) {
-    const long long R = 1 << p.box_log;
-    const long long keys = ((p.sinks + R - 1) / R + (p.window + R - 2) / R + 1) * R;
-    if ((keys + kKeys - 1) / kKeys < (long long)s.u) s.u = (unsigned)((keys + kKeys - 1) / kKeys);
-  }
-  s.u = max(s.u, 1u);
-  return s;
-}
-
-// One token's visible positions [0, s0) and [lo, pos] as boxes of R = 2^log
-// positions (aligned; the window's first and last may reach past it), 128 / R to a
-// key tile.
-struct Keys {
-  int pos, lo, s0, log, sink_boxes, first, boxes, n;
-  // position of row r of key tile v (past the last box: past pos)
-  __device__ __forceinline__ int at(int v, int r) const {
-    const int g = (v << (7 - log)) + (r >> log);
-    const int box = g < sink_boxes ? g : first + (g - sink_boxes);
-    return g < boxes ? (box << log) + (r & ((1 << log) - 1)) : 0x7fffffff;
-  }
-  __device__ __forceinline__ bool sees(int t) const { return t <= pos && (t >= lo || t < s0); }
-};
-__device__ __forceinline__ Keys keys_of(int pos, const Params& p) {
-  Keys k;
-  k.pos = pos;
-  k.log = p.box_log;
-  k.lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  k.s0 = min(p.sinks, k.lo);
-  k.first = k.lo >> k.log;
-  k.sink_boxes = min((k.s0 >> k.log) + ((k.s0 & ((1 << k.log) - 1)) != 0), k.first);
-  k.boxes = pos < 0 ? 0 : k.sink_boxes + (pos >> k.log) - k.first + 1;
-  k.n = (k.boxes + (1 << (7 - k.log)) - 1) >> (7 - k.log);
-  return k;
-}
-
-// a n / u, rounded down
-__device__ __forceinline__ int share_of(unsigned a, unsigned n, unsigned u) {
-  if (a == 0) return 0;
-  if (a == u) return (int)n;
-  if ((a | n) < 65536u) return (int)(a * n / u);
-  return (int)((unsigned long long)a * n / u);
-}
-
-// A walk over the CTA's units, row tile by row tile.  Every role walks alone; the
-// next sequence's lengths are read one sequence ahead.
-struct Walk {
-  const Params& p;
-  int hb;                       // head blocks per token: 1 or 2
-  unsigned long long left;      // units still to do
-  int b;
-  unsigned row, unit;           // of sequence b: row tile, unit of it
-  Seq s;
-  int cu_next, len_next;        // of sequence b + 1 (its end, its length)
-  // the current segment
-  int token, h0, tile_id, ta, tb;
-  Keys k;
-
-  __device__ __forceinline__ Walk(const Params& pp, int hb_, const Ctl& c, unsigned long long n)
-      : p(pp), hb(hb_), left(c.start_b < pp.B ? n : 0), b(c.start_b), row(c.start_row),
-        unit(c.start_unit) {
-    if (left == 0) return;
-    s = seq_of(__ldg(p.cu_new + b), __ldg(p.cu_new + b + 1), __ldg(p.kv.seq_lens + b), p);
-    ahead();
-  }
-  __device__ __forceinline__ void ahead() {
-    if (b + 1 < p.B) {
-      cu_next = __ldg(p.cu_new + b + 2);
-      len_next = __ldg(p.kv.seq_lens + b + 1);
-    }
-  }
-  // the next segment: a row tile and its key tiles [ta, tb) (none: ta == tb)
-  __device__ __forceinline__ bool next() {
-    if (left == 0) return false;
-    while (row >= (unsigned)s.n * hb) {  // units remain, so a sequence with some follows
-      if (++b >= p.B) return false;      // (lengths that changed under the call)
-      const int cu0 = __ldg(p.cu_new + b);
-      s = seq_of(cu0, cu_next, len_next, p);
-      ahead();
-      row = 0;
-    }
-    const unsigned e = left < s.u - unit ? unit + (unsigned)left : s.u;
-    const int kk = (int)(hb == 2 ? row >> 1 : row);
-    h0 = hb == 2 ? (int)(row & 1u) : 0;
-    const int i = (kk & 1) ? s.n - 1 - (kk >> 1) : kk >> 1;  // from both ends in turn
-    token = s.c0 + i;
-    tile_id = token * hb + h0;
-    k = keys_of(s.base + i < 0 ? -1 : s.base + i, p);
-    ta = share_of(unit, k.n, s.u);
-    tb = share_of(e, k.n, s.u);
-    left -= e - unit;
-    unit = e;
-    if (e == s.u) {
-      unit = 0;
-      ++row;
-    }
-    return true;
-  }
-};
-
 // ---- small pieces ------------------------------------------------------------
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // kW values per lane (one row, kW heads) reduced over the warp's 32 rows by
 // halving exchanges; lane l ends with head l mod kW.
 template <int kW, bool kMax>
@@ -260,22 +111,6 @@ __device__ __forceinline__ float across_rows(float (&v)[kW], int lane) {
   return v[0];
 }
 
-__device__ __forceinline__ void fma2(float& a0, float& a1, float b, float c0, float c1) {
-  unsigned long long a, bb, c;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(bb) : "f"(b));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
-  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a) : "l"(bb), "l"(c));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
-}
-__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
-  unsigned long long a, b;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
-}
-
 template <int kW>
 __device__ __forceinline__ void tmem_ldw(uint32_t ta, float (&v)[kW]) {
   if constexpr (kW == 32) tmem_ld32(ta, v); else tmem_ld16(ta, v);
@@ -299,12 +134,6 @@ __device__ __forceinline__ void tmem_stw(uint32_t ta, const float (&v)[kW]) {
   if constexpr (kW == 32) tmem_st32(ta, v); else tmem_st16(ta, v);
 }
 
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y)
-               : "memory");
-}
 // Barriers of one role's threads (barrier 0 is the CTA's).
 __device__ __forceinline__ void sync_soft() {
   asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
@@ -321,23 +150,6 @@ __device__ __forceinline__ bool vote_soft(bool v) {  // whether any of them says
 }
 __device__ __forceinline__ void sync_load() {
   asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
-}
-
-// A bounded wait that also ends when another role has given up.
-__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* dead,
-                                        unsigned long long limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*dead) return false;
-    if (global_ns() - t0 > limit_ns) {
-      *dead = 1;
-      return false;
-    }
-  }
 }
 
 // ---- the kernel --------------------------------------------------------------
@@ -370,7 +182,6 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
     mbar_init(&c.drain, 1);
     fence_mbar_init();
     c.soft_dead[0] = c.soft_dead[1] = c.dead = 0;
-    c.start_b = p.B;
   }
   if (warp == kMmaWarp) {
     tmem_alloc<kTmemCols>(&c.tmem);
@@ -383,62 +194,11 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
   pdl_wait();  // every input may come from the kernel just before
   pdl_launch_dependents();
 
-  // ---- this CTA's share of the batch's units
-  unsigned long long v0, v1;
-  {
-    constexpr int kT = cta_threads(kSrc);
-    const int per = (p.B + kT - 1) / kT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    unsigned long long mine = 0;
-    bool odd = false;
-    for (int b = b0; b < b1; ++b) {
-      const int cu0 = p.cu_new[b], cu1 = p.cu_new[b + 1], len = p.kv.seq_lens[b];
-      const Seq s = seq_of(cu0, cu1, len, p);
-      odd |= cu0 < 0 || cu1 < cu0 || cu1 > p.T || (s.n > 0 && s.base < 0);
-      mine += (unsigned long long)s.n * (unsigned)hb * s.u;
-    }
-    if (odd && blockIdx.x == 0) flag(p.status, DSA_DEV_BAD_LENGTH);
-    unsigned long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
-    }
-    if (lane == 31) c.scan[warp] = inc;
-    __syncthreads();
-    unsigned long long before = inc - mine, total = 0;
-    for (int w = 0; w < kT / 32; ++w) {
-      if (w < warp) before += c.scan[w];
-      total += c.scan[w];
-    }
-    if (total < (1ull << 32) / 256) {  // (fewer than 256 CTAs: a product of 32 bits)
-      v0 = (unsigned)total * blockIdx.x / gridDim.x;
-      v1 = (unsigned)total * (blockIdx.x + 1) / gridDim.x;
-    } else {
-      v0 = total * blockIdx.x / gridDim.x;
-      v1 = total * (blockIdx.x + 1) / gridDim.x;
-    }
-    if (v0 < v1 && v0 >= before && v0 < before + mine) {
-      unsigned long long at = before;
-      for (int b = b0; b < b1; ++b) {
-        const Seq s = seq_of(p.cu_new[b], p.cu_new[b + 1], p.kv.seq_lens[b], p);
-        const unsigned long long all = (unsigned long long)s.n * (unsigned)hb * s.u;
-        if (v0 < at + all) {
-          const unsigned long long off = v0 - at;
-          c.start_b = b;
-          c.start_row = (unsigned)(off >> 32 ? off / s.u : (unsigned)off / s.u);
-          c.start_unit = (unsigned)(off - (unsigned long long)c.start_row * s.u);
-          break;
-        }
-        at += all;
-      }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-  }
+  const unsigned long long units = find_share<kKeys, false, cta_threads(kSrc)>(
+      p, hb, blockIdx.x, gridDim.x, &c.start, blockIdx.x == 0);
   const uint32_t tmem = c.tmem;
-  const bool any = c.start_b < p.B;
-  Walk w(p, hb, c, v1 - v0);
+  const bool any = c.start.b < p.B;
+  Walk<kKeys, false> w(p, hb, c.start, units);
   // a failure drill loads nothing and issues no MMA: the first waits run out
   const bool issue = p.drill == 0;
   const unsigned long long wait_ns = p.drill ? kDrillWaitNs : kWaitNs;
@@ -665,7 +425,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       const int R = 1 << p.box_log, ng = kKeys >> p.box_log;
       int issued = 0;  // chunks of tile `tiles` under way
       // the cache row of this lane's box of a tile (-1: nothing seen, -2: no page)
-      auto box_row = [&](const Keys& k, int b, int v) -> int {
+      auto box_row = [&](const Keys<kKeys>& k, int b, int v) -> int {
         if (lane >= ng) return -1;
         const int t0 = k.at(v, lane * R);
         if (t0 > k.pos) return -1;
@@ -742,7 +502,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       // Widen a chunk of codes in place: 128 rows of 128 codes land in its first
       // block, every thread takes 8 of their 16-byte pieces into registers, and once
       // all have, both blocks take the bf16 rows.
-      auto scale_of = [&](const Keys& k, int b, int v) -> float {
+      auto scale_of = [&](const Keys<kKeys>& k, int b, int v) -> float {
         const int t = k.at(v, lt);
         if (!k.sees(t)) return 0.f;
         const int blk = t / p.kv.page_size;
@@ -799,7 +559,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       }
     } else {
       // the cache row of position t (-1: not seen or no page)
-      auto row_of = [&](const Keys& k, int b, int t) -> int {
+      auto row_of = [&](const Keys<kKeys>& k, int b, int t) -> int {
         if (t > k.pos) return -1;  // (single positions: none but visible ones)
         const int blk = t / p.kv.page_size;
         int page = -1;
@@ -974,99 +734,6 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
   }
 }
 
-// Join the partials of the row tiles that were split over CTAs, in CTA order: block
-// (g, y) takes the tile that CTA g began, heads 8 y ... (one warp per head, four
-// 16-byte pieces of the latent row a lane).
-template <int kN>
-__global__ void __launch_bounds__(256)
-    mla_chunk_join_kernel(const Params p, int n_cta) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int g = blockIdx.x, lane = threadIdx.x & 31;
-  const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int tile = p.head[g].start_tile;
-  if (tile < 0) return;
-  const int hb = (p.Hm + kN - 1) / kN;
-  const int token = tile / hb, head = (tile - token * hb) * kN + h;
-  if (head >= p.Hm) return;
-  float mx = -INFINITY, den = 0.f;
-  float4 acc[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = g; s < n_cta; ++s) {
-    int slot = 2 * g + 1;
-    bool last = false;
-    if (s > g) {
-      const Header hd = p.head[s];
-      if (hd.cont_tile == -2) continue;
-      if (hd.cont_tile != tile) break;
-      last = hd.cont_ends;
-      slot = 2 * s;
-      if (!hd.cont_some) {
-        if (last) break;
-        continue;
-      }
-    }
-    const float2 ml = p.part_ml[slot * kN + h];
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + ((long long)slot * kN + h) * kL);
-    float4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __ldcs(src + i * 32 + lane);
-    if (ml.y != 0.f) {  // a part that saw no page has nothing to add
-      const float m = fmaxf(mx, ml.x), ref = m == -INFINITY ? 0.f : m;
-      const float a = ex2_fast(mx - ref), b = ex2_fast(ml.x == -INFINITY ? 0.f : ml.x - ref);
-      den = den * a + ml.y * b;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i].x = acc[i].x * a + v[i].x * b;
-        acc[i].y = acc[i].y * a + v[i].y * b;
-        acc[i].z = acc[i].z * a + v[i].z * b;
-        acc[i].w = acc[i].w * a + v[i].w * b;
-      }
-      mx = m;
-    }
-    if (last) break;
-  }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  const long long row = (long long)token * p.Hm + head;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<uint2*>(p.out + row * kL + (i * 32 + lane) * 4) =
-        make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv),
-                   pack_bf16(acc[i].z * inv, acc[i].w * inv));
-  if (p.lse && lane == 0) p.lse[row] = den == 0.f ? -INFINITY : (mx + log2f(den)) / kLog2e;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
-// [rows, 512] bf16, boxes of 64 columns x box_rows rows, 128-byte swizzle; rows at
-// or beyond `rows` read as zeros.
-// codes: [rows, 512] bytes, boxes of 128 columns, no swizzle.
-bool row_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows,
-             bool codes = false) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)kL, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)kL * (codes ? 1 : 2)};
-  const cuuint32_t box[2] = {codes ? 128u : 64u, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int box_log_of(int page_size) {  // largest power of two that divides it, 128 at most
   int log = 0;
   while (log < 7 && page_size % (2 << log) == 0) ++log;
@@ -1125,7 +792,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   cfg.gridDim = dim3(n_cta, kN / 8, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return launch_kernel(&cfg, mla_chunk_join_kernel<kN>, p, n_cta) == cudaSuccess ? DSA_OK
+  return launch_kernel(&cfg, mla_chunk_join_kernel<kN, false>, p, n_cta) == cudaSuccess ? DSA_OK
                                                                                  : DSA_ERR_CUDA;
 }
 
