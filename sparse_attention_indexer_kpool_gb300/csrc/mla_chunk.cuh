@@ -278,13 +278,13 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, i
 // A bounded wait that also ends when another role has given up.
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* dead,
                                         unsigned long long limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
+  unsigned long long t0 = 0;
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*dead) return false;
+    if (t0 == 0) t0 = global_ns();
     if (global_ns() - t0 > limit_ns) {
       *dead = 1;
       return false;

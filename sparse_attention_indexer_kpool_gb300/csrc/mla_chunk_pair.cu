@@ -37,20 +37,24 @@ constexpr int kGroups = kKT / 8;             // of 8 rows: 4 KB, [64-column bloc
 constexpr int kStageBytes = kGroups * 4096;  // 40 KB
 constexpr int kStages = 3;
 constexpr int kQBlock = 128 * 128;           // 128 rows x 64 latent columns
-constexpr int kSoftThreads = 256;
-constexpr int kW = kKT / 2;                  // scores of a softmax thread
+// Warps 0..15 by TMEM lane quarter (warp mod 4): the quarters of this CTA's row block
+// have four softmax warps each (20 keys a thread); the other block's have two that send
+// its partial scores and two that receive its weights (40 keys a thread).
+constexpr int kRowWarps = 16;
+constexpr int kOwnWarps = 8, kTakeWarps = 4;
+constexpr int kW = kKT / 4;
 constexpr int kWidenWarps = 5;               // E4M3: two groups each
 constexpr size_t kOffQ = 0;
 constexpr size_t kOffK = 4 * (size_t)kQBlock;
 constexpr size_t kOffS = kOffK + (size_t)kStages * kStageBytes;   // [20][64 rows] x 16 B
-constexpr size_t kOffP = kOffS + (size_t)(kKT / 4) * 64 * 16;     // [10][64 rows] x 16 B
+constexpr size_t kOffP = kOffS + (size_t)(kKT / 4) * 64 * 16;     // [20][64 rows] x 8 B
 constexpr uint32_t kSBytes = kKT * 64 * 4, kPBytes = kKT * 64 * 2 + 64 * 4;
 
 struct Ctl {
   float rs[kStages][kKT];          // E4M3: the keys' row scales (first: read as float4)
   float alpha[64];                 // from the other CTA: its rows' rescale of this tile
   float inv[128];                  // 1 / sum of every row (the other CTA's rows: sent)
-  float mx[2][64], sum[2][64];     // own rows: the two threads of a row
+  float mx[4][64], sum[4][64];     // own rows: the four threads of a row
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], raw[kStages];
   uint64_t s_full[kStages], p_full[kStages], o_full, drain;
   uint64_t in_s, in_p, in_l;       // data from the other CTA
@@ -59,16 +63,16 @@ struct Ctl {
   Start start;
   uint32_t tmem;
   unsigned groups[kStages];        // groups of the tile that have a page
-  int own_dead[2], send_dead[2];
+  int own_dead[2];
   int dead;
 };
-constexpr size_t kOffCtl = kOffP + (size_t)(kKT / 8) * 64 * 16;
+constexpr size_t kOffCtl = kOffP + (size_t)(kKT / 4) * 64 * 8;
 constexpr size_t kSmem = 1024 + kOffCtl + sizeof(Ctl);
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 static_assert(256 + kStages * kKT <= 512, "TMEM columns");
 
 __host__ __device__ constexpr int pair_threads(bool codes) {
-  return kSoftThreads + 32 * (2 + (codes ? kWidenWarps : 0));
+  return 32 * (kRowWarps + 2 + (codes ? kWidenWarps : 0));
 }
 
 // ---- cluster pieces ------------------------------------------------------------
@@ -88,12 +92,19 @@ __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// 16 / 4 bytes to the other CTA; counted on its barrier
+// 16 / 8 / 4 bytes to the other CTA; counted on its barrier
 __device__ __forceinline__ void send16(uint32_t addr, uint4 v, uint32_t bar) {
   asm volatile(
       "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4},"
       " [%5];" ::"r"(addr),
       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void send8(uint32_t addr, uint32_t x, uint32_t y, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1,%2}, [%3];" ::"r"(
+          addr),
+      "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void send4(uint32_t addr, float v, uint32_t bar) {
@@ -103,34 +114,8 @@ __device__ __forceinline__ void send4(uint32_t addr, float v, uint32_t bar) {
       : "memory");
 }
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* dead,
-                                             unsigned long long limit_ns) {
-  if (try_wait_cluster(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (try_wait_cluster(bar, parity)) return true;
-    if (*dead) return false;
-    if (global_ns() - t0 > limit_ns) {
-      *dead = 1;
-      return false;
-    }
-  }
 }
 // whether the phase has completed, without waiting
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
@@ -143,14 +128,14 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// barriers of the four warps that own rows (1) and of the four that send (2)
-__device__ __forceinline__ bool vote4(int id, bool v) {
+// a barrier of the softmax warps: whether any of their threads says so
+__device__ __forceinline__ bool vote_own(bool v) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n"
-      " barrier.cta.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"(id), "r"((uint32_t)v)
+      : "r"((uint32_t)v), "n"(kOwnWarps * 32)
       : "memory");
   return r != 0;
 }
@@ -174,6 +159,34 @@ __device__ __forceinline__ void tmem_ld40(uint32_t ta, float (&v)[40]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 40; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 20 columns.
+__device__ __forceinline__ void tmem_ld20(uint32_t ta, float (&v)[20]) {
+  uint32_t r[20];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(ta));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19])
+               : "r"(ta + 16));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 20; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 10 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_st10(uint32_t ta, const uint32_t (&v)[10]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+               "r"(v[7])
+               : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(ta + 8), "r"(v[8]),
+               "r"(v[9])
+               : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 // 20 consecutive 32-bit columns.
 __device__ __forceinline__ void tmem_st20(uint32_t ta, const uint32_t (&v)[20]) {
@@ -231,7 +244,7 @@ template <bool kCodes>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes), 1)
     mla_chunk_pair_kernel(const __grid_constant__ CUtensorMap q_map,
                           const __grid_constant__ CUtensorMap kv_map, const Params p) {
-  constexpr int kTmaWarp = kSoftThreads / 32, kMmaWarp = kTmaWarp + 1, kWiden0 = kMmaWarp + 1;
+  constexpr int kTmaWarp = kRowWarps, kMmaWarp = kTmaWarp + 1, kWiden0 = kMmaWarp + 1;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl& c = *reinterpret_cast<Ctl*>(sb + kOffCtl);
@@ -248,18 +261,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
       mbar_init(&c.k_empty[i], 1);
       mbar_init(&c.raw[i], 1);
       mbar_init(&c.s_full[i], 1);
-      mbar_init(&c.p_full[i], kSoftThreads / 32);
+      mbar_init(&c.p_full[i], kOwnWarps + kTakeWarps);
     }
     mbar_init(&c.o_full, 1);
     mbar_init(&c.drain, 1);
     mbar_init(&c.in_s, 1);
     mbar_init(&c.in_p, 1);
     mbar_init(&c.in_l, 1);
-    mbar_init(&c.free_s, 4);
-    mbar_init(&c.free_p, 4);
-    mbar_init(&c.epi, kSoftThreads / 32);
+    mbar_init(&c.free_s, kOwnWarps);
+    mbar_init(&c.free_p, kTakeWarps);
+    mbar_init(&c.epi, kOwnWarps + kTakeWarps);
     fence_mbar_init();
-    c.own_dead[0] = c.own_dead[1] = c.send_dead[0] = c.send_dead[1] = c.dead = 0;
+    c.own_dead[0] = c.own_dead[1] = c.dead = 0;
   }
   if (warp == kMmaWarp) {
     tmem_alloc<512>(&c.tmem);
@@ -278,351 +291,363 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
   const unsigned long long wait_ns = p.drill ? kDrillWaitNs : kWaitNs;
   volatile int* dead = &c.dead;
 
-  if (warp < kTmaWarp) {
-    // ================= softmax, exchange, epilogue =================
-    const int qw = warp & 3, h = warp >> 2;  // TMEM lanes 32 qw .., keys 40 h ..
-    const int g = qw >> 1;                   // row block of these lanes
+  if (warp < kRowWarps) {
+    const int qw = warp & 3, part = warp >> 2;  // TMEM lanes 32 qw ..
+    const int g = qw >> 1;                      // row block of these lanes
     const bool own = g == (int)rank;
-    const int r = (qw & 1) * 32 + lane;      // row of the block
+    const int r = (qw & 1) * 32 + lane;         // row of the block
     const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16);
-    const uint32_t to_s = map_to(smem_u32(sb + kOffS) + (h * 10 * 64 + r) * 16, other);
-    const uint32_t to_p = map_to(smem_u32(sb + kOffP) + (h * 5 * 64 + r) * 16, other);
-    const uint32_t bar_s = map_to(smem_u32(&c.in_s), other),
-                   bar_p = map_to(smem_u32(&c.in_p), other),
-                   bar_l = map_to(smem_u32(&c.in_l), other),
-                   bar_free_s = map_to(smem_u32(&c.free_s), other),
-                   bar_free_p = map_to(smem_u32(&c.free_p), other);
-    const uint4* in_s = reinterpret_cast<const uint4*>(sb + kOffS) + h * 10 * 64 + r;
-    const uint4* in_p = reinterpret_cast<const uint4*>(sb + kOffP) + h * 5 * 64 + r;
-    Header hd = {-1, any ? -1 : -2, 0, 0};
-    int tiles = 0, segs = 0, sums = 0;
-    bool ok = true;
-    // the phases of the data from the other CTA are armed one ahead
-    if (any) {
-      if (own && tid == 64 * (int)rank) {
-        mbar_arrive_expect_tx(&c.in_s, kSBytes);
-        mbar_arrive_expect_tx(&c.in_l, 64 * 4);
-      }
-      if (!own && tid == 64 * (int)other) mbar_arrive_expect_tx(&c.in_p, kPBytes);
-    }
-    while (ok && w.next()) {
-      // this thread's row block: its token, its heads, what it sees
-      const bool there = p.Hm > 64 || g == 0 || w.two;
-      const int token = p.Hm > 64 ? w.token : w.token + (there ? g : 0);
-      const int head = p.Hm > 64 ? g * 64 + r : r;
-      const bool live = there && head < p.Hm;
-      const int pos_a = w.pos0 < 0 ? -1 : w.pos0;
-      // (a missing second token sees what the first one does, for nobody)
-      const int pos_b = w.two ? (w.pos0 + 1 < 0 ? -1 : w.pos0 + 1) : pos_a;
-      const Sight sa = sight_of(pos_a, p), sbt = sight_of(pos_b, p);
-      const Sight mine = g == 0 ? sa : sbt;
-      float m = -INFINITY, l = 0.f;
-      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
-        const int st = tiles % kStages, ph = (tiles / kStages) & 1;
-        const uint32_t tS = tl + 256 + (uint32_t)(st * kKT);
-        bool fine = wait_on(&c.s_full[st], ph, dead, wait_ns);
-        tc_fence_after();
-        float e[kW];
-        tmem_ld40(tS + h * kW, e);
-        // is every key of the tile seen by both blocks?
-        const int t0 = w.k.at(v, 0), t1 = w.k.at(v, kKT - 1);
-        const bool plain = c.groups[st] == (1u << kGroups) - 1 && t1 - t0 == kKT - 1 &&
-                           t0 >= max(sa.lo, sbt.lo) && t1 <= min(sa.pos, sbt.pos);
-        if (!plain && (tid >> 1) < kKT) {
-          // clear what neither sees, and what one does not see if it is not finite
-          const int key = tid >> 1;
-          const int t = w.k.at(v, key);
-          const bool paged = (c.groups[st] >> (key >> 3)) & 1u;
-          const bool ina = paged && sa(t), inb = paged && sbt(t);
-          if (!(ina && inb)) {
-            unsigned char* kr = sb + kOffK + st * kStageBytes + (key >> 3) * 4096 +
-                                (tid & 1) * 2048 + (key & 7) * 128;
-            bool odd = !(ina || inb);
-            if (!odd) {
-              for (int i = 0; i < 16; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4*>(
-                    kr + (i >> 3) * 1024 + (((i & 7) ^ (key & 7)) << 4));
-                const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
-                for (int j = 0; j < 4; ++j)
-                  odd |= (wd[j] & 0x7f80u) == 0x7f80u || (wd[j] & 0x7f800000u) == 0x7f800000u;
-              }
-            }
-            if (odd)
-              for (int i = 0; i < 16; ++i)
-                *reinterpret_cast<uint4*>(kr + (i >> 3) * 1024 +
-                                          (((i & 7) ^ (key & 7)) << 4)) =
-                    make_uint4(0u, 0u, 0u, 0u);
-          }
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_on(bar, parity, dead, wait_ns)) != 0;
+    };
+    if (!own && part < 2) {
+      // ================= send the other block's partial scores =================
+      const int h = part;  // keys 40 h ..
+      const uint32_t to_s = map_to(smem_u32(sb + kOffS) + (h * 10 * 64 + r) * 16, other);
+      const uint32_t bar_s = map_to(smem_u32(&c.in_s), other);
+      int tiles = 0;
+      bool ok = true;
+      while (ok && w.next()) {
+        for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+          const int st = tiles % kStages;
+          ok = wait_all(&c.s_full[st], (tiles / kStages) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          float e[40];
+          tmem_ld40(tl + 256 + (uint32_t)(st * kKT + h * 40), e);
+          tc_fence_before();
+          // the other CTA has read the last tile's
+          ok = tiles == 0 || wait_all(&c.free_s, (tiles - 1) & 1);
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 10; ++j)
+            send16(to_s + j * 64 * 16,
+                   make_uint4(__float_as_uint(e[4 * j]), __float_as_uint(e[4 * j + 1]),
+                              __float_as_uint(e[4 * j + 2]), __float_as_uint(e[4 * j + 3])),
+                   bar_s);
         }
+      }
+    } else {
+      // ================= softmax of the own block; weights of the other =================
+      const int q4 = part;             // own: keys 20 q4 ..
+      const int h = part & 1;          // other: keys 40 h ..
+      const int o0 = own ? q4 * 64 : h * 128, o_n = own ? 2 : 4;  // O columns, in blocks of 32
+      const bool first = own ? (warp == 2 * (int)rank) : (warp == 8 + 2 * (int)other);
+      const uint32_t to_p = map_to(smem_u32(sb + kOffP) + (q4 * 5 * 64 + r) * 8, other);
+      const uint32_t bar_p = map_to(smem_u32(&c.in_p), other),
+                     bar_l = map_to(smem_u32(&c.in_l), other),
+                     bar_free_s = map_to(smem_u32(&c.free_s), other),
+                     bar_free_p = map_to(smem_u32(&c.free_p), other);
+      const uint4* in_s = reinterpret_cast<const uint4*>(sb + kOffS) + q4 * 5 * 64 + r;
+      const uint2* in_p = reinterpret_cast<const uint2*>(sb + kOffP) + h * 10 * 64 + r;
+      const int otid = ((warp & 1) + 2 * part) * 32 + lane;  // own: 0..255
+      Header hd = {-1, any ? -1 : -2, 0, 0};
+      int tiles = 0, segs = 0, sums = 0;
+      bool ok = true;
+      // The phases of the data from the other CTA are armed one ahead.  (Nothing of
+      // the next phase is sent before every reader of this one has said so.)
+      if (any && first && lane == 0) {
         if (own) {
-          fine = fine && wait_cluster(&c.in_s, tiles & 1, dead, wait_ns);
+          mbar_arrive_expect_tx(&c.in_s, kSBytes);
+          mbar_arrive_expect_tx(&c.in_l, 64 * 4);
+        } else {
+          mbar_arrive_expect_tx(&c.in_p, kPBytes);
+        }
+      }
+      // O of the tiles so far, once the last of them is in it
+      auto rescale = [&](int tiles, float alpha) {
+        wait_on(&c.k_empty[(tiles - 1) % kStages], ((tiles - 1) / kStages) & 1, dead, wait_ns);
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll 1
+        for (int cc = 0; cc < o_n; ++cc) {
+          float o[32];
+          tmem_ld32(tl + o0 + cc * 32, o);
 #pragma unroll
-          for (int j = 0; j < 10; ++j) {
-            const uint4 x = in_s[j * 64];
-            e[4 * j] += __uint_as_float(x.x);
-            e[4 * j + 1] += __uint_as_float(x.y);
-            e[4 * j + 2] += __uint_as_float(x.z);
-            e[4 * j + 3] += __uint_as_float(x.w);
-          }
-          __syncwarp();
-          if (lane == 0) arrive_remote(bar_free_s);
-          // the keys this block sees, 40 bits
-          uint32_t see_lo = 0xffffffffu, see_hi = 0xffu;
-          if (!plain) {
-            const int ta = w.k.at(v, h * kW + lane);
-            see_lo = __ballot_sync(
-                0xffffffffu, mine(ta) && ((c.groups[st] >> ((h * kW + lane) >> 3)) & 1u));
-            const int tb = w.k.at(v, h * kW + 32 + (lane & 7));
-            see_hi = __ballot_sync(0xffffffffu,
-                                   lane < 8 && mine(tb) &&
-                                       ((c.groups[st] >> ((h * kW + 32 + (lane & 7)) >> 3)) & 1u));
-          }
-          const float nm = m == -INFINITY ? 0.f : -m;
-          if constexpr (kCodes) {
-#pragma unroll
-            for (int q = 0; q < 10; ++q) {
-              const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + h * kW)[q];
-              e[4 * q] = fmaf(e[4 * q], p.zscale * rs.x, nm);
-              e[4 * q + 1] = fmaf(e[4 * q + 1], p.zscale * rs.y, nm);
-              e[4 * q + 2] = fmaf(e[4 * q + 2], p.zscale * rs.z, nm);
-              e[4 * q + 3] = fmaf(e[4 * q + 3], p.zscale * rs.w, nm);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < kW; i += 2) fma2(e[i], e[i + 1], p.zscale, nm, nm);
-          }
-          if (!plain) {
-#pragma unroll
-            for (int i = 0; i < kW; ++i)
-              if (!((i < 32 ? see_lo >> i : see_hi >> (i - 32)) & 1u)) e[i] = -INFINITY;
-          }
-          float top = e[0];
-#pragma unroll
-          for (int i = 1; i < kW; ++i) top = fmaxf(top, e[i]);
-          if (!fine) c.own_dead[tiles & 1] = 1;
-          c.mx[h][r] = top;  // relative to the reference
-          const bool full = vote4(1, live && (m == -INFINITY || top > kRaiseAt));
-          if (c.own_dead[tiles & 1]) {
-            ok = false;
-            break;
-          }
-          if (tid == 64 * (int)rank) mbar_arrive_expect_tx(&c.in_s, kSBytes);  // the next tile's
-          float alpha = 1.f;
-          if (full) {
-            const float both = fmaxf(c.mx[0][r], c.mx[1][r]);  // of the row, relative
-            float step = 0.f;
-            if (m == -INFINITY) {
-              if (both > -INFINITY) {  // the first key that this row sees
-                m = both;              // (nothing accumulated: no rescale)
-                step = -both;
+          for (int i = 0; i < 32; ++i) o[i] *= alpha;
+          tmem_st32(tl + o0 + cc * 32, o);
+        }
+      };
+      while (ok && w.next()) {
+        // this thread's row block: its token, its heads, what it sees
+        const bool there = p.Hm > 64 || g == 0 || w.two;
+        const int token = p.Hm > 64 ? w.token : w.token + (there ? g : 0);
+        const int head = p.Hm > 64 ? g * 64 + r : r;
+        const bool live = there && head < p.Hm;
+        const int pos_a = w.pos0 < 0 ? -1 : w.pos0;
+        // (a missing second token sees what the first one does, for nobody)
+        const int pos_b = w.two ? (w.pos0 + 1 < 0 ? -1 : w.pos0 + 1) : pos_a;
+        const Sight sa = sight_of(pos_a, p), sbt = sight_of(pos_b, p);
+        const Sight mine = g == 0 ? sa : sbt;
+        float m = -INFINITY, l = 0.f;
+        for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+          const int st = tiles % kStages, ph = (tiles / kStages) & 1;
+          const uint32_t tS = tl + 256 + (uint32_t)(st * kKT);
+          if (own) {
+            bool fine = wait_on(&c.s_full[st], ph, dead, wait_ns);
+            __syncwarp();
+            tc_fence_after();
+            float e[kW];
+            tmem_ld20(tS + q4 * kW, e);
+            // is every key of the tile seen by both blocks?
+            const int t0 = w.k.at(v, 0), t1 = w.k.at(v, kKT - 1);
+            const bool plain = c.groups[st] == (1u << kGroups) - 1 && t1 - t0 == kKT - 1 &&
+                               t0 >= max(sa.lo, sbt.lo) && t1 <= min(sa.pos, sbt.pos);
+            if (!plain && (otid >> 1) < kKT) {
+              // clear what neither sees, and what one does not see if it is not finite
+              const int key = otid >> 1;
+              const int t = w.k.at(v, key);
+              const bool paged = (c.groups[st] >> (key >> 3)) & 1u;
+              const bool ina = paged && sa(t), inb = paged && sbt(t);
+              if (!(ina && inb)) {
+                unsigned char* kr = sb + kOffK + st * kStageBytes + (key >> 3) * 4096 +
+                                    (otid & 1) * 2048 + (key & 7) * 128;
+                bool odd = !(ina || inb);
+                if (!odd) {
+                  for (int i = 0; i < 16; ++i) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(
+                        kr + (i >> 3) * 1024 + (((i & 7) ^ (key & 7)) << 4));
+                    const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+                    for (int j = 0; j < 4; ++j)
+                      odd |= (wd[j] & 0x7f80u) == 0x7f80u || (wd[j] & 0x7f800000u) == 0x7f800000u;
+                  }
+                }
+                if (odd)
+                  for (int i = 0; i < 16; ++i)
+                    *reinterpret_cast<uint4*>(kr + (i >> 3) * 1024 +
+                                              (((i & 7) ^ (key & 7)) << 4)) =
+                        make_uint4(0u, 0u, 0u, 0u);
               }
-            } else if (both > kRaiseAt) {
-              m += both;
-              step = -both;
-              alpha = ex2_fast(-both);
-              l *= alpha;
+              fence_proxy_async_smem();
             }
-            // (an infinite maximum: its key's weight is NaN, as in the formula)
-#pragma unroll
-            for (int i = 0; i < kW; ++i) e[i] += step;
-          }
-#pragma unroll
-          for (int i = 0; i < kW; ++i) e[i] = ex2_fast(e[i]);
-          float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < kW; i += 4) {
-            add2(s4[0], s4[1], e[i], e[i + 1]);
-            add2(s4[2], s4[3], e[i + 2], e[i + 3]);
-          }
-          l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          // P is rounded to bf16 for the tensor cores; the sums keep the unrounded
-          // weights.  An E4M3 row's scale goes to its weights.
-          uint32_t pk[20];
-          if constexpr (kCodes) {
-#pragma unroll
-            for (int q = 0; q < 10; ++q) {
-              const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + h * kW)[q];
-              e[4 * q] *= rs.x;
-              e[4 * q + 1] *= rs.y;
-              e[4 * q + 2] *= rs.z;
-              e[4 * q + 3] *= rs.w;
+            // the keys of this warp that the own block sees, 20 bits
+            uint32_t see = 0xfffffu;
+            if (!plain) {
+              const int key = q4 * kW + min(lane, kW - 1);
+              see = __ballot_sync(0xffffffffu, mine(w.k.at(v, key)) &&
+                                                   ((c.groups[st] >> (key >> 3)) & 1u));
             }
-            if (!plain) {  // (a hidden key's scale may be anything)
+            fine = fine && wait_on(&c.in_s, tiles & 1, dead, wait_ns);
+            __syncwarp();
+            if (first && lane == 0) mbar_arrive_expect_tx(&c.in_s, kSBytes);  // the next tile's
+#pragma unroll
+            for (int j = 0; j < 5; ++j) {
+              const uint4 x = in_s[j * 64];
+              e[4 * j] += __uint_as_float(x.x);
+              e[4 * j + 1] += __uint_as_float(x.y);
+              e[4 * j + 2] += __uint_as_float(x.z);
+              e[4 * j + 3] += __uint_as_float(x.w);
+            }
+            __syncwarp();
+            if (lane == 0) arrive_remote(bar_free_s);
+            const float nm = m == -INFINITY ? 0.f : -m;
+            if constexpr (kCodes) {
+#pragma unroll
+              for (int q = 0; q < 5; ++q) {
+                const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + q4 * kW)[q];
+                e[4 * q] = fmaf(e[4 * q], p.zscale * rs.x, nm);
+                e[4 * q + 1] = fmaf(e[4 * q + 1], p.zscale * rs.y, nm);
+                e[4 * q + 2] = fmaf(e[4 * q + 2], p.zscale * rs.z, nm);
+                e[4 * q + 3] = fmaf(e[4 * q + 3], p.zscale * rs.w, nm);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kW; i += 2) fma2(e[i], e[i + 1], p.zscale, nm, nm);
+            }
+            if (!plain) {
 #pragma unroll
               for (int i = 0; i < kW; ++i)
-                if (!((i < 32 ? see_lo >> i : see_hi >> (i - 32)) & 1u)) e[i] = 0.f;
+                if (!((see >> i) & 1u)) e[i] = -INFINITY;
             }
-          }
+            float t4[4] = {e[0], e[1], e[2], e[3]};
 #pragma unroll
-          for (int i = 0; i < 20; ++i) pk[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
-          // the other CTA has taken the last tile's weights
-          if (tiles > 0 && !wait_cluster(&c.free_p, (tiles - 1) & 1, dead, wait_ns)) {
-            c.own_dead[(tiles + 1) & 1] = 1;
+            for (int i = 4; i < kW; ++i) t4[i & 3] = fmaxf(t4[i & 3], e[i]);
+            const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+            if (!fine) c.own_dead[tiles & 1] = 1;
+            c.mx[q4][r] = top;  // relative to the reference
+            // (also: every thread of a row has read its scores, which P overlays)
+            const bool full = vote_own(live && (m == -INFINITY || top > kRaiseAt));
+            if (c.own_dead[tiles & 1]) {
+              ok = false;
+              break;
+            }
+            float alpha = 1.f;
+            if (full) {
+              const float both = fmaxf(fmaxf(c.mx[0][r], c.mx[1][r]),
+                                       fmaxf(c.mx[2][r], c.mx[3][r]));  // of the row, relative
+              float step = 0.f;
+              if (m == -INFINITY) {
+                if (both > -INFINITY) {  // the first key that this row sees
+                  m = both;              // (nothing accumulated: no rescale)
+                  step = -both;
+                }
+              } else if (both > kRaiseAt) {
+                m += both;
+                step = -both;
+                alpha = ex2_fast(-both);
+                l *= alpha;
+              }
+              // (an infinite maximum: its key's weight is NaN, as in the formula)
+#pragma unroll
+              for (int i = 0; i < kW; ++i) e[i] += step;
+            }
+#pragma unroll
+            for (int i = 0; i < kW; ++i) e[i] = ex2_fast(e[i]);
+            float s4[4] = {e[0], e[1], e[2], e[3]};
+#pragma unroll
+            for (int i = 4; i < kW; i += 4) {
+              add2(s4[0], s4[1], e[i], e[i + 1]);
+              add2(s4[2], s4[3], e[i + 2], e[i + 3]);
+            }
+            l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            // P is rounded to bf16 for the tensor cores; the sums keep the unrounded
+            // weights.  An E4M3 row's scale goes to its weights.
+            uint32_t pk[10];
+            if constexpr (kCodes) {
+#pragma unroll
+              for (int q = 0; q < 5; ++q) {
+                const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + q4 * kW)[q];
+                e[4 * q] *= rs.x;
+                e[4 * q + 1] *= rs.y;
+                e[4 * q + 2] *= rs.z;
+                e[4 * q + 3] *= rs.w;
+              }
+              if (!plain) {  // (a hidden key's scale may be anything)
+#pragma unroll
+                for (int i = 0; i < kW; ++i)
+                  if (!((see >> i) & 1u)) e[i] = 0.f;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 10; ++i) pk[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+            // the other CTA has taken the last tile's weights
+            if (tiles > 0 && !wait_on(&c.free_p, (tiles - 1) & 1, dead, wait_ns)) {
+              c.own_dead[(tiles + 1) & 1] = 1;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 5; ++j)
+                send8(to_p + j * 64 * 8, pk[2 * j], pk[2 * j + 1], bar_p);
+              if (q4 == 0) send4(map_to(smem_u32(&c.alpha[r]), other), alpha, bar_p);
+            }
+            __syncwarp();
+            if (v > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) rescale(tiles, alpha);
+            tmem_st10(tS + q4 * 10, pk);
           } else {
+            // ---- the other block's weights (its scores here were read before the
+            // other CTA could make them)
+            ok = wait_all(&c.in_p, tiles & 1);
+            if (!ok) break;
+            if (first && lane == 0) mbar_arrive_expect_tx(&c.in_p, kPBytes);  // the next tile's
+            uint32_t pk[20];
 #pragma unroll
-            for (int j = 0; j < 5; ++j)
-              send16(to_p + j * 64 * 16, make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2],
-                                                    pk[4 * j + 3]), bar_p);
-            if (h == 0)
-              send4(map_to(smem_u32(&c.alpha[r]), other), alpha, bar_p);
-          }
-          if (v > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // O of the tiles so far, once the last of them is in it
-            wait_on(&c.k_empty[(tiles - 1) % kStages], ((tiles - 1) / kStages) & 1, dead, wait_ns);
-            tc_fence_after();
-#pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
-              float o[32];
-              const uint32_t ta = tl + h * 128 + cc * 32;
-              tmem_ld32(ta, o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= alpha;
-              tmem_st32(ta, o);
+            for (int j = 0; j < 10; ++j) {
+              const uint2 x = in_p[j * 64];
+              pk[2 * j] = x.x;
+              pk[2 * j + 1] = x.y;
             }
+            const float alpha = c.alpha[r];
+            const bool raised = __any_sync(0xffffffffu, alpha != 1.f);
+            if (lane == 0) arrive_remote(bar_free_p);
+            if (v > w.ta && raised) rescale(tiles, alpha);
+            tmem_st20(tS + h * 20, pk);
           }
-          tmem_st20(tS + h * 20, pk);
-        } else {
-          // ---- this block's partial scores go to the CTA that owns it
-          if (tiles > 0 && fine)
-            fine = wait_cluster(&c.free_s, (tiles - 1) & 1, dead, wait_ns);
-          if (fine) {
-#pragma unroll
-            for (int j = 0; j < 10; ++j)
-              send16(to_s + j * 64 * 16,
-                     make_uint4(__float_as_uint(e[4 * j]), __float_as_uint(e[4 * j + 1]),
-                                __float_as_uint(e[4 * j + 2]), __float_as_uint(e[4 * j + 3])),
-                     bar_s);
-          }
-          // ---- and its weights come back
-          fine = fine && wait_cluster(&c.in_p, tiles & 1, dead, wait_ns);
-          uint32_t pk[20];
-#pragma unroll
-          for (int j = 0; j < 5; ++j) {
-            const uint4 x = in_p[j * 64];
-            pk[4 * j] = x.x;
-            pk[4 * j + 1] = x.y;
-            pk[4 * j + 2] = x.z;
-            pk[4 * j + 3] = x.w;
-          }
-          const float alpha = c.alpha[r];
-          if (!fine) c.send_dead[tiles & 1] = 1;
-          // (also: both halves of the row have read their scores, which P overlays)
-          vote4(2, false);
-          if (c.send_dead[tiles & 1]) {
-            ok = false;
-            break;
-          }
-          if (tid == 64 * (int)other) mbar_arrive_expect_tx(&c.in_p, kPBytes);  // the next tile's
-          if (lane == 0) arrive_remote(bar_free_p);
-          if (v > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) {
-            wait_on(&c.k_empty[(tiles - 1) % kStages], ((tiles - 1) / kStages) & 1, dead, wait_ns);
-            tc_fence_after();
-#pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
-              float o[32];
-              const uint32_t ta = tl + h * 128 + cc * 32;
-              tmem_ld32(ta, o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= alpha;
-              tmem_st32(ta, o);
-            }
-          }
-          tmem_st20(tS + h * 20, pk);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive1(&c.p_full[st]);
         }
-        fence_proxy_async_smem();  // cleared keys
-        tc_fence_before();
+        if (!ok) break;
+        const bool some = w.tb > w.ta, whole = w.ta == 0 && w.tb == w.k.n;
+        const bool begins = some && w.ta == 0 && !whole;
+        if (begins) hd.start_tile = w.tile_id;
+        if (!whole && !begins && hd.cont_tile < 0) {
+          hd.cont_tile = w.tile_id;
+          hd.cont_some = some;
+          hd.cont_ends = w.tb == w.k.n;
+        }
+        if (!some && !whole) continue;
+        const long long row = (long long)token * p.Hm + head;
+        if (!some) {  // tokens that see nothing
+          if (own && live) {
+            __nv_bfloat16* dst = p.out + row * kL + q4 * 128;
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0u, 0u, 0u, 0u);
+            if (p.lse && q4 == 0) p.lse[row] = -INFINITY;
+          }
+          continue;
+        }
+        bool fine = wait_on(&c.o_full, segs & 1, dead, wait_ns);
         __syncwarp();
-        if (lane == 0) mbar_arrive1(&c.p_full[st]);
-      }
-      if (!ok) break;
-      const bool some = w.tb > w.ta, whole = w.ta == 0 && w.tb == w.k.n;
-      const bool begins = some && w.ta == 0 && !whole;
-      if (begins) hd.start_tile = w.tile_id;
-      if (!whole && !begins && hd.cont_tile < 0) {
-        hd.cont_tile = w.tile_id;
-        hd.cont_some = some;
-        hd.cont_ends = w.tb == w.k.n;
-      }
-      if (!some && !whole) continue;
-      const long long row = (long long)token * p.Hm + head;
-      if (!some) {  // tokens that see nothing
-        if (own && live) {
-          __nv_bfloat16* dst = p.out + row * kL + h * 256;
-          for (int i = 0; i < 32; ++i)
-            *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0u, 0u, 0u, 0u);
-          if (p.lse && h == 0) p.lse[row] = -INFINITY;
-        }
-        continue;
-      }
-      bool fine = wait_on(&c.o_full, segs & 1, dead, wait_ns);
-      ++segs;
-      tc_fence_after();
-      const int slot = 2 * (int)me + (begins ? 1 : 0);
-      if (own) {
-        c.sum[h][r] = l;
-        vote4(1, false);
-        const float sum = c.sum[0][r] + c.sum[1][r];
-        if (h == 0) {
-          if (whole) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
-            c.inv[64 * rank + r] = inv;
-            send4(map_to(smem_u32(&c.inv[64 * rank + r]), other), inv, bar_l);
-            if (p.lse && live) p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) / kLog2e;
-          } else {
-            p.part_ml[slot * 128 + 64 * rank + r] = make_float2(m, sum);
+        tc_fence_after();
+        const int slot = 2 * (int)me + (begins ? 1 : 0);
+        if (own) {
+          c.sum[q4][r] = l;
+          vote_own(false);
+          if (q4 == 0) {
+            const float sum = (c.sum[0][r] + c.sum[1][r]) + (c.sum[2][r] + c.sum[3][r]);
+            if (whole) {
+              const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
+              c.inv[64 * rank + r] = inv;
+              send4(map_to(smem_u32(&c.inv[64 * rank + r]), other), inv, bar_l);
+              if (p.lse && live)
+                p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) / kLog2e;
+            } else {
+              p.part_ml[slot * 128 + 64 * rank + r] = make_float2(m, sum);
+            }
           }
         }
-      }
-      if (whole) {
-        fine = fine && wait_cluster(&c.in_l, sums & 1, dead, wait_ns);
-        ++sums;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(&c.epi);
-      fine = wait_on(&c.epi, (segs - 1) & 1, dead, wait_ns) && fine;
-      if (vote4(own ? 1 : 2, !fine)) {  // the four warps leave together
-        ok = false;
-        break;
-      }
-      if (whole && own && tid == 64 * (int)rank) mbar_arrive_expect_tx(&c.in_l, 64 * 4);
-      // a thread holds its row's 128 latent columns 256 rank + 128 h ..
-      if (whole) {
-        const float inv = c.inv[64 * g + r];
-        __nv_bfloat16* dst = p.out + row * kL + 256 * rank + 128 * h;
+        if (whole) {
+          fine = fine && wait_on(&c.in_l, sums & 1, dead, wait_ns);
+          ++sums;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&c.epi);
+        fine = wait_on(&c.epi, segs & 1, dead, wait_ns) && fine;
+        ++segs;
+        // the softmax warps leave together
+        if (own ? vote_own(!fine) : !__all_sync(0xffffffffu, fine)) {
+          ok = false;
+          break;
+        }
+        if (whole && own && first && lane == 0) mbar_arrive_expect_tx(&c.in_l, 64 * 4);
+        // a thread holds latent columns 256 rank + o0 .. of its row
+        if (whole) {
+          const float inv = c.inv[64 * g + r];
+          __nv_bfloat16* dst = p.out + row * kL + 256 * rank + o0;
 #pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
-          float o[32];
-          tmem_ld32(tl + h * 128 + cc * 32, o);
-          if (live) {
+          for (int cc = 0; cc < o_n; ++cc) {
+            float o[32];
+            tmem_ld32(tl + o0 + cc * 32, o);
+            if (live) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(dst + cc * 32 + q * 8) = make_uint4(
-                  pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv),
-                  pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                  pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
-                  pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(dst + cc * 32 + q * 8) = make_uint4(
+                    pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv),
+                    pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                    pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
+                    pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+            }
           }
-        }
-      } else {
-        float* dst = p.part_o + ((long long)slot * 128 + 64 * g + r) * kL + 256 * rank + 128 * h;
+        } else {
+          float* dst = p.part_o + ((long long)slot * 128 + 64 * g + r) * kL + 256 * rank + o0;
 #pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
-          float o[32];
-          tmem_ld32(tl + h * 128 + cc * 32, o);
-          if (live) {
+          for (int cc = 0; cc < o_n; ++cc) {
+            float o[32];
+            tmem_ld32(tl + o0 + cc * 32, o);
+            if (live) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<float4*>(dst + cc * 32 + q * 4) =
-                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<float4*>(dst + cc * 32 + q * 4) =
+                    make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
           }
         }
+        // O, c.inv and c.sum are read: this warp's next P, which every next write of
+        // them waits for, says so
+        tc_fence_before();
       }
-      // O, c.inv and c.sum are read: this warp's next P, which every next write of
-      // them waits for, says so
-      tc_fence_before();
+      if (!ok) hd = Header{-1, -1, 0, 0};
+      if (own && first && lane == 0 && rank == 0) p.head[me] = hd;
     }
-    if (!ok) hd = Header{-1, -1, 0, 0};
-    if (tid == 0 && rank == 0) p.head[me] = hd;
   } else if (warp == kTmaWarp) {
     // ================= TMA =================
     int tiles = 0, segs = 0;
