@@ -37,12 +37,14 @@ constexpr int kGroups = kKT / 8;             // of 8 rows: 4 KB, [64-column bloc
 constexpr int kStageBytes = kGroups * 4096;  // 40 KB
 constexpr int kStages = 3;
 constexpr int kQBlock = 128 * 128;           // 128 rows x 64 latent columns
-// Warps 0..15 by TMEM lane quarter (warp mod 4): the quarters of this CTA's row block
-// have four softmax warps each (20 keys a thread); the other block's have two that send
-// its partial scores and two that receive its weights (40 keys a thread).
+// Warps 0..15 by TMEM lane quarter (warp mod 4).  The quarters of this CTA's row block
+// have two teams of softmax warps that take the tiles in turn (a tile's weights take
+// longer than its products; only raising a reference has an order); the other block's
+// have warps that send its partial scores and warps that receive its weights.  Two
+// warps share a quarter's keys: 40 a thread.
 constexpr int kRowWarps = 16;
-constexpr int kOwnWarps = 8, kTakeWarps = 4;
-constexpr int kW = kKT / 4;
+constexpr int kTeamWarps = 4;
+constexpr int kW = kKT / 2;
 constexpr int kWidenWarps = 5;               // E4M3: two groups each
 constexpr size_t kOffQ = 0;
 constexpr size_t kOffK = 4 * (size_t)kQBlock;
@@ -54,16 +56,19 @@ struct Ctl {
   float rs[kStages][kKT];          // E4M3: the keys' row scales (first: read as float4)
   float alpha[64];                 // from the other CTA: its rows' rescale of this tile
   float inv[128];                  // 1 / sum of every row (the other CTA's rows: sent)
-  float mx[4][64], sum[4][64];     // own rows: the four threads of a row
+  float m[64];                     // own rows: the reference (base 2)
+  float mx[2][2][64];              // [team][half of the keys]: a tile's row maxima
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], raw[kStages];
   uint64_t s_full[kStages], p_full[kStages], o_full, drain;
-  uint64_t in_s, in_p, in_l;       // data from the other CTA
-  uint64_t free_s, free_p;         // the other CTA has read what was sent
-  uint64_t epi;                    // the sums of a segment's rows are there
+  // [2]: by the tile's team, so that each waiter sees every phase of its barrier
+  uint64_t in_s[2], in_p, in_l;    // data from the other CTA
+  uint64_t free_s, free_p[2];      // the other CTA has read what was sent
+  uint64_t turn[2];                // the references of this tile stand
+  uint64_t sums, epi;              // the sums of a segment's rows
   Start start;
   uint32_t tmem;
   unsigned groups[kStages];        // groups of the tile that have a page
-  int own_dead[2];
+  int team_dead[2][2];
   int dead;
 };
 constexpr size_t kOffCtl = kOffP + (size_t)(kKT / 4) * 64 * 8;
@@ -128,15 +133,23 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// a barrier of the softmax warps: whether any of their threads says so
-__device__ __forceinline__ bool vote_own(bool v) {
+// a barrier of a team's warps: whether any of their threads says so
+__device__ __forceinline__ bool vote_team(int team, bool v) {
   uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-      " barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"((uint32_t)v), "n"(kOwnWarps * 32)
-      : "memory");
+  if (team == 0)
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+        " barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+        " barrier.cta.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
   return r != 0;
 }
 
@@ -159,34 +172,6 @@ __device__ __forceinline__ void tmem_ld40(uint32_t ta, float (&v)[40]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 40; ++i) v[i] = __uint_as_float(r[i]);
-}
-// 20 columns.
-__device__ __forceinline__ void tmem_ld20(uint32_t ta, float (&v)[20]) {
-  uint32_t r[20];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(ta));
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19])
-               : "r"(ta + 16));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 20; ++i) v[i] = __uint_as_float(r[i]);
-}
-// 10 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_st10(uint32_t ta, const uint32_t (&v)[10]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta),
-               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-               "r"(v[7])
-               : "memory");
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(ta + 8), "r"(v[8]),
-               "r"(v[9])
-               : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 // 20 consecutive 32-bit columns.
 __device__ __forceinline__ void tmem_st20(uint32_t ta, const uint32_t (&v)[20]) {
@@ -261,23 +246,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
       mbar_init(&c.k_empty[i], 1);
       mbar_init(&c.raw[i], 1);
       mbar_init(&c.s_full[i], 1);
-      mbar_init(&c.p_full[i], kOwnWarps + kTakeWarps);
+      mbar_init(&c.p_full[i], 2 * kTeamWarps);
     }
     mbar_init(&c.o_full, 1);
     mbar_init(&c.drain, 1);
-    mbar_init(&c.in_s, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.in_s[i], 1);
+      mbar_init(&c.free_p[i], kTeamWarps);
+      mbar_init(&c.turn[i], kTeamWarps);
+    }
     mbar_init(&c.in_p, 1);
     mbar_init(&c.in_l, 1);
-    mbar_init(&c.free_s, kOwnWarps);
-    mbar_init(&c.free_p, kTakeWarps);
-    mbar_init(&c.epi, kOwnWarps + kTakeWarps);
+    mbar_init(&c.free_s, kTeamWarps);
+    mbar_init(&c.sums, 2 * kTeamWarps);
+    mbar_init(&c.epi, 3 * kTeamWarps);
     fence_mbar_init();
-    c.own_dead[0] = c.own_dead[1] = c.dead = 0;
+    c.team_dead[0][0] = c.team_dead[0][1] = c.team_dead[1][0] = c.team_dead[1][1] = c.dead = 0;
   }
   if (warp == kMmaWarp) {
     tmem_alloc<512>(&c.tmem);
     tc_fence_before();
   }
+  if (tid < 64) c.m[tid] = -INFINITY;
   pdl_wait();  // every input may come from the kernel just before
   pdl_launch_dependents();
   const unsigned long long units = find_share<kKT, true, pair_threads(kCodes)>(
@@ -304,7 +294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
       // ================= send the other block's partial scores =================
       const int h = part;  // keys 40 h ..
       const uint32_t to_s = map_to(smem_u32(sb + kOffS) + (h * 10 * 64 + r) * 16, other);
-      const uint32_t bar_s = map_to(smem_u32(&c.in_s), other);
+      const uint32_t bar_s[2] = {map_to(smem_u32(&c.in_s[0]), other),
+                                 map_to(smem_u32(&c.in_s[1]), other)};
       int tiles = 0;
       bool ok = true;
       while (ok && w.next()) {
@@ -324,23 +315,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             send16(to_s + j * 64 * 16,
                    make_uint4(__float_as_uint(e[4 * j]), __float_as_uint(e[4 * j + 1]),
                               __float_as_uint(e[4 * j + 2]), __float_as_uint(e[4 * j + 3])),
-                   bar_s);
+                   bar_s[tiles & 1]);
         }
       }
     } else {
       // ================= softmax of the own block; weights of the other =================
-      const int q4 = part;             // own: keys 20 q4 ..
-      const int h = part & 1;          // other: keys 40 h ..
-      const int o0 = own ? q4 * 64 : h * 128, o_n = own ? 2 : 4;  // O columns, in blocks of 32
-      const bool first = own ? (warp == 2 * (int)rank) : (warp == 8 + 2 * (int)other);
-      const uint32_t to_p = map_to(smem_u32(sb + kOffP) + (q4 * 5 * 64 + r) * 8, other);
+      const int team = part >> 1, h = part & 1;  // keys 40 h ..
+      // O columns, in blocks of 32: of a segment's end, and of a rescale
+      const int o0 = own ? part * 64 : h * 128, o_n = own ? 2 : 4;
+      const bool first = own ? (warp & 3) == 2 * (int)rank && h == 0
+                             : (warp & 3) == 2 * (int)other && h == 0;
+      const uint32_t to_p = map_to(smem_u32(sb + kOffP) + (h * 10 * 64 + r) * 8, other);
       const uint32_t bar_p = map_to(smem_u32(&c.in_p), other),
                      bar_l = map_to(smem_u32(&c.in_l), other),
                      bar_free_s = map_to(smem_u32(&c.free_s), other),
-                     bar_free_p = map_to(smem_u32(&c.free_p), other);
-      const uint4* in_s = reinterpret_cast<const uint4*>(sb + kOffS) + q4 * 5 * 64 + r;
+                     bar_free_p[2] = {map_to(smem_u32(&c.free_p[0]), other),
+                                      map_to(smem_u32(&c.free_p[1]), other)};
+      const uint4* in_s = reinterpret_cast<const uint4*>(sb + kOffS) + h * 10 * 64 + r;
       const uint2* in_p = reinterpret_cast<const uint2*>(sb + kOffP) + h * 10 * 64 + r;
-      const int otid = ((warp & 1) + 2 * part) * 32 + lane;  // own: 0..255
+      const int ttid = ((warp & 1) + 2 * h) * 32 + lane;  // thread of the team
       Header hd = {-1, any ? -1 : -2, 0, 0};
       int tiles = 0, segs = 0, sums = 0;
       bool ok = true;
@@ -348,8 +341,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
       // the next phase is sent before every reader of this one has said so.)
       if (any && first && lane == 0) {
         if (own) {
-          mbar_arrive_expect_tx(&c.in_s, kSBytes);
-          mbar_arrive_expect_tx(&c.in_l, 64 * 4);
+          mbar_arrive_expect_tx(&c.in_s[team], kSBytes);
+          if (team == 0) mbar_arrive_expect_tx(&c.in_l, 64 * 4);
         } else {
           mbar_arrive_expect_tx(&c.in_p, kPBytes);
         }
@@ -360,12 +353,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
         __syncwarp();
         tc_fence_after();
 #pragma unroll 1
-        for (int cc = 0; cc < o_n; ++cc) {
+        for (int cc = 0; cc < 4; ++cc) {
           float o[32];
-          tmem_ld32(tl + o0 + cc * 32, o);
+          tmem_ld32(tl + h * 128 + cc * 32, o);
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] *= alpha;
-          tmem_st32(tl + o0 + cc * 32, o);
+          tmem_st32(tl + h * 128 + cc * 32, o);
         }
       };
       while (ok && w.next()) {
@@ -379,32 +372,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
         const int pos_b = w.two ? (w.pos0 + 1 < 0 ? -1 : w.pos0 + 1) : pos_a;
         const Sight sa = sight_of(pos_a, p), sbt = sight_of(pos_b, p);
         const Sight mine = g == 0 ? sa : sbt;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f;  // l: this thread's sum, relative to m
         for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+          if (own && (tiles & 1) != team) continue;
           const int st = tiles % kStages, ph = (tiles / kStages) & 1;
           const uint32_t tS = tl + 256 + (uint32_t)(st * kKT);
           if (own) {
+            const int turn = (tiles >> 1) & 1;
+            // is every key of the tile seen by both blocks (once it has its pages)?
+            const int t0 = w.k.at(v, 0), t1 = w.k.at(v, kKT - 1);
+            const bool span = t1 - t0 == kKT - 1 && t0 >= max(sa.lo, sbt.lo) &&
+                              t1 <= min(sa.pos, sbt.pos);
             bool fine = wait_on(&c.s_full[st], ph, dead, wait_ns);
             __syncwarp();
             tc_fence_after();
             float e[kW];
-            tmem_ld20(tS + q4 * kW, e);
-            // is every key of the tile seen by both blocks?
-            const int t0 = w.k.at(v, 0), t1 = w.k.at(v, kKT - 1);
-            const bool plain = c.groups[st] == (1u << kGroups) - 1 && t1 - t0 == kKT - 1 &&
-                               t0 >= max(sa.lo, sbt.lo) && t1 <= min(sa.pos, sbt.pos);
-            if (!plain && (otid >> 1) < kKT) {
+            tmem_ld40(tS + h * kW, e);
+            const bool plain = span && c.groups[st] == (1u << kGroups) - 1;
+            if (!plain && ttid < kKT) {
               // clear what neither sees, and what one does not see if it is not finite
-              const int key = otid >> 1;
+              const int key = ttid;
               const int t = w.k.at(v, key);
               const bool paged = (c.groups[st] >> (key >> 3)) & 1u;
               const bool ina = paged && sa(t), inb = paged && sbt(t);
               if (!(ina && inb)) {
-                unsigned char* kr = sb + kOffK + st * kStageBytes + (key >> 3) * 4096 +
-                                    (otid & 1) * 2048 + (key & 7) * 128;
+                unsigned char* kr =
+                    sb + kOffK + st * kStageBytes + (key >> 3) * 4096 + (key & 7) * 128;
                 bool odd = !(ina || inb);
                 if (!odd) {
-                  for (int i = 0; i < 16; ++i) {
+                  for (int i = 0; i < 32; ++i) {
                     const uint4 x = *reinterpret_cast<const uint4*>(
                         kr + (i >> 3) * 1024 + (((i & 7) ^ (key & 7)) << 4));
                     const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
@@ -413,25 +409,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
                   }
                 }
                 if (odd)
-                  for (int i = 0; i < 16; ++i)
+                  for (int i = 0; i < 32; ++i)
                     *reinterpret_cast<uint4*>(kr + (i >> 3) * 1024 +
                                               (((i & 7) ^ (key & 7)) << 4)) =
                         make_uint4(0u, 0u, 0u, 0u);
               }
               fence_proxy_async_smem();
             }
-            // the keys of this warp that the own block sees, 20 bits
-            uint32_t see = 0xfffffu;
+            // the keys of this warp that the own block sees, 40 bits
+            uint32_t see_lo = 0xffffffffu, see_hi = 0xffu;
             if (!plain) {
-              const int key = q4 * kW + min(lane, kW - 1);
-              see = __ballot_sync(0xffffffffu, mine(w.k.at(v, key)) &&
-                                                   ((c.groups[st] >> (key >> 3)) & 1u));
+              const int ka = h * kW + lane, kb = h * kW + 32 + (lane & 7);
+              see_lo = __ballot_sync(0xffffffffu, mine(w.k.at(v, ka)) &&
+                                                      ((c.groups[st] >> (ka >> 3)) & 1u));
+              see_hi = __ballot_sync(0xffffffffu, lane < 8 && mine(w.k.at(v, kb)) &&
+                                                      ((c.groups[st] >> (kb >> 3)) & 1u));
             }
-            fine = fine && wait_on(&c.in_s, tiles & 1, dead, wait_ns);
+            auto seen = [&](int i) { return ((i < 32 ? see_lo >> i : see_hi >> (i - 32)) & 1u) != 0; };
+            fine = fine && wait_on(&c.in_s[team], turn, dead, wait_ns);
             __syncwarp();
-            if (first && lane == 0) mbar_arrive_expect_tx(&c.in_s, kSBytes);  // the next tile's
+            if (first && lane == 0) mbar_arrive_expect_tx(&c.in_s[team], kSBytes);  // the next one
 #pragma unroll
-            for (int j = 0; j < 5; ++j) {
+            for (int j = 0; j < 10; ++j) {
               const uint4 x = in_s[j * 64];
               e[4 * j] += __uint_as_float(x.x);
               e[4 * j + 1] += __uint_as_float(x.y);
@@ -440,11 +439,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             }
             __syncwarp();
             if (lane == 0) arrive_remote(bar_free_s);
+            // the references, once the last tile's team has settled them
+            if (tiles > 0 && fine)
+              fine = wait_on(&c.turn[team ^ 1], ((tiles - 1) >> 1) & 1, dead, wait_ns);
+            __syncwarp();
+            const float m_now = c.m[r];
+            if (m_now != m) {
+              l *= ex2_fast(m - m_now);  // (0 before the first key: m = -inf)
+              m = m_now;
+            }
             const float nm = m == -INFINITY ? 0.f : -m;
             if constexpr (kCodes) {
 #pragma unroll
-              for (int q = 0; q < 5; ++q) {
-                const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + q4 * kW)[q];
+              for (int q = 0; q < 10; ++q) {
+                const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + h * kW)[q];
                 e[4 * q] = fmaf(e[4 * q], p.zscale * rs.x, nm);
                 e[4 * q + 1] = fmaf(e[4 * q + 1], p.zscale * rs.y, nm);
                 e[4 * q + 2] = fmaf(e[4 * q + 2], p.zscale * rs.z, nm);
@@ -457,24 +465,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             if (!plain) {
 #pragma unroll
               for (int i = 0; i < kW; ++i)
-                if (!((see >> i) & 1u)) e[i] = -INFINITY;
+                if (!seen(i)) e[i] = -INFINITY;
             }
             float t4[4] = {e[0], e[1], e[2], e[3]};
 #pragma unroll
             for (int i = 4; i < kW; ++i) t4[i & 3] = fmaxf(t4[i & 3], e[i]);
             const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-            if (!fine) c.own_dead[tiles & 1] = 1;
-            c.mx[q4][r] = top;  // relative to the reference
-            // (also: every thread of a row has read its scores, which P overlays)
-            const bool full = vote_own(live && (m == -INFINITY || top > kRaiseAt));
-            if (c.own_dead[tiles & 1]) {
+            if (!fine) c.team_dead[team][turn] = 1;
+            c.mx[team][h][r] = top;  // relative to the reference
+            // (also: both threads of a row have read its scores, which P overlays)
+            const bool full = vote_team(team, live && (m == -INFINITY || top > kRaiseAt));
+            if (c.team_dead[team][turn]) {
               ok = false;
               break;
             }
             float alpha = 1.f;
             if (full) {
-              const float both = fmaxf(fmaxf(c.mx[0][r], c.mx[1][r]),
-                                       fmaxf(c.mx[2][r], c.mx[3][r]));  // of the row, relative
+              const float both = fmaxf(c.mx[team][0][r], c.mx[team][1][r]);  // relative
               float step = 0.f;
               if (m == -INFINITY) {
                 if (both > -INFINITY) {  // the first key that this row sees
@@ -487,10 +494,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
                 alpha = ex2_fast(-both);
                 l *= alpha;
               }
+              if (h == 0) c.m[r] = m;
+              __syncwarp();
               // (an infinite maximum: its key's weight is NaN, as in the formula)
 #pragma unroll
               for (int i = 0; i < kW; ++i) e[i] += step;
             }
+            if (lane == 0) mbar_arrive1(&c.turn[team]);
 #pragma unroll
             for (int i = 0; i < kW; ++i) e[i] = ex2_fast(e[i]);
             float s4[4] = {e[0], e[1], e[2], e[3]};
@@ -502,11 +512,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
             // P is rounded to bf16 for the tensor cores; the sums keep the unrounded
             // weights.  An E4M3 row's scale goes to its weights.
-            uint32_t pk[10];
+            uint32_t pk[20];
             if constexpr (kCodes) {
 #pragma unroll
-              for (int q = 0; q < 5; ++q) {
-                const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + q4 * kW)[q];
+              for (int q = 0; q < 10; ++q) {
+                const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + h * kW)[q];
                 e[4 * q] *= rs.x;
                 e[4 * q + 1] *= rs.y;
                 e[4 * q + 2] *= rs.z;
@@ -515,23 +525,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
               if (!plain) {  // (a hidden key's scale may be anything)
 #pragma unroll
                 for (int i = 0; i < kW; ++i)
-                  if (!((see >> i) & 1u)) e[i] = 0.f;
+                  if (!seen(i)) e[i] = 0.f;
               }
             }
 #pragma unroll
-            for (int i = 0; i < 10; ++i) pk[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+            for (int i = 0; i < 20; ++i) pk[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
             // the other CTA has taken the last tile's weights
-            if (tiles > 0 && !wait_on(&c.free_p, (tiles - 1) & 1, dead, wait_ns)) {
-              c.own_dead[(tiles + 1) & 1] = 1;
+            if (tiles > 0 &&
+                !wait_on(&c.free_p[team ^ 1], ((tiles - 1) >> 1) & 1, dead, wait_ns)) {
+              c.team_dead[team][turn ^ 1] = 1;
             } else {
 #pragma unroll
-              for (int j = 0; j < 5; ++j)
+              for (int j = 0; j < 10; ++j)
                 send8(to_p + j * 64 * 8, pk[2 * j], pk[2 * j + 1], bar_p);
-              if (q4 == 0) send4(map_to(smem_u32(&c.alpha[r]), other), alpha, bar_p);
+              if (h == 0) send4(map_to(smem_u32(&c.alpha[r]), other), alpha, bar_p);
             }
             __syncwarp();
             if (v > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) rescale(tiles, alpha);
-            tmem_st10(tS + q4 * 10, pk);
+            tmem_st20(tS + h * 20, pk);
           } else {
             // ---- the other block's weights (its scores here were read before the
             // other CTA could make them)
@@ -547,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             }
             const float alpha = c.alpha[r];
             const bool raised = __any_sync(0xffffffffu, alpha != 1.f);
-            if (lane == 0) arrive_remote(bar_free_p);
+            if (lane == 0) arrive_remote(bar_free_p[tiles & 1]);
             if (v > w.ta && raised) rescale(tiles, alpha);
             tmem_st20(tS + h * 20, pk);
           }
@@ -568,10 +579,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
         const long long row = (long long)token * p.Hm + head;
         if (!some) {  // tokens that see nothing
           if (own && live) {
-            __nv_bfloat16* dst = p.out + row * kL + q4 * 128;
+            __nv_bfloat16* dst = p.out + row * kL + part * 128;
             for (int i = 0; i < 16; ++i)
               *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0u, 0u, 0u, 0u);
-            if (p.lse && q4 == 0) p.lse[row] = -INFINITY;
+            if (p.lse && part == 0) p.lse[row] = -INFINITY;
           }
           continue;
         }
@@ -580,18 +591,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
         tc_fence_after();
         const int slot = 2 * (int)me + (begins ? 1 : 0);
         if (own) {
-          c.sum[q4][r] = l;
-          vote_own(false);
-          if (q4 == 0) {
-            const float sum = (c.sum[0][r] + c.sum[1][r]) + (c.sum[2][r] + c.sum[3][r]);
+          // the four threads of a row: relative to the last reference
+          const float m_end = c.m[r];
+          c.mx[team][h][r] = m == -INFINITY ? l : l * ex2_fast(m - m_end);  // (no key: 0 or NaN)
+          __syncwarp();
+          if (lane == 0) mbar_arrive1(&c.sums);
+          fine = fine && wait_on(&c.sums, segs & 1, dead, wait_ns);
+          __syncwarp();
+          if (part == 0) {
+            const float sum = (c.mx[0][0][r] + c.mx[0][1][r]) + (c.mx[1][0][r] + c.mx[1][1][r]);
+            c.m[r] = -INFINITY;  // (every thread of the row has read it)
             if (whole) {
               const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
               c.inv[64 * rank + r] = inv;
               send4(map_to(smem_u32(&c.inv[64 * rank + r]), other), inv, bar_l);
               if (p.lse && live)
-                p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) / kLog2e;
+                p.lse[row] = sum == 0.f ? -INFINITY : (m_end + log2f(sum)) / kLog2e;
             } else {
-              p.part_ml[slot * 128 + 64 * rank + r] = make_float2(m, sum);
+              p.part_ml[slot * 128 + 64 * rank + r] = make_float2(m_end, sum);
             }
           }
         }
@@ -603,12 +620,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
         if (lane == 0) mbar_arrive1(&c.epi);
         fine = wait_on(&c.epi, segs & 1, dead, wait_ns) && fine;
         ++segs;
-        // the softmax warps leave together
-        if (own ? vote_own(!fine) : !__all_sync(0xffffffffu, fine)) {
+        // a team's warps leave together
+        if (own ? vote_team(team, !fine) : !__all_sync(0xffffffffu, fine)) {
           ok = false;
           break;
         }
-        if (whole && own && first && lane == 0) mbar_arrive_expect_tx(&c.in_l, 64 * 4);
+        if (whole && own && first && team == 0 && lane == 0)
+          mbar_arrive_expect_tx(&c.in_l, 64 * 4);
         // a thread holds latent columns 256 rank + o0 .. of its row
         if (whole) {
           const float inv = c.inv[64 * g + r];
@@ -641,12 +659,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             }
           }
         }
-        // O, c.inv and c.sum are read: this warp's next P, which every next write of
+        // O and c.inv are read: this warp's next P, which every next write of
         // them waits for, says so
         tc_fence_before();
       }
       if (!ok) hd = Header{-1, -1, 0, 0};
-      if (own && first && lane == 0 && rank == 0) p.head[me] = hd;
+      if (own && first && team == 0 && lane == 0 && rank == 0) p.head[me] = hd;
     }
   } else if (warp == kTmaWarp) {
     // ================= TMA =================
