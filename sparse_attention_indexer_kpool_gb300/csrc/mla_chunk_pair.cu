@@ -32,24 +32,24 @@ namespace {
 
 using namespace chunk;
 
-constexpr int kKT = 80;                      // keys of a tile
+constexpr int kKT = 64;                      // keys of a tile
 constexpr int kGroups = kKT / 8;             // of 8 rows: 4 KB, [64-column block][row][128 B]
-constexpr int kStageBytes = kGroups * 4096;  // 40 KB
-constexpr int kStages = 3;
+constexpr int kStageBytes = kGroups * 4096;  // 32 KB
+constexpr int kStages = 4;
 constexpr int kQBlock = 128 * 128;           // 128 rows x 64 latent columns
 // Warps 0..15 by TMEM lane quarter (warp mod 4).  The quarters of this CTA's row block
 // have two teams of softmax warps that take the tiles in turn (a tile's weights take
 // longer than its products; only raising a reference has an order); the other block's
 // have warps that send its partial scores and warps that receive its weights.  Two
-// warps share a quarter's keys: 40 a thread.
+// warps share a quarter's keys: 32 a thread.
 constexpr int kRowWarps = 16;
 constexpr int kTeamWarps = 4;
 constexpr int kW = kKT / 2;
-constexpr int kWidenWarps = 5;               // E4M3: two groups each
+constexpr int kWidenWarps = 4;               // E4M3: two groups each
 constexpr size_t kOffQ = 0;
 constexpr size_t kOffK = 4 * (size_t)kQBlock;
-constexpr size_t kOffS = kOffK + (size_t)kStages * kStageBytes;   // [20][64 rows] x 16 B
-constexpr size_t kOffP = kOffS + (size_t)(kKT / 4) * 64 * 16;     // [20][64 rows] x 8 B
+constexpr size_t kOffS = kOffK + (size_t)kStages * kStageBytes;   // [16][64 rows] x 16 B
+constexpr size_t kOffP = kOffS + (size_t)(kKT / 4) * 64 * 16;     // [16][64 rows] x 8 B
 constexpr uint32_t kSBytes = kKT * 64 * 4, kPBytes = kKT * 64 * 2 + 64 * 4;
 
 struct Ctl {
@@ -77,7 +77,7 @@ static_assert(kSmem <= 227 * 1024, "shared memory budget");
 static_assert(256 + kStages * kKT <= 512, "TMEM columns");
 
 __host__ __device__ constexpr int pair_threads(bool codes) {
-  return 32 * (kRowWarps + 2 + (codes ? kWidenWarps : 0));
+  return 32 * (kRowWarps + 4 + (codes ? kWidenWarps : 0));
 }
 
 // ---- cluster pieces ------------------------------------------------------------
@@ -153,37 +153,14 @@ __device__ __forceinline__ bool vote_team(int team, bool v) {
   return r != 0;
 }
 
-// 40 consecutive fp32 columns of the warp's 32 TMEM lanes.
-__device__ __forceinline__ void tmem_ld40(uint32_t ta, float (&v)[40]) {
-  uint32_t r[40];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(ta));
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]),
-                 "=r"(r[38]), "=r"(r[39])
-               : "r"(ta + 32));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 40; ++i) v[i] = __uint_as_float(r[i]);
-}
-// 20 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_st20(uint32_t ta, const uint32_t (&v)[20]) {
+// 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_st16(uint32_t ta, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
       "%14,%15,%16};" ::"r"(ta),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ta + 16),
-               "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19])
-               : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 // O += P V with P (the A operand) in TMEM; one elected lane of a converged warp.
@@ -229,12 +206,15 @@ template <bool kCodes>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes), 1)
     mla_chunk_pair_kernel(const __grid_constant__ CUtensorMap q_map,
                           const __grid_constant__ CUtensorMap kv_map, const Params p) {
-  constexpr int kTmaWarp = kRowWarps, kMmaWarp = kTmaWarp + 1, kWiden0 = kMmaWarp + 1;
+  constexpr int kWiden0 = kRowWarps + 4;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl& c = *reinterpret_cast<Ctl*>(sb + kOffCtl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cta_rank(), other = rank ^ 1u;
+  // the softmax warps sit on two of the SM's four schedulers (their lane quarters):
+  // the TMA and the MMA warp go to the other two
+  const int kTmaWarp = kRowWarps + (rank == 0 ? 2 : 0), kMmaWarp = kTmaWarp + 1;
   const int hb = (p.Hm + 63) / 64;
   const unsigned me = blockIdx.x >> 1, workers = gridDim.x >> 1;
 
@@ -292,8 +272,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
     };
     if (!own && part < 2) {
       // ================= send the other block's partial scores =================
-      const int h = part;  // keys 40 h ..
-      const uint32_t to_s = map_to(smem_u32(sb + kOffS) + (h * 10 * 64 + r) * 16, other);
+      const int h = part;  // keys 32 h ..
+      const uint32_t to_s = map_to(smem_u32(sb + kOffS) + (h * (kW / 4) * 64 + r) * 16, other);
       const uint32_t bar_s[2] = {map_to(smem_u32(&c.in_s[0]), other),
                                  map_to(smem_u32(&c.in_s[1]), other)};
       int tiles = 0;
@@ -304,14 +284,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
           ok = wait_all(&c.s_full[st], (tiles / kStages) & 1);
           if (!ok) break;
           tc_fence_after();
-          float e[40];
-          tmem_ld40(tl + 256 + (uint32_t)(st * kKT + h * 40), e);
+          float e[kW];
+          tmem_ld32(tl + 256 + (uint32_t)(st * kKT + h * kW), e);
           tc_fence_before();
           // the other CTA has read the last tile's
           ok = tiles == 0 || wait_all(&c.free_s, (tiles - 1) & 1);
           if (!ok) break;
 #pragma unroll
-          for (int j = 0; j < 10; ++j)
+          for (int j = 0; j < kW / 4; ++j)
             send16(to_s + j * 64 * 16,
                    make_uint4(__float_as_uint(e[4 * j]), __float_as_uint(e[4 * j + 1]),
                               __float_as_uint(e[4 * j + 2]), __float_as_uint(e[4 * j + 3])),
@@ -320,19 +300,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
       }
     } else {
       // ================= softmax of the own block; weights of the other =================
-      const int team = part >> 1, h = part & 1;  // keys 40 h ..
+      const int team = part >> 1, h = part & 1;  // keys 32 h ..
       // O columns, in blocks of 32: of a segment's end, and of a rescale
       const int o0 = own ? part * 64 : h * 128, o_n = own ? 2 : 4;
       const bool first = own ? (warp & 3) == 2 * (int)rank && h == 0
                              : (warp & 3) == 2 * (int)other && h == 0;
-      const uint32_t to_p = map_to(smem_u32(sb + kOffP) + (h * 10 * 64 + r) * 8, other);
+      const uint32_t to_p = map_to(smem_u32(sb + kOffP) + (h * (kW / 4) * 64 + r) * 8, other);
       const uint32_t bar_p = map_to(smem_u32(&c.in_p), other),
                      bar_l = map_to(smem_u32(&c.in_l), other),
                      bar_free_s = map_to(smem_u32(&c.free_s), other),
                      bar_free_p[2] = {map_to(smem_u32(&c.free_p[0]), other),
                                       map_to(smem_u32(&c.free_p[1]), other)};
-      const uint4* in_s = reinterpret_cast<const uint4*>(sb + kOffS) + h * 10 * 64 + r;
-      const uint2* in_p = reinterpret_cast<const uint2*>(sb + kOffP) + h * 10 * 64 + r;
+      const uint4* in_s = reinterpret_cast<const uint4*>(sb + kOffS) + h * (kW / 4) * 64 + r;
+      const uint2* in_p = reinterpret_cast<const uint2*>(sb + kOffP) + h * (kW / 4) * 64 + r;
       const int ttid = ((warp & 1) + 2 * h) * 32 + lane;  // thread of the team
       Header hd = {-1, any ? -1 : -2, 0, 0};
       int tiles = 0, segs = 0, sums = 0;
@@ -387,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             __syncwarp();
             tc_fence_after();
             float e[kW];
-            tmem_ld40(tS + h * kW, e);
+            tmem_ld32(tS + h * kW, e);
             const bool plain = span && c.groups[st] == (1u << kGroups) - 1;
             if (!plain && ttid < kKT) {
               // clear what neither sees, and what one does not see if it is not finite
@@ -416,26 +396,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
               }
               fence_proxy_async_smem();
             }
-            // the keys of this warp that the own block sees, 40 bits
-            uint32_t see_lo = 0xffffffffu, see_hi = 0xffu;
+            uint32_t see = 0xffffffffu;  // the keys of this warp that the own block sees
             if (!plain) {
-              const int ka = h * kW + lane, kb = h * kW + 32 + (lane & 7);
-              see_lo = __ballot_sync(0xffffffffu, mine(w.k.at(v, ka)) &&
-                                                      ((c.groups[st] >> (ka >> 3)) & 1u));
-              see_hi = __ballot_sync(0xffffffffu, lane < 8 && mine(w.k.at(v, kb)) &&
-                                                      ((c.groups[st] >> (kb >> 3)) & 1u));
+              const int key = h * kW + lane;
+              see = __ballot_sync(0xffffffffu, mine(w.k.at(v, key)) &&
+                                                   ((c.groups[st] >> (key >> 3)) & 1u));
             }
-            auto seen = [&](int i) { return ((i < 32 ? see_lo >> i : see_hi >> (i - 32)) & 1u) != 0; };
             fine = fine && wait_on(&c.in_s[team], turn, dead, wait_ns);
             __syncwarp();
             if (first && lane == 0) mbar_arrive_expect_tx(&c.in_s[team], kSBytes);  // the next one
 #pragma unroll
-            for (int j = 0; j < 10; ++j) {
+            for (int j = 0; j < kW / 4; ++j) {
               const uint4 x = in_s[j * 64];
-              e[4 * j] += __uint_as_float(x.x);
-              e[4 * j + 1] += __uint_as_float(x.y);
-              e[4 * j + 2] += __uint_as_float(x.z);
-              e[4 * j + 3] += __uint_as_float(x.w);
+              add2(e[4 * j], e[4 * j + 1], __uint_as_float(x.x), __uint_as_float(x.y));
+              add2(e[4 * j + 2], e[4 * j + 3], __uint_as_float(x.z), __uint_as_float(x.w));
             }
             __syncwarp();
             if (lane == 0) arrive_remote(bar_free_s);
@@ -451,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             const float nm = m == -INFINITY ? 0.f : -m;
             if constexpr (kCodes) {
 #pragma unroll
-              for (int q = 0; q < 10; ++q) {
+              for (int q = 0; q < kW / 4; ++q) {
                 const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + h * kW)[q];
                 e[4 * q] = fmaf(e[4 * q], p.zscale * rs.x, nm);
                 e[4 * q + 1] = fmaf(e[4 * q + 1], p.zscale * rs.y, nm);
@@ -465,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             if (!plain) {
 #pragma unroll
               for (int i = 0; i < kW; ++i)
-                if (!seen(i)) e[i] = -INFINITY;
+                if (!((see >> i) & 1u)) e[i] = -INFINITY;
             }
             float t4[4] = {e[0], e[1], e[2], e[3]};
 #pragma unroll
@@ -512,10 +486,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
             // P is rounded to bf16 for the tensor cores; the sums keep the unrounded
             // weights.  An E4M3 row's scale goes to its weights.
-            uint32_t pk[20];
+            uint32_t pk[kW / 2];
             if constexpr (kCodes) {
 #pragma unroll
-              for (int q = 0; q < 10; ++q) {
+              for (int q = 0; q < kW / 4; ++q) {
                 const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + h * kW)[q];
                 e[4 * q] *= rs.x;
                 e[4 * q + 1] *= rs.y;
@@ -525,33 +499,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
               if (!plain) {  // (a hidden key's scale may be anything)
 #pragma unroll
                 for (int i = 0; i < kW; ++i)
-                  if (!seen(i)) e[i] = 0.f;
+                  if (!((see >> i) & 1u)) e[i] = 0.f;
               }
             }
 #pragma unroll
-            for (int i = 0; i < 20; ++i) pk[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+            for (int i = 0; i < kW / 2; ++i) pk[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
             // the other CTA has taken the last tile's weights
             if (tiles > 0 &&
                 !wait_on(&c.free_p[team ^ 1], ((tiles - 1) >> 1) & 1, dead, wait_ns)) {
               c.team_dead[team][turn ^ 1] = 1;
             } else {
 #pragma unroll
-              for (int j = 0; j < 10; ++j)
+              for (int j = 0; j < kW / 4; ++j)
                 send8(to_p + j * 64 * 8, pk[2 * j], pk[2 * j + 1], bar_p);
               if (h == 0) send4(map_to(smem_u32(&c.alpha[r]), other), alpha, bar_p);
             }
             __syncwarp();
             if (v > w.ta && __any_sync(0xffffffffu, alpha != 1.f)) rescale(tiles, alpha);
-            tmem_st20(tS + h * 20, pk);
+            tmem_st16(tS + h * (kW / 2), pk);
           } else {
             // ---- the other block's weights (its scores here were read before the
             // other CTA could make them)
             ok = wait_all(&c.in_p, tiles & 1);
             if (!ok) break;
             if (first && lane == 0) mbar_arrive_expect_tx(&c.in_p, kPBytes);  // the next tile's
-            uint32_t pk[20];
+            uint32_t pk[kW / 2];
 #pragma unroll
-            for (int j = 0; j < 10; ++j) {
+            for (int j = 0; j < kW / 4; ++j) {
               const uint2 x = in_p[j * 64];
               pk[2 * j] = x.x;
               pk[2 * j + 1] = x.y;
@@ -560,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             const bool raised = __any_sync(0xffffffffu, alpha != 1.f);
             if (lane == 0) arrive_remote(bar_free_p[tiles & 1]);
             if (v > w.ta && raised) rescale(tiles, alpha);
-            tmem_st20(tS + h * 20, pk);
+            tmem_st16(tS + h * (kW / 2), pk);
           }
           tc_fence_before();
           __syncwarp();
@@ -812,11 +786,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
         mbar_wait_bounded(&c.drain, 0);
       }
     }
-  } else if constexpr (kCodes) {
+  } else if (kCodes && warp >= kWiden0) {
     // ================= E4M3 rows, widened in place =================
     // A group's codes (8 rows of 256, two swizzled blocks) land in the first half of
     // its 4 KB; one warp takes them into registers and writes the bf16 rows.
-    const int wi = warp - kWiden0;  // groups wi, wi + 5
+    const int wi = warp - kWiden0;  // groups wi, wi + 4
     int tiles = 0;
     bool ok = issue;
     auto scale_of = [&](const PairKeys& k, int b, int v) -> float {
