@@ -45,6 +45,21 @@ cudaError_t launch_kernel(const cudaLaunchConfig_t* cfg, void (*kernel)(KArgs...
   return e;
 }
 
+// Raise a kernel's dynamic shared-memory limit, once per device: `done` is the
+// caller's, one per kernel and size (bit d: device d has it).
+template <typename K>
+bool allow_smem(K kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
+      cudaSuccess)
+    return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
 // ---------------------------------------------------------------- status
 __device__ __forceinline__ void flag(int32_t* status, int bit) {
   if (status) atomicOr(status, bit);

@@ -9,12 +9,11 @@
 //
 // This file: the dispatch, and the generic kernel for any geometry and type
 // (fp32 activations, latent widths other than 512, fp32 pages).  One CTA of four
-// warps = one token and four heads; tiles of 64 visible positions: every warp
-// contracts whole rows for its share of them (lanes along the latent axis, the
-// row read once for the four heads), then every thread accumulates its latent
-// columns over the tile's rows.  Running maximum, sum and outputs are fp32.  It is
-// bound by the latency of its row reads (each row is read twice through L1);
-// the tcgen05 kernel takes the serving geometry.
+// warps = one token and four heads; a tile of visible rows is brought into shared
+// memory as fp32 once, thread pairs (key, head) take the scores from it, threads
+// (column, head) the output.  Running maximum, sum and outputs are fp32.  It is bound
+// by the latency of a tile's row reads and barriers (the 200-token fp32 prompt: see
+// the measurements); the tcgen05 kernels take the serving geometry.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -26,6 +25,12 @@ namespace {
 
 constexpr int kChunkThreads = 128, kChunkHeads = 4, kChunkTile = 64;
 constexpr int kChunkCols = 1024 / kChunkThreads;  // latent columns of a thread at most
+constexpr int kChunkFloats = 16384;               // of a tile's rows
+// keys of a tile: the rows (one float of padding each: columns of 32 rows in different
+// banks) fit kChunkFloats
+__host__ __device__ constexpr int chunk_tile(int L) {
+  return kChunkFloats / (L + 1) < kChunkTile ? kChunkFloats / (L + 1) : kChunkTile;
+}
 
 __device__ __forceinline__ float page_value(const PagedKv& pk, long long row, int d, int L) {
   const long long o = row * L + d;
@@ -39,10 +44,12 @@ __device__ __forceinline__ float page_value(const PagedKv& pk, long long row, in
 
 template <typename T>
 __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs a) {
-  __shared__ float sq[kChunkHeads][1024];
+  extern __shared__ float rows[];  // [tile][L + 1], then the queries [kChunkHeads][L]
   __shared__ float sz[kChunkHeads][kChunkTile];
   __shared__ int srow[kChunkTile];
   __shared__ float s_m[kChunkHeads], s_l[kChunkHeads], s_alpha[kChunkHeads];
+  const int L = a.L, Lp = a.L + 1, kt = chunk_tile(a.L);
+  float* sq = rows + kt * Lp;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -72,7 +79,8 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
 
   const long long qh = (long long)t * a.Hm + h0;
   const T* q = static_cast<const T*>(a.q_lat) + qh * a.L;
-  for (int i = tid; i < nh * a.L; i += kChunkThreads) sq[i / a.L][i % a.L] = Act<T>::to_f(q[i]);
+  for (int i = tid; i < kChunkHeads * L; i += kChunkThreads)
+    sq[i] = i < nh * L ? Act<T>::to_f(q[i]) : 0.f;
   if (tid < kChunkHeads) {
     s_m[tid] = -INFINITY;
     s_l[tid] = 0.f;
@@ -83,8 +91,8 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
 #pragma unroll
     for (int c = 0; c < kChunkCols; ++c) acc[h][c] = 0.f;
 
-  for (int v0 = 0; v0 < nv; v0 += kChunkTile) {
-    const int n = min(kChunkTile, nv - v0);
+  for (int v0 = 0; v0 < nv; v0 += kt) {
+    const int n = min(kt, nv - v0);
     __syncthreads();
     if (tid < n) {
       const int v = v0 + tid, p = v < s0 ? v : lo + (v - s0);
@@ -96,20 +104,22 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
       srow[tid] = ok ? page * a.kv.page_size + p % a.kv.page_size : -1;
     }
     __syncthreads();
-    for (int j = warp; j < n; j += kChunkThreads / 32) {
+    for (int j = warp; j < n; j += kChunkThreads / 32) {  // (a position without a page: zeros)
       const int row = srow[j];
-      float dot[kChunkHeads] = {0.f, 0.f, 0.f, 0.f};
-      if (row >= 0)
-        for (int d = lane; d < a.L; d += 32) {
-          const float x = page_value(a.kv, row, d, a.L);
+      for (int d = lane; d < L; d += 32)
+        rows[j * Lp + d] = row >= 0 ? page_value(a.kv, row, d, L) : 0.f;
+    }
+    __syncthreads();
+    for (int i = tid; i < n * kChunkHeads; i += kChunkThreads) {
+      const int j = i % n, h = i / n;
+      const float* x = rows + j * Lp;
+      const float* y = sq + h * L;
+      float d4[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int d = 0; d < L; d += 8) {  // L is a multiple of 8
 #pragma unroll
-          for (int h = 0; h < kChunkHeads; ++h) dot[h] = fmaf(x, sq[h][d], dot[h]);
-        }
-#pragma unroll
-      for (int h = 0; h < kChunkHeads; ++h) {
-        const float z = warp_sum(dot[h]);
-        if (lane == 0) sz[h][j] = row >= 0 ? z * a.sm_scale : -INFINITY;
+        for (int u = 0; u < 8; ++u) d4[u & 3] = fmaf(x[d + u], y[d + u], d4[u & 3]);
       }
+      sz[h][j] = srow[j] >= 0 ? ((d4[0] + d4[1]) + (d4[2] + d4[3])) * a.sm_scale : -INFINITY;
     }
     __syncthreads();
     if (warp < nh) {  // warp = head: two positions a lane
@@ -136,14 +146,13 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
 #pragma unroll
       for (int c = 0; c < kChunkCols; ++c) acc[h][c] *= alpha;
     }
-    for (int j = 0; j < n; ++j) {
-      const int row = srow[j];
-      if (row < 0) continue;
 #pragma unroll
-      for (int c = 0; c < kChunkCols; ++c) {
-        const int d = c * kChunkThreads + tid;
-        if (d >= a.L) break;
-        const float x = page_value(a.kv, row, d, a.L);
+    for (int c = 0; c < kChunkCols; ++c) {
+      const int d = c * kChunkThreads + tid;
+      if (d >= L) break;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const float x = rows[j * Lp + d];
 #pragma unroll
         for (int h = 0; h < kChunkHeads; ++h) acc[h][c] = fmaf(sz[h][j], x, acc[h][c]);
       }
@@ -175,7 +184,7 @@ size_t mla_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype) {
 
 int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   if (mla_chunk_umma_ok(a.L, a.dtype, a.kv.kv_dtype))
-    return mla_chunk_pair_ok(a.T, a.B, a.Hm, a.kv.page_size)
+    return a.kv.kv_dtype == DSA_BF16 && a.window == 0 && a.T >= 8 * a.B && mla_chunk_pair_ok(a.T, a.B, a.Hm, a.kv.page_size)
                ? launch_mla_chunk_pair(a, workspace, stream)
                : launch_mla_chunk_umma(a, workspace, stream);
   cudaLaunchAttribute attr;
@@ -184,11 +193,17 @@ int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.T, (a.Hm + kChunkHeads - 1) / kChunkHeads, 1);
   cfg.blockDim = dim3(kChunkThreads, 1, 1);
+  cfg.dynamicSmemBytes =
+      ((size_t)chunk_tile(a.L) * (a.L + 1) + (size_t)kChunkHeads * a.L) * sizeof(float);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   auto kernel = a.dtype == DSA_BF16 ? mla_chunk_simt_kernel<__nv_bfloat16>
                                     : mla_chunk_simt_kernel<float>;
+  if (cfg.dynamicSmemBytes > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)cfg.dynamicSmemBytes) != cudaSuccess)
+    return DSA_ERR_CUDA;
   return launch_kernel(&cfg, kernel, a) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 

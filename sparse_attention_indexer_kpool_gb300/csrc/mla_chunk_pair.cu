@@ -935,9 +935,8 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
       !group_map(&kv_map, a.kv.pages, (uint64_t)a.kv.n_pages * a.kv.page_size, kCodes))
     return DSA_ERR_CUDA;
   auto kernel = mla_chunk_pair_kernel<kCodes>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) !=
-      cudaSuccess)
-    return DSA_ERR_CUDA;
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_smem(kernel, kSmem, done)) return DSA_ERR_CUDA;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

@@ -775,9 +775,8 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
                                1u << p.box_log, kSrc == kSrcTma8))
     return DSA_ERR_CUDA;
   auto kernel = mla_chunk_kernel<kN, kSrc>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)Smem<kN>::kBytes) != cudaSuccess)
-    return DSA_ERR_CUDA;
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_smem(kernel, Smem<kN>::kBytes, done)) return DSA_ERR_CUDA;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

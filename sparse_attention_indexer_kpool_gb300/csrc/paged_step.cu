@@ -186,7 +186,11 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(PlanArgs a, int cluste
 // Row t of kv_new goes to cache row kv_rows[t].  E4M3 pages hold code = rn(x / s)
 // with one fp32 scale per row, s = max|x| / 448 over the row's finite elements
 // (1 where that is zero): the row's largest magnitude lands on the largest code,
-// and both divisions are IEEE, so the stored row is a function of the row alone.
+// and both divisions are correctly rounded, so the stored row is a function of the
+// row alone.  The elements' divisions share their divisor: q = x r with r = rn(1 / s),
+// then q + (x - q s) r, the residual exact in an FMA (Markstein's correction, IBM J.
+// Res. Dev. 34(1), 1990), which rounds x / s correctly where nothing underflows;
+// rows with an extreme scale take the plain division.
 // One warp per row, 8 elements (16 or 32 bytes) a lane and step; the row stays in
 // registers between the maximum and the conversion, so it is read once.
 // What bounds it: HBM bandwidth (a row is 2 L bytes in, L or 2 L out).
@@ -267,6 +271,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
       o[1] = make_float4(x[s][4], x[s][5], x[s][6], x[s][7]);
     } else {
       uint32_t w[2];
+      const float r = __frcp_rn(scale);
+      const bool easy = scale > 0x1p-80f && scale < 0x1p80f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[4];
@@ -274,7 +280,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
         for (int i = 0; i < 4; ++i) {
           const float e = x[s][4 * h + i];
           // a non-finite element stays visible as NaN (E4M3 has no infinity)
-          v[i] = fabsf(e) < INFINITY ? __fdiv_rn(e, scale) : NAN;
+          const float q = e * r;
+          v[i] = easy ? fmaf(fmaf(-q, scale, e), r, q) : __fdiv_rn(e, scale);
+          if (!(fabsf(e) < INFINITY)) v[i] = NAN;
         }
         const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE,
                                                      __NV_E4M3);

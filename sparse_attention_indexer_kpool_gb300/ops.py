@@ -183,11 +183,37 @@ def dsa_mla_paged_decode(q_lat, pages, row_scale, block_table, seq_lens, page_si
     _check("dsa_mla_paged_decode", code)
 
 
-def _numel(t, n, name):
-    """The buffer's length is part of the call's geometry: the library cannot see it."""
-    if t is not None and t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
-    return t
+_I32, _F32 = torch.int32, torch.float32
+
+
+def _sizes(*wanted):
+    """Raise for a (tensor or None, elements, name) of another length: the number of elements is
+    part of a call's geometry, which the library cannot see."""
+    for t, n, name in wanted:
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+
+
+def _arg(t, dtype, name, dev):
+    """Pointer of a tensor on CUDA device ``dev``.  A serving step makes many small calls: the
+    good case costs a few cheap lookups, the others end in ``_ptr``'s errors."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_contiguous() \
+            and t.get_device() == dev >= 0:
+        return t.data_ptr()
+    _ptr(t, dtype, name)
+    raise ValueError(f"{name} must be on the current CUDA device ({dev}), got {t.device}")
+
+
+def _device(t, stream):
+    """(current device, stream): every tensor of a call must be on the current device."""
+    if not t.is_cuda:
+        return -1, None
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, _stream(stream)
 
 
 def dsa_paged_plan(ctx_lens, new_lens, free_pages, free_begin, n_pages, page_size, block_table,
@@ -198,23 +224,26 @@ def dsa_paged_plan(ctx_lens, new_lens, free_pages, free_begin, n_pages, page_siz
     (extended in place), outputs ``seq_lens`` [B] (may be ``ctx_lens``), ``cu_new`` [B + 1],
     ``q_seq``, ``q_pos``, ``kv_rows`` [T] (T fixes the step's capacity), ``free_end`` [1] (may be
     ``free_begin``); ``row_base`` [B] with ``key_rows`` [T] as well, or neither.  All int32."""
-    i32 = torch.int32
     B, T = ctx_lens.numel(), q_seq.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
-    for t, n, name in ((new_lens, B, "new_lens"), (free_begin, 1, "free_begin"),
-                       (row_base, B, "row_base"), (seq_lens, B, "seq_lens"),
-                       (cu_new, B + 1, "cu_new"), (q_pos, T, "q_pos"), (kv_rows, T, "kv_rows"),
-                       (key_rows, T, "key_rows"), (free_end, 1, "free_end")):
-        _numel(t, n, name)
+    if (new_lens.numel(), free_begin.numel(), seq_lens.numel(), cu_new.numel(), q_pos.numel(),
+            kv_rows.numel(), free_end.numel()) != (B, 1, B, B + 1, T, T, 1) or row_base is not None or key_rows is not None:
+        _sizes((new_lens, B, "new_lens"), (free_begin, 1, "free_begin"),
+               (seq_lens, B, "seq_lens"), (cu_new, B + 1, "cu_new"), (q_pos, T, "q_pos"),
+               (kv_rows, T, "kv_rows"), (free_end, 1, "free_end"), (row_base, B, "row_base"),
+               (key_rows, T, "key_rows"))
+    dev, st = _device(ctx_lens, stream)
     code = _lib.load().dsa_paged_plan(
-        _ptr(ctx_lens, i32, "ctx_lens"), _ptr(new_lens, i32, "new_lens"),
-        _ptr(free_pages, i32, "free_pages"), _ptr(free_begin, i32, "free_begin"),
-        _ptr(row_base, i32, "row_base"), B, T, free_pages.numel(), int(n_pages), int(page_size),
-        block_table.shape[1], _ptr(block_table, i32, "block_table"),
-        _ptr(seq_lens, i32, "seq_lens"), _ptr(cu_new, i32, "cu_new"), _ptr(q_seq, i32, "q_seq"),
-        _ptr(q_pos, i32, "q_pos"), _ptr(kv_rows, i32, "kv_rows"), _ptr(key_rows, i32, "key_rows"),
-        _ptr(free_end, i32, "free_end"), _ptr(status, i32, "status"), _stream(stream))
+        _arg(ctx_lens, _I32, "ctx_lens", dev), _arg(new_lens, _I32, "new_lens", dev),
+        _arg(free_pages, _I32, "free_pages", dev),
+        _arg(free_begin, _I32, "free_begin", dev), _arg(row_base, _I32, "row_base", dev), B,
+        T, free_pages.numel(), int(n_pages), int(page_size), block_table.shape[1],
+        _arg(block_table, _I32, "block_table", dev),
+        _arg(seq_lens, _I32, "seq_lens", dev), _arg(cu_new, _I32, "cu_new", dev),
+        _arg(q_seq, _I32, "q_seq", dev), _arg(q_pos, _I32, "q_pos", dev),
+        _arg(kv_rows, _I32, "kv_rows", dev), _arg(key_rows, _I32, "key_rows", dev),
+        _arg(free_end, _I32, "free_end", dev), _arg(status, _I32, "status", dev), st)
     _check("dsa_paged_plan", code)
 
 
@@ -225,13 +254,13 @@ def dsa_paged_append(kv_new, kv_rows, pages, row_scale=None, status=None, stream
     if kv_new.dim() != 2 or pages.dim() != 2 or pages.shape[1] != kv_new.shape[1]:
         raise ValueError("kv_new must be [T, L] and pages [n_pages * page_size, L]")
     T, L = kv_new.shape
-    _numel(kv_rows, T, "kv_rows")
-    _numel(row_scale, pages.shape[0], "row_scale")
+    _sizes((kv_rows, T, "kv_rows"), (row_scale, pages.shape[0], "row_scale"))
+    dev, st = _device(kv_new, stream)
     code = _lib.load().dsa_paged_append(
-        _ptr(kv_new, kv_new.dtype, "kv_new"), _ptr(kv_rows, torch.int32, "kv_rows"), T, L,
-        _dtype_tag(kv_new), _ptr(pages, pages.dtype, "pages"),
-        _ptr(row_scale, torch.float32, "row_scale"), pages.shape[0], 1, _kv_tag(pages),
-        _ptr(status, torch.int32, "status"), _stream(stream))
+        _arg(kv_new, kv_new.dtype, "kv_new", dev), _arg(kv_rows, _I32, "kv_rows", dev), T,
+        L, _dtype_tag(kv_new), _arg(pages, pages.dtype, "pages", dev),
+        _arg(row_scale, _F32, "row_scale", dev), pages.shape[0], 1, _kv_tag(pages),
+        _arg(status, _I32, "status", dev), st)
     _check("dsa_paged_append", code)
 
 
@@ -253,20 +282,21 @@ def dsa_mla_paged_chunk(q_lat, pages, row_scale, block_table, seq_lens, page_siz
     if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0]:
         raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
     B = block_table.shape[0]
-    for t, n, name in ((row_scale, pages.shape[0], "row_scale"), (cu_new, B + 1, "cu_new"),
-                       (out, T * Hm * L, "out"), (lse, T * Hm, "lse")):
-        _numel(t, n, name)
     act = q_lat.dtype
-    kv = _lib.PagedKv(_ptr(pages, pages.dtype, "pages"), _ptr(row_scale, torch.float32, "row_scale"),
-                      _ptr(block_table, torch.int32, "block_table"),
-                      _ptr(seq_lens, torch.int32, "seq_lens"), pages.shape[0] // int(page_size),
+    _sizes((row_scale, pages.shape[0], "row_scale"), (cu_new, B + 1, "cu_new"),
+           (out, T * Hm * L, "out"), (lse, T * Hm, "lse"))
+    dev, st = _device(q_lat, stream)
+    kv = _lib.PagedKv(_arg(pages, pages.dtype, "pages", dev),
+                      _arg(row_scale, _F32, "row_scale", dev),
+                      _arg(block_table, _I32, "block_table", dev),
+                      _arg(seq_lens, _I32, "seq_lens", dev), pages.shape[0] // int(page_size),
                       int(page_size), block_table.shape[1], _kv_tag(pages))
     code = _lib.load().dsa_mla_paged_chunk(
-        _ptr(q_lat, act, "q_lat"), ctypes.byref(kv), _ptr(cu_new, torch.int32, "cu_new"), T, B, Hm,
-        L, int(window), int(sinks), float(sm_scale), _dtype_tag(q_lat), _ptr(out, act, "out"),
-        _ptr(lse, torch.float32, "lse"), _ptr(workspace, torch.uint8, "workspace"),
-        0 if workspace is None else workspace.numel(), _ptr(status, torch.int32, "status"),
-        _stream(stream))
+        _arg(q_lat, act, "q_lat", dev), ctypes.byref(kv),
+        _arg(cu_new, _I32, "cu_new", dev), T, B, Hm, L, int(window), int(sinks),
+        float(sm_scale), _dtype_tag(q_lat), _arg(out, act, "out", dev),
+        _arg(lse, _F32, "lse", dev), _arg(workspace, torch.uint8, "workspace", dev),
+        0 if workspace is None else workspace.numel(), _arg(status, _I32, "status", dev), st)
     _check("dsa_mla_paged_chunk", code)
 
 
