@@ -382,7 +382,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // [rows, 512] bf16, boxes of 64 columns x box_rows rows, 128-byte swizzle; rows at
 // or beyond `rows` read as zeros.
-// codes: [rows, 512] bytes, boxes of 128 columns, no swizzle.
+// codes: [rows, 512] bytes, boxes of 128 columns.
 inline bool row_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows,
              bool codes = false) {
   auto fn = encode_fn();
@@ -393,7 +393,7 @@ inline bool row_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t bo
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

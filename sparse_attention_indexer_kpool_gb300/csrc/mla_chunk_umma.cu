@@ -499,9 +499,12 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
     bool ok = issue;
     const int lt = tid - 32 * kRow0;  // 0..127: its row of every tile
     if constexpr (kSrc == kSrcTma8) {
-      // Widen a chunk of codes in place: 128 rows of 128 codes land in its first
-      // block, every thread takes 8 of their 16-byte pieces into registers, and once
-      // all have, both blocks take the bf16 rows.
+      // Widen a chunk of codes in place: 128 rows of 128 codes (swizzled like the
+      // bf16 rows) land in its first block, every thread takes 8 of their 16-byte
+      // pieces into registers, and once all have, both blocks take the bf16 rows.
+      // Eight lanes hold one piece of eight rows, so that neither the reads nor the
+      // writes of a quarter warp meet in a bank.
+      const int r8 = lane & 7, unit0 = ((tid - 32 * kRow0) >> 5) * 32 + (lane >> 3);
       auto scale_of = [&](const Keys<kKeys>& k, int b, int v) -> float {
         const int t = k.at(v, lt);
         if (!k.sees(t)) return 0.f;
@@ -523,7 +526,9 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
             uint4 raw[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-              raw[u] = *reinterpret_cast<const uint4*>(dst + (u * 128 + lt) * 16);
+              raw[u] = *reinterpret_cast<const uint4*>(
+                  dst + ((unit0 + 4 * u) >> 3) * 1024 + r8 * 128 +
+                  ((((unit0 + 4 * u) & 7) ^ r8) << 4));
             int stop = !ok;  // every thread leaves at the same chunk
             asm volatile(
                 "{\n .reg .pred p, q;\n setp.ne.u32 p, %0, 0;\n"
@@ -536,13 +541,13 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
             if (mc == 0) c.rs[lt] = rs;  // the last tile's softmax has read its own
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-              const int i = u * 128 + lt, rr = i >> 3, pc = i & 7;
+              const int rr = ((unit0 + 4 * u) >> 3) * 8 + r8, pc = (unit0 + 4 * u) & 7;
               const uint32_t x[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {
                 const int ch = 2 * pc + hf;
                 *reinterpret_cast<uint4*>(dst + (ch >> 3) * kKvBlock + rr * 128 +
-                                          (((ch & 7) ^ (rr & 7)) << 4)) =
+                                          (((ch & 7) ^ r8) << 4)) =
                     make_uint4(e4m3x2_to_bf16x2(x[2 * hf] & 0xffffu),
                                e4m3x2_to_bf16x2(x[2 * hf] >> 16),
                                e4m3x2_to_bf16x2(x[2 * hf + 1] & 0xffffu),

@@ -228,33 +228,46 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   const int t = blockIdx.x * kAppendWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (t >= n_t) return;
   const int row = kv_rows[t];
+  const T* src = kv_new + (long long)t * L;
+  float x[kSteps][8];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {  // (beside the row number, not behind it)
+    const int d = (s * 32 + lane) * 8;
+    if (d < L) {
+      Load8<T>::get(src + d, x[s]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[s][i] = 0.f;
+    }
+  }
   if (row < 0) return;
   if (row >= n_rows) {
     if (lane == 0) flag(status, DSA_DEV_BAD_PAGE);
     return;
   }
-  const T* src = kv_new + (long long)t * L;
   const long long dst = (long long)row * L;
-  float x[kSteps][8];
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int d = (s * 32 + lane) * 8;
-    if (d < L) Load8<T>::get(src + d, x[s]);
-  }
-  float scale = 1.f;
+  float scale = 1.f, r = 1.f;
+  bool easy = true;
   if (kKv == DSA_FP8_E4M3) {
     float m = 0.f;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      if ((s * 32 + lane) * 8 >= L) continue;
+    for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = fabsf(x[s][i]);
-        if (v < INFINITY) m = fmaxf(m, v);  // NaN and infinities do not set the scale
-      }
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[s][i]));  // (a NaN is passed over)
+    m = warp_max(m);
+    if (m == INFINITY) {  // an infinity does not set the scale either
+      m = 0.f;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (fabsf(x[s][i]) < INFINITY) m = fmaxf(m, fabsf(x[s][i]));
+      m = warp_max(m);
     }
-    const float q = __fdiv_rn(warp_max(m), 448.f);
+    const float q = __fdiv_rn(m, 448.f);
     scale = q > 0.f ? q : 1.f;
+    r = __frcp_rn(scale);
+    easy = scale > 0x1p-80f && scale < 0x1p80f;
     if (lane == 0) row_scale[row] = scale;
   }
 #pragma unroll
@@ -270,24 +283,26 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
       o[0] = make_float4(x[s][0], x[s][1], x[s][2], x[s][3]);
       o[1] = make_float4(x[s][4], x[s][5], x[s][6], x[s][7]);
     } else {
+      // a non-finite element stays visible as NaN (E4M3 has no infinity): the residual
+      // of an infinity is one
+      if (easy) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float q = x[s][i] * r;
+          x[s][i] = fmaf(fmaf(-q, scale, x[s][i]), r, q);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[s][i] = fabsf(x[s][i]) < INFINITY ? __fdiv_rn(x[s][i], scale) : NAN;
+      }
       uint32_t w[2];
-      const float r = __frcp_rn(scale);
-      const bool easy = scale > 0x1p-80f && scale < 0x1p80f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = x[s][4 * h + i];
-          // a non-finite element stays visible as NaN (E4M3 has no infinity)
-          const float q = e * r;
-          v[i] = easy ? fmaf(fmaf(-q, scale, e), r, q) : __fdiv_rn(e, scale);
-          if (!(fabsf(e) < INFINITY)) v[i] = NAN;
-        }
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE,
-                                                     __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE,
-                                                     __NV_E4M3);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[s][4 * h], x[s][4 * h + 1]),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+            make_float2(x[s][4 * h + 2], x[s][4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
         w[h] = lo | (hi << 16);
       }
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pages) + dst + d) = make_uint2(w[0], w[1]);
