@@ -380,21 +380,31 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// [rows, 512] bf16, boxes of 64 columns x box_rows rows, 128-byte swizzle; rows at
-// or beyond `rows` read as zeros.
-// codes: [rows, 512] bytes, boxes of 128 columns.
-inline bool row_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows,
-             bool codes = false) {
+// Rows of `row_bytes` bytes as 2-byte elements (an E4M3 row is 256 of them: with
+// 1-byte elements the same boxes landed at a third of the rate), boxes of box_cols x
+// box_rows; rows at or beyond `rows` read as zeros.
+inline bool byte_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t row_bytes,
+                     uint32_t box_cols, uint32_t box_rows, bool swizzle) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)kL, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)kL * (codes ? 1 : 2)};
-  const cuuint32_t box[2] = {codes ? 128u : 64u, box_rows};
+  const cuuint64_t dims[2] = {row_bytes / 2, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// blocks of 128 bytes x box_rows rows, 128-byte swizzle
+inline bool row_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows,
+                    bool codes = false) {
+  return byte_map(m, base, rows, codes ? kL : 2 * kL, 64, box_rows, true);
+}
+// blocks of 512 bytes x box_rows rows, to bring rows into L2
+inline bool prefetch_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows,
+                         bool codes) {
+  return byte_map(m, base, rows, codes ? kL : 2 * kL, 256, box_rows, false);
 }
 
 }  // namespace chunk

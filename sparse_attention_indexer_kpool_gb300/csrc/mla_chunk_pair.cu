@@ -857,17 +857,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
   cluster_sync();  // neither CTA's memory goes while the other may write to it
 }
 
-// [rows, 512] as 64-column (codes: 128-byte) blocks: boxes of 8 rows of this CTA's
-// half of the latent columns, 128-byte swizzle.
+// [rows, 512] as blocks of 128 bytes: boxes of 8 rows of this CTA's half of the
+// latent columns, 128-byte swizzle (E4M3 codes in pairs, as 2-byte elements).
 bool group_map(CUtensorMap* m, const void* base, uint64_t rows, bool codes) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {codes ? 128u : 64u, (cuuint64_t)rows, codes ? 4u : 8u};
+  const cuuint64_t dims[3] = {64u, (cuuint64_t)rows, codes ? 4u : 8u};
   const cuuint64_t strides[2] = {(cuuint64_t)kL * (codes ? 1 : 2), 128};
-  const cuuint32_t box[3] = {codes ? 128u : 64u, 8, codes ? 2u : 4u};
+  const cuuint32_t box[3] = {64u, 8, codes ? 2u : 4u};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

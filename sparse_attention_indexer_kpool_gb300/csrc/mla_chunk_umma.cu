@@ -156,7 +156,8 @@ __device__ __forceinline__ void sync_load() {
 template <int kN, int kSrc>
 __global__ void __launch_bounds__(cta_threads(kSrc), 1)
     mla_chunk_kernel(const __grid_constant__ CUtensorMap q_map,
-                     const __grid_constant__ CUtensorMap kv_map, const Params p) {
+                     const __grid_constant__ CUtensorMap kv_map,
+                     const __grid_constant__ CUtensorMap ahead_map, const Params p) {
   using S = Smem<kN>;
   constexpr int kW = kN / 2;  // heads per softmax thread
   constexpr int kLoad0 = kSoftThreads / 32, kRow0 = kLoad0 + tma_warps(kSrc),
@@ -470,14 +471,13 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
             __syncwarp();
             if (row >= 0) {
               unsigned char* dst = sb + S::kKv + 2 * mc * kKvBlock + lane * R * 128;
-              tma_load_2d(dst, &kv_map, mc * 128, row, &land[mc]);
+              tma_load_2d(dst, &kv_map, mc * (kSrc == kSrcTma ? 128 : 64), row, &land[mc]);
               if (kSrc == kSrcTma)
                 tma_load_2d(dst + kKvBlock, &kv_map, mc * 128 + 64, row, &land[mc]);
             }
-            if (p.prefetch && row_next >= 0) {
-              tma_prefetch_2d(&kv_map, mc * 128, row_next);
-              if (kSrc == kSrcTma) tma_prefetch_2d(&kv_map, mc * 128 + 64, row_next);
-            }
+            // the next tile's rows to L2 (a request costs the warp about as much as a load)
+            if (p.prefetch && mc < (kSrc == kSrcTma ? 2 : 1) && row_next >= 0)
+              tma_prefetch_2d(&ahead_map, mc * 256, row_next);
           }
           if (!ok) break;
           issued = 0;
@@ -773,11 +773,14 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)n_cta * 2 * kN * kL);
   p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)n_cta * 2 * kN);
-  CUtensorMap q_map, kv_map;
+  CUtensorMap q_map, kv_map, ahead_map;
   if (!row_map(&q_map, a.q_lat, (uint64_t)a.T * a.Hm, kN)) return DSA_ERR_CUDA;
-  kv_map = q_map;
-  if (is_tma(kSrc) && !row_map(&kv_map, a.kv.pages, (uint64_t)a.kv.n_pages * a.kv.page_size,
-                               1u << p.box_log, kSrc == kSrcTma8))
+  kv_map = ahead_map = q_map;
+  const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.page_size;
+  if (is_tma(kSrc) &&
+      (!row_map(&kv_map, a.kv.pages, rows, 1u << p.box_log, kSrc == kSrcTma8) ||
+       (p.prefetch &&
+        !prefetch_map(&ahead_map, a.kv.pages, rows, 1u << p.box_log, kSrc == kSrcTma8))))
     return DSA_ERR_CUDA;
   auto kernel = mla_chunk_kernel<kN, kSrc>;
   static std::atomic<unsigned long long> done{0};
@@ -792,7 +795,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   cfg.gridDim = dim3(n_cta, 1, 1);
   cfg.blockDim = dim3(cta_threads(kSrc), 1, 1);
   cfg.dynamicSmemBytes = Smem<kN>::kBytes;
-  if (launch_kernel(&cfg, kernel, q_map, kv_map, p) != cudaSuccess) return DSA_ERR_CUDA;
+  if (launch_kernel(&cfg, kernel, q_map, kv_map, ahead_map, p) != cudaSuccess) return DSA_ERR_CUDA;
   cfg.gridDim = dim3(n_cta, kN / 8, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
