@@ -45,18 +45,25 @@ constexpr int kKeys = 128;
 constexpr int kKvBlock = kKeys * 128;  // 128 rows x 64 latent columns, 16 KB
 constexpr int kSoftThreads = 256;      // warps 0..7
 
-// Row sources: TMA boxes of bf16 rows or of E4M3 codes, which four warps then widen
-// in place (page size a multiple of 8); or, for any page size, four warps that copy
-// bf16 rows or widen E4M3 rows from global memory.
+// Row sources: TMA boxes of bf16 rows or of E4M3 codes, which two teams of four warps
+// then widen in place (page size a multiple of 8); or, for any page size, four warps
+// that copy bf16 rows or widen E4M3 rows from global memory.
 constexpr int kSrcTma = 0, kSrcCopy = 1, kSrcCopy8 = 2, kSrcTma8 = 3;
 __host__ __device__ constexpr bool is_tma(int src) { return src == kSrcTma || src == kSrcTma8; }
 __host__ __device__ constexpr bool is_e4m3(int src) { return src == kSrcCopy8 || src == kSrcTma8; }
-// warps 8..: the TMA warp, then the row warps, then the MMA warp
-__host__ __device__ constexpr int tma_warps(int src) { return is_tma(src) ? 1 : 0; }
-__host__ __device__ constexpr int row_warps(int src) { return src == kSrcTma ? 0 : 4; }
-__host__ __device__ constexpr int cta_threads(int src) {
-  return kSoftThreads + 32 * (tma_warps(src) + row_warps(src) + 1);
+// warps 8..: the row warps, then the TMA warps, then the MMA warp
+__host__ __device__ constexpr int row_warps(int src) {
+  return src == kSrcTma ? 0 : (src == kSrcTma8 ? 8 : 4);
 }
+__host__ __device__ constexpr int tma_warps(int src) { return is_tma(src) ? 2 : 0; }
+// (kSrcTma8: five whole warpgroups, which share the registers out anew)
+__host__ __device__ constexpr int cta_threads(int src) {
+  return src == kSrcTma8 ? 640 : kSoftThreads + 32 * (tma_warps(src) + row_warps(src) + 1);
+}
+// kSrcTma8: 640 threads launch with 96 registers each (61,440); the softmax's two
+// warpgroups take 128, the other three keep 72: 60,416 in all.
+constexpr int kSoftRegs = 128, kRestRegs = 72;
+static_assert(2 * 128 * kSoftRegs + 3 * 128 * kRestRegs <= 640 * 96, "register split");
 
 struct Ctl {
   float m[64], nm[64], alpha[64], l[64];  // per head; first: read as float4
@@ -148,6 +155,17 @@ __device__ __forceinline__ bool vote_soft(bool v) {  // whether any of them says
       : "memory");
   return r != 0;
 }
+// whether any thread of a team of four row warps says so
+__device__ __forceinline__ bool vote_rows(int team, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n"
+      " barrier.cta.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(2 + team), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ void sync_load() {
   asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
 }
@@ -160,8 +178,8 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
                      const __grid_constant__ CUtensorMap ahead_map, const Params p) {
   using S = Smem<kN>;
   constexpr int kW = kN / 2;  // heads per softmax thread
-  constexpr int kLoad0 = kSoftThreads / 32, kRow0 = kLoad0 + tma_warps(kSrc),
-                kMmaWarp = kRow0 + row_warps(kSrc);
+  constexpr int kRow0 = kSoftThreads / 32, kTmaWarp = kRow0 + row_warps(kSrc),
+                kMmaWarp = kTmaWarp + tma_warps(kSrc);
   constexpr int kTmemCols = kN == 64 ? 512 : 256;  // S^T (kN), O^T (4 kN)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -171,7 +189,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&c.full[i], kSrc == kSrcTma ? 1 : row_warps(kSrc));
+      mbar_init(&c.full[i], kSrc == kSrcTma ? 1 : 4);
       mbar_init(&c.raw[i], 1);
       mbar_init(&c.empty[i], 1);
     }
@@ -207,7 +225,13 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
   const uint32_t pb = smem_u32(sb + S::kP);
   volatile int* dead = &c.dead;
 
-  if (warp < kLoad0) {
+  if constexpr (kSrc == kSrcTma8) {
+    if (warp < kRow0)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
+  }
+  if (warp < kRow0) {
     // ================= softmax and epilogue =================
     const int qw = warp & 3;      // TMEM lanes 32 qw ..: this thread's key row r
     const int hq = warp >> 2;     // heads kW hq ..
@@ -418,27 +442,31 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
     }
     if (!ok) hd = Header{-1, -1, 0, 0};
     if (tid == 0 && p.head) p.head[blockIdx.x] = hd;
-  } else if (warp < kRow0) {
+  } else if (is_tma(kSrc) && warp >= kTmaWarp && warp < kMmaWarp) {
     // ================= TMA =================
+    // Two warps take the chunks in turn: a copy costs the issuing warp 100 cycles and
+    // more (16-row boxes: 1,340 a chunk, four times what its part of O^T takes).
+    const int team = warp - kTmaWarp;
+    const int R = 1 << p.box_log, ng = kKeys >> p.box_log;
+    uint64_t* land = kSrc == kSrcTma ? c.full : c.raw;
     int tiles = 0, segs = 0;
     bool ok = issue;
-    {
-      const int R = 1 << p.box_log, ng = kKeys >> p.box_log;
-      int issued = 0;  // chunks of tile `tiles` under way
-      // the cache row of this lane's box of a tile (-1: nothing seen, -2: no page)
-      auto box_row = [&](const Keys<kKeys>& k, int b, int v) -> int {
-        if (lane >= ng) return -1;
-        const int t0 = k.at(v, lane * R);
-        if (t0 > k.pos) return -1;
-        const int blk = t0 / p.kv.page_size;
-        if (blk >= p.kv.max_pages) return -2;
-        const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
-        if (page < 0 || page >= p.kv.n_pages) return -2;
-        return page * p.kv.page_size + t0 % p.kv.page_size;
-      };
-      while (ok && w.next()) {
-        if (w.ta == w.tb) continue;
-        int row = box_row(w.k, w.b, w.ta);
+    int issued = 0;  // chunks of tile `tiles` under way, up to this one
+    // the cache row of this lane's box of a tile (-1: nothing seen, -2: no page)
+    auto box_row = [&](const Keys<kKeys>& k, int b, int v) -> int {
+      if (lane >= ng) return -1;
+      const int t0 = k.at(v, lane * R);
+      if (t0 > k.pos) return -1;
+      const int blk = t0 / p.kv.page_size;
+      if (blk >= p.kv.max_pages) return -2;
+      const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
+      if (page < 0 || page >= p.kv.n_pages) return -2;
+      return page * p.kv.page_size + t0 % p.kv.page_size;
+    };
+    while (ok && w.next()) {
+      if (w.ta == w.tb) continue;
+      int row = box_row(w.k, w.b, w.ta);
+      if (team == 0) {
         // the queries, once the previous segment's last product with them is done
         const bool free_q = segs == 0 || wait_on(&c.q_empty, (segs - 1) & 1, dead, wait_ns);
         if (!__all_sync(0xffffffffu, free_q)) break;
@@ -449,62 +477,63 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
                         w.token * p.Hm + w.h0 * kN, &c.q_full);
         }
         ++segs;
-        for (int v = w.ta; v < w.tb; ++v, ++tiles) {
-          const int row_next = v + 1 < w.tb ? box_row(w.k, w.b, v + 1) : -1;
-          if (row == -2) {
-            flag(p.status, DSA_DEV_BAD_PAGE);
-            row = -1;
-          }
-          const unsigned boxes = __ballot_sync(0xffffffffu, row >= 0);
-          const uint32_t bytes = __popc(boxes) * R * (kSrc == kSrcTma ? 256 : 128);
-          uint64_t* land = kSrc == kSrcTma ? c.full : c.raw;
-#pragma unroll 1
-          for (int mc = 0; mc < 4; ++mc) {
-            const bool room = tiles == 0 || wait_on(&c.empty[mc], (tiles - 1) & 1, dead, wait_ns);
-            ok = __all_sync(0xffffffffu, room);
-            if (!ok) break;
-            if (lane == 0) {
-              if (mc == 0) c.groups = boxes;  // the last tile's softmax has read its own
-              mbar_arrive_expect_tx(&land[mc], bytes);
-            }
-            issued = mc + 1;
-            __syncwarp();
-            if (row >= 0) {
-              unsigned char* dst = sb + S::kKv + 2 * mc * kKvBlock + lane * R * 128;
-              tma_load_2d(dst, &kv_map, mc * (kSrc == kSrcTma ? 128 : 64), row, &land[mc]);
-              if (kSrc == kSrcTma)
-                tma_load_2d(dst + kKvBlock, &kv_map, mc * 128 + 64, row, &land[mc]);
-            }
-            // the next tile's rows to L2 (a request costs the warp about as much as a load)
-            if (p.prefetch && mc < (kSrc == kSrcTma ? 2 : 1) && row_next >= 0)
-              tma_prefetch_2d(&ahead_map, mc * 256, row_next);
-          }
-          if (!ok) break;
-          issued = 0;
-          row = row_next;
-        }
       }
-      // after a give-up: no copy into this CTA's memory may be in flight at its end
-      if (*dead && lane == 0) {
-        for (int mc = 0; mc < 4; ++mc)
-          if (mc < issued || tiles > 0)
-            mbar_wait_bounded(&(kSrc == kSrcTma ? c.full : c.raw)[mc],
-                              (mc < issued ? tiles : tiles - 1) & 1);
-        if (segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        const int row_next = v + 1 < w.tb ? box_row(w.k, w.b, v + 1) : -1;
+        if (row == -2) {
+          flag(p.status, DSA_DEV_BAD_PAGE);
+          row = -1;
+        }
+        const unsigned boxes = __ballot_sync(0xffffffffu, row >= 0);
+        const uint32_t bytes = __popc(boxes) * R * (kSrc == kSrcTma ? 256 : 128);
+#pragma unroll 1
+        for (int mc = team; mc < 4; mc += 2) {
+          const bool room = tiles == 0 || wait_on(&c.empty[mc], (tiles - 1) & 1, dead, wait_ns);
+          ok = __all_sync(0xffffffffu, room);
+          if (!ok) break;
+          if (lane == 0) {
+            if (mc == 0) c.groups = boxes;  // the last tile's softmax has read its own
+            mbar_arrive_expect_tx(&land[mc], bytes);
+          }
+          issued = mc + 1;
+          __syncwarp();
+          if (row >= 0) {
+            unsigned char* dst = sb + S::kKv + 2 * mc * kKvBlock + lane * R * 128;
+            tma_load_2d(dst, &kv_map, mc * (kSrc == kSrcTma ? 128 : 64), row, &land[mc]);
+            if (kSrc == kSrcTma)
+              tma_load_2d(dst + kKvBlock, &kv_map, mc * 128 + 64, row, &land[mc]);
+          }
+        }
+        if (!ok) break;
+        issued = 0;
+        // the next tile's rows to L2 (bf16: half of a row each)
+        if (p.prefetch && row_next >= 0 && (kSrc == kSrcTma || team == 0))
+          tma_prefetch_2d(&ahead_map, team * 256, row_next);
+        row = row_next;
       }
     }
-  } else if (warp < kMmaWarp) {
+    // after a give-up: no copy into this CTA's memory may be in flight at its end
+    if (*dead && lane == 0) {
+      for (int mc = team; mc < 4; mc += 2)
+        if (mc < issued || tiles > 0)
+          mbar_wait_bounded(&land[mc], (mc < issued ? tiles : tiles - 1) & 1);
+      if (segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
+    }
+  } else if (warp < kRow0 + row_warps(kSrc)) {
     // ================= rows =================
     int tiles = 0, segs = 0;
     bool ok = issue;
-    const int lt = tid - 32 * kRow0;  // 0..127: its row of every tile
+    const int lt = (tid - 32 * kRow0) & 127;  // its row of every tile
     if constexpr (kSrc == kSrcTma8) {
       // Widen a chunk of codes in place: 128 rows of 128 codes (swizzled like the
       // bf16 rows) land in its first block, every thread takes 8 of their 16-byte
       // pieces into registers, and once all have, both blocks take the bf16 rows.
       // Eight lanes hold one piece of eight rows, so that neither the reads nor the
-      // writes of a quarter warp meet in a bank.
-      const int r8 = lane & 7, unit0 = ((tid - 32 * kRow0) >> 5) * 32 + (lane >> 3);
+      // writes of a quarter warp meet in a bank.  Two teams take the chunks in turn: a
+      // chunk's steps (its landing, the codes to registers, widening, the fence before
+      // the tensor cores' reads: 1,400 cycles) wait more than they work.
+      const int team = (warp - kRow0) >> 2;
+      const int r8 = lane & 7, unit0 = (lt >> 5) * 32 + (lane >> 3);
       auto scale_of = [&](const Keys<kKeys>& k, int b, int v) -> float {
         const int t = k.at(v, lt);
         if (!k.sees(t)) return 0.f;
@@ -519,7 +548,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         for (int v = w.ta; v < w.tb; ++v, ++tiles) {
           const float rs_next = v + 1 < w.tb ? scale_of(w.k, w.b, v + 1) : 0.f;
 #pragma unroll 1
-          for (int mc = 0; mc < 4; ++mc) {
+          for (int mc = team; mc < 4; mc += 2) {
             // (the codes' landing implies that the chunk was free)
             ok = ok && wait_on(&c.raw[mc], tiles & 1, dead, wait_ns);
             unsigned char* dst = sb + S::kKv + 2 * mc * kKvBlock;
@@ -529,12 +558,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
               raw[u] = *reinterpret_cast<const uint4*>(
                   dst + ((unit0 + 4 * u) >> 3) * 1024 + r8 * 128 +
                   ((((unit0 + 4 * u) & 7) ^ r8) << 4));
-            int stop = !ok;  // every thread leaves at the same chunk
-            asm volatile(
-                "{\n .reg .pred p, q;\n setp.ne.u32 p, %0, 0;\n"
-                " barrier.cta.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
-                : "+r"(stop)::"memory");
-            if (stop) {
+            if (vote_rows(team, !ok)) {  // every thread leaves at the same chunk
               ok = false;
               break;
             }
@@ -657,26 +681,16 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
           }
           // after a give-up every thread leaves at the same tile (nobody waits for
           // the others in sync_load)
-          int stop = !ok;
-          asm volatile(
-              "{\n .reg .pred p, q;\n setp.ne.u32 p, %0, 0;\n"
-              " barrier.cta.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
-              : "+r"(stop)::"memory");
-          if (stop) {
+          if (vote_rows(0, !ok)) {
             ok = false;
             break;
           }
         }
-        int stop = !ok;
-        asm volatile(
-            "{\n .reg .pred p, q;\n setp.ne.u32 p, %0, 0;\n"
-            " barrier.cta.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
-            : "+r"(stop)::"memory");
-        ok = !stop;
+        ok = !vote_rows(0, !ok);
       }
       if (*dead && lt == 0 && segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
     }
-  } else if (issue) {
+  } else if (warp == kMmaWarp && issue) {
     // ================= MMA =================
     // The whole warp runs the loop and one elected lane issues: the descriptors
     // stay in uniform registers (one lane alone: 73 instead of 51 cycles a step).
