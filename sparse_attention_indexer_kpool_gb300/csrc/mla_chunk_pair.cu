@@ -711,6 +711,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
       constexpr uint32_t id_s = umma_idesc_bf16(128, kKT, false);
       constexpr uint32_t id_o = umma_idesc_bf16(128, 256, false, true);
       const uint32_t qb = smem_u32(sb + kOffQ), kb = smem_u32(sb + kOffK);
+      // (a descriptor's low bits are the address in 16-byte units: steps add constants)
+      const uint64_t d_q = sw128_desc(qb), d_k0 = umma_desc_sw128(kb, 16, 4096),
+                     d_v0 = umma_desc_sw128(kb, 1024, 4096);
       // Two streams over the same tiles: scores as soon as a stage holds keys, outputs
       // as soon as a tile's weights are there; whichever is ready goes next (outputs
       // first: they free the stage).
@@ -729,11 +732,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
       while (left_o) {
         if (no < ns && ready(&c.p_full[no % kStages], (no / kStages) & 1)) {
           const int st = no % kStages;
-          const uint32_t k0 = kb + st * kStageBytes, a0 = tmem + 256 + st * kKT;
+          const uint64_t d_v = d_v0 + (uint32_t)(st * (kStageBytes >> 4));
+          const uint32_t a0 = tmem + 256 + st * kKT;
           tc_fence_after();
 #pragma unroll
           for (int s = 0; s < kKT / 16; ++s)
-            umma_tmem_a_elect(tmem, a0 + s * 8, umma_desc_sw128(k0 + s * 8192, 1024, 4096), id_o,
+            umma_tmem_a_elect(tmem, a0 + s * 8, d_v + s * (8192 >> 4), id_o,
                               (vo > wo.ta || s > 0) ? 1u : 0u);
           umma_commit_elect(&c.k_empty[st]);
           ++no;
@@ -750,14 +754,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
           // (the stage's keys imply that its last PV is done: its scores are free)
           if (have_q && ready(&c.k_full[ns % kStages], (ns / kStages) & 1)) {
             const int st = ns % kStages;
-            const uint32_t k0 = kb + st * kStageBytes;
+            const uint64_t d_k = d_k0 + (uint32_t)(st * (kStageBytes >> 4));
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const uint32_t blk = j >> 2, off = (j & 3) * 32;
-              umma_bf16_elect(tmem + 256 + st * kKT, sw128_desc(qb + blk * kQBlock + off),
-                              umma_desc_sw128(k0 + blk * 1024 + off, 16, 4096), id_s,
-                              j ? 1u : 0u);
+              umma_bf16_elect(tmem + 256 + st * kKT, d_q + ((blk * kQBlock + off) >> 4),
+                              d_k + ((blk * 1024 + off) >> 4), id_s, j ? 1u : 0u);
             }
             umma_commit_elect(&c.s_full[st]);
             ++ns;

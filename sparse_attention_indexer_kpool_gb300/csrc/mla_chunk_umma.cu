@@ -699,6 +699,12 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, wait_on(bar, parity, dead, wait_ns)) != 0;
     };
+    // A descriptor's low bits are the address in 16-byte units (below 2^14): a step adds
+    // a constant to a base.  (Built anew for each step they cost 70 cycles a step.)
+    const uint64_t d_k = sw128_desc(kvb), d_q = sw128_desc(qb);
+    const uint64_t d_v = umma_desc_sw128(kvb, kKvBlock, 1024);
+    const uint64_t d_p = kN == 64 ? umma_desc_sw128(pb, kKeys * 128, 1024)
+                                  : umma_desc_sw64(pb, kKeys * 64, 512);
     int tiles = 0, segs = 0;
     bool ok = true;
     while (ok && w.next()) {
@@ -713,8 +719,8 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const uint32_t blk = 2 * mc + (j >> 2), off = (j & 3) * 32;
-            umma_bf16_elect(tmem, sw128_desc(kvb + blk * kKvBlock + off),
-                            sw128_desc(qb + blk * S::kQBlock + off), id_s, (mc | j) ? 1u : 0u);
+            umma_bf16_elect(tmem, d_k + ((blk * kKvBlock + off) >> 4),
+                            d_q + ((blk * S::kQBlock + off) >> 4), id_s, (mc | j) ? 1u : 0u);
           }
         }
         if (!ok) break;
@@ -727,10 +733,9 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         for (int mc = 0; mc < 4; ++mc) {
 #pragma unroll
           for (int kr = 0; kr < 8; ++kr) {
-            const uint64_t a = umma_desc_sw128(kvb + 2 * mc * kKvBlock + kr * 2048, kKvBlock, 1024);
-            const uint64_t b = kN == 64 ? umma_desc_sw128(pb + kr * 2048, kKeys * 128, 1024)
-                                        : umma_desc_sw64(pb + kr * 1024, kKeys * 64, 512);
-            umma_bf16_elect(tmem + kN + mc * kN, a, b, id_o, (v > w.ta || kr > 0) ? 1u : 0u);
+            umma_bf16_elect(tmem + kN + mc * kN, d_v + ((2 * mc * kKvBlock + kr * 2048) >> 4),
+                            d_p + ((kr * (kN == 64 ? 2048 : 1024)) >> 4), id_o,
+                            (v > w.ta || kr > 0) ? 1u : 0u);
           }
           umma_commit_elect(&c.empty[mc]);
         }
