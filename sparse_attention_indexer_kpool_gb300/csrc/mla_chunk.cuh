@@ -21,7 +21,7 @@ constexpr float kRaiseAt = 20.f;
 
 struct Header {        // what a worker (CTA or CTA pair) left for the join
   int start_tile;      // row tile whose first units it holds but not its last (-1: none)
-  int cont_tile;       // row tile that an earlier worker began (-1: none; -2: no share at all)
+  int cont_tile;       // row tile that an earlier worker began (-1: none)
   int cont_some;       // it has a partial of that
   int cont_ends;       // and its last units
 };
@@ -118,7 +118,9 @@ __device__ __forceinline__ unsigned row_tiles(const Seq& s, int hb) {
 }
 
 // The share of worker `me` of `workers`: returns its number of units, and fills
-// *st.  Run by all kThreads threads of a CTA; ends with a barrier.
+// *st.  With fewer units than workers the first ones take one each, so that the
+// workers of a row tile are always neighbours.  Run by all kThreads threads of a CTA;
+// ends with a barrier.
 template <int kT, bool kPair, int kThreads>
 __device__ __forceinline__ unsigned long long find_share(const Params& p, int hb, unsigned me,
                                                          unsigned workers, Start* st,
@@ -149,7 +151,10 @@ __device__ __forceinline__ unsigned long long find_share(const Params& p, int hb
     if (w < warp) before += st->scan[w];
     total += st->scan[w];
   }
-  if (total < (1ull << 32) / 256) {  // (fewer than 256 workers: a product of 32 bits)
+  if (total < workers) {
+    v0 = me < total ? me : total;
+    v1 = me < total ? me + 1 : total;
+  } else if (total < (1ull << 32) / 256) {  // (fewer than 256 workers: a product of 32 bits)
     v0 = (unsigned)total * me / workers;
     v1 = (unsigned)total * (me + 1) / workers;
   } else {
@@ -293,15 +298,18 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
 }
 
 // Join the partials of the row tiles that were split over workers, in their order:
-// block (g, y) takes the tile that worker g began, rows 8 y ... (one warp per row,
-// four 16-byte pieces of the latent row a lane).
+// block (g, y) takes the tile that worker g began, rows 8 y ..; a warp takes half of
+// a row's latent columns (two 16-byte pieces a lane).  The workers behind
+// g that hold parts of the tile are found 32 at a time, a lane each, with their
+// maxima and sums; then eight partial rows are on their way at once, so that even one
+// token split over every SM joins in a few round trips to memory.
 template <int kRows, bool kPair>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
     mla_chunk_join_kernel(const Params p, int workers) {
   pdl_wait();
   pdl_launch_dependents();
-  const int g = blockIdx.x, lane = threadIdx.x & 31;
-  const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = blockIdx.y * 8 + (warp >> 1), col = (warp & 1) * 256 + lane * 4;
   const int tile = p.head[g].start_tile;
   if (tile < 0) return;
   int token, head;
@@ -320,51 +328,73 @@ __global__ void __launch_bounds__(256)
   }
   if (head >= p.Hm) return;
   float mx = -INFINITY, den = 0.f;
-  float4 acc[4];
+  float4 acc[2];
+  acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool more = true;
+  for (int s0 = g; more; s0 += 32) {
+    // lane: worker s0 + lane; those up to the one that ends the tile
+    const int s = s0 + lane;
+    Header hd = {-1, -1, 0, 0};
+    if (s < workers) hd = p.head[s];
+    const bool mine = s == g || hd.cont_tile == tile;
+    const bool ends = s != g && hd.cont_ends != 0;
+    const unsigned stop = __ballot_sync(0xffffffffu, !mine || ends);
+    const int n = stop ? __ffs(stop) - 1 : 32;            // before the stopping one
+    const int last = (stop && __shfl_sync(0xffffffffu, (int)mine, n & 31)) ? n : n - 1;
+    more = stop == 0;
+    const bool part = lane <= last && (s == g || hd.cont_some);
+    const int slot = s == g ? 2 * g + 1 : 2 * s;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (part) ml = p.part_ml[slot * kRows + h];
+    const bool some = part && ml.y != 0.f;  // (a part that saw no page adds nothing)
+    const float top = fmaxf(mx, warp_max(some ? ml.x : -INFINITY));
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float old = ex2_fast(mx - ref);   // 0 before the first part
+    const float wgt = some ? ex2_fast(ml.x == -INFINITY ? 0.f : ml.x - ref) : 0.f;
+    den = den * old + warp_sum(some ? ml.y * wgt : 0.f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = g; s < workers; ++s) {
-    int slot = 2 * g + 1;
-    bool last = false;
-    if (s > g) {
-      const Header hd = p.head[s];
-      if (hd.cont_tile == -2) continue;
-      if (hd.cont_tile != tile) break;
-      last = hd.cont_ends;
-      slot = 2 * s;
-      if (!hd.cont_some) {
-        if (last) break;
-        continue;
+    for (int q = 0; q < 2; ++q) {
+      acc[q].x *= old; acc[q].y *= old; acc[q].z *= old; acc[q].w *= old;
+    }
+    mx = top;
+    unsigned todo = __ballot_sync(0xffffffffu, some);
+    while (todo) {
+      float4 v[8][2];
+      float wv[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = todo ? __ffs(todo) - 1 : -1;
+        const int sl = __shfl_sync(0xffffffffu, slot, i & 31);
+        wv[u] = __shfl_sync(0xffffffffu, wgt, i & 31);
+        if (i < 0) wv[u] = 0.f;
+        const float4* src = reinterpret_cast<const float4*>(
+            p.part_o + ((long long)sl * kRows + h) * kL + col);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          v[u][q] = i < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcs(src + q * 32);
+        todo &= todo - 1;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          acc[q].x = fmaf(v[u][q].x, wv[u], acc[q].x);
+          acc[q].y = fmaf(v[u][q].y, wv[u], acc[q].y);
+          acc[q].z = fmaf(v[u][q].z, wv[u], acc[q].z);
+          acc[q].w = fmaf(v[u][q].w, wv[u], acc[q].w);
+        }
       }
     }
-    const float2 ml = p.part_ml[slot * kRows + h];
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + ((long long)slot * kRows + h) * kL);
-    float4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __ldcs(src + i * 32 + lane);
-    if (ml.y != 0.f) {  // a part that saw no page has nothing to add
-      const float m = fmaxf(mx, ml.x), ref = m == -INFINITY ? 0.f : m;
-      const float a = ex2_fast(mx - ref), b = ex2_fast(ml.x == -INFINITY ? 0.f : ml.x - ref);
-      den = den * a + ml.y * b;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i].x = acc[i].x * a + v[i].x * b;
-        acc[i].y = acc[i].y * a + v[i].y * b;
-        acc[i].z = acc[i].z * a + v[i].z * b;
-        acc[i].w = acc[i].w * a + v[i].w * b;
-      }
-      mx = m;
-    }
-    if (last) break;
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
   const long long row = (long long)token * p.Hm + head;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<uint2*>(p.out + row * kL + (i * 32 + lane) * 4) =
-        make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv),
-                   pack_bf16(acc[i].z * inv, acc[i].w * inv));
-  if (p.lse && lane == 0) p.lse[row] = den == 0.f ? -INFINITY : (mx + log2f(den)) / kLog2e;
+  for (int q = 0; q < 2; ++q)
+    *reinterpret_cast<uint2*>(p.out + row * kL + col + q * 128) =
+        make_uint2(pack_bf16(acc[q].x * inv, acc[q].y * inv),
+                   pack_bf16(acc[q].z * inv, acc[q].w * inv));
+  if (p.lse && lane == 0 && (warp & 1) == 0)
+    p.lse[row] = den == 0.f ? -INFINITY : (mx + log2f(den)) / kLog2e;
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

@@ -314,7 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
       const uint4* in_s = reinterpret_cast<const uint4*>(sb + kOffS) + h * (kW / 4) * 64 + r;
       const uint2* in_p = reinterpret_cast<const uint2*>(sb + kOffP) + h * (kW / 4) * 64 + r;
       const int ttid = ((warp & 1) + 2 * h) * 32 + lane;  // thread of the team
-      Header hd = {-1, any ? -1 : -2, 0, 0};
+      Header hd = {-1, -1, 0, 0};
       int tiles = 0, segs = 0, sums = 0;
       bool ok = true;
       // The phases of the data from the other CTA are armed one ahead.  (Nothing of
@@ -952,7 +952,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   cfg.dynamicSmemBytes = kSmem;
   if (launch_kernel(&cfg, kernel, q_map, kv_map, p) != cudaSuccess) return DSA_ERR_CUDA;
   cfg.gridDim = dim3(pairs, 16, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.blockDim = dim3(512, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return launch_kernel(&cfg, mla_chunk_join_kernel<128, true>, p, pairs) == cudaSuccess
              ? DSA_OK

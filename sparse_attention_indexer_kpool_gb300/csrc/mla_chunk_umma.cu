@@ -216,7 +216,6 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
   const unsigned long long units = find_share<kKeys, false, cta_threads(kSrc)>(
       p, hb, blockIdx.x, gridDim.x, &c.start, blockIdx.x == 0);
   const uint32_t tmem = c.tmem;
-  const bool any = c.start.b < p.B;
   Walk<kKeys, false> w(p, hb, c.start, units);
   // a failure drill loads nothing and issues no MMA: the first waits run out
   const bool issue = p.drill == 0;
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
     const int hq = warp >> 2;     // heads kW hq ..
     const int r = qw * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16);
-    Header hd = {-1, any ? -1 : -2, 0, 0};
+    Header hd = {-1, -1, 0, 0};
     int tiles = 0, segs = 0;      // waits so far
     bool ok = true;
     while (ok && w.next()) {
@@ -816,7 +815,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   cfg.dynamicSmemBytes = Smem<kN>::kBytes;
   if (launch_kernel(&cfg, kernel, q_map, kv_map, ahead_map, p) != cudaSuccess) return DSA_ERR_CUDA;
   cfg.gridDim = dim3(n_cta, kN / 8, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.blockDim = dim3(512, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return launch_kernel(&cfg, mla_chunk_join_kernel<kN, false>, p, n_cta) == cudaSuccess ? DSA_OK
                                                                                  : DSA_ERR_CUDA;
