@@ -183,10 +183,14 @@ size_t mla_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype) {
 }
 
 int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
-  if (mla_chunk_umma_ok(a.L, a.dtype, a.kv.kv_dtype))
-    return a.kv.kv_dtype == DSA_BF16 && a.window == 0 && a.T >= 8 * a.B && mla_chunk_pair_ok(a.T, a.B, a.Hm, a.kv.page_size)
+  if (mla_chunk_umma_ok(a.L, a.dtype, a.kv.kv_dtype)) {
+    if (a.kv.kv_dtype == DSA_FP8_E4M3 && a.kv.page_size % 8 == 0)
+      return launch_mla_chunk_f8(a, workspace, stream);
+    return a.kv.kv_dtype == DSA_BF16 && a.window == 0 && a.T >= 8 * a.B &&
+                   mla_chunk_pair_ok(a.T, a.B, a.Hm, a.kv.page_size)
                ? launch_mla_chunk_pair(a, workspace, stream)
                : launch_mla_chunk_umma(a, workspace, stream);
+  }
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

@@ -39,6 +39,7 @@ struct Params {
   int32_t* status;
   int drill, prefetch;
   int box_log;               // positions of a box, 2^box_log (copied rows: 1)
+  float o_scale;             // of the partials' output against their sums
 };
 
 // ---- the batch as units ------------------------------------------------------
@@ -274,6 +275,128 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
 }
 
+// kW values per lane (one row, kW heads) reduced over the warp's 32 rows by
+// halving exchanges; lane l ends with head l mod kW.
+template <int kW, bool kMax>
+__device__ __forceinline__ float across_rows(float (&v)[kW], int lane) {
+  if (kW == 16) {
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      const float o = __shfl_xor_sync(0xffffffffu, v[i], 16);
+      v[i] = kMax ? fmaxf(v[i], o) : v[i] + o;
+    }
+  }
+#pragma unroll
+  for (int s = kW / 2; s >= 1; s >>= 1) {
+    const bool upper = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float send = upper ? v[i] : v[i + s];
+      const float keep = upper ? v[i + s] : v[i];
+      const float recv = __shfl_xor_sync(0xffffffffu, send, s);
+      v[i] = kMax ? fmaxf(keep, recv) : keep + recv;
+    }
+  }
+  return v[0];
+}
+
+template <int kW>
+__device__ __forceinline__ void tmem_ldw(uint32_t ta, float (&v)[kW]) {
+  if constexpr (kW == 32) tmem_ld32(ta, v); else tmem_ld16(ta, v);
+}
+// Store 16 consecutive fp32 columns of the warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+      "r"(__float_as_uint(v[15]))
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+template <int kW>
+__device__ __forceinline__ void tmem_stw(uint32_t ta, const float (&v)[kW]) {
+  if constexpr (kW == 32) tmem_st32(ta, v); else tmem_st16(ta, v);
+}
+
+// Barriers of the eight softmax warps (barrier 0 is the CTA's).
+__device__ __forceinline__ void sync_soft() {
+  asm volatile("barrier.cta.sync 1, 256;" :: : "memory");
+}
+__device__ __forceinline__ bool vote_soft(bool v) {  // whether any of them says so
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " barrier.cta.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// A segment's end, by the eight softmax warps (lane quarter qw, heads kN / 2 hq ..):
+// a row tile's rows, normalised by inv[head]; O^T (kN columns a chunk of 128 latent
+// columns) from TMEM at `to`.  A lane pair holds two latent columns of every head:
+// each lane of the pair stores both columns of one of two heads.
+template <int kN>
+__device__ __forceinline__ void store_rows(const Params& p, const float* inv, uint32_t to,
+                                           long long row0, int heads, int qw, int hq, int lane) {
+  constexpr int kW = kN / 2;
+  const bool upper = lane & 1;
+#pragma unroll 1
+  for (int mc = 0; mc < 4; ++mc) {
+    float o[kW];
+    tmem_ldw<kW>(to + (uint32_t)(mc * kN + hq * kW), o);
+    __nv_bfloat16* dst =
+        p.out + (row0 + hq * kW + (upper ? 1 : 0)) * kL + mc * 128 + qw * 32 + (lane & ~1);
+#pragma unroll
+    for (int i = 0; i < kW; i += 2) {
+      const float a = o[i] * inv[hq * kW + i], b = o[i + 1] * inv[hq * kW + i + 1];
+      const float got = __shfl_xor_sync(0xffffffffu, upper ? a : b, 1);
+      if (hq * kW + i + (upper ? 1 : 0) < heads)
+        *reinterpret_cast<uint32_t*>(dst + (long long)i * kL) =
+            upper ? pack_bf16(got, b) : pack_bf16(a, got);
+    }
+  }
+}
+// an unnormalised part of a row tile, for the join
+template <int kN>
+__device__ __forceinline__ void store_part(const Params& p, int slot, uint32_t to, int heads,
+                                           int qw, int hq, int lane) {
+  constexpr int kW = kN / 2;
+  float* dst = p.part_o + ((long long)slot * kN + hq * kW) * kL + qw * 32 + lane;
+#pragma unroll 1
+  for (int mc = 0; mc < 4; ++mc) {
+    float o[kW];
+    tmem_ldw<kW>(to + (uint32_t)(mc * kN + hq * kW), o);
+#pragma unroll
+    for (int i = 0; i < kW; ++i)
+      if (hq * kW + i < heads) dst[(long long)i * kL + mc * 128] = o[i];
+  }
+}
+// a token that sees nothing
+__device__ __forceinline__ void store_nothing(const Params& p, long long row0, int heads,
+                                              int tid) {
+  for (int i = tid; i < heads * (kL / 8); i += 256)
+    *reinterpret_cast<uint4*>(p.out + row0 * kL + (long long)i * 8) = make_uint4(0u, 0u, 0u, 0u);
+  if (p.lse && tid < heads) p.lse[row0 + tid] = -INFINITY;
+}
+// whether the phase has completed, without waiting
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -386,7 +509,7 @@ __global__ void __launch_bounds__(512)
       }
     }
   }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const float inv = den == 0.f ? 0.f : p.o_scale / den;
   const long long row = (long long)token * p.Hm + head;
 #pragma unroll
   for (int q = 0; q < 2; ++q)
@@ -435,6 +558,12 @@ inline bool row_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t bo
 inline bool prefetch_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows,
                          bool codes) {
   return byte_map(m, base, rows, codes ? kL : 2 * kL, 256, box_rows, false);
+}
+
+inline int box_log_of(int page_size) {  // largest power of two that divides it, 128 at most
+  int log = 0;
+  while (log < 7 && page_size % (2 << log) == 0) ++log;
+  return log;
 }
 
 }  // namespace chunk

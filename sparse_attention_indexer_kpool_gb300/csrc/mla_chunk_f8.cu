@@ -1,0 +1,656 @@
+// The chunk attention over E4M3 pages on the 8-bit tensor-core products (bf16
+// activations, latent 512, page size a multiple of 8): the codes go to the tensor
+// cores as they are.
+//
+// Work, row tiles, key tiles, masks and the join are those of the bf16 kernel.  What
+// differs is where the precision comes from: an E4M3 code keeps its value, and the
+// other factor of each product is split into 8-bit parts whose sum it is.
+//   S^T = C (q_hi + q_lo)^T   E4M3 x E4M3.  A head's query row is scaled by a power of
+//     two to a largest magnitude in [128, 256); hi is the nearest E4M3 value, lo that
+//     of the rest.  A bf16 value has 8 significant bits, an E4M3 value 4, so hi + lo is
+//     the value itself down to 2^-9 of the scaled row (2^-17 of its largest element),
+//     and off by at most 2^-10 of it below.
+//   O^T += C^T (p_1 + p_2 + p_3)^T   E4M3 x E5M2.  A weight u = 2^(z - m) * row scale,
+//     times 2^8, is cut to 3 significant bits twice and its rest rounded: off by at
+//     most 2^-9 of itself (a bf16 weight: 2^-9 .. 2^-8), and by 2^-17 absolutely, that
+//     is 2^-25 of the reference's.  The sums keep the unrounded fp32 weights.
+// The reference m of a head is kept for u rather than for the bare weight, so that u
+// stays below 2^6 and its parts inside E5M2's range; a row scale counts there as at
+// least 2^-60, which bounds the bare weight as well.
+//
+// Why.  Widening the codes to bf16 in shared memory first took 1,960 cycles of
+// conversions and 2,000 of shared-memory traffic a tile and kept one tile at a time in
+// the 128 KB that its bf16 rows fill: 8,100 cycles a tile.  As codes a tile is 64 KB:
+// two are in flight, the softmax of one under the products of the other.  The parts
+// cost MMAs (80 steps a tile, K = 32, against 64 of K = 16 in bf16): 128 x 64 x 32 reads
+// 6 KB of shared memory for 32 cycles' work, as in the bf16 kernel, and that bounds it.
+#include "mla_chunk.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace chunk;
+
+constexpr int kKeys = 128;
+constexpr int kBlock = kKeys * 128;       // 128 rows x 128 codes, 16 KB
+constexpr int kStage = 4 * kBlock;        // a tile
+constexpr int kStages = 2;
+constexpr int kSoftThreads = 256;
+constexpr int kQueryWarps = 4, kTmaWarps = 2;
+constexpr int kThreads = kSoftThreads + 32 * (kQueryWarps + kTmaWarps + 1) + 32;  // (whole: 16)
+constexpr float kRaise8 = 6.f;            // base-2 growth of u that raises a reference
+constexpr float kUp = 256.f;              // weights in E5M2 are scaled by 2^8
+constexpr float kLeastLog = -60.f;
+
+struct Ctl {
+  float m[64], nm[64], alpha[64], l[64];  // per head; first: read as float4
+  float sq[3][64];                        // the query rows' scales, by segment
+  float red[4][64];
+  uint64_t full[kStages], empty[kStages], s_full[kStages], p_full, o_full, q_full, q_empty, drain;
+  Start start;
+  uint32_t tmem;
+  unsigned groups[kStages];               // TMA boxes of the tile that hold rows
+  int raise;
+  int soft_dead[2];
+  int dead;
+};
+
+template <int kN>
+struct Smem {
+  static constexpr int kQBlock = kN * 128;              // kN heads x 128 codes
+  static constexpr int kQPart = 4 * kQBlock;            // hi, lo
+  static constexpr int kPPart = kKeys * kN;             // a weight's part, 1 byte each
+  static constexpr size_t kKv = 0;
+  static constexpr size_t kQ = (size_t)kStages * kStage;
+  static constexpr size_t kP = kQ + 2 * (size_t)kQPart;
+  static constexpr size_t kCtl = kP + 3 * (size_t)kPPart;
+  static constexpr size_t kBytes = 1024 + kCtl + sizeof(Ctl);
+};
+static_assert(Smem<64>::kBytes <= 227 * 1024, "shared memory budget");
+
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, E4M3 A, E4M3 or E5M2 B.
+constexpr uint32_t idesc_f8(int m, int n, bool a_mn, bool b_e5m2, bool b_mn) {
+  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f8_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Shared-memory matrix descriptor, 32-byte swizzle: an atom is 8 rows of 32 bytes; the
+// 16-byte chunk c of row r is stored at chunk position c ^ ((r >> 2) & 1).
+__device__ __forceinline__ uint64_t umma_desc_sw32(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | ((uint64_t)1 << 46) | ((uint64_t)6 << 61);
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// the leading 3 significant bits (of a NaN: one)
+__device__ __forceinline__ float cut3(float x) {
+  return __uint_as_float(__float_as_uint(x) & 0xffe00000u);
+}
+
+template <int kN>
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_chunk_f8_kernel(const __grid_constant__ CUtensorMap kv_map,
+                        const __grid_constant__ CUtensorMap ahead_map,
+                        const __nv_bfloat16* __restrict__ q_lat, const Params p) {
+  using S = Smem<kN>;
+  constexpr int kW = kN / 2;  // heads per softmax thread
+  constexpr int kQuery0 = kSoftThreads / 32, kTma0 = kQuery0 + kQueryWarps,
+                kMmaWarp = kTma0 + kTmaWarps;
+  constexpr int kTmemCols = kN == 64 ? 512 : 256;  // S^T (2 kN), O^T (4 kN)
+  constexpr uint32_t kOCol = kStages * kN;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl& c = *reinterpret_cast<Ctl*>(sb + S::kCtl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hb = (p.Hm + kN - 1) / kN;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&c.full[i], kTmaWarps);
+      mbar_init(&c.empty[i], 1);
+      mbar_init(&c.s_full[i], 1);
+    }
+    mbar_init(&c.p_full, kSoftThreads / 32);
+    mbar_init(&c.o_full, 1);
+    mbar_init(&c.q_full, kQueryWarps);
+    mbar_init(&c.q_empty, 1);
+    mbar_init(&c.drain, 1);
+    fence_mbar_init();
+    c.soft_dead[0] = c.soft_dead[1] = c.dead = 0;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc<kTmemCols>(&c.tmem);
+    tc_fence_before();
+  }
+  if (tid < 64) {
+    c.m[tid] = -INFINITY;
+    c.nm[tid] = 0.f;
+  }
+  pdl_wait();  // every input may come from the kernel just before
+  pdl_launch_dependents();
+
+  const unsigned long long units = find_share<kKeys, false, kThreads>(
+      p, hb, blockIdx.x, gridDim.x, &c.start, blockIdx.x == 0);
+  const uint32_t tmem = c.tmem;
+  Walk<kKeys, false> w(p, hb, c.start, units);
+  // a failure drill loads nothing and issues no MMA: the first waits run out
+  const bool issue = p.drill == 0;
+  const unsigned long long wait_ns = p.drill ? kDrillWaitNs : kWaitNs;
+  volatile int* dead = &c.dead;
+
+  if (warp < kQuery0) {
+    // ================= softmax and epilogue =================
+    const int qw = warp & 3;      // TMEM lanes 32 qw ..: this thread's key row r
+    const int hq = warp >> 2;     // heads kW hq ..
+    const int r = qw * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16);
+    Header hd = {-1, -1, 0, 0};
+    int tiles = 0, segs = 0;
+    bool ok = true;
+    // this thread's row scale in a tile (0: not seen or no page)
+    auto scale_of = [&](const Keys<kKeys>& k, int b, int v) -> float {
+      const int t = k.at(v, r);
+      if (!k.sees(t)) return 0.f;
+      const int blk = t / p.kv.page_size;
+      if (blk >= p.kv.max_pages) return 0.f;
+      const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
+      if (page < 0 || page >= p.kv.n_pages) return 0.f;
+      return __ldg(p.kv.row_scale + (long long)page * p.kv.page_size + t % p.kv.page_size);
+    };
+    while (ok && w.next()) {
+      float l[kW];                // this row's sums
+      bool unset = true;          // some head here has no reference yet
+#pragma unroll
+      for (int i = 0; i < kW; ++i) l[i] = 0.f;
+      float rs = w.ta < w.tb ? scale_of(w.k, w.b, w.ta) : 0.f;
+      const float4* sq4 = reinterpret_cast<const float4*>(c.sq[segs % 3] + hq * kW);
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        const int st = tiles & 1;
+        const float rs_next = v + 1 < w.tb ? scale_of(w.k, w.b, v + 1) : 0.f;
+        const int t = w.k.at(v, r);
+        if (!wait_on(&c.s_full[st], (tiles >> 1) & 1, dead, wait_ns)) c.soft_dead[st] = 1;
+        __syncwarp();
+        tc_fence_after();
+        const bool valid = w.k.sees(t) && ((c.groups[st] >> (r >> w.k.log)) & 1u);
+        if (!valid) {  // the half of this row that this thread clears
+#pragma unroll 1
+          for (int blk = 2 * hq; blk < 2 * hq + 2; ++blk)
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch)  // (neighbouring rows in different banks)
+              *reinterpret_cast<uint4*>(sb + S::kKv + st * kStage + blk * kBlock + r * 128 +
+                                        ((ch ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        // (a hidden key's scale may be anything)
+        const float sc = valid ? rs : 0.f, zs = p.zscale * sc;
+        const float lg = fmaxf(log2f(fabsf(sc)), kLeastLog);  // in u's reference
+        const float high_at = kRaise8 - lg;
+        float e[kW];
+        // z = S * query scale * row scale * softmax scale
+        auto logits = [&]() {
+          tmem_ldw<kW>(tl + (uint32_t)(st * kN + hq * kW), e);
+#pragma unroll
+          for (int q = 0; q < kW / 4; ++q) {
+            const float4 s4 = sq4[q];
+            e[4 * q] *= s4.x;
+            e[4 * q + 1] *= s4.y;
+            e[4 * q + 2] *= s4.z;
+            e[4 * q + 3] *= s4.w;
+          }
+        };
+        logits();
+        bool high = unset;
+#pragma unroll
+        for (int q = 0; q < kW / 4; ++q) {  // minus the references (0: none yet)
+          const float4 nm = reinterpret_cast<const float4*>(c.nm + hq * kW)[q];
+          fma2(e[4 * q], e[4 * q + 1], zs, nm.x, nm.y);
+          fma2(e[4 * q + 2], e[4 * q + 3], zs, nm.z, nm.w);
+        }
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+          e[i] = valid ? e[i] : -INFINITY;
+          high |= e[i] > high_at;
+        }
+        // every thread takes the same branch; the flag of a failed wait was
+        // written before this barrier
+        const bool full = vote_soft(high);
+        if (c.soft_dead[st]) {
+          ok = false;
+          break;
+        }
+        if (full) {
+          logits();
+#pragma unroll
+          for (int i = 0; i < kW; ++i) e[i] = valid ? fmaf(e[i], zs, lg) : -INFINITY;
+          const float m = across_rows<kW, true>(e, lane);
+          if (lane < kW) c.red[qw][hq * kW + lane] = m;
+          if (tid == 0) c.raise = 0;
+          sync_soft();
+          if (tid < kN) {
+            const float tm = fmaxf(fmaxf(c.red[0][tid], c.red[1][tid]),
+                                   fmaxf(c.red[2][tid], c.red[3][tid]));
+            const float m_old = c.m[tid];
+            float a = 1.f;
+            if (m_old == -INFINITY) {
+              c.m[tid] = tm;  // nothing accumulated for this head yet
+            } else if (tm > m_old + kRaise8) {
+              c.m[tid] = tm;
+              a = ex2_fast(m_old - tm);
+              c.raise = 1;
+            }
+            c.alpha[tid] = a;
+            c.nm[tid] = c.m[tid] == -INFINITY ? 0.f : -c.m[tid];
+          }
+          sync_soft();
+          unset = false;
+#pragma unroll
+          for (int i = 0; i < kW; ++i) unset |= c.m[hq * kW + i] == -INFINITY;
+          logits();
+#pragma unroll
+          for (int i = 0; i < kW; ++i)
+            e[i] = valid ? fmaf(e[i], zs, c.nm[hq * kW + i]) : -INFINITY;
+        }
+        // P's place and O^T: the last tile's product is done with both
+        if (tiles > 0 &&
+            !wait_on(&c.empty[st ^ 1], ((tiles - 1) >> 1) & 1, dead, wait_ns))
+          c.soft_dead[st ^ 1] = 1;
+        __syncwarp();
+        if (full && c.raise) {
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < kW; ++i) l[i] *= c.alpha[hq * kW + i];
+          if (v > w.ta) {
+#pragma unroll 1
+            for (int mc = 0; mc < 4; ++mc) {
+              float o[kW];
+              const uint32_t ta = tl + kOCol + (uint32_t)(mc * kN + hq * kW);
+              tmem_ldw<kW>(ta, o);
+#pragma unroll
+              for (int i = 0; i < kW; ++i) o[i] *= c.alpha[hq * kW + i];
+              tmem_stw<kW>(ta, o);
+            }
+          }
+        }
+        const float up = sc * kUp;
+#pragma unroll
+        for (int q = 0; q < kW / 16; ++q) {  // 16 heads: 16 bytes of each part
+          uint32_t part[3][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float a[4], x[3][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float& ei = e[16 * q + 4 * j + i];
+              ei = ex2_fast(ei);
+              a[i] = ei * up;
+              x[0][i] = cut3(a[i]);
+              a[i] -= x[0][i];
+              x[1][i] = cut3(a[i]);
+              x[2][i] = a[i] - x[1][i];
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              part[k][j] = e5m2x2(x[k][0], x[k][1]) | (e5m2x2(x[k][2], x[k][3]) << 16);
+          }
+          const int ch = hq * (kW / 16) + q;
+          const int at = kN == 64 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)
+                                  : r * 32 + ((ch ^ ((r >> 2) & 1)) << 4);
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<uint4*>(sb + S::kP + k * S::kPPart + at) =
+                make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&c.p_full);
+#pragma unroll
+        for (int i = 0; i < kW; i += 2) add2(l[i], l[i + 1], e[i], e[i + 1]);
+        rs = rs_next;
+      }
+      if (!ok) break;
+      const bool some = w.tb > w.ta, whole = w.ta == 0 && w.tb == w.k.n;
+      const bool begins = some && w.ta == 0 && !whole;
+      if (begins) hd.start_tile = w.tile_id;
+      if (!whole && !begins && hd.cont_tile < 0) {
+        hd.cont_tile = w.tile_id;
+        hd.cont_some = some;
+        hd.cont_ends = w.tb == w.k.n;
+      }
+      if (!some && !whole) continue;
+      const int heads = min(kN, p.Hm - w.h0 * kN);
+      const long long row0 = (long long)w.token * p.Hm + w.h0 * kN;
+      if (!some) {
+        store_nothing(p, row0, heads, tid);
+        continue;
+      }
+      {
+        const float sum = across_rows<kW, false>(l, lane);
+        if (lane < kW) c.red[qw][hq * kW + lane] = sum;
+      }
+      if (!wait_on(&c.o_full, segs & 1, dead, wait_ns)) c.soft_dead[tiles & 1] = 1;
+      ++segs;
+      __syncwarp();
+      tc_fence_after();
+      sync_soft();
+      if (c.soft_dead[tiles & 1]) {
+        ok = false;
+        break;
+      }
+      if (tid < kN) {
+        const float sum = (c.red[0][tid] + c.red[1][tid]) + (c.red[2][tid] + c.red[3][tid]);
+        const float m = c.m[tid];
+        c.m[tid] = -INFINITY;
+        c.nm[tid] = 0.f;
+        if (whole) {
+          c.l[tid] = sum == 0.f ? 0.f : 1.f / (sum * kUp);  // a NaN sum stays one
+          if (p.lse && tid < heads)
+            p.lse[row0 + tid] = sum == 0.f ? -INFINITY : (m + log2f(sum)) / kLog2e;
+        } else {
+          const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
+          p.part_ml[slot * kN + tid] = make_float2(m, sum);
+        }
+      }
+      sync_soft();
+      if (whole)
+        store_rows<kN>(p, c.l, tl + kOCol, row0, heads, qw, hq, lane);
+      else
+        store_part<kN>(p, 2 * blockIdx.x + (begins ? 1 : 0), tl + kOCol, heads, qw, hq, lane);
+      tc_fence_before();  // O^T is read: the next segment's P releases it
+    }
+    if (!ok) hd = Header{-1, -1, 0, 0};
+    if (tid == 0 && p.head) p.head[blockIdx.x] = hd;
+  } else if (warp < kTma0) {
+    // ================= queries: two E4M3 parts of each head's row =================
+    // A row a warp and turn: 16 elements a lane.
+    const int wq = warp - kQuery0;
+    int segs = 0;
+    bool ok = issue;
+    while (ok && w.next()) {
+      if (w.ta == w.tb) continue;
+      const int heads = min(kN, p.Hm - w.h0 * kN);
+      const __nv_bfloat16* src = q_lat + ((long long)w.token * p.Hm + w.h0 * kN) * kL + lane * 16;
+      bool room = segs == 0;
+      for (int rr = wq; rr < kN; rr += kQueryWarps) {
+        uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (rr < heads) {
+          raw[0] = ld_stream_v4(src + (long long)rr * kL);
+          raw[1] = ld_stream_v4(src + (long long)rr * kL + 8);
+        }
+        const uint32_t u[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w,
+                               raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+        float x[16], top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[2 * i] = bf16lo(u[i]);
+          x[2 * i + 1] = bf16hi(u[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (fabsf(x[i]) < INFINITY) top = fmaxf(top, fabsf(x[i]));
+        top = warp_max(top);
+        // exponent of the largest magnitude: 2^ex <= top < 2^(ex + 1); the rows below
+        // 2^-100 count as such (their scaled elements are small, not the largest)
+        const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+        const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);    // 2^(7 - ex)
+        const float down = __uint_as_float((uint32_t)(127 + ex - 7) << 23);  // 2^(ex - 7)
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          hi[j] = lo[j] = 0u;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            // a NaN or an infinity becomes the NaN code: its head's logits are NaN
+            float a = x[4 * j + 2 * k] * up, b = x[4 * j + 2 * k + 1] * up;
+            a = fabsf(a) < INFINITY ? a : NAN;
+            b = fabsf(b) < INFINITY ? b : NAN;
+            const uint32_t h2 = e4m3x2(a, b) & 0xffffu;
+            const float2 f = from_e4m3x2(h2);
+            hi[j] |= h2 << (16 * k);
+            lo[j] |= (e4m3x2(a - f.x, b - f.y) & 0xffffu) << (16 * k);
+          }
+        }
+        if (!room) {  // the last segment's products with the queries are done
+          const bool got = wait_on(&c.q_empty, (segs - 1) & 1, dead, wait_ns);
+          ok = __all_sync(0xffffffffu, got);
+          if (!ok) break;
+          room = true;
+        }
+        unsigned char* dst = sb + S::kQ + (lane >> 3) * S::kQBlock + rr * 128 +
+                             (((lane & 7) ^ (rr & 7)) << 4);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + S::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (lane == 0) c.sq[segs % 3][rr] = down;
+      }
+      if (!ok) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&c.q_full);
+      ++segs;
+    }
+  } else if (warp < kMmaWarp) {
+    // ================= TMA: two warps, two blocks of 128 codes each =================
+    const int team = warp - kTma0;
+    const int R = 1 << p.box_log, ng = kKeys >> p.box_log;
+    int tiles = 0;
+    bool ok = issue, armed = false;
+    // the cache row of this lane's box of a tile (-1: nothing seen, -2: no page)
+    auto box_row = [&](const Keys<kKeys>& k, int b, int v) -> int {
+      if (lane >= ng) return -1;
+      const int t0 = k.at(v, lane * R);
+      if (t0 > k.pos) return -1;
+      const int blk = t0 / p.kv.page_size;
+      if (blk >= p.kv.max_pages) return -2;
+      const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
+      if (page < 0 || page >= p.kv.n_pages) return -2;
+      return page * p.kv.page_size + t0 % p.kv.page_size;
+    };
+    while (ok && w.next()) {
+      if (w.ta == w.tb) continue;
+      int row = box_row(w.k, w.b, w.ta);
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        const int row_next = v + 1 < w.tb ? box_row(w.k, w.b, v + 1) : -1;
+        if (row == -2) {
+          flag(p.status, DSA_DEV_BAD_PAGE);
+          row = -1;
+        }
+        const unsigned boxes = __ballot_sync(0xffffffffu, row >= 0);
+        const int st = tiles & 1;
+        const bool room = tiles < kStages ||
+                          wait_on(&c.empty[st], ((tiles >> 1) - 1) & 1, dead, wait_ns);
+        ok = __all_sync(0xffffffffu, room);
+        if (!ok) break;
+        if (lane == 0) {
+          if (team == 0) c.groups[st] = boxes;
+          mbar_arrive_expect_tx(&c.full[st], __popc(boxes) * R * 256);
+        }
+        armed = true;
+        __syncwarp();
+        if (row >= 0) {
+          unsigned char* dst = sb + S::kKv + st * kStage + 2 * team * kBlock + lane * R * 128;
+          tma_load_2d(dst, &kv_map, team * 128, row, &c.full[st]);
+          tma_load_2d(dst + kBlock, &kv_map, team * 128 + 64, row, &c.full[st]);
+        }
+        // the tile after the next to L2 would come too early: the next one's rows
+        if (p.prefetch && team == 0 && row_next >= 0) tma_prefetch_2d(&ahead_map, 0, row_next);
+        row = row_next;
+      }
+    }
+    // after a give-up: no copy into this CTA's memory may be in flight at its end
+    if (*dead && lane == 0 && armed)
+      for (int i = 1; i <= kStages; ++i)
+        if (tiles - i >= 0)
+          mbar_wait_bounded(&c.full[(tiles - i) & 1], ((tiles - i) >> 1) & 1);
+  } else if (warp == kMmaWarp && issue) {
+    // ================= MMA =================
+    constexpr uint32_t id_s = idesc_f8(kKeys, kN, false, false, false);
+    constexpr uint32_t id_o = idesc_f8(128, kN, true, true, true);
+    const uint32_t kvb = smem_u32(sb + S::kKv), qb = smem_u32(sb + S::kQ);
+    const uint32_t pb = smem_u32(sb + S::kP);
+    // (a descriptor's low bits are the address in 16-byte units: steps add constants)
+    const uint64_t d_k0 = sw128_desc(kvb), d_q = sw128_desc(qb);
+    const uint64_t d_v0 = umma_desc_sw128(kvb, kBlock, 1024);
+    const uint64_t d_p = kN == 64 ? umma_desc_sw64(pb, S::kPPart, 512)
+                                  : umma_desc_sw32(pb, S::kPPart, 256);
+    // Two streams over the same tiles: scores as soon as a stage holds keys, outputs as
+    // soon as a tile's weights are there; outputs first (they free the stage).
+    Walk<kKeys, false> wo(p, hb, c.start, units);
+    auto segment = [](Walk<kKeys, false>& x) {
+      while (x.next())
+        if (x.tb > x.ta) return true;
+      return false;
+    };
+    auto ready = [](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0;
+    };
+    bool ok = true, left_s = segment(w), left_o = segment(wo), have_q = false;
+    int ns = 0, no = 0, vs = w.ta, vo = wo.ta, seg = 0;
+    unsigned long long since = 0;  // time of the first idle look
+    while (left_o) {
+      if (no < ns && ready(&c.p_full, no & 1)) {
+        const uint64_t d_v = d_v0 + (uint32_t)((no & 1) * (kStage >> 4));
+        const uint32_t more = vo > wo.ta ? 1u : 0u;
+        tc_fence_after();
+#pragma unroll
+        for (int mc = 0; mc < 4; ++mc)
+#pragma unroll
+          for (int kr = 0; kr < 4; ++kr)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              umma_f8_elect(tmem + kOCol + mc * kN, d_v + ((mc * kBlock + kr * 4096) >> 4),
+                            d_p + ((k * S::kPPart + kr * 32 * kN) >> 4), id_o,
+                            (kr | k) ? 1u : more);
+        umma_commit_elect(&c.empty[no & 1]);
+        ++no;
+        if (++vo == wo.tb) {
+          umma_commit_elect(&c.o_full);
+          left_o = segment(wo);
+          vo = wo.ta;
+        }
+        since = 0;
+        continue;
+      }
+      if (left_s && ns - no < kStages) {
+        have_q = have_q || ready(&c.q_full, seg & 1);
+        // (the stage's keys imply that its last outputs are done: its scores are free)
+        if (have_q && ready(&c.full[ns & 1], (ns >> 1) & 1)) {
+          const uint64_t d_k = d_k0 + (uint32_t)((ns & 1) * (kStage >> 4));
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t blk = j >> 2, off = (j & 3) * 32;
+              umma_f8_elect(tmem + (ns & 1) * kN, d_k + ((blk * kBlock + off) >> 4),
+                            d_q + ((k * S::kQPart + blk * S::kQBlock + off) >> 4), id_s,
+                            (k | j) ? 1u : 0u);
+            }
+          umma_commit_elect(&c.s_full[ns & 1]);
+          ++ns;
+          if (++vs == w.tb) {
+            umma_commit_elect(&c.q_empty);
+            ++seg;
+            left_s = segment(w);
+            vs = w.ta;
+            have_q = false;
+          }
+          since = 0;
+          continue;
+        }
+      }
+      const unsigned long long now = global_ns();
+      if (since == 0) since = now;
+      const bool late = now - since > wait_ns;
+      if (late) *dead = 1;
+      if (__any_sync(0xffffffffu, late || *dead)) {
+        ok = false;
+        break;
+      }
+    }
+    if (!ok) {  // drain what was issued before the CTA's memory is given back
+      umma_commit_elect(&c.drain);
+      mbar_wait_bounded(&c.drain, 0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && c.dead) flag(p.status, DSA_DEV_TIMEOUT);  // outputs unspecified
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc<kTmemCols>(tmem);
+  }
+}
+
+template <int kN>
+int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
+  const int n_cta = num_sms();
+  Params p = {};
+  p.kv = a.kv;
+  p.cu_new = a.cu_new;
+  p.T = a.T;
+  p.B = a.B;
+  p.Hm = a.Hm;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.zscale = a.sm_scale * kLog2e;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.status = a.status;
+  p.drill = failure_drill();
+  p.prefetch = a.T <= 4 * a.B;
+  p.box_log = box_log_of(a.kv.page_size);
+  p.o_scale = 1.f / kUp;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)n_cta * 2 * kN * kL);
+  p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)n_cta * 2 * kN);
+  CUtensorMap kv_map, ahead_map;
+  const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.page_size;
+  if (!row_map(&kv_map, a.kv.pages, rows, 1u << p.box_log, true) ||
+      !prefetch_map(&ahead_map, a.kv.pages, rows, 1u << p.box_log, true))
+    return DSA_ERR_CUDA;
+  auto kernel = mla_chunk_f8_kernel<kN>;
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_smem(kernel, Smem<kN>::kBytes, done)) return DSA_ERR_CUDA;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(n_cta, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Smem<kN>::kBytes;
+  if (launch_kernel(&cfg, kernel, kv_map, ahead_map, static_cast<const __nv_bfloat16*>(a.q_lat),
+                    p) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  cfg.gridDim = dim3(n_cta, kN / 8, 1);
+  cfg.blockDim = dim3(512, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return launch_kernel(&cfg, mla_chunk_join_kernel<kN, false>, p, n_cta) == cudaSuccess
+             ? DSA_OK
+             : DSA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_mla_chunk_f8(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
+  return a.Hm <= 32 ? launch<32>(a, workspace, stream) : launch<64>(a, workspace, stream);
+}
+
+}  // namespace dsa

@@ -122,17 +122,6 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
-// whether the phase has completed, without waiting
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // a barrier of a team's warps: whether any of their threads says so
 __device__ __forceinline__ bool vote_team(int team, bool v) {
   uint32_t r;
@@ -928,6 +917,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.lse = a.lse;
   p.status = a.status;
   p.drill = failure_drill();
+  p.o_scale = 1.f;
   p.prefetch = a.T <= 4 * a.B;
   p.box_log = 3;
   p.part_o = static_cast<float*>(workspace);

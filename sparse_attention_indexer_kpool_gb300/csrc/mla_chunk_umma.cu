@@ -45,25 +45,14 @@ constexpr int kKeys = 128;
 constexpr int kKvBlock = kKeys * 128;  // 128 rows x 64 latent columns, 16 KB
 constexpr int kSoftThreads = 256;      // warps 0..7
 
-// Row sources: TMA boxes of bf16 rows or of E4M3 codes, which two teams of four warps
-// then widen in place (page size a multiple of 8); or, for any page size, four warps
-// that copy bf16 rows or widen E4M3 rows from global memory.
-constexpr int kSrcTma = 0, kSrcCopy = 1, kSrcCopy8 = 2, kSrcTma8 = 3;
-__host__ __device__ constexpr bool is_tma(int src) { return src == kSrcTma || src == kSrcTma8; }
-__host__ __device__ constexpr bool is_e4m3(int src) { return src == kSrcCopy8 || src == kSrcTma8; }
-// warps 8..: the row warps, then the TMA warps, then the MMA warp
-__host__ __device__ constexpr int row_warps(int src) {
-  return src == kSrcTma ? 0 : (src == kSrcTma8 ? 8 : 4);
-}
-__host__ __device__ constexpr int tma_warps(int src) { return is_tma(src) ? 2 : 0; }
-// (kSrcTma8: five whole warpgroups, which share the registers out anew)
+// Row sources: TMA boxes of bf16 rows (page size a multiple of 8); or, for any page
+// size, four warps that copy bf16 rows or widen E4M3 rows from global memory.
+constexpr int kSrcTma = 0, kSrcCopy = 1, kSrcCopy8 = 2;
+// warps 8..: two TMA warps or four row warps, then the MMA warp
+__host__ __device__ constexpr int load_warps(int src) { return src == kSrcTma ? 2 : 4; }
 __host__ __device__ constexpr int cta_threads(int src) {
-  return src == kSrcTma8 ? 640 : kSoftThreads + 32 * (tma_warps(src) + row_warps(src) + 1);
+  return kSoftThreads + 32 * (load_warps(src) + 1);
 }
-// kSrcTma8: 640 threads launch with 96 registers each (61,440); the softmax's two
-// warpgroups take 128, the other three keep 72: 60,416 in all.
-constexpr int kSoftRegs = 128, kRestRegs = 72;
-static_assert(2 * 128 * kSoftRegs + 3 * 128 * kRestRegs <= 640 * 96, "register split");
 
 struct Ctl {
   float m[64], nm[64], alpha[64], l[64];  // per head; first: read as float4
@@ -71,7 +60,7 @@ struct Ctl {
   float rs[kKeys];
   int valid[kKeys];               // copied rows: the position is seen and has a page
   int prow[2][kKeys];
-  uint64_t full[4], empty[4], raw[4], s_full, p_full, o_full, q_full, q_empty, drain;
+  uint64_t full[4], empty[4], s_full, p_full, o_full, q_full, q_empty, drain;
   Start start;
   uint32_t tmem;
   unsigned groups;                // TMA boxes of the tile that hold rows
@@ -93,76 +82,14 @@ struct Smem {
 static_assert(Smem<64>::kBytes <= 227 * 1024, "shared memory budget");
 
 // ---- small pieces ------------------------------------------------------------
-// kW values per lane (one row, kW heads) reduced over the warp's 32 rows by
-// halving exchanges; lane l ends with head l mod kW.
-template <int kW, bool kMax>
-__device__ __forceinline__ float across_rows(float (&v)[kW], int lane) {
-  if (kW == 16) {
-#pragma unroll
-    for (int i = 0; i < kW; ++i) {
-      const float o = __shfl_xor_sync(0xffffffffu, v[i], 16);
-      v[i] = kMax ? fmaxf(v[i], o) : v[i] + o;
-    }
-  }
-#pragma unroll
-  for (int s = kW / 2; s >= 1; s >>= 1) {
-    const bool upper = (lane & s) != 0;
-#pragma unroll
-    for (int i = 0; i < s; ++i) {
-      const float send = upper ? v[i] : v[i + s];
-      const float keep = upper ? v[i + s] : v[i];
-      const float recv = __shfl_xor_sync(0xffffffffu, send, s);
-      v[i] = kMax ? fmaxf(keep, recv) : keep + recv;
-    }
-  }
-  return v[0];
-}
-
-template <int kW>
-__device__ __forceinline__ void tmem_ldw(uint32_t ta, float (&v)[kW]) {
-  if constexpr (kW == 32) tmem_ld32(ta, v); else tmem_ld16(ta, v);
-}
-// Store 16 consecutive fp32 columns of the warp's 32 TMEM lanes.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
-      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
-      "r"(__float_as_uint(v[15]))
-      : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-template <int kW>
-__device__ __forceinline__ void tmem_stw(uint32_t ta, const float (&v)[kW]) {
-  if constexpr (kW == 32) tmem_st32(ta, v); else tmem_st16(ta, v);
-}
-
-// Barriers of one role's threads (barrier 0 is the CTA's).
-__device__ __forceinline__ void sync_soft() {
-  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
-}
-__device__ __forceinline__ bool vote_soft(bool v) {  // whether any of them says so
+// whether any thread of the four row warps says so
+__device__ __forceinline__ bool vote_rows(bool v) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-      " barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      " barrier.cta.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)v), "n"(kSoftThreads)
-      : "memory");
-  return r != 0;
-}
-// whether any thread of a team of four row warps says so
-__device__ __forceinline__ bool vote_rows(int team, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n"
-      " barrier.cta.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"(2 + team), "r"((uint32_t)v)
+      : "r"((uint32_t)v)
       : "memory");
   return r != 0;
 }
@@ -178,8 +105,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
                      const __grid_constant__ CUtensorMap ahead_map, const Params p) {
   using S = Smem<kN>;
   constexpr int kW = kN / 2;  // heads per softmax thread
-  constexpr int kRow0 = kSoftThreads / 32, kTmaWarp = kRow0 + row_warps(kSrc),
-                kMmaWarp = kTmaWarp + tma_warps(kSrc);
+  constexpr int kLoad0 = kSoftThreads / 32, kMmaWarp = kLoad0 + load_warps(kSrc);
   constexpr int kTmemCols = kN == 64 ? 512 : 256;  // S^T (kN), O^T (4 kN)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -190,7 +116,6 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(&c.full[i], kSrc == kSrcTma ? 1 : 4);
-      mbar_init(&c.raw[i], 1);
       mbar_init(&c.empty[i], 1);
     }
     mbar_init(&c.s_full, 1);
@@ -224,13 +149,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
   const uint32_t pb = smem_u32(sb + S::kP);
   volatile int* dead = &c.dead;
 
-  if constexpr (kSrc == kSrcTma8) {
-    if (warp < kRow0)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
-  }
-  if (warp < kRow0) {
+  if (warp < kLoad0) {
     // ================= softmax and epilogue =================
     const int qw = warp & 3;      // TMEM lanes 32 qw ..: this thread's key row r
     const int hq = warp >> 2;     // heads kW hq ..
@@ -252,7 +171,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         tmem_ldw<kW>(tl + hq * kW, e);
         bool valid;
         float rs = 1.f;
-        if constexpr (is_tma(kSrc)) {
+        if constexpr (kSrc == kSrcTma) {
           valid = w.k.sees(t) && ((c.groups >> (r >> w.k.log)) & 1u);
           if (!valid) {  // the half of this row that this thread clears
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -266,8 +185,8 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         } else {
           valid = c.valid[r] != 0;
         }
-        if constexpr (is_e4m3(kSrc)) rs = valid ? c.rs[r] : 0.f;
-        const float zs = is_e4m3(kSrc) ? p.zscale * rs : p.zscale;
+        if constexpr (kSrc == kSrcCopy8) rs = valid ? c.rs[r] : 0.f;
+        const float zs = (kSrc == kSrcCopy8) ? p.zscale * rs : p.zscale;
         bool high = unset;
 #pragma unroll
         for (int q = 0; q < kW / 4; ++q) {  // minus the references (0: none yet)
@@ -339,7 +258,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         // weights.  An E4M3 row's scale goes to its weights, so the tile holds codes.
 #pragma unroll
         for (int q = 0; q < kW / 8; ++q) {
-          const float sc = is_e4m3(kSrc) ? rs : 1.f;
+          const float sc = (kSrc == kSrcCopy8) ? rs : 1.f;
           const uint4 pk4 = make_uint4(pack_bf16(e[8 * q] * sc, e[8 * q + 1] * sc),
                                  pack_bf16(e[8 * q + 2] * sc, e[8 * q + 3] * sc),
                                  pack_bf16(e[8 * q + 4] * sc, e[8 * q + 5] * sc),
@@ -369,10 +288,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       const int heads = min(kN, p.Hm - w.h0 * kN);
       const long long row0 = (long long)w.token * p.Hm + w.h0 * kN;
       if (!some) {  // a token that sees nothing
-        for (int i = tid; i < heads * (kL / 8); i += kSoftThreads)
-          *reinterpret_cast<uint4*>(p.out + row0 * kL + (long long)i * 8) =
-              make_uint4(0u, 0u, 0u, 0u);
-        if (p.lse && tid < heads) p.lse[row0 + tid] = -INFINITY;
+        store_nothing(p, row0, heads, tid);
         continue;
       }
       {
@@ -402,52 +318,20 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         }
       }
       sync_soft();
-      if (whole) {
-        // a lane pair holds two latent columns of every head: each lane of the pair
-        // stores both columns of one of two heads
-        float inv[kW];
-#pragma unroll
-        for (int i = 0; i < kW; ++i) inv[i] = c.l[hq * kW + i];
-        const bool upper = lane & 1;
-#pragma unroll 1
-        for (int mc = 0; mc < 4; ++mc) {
-          float o[kW];
-          tmem_ldw<kW>(tl + (uint32_t)(kN + mc * kN + hq * kW), o);
-          __nv_bfloat16* dst =
-              p.out + (row0 + hq * kW + (upper ? 1 : 0)) * kL + mc * 128 + qw * 32 + (lane & ~1);
-#pragma unroll
-          for (int i = 0; i < kW; i += 2) {
-            const float a = o[i] * inv[i], b = o[i + 1] * inv[i + 1];
-            const float got = __shfl_xor_sync(0xffffffffu, upper ? a : b, 1);
-            if (hq * kW + i + (upper ? 1 : 0) < heads)
-              *reinterpret_cast<uint32_t*>(dst + (long long)i * kL) =
-                  upper ? pack_bf16(got, b) : pack_bf16(a, got);
-          }
-        }
-      } else {
-        float* dst = p.part_o +
-                     ((long long)(2 * blockIdx.x + (begins ? 1 : 0)) * kN + hq * kW) * kL +
-                     qw * 32 + lane;
-#pragma unroll 1
-        for (int mc = 0; mc < 4; ++mc) {
-          float o[kW];
-          tmem_ldw<kW>(tl + (uint32_t)(kN + mc * kN + hq * kW), o);
-#pragma unroll
-          for (int i = 0; i < kW; ++i)
-            if (hq * kW + i < heads) dst[(long long)i * kL + mc * 128] = o[i];
-        }
-      }
+      if (whole)
+        store_rows<kN>(p, c.l, tl + kN, row0, heads, qw, hq, lane);
+      else
+        store_part<kN>(p, 2 * blockIdx.x + (begins ? 1 : 0), tl + kN, heads, qw, hq, lane);
       tc_fence_before();  // O^T is read: the next segment's P releases it
     }
     if (!ok) hd = Header{-1, -1, 0, 0};
     if (tid == 0 && p.head) p.head[blockIdx.x] = hd;
-  } else if (is_tma(kSrc) && warp >= kTmaWarp && warp < kMmaWarp) {
+  } else if (kSrc == kSrcTma && warp < kMmaWarp) {
     // ================= TMA =================
     // Two warps take the chunks in turn: a copy costs the issuing warp 100 cycles and
     // more (16-row boxes: 1,340 a chunk, four times what its part of O^T takes).
-    const int team = warp - kTmaWarp;
+    const int team = warp - kLoad0;
     const int R = 1 << p.box_log, ng = kKeys >> p.box_log;
-    uint64_t* land = kSrc == kSrcTma ? c.full : c.raw;
     int tiles = 0, segs = 0;
     bool ok = issue;
     int issued = 0;  // chunks of tile `tiles` under way, up to this one
@@ -484,7 +368,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
           row = -1;
         }
         const unsigned boxes = __ballot_sync(0xffffffffu, row >= 0);
-        const uint32_t bytes = __popc(boxes) * R * (kSrc == kSrcTma ? 256 : 128);
+        const uint32_t bytes = __popc(boxes) * R * 256;
 #pragma unroll 1
         for (int mc = team; mc < 4; mc += 2) {
           const bool room = tiles == 0 || wait_on(&c.empty[mc], (tiles - 1) & 1, dead, wait_ns);
@@ -492,21 +376,20 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
           if (!ok) break;
           if (lane == 0) {
             if (mc == 0) c.groups = boxes;  // the last tile's softmax has read its own
-            mbar_arrive_expect_tx(&land[mc], bytes);
+            mbar_arrive_expect_tx(&c.full[mc], bytes);
           }
           issued = mc + 1;
           __syncwarp();
           if (row >= 0) {
             unsigned char* dst = sb + S::kKv + 2 * mc * kKvBlock + lane * R * 128;
-            tma_load_2d(dst, &kv_map, mc * (kSrc == kSrcTma ? 128 : 64), row, &land[mc]);
-            if (kSrc == kSrcTma)
-              tma_load_2d(dst + kKvBlock, &kv_map, mc * 128 + 64, row, &land[mc]);
+            tma_load_2d(dst, &kv_map, mc * 128, row, &c.full[mc]);
+            tma_load_2d(dst + kKvBlock, &kv_map, mc * 128 + 64, row, &c.full[mc]);
           }
         }
         if (!ok) break;
         issued = 0;
-        // the next tile's rows to L2 (bf16: half of a row each)
-        if (p.prefetch && row_next >= 0 && (kSrc == kSrcTma || team == 0))
+        // the next tile's rows to L2, half of a row each
+        if (p.prefetch && row_next >= 0)
           tma_prefetch_2d(&ahead_map, team * 256, row_next);
         row = row_next;
       }
@@ -515,77 +398,15 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
     if (*dead && lane == 0) {
       for (int mc = team; mc < 4; mc += 2)
         if (mc < issued || tiles > 0)
-          mbar_wait_bounded(&land[mc], (mc < issued ? tiles : tiles - 1) & 1);
+          mbar_wait_bounded(&c.full[mc], (mc < issued ? tiles : tiles - 1) & 1);
       if (segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
     }
-  } else if (warp < kRow0 + row_warps(kSrc)) {
+  } else if (warp < kMmaWarp) {
     // ================= rows =================
     int tiles = 0, segs = 0;
     bool ok = issue;
-    const int lt = (tid - 32 * kRow0) & 127;  // its row of every tile
-    if constexpr (kSrc == kSrcTma8) {
-      // Widen a chunk of codes in place: 128 rows of 128 codes (swizzled like the
-      // bf16 rows) land in its first block, every thread takes 8 of their 16-byte
-      // pieces into registers, and once all have, both blocks take the bf16 rows.
-      // Eight lanes hold one piece of eight rows, so that neither the reads nor the
-      // writes of a quarter warp meet in a bank.  Two teams take the chunks in turn: a
-      // chunk's steps (its landing, the codes to registers, widening, the fence before
-      // the tensor cores' reads: 1,400 cycles) wait more than they work.
-      const int team = (warp - kRow0) >> 2;
-      const int r8 = lane & 7, unit0 = (lt >> 5) * 32 + (lane >> 3);
-      auto scale_of = [&](const Keys<kKeys>& k, int b, int v) -> float {
-        const int t = k.at(v, lt);
-        if (!k.sees(t)) return 0.f;
-        const int blk = t / p.kv.page_size;
-        if (blk >= p.kv.max_pages) return 0.f;
-        const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
-        if (page < 0 || page >= p.kv.n_pages) return 0.f;
-        return __ldg(p.kv.row_scale + (long long)page * p.kv.page_size + t % p.kv.page_size);
-      };
-      while (ok && w.next()) {
-        float rs = w.ta < w.tb ? scale_of(w.k, w.b, w.ta) : 0.f;
-        for (int v = w.ta; v < w.tb; ++v, ++tiles) {
-          const float rs_next = v + 1 < w.tb ? scale_of(w.k, w.b, v + 1) : 0.f;
-#pragma unroll 1
-          for (int mc = team; mc < 4; mc += 2) {
-            // (the codes' landing implies that the chunk was free)
-            ok = ok && wait_on(&c.raw[mc], tiles & 1, dead, wait_ns);
-            unsigned char* dst = sb + S::kKv + 2 * mc * kKvBlock;
-            uint4 raw[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              raw[u] = *reinterpret_cast<const uint4*>(
-                  dst + ((unit0 + 4 * u) >> 3) * 1024 + r8 * 128 +
-                  ((((unit0 + 4 * u) & 7) ^ r8) << 4));
-            if (vote_rows(team, !ok)) {  // every thread leaves at the same chunk
-              ok = false;
-              break;
-            }
-            if (mc == 0) c.rs[lt] = rs;  // the last tile's softmax has read its own
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int rr = ((unit0 + 4 * u) >> 3) * 8 + r8, pc = (unit0 + 4 * u) & 7;
-              const uint32_t x[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const int ch = 2 * pc + hf;
-                *reinterpret_cast<uint4*>(dst + (ch >> 3) * kKvBlock + rr * 128 +
-                                          (((ch & 7) ^ r8) << 4)) =
-                    make_uint4(e4m3x2_to_bf16x2(x[2 * hf] & 0xffffu),
-                               e4m3x2_to_bf16x2(x[2 * hf] >> 16),
-                               e4m3x2_to_bf16x2(x[2 * hf + 1] & 0xffffu),
-                               e4m3x2_to_bf16x2(x[2 * hf + 1] >> 16));
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive1(&c.full[mc]);
-          }
-          if (!ok) break;
-          rs = rs_next;
-        }
-      }
-    } else {
+    const int lt = tid - kSoftThreads;  // 0..127: its row of every tile
+    {
       // the cache row of position t (-1: not seen or no page)
       auto row_of = [&](const Keys<kKeys>& k, int b, int t) -> int {
         if (t > k.pos) return -1;  // (single positions: none but visible ones)
@@ -680,16 +501,16 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
           }
           // after a give-up every thread leaves at the same tile (nobody waits for
           // the others in sync_load)
-          if (vote_rows(0, !ok)) {
+          if (vote_rows(!ok)) {
             ok = false;
             break;
           }
         }
-        ok = !vote_rows(0, !ok);
+        ok = !vote_rows(!ok);
       }
       if (*dead && lt == 0 && segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
     }
-  } else if (warp == kMmaWarp && issue) {
+  } else if (issue) {
     // ================= MMA =================
     // The whole warp runs the loop and one elected lane issues: the descriptors
     // stay in uniform registers (one lane alone: 73 instead of 51 cycles a step).
@@ -757,12 +578,6 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
   }
 }
 
-int box_log_of(int page_size) {  // largest power of two that divides it, 128 at most
-  int log = 0;
-  while (log < 7 && page_size % (2 << log) == 0) ++log;
-  return log;
-}
-
 template <int kN>
 size_t workspace_bytes(int n_cta) {
   return (size_t)n_cta * 2 * kN * (kL * 4 + 8) + (size_t)n_cta * sizeof(Header);
@@ -784,10 +599,11 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.lse = a.lse;
   p.status = a.status;
   p.drill = failure_drill();
+  p.o_scale = 1.f;
   // rows that few tokens share come from HBM: the tile after the next is brought
   // into L2 meanwhile
   p.prefetch = a.T <= 4 * a.B;
-  p.box_log = is_tma(kSrc) ? box_log_of(a.kv.page_size) : 0;
+  p.box_log = kSrc == kSrcTma ? box_log_of(a.kv.page_size) : 0;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)n_cta * 2 * kN * kL);
   p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)n_cta * 2 * kN);
@@ -795,10 +611,9 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   if (!row_map(&q_map, a.q_lat, (uint64_t)a.T * a.Hm, kN)) return DSA_ERR_CUDA;
   kv_map = ahead_map = q_map;
   const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.page_size;
-  if (is_tma(kSrc) &&
-      (!row_map(&kv_map, a.kv.pages, rows, 1u << p.box_log, kSrc == kSrcTma8) ||
-       (p.prefetch &&
-        !prefetch_map(&ahead_map, a.kv.pages, rows, 1u << p.box_log, kSrc == kSrcTma8))))
+  if (kSrc == kSrcTma &&
+      (!row_map(&kv_map, a.kv.pages, rows, 1u << p.box_log) ||
+       (p.prefetch && !prefetch_map(&ahead_map, a.kv.pages, rows, 1u << p.box_log, false))))
     return DSA_ERR_CUDA;
   auto kernel = mla_chunk_kernel<kN, kSrc>;
   static std::atomic<unsigned long long> done{0};
@@ -823,12 +638,9 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
 
 template <int kN>
 int launch_src(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
-  const bool codes = a.kv.kv_dtype == DSA_FP8_E4M3;
-  if (a.kv.page_size % 8 == 0)
-    return codes ? launch<kN, kSrcTma8>(a, workspace, stream)
-                 : launch<kN, kSrcTma>(a, workspace, stream);
-  return codes ? launch<kN, kSrcCopy8>(a, workspace, stream)
-               : launch<kN, kSrcCopy>(a, workspace, stream);
+  if (a.kv.kv_dtype == DSA_FP8_E4M3) return launch<kN, kSrcCopy8>(a, workspace, stream);
+  return a.kv.page_size % 8 == 0 ? launch<kN, kSrcTma>(a, workspace, stream)
+                                 : launch<kN, kSrcCopy>(a, workspace, stream);
 }
 
 }  // namespace
