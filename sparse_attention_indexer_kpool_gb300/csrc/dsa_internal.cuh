@@ -380,6 +380,7 @@ bool mla_chunk_umma_ok(int L, int dtype, int kv_dtype);
 size_t mla_chunk_umma_workspace_size(int Hm);
 int launch_mla_chunk_umma(const ChunkArgs& a, void* workspace, cudaStream_t stream);
 // the same over E4M3 pages of a multiple of 8 rows, on the 8-bit products
+size_t mla_chunk_f8_workspace_size(int T, int Hm);
 int launch_mla_chunk_f8(const ChunkArgs& a, void* workspace, cudaStream_t stream);
 // the same on pairs of CTAs: two tokens' rows share every key row
 bool mla_chunk_pair_ok(int T, int B, int Hm, int page_size);

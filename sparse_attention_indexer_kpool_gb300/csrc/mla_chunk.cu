@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
 size_t mla_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype) {
   if (T < 1 || !mla_chunk_umma_ok(L, dtype, kv_dtype)) return 0;
   const size_t one = mla_chunk_umma_workspace_size(Hm);
-  const size_t two = Hm > 32 ? mla_chunk_pair_workspace_size() : 0;
+  const size_t two = kv_dtype == DSA_FP8_E4M3 ? mla_chunk_f8_workspace_size(T, Hm)
+                                              : (Hm > 32 ? mla_chunk_pair_workspace_size() : 0);
   return one > two ? one : two;
 }
 

@@ -40,10 +40,12 @@ struct Params {
   int drill, prefetch;
   int box_log;               // positions of a box, 2^box_log (copied rows: 1)
   float o_scale;             // of the partials' output against their sums
+  int extra;                 // what a row tile costs beside its key tiles, in units
 };
 
 // ---- the batch as units ------------------------------------------------------
-// A unit is one key tile of kT positions for one row tile.  kPair: a row tile is two
+// A unit is one key tile of kT positions for one row tile; its queries, its first
+// tile's wait and its end count as Params::extra more.  kPair: a row tile is two
 // tokens and a block of 64 heads, or one token and two such blocks (Hm > 64);
 // otherwise one token and a block of heads.
 struct Seq {
@@ -64,7 +66,7 @@ __device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p
         ((p.sinks + R - 1) / R + (p.window + (kPair ? 1 : 0) + R - 2) / R + 1) * R;
     if ((keys + kT - 1) / kT < (long long)s.u) s.u = (unsigned)((keys + kT - 1) / kT);
   }
-  s.u = max(s.u, 1u);
+  s.u = max(s.u, 1u) + (unsigned)p.extra;
   return s;
 }
 

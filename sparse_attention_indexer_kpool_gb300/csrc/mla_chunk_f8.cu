@@ -12,8 +12,9 @@
 //     and off by at most 2^-10 of it below.
 //   O^T += C^T (p_1 + p_2 + p_3)^T   E4M3 x E5M2.  A weight u = 2^(z - m) * row scale,
 //     times 2^8, is cut to 3 significant bits twice and its rest rounded: off by at
-//     most 2^-9 of itself (a bf16 weight: 2^-9 .. 2^-8), and by 2^-17 absolutely, that
-//     is 2^-25 of the reference's.  The sums keep the unrounded fp32 weights.
+//     most 2^-9 of itself (a bf16 weight: up to 2^-8), and, where a part falls below
+//     E5M2's least normal value, by 2^-17 a part, 2^-23 of a weight at the reference in
+//     all.  The sums keep the unrounded fp32 weights.
 // The reference m of a head is kept for u rather than for the bare weight, so that u
 // stays below 2^6 and its parts inside E5M2's range; a row scale counts there as at
 // least 2^-60, which bounds the bare weight as well.
@@ -36,17 +37,18 @@ constexpr int kBlock = kKeys * 128;       // 128 rows x 128 codes, 16 KB
 constexpr int kStage = 4 * kBlock;        // a tile
 constexpr int kStages = 2;
 constexpr int kSoftThreads = 256;
-constexpr int kQueryWarps = 4, kTmaWarps = 2;
-constexpr int kThreads = kSoftThreads + 32 * (kQueryWarps + kTmaWarps + 1) + 32;  // (whole: 16)
+constexpr int kTmaWarps = 2;
+constexpr int kThreads = kSoftThreads + 32 * (kTmaWarps + 1);
 constexpr float kRaise8 = 6.f;            // base-2 growth of u that raises a reference
 constexpr float kUp = 256.f;              // weights in E5M2 are scaled by 2^8
 constexpr float kLeastLog = -60.f;
 
 struct Ctl {
   float m[64], nm[64], alpha[64], l[64];  // per head; first: read as float4
-  float sq[3][64];                        // the query rows' scales, by segment
+  float sq[64];                           // the query rows' scales
   float red[4][64];
-  uint64_t full[kStages], empty[kStages], s_full[kStages], p_full, o_full, q_full, q_empty, drain;
+  uint64_t full[kStages][4], empty[kStages][4];  // by block of 128 codes
+  uint64_t s_full[kStages], p_full, o_full, q_full, q_empty, drain;
   Start start;
   uint32_t tmem;
   unsigned groups[kStages];               // TMA boxes of the tile that hold rows
@@ -103,15 +105,67 @@ __device__ __forceinline__ float cut3(float x) {
   return __uint_as_float(__float_as_uint(x) & 0xffe00000u);
 }
 
+// The query rows in two E4M3 parts, for the kernel below: row r's 512 hi codes, then
+// its 512 lo codes, and its scale.  A warp a row, 16 elements a lane.  Bound by its
+// 1 KB in and 1 KB out a row; inside the attention the same work held every row
+// tile's first product back (20,000 cycles of one warp's latency a tile).
+__global__ void __launch_bounds__(256)
+    mla_chunk_query_kernel(const __nv_bfloat16* __restrict__ q_lat, long long rows,
+                           uint8_t* __restrict__ codes, float* __restrict__ scale) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const __nv_bfloat16* src = q_lat + row * kL + lane * 16;
+  const uint4 r0 = ld_stream_v4(src), r1 = ld_stream_v4(src + 8);
+  const uint32_t u[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+  float x[16], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = bf16lo(u[i]);
+    x[2 * i + 1] = bf16hi(u[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (fabsf(x[i]) < INFINITY) top = fmaxf(top, fabsf(x[i]));
+  top = warp_max(top);
+  // exponent of the largest magnitude: 2^ex <= top < 2^(ex + 1); a row below 2^-100
+  // counts as such
+  const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+  const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);    // 2^(7 - ex)
+  const float down = __uint_as_float((uint32_t)(127 + ex - 7) << 23);  // 2^(ex - 7)
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    hi[j] = lo[j] = 0u;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      // a NaN or an infinity becomes the NaN code: its head's logits are NaN
+      float a = x[4 * j + 2 * k] * up, b = x[4 * j + 2 * k + 1] * up;
+      a = fabsf(a) < INFINITY ? a : NAN;
+      b = fabsf(b) < INFINITY ? b : NAN;
+      const uint32_t h2 = e4m3x2(a, b) & 0xffffu;
+      const float2 f = from_e4m3x2(h2);
+      hi[j] |= h2 << (16 * k);
+      lo[j] |= (e4m3x2(a - f.x, b - f.y) & 0xffffu) << (16 * k);
+    }
+  }
+  uint8_t* dst = codes + row * (2 * kL) + lane * 16;
+  *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(dst + kL) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  if (lane == 0) scale[row] = down;
+}
+
 template <int kN>
 __global__ void __launch_bounds__(kThreads, 1)
-    mla_chunk_f8_kernel(const __grid_constant__ CUtensorMap kv_map,
+    mla_chunk_f8_kernel(const __grid_constant__ CUtensorMap q_map,
+                        const __grid_constant__ CUtensorMap kv_map,
                         const __grid_constant__ CUtensorMap ahead_map,
-                        const __nv_bfloat16* __restrict__ q_lat, const Params p) {
+                        const float* __restrict__ q_scale, const Params p) {
   using S = Smem<kN>;
   constexpr int kW = kN / 2;  // heads per softmax thread
-  constexpr int kQuery0 = kSoftThreads / 32, kTma0 = kQuery0 + kQueryWarps,
-                kMmaWarp = kTma0 + kTmaWarps;
+  constexpr int kTma0 = kSoftThreads / 32, kMmaWarp = kTma0 + kTmaWarps;
   constexpr int kTmemCols = kN == 64 ? 512 : 256;  // S^T (2 kN), O^T (4 kN)
   constexpr uint32_t kOCol = kStages * kN;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -122,13 +176,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&c.full[i], kTmaWarps);
-      mbar_init(&c.empty[i], 1);
+      for (int blk = 0; blk < 4; ++blk) {
+        mbar_init(&c.full[i][blk], 1);
+        mbar_init(&c.empty[i][blk], 1);
+      }
       mbar_init(&c.s_full[i], 1);
     }
     mbar_init(&c.p_full, kSoftThreads / 32);
     mbar_init(&c.o_full, 1);
-    mbar_init(&c.q_full, kQueryWarps);
+    mbar_init(&c.q_full, 1);
     mbar_init(&c.q_empty, 1);
     mbar_init(&c.drain, 1);
     fence_mbar_init();
@@ -154,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned long long wait_ns = p.drill ? kDrillWaitNs : kWaitNs;
   volatile int* dead = &c.dead;
 
-  if (warp < kQuery0) {
+  if (warp < kTma0) {
     // ================= softmax and epilogue =================
     const int qw = warp & 3;      // TMEM lanes 32 qw ..: this thread's key row r
     const int hq = warp >> 2;     // heads kW hq ..
@@ -179,7 +235,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kW; ++i) l[i] = 0.f;
       float rs = w.ta < w.tb ? scale_of(w.k, w.b, w.ta) : 0.f;
-      const float4* sq4 = reinterpret_cast<const float4*>(c.sq[segs % 3] + hq * kW);
+      const float4* sq4 = reinterpret_cast<const float4*>(c.sq + hq * kW);
+      const int heads = min(kN, p.Hm - w.h0 * kN);
+      const long long row0 = (long long)w.token * p.Hm + w.h0 * kN;
+      if (tid < kN) c.sq[tid] = tid < heads ? __ldg(q_scale + row0 + tid) : 0.f;
+      sync_soft();
       for (int v = w.ta; v < w.tb; ++v, ++tiles) {
         const int st = tiles & 1;
         const float rs_next = v + 1 < w.tb ? scale_of(w.k, w.b, v + 1) : 0.f;
@@ -265,62 +325,63 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kW; ++i)
             e[i] = valid ? fmaf(e[i], zs, c.nm[hq * kW + i]) : -INFINITY;
         }
-        // P's place and O^T: the last tile's product is done with both
-        if (tiles > 0 &&
-            !wait_on(&c.empty[st ^ 1], ((tiles - 1) >> 1) & 1, dead, wait_ns))
-          c.soft_dead[st ^ 1] = 1;
-        __syncwarp();
         if (full && c.raise) {
-          tc_fence_after();
 #pragma unroll
           for (int i = 0; i < kW; ++i) l[i] *= c.alpha[hq * kW + i];
-          if (v > w.ta) {
-#pragma unroll 1
-            for (int mc = 0; mc < 4; ++mc) {
-              float o[kW];
-              const uint32_t ta = tl + kOCol + (uint32_t)(mc * kN + hq * kW);
-              tmem_ldw<kW>(ta, o);
+        }
+        // the weights and their parts (in registers: the last tile's may still be read)
+        const float up = sc * kUp;
+        uint32_t part[3][kW / 4];
 #pragma unroll
-              for (int i = 0; i < kW; ++i) o[i] *= c.alpha[hq * kW + i];
-              tmem_stw<kW>(ta, o);
-            }
+        for (int j = 0; j < kW / 4; ++j) {
+          float a[4], x[3][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float& ei = e[4 * j + i];
+            ei = ex2_fast(ei);
+            a[i] = ei * up;
+            x[0][i] = cut3(a[i]);
+            a[i] -= x[0][i];
+            x[1][i] = cut3(a[i]);
+            x[2][i] = a[i] - x[1][i];
+          }
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            part[k][j] = e5m2x2(x[k][0], x[k][1]) | (e5m2x2(x[k][2], x[k][3]) << 16);
+          add2(l[4 * j], l[4 * j + 1], e[4 * j], e[4 * j + 1]);
+          add2(l[4 * j + 2], l[4 * j + 3], e[4 * j + 2], e[4 * j + 3]);
+        }
+        // P's place and O^T: the last tile's product is done with both
+        if (tiles > 0 &&
+            !wait_on(&c.empty[st ^ 1][3], ((tiles - 1) >> 1) & 1, dead, wait_ns))
+          c.soft_dead[st ^ 1] = 1;
+        __syncwarp();
+        if (full && c.raise && v > w.ta) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int mc = 0; mc < 4; ++mc) {
+            float o[kW];
+            const uint32_t ta = tl + kOCol + (uint32_t)(mc * kN + hq * kW);
+            tmem_ldw<kW>(ta, o);
+#pragma unroll
+            for (int i = 0; i < kW; ++i) o[i] *= c.alpha[hq * kW + i];
+            tmem_stw<kW>(ta, o);
           }
         }
-        const float up = sc * kUp;
 #pragma unroll
         for (int q = 0; q < kW / 16; ++q) {  // 16 heads: 16 bytes of each part
-          uint32_t part[3][4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float a[4], x[3][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float& ei = e[16 * q + 4 * j + i];
-              ei = ex2_fast(ei);
-              a[i] = ei * up;
-              x[0][i] = cut3(a[i]);
-              a[i] -= x[0][i];
-              x[1][i] = cut3(a[i]);
-              x[2][i] = a[i] - x[1][i];
-            }
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-              part[k][j] = e5m2x2(x[k][0], x[k][1]) | (e5m2x2(x[k][2], x[k][3]) << 16);
-          }
           const int ch = hq * (kW / 16) + q;
           const int at = kN == 64 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)
                                   : r * 32 + ((ch ^ ((r >> 2) & 1)) << 4);
 #pragma unroll
           for (int k = 0; k < 3; ++k)
-            *reinterpret_cast<uint4*>(sb + S::kP + k * S::kPPart + at) =
-                make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
+            *reinterpret_cast<uint4*>(sb + S::kP + k * S::kPPart + at) = make_uint4(
+                part[k][4 * q], part[k][4 * q + 1], part[k][4 * q + 2], part[k][4 * q + 3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive1(&c.p_full);
-#pragma unroll
-        for (int i = 0; i < kW; i += 2) add2(l[i], l[i + 1], e[i], e[i + 1]);
         rs = rs_next;
       }
       if (!ok) break;
@@ -333,8 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         hd.cont_ends = w.tb == w.k.n;
       }
       if (!some && !whole) continue;
-      const int heads = min(kN, p.Hm - w.h0 * kN);
-      const long long row0 = (long long)w.token * p.Hm + w.h0 * kN;
       if (!some) {
         store_nothing(p, row0, heads, tid);
         continue;
@@ -375,80 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) hd = Header{-1, -1, 0, 0};
     if (tid == 0 && p.head) p.head[blockIdx.x] = hd;
-  } else if (warp < kTma0) {
-    // ================= queries: two E4M3 parts of each head's row =================
-    // A row a warp and turn: 16 elements a lane.
-    const int wq = warp - kQuery0;
-    int segs = 0;
-    bool ok = issue;
-    while (ok && w.next()) {
-      if (w.ta == w.tb) continue;
-      const int heads = min(kN, p.Hm - w.h0 * kN);
-      const __nv_bfloat16* src = q_lat + ((long long)w.token * p.Hm + w.h0 * kN) * kL + lane * 16;
-      bool room = segs == 0;
-      for (int rr = wq; rr < kN; rr += kQueryWarps) {
-        uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-        if (rr < heads) {
-          raw[0] = ld_stream_v4(src + (long long)rr * kL);
-          raw[1] = ld_stream_v4(src + (long long)rr * kL + 8);
-        }
-        const uint32_t u[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w,
-                               raw[1].x, raw[1].y, raw[1].z, raw[1].w};
-        float x[16], top = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[2 * i] = bf16lo(u[i]);
-          x[2 * i + 1] = bf16hi(u[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (fabsf(x[i]) < INFINITY) top = fmaxf(top, fabsf(x[i]));
-        top = warp_max(top);
-        // exponent of the largest magnitude: 2^ex <= top < 2^(ex + 1); the rows below
-        // 2^-100 count as such (their scaled elements are small, not the largest)
-        const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-        const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);    // 2^(7 - ex)
-        const float down = __uint_as_float((uint32_t)(127 + ex - 7) << 23);  // 2^(ex - 7)
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          hi[j] = lo[j] = 0u;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            // a NaN or an infinity becomes the NaN code: its head's logits are NaN
-            float a = x[4 * j + 2 * k] * up, b = x[4 * j + 2 * k + 1] * up;
-            a = fabsf(a) < INFINITY ? a : NAN;
-            b = fabsf(b) < INFINITY ? b : NAN;
-            const uint32_t h2 = e4m3x2(a, b) & 0xffffu;
-            const float2 f = from_e4m3x2(h2);
-            hi[j] |= h2 << (16 * k);
-            lo[j] |= (e4m3x2(a - f.x, b - f.y) & 0xffffu) << (16 * k);
-          }
-        }
-        if (!room) {  // the last segment's products with the queries are done
-          const bool got = wait_on(&c.q_empty, (segs - 1) & 1, dead, wait_ns);
-          ok = __all_sync(0xffffffffu, got);
-          if (!ok) break;
-          room = true;
-        }
-        unsigned char* dst = sb + S::kQ + (lane >> 3) * S::kQBlock + rr * 128 +
-                             (((lane & 7) ^ (rr & 7)) << 4);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + S::kQPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        if (lane == 0) c.sq[segs % 3][rr] = down;
-      }
-      if (!ok) break;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(&c.q_full);
-      ++segs;
-    }
   } else if (warp < kMmaWarp) {
     // ================= TMA: two warps, two blocks of 128 codes each =================
     const int team = warp - kTma0;
     const int R = 1 << p.box_log, ng = kKeys >> p.box_log;
-    int tiles = 0;
-    bool ok = issue, armed = false;
+    int tiles = 0, segs = 0;
+    bool ok = issue;
+    int issued = 0;  // blocks of tile `tiles` under way, up to this one
     // the cache row of this lane's box of a tile (-1: nothing seen, -2: no page)
     auto box_row = [&](const Keys<kKeys>& k, int b, int v) -> int {
       if (lane >= ng) return -1;
@@ -463,6 +455,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && w.next()) {
       if (w.ta == w.tb) continue;
       int row = box_row(w.k, w.b, w.ta);
+      if (team == 0) {
+        // the queries' parts, once the last segment's products with them are done
+        const bool free_q = segs == 0 || wait_on(&c.q_empty, (segs - 1) & 1, dead, wait_ns);
+        ok = __all_sync(0xffffffffu, free_q);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&c.q_full, 2 * S::kQPart);
+          for (int i = 0; i < 8; ++i)
+            tma_load_2d(sb + S::kQ + i * S::kQBlock, &q_map, i * 64, w.token * p.Hm + w.h0 * kN,
+                        &c.q_full);
+        }
+        ++segs;
+      }
       for (int v = w.ta; v < w.tb; ++v, ++tiles) {
         const int row_next = v + 1 < w.tb ? box_row(w.k, w.b, v + 1) : -1;
         if (row == -2) {
@@ -471,31 +476,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const unsigned boxes = __ballot_sync(0xffffffffu, row >= 0);
         const int st = tiles & 1;
-        const bool room = tiles < kStages ||
-                          wait_on(&c.empty[st], ((tiles >> 1) - 1) & 1, dead, wait_ns);
-        ok = __all_sync(0xffffffffu, room);
+#pragma unroll 1
+        for (int blk = team; blk < 4; blk += 2) {
+          const bool room = tiles < kStages ||
+                            wait_on(&c.empty[st][blk], ((tiles >> 1) - 1) & 1, dead, wait_ns);
+          ok = __all_sync(0xffffffffu, room);
+          if (!ok) break;
+          if (lane == 0) {
+            if (blk == 0) c.groups[st] = boxes;
+            mbar_arrive_expect_tx(&c.full[st][blk], __popc(boxes) * R * 128);
+          }
+          issued = blk + 1;
+          __syncwarp();
+          if (row >= 0)
+            tma_load_2d(sb + S::kKv + st * kStage + blk * kBlock + lane * R * 128, &kv_map,
+                        blk * 64, row, &c.full[st][blk]);
+        }
         if (!ok) break;
-        if (lane == 0) {
-          if (team == 0) c.groups[st] = boxes;
-          mbar_arrive_expect_tx(&c.full[st], __popc(boxes) * R * 256);
-        }
-        armed = true;
-        __syncwarp();
-        if (row >= 0) {
-          unsigned char* dst = sb + S::kKv + st * kStage + 2 * team * kBlock + lane * R * 128;
-          tma_load_2d(dst, &kv_map, team * 128, row, &c.full[st]);
-          tma_load_2d(dst + kBlock, &kv_map, team * 128 + 64, row, &c.full[st]);
-        }
-        // the tile after the next to L2 would come too early: the next one's rows
-        if (p.prefetch && team == 0 && row_next >= 0) tma_prefetch_2d(&ahead_map, 0, row_next);
+        issued = 0;
+        if (p.prefetch && team == 0 && row_next >= 0)  // the next tile's rows to L2
+          tma_prefetch_2d(&ahead_map, 0, row_next);
         row = row_next;
       }
     }
     // after a give-up: no copy into this CTA's memory may be in flight at its end
-    if (*dead && lane == 0 && armed)
-      for (int i = 1; i <= kStages; ++i)
-        if (tiles - i >= 0)
-          mbar_wait_bounded(&c.full[(tiles - i) & 1], ((tiles - i) >> 1) & 1);
+    if (*dead && lane == 0) {
+      if (segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
+      for (int blk = team; blk < 4; blk += 2)
+        for (int i = blk < issued ? 0 : 1; i <= kStages; ++i)
+          if (tiles - i >= 0)
+            mbar_wait_bounded(&c.full[(tiles - i) & 1][blk], ((tiles - i) >> 1) & 1);
+    }
   } else if (warp == kMmaWarp && issue) {
     // ================= MMA =================
     constexpr uint32_t id_s = idesc_f8(kKeys, kN, false, false, false);
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t more = vo > wo.ta ? 1u : 0u;
         tc_fence_after();
 #pragma unroll
-        for (int mc = 0; mc < 4; ++mc)
+        for (int mc = 0; mc < 4; ++mc) {
 #pragma unroll
           for (int kr = 0; kr < 4; ++kr)
 #pragma unroll
@@ -535,7 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_f8_elect(tmem + kOCol + mc * kN, d_v + ((mc * kBlock + kr * 4096) >> 4),
                             d_p + ((k * S::kPPart + kr * 32 * kN) >> 4), id_o,
                             (kr | k) ? 1u : more);
-        umma_commit_elect(&c.empty[no & 1]);
+          umma_commit_elect(&c.empty[no & 1][mc]);
+        }
         ++no;
         if (++vo == wo.tb) {
           umma_commit_elect(&c.o_full);
@@ -548,18 +560,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (left_s && ns - no < kStages) {
         have_q = have_q || ready(&c.q_full, seg & 1);
         // (the stage's keys imply that its last outputs are done: its scores are free)
-        if (have_q && ready(&c.full[ns & 1], (ns >> 1) & 1)) {
+        if (have_q && ready(&c.full[ns & 1][0], (ns >> 1) & 1)) {
           const uint64_t d_k = d_k0 + (uint32_t)((ns & 1) * (kStage >> 4));
-          tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const uint32_t blk = j >> 2, off = (j & 3) * 32;
-              umma_f8_elect(tmem + (ns & 1) * kN, d_k + ((blk * kBlock + off) >> 4),
-                            d_q + ((k * S::kQPart + blk * S::kQBlock + off) >> 4), id_s,
-                            (k | j) ? 1u : 0u);
+          for (int blk = 0; blk < 4; ++blk) {
+            if (blk > 0) {
+              const bool here = wait_on(&c.full[ns & 1][blk], (ns >> 1) & 1, dead, wait_ns);
+              ok = __all_sync(0xffffffffu, here);
+              if (!ok) break;
             }
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t off = (j & 3) * 32, part = j >> 2;
+              umma_f8_elect(tmem + (ns & 1) * kN, d_k + ((blk * kBlock + off) >> 4),
+                            d_q + ((part * S::kQPart + blk * S::kQBlock + off) >> 4), id_s,
+                            (blk | j) ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
           umma_commit_elect(&c.s_full[ns & 1]);
           ++ns;
           if (++vs == w.tb) {
@@ -596,6 +615,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// the partials' place at the workspace's front
+template <int kN>
+size_t part_bytes(int n_cta) {
+  const size_t n = (size_t)n_cta * 2 * kN * (kL * 4 + 8) + (size_t)n_cta * sizeof(Header);
+  return (n + 127) / 128 * 128;
+}
+
 template <int kN>
 int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   const int n_cta = num_sms();
@@ -615,12 +641,17 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.prefetch = a.T <= 4 * a.B;
   p.box_log = box_log_of(a.kv.page_size);
   p.o_scale = 1.f / kUp;
+  p.extra = 2;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)n_cta * 2 * kN * kL);
   p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)n_cta * 2 * kN);
-  CUtensorMap kv_map, ahead_map;
+  const long long q_rows = (long long)a.T * a.Hm;
+  uint8_t* q_codes = static_cast<uint8_t*>(workspace) + part_bytes<kN>(n_cta);
+  float* q_scale = reinterpret_cast<float*>(q_codes + (size_t)q_rows * 2 * kL);
+  CUtensorMap q_map, kv_map, ahead_map;
   const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.page_size;
-  if (!row_map(&kv_map, a.kv.pages, rows, 1u << p.box_log, true) ||
+  if (!byte_map(&q_map, q_codes, (uint64_t)q_rows, 2 * kL, 64, kN, true) ||
+      !row_map(&kv_map, a.kv.pages, rows, 1u << p.box_log, true) ||
       !prefetch_map(&ahead_map, a.kv.pages, rows, 1u << p.box_log, true))
     return DSA_ERR_CUDA;
   auto kernel = mla_chunk_f8_kernel<kN>;
@@ -633,11 +664,16 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)((q_rows + 7) / 8), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  if (launch_kernel(&cfg, mla_chunk_query_kernel, static_cast<const __nv_bfloat16*>(a.q_lat),
+                    q_rows, q_codes, q_scale) != cudaSuccess)
+    return DSA_ERR_CUDA;
   cfg.gridDim = dim3(n_cta, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = Smem<kN>::kBytes;
-  if (launch_kernel(&cfg, kernel, kv_map, ahead_map, static_cast<const __nv_bfloat16*>(a.q_lat),
-                    p) != cudaSuccess)
+  if (launch_kernel(&cfg, kernel, q_map, kv_map, ahead_map, (const float*)q_scale, p) !=
+      cudaSuccess)
     return DSA_ERR_CUDA;
   cfg.gridDim = dim3(n_cta, kN / 8, 1);
   cfg.blockDim = dim3(512, 1, 1);
@@ -648,6 +684,11 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
 }
 
 }  // namespace
+
+size_t mla_chunk_f8_workspace_size(int T, int Hm) {
+  const size_t parts = Hm <= 32 ? part_bytes<32>(num_sms()) : part_bytes<64>(num_sms());
+  return parts + (size_t)T * Hm * (2 * kL + 4);
+}
 
 int launch_mla_chunk_f8(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   return a.Hm <= 32 ? launch<32>(a, workspace, stream) : launch<64>(a, workspace, stream);

@@ -918,6 +918,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.status = a.status;
   p.drill = failure_drill();
   p.o_scale = 1.f;
+  p.extra = 4;
   p.prefetch = a.T <= 4 * a.B;
   p.box_log = 3;
   p.part_o = static_cast<float*>(workspace);

@@ -600,6 +600,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.status = a.status;
   p.drill = failure_drill();
   p.o_scale = 1.f;
+  p.extra = 2;
   // rows that few tokens share come from HBM: the tile after the next is brought
   // into L2 meanwhile
   p.prefetch = a.T <= 4 * a.B;
