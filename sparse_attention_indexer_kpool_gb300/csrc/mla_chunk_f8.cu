@@ -37,12 +37,8 @@ constexpr int kBlock = kKeys * 128;       // 128 rows x 128 codes, 16 KB
 constexpr int kStage = 4 * kBlock;        // a tile
 constexpr int kStages = 2;
 constexpr int kSoftThreads = 256;
-// A copy costs the warp that issues it 100 cycles; small pages take many.  Four warps
-// issue where the softmax needs few registers, two otherwise.
-__host__ __device__ constexpr int tma_warps(int n) { return n == 32 ? 4 : 2; }
-__host__ __device__ constexpr int cta_threads(int n) {
-  return kSoftThreads + 32 * (tma_warps(n) + 1);
-}
+constexpr int kTmaWarps = 2;
+constexpr int kThreads = kSoftThreads + 32 * (kTmaWarps + 1);
 constexpr float kRaise8 = 6.f;            // base-2 growth of u that raises a reference
 constexpr float kUp = 256.f;              // weights in E5M2 are scaled by 2^8
 constexpr float kLeastLog = -60.f;
@@ -162,14 +158,14 @@ __global__ void __launch_bounds__(256)
 }
 
 template <int kN>
-__global__ void __launch_bounds__(cta_threads(kN), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     mla_chunk_f8_kernel(const __grid_constant__ CUtensorMap q_map,
                         const __grid_constant__ CUtensorMap kv_map,
                         const __grid_constant__ CUtensorMap ahead_map,
                         const float* __restrict__ q_scale, const Params p) {
   using S = Smem<kN>;
   constexpr int kW = kN / 2;  // heads per softmax thread
-  constexpr int kTmaWarps = tma_warps(kN), kTma0 = kSoftThreads / 32, kMmaWarp = kTma0 + kTmaWarps;
+  constexpr int kTma0 = kSoftThreads / 32, kMmaWarp = kTma0 + kTmaWarps;
   constexpr int kTmemCols = kN == 64 ? 512 : 256;  // S^T (2 kN), O^T (4 kN)
   constexpr uint32_t kOCol = kStages * kN;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -205,7 +201,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
   pdl_wait();  // every input may come from the kernel just before
   pdl_launch_dependents();
 
-  const unsigned long long units = find_share<kKeys, false, cta_threads(kN)>(
+  const unsigned long long units = find_share<kKeys, false, kThreads>(
       p, hb, blockIdx.x, gridDim.x, &c.start, blockIdx.x == 0);
   const uint32_t tmem = c.tmem;
   Walk<kKeys, false> w(p, hb, c.start, units);
@@ -439,7 +435,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
     if (!ok) hd = Header{-1, -1, 0, 0};
     if (tid == 0 && p.head) p.head[blockIdx.x] = hd;
   } else if (warp < kMmaWarp) {
-    // ================= TMA: the blocks of 128 codes, shared by the warps =================
+    // ================= TMA: two warps, two blocks of 128 codes each =================
     const int team = warp - kTma0;
     const int R = 1 << p.box_log, ng = kKeys >> p.box_log;
     int tiles = 0, segs = 0;
@@ -481,7 +477,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
         const unsigned boxes = __ballot_sync(0xffffffffu, row >= 0);
         const int st = tiles & 1;
 #pragma unroll 1
-        for (int blk = team; blk < 4; blk += kTmaWarps) {
+        for (int blk = team; blk < 4; blk += 2) {
           const bool room = tiles < kStages ||
                             wait_on(&c.empty[st][blk], ((tiles >> 1) - 1) & 1, dead, wait_ns);
           ok = __all_sync(0xffffffffu, room);
@@ -498,7 +494,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
         }
         if (!ok) break;
         issued = 0;
-        if (p.prefetch && team == kTmaWarps - 1 && row_next >= 0)  // the next tile's rows to L2
+        if (p.prefetch && team == 0 && row_next >= 0)  // the next tile's rows to L2
           tma_prefetch_2d(&ahead_map, 0, row_next);
         row = row_next;
       }
@@ -506,7 +502,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
     // after a give-up: no copy into this CTA's memory may be in flight at its end
     if (*dead && lane == 0) {
       if (segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
-      for (int blk = team; blk < 4; blk += kTmaWarps)
+      for (int blk = team; blk < 4; blk += 2)
         for (int i = blk < issued ? 0 : 1; i <= kStages; ++i)
           if (tiles - i >= 0)
             mbar_wait_bounded(&c.full[(tiles - i) & 1][blk], ((tiles - i) >> 1) & 1);
@@ -674,7 +670,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
                     q_rows, q_codes, q_scale) != cudaSuccess)
     return DSA_ERR_CUDA;
   cfg.gridDim = dim3(n_cta, 1, 1);
-  cfg.blockDim = dim3(cta_threads(kN), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = Smem<kN>::kBytes;
   if (launch_kernel(&cfg, kernel, q_map, kv_map, ahead_map, (const float*)q_scale, p) !=
       cudaSuccess)
