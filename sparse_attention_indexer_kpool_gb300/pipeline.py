@@ -4,6 +4,13 @@
 memory); ``run_layer`` issues the five library calls in the order of the DSA
 module page's pipeline (compress -> index_scores -> topk_pools ->
 expand_selection -> MLA over the selected rows) on one stream.
+
+``PagedStep`` holds a serving step over a paged latent cache (module
+glm5next_dsa, Modules, attend: the paged decode): plan_step gives the step's new
+tokens their sequences, positions and cache rows, append_step stores their latent
+rows, attend_step attends to all that they see, or select_step and
+attend_selected_step to a selection.  Nothing in it reads the GPU back: a step is
+captured into a graph once and replayed for the next tokens.
 """
 from __future__ import annotations
 
@@ -12,7 +19,7 @@ from dataclasses import dataclass
 import torch
 
 from . import ops
-from .synth import Batch
+from .synth import Batch, PagedCache
 
 
 @dataclass
@@ -145,3 +152,86 @@ def project(pi, buf: ProjectionBuffers, weights_scale: float, kv_rows=None, stre
     ops.dsa_indexer_project(pi.x, pi.w_kgw, pi.cq, pi.w_q, pi.w_uk_t, weights_scale, buf.k,
                             buf.gate, buf.weights, buf.q, buf.q_nope, buf.q_lat, buf.ws,
                             kv_rows, buf.status, stream)
+
+
+@dataclass
+class PagedStep:
+    """Buffers of a serving step of up to T new tokens over a ``PagedCache`` whose pages come
+    from one free list; every layer of a model shares the plan, its cache rows and pages."""
+    free_pages: torch.Tensor   # [n_free] int32 pages, taken from free_begin on
+    free_begin: torch.Tensor   # [1] int32
+    cu_new: torch.Tensor       # [B + 1] int32: the plan's token axis
+    q_seq: torch.Tensor        # [T] int32
+    q_pos: torch.Tensor
+    kv_rows: torch.Tensor
+    key_rows: torch.Tensor
+    out: torch.Tensor          # [T, Hm, L]
+    lse: torch.Tensor          # [T, Hm] fp32
+    ws: torch.Tensor | None
+    status: torch.Tensor
+    scores: torch.Tensor | None = None        # a selection's (alloc with its batch)
+    pool_ids: torch.Tensor | None = None
+    token_ids: torch.Tensor | None = None     # [T, out_width] int32
+    ws_select: torch.Tensor | None = None
+    ws_selected: torch.Tensor | None = None
+
+    @staticmethod
+    def alloc(cache: PagedCache, free_pages, T: int, Hm: int, dtype=torch.bfloat16,
+              bt: Batch | None = None) -> "PagedStep":
+        dev, L = cache.pages.device, cache.pages.shape[1]
+        B = cache.seq_lens.numel()
+        i32 = lambda n: torch.zeros(n, dtype=torch.int32, device=dev)  # noqa: E731
+        out = torch.zeros(T, Hm, L, dtype=dtype, device=dev)
+        ws = ops.mla_paged_chunk_workspace_bytes(out, cache.pages)
+        step = PagedStep(
+            free_pages=free_pages, free_begin=i32(1), cu_new=i32(B + 1), q_seq=i32(T),
+            q_pos=i32(T), kv_rows=i32(T), key_rows=i32(T), out=out,
+            lse=torch.zeros(T, Hm, dtype=torch.float32, device=dev),
+            ws=torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None, status=i32(1))
+        if bt is not None:
+            g = bt.geo
+            ws_s = ops.select_workspace_bytes(T, bt.P_ld, g.select_k)
+            ws_m = ops.mla_paged_workspace_bytes(out, cache.pages, g.out_width)
+            step.scores = torch.empty(T, bt.P_ld, dtype=torch.float32, device=dev)
+            step.pool_ids = torch.empty(T, g.select_k, dtype=torch.int32, device=dev)
+            step.token_ids = torch.empty(T, g.out_width, dtype=torch.int32, device=dev)
+            step.ws_select = torch.zeros(max(ws_s, 16), dtype=torch.uint8, device=dev)
+            step.ws_selected = torch.empty(max(ws_m, 16), dtype=torch.uint8, device=dev)
+        return step
+
+
+def plan_step(cache: PagedCache, step: PagedStep, new_lens, row_base=None, stream=None):
+    """The step of ``new_lens`` [B] tokens: lengths, table and free list move on in place."""
+    ops.dsa_paged_plan(cache.seq_lens, new_lens, step.free_pages, step.free_begin,
+                       cache.pages.shape[0] // cache.page_size, cache.page_size,
+                       cache.block_table, cache.seq_lens, step.cu_new, step.q_seq, step.q_pos,
+                       step.kv_rows, step.free_begin, row_base,
+                       None if row_base is None else step.key_rows, step.status, stream)
+
+
+def append_step(cache: PagedCache, step: PagedStep, kv_new, stream=None):
+    """Store the step's latent rows ``kv_new`` [T, L] in one layer's cache."""
+    ops.dsa_paged_append(kv_new, step.kv_rows, cache.pages, cache.row_scale, step.status, stream)
+
+
+def attend_step(cache: PagedCache, step: PagedStep, q_lat, sm_scale, window=0, sinks=0,
+                stream=None):
+    """Dense attention of the step's tokens (``q_lat`` [T, Hm, L]) into ``step.out``, ``lse``."""
+    ops.dsa_mla_paged_chunk(q_lat, cache.pages, cache.row_scale, cache.block_table,
+                            cache.seq_lens, cache.page_size, step.cu_new, window, sinks, sm_scale,
+                            step.out, step.lse, step.ws, step.status, stream)
+
+
+def select_step(bt: Batch, buf: LayerBuffers, step: PagedStep, q, weights, stream=None):
+    """``step.token_ids``: what the step's tokens select among the pools of ``buf`` (``q``
+    [T, H, D], ``weights`` [T, H]); rows behind the last token select nothing."""
+    ops.dsa_select(q, weights, bt.scale, buf.pool_keys, buf.pool_start, buf.pool_valid,
+                   buf.n_pools, bt.cu_pool_cap, step.q_seq, step.q_pos, bt.geo.kpool, step.scores,
+                   step.pool_ids, step.token_ids, step.ws_select, step.status, stream)
+
+
+def attend_selected_step(cache: PagedCache, step: PagedStep, q_lat, sm_scale, stream=None):
+    """Attention of the step's tokens over ``step.token_ids`` into ``step.out``, ``lse``."""
+    ops.dsa_mla_paged_decode(q_lat, cache.pages, cache.row_scale, cache.block_table,
+                             cache.seq_lens, cache.page_size, step.q_seq, step.token_ids, sm_scale,
+                             step.out, step.lse, step.ws_selected, step.status, stream)
