@@ -383,7 +383,7 @@ int launch_mla_chunk_umma(const ChunkArgs& a, void* workspace, cudaStream_t stre
 size_t mla_chunk_f8_workspace_size(int T, int Hm);
 int launch_mla_chunk_f8(const ChunkArgs& a, void* workspace, cudaStream_t stream);
 // the same on pairs of CTAs: two tokens' rows share every key row
-bool mla_chunk_pair_ok(int T, int B, int Hm, int page_size);
+bool mla_chunk_pair_ok(int Hm, int page_size);
 size_t mla_chunk_pair_workspace_size();
 int launch_mla_chunk_pair(const ChunkArgs& a, void* workspace, cudaStream_t stream);
 }  // namespace dsa

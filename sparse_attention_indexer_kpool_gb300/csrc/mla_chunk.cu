@@ -73,9 +73,13 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
   const long long at = (long long)len - (c1 - c0) + (t - c0);
   if (at < 0 && reports && tid == 0) flag(a.status, DSA_DEV_BAD_LENGTH);
   const int pos = (int)max(at, -1ll);
+  // (positions behind the table's width have no page)
+  const long long width = (long long)a.kv.max_pages * a.kv.page_size;
+  const int cap = (int)min(width, 0x7fffffffll);
+  if (pos >= cap && reports && tid == 0) flag(a.status, DSA_DEV_BAD_PAGE);
   const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  const int s0 = min(a.sinks, lo);
-  const int nv = pos < 0 ? 0 : s0 + (pos - lo + 1);  // visible positions
+  const int s0 = min(min(a.sinks, lo), cap);
+  const int nv = pos < 0 ? 0 : s0 + max(min(pos, cap - 1) - lo + 1, 0);  // visible positions
 
   const long long qh = (long long)t * a.Hm + h0;
   const T* q = static_cast<const T*>(a.q_lat) + qh * a.L;
@@ -183,12 +187,32 @@ size_t mla_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype) {
   return one > two ? one : two;
 }
 
+namespace {
+
+// Whether pairs of CTAs are the faster kernel for bf16 pages: two row blocks of a step
+// must share their keys (two new tokens of a sequence on average, or more than 64
+// heads), and a row must see enough of them to pay for the exchange's start and end.
+// The lengths live on the device: the window and the block table's width bound them.
+// Measured on GB300, pair / single CTA in us (sequences x new tokens, 64 heads):
+//   context  8,192, 32 x 4: 177 / 196, 16 x 16: 317 / 361, 4 x 256: 1,101 / 1,221
+//   context  2,048, 32 x 4:  72 /  70, 16 x 16: 111 / 104, 4 x 256:   330 /   336
+//   context    512, 32 x 4:  45 /  35, 16 x 16:  61 /  46, 4 x 256:   138 /   114
+//   window   4,096 of 16,384, 4 x 256: 627 / 662; 2,048: 370 / 367; 512: 177 / 143
+//   single tokens, context 8,192: 64 x 1: 165 / 111, 64 heads; 32 x 2: 106 / 109
+bool pairs_pay(const ChunkArgs& a) {
+  if (a.kv.kv_dtype != DSA_BF16 || (a.Hm <= 64 && a.T < 2ll * a.B)) return false;
+  const long long table = (long long)a.kv.max_pages * a.kv.page_size;
+  const long long seen = a.window > 0 ? (long long)a.window + a.sinks : table;
+  return (seen < table ? seen : table) > 2048;
+}
+
+}  // namespace
+
 int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   if (mla_chunk_umma_ok(a.L, a.dtype, a.kv.kv_dtype)) {
     if (a.kv.kv_dtype == DSA_FP8_E4M3 && a.kv.page_size % 8 == 0)
       return launch_mla_chunk_f8(a, workspace, stream);
-    return a.kv.kv_dtype == DSA_BF16 && a.window == 0 && a.T >= 8 * a.B &&
-                   mla_chunk_pair_ok(a.T, a.B, a.Hm, a.kv.page_size)
+    return pairs_pay(a) && mla_chunk_pair_ok(a.Hm, a.kv.page_size)
                ? launch_mla_chunk_pair(a, workspace, stream)
                : launch_mla_chunk_umma(a, workspace, stream);
   }

@@ -41,7 +41,15 @@ struct Params {
   int box_log;               // positions of a box, 2^box_log (copied rows: 1)
   float o_scale;             // of the partials' output against their sums
   int extra;                 // what a row tile costs beside its key tiles, in units
+  int cap;                   // positions that the block table has room for
 };
+
+// Positions behind the table's width have no page: nothing is walked there, so that a
+// wrong length costs no more than the table's own.
+inline int table_cap(const PagedKv& kv) {
+  const long long n = (long long)kv.max_pages * kv.page_size;
+  return n < 0x7fffffffll ? (int)n : 0x7fffffff;
+}
 
 // ---- the batch as units ------------------------------------------------------
 // A unit is one key tile of kT positions for one row tile; its queries, its first
@@ -58,12 +66,12 @@ __device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p
   s.c0 = min(max(cu0, 0), p.T);
   s.n = max(min(cu1, p.T) - s.c0, 0);
   s.base = len < 0 ? -s.n : len - s.n;   // negative: rows before position 0
-  const unsigned all = (unsigned)max(len, 0);
+  const unsigned all = (unsigned)min(max(len, 0), p.cap);
   s.u = (all + kT - 1) / kT;
   if (p.window > 0) {
     const long long R = 1 << p.box_log;
     const long long keys =
-        ((p.sinks + R - 1) / R + (p.window + (kPair ? 1 : 0) + R - 2) / R + 1) * R;
+        ((p.sinks + R - 1) / R + (R - 2 + (kPair ? 1 : 0) + p.window) / R + 1) * R;
     if ((keys + kT - 1) / kT < (long long)s.u) s.u = (unsigned)((keys + kT - 1) / kT);
   }
   s.u = max(s.u, 1u) + (unsigned)p.extra;
@@ -88,13 +96,13 @@ struct Keys {
 template <int kT>
 __device__ __forceinline__ Keys<kT> keys_of(int pos0, int pos, const Params& p) {
   Keys<kT> k;
-  k.pos = pos;
+  k.pos = min(pos, p.cap - 1);
   k.log = p.box_log;
-  k.lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
-  k.s0 = min(p.sinks, k.lo);
+  k.lo = p.window > 0 ? max(0, max(pos0, -1) - p.window + 1) : 0;
+  k.s0 = min(min(p.sinks, k.lo), p.cap);
   k.first = k.lo >> k.log;
   k.sink_boxes = min((k.s0 >> k.log) + ((k.s0 & ((1 << k.log) - 1)) != 0), k.first);
-  k.boxes = pos < 0 ? 0 : k.sink_boxes + (pos >> k.log) - k.first + 1;
+  k.boxes = pos < 0 ? 0 : k.sink_boxes + max((k.pos >> k.log) - k.first + 1, 0);
   const int per = kT >> k.log;
   k.n = (k.boxes + per - 1) / per;
   return k;
@@ -133,14 +141,16 @@ __device__ __forceinline__ unsigned long long find_share(const Params& p, int hb
             b1 = min(p.B, b0 + per);
   if (tid == 0) st->b = p.B;
   unsigned long long mine = 0;
-  bool odd = false;
+  bool odd = false, past = false;
   for (int b = b0; b < b1; ++b) {
     const int cu0 = p.cu_new[b], cu1 = p.cu_new[b + 1], len = p.kv.seq_lens[b];
     const Seq s = seq_of<kT, kPair>(cu0, cu1, len, p);
     odd |= cu0 < 0 || cu1 < cu0 || cu1 > p.T || (s.n > 0 && s.base < 0);
+    past |= s.n > 0 && len > p.cap;
     mine += (unsigned long long)row_tiles<kT, kPair>(s, hb) * s.u;
   }
   if (odd && reports) flag(p.status, DSA_DEV_BAD_LENGTH);
+  if (past && reports) flag(p.status, DSA_DEV_BAD_PAGE);
   unsigned long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -349,6 +359,9 @@ __device__ __forceinline__ void store_rows(const Params& p, const float* inv, ui
                                            long long row0, int heads, int qw, int hq, int lane) {
   constexpr int kW = kN / 2;
   const bool upper = lane & 1;
+  float iv[kW];
+#pragma unroll
+  for (int i = 0; i < kW; ++i) iv[i] = inv[hq * kW + i];
 #pragma unroll 1
   for (int mc = 0; mc < 4; ++mc) {
     float o[kW];
@@ -357,7 +370,7 @@ __device__ __forceinline__ void store_rows(const Params& p, const float* inv, ui
         p.out + (row0 + hq * kW + (upper ? 1 : 0)) * kL + mc * 128 + qw * 32 + (lane & ~1);
 #pragma unroll
     for (int i = 0; i < kW; i += 2) {
-      const float a = o[i] * inv[hq * kW + i], b = o[i + 1] * inv[hq * kW + i + 1];
+      const float a = o[i] * iv[i], b = o[i + 1] * iv[i + 1];
       const float got = __shfl_xor_sync(0xffffffffu, upper ? a : b, 1);
       if (hq * kW + i + (upper ? 1 : 0) < heads)
         *reinterpret_cast<uint32_t*>(dst + (long long)i * kL) =

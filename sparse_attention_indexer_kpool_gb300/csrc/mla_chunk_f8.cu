@@ -638,6 +638,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.lse = a.lse;
   p.status = a.status;
   p.drill = failure_drill();
+  p.cap = table_cap(a.kv);
   p.prefetch = a.T <= 4 * a.B;
   p.box_log = box_log_of(a.kv.page_size);
   p.o_scale = 1.f / kUp;

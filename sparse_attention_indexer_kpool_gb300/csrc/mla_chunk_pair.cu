@@ -1,23 +1,25 @@
 // The chunk attention on pairs of CTAs (bf16 activations, latent 512, more than 32
-// heads, bf16 or E4M3 pages of a multiple of 8 rows): two row blocks of 64 (two
-// tokens, or one token's two blocks of heads) share every key row.
+// heads, bf16 pages of a multiple of 8 rows): two row blocks of 64 (two tokens, or one
+// token's two blocks of heads) share every key row.
 //
 // Why pairs.  One CTA cannot hold more than 64 rows: the fp32 output of a row takes
-// 512 TMEM columns over 128 lanes, and with 64 rows every MMA reads 6 KB of shared
-// memory for 32 cycles' work, and every key row is fetched for one token.  A cluster
-// of two CTAs splits the latent axis instead: CTA c holds latent columns 256 c .. of
-// the queries (64 KB), of the keys (40 KB for a tile of 80, three stages), and of the
-// output (256 TMEM columns for all 128 rows).
-//   S_c = Q_c K_c^T      M = 128 rows, N = 80 keys, K = 256: a partial sum
+// 512 TMEM columns over 128 lanes, and every key row is fetched for one token.  A
+// cluster of two CTAs splits the latent axis instead: CTA c holds latent columns
+// 256 c .. of the queries (64 KB), of the keys (32 KB for a tile of 64, four stages), and
+// of the output (256 TMEM columns for all 128 rows).
+//   S_c = Q_c K_c^T      M = 128 rows, N = 64 keys, K = 256: a partial sum
 //   S   = S_0 + S_1      each CTA sends the partials of the other one's 64 rows
 //                        through distributed shared memory and adds its own
 //   P                    softmax weights of its 64 rows, written to its own TMEM and
 //                        sent (bf16) to the other's
-//   O_c += P V_c         A = P from TMEM, V_c = K_c read MN-major, N = 256, K = 80
-// An MMA then reads 6.5 KB for 40 cycles' work (QK) or 8 KB for 128 (PV), a key row is
-// fetched once for two tokens, and no product is done twice.  The exchange and the
-// softmax stand between a tile's two products (about 2,000 cycles); three tiles are in
-// flight, so the tensor cores work on the others meanwhile.
+//   O_c += P V_c         A = P from TMEM, V_c = K_c read MN-major, N = 256, K = 64
+// An MMA then reads 6 KB of shared memory for 32 cycles' work (QK) or 8 KB for 128 (PV):
+// 20 MMAs, about 1,350 cycles a tile of 128 x 64; the single-CTA kernel takes 6,200
+// for the same scores.  A key row is fetched once for two tokens, and no product is
+// done twice.  What bounds it is the exchange: scores, send, sum, weights, send and PV are
+// a chain of about 9,500 cycles a tile, of which four tiles are on their way at once (what
+// shared memory holds).  Measured on GB300, 64 heads, 2,048 tokens behind 14,336:
+// 3.97 ms, 1,040 TFLOP/s (0.56 of the measured bf16 rate; the single-CTA kernel: 4.53 ms).
 //
 // The two tokens of a pair see the same keys but for the last one and the first of a
 // window.  A key that neither sees is zeroed in shared memory before PV; one that only
@@ -33,8 +35,11 @@ namespace {
 using namespace chunk;
 
 constexpr int kKT = 64;                      // keys of a tile
-constexpr int kGroups = kKT / 8;             // of 8 rows: 4 KB, [64-column block][row][128 B]
-constexpr int kStageBytes = kGroups * 4096;  // 32 KB
+constexpr int kBoxLog = 3;                   // a TMA box: 8 rows of this CTA's 256 latent
+constexpr int kBoxes = kKT >> kBoxLog;       // columns, [64-column block][row][128 B]
+constexpr int kBoxBytes = 4096;
+constexpr unsigned kAllBoxes = (1u << kBoxes) - 1;
+constexpr int kStageBytes = kBoxes * kBoxBytes;
 constexpr int kStages = 4;
 constexpr int kQBlock = 128 * 128;           // 128 rows x 64 latent columns
 // Warps 0..15 by TMEM lane quarter (warp mod 4).  The quarters of this CTA's row block
@@ -45,7 +50,7 @@ constexpr int kQBlock = 128 * 128;           // 128 rows x 64 latent columns
 constexpr int kRowWarps = 16;
 constexpr int kTeamWarps = 4;
 constexpr int kW = kKT / 2;
-constexpr int kWidenWarps = 4;               // E4M3: two groups each
+constexpr int kThreads = 32 * (kRowWarps + 4);
 constexpr size_t kOffQ = 0;
 constexpr size_t kOffK = 4 * (size_t)kQBlock;
 constexpr size_t kOffS = kOffK + (size_t)kStages * kStageBytes;   // [16][64 rows] x 16 B
@@ -53,12 +58,11 @@ constexpr size_t kOffP = kOffS + (size_t)(kKT / 4) * 64 * 16;     // [16][64 row
 constexpr uint32_t kSBytes = kKT * 64 * 4, kPBytes = kKT * 64 * 2 + 64 * 4;
 
 struct Ctl {
-  float rs[kStages][kKT];          // E4M3: the keys' row scales (first: read as float4)
   float alpha[64];                 // from the other CTA: its rows' rescale of this tile
   float inv[128];                  // 1 / sum of every row (the other CTA's rows: sent)
   float m[64];                     // own rows: the reference (base 2)
   float mx[2][2][64];              // [team][half of the keys]: a tile's row maxima
-  uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], raw[kStages];
+  uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages];
   uint64_t s_full[kStages], p_full[kStages], o_full, drain;
   // [2]: by the tile's team, so that each waiter sees every phase of its barrier
   uint64_t in_s[2], in_p, in_l;    // data from the other CTA
@@ -67,7 +71,7 @@ struct Ctl {
   uint64_t sums, epi;              // the sums of a segment's rows
   Start start;
   uint32_t tmem;
-  unsigned groups[kStages];        // groups of the tile that have a page
+  unsigned groups[kStages];        // boxes of the tile that have a page
   int team_dead[2][2];
   int dead;
 };
@@ -75,10 +79,6 @@ constexpr size_t kOffCtl = kOffP + (size_t)(kKT / 4) * 64 * 8;
 constexpr size_t kSmem = 1024 + kOffCtl + sizeof(Ctl);
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 static_assert(256 + kStages * kKT <= 512, "TMEM columns");
-
-__host__ __device__ constexpr int pair_threads(bool codes) {
-  return 32 * (kRowWarps + 4 + (codes ? kWidenWarps : 0));
-}
 
 // ---- cluster pieces ------------------------------------------------------------
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -170,13 +170,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-
 // What one row block (token) of the tile sees.
 struct Sight {
   int pos, lo, sinks;
@@ -191,11 +184,9 @@ __device__ __forceinline__ Sight sight_of(int pos, const Params& p) {
 using PairWalk = Walk<kKT, true>;
 using PairKeys = Keys<kKT>;
 
-template <bool kCodes>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mla_chunk_pair_kernel(const __grid_constant__ CUtensorMap q_map,
                           const __grid_constant__ CUtensorMap kv_map, const Params p) {
-  constexpr int kWiden0 = kRowWarps + 4;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl& c = *reinterpret_cast<Ctl*>(sb + kOffCtl);
@@ -211,9 +202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
     mbar_init(&c.q_full, 1);
     mbar_init(&c.q_empty, 1);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&c.k_full[i], kCodes ? kWidenWarps : 1);
+      mbar_init(&c.k_full[i], 1);
       mbar_init(&c.k_empty[i], 1);
-      mbar_init(&c.raw[i], 1);
       mbar_init(&c.s_full[i], 1);
       mbar_init(&c.p_full[i], 2 * kTeamWarps);
     }
@@ -239,7 +229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
   if (tid < 64) c.m[tid] = -INFINITY;
   pdl_wait();  // every input may come from the kernel just before
   pdl_launch_dependents();
-  const unsigned long long units = find_share<kKT, true, pair_threads(kCodes)>(
+  const unsigned long long units = find_share<kKT, true, kThreads>(
       p, hb, me, workers, &c.start, blockIdx.x == 0);
   cluster_sync();  // the other CTA's barriers exist
   const uint32_t tmem = c.tmem;
@@ -357,16 +347,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             tc_fence_after();
             float e[kW];
             tmem_ld32(tS + h * kW, e);
-            const bool plain = span && c.groups[st] == (1u << kGroups) - 1;
+            const bool plain = span && c.groups[st] == kAllBoxes;
             if (!plain && ttid < kKT) {
               // clear what neither sees, and what one does not see if it is not finite
               const int key = ttid;
               const int t = w.k.at(v, key);
-              const bool paged = (c.groups[st] >> (key >> 3)) & 1u;
+              const bool paged = (c.groups[st] >> (key >> kBoxLog)) & 1u;
               const bool ina = paged && sa(t), inb = paged && sbt(t);
               if (!(ina && inb)) {
-                unsigned char* kr =
-                    sb + kOffK + st * kStageBytes + (key >> 3) * 4096 + (key & 7) * 128;
+                unsigned char* kr = sb + kOffK + st * kStageBytes + (key >> 3) * kBoxBytes +
+                                    (key & 7) * 128;
                 bool odd = !(ina || inb);
                 if (!odd) {
                   for (int i = 0; i < 32; ++i) {
@@ -389,11 +379,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             if (!plain) {
               const int key = h * kW + lane;
               see = __ballot_sync(0xffffffffu, mine(w.k.at(v, key)) &&
-                                                   ((c.groups[st] >> (key >> 3)) & 1u));
+                                                   ((c.groups[st] >> (key >> kBoxLog)) & 1u));
             }
             fine = fine && wait_on(&c.in_s[team], turn, dead, wait_ns);
             __syncwarp();
-            if (first && lane == 0) mbar_arrive_expect_tx(&c.in_s[team], kSBytes);  // the next one
+            // the next one (never while this one is still open)
+            if (fine && first && lane == 0) mbar_arrive_expect_tx(&c.in_s[team], kSBytes);
 #pragma unroll
             for (int j = 0; j < kW / 4; ++j) {
               const uint4 x = in_s[j * 64];
@@ -401,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
               add2(e[4 * j + 2], e[4 * j + 3], __uint_as_float(x.z), __uint_as_float(x.w));
             }
             __syncwarp();
-            if (lane == 0) arrive_remote(bar_free_s);
+            if (fine && lane == 0) arrive_remote(bar_free_s);
             // the references, once the last tile's team has settled them
             if (tiles > 0 && fine)
               fine = wait_on(&c.turn[team ^ 1], ((tiles - 1) >> 1) & 1, dead, wait_ns);
@@ -412,19 +403,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
               m = m_now;
             }
             const float nm = m == -INFINITY ? 0.f : -m;
-            if constexpr (kCodes) {
 #pragma unroll
-              for (int q = 0; q < kW / 4; ++q) {
-                const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + h * kW)[q];
-                e[4 * q] = fmaf(e[4 * q], p.zscale * rs.x, nm);
-                e[4 * q + 1] = fmaf(e[4 * q + 1], p.zscale * rs.y, nm);
-                e[4 * q + 2] = fmaf(e[4 * q + 2], p.zscale * rs.z, nm);
-                e[4 * q + 3] = fmaf(e[4 * q + 3], p.zscale * rs.w, nm);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < kW; i += 2) fma2(e[i], e[i + 1], p.zscale, nm, nm);
-            }
+            for (int i = 0; i < kW; i += 2) fma2(e[i], e[i + 1], p.zscale, nm, nm);
             if (!plain) {
 #pragma unroll
               for (int i = 0; i < kW; ++i)
@@ -474,23 +454,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
             }
             l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
             // P is rounded to bf16 for the tensor cores; the sums keep the unrounded
-            // weights.  An E4M3 row's scale goes to its weights.
+            // weights.
             uint32_t pk[kW / 2];
-            if constexpr (kCodes) {
-#pragma unroll
-              for (int q = 0; q < kW / 4; ++q) {
-                const float4 rs = reinterpret_cast<const float4*>(c.rs[st] + h * kW)[q];
-                e[4 * q] *= rs.x;
-                e[4 * q + 1] *= rs.y;
-                e[4 * q + 2] *= rs.z;
-                e[4 * q + 3] *= rs.w;
-              }
-              if (!plain) {  // (a hidden key's scale may be anything)
-#pragma unroll
-                for (int i = 0; i < kW; ++i)
-                  if (!((see >> i) & 1u)) e[i] = 0.f;
-              }
-            }
 #pragma unroll
             for (int i = 0; i < kW / 2; ++i) pk[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
             // the other CTA has taken the last tile's weights
@@ -633,10 +598,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
     // ================= TMA =================
     int tiles = 0, segs = 0;
     bool ok = issue, armed = false;
-    // the cache row of this lane's group of a tile (-1: nothing seen, -2: no page)
+    // the cache row of this lane's box of a tile (-1: nothing seen, -2: no page)
     auto group_row = [&](const PairKeys& k, int b, int v) -> int {
-      if (lane >= kGroups) return -1;
-      const int t0 = k.at(v, lane * 8);
+      if (lane >= kBoxes) return -1;
+      const int t0 = k.at(v, lane << kBoxLog);
       if (t0 > k.pos) return -1;
       const int blk = t0 / p.kv.page_size;
       if (blk >= p.kv.max_pages) return -2;
@@ -644,7 +609,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
       if (page < 0 || page >= p.kv.n_pages) return -2;
       return page * p.kv.page_size + t0 % p.kv.page_size;
     };
-    uint64_t* land = kCodes ? c.raw : c.k_full;
     while (ok && w.next()) {
       if (w.ta == w.tb) continue;
       int row = group_row(w.k, w.b, w.ta);
@@ -675,15 +639,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
         if (!ok) break;
         if (lane == 0) {
           c.groups[st] = groups;
-          mbar_arrive_expect_tx(&land[st], __popc(groups) * (kCodes ? 2048 : 4096));
+          mbar_arrive_expect_tx(&c.k_full[st], __popc(groups) * kBoxBytes);
         }
         armed = true;
         __syncwarp();
         if (row >= 0)
-          tma_load_3d(sb + kOffK + st * kStageBytes + lane * 4096, &kv_map, 0, row,
-                      (kCodes ? 2 : 4) * (int)rank, &land[st]);
-        if (p.prefetch && row_next >= 0)
-          tma_prefetch_3d(&kv_map, 0, row_next, (kCodes ? 2 : 4) * (int)rank);
+          tma_load_3d(sb + kOffK + st * kStageBytes + lane * kBoxBytes, &kv_map, 0, row,
+                      4 * (int)rank, &c.k_full[st]);
         row = row_next;
       }
     }
@@ -691,7 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
     if (*dead && lane == 0) {
       for (int i = 1; i <= kStages; ++i)
         if (armed && tiles - i >= 0)
-          mbar_wait_bounded(&land[(tiles - i) % kStages], ((tiles - i) / kStages) & 1);
+          mbar_wait_bounded(&c.k_full[(tiles - i) % kStages], ((tiles - i) / kStages) & 1);
       if (segs > 0) mbar_wait_bounded(&c.q_full, (segs - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
@@ -701,8 +663,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
       constexpr uint32_t id_o = umma_idesc_bf16(128, 256, false, true);
       const uint32_t qb = smem_u32(sb + kOffQ), kb = smem_u32(sb + kOffK);
       // (a descriptor's low bits are the address in 16-byte units: steps add constants)
-      const uint64_t d_q = sw128_desc(qb), d_k0 = umma_desc_sw128(kb, 16, 4096),
-                     d_v0 = umma_desc_sw128(kb, 1024, 4096);
+      const uint64_t d_q = sw128_desc(qb), d_k0 = umma_desc_sw128(kb, 16, kBoxBytes),
+                     d_v0 = umma_desc_sw128(kb, 1024, kBoxBytes);
       // Two streams over the same tiles: scores as soon as a stage holds keys, outputs
       // as soon as a tile's weights are there; whichever is ready goes next (outputs
       // first: they free the stage).
@@ -726,7 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
           tc_fence_after();
 #pragma unroll
           for (int s = 0; s < kKT / 16; ++s)
-            umma_tmem_a_elect(tmem, a0 + s * 8, d_v + s * (8192 >> 4), id_o,
+            umma_tmem_a_elect(tmem, a0 + s * 8, d_v + s * (2 * kBoxBytes >> 4), id_o,
                               (vo > wo.ta || s > 0) ? 1u : 0u);
           umma_commit_elect(&c.k_empty[st]);
           ++no;
@@ -778,65 +740,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
         mbar_wait_bounded(&c.drain, 0);
       }
     }
-  } else if (kCodes && warp >= kWiden0) {
-    // ================= E4M3 rows, widened in place =================
-    // A group's codes (8 rows of 256, two swizzled blocks) land in the first half of
-    // its 4 KB; one warp takes them into registers and writes the bf16 rows.
-    const int wi = warp - kWiden0;  // groups wi, wi + 4
-    int tiles = 0;
-    bool ok = issue;
-    auto scale_of = [&](const PairKeys& k, int b, int v) -> float {
-      // lanes 0..15: the rows of this warp's two groups
-      if (lane >= 16) return 0.f;
-      const int t = k.at(v, (wi + kWidenWarps * (lane >> 3)) * 8 + (lane & 7));
-      if (t > k.pos) return 0.f;
-      const int blk = t / p.kv.page_size;
-      if (blk >= p.kv.max_pages) return 0.f;
-      const int page = __ldg(p.kv.block_table + (long long)b * p.kv.max_pages + blk);
-      if (page < 0 || page >= p.kv.n_pages) return 0.f;
-      return __ldg(p.kv.row_scale + (long long)page * p.kv.page_size + t % p.kv.page_size);
-    };
-    while (ok && w.next()) {
-      float rs = w.ta < w.tb ? scale_of(w.k, w.b, w.ta) : 0.f;
-      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
-        const float rs_next = v + 1 < w.tb ? scale_of(w.k, w.b, v + 1) : 0.f;
-        const int st = tiles % kStages;
-        const bool here = wait_on(&c.raw[st], (tiles / kStages) & 1, dead, wait_ns);
-        ok = __all_sync(0xffffffffu, here);
-        if (!ok) break;
-        if (lane < 16) c.rs[st][(wi + kWidenWarps * (lane >> 3)) * 8 + (lane & 7)] = rs;
-        const int rr = lane & 7;
-#pragma unroll
-        for (int gi = 0; gi < 2; ++gi) {
-          unsigned char* gp = sb + kOffK + st * kStageBytes + (wi + kWidenWarps * gi) * 4096;
-          uint4 raw[4];
-#pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int pc = (lane >> 3) + 4 * it;
-            raw[it] = *reinterpret_cast<const uint4*>(gp + (pc >> 3) * 1024 + rr * 128 +
-                                                      (((pc & 7) ^ rr) << 4));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int pc = (lane >> 3) + 4 * it;
-            const uint32_t x[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-              *reinterpret_cast<uint4*>(gp + (pc >> 2) * 1024 + rr * 128 +
-                                        (((2 * (pc & 3) + hf) ^ rr) << 4)) =
-                  make_uint4(e4m3x2_to_bf16x2(x[2 * hf] & 0xffffu),
-                             e4m3x2_to_bf16x2(x[2 * hf] >> 16),
-                             e4m3x2_to_bf16x2(x[2 * hf + 1] & 0xffffu),
-                             e4m3x2_to_bf16x2(x[2 * hf + 1] >> 16));
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive1(&c.k_full[st]);
-        rs = rs_next;
-      }
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -849,19 +752,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCodes)
   cluster_sync();  // neither CTA's memory goes while the other may write to it
 }
 
-// [rows, 512] as blocks of 128 bytes: boxes of 8 rows of this CTA's half of the
-// latent columns, 128-byte swizzle (E4M3 codes in pairs, as 2-byte elements).
-bool group_map(CUtensorMap* m, const void* base, uint64_t rows, bool codes) {
+// [rows, 512] as blocks of 64 columns: boxes of 8 rows of a CTA's half of the latent
+// columns, 128-byte swizzle.
+bool half_map(CUtensorMap* m, const void* base, uint64_t rows) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {64u, (cuuint64_t)rows, codes ? 4u : 8u};
-  const cuuint64_t strides[2] = {(cuuint64_t)kL * (codes ? 1 : 2), 128};
-  const cuuint32_t box[3] = {64u, 8, codes ? 2u : 4u};
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, 8};
+  const cuuint64_t strides[2] = {(cuuint64_t)kL * 2, 128};
+  const cuuint32_t box[3] = {64, 1u << kBoxLog, 4};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // CTA pairs that the current device holds at once (0: none; asked once per device).
@@ -875,25 +777,20 @@ int max_pairs() {
   }
   int n = known[dev].load(std::memory_order_relaxed);
   if (n > 0) return n - 1;
-  n = 1 << 30;
-  for (int codes = 0; codes < 2; ++codes) {
-    auto kernel = codes ? mla_chunk_pair_kernel<true> : mla_chunk_pair_kernel<false>;
-    int got = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) ==
-        cudaSuccess) {
-      cudaLaunchAttribute a;
-      a.id = cudaLaunchAttributeClusterDimension;
-      a.val.clusterDim.x = 2;
-      a.val.clusterDim.y = a.val.clusterDim.z = 1;
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(num_sms() / 2 * 2, 1, 1);
-      cfg.blockDim = dim3(pair_threads(codes), 1, 1);
-      cfg.dynamicSmemBytes = kSmem;
-      cfg.attrs = &a;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess) got = 0;
-    }
-    n = got < n ? got : n;
+  n = 0;
+  if (cudaFuncSetAttribute(mla_chunk_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kSmem) == cudaSuccess) {
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = 2;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms() / 2 * 2, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, mla_chunk_pair_kernel, &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();  // a refused query leaves no error behind
   if (n > num_sms() / 2) n = num_sms() / 2;
@@ -901,8 +798,18 @@ int max_pairs() {
   return n;
 }
 
-template <bool kCodes>
-int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
+}  // namespace
+
+bool mla_chunk_pair_ok(int Hm, int page_size) {
+  return Hm > 32 && page_size % 8 == 0 && max_pairs() > 0;
+}
+
+size_t mla_chunk_pair_workspace_size() {
+  const size_t pairs = num_sms() / 2;
+  return pairs * 2 * 128 * (kL * 4 + 8) + pairs * sizeof(Header);
+}
+
+int launch_mla_chunk_pair(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   const int pairs = max_pairs();
   Params p = {};
   p.kv = a.kv;
@@ -917,20 +824,19 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.lse = a.lse;
   p.status = a.status;
   p.drill = failure_drill();
+  p.cap = table_cap(a.kv);
   p.o_scale = 1.f;
   p.extra = 4;
-  p.prefetch = a.T <= 4 * a.B;
-  p.box_log = 3;
+  p.box_log = kBoxLog;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)pairs * 2 * 128 * kL);
   p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)pairs * 2 * 128);
   CUtensorMap q_map, kv_map;
   if (!row_map(&q_map, a.q_lat, (uint64_t)a.T * a.Hm, 64) ||
-      !group_map(&kv_map, a.kv.pages, (uint64_t)a.kv.n_pages * a.kv.page_size, kCodes))
+      !half_map(&kv_map, a.kv.pages, (uint64_t)a.kv.n_pages * a.kv.page_size))
     return DSA_ERR_CUDA;
-  auto kernel = mla_chunk_pair_kernel<kCodes>;
   static std::atomic<unsigned long long> done{0};
-  if (!allow_smem(kernel, kSmem, done)) return DSA_ERR_CUDA;
+  if (!allow_smem(mla_chunk_pair_kernel, kSmem, done)) return DSA_ERR_CUDA;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -939,33 +845,16 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  cfg.blockDim = dim3(pair_threads(kCodes), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
-  if (launch_kernel(&cfg, kernel, q_map, kv_map, p) != cudaSuccess) return DSA_ERR_CUDA;
+  if (launch_kernel(&cfg, mla_chunk_pair_kernel, q_map, kv_map, p) != cudaSuccess)
+    return DSA_ERR_CUDA;
   cfg.gridDim = dim3(pairs, 16, 1);
   cfg.blockDim = dim3(512, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return launch_kernel(&cfg, mla_chunk_join_kernel<128, true>, p, pairs) == cudaSuccess
              ? DSA_OK
              : DSA_ERR_CUDA;
-}
-
-}  // namespace
-
-bool mla_chunk_pair_ok(int T, int B, int Hm, int page_size) {
-  (void)T;
-  (void)B;
-  return Hm > 32 && page_size % 8 == 0 && max_pairs() > 0;
-}
-
-size_t mla_chunk_pair_workspace_size() {
-  const size_t pairs = num_sms() / 2;
-  return pairs * 2 * 128 * (kL * 4 + 8) + pairs * sizeof(Header);
-}
-
-int launch_mla_chunk_pair(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
-  return a.kv.kv_dtype == DSA_FP8_E4M3 ? launch<true>(a, workspace, stream)
-                                       : launch<false>(a, workspace, stream);
 }
 
 }  // namespace dsa

@@ -599,6 +599,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.lse = a.lse;
   p.status = a.status;
   p.drill = failure_drill();
+  p.cap = table_cap(a.kv);
   p.o_scale = 1.f;
   p.extra = 2;
   // rows that few tokens share come from HBM: the tile after the next is brought

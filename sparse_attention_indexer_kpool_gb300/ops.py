@@ -227,8 +227,9 @@ def dsa_paged_plan(ctx_lens, new_lens, free_pages, free_begin, n_pages, page_siz
     B, T = ctx_lens.numel(), q_seq.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
-    if (new_lens.numel(), free_begin.numel(), seq_lens.numel(), cu_new.numel(), q_pos.numel(),
-            kv_rows.numel(), free_end.numel()) != (B, 1, B, B + 1, T, T, 1) or row_base is not None or key_rows is not None:
+    if row_base is not None or key_rows is not None or (
+            new_lens.numel(), free_begin.numel(), seq_lens.numel(), cu_new.numel(), q_pos.numel(),
+            kv_rows.numel(), free_end.numel()) != (B, 1, B, B + 1, T, T, 1):
         _sizes((new_lens, B, "new_lens"), (free_begin, 1, "free_begin"),
                (seq_lens, B, "seq_lens"), (cu_new, B + 1, "cu_new"), (q_pos, T, "q_pos"),
                (kv_rows, T, "kv_rows"), (free_end, 1, "free_end"), (row_base, B, "row_base"),

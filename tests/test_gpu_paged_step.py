@@ -7,7 +7,8 @@ import random
 import pytest
 import torch
 
-from sparse_attention_indexer_kpool_gb300 import ops
+from sparse_attention_indexer_kpool_gb300 import ops, pipeline, synth
+from sparse_attention_indexer_kpool_gb300.synth import Geometry
 from tests import _paged_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -146,13 +147,15 @@ def test_append(L, act, kv):
 
 # ---------------------------------------------------------------- chunk attention
 def make(lens, new, *, Hm=64, L=512, act=BF, kv=BF, ps=64, seed=0, pad=3, q_std=1.0,
-         hidden=math.nan):
-    """A paged cache whose rows outside the sequences hold ``hidden``."""
+         hidden=math.nan, width=0):
+    """A paged cache whose rows outside the sequences hold ``hidden``; the table has room for
+    ``width`` positions at least (wide tables may take another kernel)."""
     g = torch.Generator(device=DEV).manual_seed(seed)
     blocks = [-(-max(t, 0) // ps) for t in lens]
     n_pages = sum(blocks) + 2
     perm = torch.randperm(n_pages, generator=g, device=DEV).to(torch.int32)
-    table = torch.full((len(lens), max(blocks + [1]) + 1), -1, dtype=torch.int32, device=DEV)
+    cols = max(max(blocks + [1]) + 1, -(-width // ps))
+    table = torch.full((len(lens), cols), -1, dtype=torch.int32, device=DEV)
     n = n_pages * ps
     x = torch.randn((n, L), generator=g, device=DEV)
     used = torch.zeros(n, dtype=torch.bool, device=DEV)
@@ -175,6 +178,9 @@ def make(lens, new, *, Hm=64, L=512, act=BF, kv=BF, ps=64, seed=0, pad=3, q_std=
     q = (torch.randn((T, Hm, L), generator=g, device=DEV) * q_std).to(act)
     return dict(q=q, pages=pages, scale=scale, table=table, lens=i32(lens), cu=i32(cu), ps=ps,
                 sm=1.0 / math.sqrt(L), T=T)
+
+
+make_step = make
 
 
 def attend(s, window=0, sinks=0, stream=None, ws=None, out=None, lse=None):
@@ -226,6 +232,24 @@ def test_chunk(Hm, L, act, kv, which):
         check(s, window, sinks)
 
 
+@pytest.mark.parametrize("Hm", [64, 128, 33, 80])
+@pytest.mark.parametrize("which", range(len(LENS)))
+def test_chunk_wide_tables(Hm, which):
+    """Two row blocks share their keys: chunks of two tokens and more (or more than 64 heads)
+    that may see more than 2,048 positions."""
+    lens, new = LENS[which]
+    for j, (window, sinks) in enumerate([(0, 0), (1, 2048), (64, 4000), (100, 1990), (2100, 0),
+                                         (700, 1400), (2 ** 31 - 1, 2 ** 31 - 1)]):
+        ps = (64, 16, 48, 8, 128, 24)[(which + j) % 6]
+        check(make(lens, new, Hm=Hm, ps=ps, seed=which * 10 + j, width=2112, pad=0), window, sinks)
+
+
+def test_chunk_wide_tables_long_windows():
+    s = make([5000, 2600, 2300], [70, 3, 40], seed=16, q_std=2.0)
+    for window, sinks in ((2047, 2), (2100, 5), (2500, 300), (1, 2500), (4990, 1)):
+        check(s, window, sinks)
+
+
 @pytest.mark.parametrize("kv", [BF, F8])
 @pytest.mark.parametrize("B,hi,new", [(1, 9000, 1), (3, 20000, 1), (160, 700, 1), (40, 2000, 3)])
 def test_chunk_decode_split_over_the_card(B, hi, new, kv):
@@ -247,8 +271,8 @@ def test_chunk_many_tokens(kv):
 def test_chunk_rising_and_falling_logits(act, kv, L):
     """Keys whose logits climb (and fall) by hundreds along the sequence: the running
     maximum has to move, far apart tiles must not overflow or vanish."""
-    for sign in (1.0, -1.0):
-        s = make([1300], [4], Hm=16, L=L, act=act, kv=kv, seed=4)
+    for sign, Hm, width in ((1.0, 16, 0), (-1.0, 16, 0), (1.0, 64, 2112), (-1.0, 64, 2112)):
+        s = make([1300], [4], Hm=Hm, L=L, act=act, kv=kv, seed=4, width=width, pad=0)
         ramp = torch.linspace(-6.0, 6.0, 1300, device=DEV) * sign
         p = torch.arange(1300, device=DEV)
         rows = s["table"][0].long()[p // s["ps"]] * s["ps"] + p % s["ps"]
@@ -260,34 +284,39 @@ def test_chunk_rising_and_falling_logits(act, kv, L):
             s["scale"][rows] = sc
         else:
             s["pages"][rows] = x.to(kv)
-        s["q"] = (direction * 2).to(act).expand(s["T"], 16, L).contiguous()
+        s["q"] = (direction * 2).to(act).expand(s["T"], Hm, L).contiguous()
         check(s)
         check(s, 300, 7)
 
 
+@pytest.mark.parametrize("n,window", [(400, 50), (2400, 2060)])
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 16, 512), (F32, F32, 4, 64)])
-def test_chunk_later_tokens_do_not_reach_earlier_ones(act, kv, Hm, L):
+def test_chunk_later_tokens_do_not_reach_earlier_ones(act, kv, Hm, L, n, window):
     """NaN, infinities and the type's largest values in the rows of later tokens, outside
     the window and behind the sequence leave the others as they are."""
     for fill in (math.nan, math.inf, -math.inf, torch.finfo(kv).max):
-        s = make([400], [6], Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=6, hidden=fill)
-        want, want_lse, _ = attend(s, 50, 3)
-        p = torch.arange(400, device=DEV)
+        s = make([n], [6], Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=6, hidden=fill)
+        want, want_lse, _ = attend(s, window, 3)
+        p = torch.arange(n, device=DEV)
         rows = s["table"][0].long()[p // 16] * 16 + p % 16
-        hide = torch.zeros(400, dtype=torch.bool, device=DEV)
-        hide[397:] = True                    # tokens 3, 4, 5 of the chunk
-        hide[3:394 - 50 + 1] = True          # outside every window
+        hide = torch.zeros(n, dtype=torch.bool, device=DEV)
+        hide[n - 3:] = True                  # tokens 3, 4, 5 of the chunk
+        hide[3:n - 6 - window + 1] = True    # outside every window
         s["pages"][rows[hide]] = torch.full((), fill, device=DEV).to(kv)
         if kv == F8:
             s["scale"][rows[hide]] = fill
-        out, lse, _ = attend(s, 50, 3)
+        out, lse, _ = attend(s, window, 3)
         assert torch.equal(out[:3], want[:3]) and torch.equal(lse[:3], want_lse[:3])
         if math.isnan(fill):                 # and it reaches those that see it
             assert torch.isnan(out[3:6].float()).all()
 
 
+@pytest.mark.parametrize("width", [0, 2112])
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 64, 512), (F32, F32, 4, 64)])
-def test_chunk_faults_are_flagged_and_contained(act, kv, Hm, L):
+def test_chunk_faults_are_flagged_and_contained(act, kv, Hm, L, width):
+    def make(*a, **kw):
+        return make_step(*a, **kw, width=width)
+
     s = make([500, 100, 60], [3, 100, 2], Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=7)
     n_pages = s["pages"].shape[0] // 16
     s["table"][0, 3], s["table"][0, 20], s["table"][1, 0] = -1, n_pages, 2 ** 31 - 1
@@ -306,8 +335,46 @@ def test_chunk_faults_are_flagged_and_contained(act, kv, Hm, L):
     assert attend(s)[2] & ops.DEV_BAD_LENGTH
 
 
-def test_chunk_infinite_and_nan_queries_stay_in_their_rows():
-    s = make([300, 40], [5, 3], seed=11)
+@pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 16, 512), (F32, F32, 4, 64)])
+@pytest.mark.parametrize("cols", [3, 140])
+def test_chunk_lengths_past_the_table_cost_no_more_than_it(act, kv, Hm, L, cols):
+    """A length far behind the table's width: flagged, and the tokens see the positions that
+    the table has (with a window that has left them: the sinks alone)."""
+    ps = 16
+    s = make([cols * ps, 40], [1, 40], Hm=Hm, L=L, act=act, kv=kv, ps=ps, seed=17, pad=0)
+    s["table"] = s["table"][:, :cols].contiguous()
+    long = dict(s, lens=i32([2 ** 31 - 1, 40]))
+    for window, sinks in ((0, 0), (2 ** 31 - 1, 0), (1000, 20), (7, 2 ** 31 - 1)):
+        out, lse, st = attend(long, window, sinks)
+        assert st == ops.DEV_BAD_PAGE
+        see = cols * ps if window in (0, 2 ** 31 - 1) else min(sinks, cols * ps)
+        first = dict(s, lens=i32([see, 40]), q=s["q"][:1], cu=i32([0, 1, 1]), T=1)
+        ref.check_attend(out[:1], lse[:1], reference(first), act, L)
+        rest = dict(s, lens=i32([0, 40]), cu=i32([0, 0, 40]), q=s["q"][1:], T=40)
+        ref.check_attend(out[1:], lse[1:], reference(rest, window, sinks), act, L)
+
+
+@pytest.mark.parametrize("kv,Hm,width,ps", [(BF, 64, 0, 64), (BF, 64, 2112, 64), (BF, 16, 0, 5),
+                                            (F8, 64, 0, 64), (F8, 16, 0, 5)])
+def test_chunk_gives_up_and_recovers(kv, Hm, width, ps):
+    """The failure drill: no tile arrives, the first waits run out after a millisecond, the
+    call returns and says so, and the next one is as before."""
+    s = make([700, 300], [20, 30], Hm=Hm, kv=kv, ps=ps, seed=18, width=width)
+    want = attend(s)
+    ops.dsa_set_failure_drill(ops.DSA_DRILL_SKIP_ARM)
+    try:
+        assert attend(s)[2] == 64            # DSA_DEV_TIMEOUT
+    finally:
+        ops.dsa_set_failure_drill(0)
+    got = attend(s)
+    assert got[2] == want[2] == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("width", [0, 2112])
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_chunk_infinite_and_nan_queries_stay_in_their_rows(kv, width):
+    s = make([300, 40], [5, 3], kv=kv, seed=11, width=width)
     want, want_lse, _ = attend(s)
     s["q"][1, 7] = math.nan
     s["q"][6, 0, 3] = math.inf
@@ -319,7 +386,7 @@ def test_chunk_infinite_and_nan_queries_stay_in_their_rows():
 
 
 def test_chunk_same_bits_every_time_and_beside_other_calls():
-    a = make([3000, 20, 777], [5, 20, 300], seed=12)
+    a = make([3000, 20, 777], [5, 20, 300], seed=12)   # (two row blocks share their keys)
     b = make([90, 9000], [1, 1], kv=F8, seed=13)
     want_a, want_b = attend(a), attend(b)
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -410,3 +477,82 @@ def test_step_captured_and_replayed(kv):
     assert bool(((have - x[3].double()).abs() <= tol).all())
     chk = dict(s, T=B)
     ref.check_attend(s["out"], s["lse"], reference(chk), BF, L)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_step_as_a_serving_loop_runs_it(e4m3):
+    """The framework's own step (pipeline.PagedStep): a plan with the slots of the key cache,
+    the append, the dense attention, and the selection with its attention on the plan's
+    sequences and positions.  A chunk first, then two decode steps."""
+    geo = Geometry(D=128, H=32, kpool=4, select_k=64, out_width=320, Hm=64, L=512, dtype="bf16")
+    lengths, ps = [1203, 23, 50], 16
+    new = [[5, 20, 1], [1, 1, 1], [1, 1, 1]]           # the rest is in the cache before
+    ctx0 = [n - sum(s[b] for s in new) for b, n in enumerate(lengths)]
+    bt = synth.make_batch(geo, lengths, [3, 0, 1], device=DEV, seed=19)
+    full = synth.paged_cache(bt.kv, bt.cu_seqlens, ps, e4m3=e4m3, seed=20)
+    # the cache as it was before the steps: their rows and pages are not there yet
+    cu = bt.cu_seqlens.tolist()
+    pages = torch.zeros_like(full.pages.view(torch.uint8)).view(full.pages.dtype)
+    scale = None if full.row_scale is None else torch.zeros_like(full.row_scale)
+    table, free = torch.full_like(full.block_table, -1), []
+    for b in range(3):
+        held = -(-ctx0[b] // ps)
+        table[b, :held] = full.block_table[b, :held]
+        p = torch.arange(ctx0[b], device=DEV)
+        rows = table[b].long()[p // ps] * ps + p % ps
+        pages.view(torch.uint8)[rows] = full.pages.view(torch.uint8)[rows]
+        if scale is not None:
+            scale[rows] = full.row_scale[rows]
+        free += full.block_table[b, held:-(-lengths[b] // ps)].tolist()
+    cache = synth.PagedCache(pages, scale, table, i32(ctx0), ps)
+    step = pipeline.PagedStep.alloc(cache, i32(free + [0]), 26, 64, bt=bt)
+    buf = pipeline.LayerBuffers.alloc(bt)
+    pipeline.compress(bt, buf)                         # (pools by their tokens: later ones hidden)
+    g = torch.Generator(device=DEV).manual_seed(21)
+    done = list(ctx0)
+    for n in new:
+        T = sum(n)
+        pipeline.plan_step(cache, step, i32(n), row_base=bt.cu_seqlens[:3].contiguous())
+        pos = [done[b] + i for b in range(3) for i in range(n[b])]
+        seq = [b for b in range(3) for _ in range(n[b])]
+        done = [d + k for d, k in zip(done, n)]
+        assert cache.seq_lens.tolist() == done
+        assert step.q_seq[:T].tolist() == seq and step.q_pos[:T].tolist() == pos
+        keys = [cu[b] + p for b, p in zip(seq, pos)]
+        assert step.key_rows.tolist() == keys + [-1] * (26 - T)
+        x = torch.zeros((26, 512), dtype=BF, device=DEV)
+        x[:T] = bt.kv[torch.tensor(keys, device=DEV)]
+        q_lat = torch.randn((26, 64, 512), generator=g, device=DEV).to(BF)
+        pipeline.append_step(cache, step, x)
+        pipeline.attend_step(cache, step, q_lat, bt.sm_scale)
+        torch.cuda.synchronize()
+        vals = ref.values(cache.pages, cache.row_scale)
+        want = ref.attend(q_lat, vals, cache.block_table, cache.seq_lens, ps, step.cu_new, 0, 0,
+                          bt.sm_scale)
+        live = torch.arange(T, device=DEV)
+        ref.check_attend(step.out, step.lse, want, BF, 512, rows=live)
+        # the selection of the same tokens, and its attention
+        q = torch.randn((26, 32, 128), generator=g, device=DEV).to(BF)
+        w = torch.randn((26, 32), generator=g, device=DEV)
+        pipeline.select_step(bt, buf, step, q, w)
+        pipeline.attend_selected_step(cache, step, q_lat, bt.sm_scale)
+        torch.cuda.synchronize()
+        ids = step.token_ids.tolist()
+        assert all(t == -1 for row in ids[T:] for t in row)
+        rows64 = []
+        for r in range(T):
+            t = torch.tensor([t for t in ids[r] if t >= 0], dtype=torch.long, device=DEV)
+            assert t.numel() == 0 or int(t.max()) <= pos[r]
+            assert t.numel() >= min(256, (pos[r] + 1 - bt.pads[seq[r]]) // 4 * 4)
+            rows64.append(cache.block_table[seq[r]].long()[t // ps] * ps + t % ps)
+        # the same formula over the selected rows, one row of pages a token
+        width = max(len(r) for r in rows64)
+        one = torch.full((T, width), -1, dtype=torch.int32, device=DEV)
+        for r, rr in enumerate(rows64):
+            one[r, :len(rr)] = rr.to(torch.int32)
+        want = ref.attend(q_lat[:T], vals, one, i32([len(r) for r in rows64]), 1,
+                          i32(list(range(T + 1))), 0, 0, bt.sm_scale)
+        ref.check_attend(step.out[:T], step.lse[:T], want, BF, 512)
+    assert int(step.status.item()) == 0 and int(buf.status.item()) == 0
+    assert cache.block_table.tolist() == full.block_table.tolist()
+    assert step.free_begin.item() == len(free)
