@@ -350,11 +350,27 @@ __device__ __forceinline__ bool vote_soft(bool v) {  // whether any of them says
   return r != 0;
 }
 
+// A chunk's output columns of a thread's heads: the sum of kParts accumulators side by
+// side (kN columns each).
+template <int kN, int kParts>
+__device__ __forceinline__ void load_o(uint32_t to, int mc, int hq, float (&o)[kN / 2]) {
+  constexpr int kW = kN / 2;
+  const uint32_t ta = to + (uint32_t)(mc * kParts * kN + hq * kW);
+  tmem_ldw<kW>(ta, o);
+#pragma unroll
+  for (int k = 1; k < kParts; ++k) {
+    float x[kW];
+    tmem_ldw<kW>(ta + k * kN, x);
+#pragma unroll
+    for (int i = 0; i < kW; ++i) o[i] += x[i];
+  }
+}
+
 // A segment's end, by the eight softmax warps (lane quarter qw, heads kN / 2 hq ..):
 // a row tile's rows, normalised by inv[head]; O^T (kN columns a chunk of 128 latent
 // columns) from TMEM at `to`.  A lane pair holds two latent columns of every head:
 // each lane of the pair stores both columns of one of two heads.
-template <int kN>
+template <int kN, int kParts = 1>
 __device__ __forceinline__ void store_rows(const Params& p, const float* inv, uint32_t to,
                                            long long row0, int heads, int qw, int hq, int lane) {
   constexpr int kW = kN / 2;
@@ -365,7 +381,7 @@ __device__ __forceinline__ void store_rows(const Params& p, const float* inv, ui
 #pragma unroll 1
   for (int mc = 0; mc < 4; ++mc) {
     float o[kW];
-    tmem_ldw<kW>(to + (uint32_t)(mc * kN + hq * kW), o);
+    load_o<kN, kParts>(to, mc, hq, o);
     __nv_bfloat16* dst =
         p.out + (row0 + hq * kW + (upper ? 1 : 0)) * kL + mc * 128 + qw * 32 + (lane & ~1);
 #pragma unroll
@@ -379,7 +395,7 @@ __device__ __forceinline__ void store_rows(const Params& p, const float* inv, ui
   }
 }
 // an unnormalised part of a row tile, for the join
-template <int kN>
+template <int kN, int kParts = 1>
 __device__ __forceinline__ void store_part(const Params& p, int slot, uint32_t to, int heads,
                                            int qw, int hq, int lane) {
   constexpr int kW = kN / 2;
@@ -387,7 +403,7 @@ __device__ __forceinline__ void store_part(const Params& p, int slot, uint32_t t
 #pragma unroll 1
   for (int mc = 0; mc < 4; ++mc) {
     float o[kW];
-    tmem_ldw<kW>(to + (uint32_t)(mc * kN + hq * kW), o);
+    load_o<kN, kParts>(to, mc, hq, o);
 #pragma unroll
     for (int i = 0; i < kW; ++i)
       if (hq * kW + i < heads) dst[(long long)i * kL + mc * 128] = o[i];

@@ -60,11 +60,16 @@ struct Ctl {
 template <int kN>
 struct Smem {
   static constexpr int kQBlock = kN * 128;              // kN heads x 128 codes
-  static constexpr int kQPart = 4 * kQBlock;            // hi, lo
+  // One MMA takes both parts of the queries as 2 kN rows, [block][part][head], and the
+  // three parts of 32 heads' weights as 96 columns of P; each part has its own columns
+  // of the result, which the softmax (and the end) adds.  (64 heads' outputs in three
+  // parts do not fit TMEM: there the parts add up in the accumulator.)
+  static constexpr int kOParts = kN == 32 ? 3 : 1;
+  static constexpr uint32_t kSCols = 2 * kN, kOCols = kOParts * kN;  // of a stage, of a chunk
   static constexpr int kPPart = kKeys * kN;             // a weight's part, 1 byte each
   static constexpr size_t kKv = 0;
   static constexpr size_t kQ = (size_t)kStages * kStage;
-  static constexpr size_t kP = kQ + 2 * (size_t)kQPart;
+  static constexpr size_t kP = kQ + 8 * (size_t)kQBlock;
   static constexpr size_t kCtl = kP + 3 * (size_t)kPPart;
   static constexpr size_t kBytes = 1024 + kCtl + sizeof(Ctl);
 };
@@ -166,8 +171,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Smem<kN>;
   constexpr int kW = kN / 2;  // heads per softmax thread
   constexpr int kTma0 = kSoftThreads / 32, kMmaWarp = kTma0 + kTmaWarps;
-  constexpr int kTmemCols = kN == 64 ? 512 : 256;  // S^T (2 kN), O^T (4 kN)
-  constexpr uint32_t kOCol = kStages * kN;
+  constexpr uint32_t kOCol = kStages * S::kSCols;
+  constexpr int kTmemCols = 512;
+  static_assert(kOCol + 4 * S::kOCols <= kTmemCols, "TMEM columns");
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl& c = *reinterpret_cast<Ctl*>(sb + S::kCtl);
@@ -263,7 +269,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         float e[kW];
         // z = S * query scale * row scale * softmax scale
         auto logits = [&]() {
-          tmem_ldw<kW>(tl + (uint32_t)(st * kN + hq * kW), e);
+          const uint32_t ts = tl + st * S::kSCols + (uint32_t)(hq * kW);
+          tmem_ldw<kW>(ts, e);
+#pragma unroll
+          for (int g = 0; g < kW; g += 16) {
+            float lo[16];
+            tmem_ld16(ts + kN + g, lo);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) add2(e[g + i], e[g + i + 1], lo[i], lo[i + 1]);
+          }
 #pragma unroll
           for (int q = 0; q < kW / 4; ++q) {
             const float4 s4 = sq4[q];
@@ -359,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (full && c.raise && v > w.ta) {
           tc_fence_after();
 #pragma unroll 1
-          for (int mc = 0; mc < 4; ++mc) {
+          for (int mc = 0; mc < 4 * S::kOParts; ++mc) {
             float o[kW];
             const uint32_t ta = tl + kOCol + (uint32_t)(mc * kN + hq * kW);
             tmem_ldw<kW>(ta, o);
@@ -427,9 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       sync_soft();
       if (whole)
-        store_rows<kN>(p, c.l, tl + kOCol, row0, heads, qw, hq, lane);
+        store_rows<kN, S::kOParts>(p, c.l, tl + kOCol, row0, heads, qw, hq, lane);
       else
-        store_part<kN>(p, 2 * blockIdx.x + (begins ? 1 : 0), tl + kOCol, heads, qw, hq, lane);
+        store_part<kN, S::kOParts>(p, 2 * blockIdx.x + (begins ? 1 : 0), tl + kOCol, heads, qw, hq, lane);
       tc_fence_before();  // O^T is read: the next segment's P releases it
     }
     if (!ok) hd = Header{-1, -1, 0, 0};
@@ -461,9 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, free_q);
         if (!ok) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&c.q_full, 2 * S::kQPart);
+          mbar_arrive_expect_tx(&c.q_full, 8 * S::kQBlock);
           for (int i = 0; i < 8; ++i)
-            tma_load_2d(sb + S::kQ + i * S::kQBlock, &q_map, i * 64, w.token * p.Hm + w.h0 * kN,
+            tma_load_2d(sb + S::kQ + (2 * (i & 3) + (i >> 2)) * S::kQBlock, &q_map, i * 64, w.token * p.Hm + w.h0 * kN,
                         &c.q_full);
         }
         ++segs;
@@ -509,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp && issue) {
     // ================= MMA =================
-    constexpr uint32_t id_s = idesc_f8(kKeys, kN, false, false, false);
-    constexpr uint32_t id_o = idesc_f8(128, kN, true, true, true);
+    constexpr uint32_t id_s = idesc_f8(kKeys, 2 * kN, false, false, false);
+    constexpr uint32_t id_o = idesc_f8(128, S::kOCols, true, true, true);
     const uint32_t kvb = smem_u32(sb + S::kKv), qb = smem_u32(sb + S::kQ);
     const uint32_t pb = smem_u32(sb + S::kP);
     // (a descriptor's low bits are the address in 16-byte units: steps add constants)
@@ -542,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kr = 0; kr < 4; ++kr)
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-              umma_f8_elect(tmem + kOCol + mc * kN, d_v + ((mc * kBlock + kr * 4096) >> 4),
+            for (int k = 0; k < 3 / S::kOParts; ++k)
+              umma_f8_elect(tmem + kOCol + mc * S::kOCols, d_v + ((mc * kBlock + kr * 4096) >> 4),
                             d_p + ((k * S::kPPart + kr * 32 * kN) >> 4), id_o,
                             (kr | k) ? 1u : more);
           umma_commit_elect(&c.empty[no & 1][mc]);
@@ -571,12 +585,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t off = (j & 3) * 32, part = j >> 2;
-              umma_f8_elect(tmem + (ns & 1) * kN, d_k + ((blk * kBlock + off) >> 4),
-                            d_q + ((part * S::kQPart + blk * S::kQBlock + off) >> 4), id_s,
+            for (int j = 0; j < 4; ++j)
+              umma_f8_elect(tmem + (ns & 1) * S::kSCols, d_k + ((blk * kBlock + j * 32) >> 4),
+                            d_q + ((blk * 2 * S::kQBlock + j * 32) >> 4), id_s,
                             (blk | j) ? 1u : 0u);
-            }
           }
           if (!ok) break;
           umma_commit_elect(&c.s_full[ns & 1]);
