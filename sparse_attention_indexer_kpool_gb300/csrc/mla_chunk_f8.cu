@@ -16,7 +16,7 @@
 //     E5M2's least normal value, by 2^-17 a part, 2^-23 of a weight at the reference in
 //     all.  The sums keep the unrounded fp32 weights.
 // The reference m of a head is kept for u rather than for the bare weight, so that u
-// stays below 2^6 and its parts inside E5M2's range; a row scale counts there as at
+// stays below 2^7 and its parts inside E5M2's range; a row scale counts there as at
 // least 2^-60, which bounds the bare weight as well.
 //
 // Why.  Widening the codes to bf16 in shared memory first took 1,960 cycles of
@@ -39,7 +39,7 @@ constexpr int kStages = 2;
 constexpr int kSoftThreads = 256;
 constexpr int kTmaWarps = 2;
 constexpr int kThreads = kSoftThreads + 32 * (kTmaWarps + 1);
-constexpr float kRaise8 = 6.f;            // base-2 growth of u that raises a reference
+constexpr float kRaise8 = 7.f;            // base-2 growth of u that raises a reference
 constexpr float kUp = 256.f;              // weights in E5M2 are scaled by 2^8
 constexpr float kLeastLog = -60.f;
 
@@ -532,8 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t d_v0 = umma_desc_sw128(kvb, kBlock, 1024);
     const uint64_t d_p = kN == 64 ? umma_desc_sw64(pb, S::kPPart, 512)
                                   : umma_desc_sw32(pb, S::kPPart, 256);
-    // Two streams over the same tiles: scores as soon as a stage holds keys, outputs as
-    // soon as a tile's weights are there; outputs first (they free the stage).
+    // Two streams over the same tiles: scores block by block as a stage's keys arrive,
+    // outputs as soon as a tile's weights are there; outputs first (they free the
+    // stage), also between the blocks of a tile whose keys are still under way.
     Walk<kKeys, false> wo(p, hb, c.start, units);
     auto segment = [](Walk<kKeys, false>& x) {
       while (x.next())
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0;
     };
     bool ok = true, left_s = segment(w), left_o = segment(wo), have_q = false;
-    int ns = 0, no = 0, vs = w.ta, vo = wo.ta, seg = 0;
+    int ns = 0, blk = 0, no = 0, vs = w.ta, vo = wo.ta, seg = 0;
     unsigned long long since = 0;  // time of the first idle look
     while (left_o) {
       if (no < ns && ready(&c.p_full, no & 1)) {
@@ -574,31 +575,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (left_s && ns - no < kStages) {
         have_q = have_q || ready(&c.q_full, seg & 1);
         // (the stage's keys imply that its last outputs are done: its scores are free)
-        if (have_q && ready(&c.full[ns & 1][0], (ns >> 1) & 1)) {
-          const uint64_t d_k = d_k0 + (uint32_t)((ns & 1) * (kStage >> 4));
+        if (have_q && ready(&c.full[ns & 1][blk], (ns >> 1) & 1)) {
+          const uint64_t d_k =
+              d_k0 + (uint32_t)((ns & 1) * (kStage >> 4) + blk * (kBlock >> 4));
+          const uint64_t d_qb = d_q + (uint32_t)(blk * (2 * S::kQBlock >> 4));
+          tc_fence_after();
 #pragma unroll
-          for (int blk = 0; blk < 4; ++blk) {
-            if (blk > 0) {
-              const bool here = wait_on(&c.full[ns & 1][blk], (ns >> 1) & 1, dead, wait_ns);
-              ok = __all_sync(0xffffffffu, here);
-              if (!ok) break;
+          for (int j = 0; j < 4; ++j)
+            umma_f8_elect(tmem + (ns & 1) * S::kSCols, d_k + (j * 32 >> 4), d_qb + (j * 32 >> 4),
+                          id_s, (blk | j) ? 1u : 0u);
+          if (++blk == 4) {
+            blk = 0;
+            umma_commit_elect(&c.s_full[ns & 1]);
+            ++ns;
+            if (++vs == w.tb) {
+              umma_commit_elect(&c.q_empty);
+              ++seg;
+              left_s = segment(w);
+              vs = w.ta;
+              have_q = false;
             }
-            tc_fence_after();
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              umma_f8_elect(tmem + (ns & 1) * S::kSCols, d_k + ((blk * kBlock + j * 32) >> 4),
-                            d_q + ((blk * 2 * S::kQBlock + j * 32) >> 4), id_s,
-                            (blk | j) ? 1u : 0u);
-          }
-          if (!ok) break;
-          umma_commit_elect(&c.s_full[ns & 1]);
-          ++ns;
-          if (++vs == w.tb) {
-            umma_commit_elect(&c.q_empty);
-            ++seg;
-            left_s = segment(w);
-            vs = w.ta;
-            have_q = false;
           }
           since = 0;
           continue;
@@ -654,7 +650,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.prefetch = a.T <= 4 * a.B;
   p.box_log = box_log_of(a.kv.page_size);
   p.o_scale = 1.f / kUp;
-  p.extra = 2;
+  p.extra = 1;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)n_cta * 2 * kN * kL);
   p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)n_cta * 2 * kN);
