@@ -26,29 +26,71 @@ namespace {
 constexpr int kChunkThreads = 128, kChunkHeads = 4, kChunkTile = 64;
 constexpr int kChunkCols = 1024 / kChunkThreads;  // latent columns of a thread at most
 constexpr int kChunkFloats = 16384;               // of a tile's rows
-// keys of a tile: the rows (one float of padding each: columns of 32 rows in different
-// banks) fit kChunkFloats
+// A row in shared memory is L + 4 floats apart from the next (L is a multiple of 8: an
+// odd number of 16-byte pieces), so that eight threads' pieces of eight rows lie in
+// different banks, as those of one row do.
+__host__ __device__ constexpr int chunk_pitch(int L) { return L + 4; }
 __host__ __device__ constexpr int chunk_tile(int L) {
-  return kChunkFloats / (L + 1) < kChunkTile ? kChunkFloats / (L + 1) : kChunkTile;
+  return kChunkFloats / chunk_pitch(L) < kChunkTile ? kChunkFloats / chunk_pitch(L) : kChunkTile;
 }
 
-__device__ __forceinline__ float page_value(const PagedKv& pk, long long row, int d, int L) {
-  const long long o = row * L + d;
-  if (pk.kv_dtype == DSA_BF16)
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(pk.pages)[o]);
-  if (pk.kv_dtype == DSA_F32) return static_cast<const float*>(pk.pages)[o];
-  const __half_raw h =
-      __nv_cvt_fp8_to_halfraw(static_cast<const __nv_fp8_storage_t*>(pk.pages)[o], __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h)) * pk.row_scale[row];
-}
+// Eight elements of a cache row.
+template <int kKv> struct Piece;
+template <> struct Piece<DSA_BF16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const PagedKv& kv, long long row, int at, int L) {
+    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(kv.pages) +
+                                             row * L + at));
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16lo(u[i]);
+      f[2 * i + 1] = bf16hi(u[i]);
+    }
+  }
+};
+template <> struct Piece<DSA_F32> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const PagedKv& kv, long long row, int at, int L) {
+    const float4* p =
+        reinterpret_cast<const float4*>(static_cast<const float*>(kv.pages) + row * L + at);
+    a = __ldg(p);
+    b = __ldg(p + 1);
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
+template <> struct Piece<DSA_FP8_E4M3> {
+  uint2 v;
+  float s;
+  __device__ __forceinline__ void load(const PagedKv& kv, long long row, int at, int L) {
+    v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(kv.pages) + row * L + at));
+    s = __ldg(kv.row_scale + row);
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    const uint32_t u[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)u[i], __NV_E4M3);
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      f[2 * i] = x.x * s;
+      f[2 * i + 1] = x.y * s;
+    }
+  }
+};
 
-template <typename T>
+template <typename T, int kKv>
 __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs a) {
-  extern __shared__ float rows[];  // [tile][L + 1], then the queries [kChunkHeads][L]
-  __shared__ float sz[kChunkHeads][kChunkTile];
-  __shared__ int srow[kChunkTile];
-  __shared__ float s_m[kChunkHeads], s_l[kChunkHeads], s_alpha[kChunkHeads];
-  const int L = a.L, Lp = a.L + 1, kt = chunk_tile(a.L);
+  extern __shared__ __align__(16) float rows[];  // [tile][pitch], then queries [kChunkHeads][L]
+  __shared__ __align__(16) float sz[kChunkTile][kChunkHeads];
+  __shared__ int srow[2][kChunkTile];
+  __shared__ float s_m[kChunkHeads], s_l[kChunkHeads];
+  __shared__ __align__(16) float s_alpha[kChunkHeads];
+  const int L = a.L, Lp = chunk_pitch(a.L), kt = chunk_tile(a.L);
   float* sq = rows + kt * Lp;
   pdl_wait();
   pdl_launch_dependents();
@@ -89,76 +131,104 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
     s_m[tid] = -INFINITY;
     s_l[tid] = 0.f;
   }
+  // thread j: the cache row of the tile's position j (-1: no page)
+  auto find_row = [&](int v, int* dst) {
+    if (tid >= kt || v + tid >= nv) return;
+    const int p = v + tid < s0 ? v + tid : lo + (v + tid - s0);
+    const int page = a.kv.block_table[(long long)b * a.kv.max_pages + p / a.kv.page_size];
+    const bool ok = page >= 0 && page < a.kv.n_pages;
+    if (!ok && reports) flag(a.status, DSA_DEV_BAD_PAGE);
+    dst[tid] = ok ? page * a.kv.page_size + p % a.kv.page_size : -1;
+  };
+  find_row(0, srow[0]);
   float acc[kChunkHeads][kChunkCols];
 #pragma unroll
   for (int h = 0; h < kChunkHeads; ++h)
 #pragma unroll
     for (int c = 0; c < kChunkCols; ++c) acc[h][c] = 0.f;
 
-  for (int v0 = 0; v0 < nv; v0 += kt) {
-    const int n = min(kt, nv - v0);
+  const int pieces = L / 8;
+  for (int v0 = 0, par = 0; v0 < nv; v0 += kt, par ^= 1) {
+    const int n = min(kt, nv - v0), total = n * pieces;
     __syncthreads();
-    if (tid < n) {
-      const int v = v0 + tid, p = v < s0 ? v : lo + (v - s0);
-      const int blk = p / a.kv.page_size;
-      const int page =
-          blk < a.kv.max_pages ? a.kv.block_table[(long long)b * a.kv.max_pages + blk] : -1;
-      const bool ok = page >= 0 && page < a.kv.n_pages;
-      if (!ok && reports) flag(a.status, DSA_DEV_BAD_PAGE);
-      srow[tid] = ok ? page * a.kv.page_size + p % a.kv.page_size : -1;
+    for (int i0 = tid; i0 < total; i0 += 4 * kChunkThreads) {
+      Piece<kKv> x[4];  // four loads on their way at once
+      int row[4], j[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kChunkThreads;
+        j[u] = i / pieces;
+        row[u] = i < total ? srow[par][j[u]] : -1;
+        if (row[u] >= 0) x[u].load(a.kv, row[u], (i - j[u] * pieces) * 8, L);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kChunkThreads;
+        if (i >= total) break;
+        float f[8];
+        x[u].values(f);
+        float4* dst = reinterpret_cast<float4*>(rows + j[u] * Lp + (i - j[u] * pieces) * 8);
+        const bool some = row[u] >= 0;  // (a position without a page: zeros)
+        dst[0] = some ? make_float4(f[0], f[1], f[2], f[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        dst[1] = some ? make_float4(f[4], f[5], f[6], f[7]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     }
-    __syncthreads();
-    for (int j = warp; j < n; j += kChunkThreads / 32) {  // (a position without a page: zeros)
-      const int row = srow[j];
-      for (int d = lane; d < L; d += 32)
-        rows[j * Lp + d] = row >= 0 ? page_value(a.kv, row, d, L) : 0.f;
-    }
+    find_row(v0 + kt, srow[par ^ 1]);  // the next tile's, under this one's work
     __syncthreads();
     for (int i = tid; i < n * kChunkHeads; i += kChunkThreads) {
-      const int j = i % n, h = i / n;
-      const float* x = rows + j * Lp;
-      const float* y = sq + h * L;
-      float d4[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int d = 0; d < L; d += 8) {  // L is a multiple of 8
-#pragma unroll
-        for (int u = 0; u < 8; ++u) d4[u & 3] = fmaf(x[d + u], y[d + u], d4[u & 3]);
+      const int h = i / n, j = i - h * n;
+      const float4* x = reinterpret_cast<const float4*>(rows + j * Lp);
+      const float4* y = reinterpret_cast<const float4*>(sq + h * L);
+      float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < L / 4; ++k) {
+        const float4 xv = x[k], yv = y[k];
+        d.x = fmaf(xv.x, yv.x, d.x);
+        d.y = fmaf(xv.y, yv.y, d.y);
+        d.z = fmaf(xv.z, yv.z, d.z);
+        d.w = fmaf(xv.w, yv.w, d.w);
       }
-      sz[h][j] = srow[j] >= 0 ? ((d4[0] + d4[1]) + (d4[2] + d4[3])) * a.sm_scale : -INFINITY;
+      sz[j][h] = srow[par][j] >= 0 ? ((d.x + d.y) + (d.z + d.w)) * a.sm_scale : -INFINITY;
     }
     __syncthreads();
     if (warp < nh) {  // warp = head: two positions a lane
-      const float za = lane < n ? sz[warp][lane] : -INFINITY;
-      const float zb = lane + 32 < n ? sz[warp][lane + 32] : -INFINITY;
+      const float za = lane < n ? sz[lane][warp] : -INFINITY;
+      const float zb = lane + 32 < n ? sz[lane + 32][warp] : -INFINITY;
       const float m_old = s_m[warp], m = fmaxf(m_old, warp_max(fmaxf(za, zb)));
       const float ref = m == -INFINITY ? 0.f : m;
       const float ea = expf(za - ref), eb = expf(zb - ref);
       const float sum = warp_sum(ea + eb);
       __syncwarp();
-      sz[warp][lane] = ea;
-      sz[warp][lane + 32] = eb;
+      sz[lane][warp] = ea;
+      sz[lane + 32][warp] = eb;
       if (lane == 0) {
         const float alpha = expf(m_old - ref);  // 0 before the first visible position
         s_m[warp] = m;
         s_l[warp] = s_l[warp] * alpha + sum;
         s_alpha[warp] = alpha;
       }
+    } else {  // no such head
+      sz[lane][warp] = sz[lane + 32][warp] = 0.f;
+      if (lane == 0) s_alpha[warp] = 0.f;
     }
     __syncthreads();
-#pragma unroll
-    for (int h = 0; h < kChunkHeads; ++h) {
-      const float alpha = h < nh ? s_alpha[h] : 0.f;
-#pragma unroll
-      for (int c = 0; c < kChunkCols; ++c) acc[h][c] *= alpha;
-    }
+    const float4 alpha = *reinterpret_cast<const float4*>(s_alpha);
 #pragma unroll
     for (int c = 0; c < kChunkCols; ++c) {
       const int d = c * kChunkThreads + tid;
       if (d >= L) break;
-#pragma unroll 4
+      acc[0][c] *= alpha.x;
+      acc[1][c] *= alpha.y;
+      acc[2][c] *= alpha.z;
+      acc[3][c] *= alpha.w;
+#pragma unroll 8
       for (int j = 0; j < n; ++j) {
         const float x = rows[j * Lp + d];
-#pragma unroll
-        for (int h = 0; h < kChunkHeads; ++h) acc[h][c] = fmaf(sz[h][j], x, acc[h][c]);
+        const float4 w = *reinterpret_cast<const float4*>(sz[j]);
+        acc[0][c] = fmaf(w.x, x, acc[0][c]);
+        acc[1][c] = fmaf(w.y, x, acc[1][c]);
+        acc[2][c] = fmaf(w.z, x, acc[2][c]);
+        acc[3][c] = fmaf(w.w, x, acc[3][c]);
       }
     }
   }
@@ -175,6 +245,13 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
     }
     if (a.lse && tid == 0) a.lse[qh + h] = l == 0.f ? -INFINITY : s_m[h] + logf(l);
   }
+}
+
+template <typename T>
+auto simt_kernel(int kv_dtype) {
+  return kv_dtype == DSA_BF16  ? mla_chunk_simt_kernel<T, DSA_BF16>
+         : kv_dtype == DSA_F32 ? mla_chunk_simt_kernel<T, DSA_F32>
+                               : mla_chunk_simt_kernel<T, DSA_FP8_E4M3>;
 }
 
 }  // namespace
@@ -223,12 +300,12 @@ int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   cfg.gridDim = dim3(a.T, (a.Hm + kChunkHeads - 1) / kChunkHeads, 1);
   cfg.blockDim = dim3(kChunkThreads, 1, 1);
   cfg.dynamicSmemBytes =
-      ((size_t)chunk_tile(a.L) * (a.L + 1) + (size_t)kChunkHeads * a.L) * sizeof(float);
+      ((size_t)chunk_tile(a.L) * chunk_pitch(a.L) + (size_t)kChunkHeads * a.L) * sizeof(float);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  auto kernel = a.dtype == DSA_BF16 ? mla_chunk_simt_kernel<__nv_bfloat16>
-                                    : mla_chunk_simt_kernel<float>;
+  auto kernel = a.dtype == DSA_BF16 ? simt_kernel<__nv_bfloat16>(a.kv.kv_dtype)
+                                    : simt_kernel<float>(a.kv.kv_dtype);
   if (cfg.dynamicSmemBytes > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)cfg.dynamicSmemBytes) != cudaSuccess)
