@@ -23,7 +23,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kChunkThreads = 128, kChunkHeads = 4, kChunkTile = 64;
+constexpr int kChunkThreads = 128, kChunkHeads = 4, kChunkTile = 128;
 constexpr int kChunkCols = 1024 / kChunkThreads;  // latent columns of a thread at most
 constexpr int kChunkFloats = 16384;               // of a tile's rows
 // A row in shared memory is L + 4 floats apart from the next (L is a multiple of 8: an
@@ -191,16 +191,22 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
       sz[j][h] = srow[par][j] >= 0 ? ((d.x + d.y) + (d.z + d.w)) * a.sm_scale : -INFINITY;
     }
     __syncthreads();
-    if (warp < nh) {  // warp = head: two positions a lane
-      const float za = lane < n ? sz[lane][warp] : -INFINITY;
-      const float zb = lane + 32 < n ? sz[lane + 32][warp] : -INFINITY;
-      const float m_old = s_m[warp], m = fmaxf(m_old, warp_max(fmaxf(za, zb)));
+    if (warp < nh) {  // warp = head: four positions a lane
+      float z[kChunkTile / 32], top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int u = 0; u < kChunkTile / 32; ++u) {
+        z[u] = lane + 32 * u < n ? sz[lane + 32 * u][warp] : -INFINITY;
+        top = fmaxf(top, z[u]);
+      }
+      const float m_old = s_m[warp], m = fmaxf(m_old, warp_max(top));
       const float ref = m == -INFINITY ? 0.f : m;
-      const float ea = expf(za - ref), eb = expf(zb - ref);
-      const float sum = warp_sum(ea + eb);
-      __syncwarp();
-      sz[lane][warp] = ea;
-      sz[lane + 32][warp] = eb;
+#pragma unroll
+      for (int u = 0; u < kChunkTile / 32; ++u) {
+        z[u] = expf(z[u] - ref);
+        sum += z[u];
+        sz[lane + 32 * u][warp] = z[u];
+      }
+      sum = warp_sum(sum);
       if (lane == 0) {
         const float alpha = expf(m_old - ref);  // 0 before the first visible position
         s_m[warp] = m;
@@ -208,7 +214,8 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
         s_alpha[warp] = alpha;
       }
     } else {  // no such head
-      sz[lane][warp] = sz[lane + 32][warp] = 0.f;
+#pragma unroll
+      for (int u = 0; u < kChunkTile / 32; ++u) sz[lane + 32 * u][warp] = 0.f;
       if (lane == 0) s_alpha[warp] = 0.f;
     }
     __syncthreads();
