@@ -451,104 +451,178 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
   }
 }
 
-// Join the partials of the row tiles that were split over workers, in their order:
-// block (g, y) takes the tile that worker g began, rows 8 y ..; a warp takes half of
-// a row's latent columns (two 16-byte pieces a lane).  The workers behind
-// g that hold parts of the tile are found 32 at a time, a lane each, with their
-// maxima and sums; then eight partial rows are on their way at once, so that even one
-// token split over every SM joins in a few round trips to memory.
-template <int kRows, bool kPair>
-__global__ void __launch_bounds__(512)
-    mla_chunk_join_kernel(const Params p, int workers) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.y * 8 + (warp >> 1), col = (warp & 1) * 256 + lane * 4;
-  const int tile = p.head[g].start_tile;
-  if (tile < 0) return;
-  int token, head;
-  if (kPair) {
-    token = tile >> 1;
-    head = h;
-    if (p.Hm <= 64 && h >= 64) {  // the second token's rows
-      if (!(tile & 1)) return;
-      ++token;
-      head = h - 64;
-    }
-  } else {
-    const int hb = (p.Hm + kRows - 1) / kRows;
-    token = tile / hb;
-    head = (tile - token * hb) * kRows + h;
-  }
-  if (head >= p.Hm) return;
-  float mx = -INFINITY, den = 0.f;
+// Join the partials of the row tiles that were split over workers, in their order.  A
+// tile's workers are neighbours: every block reads all headers and lists the workers that
+// began a tile.  A piece of the work is half of a row (two 16-byte pieces a lane); the
+// pieces of all tiles are dealt out to the warps of two blocks an SM, so that one wave of
+// blocks does it.  Where few tiles leave many partials (16,384 keys of one token: 128 of
+// 128 KB) a block takes a piece and each of its warps a sixteenth of its partials.
+// Bound by round trips to memory (headers, maxima and sums, partial rows) and, where
+// every worker left partials, by their 128 KB a part.
+constexpr int kMaxWorkers = 256;
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
+struct Joined {
+  float mx, den;
   float4 acc[2];
-  acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-  bool more = true;
-  for (int s0 = g; more; s0 += 32) {
-    // lane: worker s0 + lane; those up to the one that ends the tile
+};
+// The parts s0 .. s1 - 1 of row h, latent columns col .. and col + 128 ..: 32 workers' maxima
+// and sums at once, a lane each, then four partial rows on their way at once.
+template <int kRows>
+__device__ __forceinline__ Joined join_parts(const Params& p, const Header* heads, int g0, int s0,
+                                             int s1, int h, int col, int lane) {
+  Joined j;
+  j.mx = -INFINITY;
+  j.den = 0.f;
+  j.acc[0] = j.acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (; s0 < s1; s0 += 32) {
     const int s = s0 + lane;
-    Header hd = {-1, -1, 0, 0};
-    if (s < workers) hd = p.head[s];
-    const bool mine = s == g || hd.cont_tile == tile;
-    const bool ends = s != g && hd.cont_ends != 0;
-    const unsigned stop = __ballot_sync(0xffffffffu, !mine || ends);
-    const int n = stop ? __ffs(stop) - 1 : 32;            // before the stopping one
-    const int last = (stop && __shfl_sync(0xffffffffu, (int)mine, n & 31)) ? n : n - 1;
-    more = stop == 0;
-    const bool part = lane <= last && (s == g || hd.cont_some);
-    const int slot = s == g ? 2 * g + 1 : 2 * s;
+    const bool part = s < s1 && (s == g0 || heads[s].cont_some);
+    const int slot = s == g0 ? 2 * s + 1 : 2 * s;
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (part) ml = p.part_ml[slot * kRows + h];
+    if (part) ml = p.part_ml[(long long)slot * kRows + h];
     const bool some = part && ml.y != 0.f;  // (a part that saw no page adds nothing)
-    const float top = fmaxf(mx, warp_max(some ? ml.x : -INFINITY));
+    const float top = fmaxf(j.mx, warp_max(some ? ml.x : -INFINITY));
     const float ref = top == -INFINITY ? 0.f : top;
-    const float old = ex2_fast(mx - ref);   // 0 before the first part
+    const float old = ex2_fast(j.mx - ref);   // 0 before the first part
     const float wgt = some ? ex2_fast(ml.x == -INFINITY ? 0.f : ml.x - ref) : 0.f;
-    den = den * old + warp_sum(some ? ml.y * wgt : 0.f);
+    j.den = j.den * old + warp_sum(some ? ml.y * wgt : 0.f);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      acc[q].x *= old; acc[q].y *= old; acc[q].z *= old; acc[q].w *= old;
+      j.acc[q].x *= old; j.acc[q].y *= old; j.acc[q].z *= old; j.acc[q].w *= old;
     }
-    mx = top;
+    j.mx = top;
     unsigned todo = __ballot_sync(0xffffffffu, some);
     while (todo) {
-      float4 v[8][2];
-      float wv[8];
+      float4 v[4][2];
+      float wv[4];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 4; ++u) {
         const int i = todo ? __ffs(todo) - 1 : -1;
         const int sl = __shfl_sync(0xffffffffu, slot, i & 31);
         wv[u] = __shfl_sync(0xffffffffu, wgt, i & 31);
         if (i < 0) wv[u] = 0.f;
-        const float4* src = reinterpret_cast<const float4*>(
-            p.part_o + ((long long)sl * kRows + h) * kL + col);
+        const float4* src =
+            reinterpret_cast<const float4*>(p.part_o + ((long long)sl * kRows + h) * kL + col);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           v[u][q] = i < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcs(src + q * 32);
         todo &= todo - 1;
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 4; ++u) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          acc[q].x = fmaf(v[u][q].x, wv[u], acc[q].x);
-          acc[q].y = fmaf(v[u][q].y, wv[u], acc[q].y);
-          acc[q].z = fmaf(v[u][q].z, wv[u], acc[q].z);
-          acc[q].w = fmaf(v[u][q].w, wv[u], acc[q].w);
+          j.acc[q].x = fmaf(v[u][q].x, wv[u], j.acc[q].x);
+          j.acc[q].y = fmaf(v[u][q].y, wv[u], j.acc[q].y);
+          j.acc[q].z = fmaf(v[u][q].z, wv[u], j.acc[q].z);
+          j.acc[q].w = fmaf(v[u][q].w, wv[u], j.acc[q].w);
         }
       }
     }
   }
-  const float inv = den == 0.f ? 0.f : p.o_scale / den;
-  const long long row = (long long)token * p.Hm + head;
+  return j;
+}
+
+template <int kRows, bool kPair>
+__global__ void __launch_bounds__(kJoinThreads, 2)
+    mla_chunk_join_kernel(const Params p, int workers) {
+  __shared__ __align__(16) Header heads[kMaxWorkers];
+  __shared__ int begun[kMaxWorkers], n_begun;  // workers that began a tile
+  __shared__ float s_mx[kJoinWarps], s_den[kJoinWarps];
+  __shared__ __align__(16) float s_acc[kJoinWarps][256];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < workers; i += kJoinThreads)
+    *reinterpret_cast<int4*>(heads + i) = *reinterpret_cast<const int4*>(p.head + i);
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0;
+    for (int s = 0; s < workers; s += 32) {
+      const bool hit = s + lane < workers && heads[s + lane].start_tile >= 0;
+      const unsigned all = __ballot_sync(0xffffffffu, hit);
+      if (hit) begun[n + __popc(all & ((1u << lane) - 1))] = s + lane;
+      n += __popc(all);
+    }
+    if (lane == 0) n_begun = n;
+  }
+  __syncthreads();
+  const int pieces = n_begun * 2 * kRows;
+  const bool wide = pieces <= 2 * (int)gridDim.x;  // a block per piece
+  const int step = wide ? gridDim.x : gridDim.x * kJoinWarps;
+#pragma unroll 1
+  for (int i = wide ? blockIdx.x : warp * gridDim.x + blockIdx.x; i < pieces; i += step) {
+    const int g0 = begun[i / (2 * kRows)], h = (i >> 1) & (kRows - 1), c0 = (i & 1) * 256;
+    const int tile = heads[g0].start_tile;
+    int token, head;
+    if (kPair) {
+      token = tile >> 1;
+      head = h;
+      if (p.Hm <= 64 && h >= 64) {  // the second token's rows
+        if (!(tile & 1)) continue;
+        ++token;
+        head = h - 64;
+      }
+    } else {
+      const int hb = (p.Hm + kRows - 1) / kRows;
+      token = tile / hb;
+      head = (tile - token * hb) * kRows + h;
+    }
+    if (head >= p.Hm) continue;
+    const long long row = (long long)token * p.Hm + head;
+    int n = 1;  // its workers: g0 .. g0 + n - 1
+    for (unsigned stop = 0; !stop;) {
+      const int s = g0 + n + lane;
+      const Header hd = heads[min(s, workers - 1)];
+      const bool mine = s < workers && hd.cont_tile == tile;
+      stop = __ballot_sync(0xffffffffu, !mine || hd.cont_ends);
+      const int k = stop ? __ffs(stop) - 1 : 32;  // before the stopping one
+      n += k + (stop ? __shfl_sync(0xffffffffu, (int)mine, k & 31) : 0);
+    }
+    const int per = wide ? (n + kJoinWarps - 1) / kJoinWarps : n;
+    const int s0 = g0 + (wide ? min(n, warp * per) : 0);
+    const Joined j = join_parts<kRows>(p, heads, g0, s0, min(s0 + per, g0 + n), h,
+                                       c0 + lane * 4, lane);
+    if (!wide) {
+      const float inv = j.den == 0.f ? 0.f : p.o_scale / j.den;
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-    *reinterpret_cast<uint2*>(p.out + row * kL + col + q * 128) =
-        make_uint2(pack_bf16(acc[q].x * inv, acc[q].y * inv),
-                   pack_bf16(acc[q].z * inv, acc[q].w * inv));
-  if (p.lse && lane == 0 && (warp & 1) == 0)
-    p.lse[row] = den == 0.f ? -INFINITY : (mx + log2f(den)) / kLog2e;
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<uint2*>(p.out + row * kL + c0 + q * 128 + lane * 4) =
+            make_uint2(pack_bf16(j.acc[q].x * inv, j.acc[q].y * inv),
+                       pack_bf16(j.acc[q].z * inv, j.acc[q].w * inv));
+      if (p.lse && lane == 0 && c0 == 0)
+        p.lse[row] = j.den == 0.f ? -INFINITY : (j.mx + log2f(j.den)) / kLog2e;
+      continue;
+    }
+    if (lane == 0) {
+      s_mx[warp] = j.mx;
+      s_den[warp] = j.den;
+    }
+    *reinterpret_cast<float4*>(&s_acc[warp][lane * 4]) = j.acc[0];
+    *reinterpret_cast<float4*>(&s_acc[warp][128 + lane * 4]) = j.acc[1];
+    __syncthreads();
+    if (tid < 128) {
+      float mx = -INFINITY, den = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, s_mx[w]);
+      const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        // (no maximum: no part, or a NaN sum, which stays one)
+        const float e = s_mx[w] == -INFINITY ? 1.f : ex2_fast(s_mx[w] - ref);
+        const float2 x = *reinterpret_cast<const float2*>(&s_acc[w][tid * 2]);
+        den = fmaf(s_den[w], e, den);
+        a = fmaf(x.x, e, a);
+        b = fmaf(x.y, e, b);
+      }
+      const float inv = den == 0.f ? 0.f : p.o_scale / den;
+      *reinterpret_cast<uint32_t*>(p.out + row * kL + c0 + tid * 2) = pack_bf16(a * inv, b * inv);
+      if (p.lse && tid == 0 && c0 == 0)
+        p.lse[row] = den == 0.f ? -INFINITY : (mx + log2f(den)) / kLog2e;
+    }
+    __syncthreads();
+  }
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

@@ -849,8 +849,8 @@ int launch_mla_chunk_pair(const ChunkArgs& a, void* workspace, cudaStream_t stre
   cfg.dynamicSmemBytes = kSmem;
   if (launch_kernel(&cfg, mla_chunk_pair_kernel, q_map, kv_map, p) != cudaSuccess)
     return DSA_ERR_CUDA;
-  cfg.gridDim = dim3(pairs, 16, 1);
-  cfg.blockDim = dim3(512, 1, 1);
+  cfg.gridDim = dim3(2 * num_sms(), 1, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return launch_kernel(&cfg, mla_chunk_join_kernel<128, true>, p, pairs) == cudaSuccess
              ? DSA_OK

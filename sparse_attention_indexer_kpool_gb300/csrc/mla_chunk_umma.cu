@@ -631,8 +631,8 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   cfg.blockDim = dim3(cta_threads(kSrc), 1, 1);
   cfg.dynamicSmemBytes = Smem<kN>::kBytes;
   if (launch_kernel(&cfg, kernel, q_map, kv_map, ahead_map, p) != cudaSuccess) return DSA_ERR_CUDA;
-  cfg.gridDim = dim3(n_cta, kN / 8, 1);
-  cfg.blockDim = dim3(512, 1, 1);
+  cfg.gridDim = dim3(2 * num_sms(), 1, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return launch_kernel(&cfg, mla_chunk_join_kernel<kN, false>, p, n_cta) == cudaSuccess ? DSA_OK
                                                                                  : DSA_ERR_CUDA;
