@@ -1,5 +1,9 @@
 // What the tensor-core kernels of the chunk attention share: the batch as units of
 // work, a walk over a CTA's (or CTA pair's) share of them, the join of partials.
+//
+// Equal shares of the whole batch's units, whatever its lengths, keep every SM at work
+// to the end; the price is that a share may begin and end inside a row tile, whose two
+// or more partials (fp32, 128 KB for 64 heads) go through memory once.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -37,7 +41,7 @@ struct Params {
   float2* part_ml;           // [2 workers][rows of a tile]
   Header* head;
   int32_t* status;
-  int drill, prefetch;
+  int drill;
   int box_log;               // positions of a box, 2^box_log (copied rows: 1)
   float o_scale;             // of the partials' output against their sums
   int extra;                 // what a row tile costs beside its key tiles, in units

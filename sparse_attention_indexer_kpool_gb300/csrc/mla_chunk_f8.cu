@@ -19,12 +19,21 @@
 // stays below 2^7 and its parts inside E5M2's range; a row scale counts there as at
 // least 2^-60, which bounds the bare weight as well.
 //
-// Why.  Widening the codes to bf16 in shared memory first took 1,960 cycles of
-// conversions and 2,000 of shared-memory traffic a tile and kept one tile at a time in
-// the 128 KB that its bf16 rows fill: 8,100 cycles a tile.  As codes a tile is 64 KB:
-// two are in flight, the softmax of one under the products of the other.  The parts
-// cost MMAs (80 steps a tile, K = 32, against 64 of K = 16 in bf16): 128 x 64 x 32 reads
-// 6 KB of shared memory for 32 cycles' work, as in the bf16 kernel, and that bounds it.
+// Why.  Widening the codes to bf16 in shared memory took 1,960 cycles of conversions
+// and 2,000 of shared-memory traffic a tile and kept one tile at a time in the 128 KB
+// that its bf16 rows fill: 8,100 cycles a tile.  As codes a tile is 64 KB: two are in
+// flight, the softmax of one under the products of the other.
+//
+// What bounds it.  64 heads: the products.  S^T is 16 MMAs of 128 x 128 x 32 (both query
+// parts as N, 66 cycles each), O^T 48 of 128 x 64 x 32 (50 cycles, 6 KB of shared memory
+// each), about 4,000 cycles a tile with the next tile's rows through the same port; 4,700
+// measured, 5,500 where a reference is raised.  32 heads and fewer: S^T 16 of N = 64 and
+// O^T 16 of N = 96 (the three weight parts beside one another), 1,700 cycles, so the
+// chain load, S^T, softmax, O^T of a tile, two in flight: 4,000 cycles.
+// Measured on GB300: 12 sequences of 1 to 300 new tokens on up to 5,000 keys, 64 heads,
+// 678 us (729 TFLOP/s counted once; one part of the queries after the other: 773); 16
+// heads, 64 single tokens on 4,096 to 16,000 keys in pages of 16, 87 us (334 MB: 3.8
+// TB/s, 0.57 of the measured copy rate; parts one after the other: 103).
 #include "mla_chunk.cuh"
 
 namespace dsa {
@@ -508,8 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         issued = 0;
-        if (p.prefetch && team == 0 && row_next >= 0)  // the next tile's rows to L2
-          tma_prefetch_2d(&ahead_map, 0, row_next);
+        // the next tile's rows to L2 (16 heads, 64 single tokens on 8,192 keys: 70.6 us,
+        // without 73.4; no difference where tokens share the rows)
+        if (team == 0 && row_next >= 0) tma_prefetch_2d(&ahead_map, 0, row_next);
         row = row_next;
       }
     }
@@ -647,7 +657,6 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.status = a.status;
   p.drill = failure_drill();
   p.cap = table_cap(a.kv);
-  p.prefetch = a.T <= 4 * a.B;
   p.box_log = box_log_of(a.kv.page_size);
   p.o_scale = 1.f / kUp;
   p.extra = 1;
@@ -700,6 +709,7 @@ size_t mla_chunk_f8_workspace_size(int T, int Hm) {
 }
 
 int launch_mla_chunk_f8(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
+  // (16 heads, 64 single tokens on 8,192 keys: 71 us; in 64 columns 103)
   return a.Hm <= 32 ? launch<32>(a, workspace, stream) : launch<64>(a, workspace, stream);
 }
 

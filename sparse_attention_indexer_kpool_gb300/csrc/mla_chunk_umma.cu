@@ -1,18 +1,19 @@
 // NoPE MLA of a step's new tokens over the paged latent cache on the tcgen05
-// tensor cores (bf16 activations, latent 512, bf16 or E4M3 pages).
+// tensor cores, a CTA at a time (bf16 activations, latent 512, bf16 pages of any size;
+// E4M3 pages whose size is no multiple of 8).
 //
 // Module glm5next_dsa, "Traps carried from Slice 8" (NoPE: a score is the plain
 // latent dot product) and Constants, MASKED_ATTN_MAX_KEYS (dense masked
 // attention).  In absorbed MLA the value of a latent row is the row itself, so
 // one tile of rows feeds both products.
 //
-// Work.  A row tile is one token and up to kN of its heads; its keys are 128-row
-// tiles of positions, the sinks' tiles first, then those from the window's first
-// position (0 without one) to the token's own.  A tile's rows share one mask, by
-// position alone: what a token does not see is zeroed in shared memory before
-// the second product reads it, so nothing there (NaN, infinity) reaches the
-// output.  One persistent CTA per SM takes an equal, contiguous share of the
-// (row tile, key tile) units of the whole batch, found from the lengths by a scan
+// Work.  A row tile is one token and up to kN of its heads; its keys are what it sees in
+// aligned boxes of positions (the sinks' boxes, then those from the window's first
+// position, 0 without one, to the token's own), 128 positions to a key tile.  A tile's
+// rows share one mask, by position alone: what a token does not see is zeroed in
+// shared memory before the second product reads it, so nothing there (NaN, infinity)
+// reaches the output.  One persistent CTA per SM takes an equal, contiguous share of
+// the (row tile, key tile) units of the whole batch, found from the lengths by a scan
 // in every CTA; a row tile whose units fall to several CTAs leaves partials (O
 // unnormalised, maximum, sum) that a second kernel joins in CTA order.  Units
 // are counted with the longest token's tiles for every token of a sequence and
@@ -28,12 +29,16 @@
 // relative precision at any scale, so a stale reference costs nothing, and no
 // tile but such a one needs a maximum across rows.
 //
-// What bounds it.  One 128 x 64 x 16 MMA reads 6 KB of shared memory at 128
-// bytes a cycle (measured 51 cycles; the tensor cores alone would take 32), the
-// next tile's rows are written through the same port (1,024 cycles), and the
-// softmax of a tile stands between its two products: rows 128 KB, queries 64 KB
-// and P 16 KB leave no room for a second tile, so the tile is handed on in four
-// column chunks, each refilled as soon as its part of O^T is done.
+// What bounds it.  Single tokens: HBM, and a tile's latency.  Otherwise the tile itself:
+// one 128 x 64 x 16 MMA reads 6 KB of shared memory at 128 bytes a cycle (measured 51
+// cycles; the tensor cores alone would take 32), the next tile's rows are written
+// through the same port (1,024 cycles), and the softmax of a tile stands between its two
+// products: rows 128 KB, queries 64 KB and P 16 KB leave no room for a second tile, so
+// the tile is handed on in four column chunks, each refilled as soon as its part of
+// O^T is done.  About 5,500 cycles a tile, of which 4,300 are shared-memory traffic.
+// Measured on GB300, 64 heads: 64 single tokens on 4,096 to 16,000 keys 130 us (667 MB:
+// 5.1 TB/s, 0.76 of the measured copy rate); chunks of 1 to 128 tokens of 16 sequences
+// under a window of 512 and 4 sinks 94 us (430 TFLOP/s); one token on 256 keys 14.6 us.
 #include "mla_chunk.cuh"
 
 namespace dsa {
@@ -388,9 +393,9 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         }
         if (!ok) break;
         issued = 0;
-        // the next tile's rows to L2, half of a row each
-        if (p.prefetch && row_next >= 0)
-          tma_prefetch_2d(&ahead_map, team * 256, row_next);
+        // the next tile's rows to L2, half of a row each (64 single tokens on 8,192
+        // keys: 111 us, without 122; no difference where tokens share the rows)
+        if (row_next >= 0) tma_prefetch_2d(&ahead_map, team * 256, row_next);
         row = row_next;
       }
     }
@@ -602,9 +607,6 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   p.cap = table_cap(a.kv);
   p.o_scale = 1.f;
   p.extra = 2;
-  // rows that few tokens share come from HBM: the tile after the next is brought
-  // into L2 meanwhile
-  p.prefetch = a.T <= 4 * a.B;
   p.box_log = kSrc == kSrcTma ? box_log_of(a.kv.page_size) : 0;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)n_cta * 2 * kN * kL);
@@ -615,7 +617,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.page_size;
   if (kSrc == kSrcTma &&
       (!row_map(&kv_map, a.kv.pages, rows, 1u << p.box_log) ||
-       (p.prefetch && !prefetch_map(&ahead_map, a.kv.pages, rows, 1u << p.box_log, false))))
+       !prefetch_map(&ahead_map, a.kv.pages, rows, 1u << p.box_log, false)))
     return DSA_ERR_CUDA;
   auto kernel = mla_chunk_kernel<kN, kSrc>;
   static std::atomic<unsigned long long> done{0};
@@ -638,6 +640,9 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
                                                                                  : DSA_ERR_CUDA;
 }
 
+// TMA takes boxes of 8 rows and more, so pages of a multiple of 8; any other page size is
+// copied row by row (64 single tokens on 8,192 keys in pages of 64: 111 us by TMA, 190
+// copied).
 template <int kN>
 int launch_src(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   if (a.kv.kv_dtype == DSA_FP8_E4M3) return launch<kN, kSrcCopy8>(a, workspace, stream);
@@ -655,6 +660,8 @@ size_t mla_chunk_umma_workspace_size(int Hm) {
   return Hm <= 32 ? workspace_bytes<32>(num_sms()) : workspace_bytes<64>(num_sms());
 }
 
+// Up to 32 heads take half the columns (16 heads, 16 sequences x 32 tokens on 1,024 keys:
+// 86 us, in 64 columns 103; 4 tokens on 4,096: 49 and 57).
 int launch_mla_chunk_umma(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   return a.Hm <= 32 ? launch_src<32>(a, workspace, stream)
                     : launch_src<64>(a, workspace, stream);

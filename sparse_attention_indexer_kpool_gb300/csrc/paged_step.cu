@@ -16,7 +16,8 @@
 // What bounds it: the launch and two dependent round trips to memory (lengths,
 // then free pages).  When seq_lens or free_end are written in place, the CTAs
 // form one cluster (8 at most) and write only after a cluster barrier behind
-// everyone's reads.
+// everyone's reads.  Measured on GB300: 64 decode requests 3.5 us, 512 requests with
+// 64,536 new tokens in place 4.9 us.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -193,7 +194,10 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(PlanArgs a, int cluste
 // rows with an extreme scale take the plain division.
 // One warp per row, 8 elements (16 or 32 bytes) a lane and step; the row stays in
 // registers between the maximum and the conversion, so it is read once.
-// What bounds it: HBM bandwidth (a row is 2 L bytes in, L or 2 L out).
+// What bounds it: HBM bandwidth (a row is 2 L bytes in, L or 2 L out) and, for E4M3, the
+// conversions.  Measured on GB300, L = 512: 65,536 bf16 rows to E4M3 18.4 us (101 MB: 5.5
+// TB/s, 0.81 of the measured copy rate; two and four rows a warp were slower), 16,383 to
+// bf16 4.7 us, 64 rows 1.1 us.
 template <typename T> struct Load8;
 template <> struct Load8<__nv_bfloat16> {
   static __device__ __forceinline__ void get(const __nv_bfloat16* p, float (&x)[8]) {
