@@ -280,11 +280,11 @@ namespace {
 // heads), and a row must see enough of them to pay for the exchange's start and end.
 // The lengths live on the device: the window and the block table's width bound them.
 // Measured on GB300, pair / single CTA in us (sequences x new tokens, 64 heads):
-//   context  8,192, 32 x 4: 177 / 196, 16 x 16: 317 / 361, 4 x 256: 1,101 / 1,221
+//   context  8,192, 32 x 4: 181 / 196, 16 x 16: 318 / 361, 4 x 256: 1,092 / 1,221
 //   context  2,048, 32 x 4:  72 /  70, 16 x 16: 111 / 104, 4 x 256:   330 /   336
 //   context    512, 32 x 4:  45 /  35, 16 x 16:  61 /  46, 4 x 256:   138 /   114
-//   window   4,096 of 16,384, 4 x 256: 627 / 662; 2,048: 370 / 367; 512: 177 / 143
-//   single tokens, context 8,192: 64 x 1: 165 / 111, 64 heads; 32 x 2: 106 / 109
+//   window   4,096 of 16,384, 4 x 256: 620 / 662; 2,048: 367 / 367; 512: 177 / 143
+//   context  8,192, 32 x 2: 108 / 109, single tokens 64 x 1: 165 / 111
 bool pairs_pay(const ChunkArgs& a) {
   if (a.kv.kv_dtype != DSA_BF16 || (a.Hm <= 64 && a.T < 2ll * a.B)) return false;
   const long long table = (long long)a.kv.max_pages * a.kv.page_size;

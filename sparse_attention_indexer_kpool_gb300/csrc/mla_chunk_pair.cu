@@ -19,7 +19,7 @@
 // done twice.  What bounds it is the exchange: scores, send, sum, weights, send and PV are
 // a chain of about 9,500 cycles a tile, of which four tiles are on their way at once (what
 // shared memory holds).  Measured on GB300, 64 heads, 2,048 tokens behind 14,336:
-// 3.97 ms, 1,040 TFLOP/s (0.56 of the measured bf16 rate; the single-CTA kernel: 4.53 ms).
+// 3.94 ms, 1,045 TFLOP/s (0.56 of the measured bf16 rate; the single-CTA kernel: 4.53 ms).
 //
 // The two tokens of a pair see the same keys but for the last one and the first of a
 // window.  A key that neither sees is zeroed in shared memory before PV; one that only
@@ -837,18 +837,21 @@ int launch_mla_chunk_pair(const ChunkArgs& a, void* workspace, cudaStream_t stre
     return DSA_ERR_CUDA;
   static std::atomic<unsigned long long> done{0};
   if (!allow_smem(mla_chunk_pair_kernel, kSmem, done)) return DSA_ERR_CUDA;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  // Not launched beside the end of the kernel before it: pairs that are placed while other
+  // blocks still hold SMs run slower to their end (2,048 tokens behind 14,336: 3.94 ms, and
+  // 4.04 or 4.12 ms beside a kernel of 304 or 1,216 blocks).
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   cfg.gridDim = dim3(2 * pairs, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   if (launch_kernel(&cfg, mla_chunk_pair_kernel, q_map, kv_map, p) != cudaSuccess)
     return DSA_ERR_CUDA;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   cfg.gridDim = dim3(2 * num_sms(), 1, 1);
   cfg.blockDim = dim3(kJoinThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
