@@ -344,7 +344,8 @@ int dsa_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, const int32
  *   code = x / row_scale[r], rounded to nearest, at most 448 in magnitude; a
  *   NaN or infinite element becomes the NaN code.
  * Other rows of the cache are left as they were.  Two tokens with the same cache
- * row leave it with elements of either and the scale of either.
+ * row leave it with elements of either and the scale of either.  The pages may not
+ * overlap kv_new.
  * Supported: L a multiple of 8 up to 1024, any pairing of the dtypes.  16-byte
  * aligned kv_new and pages.
  * Device faults: DSA_DEV_BAD_PAGE (kv_rows[t] past the cache: the row is dropped).
@@ -368,7 +369,7 @@ int dsa_paged_append(const void* kv_new, const int32_t* kv_rows, int T, int L, i
  *   out[row, h, :] = sum_t softmax(z)_t * c_t;  lse[row, h] = log(sum_t exp(z_t))
  * Nothing seen gives out = 0 and lse = -inf.  What a token does not see does not
  * reach its output, whatever the cache holds there.  Rows of out and lse behind
- * cu_new[B] are left as they were.
+ * cu_new[B] are left as they were.  No output may overlap an input.
  *
  *   q_lat [T, Hm, L] activation dtype; kv as for dsa_mla_paged_decode (seq_lens
  *   counts the new tokens); cu_new [B+1] int32, not decreasing, within [0, T]

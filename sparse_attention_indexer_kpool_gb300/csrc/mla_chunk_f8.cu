@@ -5,11 +5,12 @@
 // Work, row tiles, key tiles, masks and the join are those of the bf16 kernel.  What
 // differs is where the precision comes from: an E4M3 code keeps its value, and the
 // other factor of each product is split into 8-bit parts whose sum it is.
-//   S^T = C (q_hi + q_lo)^T   E4M3 x E4M3.  A head's query row is scaled by a power of
-//     two to a largest magnitude in [128, 256); hi is the nearest E4M3 value, lo that
-//     of the rest.  A bf16 value has 8 significant bits, an E4M3 value 4, so hi + lo is
-//     the value itself down to 2^-9 of the scaled row (2^-17 of its largest element),
-//     and off by at most 2^-10 of it below.
+//   S^T = C q_hi^T + 2^-4 C q_lo^T   E4M3 x E4M3.  A head's query row is scaled by a power
+//     of two to a largest magnitude in [128, 256); hi is the nearest E4M3 value (off by
+//     16 at most), lo that of 16 times the rest.  A bf16 value has 8 significant bits, an
+//     E4M3 value 4, so the two are the value itself down to 2^-6 of the scaled row, and
+//     off by at most 2^-14 below: 2^-21 of the row's largest element.  (Beside an element
+//     2^12 times as large, a bf16 element's own rounding is as coarse.)
 //   O^T += C^T (p_1 + p_2 + p_3)^T   E4M3 x E5M2.  A weight u = 2^(z - m) * row scale,
 //     times 2^8, is cut to 3 significant bits twice and its rest rounded: off by at
 //     most 2^-9 of itself (a bf16 weight: up to 2^-8), and, where a part falls below
@@ -51,6 +52,7 @@ constexpr int kThreads = kSoftThreads + 32 * (kTmaWarps + 1);
 constexpr float kRaise8 = 7.f;            // base-2 growth of u that raises a reference
 constexpr float kUp = 256.f;              // weights in E5M2 are scaled by 2^8
 constexpr float kLeastLog = -60.f;
+constexpr float kLoUp = 16.f;             // of the queries' lo parts
 
 struct Ctl {
   float m[64], nm[64], alpha[64], l[64];  // per head; first: read as float4
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(256)
       const uint32_t h2 = e4m3x2(a, b) & 0xffffu;
       const float2 f = from_e4m3x2(h2);
       hi[j] |= h2 << (16 * k);
-      lo[j] |= (e4m3x2(a - f.x, b - f.y) & 0xffffu) << (16 * k);
+      lo[j] |= (e4m3x2((a - f.x) * kLoUp, (b - f.y) * kLoUp) & 0xffffu) << (16 * k);
     }
   }
   uint8_t* dst = codes + row * (2 * kL) + lane * 16;
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lg = fmaxf(log2f(fabsf(sc)), kLeastLog);  // in u's reference
         const float high_at = kRaise8 - lg;
         float e[kW];
-        // z = S * query scale * row scale * softmax scale
+        // z = S * query scale * row scale * softmax scale, S of both parts
         auto logits = [&]() {
           const uint32_t ts = tl + st * S::kSCols + (uint32_t)(hq * kW);
           tmem_ldw<kW>(ts, e);
@@ -285,7 +287,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             float lo[16];
             tmem_ld16(ts + kN + g, lo);
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) add2(e[g + i], e[g + i + 1], lo[i], lo[i + 1]);
+            for (int i = 0; i < 16; i += 2) {
+              fma2(lo[i], lo[i + 1], 1.f / kLoUp, e[g + i], e[g + i + 1]);
+              e[g + i] = lo[i];
+              e[g + i + 1] = lo[i + 1];
+            }
           }
 #pragma unroll
           for (int q = 0; q < kW / 4; ++q) {

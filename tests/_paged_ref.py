@@ -104,31 +104,47 @@ def attend(q_lat, rows64, table, seq_lens, page_size, cu_new, window, sinks, sm_
             w = torch.softmax(z, -1)
             out[r] = w @ c
             mag[r] = w @ c.abs()
-            dot[r] = ((q.abs() @ c.abs().T) * sm_scale).amax(-1)
+            dot[r] = ((q.abs() @ c.abs().T) * abs(sm_scale)).amax(-1)
             seen[r] = pr.numel()
     return out, lse, mag, dot, seen
 
 
-def attend_bounds(ref, dtype, L):
+def attend_bounds(ref, dtype, L, dz_more=0.0, out_more=0.0):
     """Largest errors of an attention that keeps logits, sums and outputs in fp32.
     A logit is a sum of L fp32 products: off by at most dz = L 2^-24 sum|q c| (twice that
     where the order is not known) and 2^-21 of itself for the base-2 scaling and the
     exponential; a weight by that relatively, so is their sum.  A weight is rounded to bf16
     for the second product (2^-8) in the bf16 kernels, the sum over n positions adds
-    n 2^-23, the result is rounded once."""
+    n 2^-23, the result is rounded once.  ``dz_more`` [T, Hm]: what the logits may be off by
+    beside that; ``out_more``: the outputs (``underflow``)."""
     out, lse, mag, dot, seen = ref
     half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
-    dz = 2 * L * 2.0 ** -24 * dot + 2.0 ** -21 * dot
+    dz = 2 * L * 2.0 ** -24 * dot + 2.0 ** -21 * dot + dz_more
     n = seen.double()[:, None]
     rel = 2 * dz + n * 2.0 ** -23 + 2.0 ** -20 + (2.0 ** -8 if dtype == torch.bfloat16 else 0.0)
-    tol_out = rel[..., None] * mag * 1.01 + half * out.abs() + 1e-30
+    tol_out = rel[..., None] * mag * 1.01 + half * out.abs() + 1e-30 + out_more
     tol_lse = dz + n * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * torch.where(
         torch.isfinite(lse), lse.abs(), 0.0)
     return tol_out, tol_lse
 
 
-def check_attend(out, lse, ref, dtype, L, rows=None):
-    tol_out, tol_lse = attend_bounds(ref, dtype, L)
+def underflow(pages, row_scale, act):
+    """What E5M2 weights lose of the smallest ones, per latent column (E4M3 pages under bf16
+    activations).  A weight w_t times its row's scale r_t, relative to a reference that the
+    largest of these products reaches, is held times 2^8 in three parts of E5M2, whose least
+    step is 2^-16: off by at most 3 * 2^-17 in all where a part falls below the normal range, so
+    the sum over keys by e = 3 * 2^-25 sum_t |code_t|.  The sum of the weights is at least that of
+    the key whose product reaches the reference, 1 / r: the output is off by at most e max r."""
+    if row_scale is None or act != torch.bfloat16:
+        return 0.0
+    codes = pages.view(torch.float8_e4m3fn) if pages.dtype == torch.uint8 else pages
+    keep = torch.isfinite(row_scale)
+    codes = torch.nan_to_num(codes.float()[keep]).abs().double().sum(0)
+    return 3 * 2.0 ** -25 * codes * row_scale[keep].double().max()
+
+
+def check_attend(out, lse, ref, dtype, L, rows=None, dz_more=0.0, out_more=0.0):
+    tol_out, tol_lse = attend_bounds(ref, dtype, L, dz_more, out_more)
     want_out, want_lse = ref[0], ref[1]
     if rows is not None:
         out, lse, want_out, want_lse, tol_out, tol_lse = (

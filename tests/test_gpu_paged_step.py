@@ -208,7 +208,8 @@ def check(s, window=0, sinks=0, status=0):
     live = s["cu"][-1].item()
     r = reference(s, window, sinks)
     ref.check_attend(out, lse, r, s["q"].dtype, s["q"].shape[2],
-                     rows=torch.arange(live, device=DEV))
+                     rows=torch.arange(live, device=DEV),
+                     out_more=ref.underflow(s["pages"], s["scale"], s["q"].dtype))
     assert bool((out[live:] == 7.0).all()) and bool((lse[live:] == 7.0).all())
     return out, lse
 
@@ -333,6 +334,41 @@ def test_chunk_faults_are_flagged_and_contained(act, kv, Hm, L, width):
     assert st & ops.DEV_BAD_LENGTH and torch.isfinite(out.float()).all()
     s["cu"] = i32([20, 3, 7])
     assert attend(s)[2] & ops.DEV_BAD_LENGTH
+
+
+@pytest.mark.parametrize("act,kv,Hm,L,width", [(BF, BF, 64, 512, 0), (BF, BF, 64, 512, 2112),
+                                               (BF, F8, 64, 512, 0), (BF, F8, 16, 512, 0),
+                                               (F32, F32, 4, 64, 0)])
+def test_chunk_softmax_scales(act, kv, Hm, L, width):
+    """No scale, a negative one, and one that leaves a weight or two."""
+    for sm in (0.0, -0.05, 1.5):
+        s = make([700, 90], [6, 3], Hm=Hm, L=L, act=act, kv=kv, seed=22, width=width)
+        s["sm"] = sm
+        check(s)
+        check(s, 100, 3)
+
+
+@pytest.mark.parametrize("Hm,ps", [(64, 64), (16, 16), (64, 5)])
+def test_chunk_e4m3_queries_with_a_large_element(Hm, ps):
+    """A query element far above the others, in a latent column where the keys are small, so
+    that the others make the logits.  The queries' 8-bit parts are off by at most 2^-21 of a
+    row's largest element (the widened rows' kernel: not at all): 2^-21 max|q| sum|c| of a
+    logit."""
+    s = make([900, 40], [5, 3], Hm=Hm, kv=F8, ps=ps, seed=23)
+    vals = ref.values(s["pages"], s["scale"])
+    vals[:, 7] *= 1e-4
+    codes, scale = ref.quantise(torch.nan_to_num(vals).float())
+    s["pages"], s["scale"] = codes, scale
+    for big in (30.0, 1000.0, 30000.0):
+        s["q"][:, :, 7] = big
+        s["q"][:, ::2, 7] = -big
+        out, lse, st = attend(s)
+        assert st == 0
+        live = int(s["cu"][-1])
+        largest = ref.values(s["pages"], s["scale"]).abs().sum(1).max()
+        more = 2.0 ** -21 * s["q"].double().abs().amax(2) * largest * s["sm"]
+        ref.check_attend(out, lse, reference(s), BF, 512, rows=torch.arange(live, device=DEV),
+                         dz_more=more, out_more=ref.underflow(s["pages"], s["scale"], BF))
 
 
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 16, 512), (F32, F32, 4, 64)])
