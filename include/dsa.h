@@ -317,8 +317,8 @@ size_t dsa_mla_paged_decode_workspace_size(int Q, int Hm, int L, int out_width, 
  *   used up, table too narrow) gets -1 where the table has the entry, its tokens
  *   kv_rows -1, and the step DSA_DEV_NO_PAGE.
  * Apart from the two in-place forms, no output may overlap an input or another
- * output.  Supported: B <= DSA_PLAN_MAX_B, T <= DSA_PLAN_MAX_T.  One launch, no
- * workspace.  B == 0 is a no-op that writes nothing.
+ * output.  Supported: B <= DSA_PLAN_MAX_B, T and B * max_pages <= DSA_PLAN_MAX_T
+ * (key_rows: row_base[b] + q_pos below 2^31).  One launch, no workspace.  B == 0 is a no-op that writes nothing.
  * Device faults: DSA_DEV_BAD_LENGTH (a negative length, or one past 2^31 - 1
  * tokens: no new tokens for that sequence, and 0 cached ones where ctx_lens[b] is
  * negative; a negative free_begin: no free pages), DSA_DEV_TOKEN_CAP,

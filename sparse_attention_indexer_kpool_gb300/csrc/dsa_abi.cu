@@ -145,6 +145,7 @@ int check_plan(const dsa::PlanArgs& a) {
   if (a.T > 0 && (a.row_base == nullptr) != (a.key_rows == nullptr)) return DSA_ERR_INVALID_ARG;
   if ((long long)a.n_pages * a.page_size > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
   if (a.B > DSA_PLAN_MAX_B || a.T > DSA_PLAN_MAX_T) return DSA_ERR_UNSUPPORTED;
+  if ((long long)a.B * a.max_pages > DSA_PLAN_MAX_T) return DSA_ERR_UNSUPPORTED;
   if (a.B == 0) return kNoWork;
   if (!a.ctx_lens || !a.new_lens || !a.free_begin || !a.block_table || !a.seq_lens || !a.cu_new ||
       !a.free_end || (a.n_free > 0 && !a.free_pages))

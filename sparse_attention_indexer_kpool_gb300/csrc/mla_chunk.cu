@@ -318,9 +318,10 @@ int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   cfg.numAttrs = 1;
   auto kernel = a.dtype == DSA_BF16 ? simt_kernel<__nv_bfloat16>(a.kv.kv_dtype)
                                     : simt_kernel<float>(a.kv.kv_dtype);
-  if (cfg.dynamicSmemBytes > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)cfg.dynamicSmemBytes) != cudaSuccess)
+  // (the largest size once a kernel: another thread's call may come between)
+  static std::atomic<unsigned long long> done[2][3];
+  if (!allow_smem(kernel, (kChunkFloats + kChunkHeads * 1024) * sizeof(float),
+                  done[a.dtype == DSA_BF16][a.kv.kv_dtype]))
     return DSA_ERR_CUDA;
   return launch_kernel(&cfg, kernel, a) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(PlanArgs a, int cluste
   const int stride = gridDim.x * blockDim.x, tid0 = blockIdx.x * blockDim.x + threadIdx.x;
   for (int b = tid0; b <= B; b += stride) {
     a.cu_new[b] = cu[b];
-    if (b < B) a.seq_lens[b] = ctx[b] + cu[b + 1] - cu[b];
+    if (b < B) a.seq_lens[b] = ctx[b] + (cu[b + 1] - cu[b]);
   }
   for (int k = tid0; k < (int)total_pages; k += stride) {
     const int b = find_segment(off, B, k);
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(PlanArgs a, int cluste
       continue;
     }
     const int b = find_segment(cu, B, t);
-    const int pos = ctx[b] + t - cu[b], blk = pos / ps, have = blocks_of(ctx[b], ps);
+    const int pos = ctx[b] + (t - cu[b]), blk = pos / ps, have = blocks_of(ctx[b], ps);
     int id = -1;
     if (blk < a.max_pages) {
       if (blk >= have) {
@@ -332,7 +332,7 @@ template <typename T, int kKv>
 int append_steps(const void* kv_new, const int32_t* kv_rows, int n_t, int L, void* pages,
                  float* row_scale, int n_rows, int32_t* status, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = pdl_config((n_t + kAppendWarps - 1) / kAppendWarps,
+  const cudaLaunchConfig_t cfg = pdl_config((int)((n_t + kAppendWarps - 1ll) / kAppendWarps),
                                             kAppendWarps * 32, 0, stream, attr);
   auto kernel = L <= 256 ? paged_append_kernel<T, kKv, 1>
                          : (L <= 512 ? paged_append_kernel<T, kKv, 2>
@@ -358,10 +358,9 @@ int append_kv(const void* kv_new, const int32_t* kv_rows, int n_t, int L, int kv
 
 int launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
   const size_t smem = (size_t)(3 * a.B + 2) * 4;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return DSA_ERR_CUDA;
+  // (the largest size once: another thread's call may come between)
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_smem(paged_plan_kernel, (3 * DSA_PLAN_MAX_B + 2) * 4, done)) return DSA_ERR_CUDA;
   // one thread a token up to the CTAs that the scans are repeated in
   const long long work = a.T > a.B ? a.T : a.B;
   const int block = work <= 256 ? 256 : 1024;

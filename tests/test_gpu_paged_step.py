@@ -3,6 +3,7 @@ fp32 divisions, the chunk attention against 64 bits within the bounds of its
 roundings, and the three together with the selection that they feed."""
 import math
 import random
+import threading
 
 import pytest
 import torch
@@ -106,6 +107,61 @@ def test_plan_faults_are_flagged_and_contained():
     check_plan(ctx, new, free, begin, n_pages, ps, table, T)
 
 
+@pytest.mark.parametrize("lens_in_place,list_in_place", [(True, False), (False, True)])
+def test_plan_half_in_place(lens_in_place, list_in_place):
+    ctx, new, free, begin, n_pages, ps, table, T, base = random_plan(8, 3000, 16, 4, 300, 9)
+    c, fb, tab, B = i32(ctx), i32([begin]), i32(table), 3000
+    e = lambda n: torch.full((n,), -77, dtype=torch.int32, device=DEV)  # noqa: E731
+    out = dict(seq_lens=c if lens_in_place else e(B), cu_new=e(B + 1), q_seq=e(T), q_pos=e(T),
+               kv_rows=e(T))
+    end = fb if list_in_place else e(1)
+    ops.dsa_paged_plan(c, i32(new), i32(free), fb, n_pages, ps, tab, out["seq_lens"],
+                       out["cu_new"], out["q_seq"], out["q_pos"], out["kv_rows"], end)
+    want, _ = ref.plan(ctx, new, free, begin, n_pages, ps, [list(r) for r in table], T)
+    assert all(out[k].tolist() == want[k] for k in out)
+    assert tab.tolist() == want["table"] and end.item() == want["free_end"]
+
+
+def test_plan_at_the_end_of_the_positions():
+    """Positions just below 2^31, behind many other tokens of the step."""
+    hi = 2 ** 31 - 1
+    ctx, new = [0, hi - 3, hi - 700, 5], [5000, 3, 700, 1]
+    ps = 1 << 20
+    table = [[-1] * 2048, list(range(2048)), list(range(2047, -1, -1)), [0] + [-1] * 2047]
+    check_plan(ctx, new, [7, 9], 0, 2047, ps, table, 5800)
+
+
+def test_calls_from_two_threads():
+    """The plan and the generic attention at different sizes from two threads, a stream each."""
+    def work(B, L, out):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            ctx, new, free, begin, n_pages, ps, table, T, _ = random_plan(B, B, 16, 2, 40, 5)
+            want, _ = ref.plan(ctx, new, free, begin, n_pages, ps, [list(r) for r in table], T)
+            s = make([70, 9], [3, 2], Hm=2, L=L, act=F32, kv=F32, ps=16, seed=L)
+            exp = reference(s)
+            for _ in range(20):
+                tab, e = i32(table), lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)
+                rows, cu = e(T), e(B + 1)
+                ops.dsa_paged_plan(i32(ctx), i32(new), i32(free), i32([begin]), n_pages, ps, tab,
+                                   e(B), cu, e(T), e(T), rows, e(1))
+                o, ls = torch.empty_like(s["q"]), torch.empty(s["q"].shape[:2], device=DEV)
+                ops.dsa_mla_paged_chunk(s["q"], s["pages"], None, s["table"], s["lens"], 16,
+                                        s["cu"], 0, 0, s["sm"], o, ls)
+                torch.cuda.current_stream().synchronize()
+                assert rows.tolist() == want["kv_rows"] and tab.tolist() == want["table"]
+                ref.check_attend(o, ls, exp, F32, L, rows=torch.arange(5, device=DEV))
+            out.append(B)
+
+    done = []
+    threads = [threading.Thread(target=work, args=(B, L, done)) for B, L in ((8192, 1024),
+                                                                              (4200, 520))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert sorted(done) == [4200, 8192]
+
+
 # ---------------------------------------------------------------- append
 @pytest.mark.parametrize("L", [8, 64, 248, 512, 520, 1024])
 @pytest.mark.parametrize("act", [BF, F32])
@@ -143,6 +199,48 @@ def test_append(L, act, kv):
                            torch.nan_to_num(want.float(), nan=12345.0))
         if kv == F8:
             assert torch.equal(scale, want_s)
+
+
+@pytest.mark.parametrize("kv,L,act", [(BF, 512, BF), (F8, 512, BF), (F32, 1024, F32)])
+@pytest.mark.parametrize("ps", [64, 5])
+def test_rows_past_32_bits(kv, L, act, ps):
+    """A cache whose elements pass 2^31 (2^32 bytes and more but for E4M3): rows appended to its
+    last pages and attended to."""
+    n_pages = -(-(2 ** 31 + 2 ** 24) // (L * ps))
+    pages = torch.empty((n_pages * ps, L), dtype=kv, device=DEV)
+    scale = torch.empty(n_pages * ps, device=DEV) if kv == F8 else None
+    g = torch.Generator(device=DEV).manual_seed(24)
+    n = 150
+    x = torch.randn((n, L), generator=g, device=DEV).to(act)
+    blocks = -(-n // ps)
+    table = torch.arange(n_pages - 1, n_pages - 1 - blocks, -1, device=DEV).to(torch.int32)[None]
+    p = torch.arange(n, device=DEV)
+    rows = table[0].long()[p // ps] * ps + p % ps
+    assert int(rows.min()) * L > 2 ** 31
+    st = i32([0])
+    ops.dsa_paged_append(x, rows.to(torch.int32), pages, scale, status=st)
+    used = pages[rows.min():]                       # (the last pages, in 64 bits)
+    first = int(rows.min()) // ps * ps
+    vals = ref.values(pages[first:], None if scale is None else scale[first:])
+    have = vals[rows - first]
+    tol = x.double().abs() * (2.0 ** -4 if kv == F8 else 2.0 ** -8)
+    if kv == F8:
+        tol = torch.maximum(tol, 2.0 ** -10 * scale[rows].double()[:, None]) * 1.001
+    assert bool(((have - x.double()).abs() <= tol).all()) and used.shape[0] >= n
+    for Hm in ((64, 16) if act == BF else (4,)):
+        q = torch.randn((9, Hm, L), generator=g, device=DEV).to(act)
+        for width in (0, 2112):
+            tab = torch.full((1, max(blocks, -(-width // ps))), -1, dtype=torch.int32, device=DEV)
+            tab[:, :blocks] = table
+            s = dict(q=q, pages=pages, scale=scale, table=tab, lens=i32([n]), cu=i32([0, 9]),
+                     ps=ps, sm=1.0 / math.sqrt(L), T=9)
+            out, lse, status = attend(s)
+            assert status == 0
+            near = dict(s, table=torch.where(tab >= 0, tab - first // ps, tab))
+            want = ref.attend(q, vals, near["table"], s["lens"], ps, s["cu"], 0, 0, s["sm"])
+            more = ref.underflow(pages[rows], None if scale is None else scale[rows], act)
+            ref.check_attend(out, lse, want, act, L, out_more=more)
+    assert st.item() == 0
 
 
 # ---------------------------------------------------------------- chunk attention
@@ -334,6 +432,26 @@ def test_chunk_faults_are_flagged_and_contained(act, kv, Hm, L, width):
     assert st & ops.DEV_BAD_LENGTH and torch.isfinite(out.float()).all()
     s["cu"] = i32([20, 3, 7])
     assert attend(s)[2] & ops.DEV_BAD_LENGTH
+
+
+@pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, BF, 16, 512), (BF, F8, 64, 512),
+                                         (F32, F32, 4, 64)])
+def test_chunk_many_sequences_of_which_few_have_tokens(act, kv, Hm, L):
+    """8,192 sequences with five tokens among them; none at all; no lse; codes as bytes."""
+    lens, new = [0] * 8192, [0] * 8192
+    for b, n, k in ((0, 40, 1), (17, 300, 2), (8191, 129, 2)):
+        lens[b], new[b] = n, k
+    s = make(lens, new, Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=25)
+    out, _ = check(s)
+    check(dict(s, cu=i32([0] * 8193)))
+    T, got = s["T"], torch.full_like(s["q"], 7.0)
+    ws = torch.empty(ops.mla_paged_chunk_workspace_bytes(s["q"], s["pages"]), dtype=torch.uint8,
+                     device=DEV)
+    pages = s["pages"].view(torch.uint8) if kv == F8 else s["pages"]
+    ops.dsa_mla_paged_chunk(s["q"], pages, s["scale"], s["table"], s["lens"], 16, s["cu"], 0, 0,
+                            s["sm"], got, None, ws if ws.numel() else None)
+    torch.cuda.synchronize()
+    assert torch.equal(got, out) and T == 8
 
 
 @pytest.mark.parametrize("act,kv,Hm,L,width", [(BF, BF, 64, 512, 0), (BF, BF, 64, 512, 2112),

@@ -42,6 +42,7 @@ def test_plan_validation(lib):
     assert plan(lib, n_pages=1 << 20, ps=1 << 12) == ERR["DSA_ERR_UNSUPPORTED"]
     assert plan(lib, B=header_define("DSA_PLAN_MAX_B") + 1) == ERR["DSA_ERR_UNSUPPORTED"]
     assert plan(lib, T=header_define("DSA_PLAN_MAX_T") + 1) == ERR["DSA_ERR_UNSUPPORTED"]
+    assert plan(lib, B=1 << 10, width=1 << 20) == ERR["DSA_ERR_UNSUPPORTED"]
     for name in ("ctx", "new", "free", "begin", "table", "lens", "cu", "qs", "qp", "rows", "end",
                  "st"):
         assert plan(lib, **{name: A + 2}) == ERR["DSA_ERR_MISALIGNED"], name
