@@ -318,7 +318,8 @@ size_t dsa_mla_paged_decode_workspace_size(int Q, int Hm, int L, int out_width, 
  *   kv_rows -1, and the step DSA_DEV_NO_PAGE.
  * Apart from the two in-place forms, no output may overlap an input or another
  * output.  Supported: B <= DSA_PLAN_MAX_B, T and B * max_pages <= DSA_PLAN_MAX_T
- * (key_rows: row_base[b] + q_pos below 2^31).  One launch, no workspace.  B == 0 is a no-op that writes nothing.
+ * (key_rows: row_base[b] + q_pos below 2^31).  One launch, no workspace.  B == 0 is a
+ * no-op that writes nothing.
  * Device faults: DSA_DEV_BAD_LENGTH (a negative length, or one past 2^31 - 1
  * tokens: no new tokens for that sequence, and 0 cached ones where ctx_lens[b] is
  * negative; a negative free_begin: no free pages), DSA_DEV_TOKEN_CAP,
@@ -378,7 +379,9 @@ int dsa_paged_append(const void* kv_new, const int32_t* kv_rows, int T, int L, i
  *   workspace: dsa_mla_paged_chunk_workspace_size(...) bytes, 16-byte aligned, no
  *   initial value; calls in flight at the same time must not share one
  * The lengths are read on the GPU: a captured call follows them when replayed.
- * Outputs are deterministic.
+ * Outputs are deterministic.  E4M3 pages (bf16 activations, L = 512, page_size a
+ * multiple of 8): a query element is kept to 2^-21 of its row's largest, and a weight
+ * below 2^-24 of the largest may be lost.
  * Supported: L multiple of 8 up to 1024 and Hm up to 128 in both dtypes, with
  * pages of any kv_dtype; T * Hm < 2^31, B <= DSA_PLAN_MAX_B.
  * Device faults: DSA_DEV_BAD_PAGE (a visible position past the table or on a page

@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (whole)
         store_rows<kN, S::kOParts>(p, c.l, tl + kOCol, row0, heads, qw, hq, lane);
       else
-        store_part<kN, S::kOParts>(p, 2 * blockIdx.x + (begins ? 1 : 0), tl + kOCol, heads, qw, hq, lane);
+        store_part<kN, S::kOParts>(p, 2 * blockIdx.x + (begins ? 1 : 0), tl + kOCol, heads, qw, hq,
+                                   lane);
       tc_fence_before();  // O^T is read: the next segment's P releases it
     }
     if (!ok) hd = Header{-1, -1, 0, 0};
@@ -492,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           mbar_arrive_expect_tx(&c.q_full, 8 * S::kQBlock);
           for (int i = 0; i < 8; ++i)
-            tma_load_2d(sb + S::kQ + (2 * (i & 3) + (i >> 2)) * S::kQBlock, &q_map, i * 64, w.token * p.Hm + w.h0 * kN,
-                        &c.q_full);
+            tma_load_2d(sb + S::kQ + (2 * (i & 3) + (i >> 2)) * S::kQBlock, &q_map, i * 64,
+                        w.token * p.Hm + w.h0 * kN, &c.q_full);
         }
         ++segs;
       }
