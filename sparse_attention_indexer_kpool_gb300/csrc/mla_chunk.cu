@@ -277,19 +277,27 @@ namespace {
 
 // Whether pairs of CTAs are the faster kernel for bf16 pages: two row blocks of a step
 // must share their keys (two new tokens of a sequence on average, or more than 64
-// heads), and a row must see enough of them to pay for the exchange's start and end.
-// The lengths live on the device: the window and the block table's width bound them.
-// Measured on GB300, pair / single CTA in us (sequences x new tokens, 64 heads):
+// heads), a row must see enough of them to pay for the exchange's start and end (2,048),
+// and every pair must have enough tiles of 64 keys to hide it (64).  The lengths live on
+// the device: the window and the block table's width bound them.
+// Measured on GB300, pair / single CTA in us (sequences x new tokens, 64 heads; tiles a
+// pair):
 //   context  8,192, 32 x 4: 181 / 196, 16 x 16: 318 / 361, 4 x 256: 1,092 / 1,221
-//   context  2,048, 32 x 4:  72 /  70, 16 x 16: 111 / 104, 4 x 256:   330 /   336
-//   context    512, 32 x 4:  45 /  35, 16 x 16:  61 /  46, 4 x 256:   138 /   114
+//   context  4,096, 4 x 8 (13): 50 / 38, 8 x 8 (27): 68 / 59, 1 x 128 (54): 103 / 102,
+//            32 x 4 (54): 111 / 122, 1 x 256 (108): 171 / 178
+//   context  2,048, 16 x 16: 111 / 104, 4 x 256: 330 / 336
+//   context    512, 16 x 16:  61 /  46, 4 x 256: 138 / 114
+//   one sequence, 4 on 65,536 (27): 61 / 61, 8 on 131,072 (108): 157 / 168
 //   window   4,096 of 16,384, 4 x 256: 620 / 662; 2,048: 367 / 367; 512: 177 / 143
 //   context  8,192, 32 x 2: 108 / 109, single tokens 64 x 1: 165 / 111
+//   128 heads, context 8,192, 4 x 4 (27): 63 / 54, 16 x 4 (108): 178 / 207
 bool pairs_pay(const ChunkArgs& a) {
   if (a.kv.kv_dtype != DSA_BF16 || (a.Hm <= 64 && a.T < 2ll * a.B)) return false;
   const long long table = (long long)a.kv.max_pages * a.kv.page_size;
-  const long long seen = a.window > 0 ? (long long)a.window + a.sinks : table;
-  return (seen < table ? seen : table) > 2048;
+  const long long bound = a.window > 0 ? (long long)a.window + a.sinks : table;
+  const long long seen = bound < table ? bound : table;
+  const long long row_tiles = a.Hm <= 64 ? (a.T + 1ll) / 2 : a.T;
+  return seen > 2048 && row_tiles * ((seen + 63) / 64) >= 64 * (num_sms() / 2);
 }
 
 }  // namespace

@@ -14,6 +14,7 @@ from tests import _paged_ref as ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+WIDE = 320_000     # positions of a table whose width lets a few tokens' keys be many
 BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 
@@ -139,7 +140,7 @@ def test_calls_from_two_threads():
             want, _ = ref.plan(ctx, new, free, begin, n_pages, ps, [list(r) for r in table], T)
             s = make([70, 9], [3, 2], Hm=2, L=L, act=F32, kv=F32, ps=16, seed=L)
             exp = reference(s)
-            for _ in range(20):
+            for _ in range(6):
                 tab, e = i32(table), lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)
                 rows, cu = e(T), e(B + 1)
                 ops.dsa_paged_plan(i32(ctx), i32(new), i32(free), i32([begin]), n_pages, ps, tab,
@@ -229,7 +230,7 @@ def test_rows_past_32_bits(kv, L, act, ps):
     assert bool(((have - x.double()).abs() <= tol).all()) and used.shape[0] >= n
     for Hm in ((64, 16) if act == BF else (4,)):
         q = torch.randn((9, Hm, L), generator=g, device=DEV).to(act)
-        for width in (0, 2112):
+        for width in (0, WIDE):
             tab = torch.full((1, max(blocks, -(-width // ps))), -1, dtype=torch.int32, device=DEV)
             tab[:, :blocks] = table
             s = dict(q=q, pages=pages, scale=scale, table=tab, lens=i32([n]), cu=i32([0, 9]),
@@ -335,17 +336,18 @@ def test_chunk(Hm, L, act, kv, which):
 @pytest.mark.parametrize("which", range(len(LENS)))
 def test_chunk_wide_tables(Hm, which):
     """Two row blocks share their keys: chunks of two tokens and more (or more than 64 heads)
-    that may see more than 2,048 positions."""
+    that may see many positions."""
     lens, new = LENS[which]
-    for j, (window, sinks) in enumerate([(0, 0), (1, 2048), (64, 4000), (100, 1990), (2100, 0),
-                                         (700, 1400), (2 ** 31 - 1, 2 ** 31 - 1)]):
+    for j, (window, sinks) in enumerate([(0, 0), (1, WIDE), (64, WIDE), (100, 2 ** 31 - 1),
+                                         (WIDE, 0), (WIDE, 7), (2 ** 31 - 1, 2 ** 31 - 1)]):
         ps = (64, 16, 48, 8, 128, 24)[(which + j) % 6]
-        check(make(lens, new, Hm=Hm, ps=ps, seed=which * 10 + j, width=2112, pad=0), window, sinks)
+        check(make(lens, new, Hm=Hm, ps=ps, seed=which * 10 + j, width=WIDE, pad=0), window, sinks)
 
 
 def test_chunk_wide_tables_long_windows():
-    s = make([5000, 2600, 2300], [70, 3, 40], seed=16, q_std=2.0)
-    for window, sinks in ((2047, 2), (2100, 5), (2500, 300), (1, 2500), (4990, 1)):
+    s = make([5000, 2600, 2300], [200, 3, 120], seed=16, q_std=2.0)
+    for window, sinks in ((2047, 2), (2100, 5), (2500, 300), (1, 2500), (4990, 1), (64, 4000),
+                          (100, 1990), (700, 1400)):
         check(s, window, sinks)
 
 
@@ -370,7 +372,7 @@ def test_chunk_many_tokens(kv):
 def test_chunk_rising_and_falling_logits(act, kv, L):
     """Keys whose logits climb (and fall) by hundreds along the sequence: the running
     maximum has to move, far apart tiles must not overflow or vanish."""
-    for sign, Hm, width in ((1.0, 16, 0), (-1.0, 16, 0), (1.0, 64, 2112), (-1.0, 64, 2112)):
+    for sign, Hm, width in ((1.0, 16, 0), (-1.0, 16, 0), (1.0, 64, WIDE), (-1.0, 64, WIDE)):
         s = make([1300], [4], Hm=Hm, L=L, act=act, kv=kv, seed=4, width=width, pad=0)
         ramp = torch.linspace(-6.0, 6.0, 1300, device=DEV) * sign
         p = torch.arange(1300, device=DEV)
@@ -388,29 +390,30 @@ def test_chunk_rising_and_falling_logits(act, kv, L):
         check(s, 300, 7)
 
 
-@pytest.mark.parametrize("n,window", [(400, 50), (2400, 2060)])
+@pytest.mark.parametrize("n,m,window", [(400, 6, 50), (2500, 320, 2060)])
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 16, 512), (F32, F32, 4, 64)])
-def test_chunk_later_tokens_do_not_reach_earlier_ones(act, kv, Hm, L, n, window):
+def test_chunk_later_tokens_do_not_reach_earlier_ones(act, kv, Hm, L, n, m, window):
     """NaN, infinities and the type's largest values in the rows of later tokens, outside
     the window and behind the sequence leave the others as they are."""
     for fill in (math.nan, math.inf, -math.inf, torch.finfo(kv).max):
-        s = make([n], [6], Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=6, hidden=fill)
+        s = make([n], [m], Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=6, hidden=fill)
         want, want_lse, _ = attend(s, window, 3)
         p = torch.arange(n, device=DEV)
         rows = s["table"][0].long()[p // 16] * 16 + p % 16
         hide = torch.zeros(n, dtype=torch.bool, device=DEV)
-        hide[n - 3:] = True                  # tokens 3, 4, 5 of the chunk
-        hide[3:n - 6 - window + 1] = True    # outside every window
+        hide[n - 3:] = True                  # the chunk's last three tokens
+        hide[3:n - m - window + 1] = True    # outside every window
         s["pages"][rows[hide]] = torch.full((), fill, device=DEV).to(kv)
         if kv == F8:
             s["scale"][rows[hide]] = fill
         out, lse, _ = attend(s, window, 3)
-        assert torch.equal(out[:3], want[:3]) and torch.equal(lse[:3], want_lse[:3])
+        k = m - 3
+        assert torch.equal(out[:k], want[:k]) and torch.equal(lse[:k], want_lse[:k])
         if math.isnan(fill):                 # and it reaches those that see it
-            assert torch.isnan(out[3:6].float()).all()
+            assert torch.isnan(out[k:m].float()).all()
 
 
-@pytest.mark.parametrize("width", [0, 2112])
+@pytest.mark.parametrize("width", [0, WIDE])
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 64, 512), (F32, F32, 4, 64)])
 def test_chunk_faults_are_flagged_and_contained(act, kv, Hm, L, width):
     def make(*a, **kw):
@@ -454,7 +457,7 @@ def test_chunk_many_sequences_of_which_few_have_tokens(act, kv, Hm, L):
     assert torch.equal(got, out) and T == 8
 
 
-@pytest.mark.parametrize("act,kv,Hm,L,width", [(BF, BF, 64, 512, 0), (BF, BF, 64, 512, 2112),
+@pytest.mark.parametrize("act,kv,Hm,L,width", [(BF, BF, 64, 512, 0), (BF, BF, 64, 512, WIDE),
                                                (BF, F8, 64, 512, 0), (BF, F8, 16, 512, 0),
                                                (F32, F32, 4, 64, 0)])
 def test_chunk_softmax_scales(act, kv, Hm, L, width):
@@ -490,7 +493,7 @@ def test_chunk_e4m3_queries_with_a_large_element(Hm, ps):
 
 
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 16, 512), (F32, F32, 4, 64)])
-@pytest.mark.parametrize("cols", [3, 140])
+@pytest.mark.parametrize("cols", [3, WIDE // 16])
 def test_chunk_lengths_past_the_table_cost_no_more_than_it(act, kv, Hm, L, cols):
     """A length far behind the table's width: flagged, and the tokens see the positions that
     the table has (with a window that has left them: the sinks alone)."""
@@ -508,7 +511,7 @@ def test_chunk_lengths_past_the_table_cost_no_more_than_it(act, kv, Hm, L, cols)
         ref.check_attend(out[1:], lse[1:], reference(rest, window, sinks), act, L)
 
 
-@pytest.mark.parametrize("kv,Hm,width,ps", [(BF, 64, 0, 64), (BF, 64, 2112, 64), (BF, 16, 0, 5),
+@pytest.mark.parametrize("kv,Hm,width,ps", [(BF, 64, 0, 64), (BF, 64, WIDE, 64), (BF, 16, 0, 5),
                                             (F8, 64, 0, 64), (F8, 16, 0, 5)])
 def test_chunk_gives_up_and_recovers(kv, Hm, width, ps):
     """The failure drill: no tile arrives, the first waits run out after a millisecond, the
@@ -525,7 +528,7 @@ def test_chunk_gives_up_and_recovers(kv, Hm, width, ps):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-@pytest.mark.parametrize("width", [0, 2112])
+@pytest.mark.parametrize("width", [0, WIDE])
 @pytest.mark.parametrize("kv", [BF, F8])
 def test_chunk_infinite_and_nan_queries_stay_in_their_rows(kv, width):
     s = make([300, 40], [5, 3], kv=kv, seed=11, width=width)
