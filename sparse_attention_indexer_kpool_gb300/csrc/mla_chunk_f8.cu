@@ -55,7 +55,7 @@ constexpr float kLeastLog = -60.f;
 constexpr float kLoUp = 16.f;             // of the queries' lo parts
 
 struct Ctl {
-  float m[64], nm[64], alpha[64], l[64];  // per head; first: read as float4
+  float m[64], nm[64], alpha[64], l[64], move[64];  // per head; first: read as float4
   float sq[64];                           // the query rows' scales
   float red[4][64];
   uint64_t full[kStages][4], empty[kStages][4];  // by block of 128 codes
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float high_at = kRaise8 - lg;
         float e[kW];
         // z = S * query scale * row scale * softmax scale, S of both parts
-        auto logits = [&]() {
+        {
           const uint32_t ts = tl + st * S::kSCols + (uint32_t)(hq * kW);
           tmem_ldw<kW>(ts, e);
 #pragma unroll
@@ -301,8 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             e[4 * q + 2] *= s4.z;
             e[4 * q + 3] *= s4.w;
           }
-        };
-        logits();
+        }
         bool high = unset;
 #pragma unroll
         for (int q = 0; q < kW / 4; ++q) {  // minus the references (0: none yet)
@@ -323,36 +322,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (full) {
-          logits();
+          float top[kW];  // of u, relative to the references so far
 #pragma unroll
-          for (int i = 0; i < kW; ++i) e[i] = valid ? fmaf(e[i], zs, lg) : -INFINITY;
-          const float m = across_rows<kW, true>(e, lane);
+          for (int i = 0; i < kW; ++i) top[i] = e[i] + lg;
+          const float m = across_rows<kW, true>(top, lane);
           if (lane < kW) c.red[qw][hq * kW + lane] = m;
           if (tid == 0) c.raise = 0;
           sync_soft();
           if (tid < kN) {
-            const float tm = fmaxf(fmaxf(c.red[0][tid], c.red[1][tid]),
-                                   fmaxf(c.red[2][tid], c.red[3][tid]));
+            const float rel = fmaxf(fmaxf(c.red[0][tid], c.red[1][tid]),
+                                    fmaxf(c.red[2][tid], c.red[3][tid]));
             const float m_old = c.m[tid];
-            float a = 1.f;
-            if (m_old == -INFINITY) {
-              c.m[tid] = tm;  // nothing accumulated for this head yet
-            } else if (tm > m_old + kRaise8) {
-              c.m[tid] = tm;
-              a = ex2_fast(m_old - tm);
+            float a = 1.f, move = 0.f;
+            if (m_old == -INFINITY) {  // nothing accumulated for this head yet
+              c.m[tid] = rel;
+              if (rel != -INFINITY) move = -rel;
+            } else if (rel > kRaise8) {
+              c.m[tid] = m_old + rel;
+              a = ex2_fast(-rel);
+              move = -rel;
               c.raise = 1;
             }
             c.alpha[tid] = a;
+            c.move[tid] = move;
             c.nm[tid] = c.m[tid] == -INFINITY ? 0.f : -c.m[tid];
           }
           sync_soft();
           unset = false;
 #pragma unroll
           for (int i = 0; i < kW; ++i) unset |= c.m[hq * kW + i] == -INFINITY;
-          logits();
+          // (an infinite maximum: its key's weight is NaN, as in the formula)
 #pragma unroll
-          for (int i = 0; i < kW; ++i)
-            e[i] = valid ? fmaf(e[i], zs, c.nm[hq * kW + i]) : -INFINITY;
+          for (int i = 0; i < kW; ++i) e[i] += c.move[hq * kW + i];
         }
         if (full && c.raise) {
 #pragma unroll

@@ -60,7 +60,7 @@ __host__ __device__ constexpr int cta_threads(int src) {
 }
 
 struct Ctl {
-  float m[64], nm[64], alpha[64], l[64];  // per head; first: read as float4
+  float m[64], nm[64], alpha[64], l[64], move[64];  // per head; first: read as float4
   float red[4][64];
   float rs[kKeys];
   int valid[kKeys];               // copied rows: the position is seen and has a page
@@ -212,26 +212,29 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
           break;
         }
         if (full) {
-          tmem_ldw<kW>(tl + hq * kW, e);
+          float top[kW];  // relative to the references so far
 #pragma unroll
-          for (int i = 0; i < kW; ++i) e[i] = valid ? e[i] * zs : -INFINITY;
-          const float m = across_rows<kW, true>(e, lane);
+          for (int i = 0; i < kW; ++i) top[i] = e[i];
+          const float m = across_rows<kW, true>(top, lane);
           if (lane < kW) c.red[qw][hq * kW + lane] = m;
           if (tid == 0) c.raise = 0;
           sync_soft();
           if (tid < kN) {
-            const float tm = fmaxf(fmaxf(c.red[0][tid], c.red[1][tid]),
-                                   fmaxf(c.red[2][tid], c.red[3][tid]));
+            const float rel = fmaxf(fmaxf(c.red[0][tid], c.red[1][tid]),
+                                    fmaxf(c.red[2][tid], c.red[3][tid]));
             const float m_old = c.m[tid];
-            float a = 1.f;
-            if (m_old == -INFINITY) {
-              c.m[tid] = tm;  // nothing accumulated for this head yet
-            } else if (tm > m_old + kRaiseAt) {
-              c.m[tid] = tm;
-              a = ex2_fast(m_old - tm);
+            float a = 1.f, move = 0.f;
+            if (m_old == -INFINITY) {  // nothing accumulated for this head yet
+              c.m[tid] = rel;
+              if (rel != -INFINITY) move = -rel;
+            } else if (rel > kRaiseAt) {
+              c.m[tid] = m_old + rel;
+              a = ex2_fast(-rel);
+              move = -rel;
               c.raise = 1;
             }
             c.alpha[tid] = a;
+            c.move[tid] = move;
             c.nm[tid] = c.m[tid] == -INFINITY ? 0.f : -c.m[tid];
           }
           sync_soft();
@@ -253,9 +256,9 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
               }
             }
           }
-          tmem_ldw<kW>(tl + hq * kW, e);
+          // (an infinite maximum: its key's weight is NaN, as in the formula)
 #pragma unroll
-          for (int i = 0; i < kW; ++i) e[i] = valid ? fmaf(e[i], zs, c.nm[hq * kW + i]) : -INFINITY;
+          for (int i = 0; i < kW; ++i) e[i] += c.move[hq * kW + i];
         }
 #pragma unroll
         for (int i = 0; i < kW; ++i) e[i] = ex2_fast(e[i]);
