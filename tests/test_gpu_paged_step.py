@@ -134,33 +134,40 @@ def test_plan_at_the_end_of_the_positions():
 
 def test_calls_from_two_threads():
     """The plan and the generic attention at different sizes from two threads, a stream each."""
-    def work(B, L, out):
+    jobs, got = [], {}
+    for B, L in ((8192, 1024), (4200, 520)):
+        p = random_plan(B, B, 16, 2, 40, 5)
+        s = make([70, 9], [3, 2], Hm=2, L=L, act=F32, kv=F32, ps=16, seed=L)
+        jobs.append((B, L, p, s, [i32(x) for x in (p[0], p[1], p[2], [p[3]], p[6])]))
+    torch.cuda.synchronize()
+
+    def work(B, p, s, inputs):
+        ctx, new, free, begin, table = inputs
         with torch.cuda.stream(torch.cuda.Stream()):
-            ctx, new, free, begin, n_pages, ps, table, T, _ = random_plan(B, B, 16, 2, 40, 5)
-            want, _ = ref.plan(ctx, new, free, begin, n_pages, ps, [list(r) for r in table], T)
-            s = make([70, 9], [3, 2], Hm=2, L=L, act=F32, kv=F32, ps=16, seed=L)
-            exp = reference(s)
-            for _ in range(6):
-                tab, e = i32(table), lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)
-                rows, cu = e(T), e(B + 1)
-                ops.dsa_paged_plan(i32(ctx), i32(new), i32(free), i32([begin]), n_pages, ps, tab,
-                                   e(B), cu, e(T), e(T), rows, e(1))
+            e = lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)  # noqa: E731
+            runs = []
+            for _ in range(20):
+                tab, rows = table.clone(), e(p[7])
+                ops.dsa_paged_plan(ctx, new, free, begin, p[4], p[5], tab, e(B), e(B + 1), e(p[7]),
+                                   e(p[7]), rows, e(1))
                 o, ls = torch.empty_like(s["q"]), torch.empty(s["q"].shape[:2], device=DEV)
                 ops.dsa_mla_paged_chunk(s["q"], s["pages"], None, s["table"], s["lens"], 16,
                                         s["cu"], 0, 0, s["sm"], o, ls)
-                torch.cuda.current_stream().synchronize()
-                assert rows.tolist() == want["kv_rows"] and tab.tolist() == want["table"]
-                ref.check_attend(o, ls, exp, F32, L, rows=torch.arange(5, device=DEV))
-            out.append(B)
+                runs.append((rows, tab, o, ls))
+            torch.cuda.current_stream().synchronize()
+            got[B] = runs
 
-    done = []
-    threads = [threading.Thread(target=work, args=(B, L, done)) for B, L in ((8192, 1024),
-                                                                              (4200, 520))]
+    threads = [threading.Thread(target=work, args=(B, p, s, x)) for B, _, p, s, x in jobs]
     for th in threads:
         th.start()
     for th in threads:
         th.join()
-    assert sorted(done) == [4200, 8192]
+    for B, L, p, s, _ in jobs:
+        want, _ = ref.plan(p[0], p[1], p[2], p[3], p[4], p[5], [list(r) for r in p[6]], p[7])
+        exp = reference(s)
+        for rows, tab, o, ls in got[B]:
+            assert rows.tolist() == want["kv_rows"] and tab.tolist() == want["table"]
+            ref.check_attend(o, ls, exp, F32, L, rows=torch.arange(5, device=DEV))
 
 
 # ---------------------------------------------------------------- append
