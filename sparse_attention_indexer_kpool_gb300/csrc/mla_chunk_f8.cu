@@ -28,13 +28,15 @@
 // What bounds it.  64 heads: the products.  S^T is 16 MMAs of 128 x 128 x 32 (both query
 // parts as N, 66 cycles each), O^T 48 of 128 x 64 x 32 (50 cycles, 6 KB of shared memory
 // each), about 4,000 cycles a tile with the next tile's rows through the same port; 4,700
-// measured, 5,500 where a reference is raised.  32 heads and fewer: S^T 16 of N = 64 and
+// measured, 700 more where a reference is raised.  32 heads and fewer: S^T 16 of N = 64 and
 // O^T 16 of N = 96 (the three weight parts beside one another), 1,700 cycles, so the
 // chain load, S^T, softmax, O^T of a tile, two in flight: 4,000 cycles.
 // Measured on GB300: 12 sequences of 1 to 300 new tokens on up to 5,000 keys, 64 heads,
-// 678 us (729 TFLOP/s counted once; one part of the queries after the other: 773); 16
-// heads, 64 single tokens on 4,096 to 16,000 keys in pages of 16, 87 us (334 MB: 3.8
-// TB/s, 0.57 of the measured copy rate; parts one after the other: 103).
+// 666 us (742 TFLOP/s counted once; one part of the queries after the other: 773); 16
+// heads, 64 single tokens on 4,096 to 16,000 keys in pages of 16, 86 us (334 MB: 3.9
+// TB/s, 0.57 of the measured copy rate; parts one after the other: 103).  A softmax
+// thread has half of a tile's heads; a quarter each, on twice the warps, took longer (704
+// us on the former).
 #include "mla_chunk.cuh"
 
 namespace dsa {
