@@ -386,7 +386,7 @@ int dsa_paged_append(const void* kv_new, const int32_t* kv_rows, int T, int L, i
  * pages of any kv_dtype; T * Hm < 2^31, B <= DSA_PLAN_MAX_B.
  * Device faults: DSA_DEV_BAD_PAGE (a visible position past the table or on a page
  * outside [0, n_pages): skipped), DSA_DEV_BAD_LENGTH (rows without a position see
- * nothing; cu_new is cut to [0, T] and taken as empty where it decreases),
+ * nothing; cu_new is cut to [0, T]; where it decreases, the outputs are unspecified),
  * DSA_DEV_TIMEOUT (outputs unspecified).
  */
 int dsa_mla_paged_chunk(const void* q_lat, const dsa_paged_kv* kv, const int32_t* cu_new, int T,

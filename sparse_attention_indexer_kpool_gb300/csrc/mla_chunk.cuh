@@ -145,12 +145,13 @@ __device__ __forceinline__ unsigned long long find_share(const Params& p, int hb
             b1 = min(p.B, b0 + per);
   if (tid == 0) st->b = p.B;
   unsigned long long mine = 0;
-  bool odd = false, past = false;
+  bool odd = false, past = false, falls = false;
   for (int b = b0; b < b1; ++b) {
     const int cu0 = p.cu_new[b], cu1 = p.cu_new[b + 1], len = p.kv.seq_lens[b];
     const Seq s = seq_of<kT, kPair>(cu0, cu1, len, p);
     odd |= cu0 < 0 || cu1 < cu0 || cu1 > p.T || (s.n > 0 && s.base < 0);
     past |= s.n > 0 && len > p.cap;
+    falls |= cu1 < cu0;
     mine += (unsigned long long)row_tiles<kT, kPair>(s, hb) * s.u;
   }
   if (odd && reports) flag(p.status, DSA_DEV_BAD_LENGTH);
@@ -162,12 +163,14 @@ __device__ __forceinline__ unsigned long long find_share(const Params& p, int hb
     if (lane >= o) inc += u;
   }
   if (lane == 31) st->scan[warp] = inc;
-  __syncthreads();
+  // rows of several sequences at once (the work would have no bound): nothing is done
+  falls = __syncthreads_or(falls);
   unsigned long long before = inc - mine, total = 0, v0, v1;
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += st->scan[w];
     total += st->scan[w];
   }
+  if (falls) total = 0;
   if (total < workers) {
     v0 = me < total ? me : total;
     v1 = me < total ? me + 1 : total;

@@ -444,6 +444,24 @@ def test_chunk_faults_are_flagged_and_contained(act, kv, Hm, L, width):
     assert attend(s)[2] & ops.DEV_BAD_LENGTH
 
 
+@pytest.mark.parametrize("act,kv,Hm,L,width", [(BF, BF, 64, 512, 0), (BF, BF, 128, 512, 3200),
+                                               (BF, F8, 16, 512, 0), (F32, F32, 4, 64, 0)])
+def test_chunk_rows_of_many_sequences_at_once_do_not_multiply(act, kv, Hm, L, width):
+    """Ends that rise and fall would give every row to thousands of sequences: flagged, and
+    over soon."""
+    s = make([900] + [0] * 8191, [600] + [0] * 8191, Hm=Hm, L=L, act=act, kv=kv, ps=16, seed=26,
+             width=width, pad=0)
+    s["cu"] = i32([0, 600] * 4096 + [0])
+    s["lens"] = i32([900] * 8192)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    attend(s)
+    start.record()
+    st = attend(s)[2]
+    end.record()
+    torch.cuda.synchronize()
+    assert st & ops.DEV_BAD_LENGTH and start.elapsed_time(end) < 100.0
+
+
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, BF, 16, 512), (BF, F8, 64, 512),
                                          (F32, F32, 4, 64)])
 def test_chunk_many_sequences_of_which_few_have_tokens(act, kv, Hm, L):
@@ -550,7 +568,7 @@ def test_chunk_infinite_and_nan_queries_stay_in_their_rows(kv, width):
 
 
 def test_chunk_same_bits_every_time_and_beside_other_calls():
-    a = make([3000, 20, 777], [5, 20, 300], seed=12)   # (two row blocks share their keys)
+    a = make([3100, 20, 777], [5, 20, 300], seed=12, width=WIDE)   # (row blocks share their keys)
     b = make([90, 9000], [1, 1], kv=F8, seed=13)
     want_a, want_b = attend(a), attend(b)
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -571,6 +589,29 @@ def test_chunk_same_bits_every_time_and_beside_other_calls():
     for i, (out, lse, _) in enumerate(got):
         want = (want_a, want_b)[i % 2]
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("kv,Hm,width", [(BF, 64, WIDE), (BF, 128, WIDE), (F8, 64, 0), (F8, 16, 0)])
+def test_chunk_captured_follows_lengths(kv, Hm, width):
+    """A captured call replayed after its lengths and the step's rows have changed."""
+    first = make([900, 40, 300], [30, 2, 8], Hm=Hm, kv=kv, seed=27, width=width, pad=0)
+    s = {k: v.clone() if torch.is_tensor(v) else v for k, v in first.items()}
+    out, lse = torch.full_like(s["q"], 7.0), torch.full((40, Hm), 7.0, device=DEV)
+    ws = torch.empty(ops.mla_paged_chunk_workspace_bytes(s["q"], s["pages"]), dtype=torch.uint8,
+                     device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.dsa_mla_paged_chunk(s["q"], s["pages"], s["scale"], s["table"], s["lens"], s["ps"],
+                                s["cu"], 0, 0, s["sm"], out, lse, ws)
+    for now in (first, dict(first, lens=i32([899, 39, 64]), cu=i32([0, 3, 39, 40]))):
+        s["lens"].copy_(now["lens"])
+        s["cu"].copy_(now["cu"])
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = reference(now)
+        ref.check_attend(out, lse, want, BF, 512, rows=torch.arange(int(now["cu"][-1]), device=DEV),
+                         out_more=ref.underflow(s["pages"], s["scale"], BF))
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
