@@ -305,7 +305,7 @@ bool pairs_pay(const ChunkArgs& a) {
 int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   if (mla_chunk_umma_ok(a.L, a.dtype, a.kv.kv_dtype)) {
     // E4M3 codes as they are need TMA's boxes of 8 rows; other page sizes are widened
-    // (pages of 64, 16 heads, 64 single tokens on 8,192 keys: 71 us, widened 141; 64
+    // (pages of 64, 16 heads, 64 single tokens on 8,192 keys: 65 us, widened 141; 64
     // heads, 4 x 128 tokens on 4,096 keys: 354 and 495)
     if (a.kv.kv_dtype == DSA_FP8_E4M3 && a.kv.page_size % 8 == 0)
       return launch_mla_chunk_f8(a, workspace, stream);

@@ -342,27 +342,33 @@ __device__ __forceinline__ void tmem_stw(uint32_t ta, const float (&v)[kW]) {
   if constexpr (kW == 32) tmem_st32(ta, v); else tmem_st16(ta, v);
 }
 
-// Barriers of the eight softmax warps (barrier 0 is the CTA's).
+// Heads of a softmax thread, of kN a row tile: half of them, but 16 at least; four warps (a
+// TMEM lane quarter each) for every such group.
+__host__ __device__ constexpr int heads_of(int n) { return n == 64 ? 32 : 16; }
+__host__ __device__ constexpr int soft_threads(int n) { return 128 * (n / heads_of(n)); }
+// Barriers of the softmax threads (barrier 0 is the CTA's).
+template <int kThreads>
 __device__ __forceinline__ void sync_soft() {
-  asm volatile("barrier.cta.sync 1, 256;" :: : "memory");
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
+template <int kThreads>
 __device__ __forceinline__ bool vote_soft(bool v) {  // whether any of them says so
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-      " barrier.cta.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+      " barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)v)
+      : "r"((uint32_t)v), "n"(kThreads)
       : "memory");
   return r != 0;
 }
 
 // A chunk's output columns of a thread's heads: the sum of kParts accumulators side by
-// side (kN columns each).
-template <int kN, int kParts>
-__device__ __forceinline__ void load_o(uint32_t to, int mc, int hq, float (&o)[kN / 2]) {
-  constexpr int kW = kN / 2;
-  const uint32_t ta = to + (uint32_t)(mc * kParts * kN + hq * kW);
+// side (kN columns each; the next chunk's begin kCols on).
+template <int kN, int kParts, int kCols>
+__device__ __forceinline__ void load_o(uint32_t to, int mc, int hq, float (&o)[heads_of(kN)]) {
+  constexpr int kW = heads_of(kN);
+  const uint32_t ta = to + (uint32_t)(mc * kCols + hq * kW);
   tmem_ldw<kW>(ta, o);
 #pragma unroll
   for (int k = 1; k < kParts; ++k) {
@@ -373,14 +379,14 @@ __device__ __forceinline__ void load_o(uint32_t to, int mc, int hq, float (&o)[k
   }
 }
 
-// A segment's end, by the eight softmax warps (lane quarter qw, heads kN / 2 hq ..):
+// A segment's end, by the softmax warps (lane quarter qw, heads heads_of(kN) hq ..):
 // a row tile's rows, normalised by inv[head]; O^T (kN columns a chunk of 128 latent
 // columns) from TMEM at `to`.  A lane pair holds two latent columns of every head:
 // each lane of the pair stores both columns of one of two heads.
-template <int kN, int kParts = 1>
+template <int kN, int kParts = 1, int kCols = kN>
 __device__ __forceinline__ void store_rows(const Params& p, const float* inv, uint32_t to,
                                            long long row0, int heads, int qw, int hq, int lane) {
-  constexpr int kW = kN / 2;
+  constexpr int kW = heads_of(kN);
   const bool upper = lane & 1;
   float iv[kW];
 #pragma unroll
@@ -388,7 +394,7 @@ __device__ __forceinline__ void store_rows(const Params& p, const float* inv, ui
 #pragma unroll 1
   for (int mc = 0; mc < 4; ++mc) {
     float o[kW];
-    load_o<kN, kParts>(to, mc, hq, o);
+    load_o<kN, kParts, kCols>(to, mc, hq, o);
     __nv_bfloat16* dst =
         p.out + (row0 + hq * kW + (upper ? 1 : 0)) * kL + mc * 128 + qw * 32 + (lane & ~1);
 #pragma unroll
@@ -402,24 +408,25 @@ __device__ __forceinline__ void store_rows(const Params& p, const float* inv, ui
   }
 }
 // an unnormalised part of a row tile, for the join
-template <int kN, int kParts = 1>
+template <int kN, int kParts = 1, int kCols = kN>
 __device__ __forceinline__ void store_part(const Params& p, int slot, uint32_t to, int heads,
                                            int qw, int hq, int lane) {
-  constexpr int kW = kN / 2;
+  constexpr int kW = heads_of(kN);
   float* dst = p.part_o + ((long long)slot * kN + hq * kW) * kL + qw * 32 + lane;
 #pragma unroll 1
   for (int mc = 0; mc < 4; ++mc) {
     float o[kW];
-    load_o<kN, kParts>(to, mc, hq, o);
+    load_o<kN, kParts, kCols>(to, mc, hq, o);
 #pragma unroll
     for (int i = 0; i < kW; ++i)
       if (hq * kW + i < heads) dst[(long long)i * kL + mc * 128] = o[i];
   }
 }
 // a token that sees nothing
+template <int kThreads>
 __device__ __forceinline__ void store_nothing(const Params& p, long long row0, int heads,
                                               int tid) {
-  for (int i = tid; i < heads * (kL / 8); i += 256)
+  for (int i = tid; i < heads * (kL / 8); i += kThreads)
     *reinterpret_cast<uint4*>(p.out + row0 * kL + (long long)i * 8) = make_uint4(0u, 0u, 0u, 0u);
   if (p.lse && tid < heads) p.lse[row0 + tid] = -INFINITY;
 }

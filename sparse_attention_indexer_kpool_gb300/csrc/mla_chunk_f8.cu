@@ -30,11 +30,13 @@
 // each), about 4,000 cycles a tile with the next tile's rows through the same port; 4,700
 // measured, 700 more where a reference is raised.  32 heads and fewer: S^T 16 of N = 64 and
 // O^T 16 of N = 96 (the three weight parts beside one another), 1,700 cycles, so the
-// chain load, S^T, softmax, O^T of a tile, two in flight: 4,000 cycles.
+// chain load, S^T, softmax, O^T of a tile, two in flight: 4,000 cycles.  16 heads and fewer
+// leave room for a third tile.
 // Measured on GB300: 12 sequences of 1 to 300 new tokens on up to 5,000 keys, 64 heads,
 // 666 us (742 TFLOP/s counted once; one part of the queries after the other: 773); 16
-// heads, 64 single tokens on 4,096 to 16,000 keys in pages of 16, 86 us (334 MB: 3.9
-// TB/s, 0.57 of the measured copy rate; parts one after the other: 103).  A softmax
+// heads, 64 single tokens on 4,096 to 16,000 keys in pages of 16, 78 us (334 MB: 4.3
+// TB/s, 0.63 of the measured copy rate; two tiles in flight: 86, and 103 with the parts one
+// after the other).  A softmax
 // thread has half of a tile's heads; a quarter each, on twice the warps, took longer (704
 // us on the former).
 #include "mla_chunk.cuh"
@@ -47,15 +49,16 @@ using namespace chunk;
 constexpr int kKeys = 128;
 constexpr int kBlock = kKeys * 128;       // 128 rows x 128 codes, 16 KB
 constexpr int kStage = 4 * kBlock;        // a tile
-constexpr int kStages = 2;
-constexpr int kSoftThreads = 256;
 constexpr int kTmaWarps = 2;
-constexpr int kThreads = kSoftThreads + 32 * (kTmaWarps + 1);
+__host__ __device__ constexpr int cta_threads(int n) {
+  return soft_threads(n) + 32 * (kTmaWarps + 1);
+}
 constexpr float kRaise8 = 7.f;            // base-2 growth of u that raises a reference
 constexpr float kUp = 256.f;              // weights in E5M2 are scaled by 2^8
 constexpr float kLeastLog = -60.f;
 constexpr float kLoUp = 16.f;             // of the queries' lo parts
 
+template <int kStages>
 struct Ctl {
   float m[64], nm[64], alpha[64], l[64], move[64];  // per head; first: read as float4
   float sq[64];                           // the query rows' scales
@@ -64,7 +67,7 @@ struct Ctl {
   uint64_t s_full[kStages], p_full, o_full, q_full, q_empty, drain;
   Start start;
   uint32_t tmem;
-  unsigned groups[kStages];               // TMA boxes of the tile that hold rows
+  unsigned groups[kStages];            // TMA boxes of the tile that hold rows
   int raise;
   int soft_dead[2];
   int dead;
@@ -72,21 +75,26 @@ struct Ctl {
 
 template <int kN>
 struct Smem {
+  static constexpr int kStages = kN == 16 ? 3 : 2;      // tiles in flight: what fits
   static constexpr int kQBlock = kN * 128;              // kN heads x 128 codes
   // One MMA takes both parts of the queries as 2 kN rows, [block][part][head], and the
-  // three parts of 32 heads' weights as 96 columns of P; each part has its own columns
-  // of the result, which the softmax (and the end) adds.  (64 heads' outputs in three
-  // parts do not fit TMEM: there the parts add up in the accumulator.)
-  static constexpr int kOParts = kN == 32 ? 3 : 1;
-  static constexpr uint32_t kSCols = 2 * kN, kOCols = kOParts * kN;  // of a stage, of a chunk
-  static constexpr int kPPart = kKeys * kN;             // a weight's part, 1 byte each
+  // three parts of up to 32 heads' weights as 3 kN columns of P; each part has its own
+  // columns of the result, which the softmax (and the end) adds.  (64 heads' outputs in
+  // three parts do not fit TMEM: there the parts add up in the accumulator.)
+  static constexpr int kOParts = kN == 64 ? 1 : 3, kON = kOParts * kN;
+  static constexpr uint32_t kSCols = 2 * kN, kOCols = (kON + 31) / 32 * 32;  // stage, chunk
+  // P: rows of a key's weights, 64 or 32 bytes each: a part of 64 or of 32 heads, or two
+  // parts of 16 (the third has half a buffer)
+  static constexpr int kPRow = kN == 64 ? 64 : 32, kPBufs = kN == 16 ? 2 : 3;
+  static constexpr int kPPart = kKeys * kPRow;
   static constexpr size_t kKv = 0;
   static constexpr size_t kQ = (size_t)kStages * kStage;
   static constexpr size_t kP = kQ + 8 * (size_t)kQBlock;
-  static constexpr size_t kCtl = kP + 3 * (size_t)kPPart;
-  static constexpr size_t kBytes = 1024 + kCtl + sizeof(Ctl);
+  static constexpr size_t kCtl = kP + kPBufs * (size_t)kPPart;
+  static constexpr size_t kBytes = 1024 + kCtl + sizeof(Ctl<kStages>);
 };
-static_assert(Smem<64>::kBytes <= 227 * 1024, "shared memory budget");
+static_assert(Smem<64>::kBytes <= 227 * 1024 && Smem<16>::kBytes <= 227 * 1024,
+              "shared memory budget");
 
 // Instruction descriptor, kind::f8f6f4: fp32 accumulator, E4M3 A, E4M3 or E5M2 B.
 constexpr uint32_t idesc_f8(int m, int n, bool a_mn, bool b_e5m2, bool b_mn) {
@@ -176,20 +184,23 @@ __global__ void __launch_bounds__(256)
 }
 
 template <int kN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(cta_threads(kN), 1)
     mla_chunk_f8_kernel(const __grid_constant__ CUtensorMap q_map,
                         const __grid_constant__ CUtensorMap kv_map,
                         const __grid_constant__ CUtensorMap ahead_map,
                         const float* __restrict__ q_scale, const Params p) {
   using S = Smem<kN>;
-  constexpr int kW = kN / 2;  // heads per softmax thread
-  constexpr int kTma0 = kSoftThreads / 32, kMmaWarp = kTma0 + kTmaWarps;
+  constexpr int kStages = S::kStages, kSoft = soft_threads(kN);
+  auto stage_of = [](int tile) { return (int)((unsigned)tile % (unsigned)kStages); };
+  auto phase_of = [](int tile) { return (unsigned)tile / (unsigned)kStages & 1u; };
+  constexpr int kW = heads_of(kN), kGroups = kN / kW;  // heads of a softmax thread
+  constexpr int kTma0 = kSoft / 32, kMmaWarp = kTma0 + kTmaWarps;
   constexpr uint32_t kOCol = kStages * S::kSCols;
   constexpr int kTmemCols = 512;
   static_assert(kOCol + 4 * S::kOCols <= kTmemCols, "TMEM columns");
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Ctl& c = *reinterpret_cast<Ctl*>(sb + S::kCtl);
+  auto& c = *reinterpret_cast<Ctl<S::kStages>*>(sb + S::kCtl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hb = (p.Hm + kN - 1) / kN;
 
@@ -201,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_init(&c.s_full[i], 1);
     }
-    mbar_init(&c.p_full, kSoftThreads / 32);
+    mbar_init(&c.p_full, kSoft / 32);
     mbar_init(&c.o_full, 1);
     mbar_init(&c.q_full, 1);
     mbar_init(&c.q_empty, 1);
@@ -220,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // every input may come from the kernel just before
   pdl_launch_dependents();
 
-  const unsigned long long units = find_share<kKeys, false, kThreads>(
+  const unsigned long long units = find_share<kKeys, false, cta_threads(kN)>(
       p, hb, blockIdx.x, gridDim.x, &c.start, blockIdx.x == 0);
   const uint32_t tmem = c.tmem;
   Walk<kKeys, false> w(p, hb, c.start, units);
@@ -258,18 +269,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int heads = min(kN, p.Hm - w.h0 * kN);
       const long long row0 = (long long)w.token * p.Hm + w.h0 * kN;
       if (tid < kN) c.sq[tid] = tid < heads ? __ldg(q_scale + row0 + tid) : 0.f;
-      sync_soft();
+      sync_soft<kSoft>();
       for (int v = w.ta; v < w.tb; ++v, ++tiles) {
-        const int st = tiles & 1;
+        const int st = stage_of(tiles), dead_at = tiles & 1;
         const float rs_next = v + 1 < w.tb ? scale_of(w.k, w.b, v + 1) : 0.f;
         const int t = w.k.at(v, r);
-        if (!wait_on(&c.s_full[st], (tiles >> 1) & 1, dead, wait_ns)) c.soft_dead[st] = 1;
+        if (!wait_on(&c.s_full[st], phase_of(tiles), dead, wait_ns))
+          c.soft_dead[dead_at] = 1;
         __syncwarp();
         tc_fence_after();
         const bool valid = w.k.sees(t) && ((c.groups[st] >> (r >> w.k.log)) & 1u);
-        if (!valid) {  // the half of this row that this thread clears
+        if (!valid) {  // the part of this row that this thread clears
 #pragma unroll 1
-          for (int blk = 2 * hq; blk < 2 * hq + 2; ++blk)
+          for (int blk = 4 / kGroups * hq; blk < 4 / kGroups * (hq + 1); ++blk)
 #pragma unroll
             for (int ch = 0; ch < 8; ++ch)  // (neighbouring rows in different banks)
               *reinterpret_cast<uint4*>(sb + S::kKv + st * kStage + blk * kBlock + r * 128 +
@@ -318,8 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every thread takes the same branch; the flag of a failed wait was
         // written before this barrier
-        const bool full = vote_soft(high);
-        if (c.soft_dead[st]) {
+        const bool full = vote_soft<kSoft>(high);
+        if (c.soft_dead[dead_at]) {
           ok = false;
           break;
         }
@@ -330,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m = across_rows<kW, true>(top, lane);
           if (lane < kW) c.red[qw][hq * kW + lane] = m;
           if (tid == 0) c.raise = 0;
-          sync_soft();
+          sync_soft<kSoft>();
           if (tid < kN) {
             const float rel = fmaxf(fmaxf(c.red[0][tid], c.red[1][tid]),
                                     fmaxf(c.red[2][tid], c.red[3][tid]));
@@ -349,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             c.move[tid] = move;
             c.nm[tid] = c.m[tid] == -INFINITY ? 0.f : -c.m[tid];
           }
-          sync_soft();
+          sync_soft<kSoft>();
           unset = false;
 #pragma unroll
           for (int i = 0; i < kW; ++i) unset |= c.m[hq * kW + i] == -INFINITY;
@@ -384,31 +396,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           add2(l[4 * j + 2], l[4 * j + 3], e[4 * j + 2], e[4 * j + 3]);
         }
         // P's place and O^T: the last tile's product is done with both
-        if (tiles > 0 &&
-            !wait_on(&c.empty[st ^ 1][3], ((tiles - 1) >> 1) & 1, dead, wait_ns))
-          c.soft_dead[st ^ 1] = 1;
+        if (tiles > 0 && !wait_on(&c.empty[stage_of(tiles - 1)][3],
+                                  phase_of(tiles - 1), dead, wait_ns))
+          c.soft_dead[dead_at ^ 1] = 1;
         __syncwarp();
         if (full && c.raise && v > w.ta) {
           tc_fence_after();
 #pragma unroll 1
-          for (int mc = 0; mc < 4 * S::kOParts; ++mc) {
+          for (int i = 0; i < 4 * S::kOParts; ++i) {
             float o[kW];
-            const uint32_t ta = tl + kOCol + (uint32_t)(mc * kN + hq * kW);
+            const uint32_t ta = tl + kOCol + (i / S::kOParts) * S::kOCols +
+                                (uint32_t)(i % S::kOParts * kN + hq * kW);
             tmem_ldw<kW>(ta, o);
 #pragma unroll
-            for (int i = 0; i < kW; ++i) o[i] *= c.alpha[hq * kW + i];
+            for (int j = 0; j < kW; ++j) o[j] *= c.alpha[hq * kW + j];
             tmem_stw<kW>(ta, o);
           }
         }
 #pragma unroll
         for (int q = 0; q < kW / 16; ++q) {  // 16 heads: 16 bytes of each part
-          const int ch = hq * (kW / 16) + q;
-          const int at = kN == 64 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)
-                                  : r * 32 + ((ch ^ ((r >> 2) & 1)) << 4);
 #pragma unroll
-          for (int k = 0; k < 3; ++k)
-            *reinterpret_cast<uint4*>(sb + S::kP + k * S::kPPart + at) = make_uint4(
+          for (int k = 0; k < 3; ++k) {
+            const int buf = kN == 16 ? k >> 1 : k;
+            const int ch = kN == 16 ? k & 1 : hq * (kW / 16) + q;
+            const int at = kN == 64 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)
+                                    : r * 32 + ((ch ^ ((r >> 2) & 1)) << 4);
+            *reinterpret_cast<uint4*>(sb + S::kP + buf * S::kPPart + at) = make_uint4(
                 part[k][4 * q], part[k][4 * q + 1], part[k][4 * q + 2], part[k][4 * q + 3]);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -427,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!some && !whole) continue;
       if (!some) {
-        store_nothing(p, row0, heads, tid);
+        store_nothing<kSoft>(p, row0, heads, tid);
         continue;
       }
       {
@@ -438,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++segs;
       __syncwarp();
       tc_fence_after();
-      sync_soft();
+      sync_soft<kSoft>();
       if (c.soft_dead[tiles & 1]) {
         ok = false;
         break;
@@ -457,12 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.part_ml[slot * kN + tid] = make_float2(m, sum);
         }
       }
-      sync_soft();
+      sync_soft<kSoft>();
       if (whole)
-        store_rows<kN, S::kOParts>(p, c.l, tl + kOCol, row0, heads, qw, hq, lane);
+        store_rows<kN, S::kOParts, S::kOCols>(p, c.l, tl + kOCol, row0, heads, qw, hq, lane);
       else
-        store_part<kN, S::kOParts>(p, 2 * blockIdx.x + (begins ? 1 : 0), tl + kOCol, heads, qw, hq,
-                                   lane);
+        store_part<kN, S::kOParts, S::kOCols>(p, 2 * blockIdx.x + (begins ? 1 : 0), tl + kOCol,
+                                              heads, qw, hq, lane);
       tc_fence_before();  // O^T is read: the next segment's P releases it
     }
     if (!ok) hd = Header{-1, -1, 0, 0};
@@ -508,11 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           row = -1;
         }
         const unsigned boxes = __ballot_sync(0xffffffffu, row >= 0);
-        const int st = tiles & 1;
+        const int st = stage_of(tiles);
 #pragma unroll 1
         for (int blk = team; blk < 4; blk += 2) {
           const bool room = tiles < kStages ||
-                            wait_on(&c.empty[st][blk], ((tiles >> 1) - 1) & 1, dead, wait_ns);
+                            wait_on(&c.empty[st][blk], phase_of(tiles) ^ 1u, dead, wait_ns);
           ok = __all_sync(0xffffffffu, room);
           if (!ok) break;
           if (lane == 0) {
@@ -527,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         issued = 0;
-        // the next tile's rows to L2 (16 heads, 64 single tokens on 8,192 keys: 70.6 us,
-        // without 73.4; no difference where tokens share the rows)
+        // the next tile's rows to L2 (32 heads' columns, 64 single tokens on 8,192 keys: 70.6
+        // us, without 73.4; no difference where tokens share the rows)
         if (team == 0 && row_next >= 0) tma_prefetch_2d(&ahead_map, 0, row_next);
         row = row_next;
       }
@@ -539,12 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int blk = team; blk < 4; blk += 2)
         for (int i = blk < issued ? 0 : 1; i <= kStages; ++i)
           if (tiles - i >= 0)
-            mbar_wait_bounded(&c.full[(tiles - i) & 1][blk], ((tiles - i) >> 1) & 1);
+            mbar_wait_bounded(&c.full[stage_of(tiles - i)][blk], phase_of(tiles - i));
     }
   } else if (warp == kMmaWarp && issue) {
     // ================= MMA =================
     constexpr uint32_t id_s = idesc_f8(kKeys, 2 * kN, false, false, false);
-    constexpr uint32_t id_o = idesc_f8(128, S::kOCols, true, true, true);
+    constexpr uint32_t id_o = idesc_f8(128, S::kON, true, true, true);
     const uint32_t kvb = smem_u32(sb + S::kKv), qb = smem_u32(sb + S::kQ);
     const uint32_t pb = smem_u32(sb + S::kP);
     // (a descriptor's low bits are the address in 16-byte units: steps add constants)
@@ -569,7 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned long long since = 0;  // time of the first idle look
     while (left_o) {
       if (no < ns && ready(&c.p_full, no & 1)) {
-        const uint64_t d_v = d_v0 + (uint32_t)((no & 1) * (kStage >> 4));
+        const int st = stage_of(no);
+        const uint64_t d_v = d_v0 + (uint32_t)(st * (kStage >> 4));
         const uint32_t more = vo > wo.ta ? 1u : 0u;
         tc_fence_after();
 #pragma unroll
@@ -579,9 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 3 / S::kOParts; ++k)
               umma_f8_elect(tmem + kOCol + mc * S::kOCols, d_v + ((mc * kBlock + kr * 4096) >> 4),
-                            d_p + ((k * S::kPPart + kr * 32 * kN) >> 4), id_o,
+                            d_p + ((k * S::kPPart + kr * 32 * S::kPRow) >> 4), id_o,
                             (kr | k) ? 1u : more);
-          umma_commit_elect(&c.empty[no & 1][mc]);
+          umma_commit_elect(&c.empty[st][mc]);
         }
         ++no;
         if (++vo == wo.tb) {
@@ -595,18 +611,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (left_s && ns - no < kStages) {
         have_q = have_q || ready(&c.q_full, seg & 1);
         // (the stage's keys imply that its last outputs are done: its scores are free)
-        if (have_q && ready(&c.full[ns & 1][blk], (ns >> 1) & 1)) {
-          const uint64_t d_k =
-              d_k0 + (uint32_t)((ns & 1) * (kStage >> 4) + blk * (kBlock >> 4));
+        const int st = stage_of(ns);
+        if (have_q && ready(&c.full[st][blk], phase_of(ns))) {
+          const uint64_t d_k = d_k0 + (uint32_t)(st * (kStage >> 4) + blk * (kBlock >> 4));
           const uint64_t d_qb = d_q + (uint32_t)(blk * (2 * S::kQBlock >> 4));
           tc_fence_after();
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            umma_f8_elect(tmem + (ns & 1) * S::kSCols, d_k + (j * 32 >> 4), d_qb + (j * 32 >> 4),
+            umma_f8_elect(tmem + st * S::kSCols, d_k + (j * 32 >> 4), d_qb + (j * 32 >> 4),
                           id_s, (blk | j) ? 1u : 0u);
           if (++blk == 4) {
             blk = 0;
-            umma_commit_elect(&c.s_full[ns & 1]);
+            umma_commit_elect(&c.s_full[st]);
             ++ns;
             if (++vs == w.tb) {
               umma_commit_elect(&c.q_empty);
@@ -698,7 +714,7 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
                     q_rows, q_codes, q_scale) != cudaSuccess)
     return DSA_ERR_CUDA;
   cfg.gridDim = dim3(n_cta, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(cta_threads(kN), 1, 1);
   cfg.dynamicSmemBytes = Smem<kN>::kBytes;
   if (launch_kernel(&cfg, kernel, q_map, kv_map, ahead_map, (const float*)q_scale, p) !=
       cudaSuccess)
@@ -714,13 +730,18 @@ int launch(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
 }  // namespace
 
 size_t mla_chunk_f8_workspace_size(int T, int Hm) {
-  const size_t parts = Hm <= 32 ? part_bytes<32>(num_sms()) : part_bytes<64>(num_sms());
+  const size_t parts = Hm <= 16   ? part_bytes<16>(num_sms())
+                       : Hm <= 32 ? part_bytes<32>(num_sms())
+                                  : part_bytes<64>(num_sms());
   return parts + (size_t)T * Hm * (2 * kL + 4);
 }
 
 int launch_mla_chunk_f8(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
-  // (16 heads, 64 single tokens on 8,192 keys: 71 us; in 64 columns 103)
-  return a.Hm <= 32 ? launch<32>(a, workspace, stream) : launch<64>(a, workspace, stream);
+  // (16 heads, 64 single tokens on 8,192 keys: 65 us, as 32 heads 73, as 64 103; 4 x 128
+  // tokens on 4,096 keys: 195, 223 and 334)
+  return a.Hm <= 16   ? launch<16>(a, workspace, stream)
+         : a.Hm <= 32 ? launch<32>(a, workspace, stream)
+                      : launch<64>(a, workspace, stream);
 }
 
 }  // namespace dsa

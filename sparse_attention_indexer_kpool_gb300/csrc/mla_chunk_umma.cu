@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
         }
         // every thread takes the same branch; the flag of a failed wait was
         // written before this barrier
-        const bool full = vote_soft(high);
+        const bool full = vote_soft<kSoftThreads>(high);
         if (c.soft_dead[tiles & 1]) {
           ok = false;
           break;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
           const float m = across_rows<kW, true>(top, lane);
           if (lane < kW) c.red[qw][hq * kW + lane] = m;
           if (tid == 0) c.raise = 0;
-          sync_soft();
+          sync_soft<kSoftThreads>();
           if (tid < kN) {
             const float rel = fmaxf(fmaxf(c.red[0][tid], c.red[1][tid]),
                                     fmaxf(c.red[2][tid], c.red[3][tid]));
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
             c.move[tid] = move;
             c.nm[tid] = c.m[tid] == -INFINITY ? 0.f : -c.m[tid];
           }
-          sync_soft();
+          sync_soft<kSoftThreads>();
           unset = false;
 #pragma unroll
           for (int i = 0; i < kW; ++i) unset |= c.m[hq * kW + i] == -INFINITY;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       const int heads = min(kN, p.Hm - w.h0 * kN);
       const long long row0 = (long long)w.token * p.Hm + w.h0 * kN;
       if (!some) {  // a token that sees nothing
-        store_nothing(p, row0, heads, tid);
+        store_nothing<kSoftThreads>(p, row0, heads, tid);
         continue;
       }
       {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       if (!wait_on(&c.o_full, segs & 1, dead, wait_ns)) c.soft_dead[tiles & 1] = 1;
       ++segs;
       tc_fence_after();
-      sync_soft();
+      sync_soft<kSoftThreads>();
       if (c.soft_dead[tiles & 1]) {
         ok = false;
         break;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
           p.part_ml[slot * kN + tid] = make_float2(m, sum);
         }
       }
-      sync_soft();
+      sync_soft<kSoftThreads>();
       if (whole)
         store_rows<kN>(p, c.l, tl + kN, row0, heads, qw, hq, lane);
       else
