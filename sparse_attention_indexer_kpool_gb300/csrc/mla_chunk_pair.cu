@@ -69,6 +69,7 @@ struct Ctl {
   uint64_t free_s, free_p[2];      // the other CTA has read what was sent
   uint64_t turn[2];                // the references of this tile stand
   uint64_t sums, epi;              // the sums of a segment's rows
+  uint64_t o_free;                 // a segment's outputs are read
   Start start;
   uint32_t tmem;
   unsigned groups[kStages];        // boxes of the tile that have a page
@@ -219,6 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&c.free_s, kTeamWarps);
     mbar_init(&c.sums, 2 * kTeamWarps);
     mbar_init(&c.epi, 3 * kTeamWarps);
+    mbar_init(&c.o_free, 3 * kTeamWarps);
     fence_mbar_init();
     c.team_dead[0][0] = c.team_dead[0][1] = c.team_dead[1][0] = c.team_dead[1][1] = c.dead = 0;
   }
@@ -587,9 +589,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // O and c.inv are read: this warp's next P, which every next write of
-        // them waits for, says so
+        // O is read.  (This warp's next P does not say so in time: the next segment's
+        // first tile is one team's, and the other team may still be reading.)
         tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&c.o_free);
       }
       if (!ok) hd = Header{-1, -1, 0, 0};
       if (own && first && team == 0 && lane == 0 && rank == 0) p.head[me] = hd;
@@ -677,11 +681,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto ready = [](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0;
       };
-      bool ok = true, left_s = segment(w), left_o = segment(wo), have_q = false;
-      int ns = 0, no = 0, vs = w.ta, vo = wo.ta, seg = 0;
+      // have_o: every warp has read the last segment's outputs
+      bool ok = true, left_s = segment(w), left_o = segment(wo), have_q = false, have_o = true;
+      int ns = 0, no = 0, vs = w.ta, vo = wo.ta, seg = 0, ends = 0;
       unsigned long long since = 0;  // time of the first idle look
       while (left_o) {
-        if (no < ns && ready(&c.p_full[no % kStages], (no / kStages) & 1)) {
+        if (!have_o) have_o = ready(&c.o_free, (ends - 1) & 1);
+        if (have_o && no < ns && ready(&c.p_full[no % kStages], (no / kStages) & 1)) {
           const int st = no % kStages;
           const uint64_t d_v = d_v0 + (uint32_t)(st * (kStageBytes >> 4));
           const uint32_t a0 = tmem + 256 + st * kKT;
@@ -696,6 +702,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             umma_commit_elect(&c.o_full);
             left_o = segment(wo);
             vo = wo.ta;
+            ++ends;
+            have_o = false;
           }
           since = 0;
           continue;

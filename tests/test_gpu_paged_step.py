@@ -397,6 +397,20 @@ def test_chunk_rising_and_falling_logits(act, kv, L):
         check(s, 300, 7)
 
 
+@pytest.mark.parametrize("Hm", [64, 40, 100])
+def test_chunk_wide_tables_short_rows_one_after_the_other(Hm):
+    """Hundreds of row tiles of two to four key tiles: the first outputs of one may not reach
+    the accumulators before every warp has read those of the one before."""
+    rng = random.Random(Hm)
+    lens = [rng.choice((80, 100, 128, 200, 256)) for _ in range(500)]
+    new = [rng.choice((1, 2, 2, 2, 3)) for _ in lens]
+    s = make(lens, new, Hm=Hm, ps=16, seed=28, width=WIDE, pad=0, q_std=2.0)
+    want = check(s)
+    for _ in range(20):
+        out, lse, st = attend(s)
+        assert st == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 @pytest.mark.parametrize("n,m,window", [(400, 6, 50), (2500, 320, 2060)])
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 16, 512), (F32, F32, 4, 64)])
 def test_chunk_later_tokens_do_not_reach_earlier_ones(act, kv, Hm, L, n, m, window):
