@@ -542,9 +542,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
+        float inv = 0.f;
         if (whole) {
           fine = fine && wait_on(&c.in_l, sums & 1, dead, wait_ns);
           ++sums;
+          // read before `epi`: the other CTA's next sums may follow one tile of the next
+          // segment, whose weights come from warps that have passed it
+          if (!own) inv = c.inv[64 * g + r];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive1(&c.epi);
@@ -559,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&c.in_l, 64 * 4);
         // a thread holds latent columns 256 rank + o0 .. of its row
         if (whole) {
-          const float inv = c.inv[64 * g + r];
+          if (own) inv = c.inv[64 * g + r];  // (part 0's, before `epi`)
           __nv_bfloat16* dst = p.out + row * kL + 256 * rank + o0;
 #pragma unroll 1
           for (int cc = 0; cc < o_n; ++cc) {

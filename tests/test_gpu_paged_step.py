@@ -411,6 +411,19 @@ def test_chunk_wide_tables_short_rows_one_after_the_other(Hm):
         assert st == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("Hm", [64, 40, 100])
+def test_chunk_wide_tables_rows_of_one_tile(Hm):
+    """Hundreds of row tiles of a single key tile, whose sums differ widely: no row may be
+    normalised by the next one's."""
+    rng = random.Random(Hm)
+    lens = [rng.randint(2, 64) for _ in range(900)]
+    s = make(lens, [2] * 900, Hm=Hm, ps=16, seed=29, width=WIDE, pad=0, q_std=4.0)
+    want = check(s)
+    for _ in range(20):
+        out, lse, st = attend(s)
+        assert st == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 @pytest.mark.parametrize("n,m,window", [(400, 6, 50), (2500, 320, 2060)])
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 16, 512), (F32, F32, 4, 64)])
 def test_chunk_later_tokens_do_not_reach_earlier_ones(act, kv, Hm, L, n, m, window):
