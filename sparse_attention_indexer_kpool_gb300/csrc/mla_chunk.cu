@@ -133,10 +133,11 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
     s_m[tid] = -INFINITY;
     s_l[tid] = 0.f;
   }
-  // thread j: the cache row of the tile's position j (-1: no page)
-  auto find_row = [&](int v, int* dst) {
-    if (tid >= kt || v + tid >= nv) return;
-    const int p = v + tid < s0 ? v + tid : lo + (v + tid - s0);
+  // thread j: the cache row of the tile's position j (-1: no page); v may pass an int in
+  // the last tile
+  auto find_row = [&](unsigned v, int* dst) {
+    if (tid >= kt || v + tid >= (unsigned)nv) return;
+    const int i = (int)(v + tid), p = i < s0 ? i : lo + (i - s0);
     const int page = a.kv.block_table[(long long)b * a.kv.max_pages + p / a.kv.page_size];
     const bool ok = page >= 0 && page < a.kv.n_pages;
     if (!ok && reports) flag(a.status, DSA_DEV_BAD_PAGE);
@@ -150,8 +151,9 @@ __global__ void __launch_bounds__(kChunkThreads) mla_chunk_simt_kernel(ChunkArgs
     for (int c = 0; c < kChunkCols; ++c) acc[h][c] = 0.f;
 
   const int pieces = L / 8;
-  for (int v0 = 0, par = 0; v0 < nv; v0 += kt, par ^= 1) {
-    const int n = min(kt, nv - v0), total = n * pieces;
+  int par = 0;
+  for (unsigned v0 = 0; v0 < (unsigned)nv; v0 += kt, par ^= 1) {
+    const int n = min(kt, nv - (int)v0), total = n * pieces;
     __syncthreads();
     for (int i0 = tid; i0 < total; i0 += 4 * kChunkThreads) {
       Piece<kKv> x[4];  // four loads on their way at once

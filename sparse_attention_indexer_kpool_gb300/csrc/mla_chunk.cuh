@@ -88,11 +88,13 @@ __device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p
 template <int kT>
 struct Keys {
   int pos, lo, s0, log, sink_boxes, first, boxes, n;
-  // position of row r of key tile v (past the last box: past pos)
+  // position of row r of key tile v (past the last box: past pos); boxes of one position
+  // may number 2^31 - 1, so that the last tile's count passes an int
   __device__ __forceinline__ int at(int v, int r) const {
-    const int g = v * (kT >> log) + (r >> log);
-    const int box = g < sink_boxes ? g : first + (g - sink_boxes);
-    return g < boxes ? (box << log) + (r & ((1 << log) - 1)) : 0x7fffffff;
+    const unsigned g = (unsigned)v * (unsigned)(kT >> log) + (unsigned)(r >> log);
+    if (g >= (unsigned)boxes) return 0x7fffffff;
+    const int box = (int)g < sink_boxes ? (int)g : first + ((int)g - sink_boxes);
+    return (box << log) + (r & ((1 << log) - 1));
   }
   __device__ __forceinline__ bool sees(int t) const { return t <= pos && (t >= lo || t < s0); }
 };
@@ -107,8 +109,8 @@ __device__ __forceinline__ Keys<kT> keys_of(int pos0, int pos, const Params& p) 
   k.first = k.lo >> k.log;
   k.sink_boxes = min((k.s0 >> k.log) + ((k.s0 & ((1 << k.log) - 1)) != 0), k.first);
   k.boxes = pos < 0 ? 0 : k.sink_boxes + max((k.pos >> k.log) - k.first + 1, 0);
-  const int per = kT >> k.log;
-  k.n = (k.boxes + per - 1) / per;
+  const unsigned per = kT >> k.log;
+  k.n = (int)(((unsigned)k.boxes + per - 1) / per);
   return k;
 }
 

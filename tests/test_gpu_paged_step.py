@@ -563,6 +563,33 @@ def test_chunk_lengths_past_the_table_cost_no_more_than_it(act, kv, Hm, L, cols)
         ref.check_attend(out[1:], lse[1:], reference(rest, window, sinks), act, L)
 
 
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_chunk_of_2_to_the_31_positions(kv):
+    """The longest sequence that the lengths can say, on pages of an odd size: 2^24 tiles whose
+    last one's rows count past an int.  One page serves all blocks, its rows are alike, so the
+    output is a row.  A CTA adds up 2^24 / SMs tiles of eight products in fp32, each sum off by
+    at most 2^-23 of itself: 2^4 / SMs of the output in all, a sixteenth of that (one addition
+    a tile, 2^-24) of the sum, half as much again for the roundings of weights and result."""
+    ps, n = 1001, 2 ** 31 - 1
+    g = torch.Generator(device=DEV).manual_seed(30)
+    row = torch.randn((1, 512), generator=g, device=DEV)
+    pages, scale = ref.quantise(row) if kv == F8 else (row.to(kv), None)
+    pages = pages.view(torch.uint8).repeat(ps, 1).view(kv)
+    scale = None if scale is None else scale.repeat(ps)
+    table = torch.zeros((1, -(-n // ps)), dtype=torch.int32, device=DEV)
+    q = torch.randn((1, 16, 512), generator=g, device=DEV).to(BF)
+    s = dict(q=q, pages=pages, scale=scale, table=table, lens=i32([n]), cu=i32([0, 1]), ps=ps,
+             sm=1.0 / math.sqrt(512), T=1)
+    out, lse, st = attend(s)
+    assert st == 0
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rel = 16.0 / sms * (1 + 1 / 16 + 0.5)
+    want = ref.values(pages, scale)[0]
+    assert bool(((out.double() - want).abs() <= rel * want.abs()).all())
+    z = (q[0].double() @ want) * s["sm"]
+    assert bool((lse[0].double() - z - math.log(n)).abs().max() <= 1.0 / sms + 1e-3)
+
+
 @pytest.mark.parametrize("kv,Hm,width,ps", [(BF, 64, 0, 64), (BF, 64, WIDE, 64), (BF, 16, 0, 5),
                                             (F8, 64, 0, 64), (F8, 16, 0, 5)])
 def test_chunk_gives_up_and_recovers(kv, Hm, width, ps):
