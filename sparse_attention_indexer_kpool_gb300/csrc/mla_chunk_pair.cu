@@ -22,9 +22,11 @@
 // 3.94 ms, 1,045 TFLOP/s (0.56 of the measured bf16 rate; the single-CTA kernel: 4.53 ms).
 //
 // The two tokens of a pair see the same keys but for the last one and the first of a
-// window.  A key that neither sees is zeroed in shared memory before PV; one that only
-// one of them sees is zeroed if it holds a NaN or an infinity (its logit is then one,
-// too, which makes the seeing token's sums NaN), so that nothing masked reaches a row.
+// window.  A key that neither sees is zeroed in shared memory before PV, and so is one that
+// only one of them sees if it holds a NaN or an infinity: nothing masked reaches a row.
+// The seeing token's logit is then NaN or infinite, too, and its sums NaN, unless the
+// logit is minus infinity: a weight of 0 times the infinity is NaN in that latent column
+// alone, so these columns are noted and stored as NaN.
 //
 // Every wait is bounded; both CTAs meet at a cluster barrier before either ends.
 #include "mla_chunk.cuh"
@@ -73,6 +75,9 @@ struct Ctl {
   Start start;
   uint32_t tmem;
   unsigned groups[kStages];        // boxes of the tile that have a page
+  // by segment (its parity) and row block: latent columns in which a zeroed key that only
+  // this block sees is not finite
+  uint32_t odd[2][2][8];
   int team_dead[2][2];
   int dead;
 };
@@ -229,6 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   if (tid < 64) c.m[tid] = -INFINITY;
+  if (tid < 32) c.odd[tid >> 4][(tid >> 3) & 1][tid & 7] = 0u;
   pdl_wait();  // every input may come from the kernel just before
   pdl_launch_dependents();
   const unsigned long long units = find_share<kKT, true, kThreads>(
@@ -361,12 +367,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                     (key & 7) * 128;
                 bool odd = !(ina || inb);
                 if (!odd) {
+                  uint32_t* cols = c.odd[segs & 1][inb ? 1 : 0];  // (one such key a block)
                   for (int i = 0; i < 32; ++i) {
                     const uint4 x = *reinterpret_cast<const uint4*>(
                         kr + (i >> 3) * 1024 + (((i & 7) ^ (key & 7)) << 4));
                     const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
-                    for (int j = 0; j < 4; ++j)
-                      odd |= (wd[j] & 0x7f80u) == 0x7f80u || (wd[j] & 0x7f800000u) == 0x7f800000u;
+                    uint32_t bits = 0u;
+                    for (int j = 0; j < 4; ++j) {
+                      if ((wd[j] & 0x7f80u) == 0x7f80u) bits |= 1u << (2 * j);
+                      if ((wd[j] & 0x7f800000u) == 0x7f800000u) bits |= 2u << (2 * j);
+                    }
+                    if (bits) {
+                      cols[i >> 2] |= bits << ((i & 3) * 8);
+                      odd = true;
+                    }
                   }
                 }
                 if (odd)
@@ -531,6 +545,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (part == 0) {
             const float sum = (c.mx[0][0][r] + c.mx[0][1][r]) + (c.mx[1][0][r] + c.mx[1][1][r]);
             c.m[r] = -INFINITY;  // (every thread of the row has read it)
+            // the next segment's columns (every warp has stored the one before's)
+            if (r < 16) c.odd[(segs & 1) ^ 1][(r >> 3) & 1][r & 7] = 0u;
             if (whole) {
               const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
               c.inv[64 * rank + r] = inv;
@@ -562,13 +578,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (whole && own && first && team == 0 && lane == 0)
           mbar_arrive_expect_tx(&c.in_l, 64 * 4);
         // a thread holds latent columns 256 rank + o0 .. of its row
+        const uint32_t* cols = c.odd[(segs - 1) & 1][g] + (o0 >> 5);
+        auto load_o32 = [&](int cc, float (&o)[32]) {
+          tmem_ld32(tl + o0 + cc * 32, o);
+          const uint32_t bits = cols[cc];
+          if (bits) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((bits >> i) & 1u) o[i] = NAN;
+          }
+        };
         if (whole) {
           if (own) inv = c.inv[64 * g + r];  // (part 0's, before `epi`)
           __nv_bfloat16* dst = p.out + row * kL + 256 * rank + o0;
 #pragma unroll 1
           for (int cc = 0; cc < o_n; ++cc) {
             float o[32];
-            tmem_ld32(tl + o0 + cc * 32, o);
+            load_o32(cc, o);
             if (live) {
 #pragma unroll
               for (int q = 0; q < 4; ++q)
@@ -584,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int cc = 0; cc < o_n; ++cc) {
             float o[32];
-            tmem_ld32(tl + o0 + cc * 32, o);
+            load_o32(cc, o);
             if (live) {
 #pragma unroll
               for (int q = 0; q < 8; ++q)

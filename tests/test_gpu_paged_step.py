@@ -447,6 +447,47 @@ def test_chunk_later_tokens_do_not_reach_earlier_ones(act, kv, Hm, L, n, m, wind
             assert torch.isnan(out[k:m].float()).all()
 
 
+@pytest.mark.parametrize("window,m", [(0, 6), (2100, 6), (2100, 320)])
+@pytest.mark.parametrize("act,Hm,L,width", [(BF, 64, 512, 0), (BF, 64, 512, WIDE),
+                                            (BF, 40, 512, WIDE), (F32, 4, 64, 0)])
+def test_chunk_infinite_keys(act, Hm, L, width, window, m):
+    """Infinities in the last token's key, and in the one that leaves the window with it.  Where a
+    query makes its logit minus infinity its weight is 0, and 0 times infinity NaN: in those
+    latent columns alone.  Other queries' logits are infinite or NaN, and their outputs NaN.  A
+    token that does not see the key keeps every bit."""
+    n, ps = 2500, 16
+    s = make([n], [m], Hm=Hm, L=L, act=act, kv=act, ps=ps, seed=31, width=width, pad=0)
+    d = [7, L - 20]                                     # (one in each half of the columns)
+    h = torch.arange(Hm, device=DEV)
+    s["q"][:, :, d[0]] = (s["q"][:, :, d[0]].abs() + 0.5) * torch.where(h % 4 == 1, 1, -1)[:, None].T
+    s["q"][:, :, d[1]] = (s["q"][:, :, d[1]].abs() + 0.5) * torch.where(h % 4 == 2, -1, 1)[:, None].T
+    want, want_lse, _ = attend(s, window, 3)
+    p = torch.arange(n, device=DEV)
+    rows = s["table"][0].long()[p // ps] * ps + p % ps
+    keys = [n - 1] + ([n - 1 - window] if window else [])
+    for k in keys:
+        s["pages"][rows[k], d[0]] = math.inf
+        s["pages"][rows[k], d[1]] = -math.inf
+    out, lse, st = attend(s, window, 3)
+    assert st == 0
+    low = (h % 4 == 0) | (h % 4 == 3)                   # minus infinity in both columns
+    for i in range(m):
+        at = n - m + i
+        see = (p <= at) & ((p > at - window) | (p < 3) if window else True)
+        if not any(bool(see[k]) for k in keys):
+            assert torch.equal(out[i], want[i]) and torch.equal(lse[i], want_lse[i])
+            continue
+        assert torch.isnan(out[i][~low].float()).all()
+        see[keys] = False
+        one = rows[see].to(torch.int32)[None]
+        exp = ref.attend(s["q"][i:i + 1, low], ref.values(s["pages"], None), one,
+                         i32([one.shape[1]]), 1, i32([0, 1]), 0, 0, s["sm"])
+        got = out[i:i + 1, low]
+        assert torch.isnan(got[:, :, d].float()).all(), (i, "columns")
+        got[:, :, d] = exp[0][:, :, d].to(act)
+        ref.check_attend(got, lse[i:i + 1, low], exp, act, L)
+
+
 @pytest.mark.parametrize("width", [0, WIDE])
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 64, 512), (F32, F32, 4, 64)])
 def test_chunk_faults_are_flagged_and_contained(act, kv, Hm, L, width):
