@@ -708,16 +708,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (x.tb > x.ta) return true;
         return false;
       };
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_on(bar, parity, dead, wait_ns)) != 0;
+      };
       auto ready = [](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0;
       };
-      // have_o: every warp has read the last segment's outputs
-      bool ok = true, left_s = segment(w), left_o = segment(wo), have_q = false, have_o = true;
+      bool ok = true, left_s = segment(w), left_o = segment(wo), have_q = false;
       int ns = 0, no = 0, vs = w.ta, vo = wo.ta, seg = 0, ends = 0;
       unsigned long long since = 0;  // time of the first idle look
       while (left_o) {
-        if (!have_o) have_o = ready(&c.o_free, (ends - 1) & 1);
-        if (have_o && no < ns && ready(&c.p_full[no % kStages], (no / kStages) & 1)) {
+        if (no < ns && ready(&c.p_full[no % kStages], (no / kStages) & 1)) {
           const int st = no % kStages;
           const uint64_t d_v = d_v0 + (uint32_t)(st * (kStageBytes >> 4));
           const uint32_t a0 = tmem + 256 + st * kKT;
@@ -732,8 +733,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             umma_commit_elect(&c.o_full);
             left_o = segment(wo);
             vo = wo.ta;
+            // (every warp reads the segment's outputs before the next one's first product)
+            if (left_o && !wait_all(&c.o_free, ends & 1)) {
+              ok = false;
+              break;
+            }
             ++ends;
-            have_o = false;
           }
           since = 0;
           continue;
