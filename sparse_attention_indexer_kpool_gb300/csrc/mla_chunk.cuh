@@ -467,6 +467,15 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
   }
 }
 
+// log of the sum of 2^z, from its reference and the sum relative to it: the sum's exponent is
+// added to the reference first, so that a large one against a low reference costs no digits.
+__device__ __forceinline__ float lse_of(float m, float sum) {
+  if (sum == 0.f) return -INFINITY;
+  int ex;
+  const float f = frexpf(sum, &ex);
+  return (m + (float)ex + log2f(f)) / kLog2e;
+}
+
 // Join the partials of the row tiles that were split over workers, in their order.  A
 // tile's workers are neighbours: every block reads all headers and lists the workers that
 // began a tile.  A piece of the work is half of a row (two 16-byte pieces a lane); the
@@ -608,7 +617,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
             make_uint2(pack_bf16(j.acc[q].x * inv, j.acc[q].y * inv),
                        pack_bf16(j.acc[q].z * inv, j.acc[q].w * inv));
       if (p.lse && lane == 0 && c0 == 0)
-        p.lse[row] = j.den == 0.f ? -INFINITY : (j.mx + log2f(j.den)) / kLog2e;
+        p.lse[row] = lse_of(j.mx, j.den);
       continue;
     }
     if (lane == 0) {
@@ -635,7 +644,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       const float inv = den == 0.f ? 0.f : p.o_scale / den;
       *reinterpret_cast<uint32_t*>(p.out + row * kL + c0 + tid * 2) = pack_bf16(a * inv, b * inv);
       if (p.lse && tid == 0 && c0 == 0)
-        p.lse[row] = den == 0.f ? -INFINITY : (mx + log2f(den)) / kLog2e;
+        p.lse[row] = lse_of(mx, den);
     }
     __syncthreads();
   }

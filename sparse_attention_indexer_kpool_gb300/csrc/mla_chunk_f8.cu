@@ -18,7 +18,8 @@
 //     all.  The sums keep the unrounded fp32 weights.
 // The reference m of a head is kept for u rather than for the bare weight, so that u
 // stays below 2^7 and its parts inside E5M2's range; a row scale counts there as at
-// least 2^-60, which bounds the bare weight as well.
+// least 2^-60, which bounds the bare weight as well.  A row whose codes are all zero adds to
+// the sums alone: its scale, whatever it is, does not set the reference.
 //
 // Why.  Widening the codes to bf16 in shared memory took 1,960 cycles of conversions
 // and 2,000 of shared-memory traffic a tile and kept one tile at a time in the 128 KB
@@ -259,6 +260,24 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
       if (page < 0 || page >= p.kv.n_pages) return 0.f;
       return __ldg(p.kv.row_scale + (long long)page * p.kv.page_size + t % p.kv.page_size);
     };
+    // Whether this thread's row has no code but zeros: looked for only where its scores
+    // are (e: minus the references) zero or, by the queries, NaN.
+    auto adds_nothing = [&](const float (&e)[kW], float sc, int st, int tile) -> bool {
+      bool zero = fabsf(sc) < INFINITY;
+#pragma unroll
+      for (int i = 0; i < kW; ++i) {
+        const float nm = c.nm[hq * kW + i];
+        zero = zero && !(e[i] < nm || e[i] > nm);
+      }
+#pragma unroll 1
+      for (int i = 0; zero && i < 32; ++i) {
+        if ((i & 7) == 0 && !wait_on(&c.full[st][i >> 3], phase_of(tile), dead, wait_ns)) break;
+        const uint4 x = *reinterpret_cast<const uint4*>(
+            sb + S::kKv + st * kStage + (i >> 3) * kBlock + r * 128 + (((i & 7) ^ (r & 7)) << 4));
+        zero = ((x.x | x.y | x.z | x.w) & 0x7f7f7f7fu) == 0u;
+      }
+      return zero;
+    };
     while (ok && w.next()) {
       float l[kW];                // this row's sums
       bool unset = true;          // some head here has no reference yet
@@ -289,7 +308,8 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
         }
         // (a hidden key's scale may be anything)
         const float sc = valid ? rs : 0.f, zs = p.zscale * sc;
-        const float lg = fmaxf(log2f(fabsf(sc)), kLeastLog);  // in u's reference
+        float lg = fmaxf(log2f(fabsf(sc)), kLeastLog);  // in u's reference
+        float up = sc * kUp;
         const float high_at = kRaise8 - lg;
         float e[kW];
         // z = S * query scale * row scale * softmax scale, S of both parts
@@ -336,6 +356,11 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
           break;
         }
         if (full) {
+          if (adds_nothing(e, sc, st, tiles)) {
+            lg = kLeastLog;
+            up = 0.f;
+          }
+          __syncwarp();
           float top[kW];  // of u, relative to the references so far
 #pragma unroll
           for (int i = 0; i < kW; ++i) top[i] = e[i] + lg;
@@ -374,7 +399,6 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
           for (int i = 0; i < kW; ++i) l[i] *= c.alpha[hq * kW + i];
         }
         // the weights and their parts (in registers: the last tile's may still be read)
-        const float up = sc * kUp;
         uint32_t part[3][kW / 4];
 #pragma unroll
         for (int j = 0; j < kW / 4; ++j) {
@@ -465,8 +489,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
         c.nm[tid] = 0.f;
         if (whole) {
           c.l[tid] = sum == 0.f ? 0.f : 1.f / (sum * kUp);  // a NaN sum stays one
-          if (p.lse && tid < heads)
-            p.lse[row0 + tid] = sum == 0.f ? -INFINITY : (m + log2f(sum)) / kLog2e;
+          if (p.lse && tid < heads) p.lse[row0 + tid] = lse_of(m, sum);
         } else {
           const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
           p.part_ml[slot * kN + tid] = make_float2(m, sum);

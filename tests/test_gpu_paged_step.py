@@ -585,6 +585,73 @@ def test_chunk_e4m3_queries_with_a_large_element(Hm, ps):
                          dz_more=more, out_more=ref.underflow(s["pages"], s["scale"], BF))
 
 
+def e4m3_step(rows, scales=None, Hm=64, ps=64, n_new=3, seed=32, q=None):
+    """One sequence whose cache holds the given rows (E4M3 codes made from them; ``scales``: of
+    the codes of rows with a largest magnitude of 448) and its last tokens' queries."""
+    n = rows.shape[0]
+    s = make([n], [n_new], Hm=Hm, kv=F8, ps=ps, seed=seed, pad=0, hidden=0.0)
+    codes, sc = ref.quantise(rows)
+    p = torch.arange(n, device=DEV)
+    at = s["table"][0].long()[p // ps] * ps + p % ps
+    s["pages"].view(torch.uint8)[at] = codes.view(torch.uint8)
+    s["scale"].fill_(1.0)
+    s["scale"][at] = sc if scales is None else scales
+    if q is not None:
+        s["q"] = q.to(BF).contiguous()
+    return s, at
+
+
+def check_e4m3(s, at, zero=()):
+    """Against 64 bits; what E5M2 weights lose is relative to the largest weight times row scale
+    of the rows seen that are not zero."""
+    out, lse, st = attend(s)
+    assert st == 0
+    keep = torch.ones(at.shape[0], dtype=torch.bool, device=DEV)
+    keep[list(zero)] = False
+    more = 0.0
+    if s["ps"] % 8 == 0:
+        # a product u = weight * scale at the reference or above is 2^8 and more in E5M2; the
+        # output is the sum of u * code over the sum of the weights, so it is off by at most 3 *
+        # 2^-25 sum|code| max(u) / sum of the weights, max(u) over rows that are not zero
+        vals = ref.values(s["pages"], s["scale"])[at]
+        z = torch.einsum("thl,nl->thn", s["q"].double(), vals) * s["sm"]
+        n, m = at.shape[0], s["T"]
+        see = torch.arange(n, device=DEV)[None] <= n - m + torch.arange(m, device=DEV)[:, None]
+        w = torch.softmax(z.masked_fill(~see[:, None], -math.inf), -1)
+        u = (w * s["scale"][at].double())[:, :, keep].amax(-1)
+        codes = s["pages"][at].float().abs().double().sum(0)
+        more = 3 * 2.0 ** -25 * codes * u[..., None]
+    ref.check_attend(out, lse, reference(s), BF, 512, out_more=more)
+    return out
+
+
+@pytest.mark.parametrize("Hm,ps", [(64, 64), (16, 64), (32, 64), (64, 5)])
+@pytest.mark.parametrize("size,toward", [(0.01, 0.0), (1e-2, -9.0), (1e-3, -4.0), (1e-5, 0.0),
+                                         (1e-5, 3.0)])
+def test_chunk_e4m3_zero_rows(Hm, ps, size, toward):
+    """All-zero rows (stored with a scale of 1) among small ones: their weights count, their
+    scale does not.  ``toward``: the small rows' logits against the zero rows', base e."""
+    g = torch.Generator(device=DEV).manual_seed(33)
+    n, zero = 700, [0, 5, 130, 131, 500, 698]
+    rows = torch.randn((n, 512), generator=g, device=DEV) * size
+    rows[:, 3] = 2.0 * size
+    rows[zero] = 0.0
+    q = torch.randn((3, Hm, 512), generator=g, device=DEV) * 0.1
+    q[:, :, 3] = toward * math.sqrt(512.0) / (2.0 * size)
+    s, at = e4m3_step(rows, Hm=Hm, ps=ps, q=q)
+    assert bool((s["scale"][at[zero]] == 1.0).all())
+    check_e4m3(s, at, zero)
+
+
+@pytest.mark.parametrize("n", [1, 3, 200, 9000])
+def test_chunk_e4m3_nothing_but_zero_rows(n):
+    """Every logit is 0: out 0 and lse log n, the sum of n ones being exact."""
+    s, _ = e4m3_step(torch.zeros((n, 512), device=DEV), n_new=1)
+    out, lse, st = attend(s)
+    assert st == 0 and bool((out == 0).all())
+    assert bool(((lse.double() - math.log(n)).abs() <= 2.0 ** -21 + 2.0 ** -22 * math.log(n)).all())
+
+
 @pytest.mark.parametrize("act,kv,Hm,L", [(BF, BF, 64, 512), (BF, F8, 16, 512), (F32, F32, 4, 64)])
 @pytest.mark.parametrize("cols", [3, WIDE // 16])
 def test_chunk_lengths_past_the_table_cost_no_more_than_it(act, kv, Hm, L, cols):
