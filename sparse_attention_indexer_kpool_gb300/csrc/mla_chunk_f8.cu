@@ -157,11 +157,12 @@ __global__ void __launch_bounds__(256)
   for (int i = 0; i < 16; ++i)
     if (fabsf(x[i]) < INFINITY) top = fmaxf(top, fabsf(x[i]));
   top = warp_max(top);
-  // exponent of the largest magnitude: 2^ex <= top < 2^(ex + 1); a row below 2^-100
-  // counts as such
-  const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-  const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);    // 2^(7 - ex)
-  const float down = __uint_as_float((uint32_t)(127 + ex - 7) << 23);  // 2^(ex - 7)
+  // exponent of the largest magnitude: 2^ex <= top < 2^(ex + 1) (below the normal numbers:
+  // theirs, at which the elements are still multiples of 1); 2^(7 - ex) in two factors
+  const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -126), half = (7 - ex) >> 1;
+  auto pow2 = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
+  const float up0 = pow2(half), up1 = pow2(7 - ex - half);
+  const float down = pow2(-half) * pow2(half + ex - 7);  // 2^(ex - 7)
   uint32_t hi[4], lo[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       // a NaN or an infinity becomes the NaN code: its head's logits are NaN
-      float a = x[4 * j + 2 * k] * up, b = x[4 * j + 2 * k + 1] * up;
+      float a = x[4 * j + 2 * k] * up0 * up1, b = x[4 * j + 2 * k + 1] * up0 * up1;
       a = fabsf(a) < INFINITY ? a : NAN;
       b = fabsf(b) < INFINITY ? b : NAN;
       const uint32_t h2 = e4m3x2(a, b) & 0xffffu;

@@ -601,11 +601,15 @@ def e4m3_step(rows, scales=None, Hm=64, ps=64, n_new=3, seed=32, q=None):
     return s, at
 
 
-def check_e4m3(s, at, zero=()):
+def check_e4m3(s, at, zero=(), shift=0):
     """Against 64 bits; what E5M2 weights lose is relative to the largest weight times row scale
-    of the rows seen that are not zero."""
+    of the rows seen that are not zero.  The comparison is made 2^shift higher, by rows times
+    that and queries divided by it (which leaves the logits)."""
     out, lse, st = attend(s)
     assert st == 0
+    out = out.double() * 2.0 ** shift
+    assert torch.isfinite(out).all()
+    s = dict(s, q=s["q"].double() * 2.0 ** -shift, scale=s["scale"].double() * 2.0 ** shift)
     keep = torch.ones(at.shape[0], dtype=torch.bool, device=DEV)
     keep[list(zero)] = False
     more = 0.0
@@ -641,6 +645,19 @@ def test_chunk_e4m3_zero_rows(Hm, ps, size, toward):
     s, at = e4m3_step(rows, Hm=Hm, ps=ps, q=q)
     assert bool((s["scale"][at[zero]] == 1.0).all())
     check_e4m3(s, at, zero)
+
+
+@pytest.mark.parametrize("Hm,ps", [(64, 64), (16, 64), (32, 64), (64, 5)])
+@pytest.mark.parametrize("size", [-90, -104, -118, -125, -130])
+def test_chunk_e4m3_small_queries(Hm, ps, size):
+    """Queries of 2^size (2^-130: multiples of the least bf16 value), a softmax scale and row
+    scales that make their logits ordinary."""
+    g = torch.Generator(device=DEV).manual_seed(35)
+    rows = torch.randn((300, 512), generator=g, device=DEV)
+    q = torch.randn((3, Hm, 512), generator=g, device=DEV) * 2.0 ** size
+    s, at = e4m3_step(rows, torch.full((300,), 2.0 ** 110, device=DEV), Hm=Hm, ps=ps, q=q)
+    s["sm"] *= 2.0 ** (-118 - size)
+    check_e4m3(s, at, shift=-110)
 
 
 @pytest.mark.parametrize("n", [1, 3, 200, 9000])
