@@ -380,8 +380,11 @@ int dsa_paged_append(const void* kv_new, const int32_t* kv_rows, int T, int L, i
  *   initial value; calls in flight at the same time must not share one
  * The lengths are read on the GPU: a captured call follows them when replayed.
  * Outputs are deterministic.  E4M3 pages (bf16 activations, L = 512, page_size a
- * multiple of 8): a query element is kept to 2^-21 of its row's largest, and a weight
- * below 2^-24 of the largest may be lost.
+ * multiple of 8): a query element is kept to 2^-21 of its row's largest.  A weight is
+ * kept to 2^-9 of itself and counts with its row's scale: where weight * row_scale is
+ * below 2^-24 of the largest such product of a row that is not all zero, it may be
+ * lost to out (not to lse).  The scales of the rows that a token sees, all-zero rows
+ * aside, may lie 2^60 apart; out is unspecified for scales further apart than that.
  * Supported: L multiple of 8 up to 1024 and Hm up to 128 in both dtypes, with
  * pages of any kv_dtype; T * Hm < 2^31, B <= DSA_PLAN_MAX_B.
  * Device faults: DSA_DEV_BAD_PAGE (a visible position past the table or on a page

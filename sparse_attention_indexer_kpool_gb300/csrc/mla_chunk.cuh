@@ -409,19 +409,23 @@ __device__ __forceinline__ void store_rows(const Params& p, const float* inv, ui
     }
   }
 }
-// an unnormalised part of a row tile, for the join
+// an unnormalised part of a row tile for the join (times unit[head], if given)
 template <int kN, int kParts = 1, int kCols = kN>
 __device__ __forceinline__ void store_part(const Params& p, int slot, uint32_t to, int heads,
-                                           int qw, int hq, int lane) {
+                                           int qw, int hq, int lane,
+                                           const float* unit = nullptr) {
   constexpr int kW = heads_of(kN);
   float* dst = p.part_o + ((long long)slot * kN + hq * kW) * kL + qw * 32 + lane;
+  float iv[kW];
+#pragma unroll
+  for (int i = 0; i < kW; ++i) iv[i] = unit ? unit[hq * kW + i] : 1.f;
 #pragma unroll 1
   for (int mc = 0; mc < 4; ++mc) {
     float o[kW];
     load_o<kN, kParts, kCols>(to, mc, hq, o);
 #pragma unroll
     for (int i = 0; i < kW; ++i)
-      if (hq * kW + i < heads) dst[(long long)i * kL + mc * 128] = o[i];
+      if (hq * kW + i < heads) dst[(long long)i * kL + mc * 128] = o[i] * iv[i];
   }
 }
 // a token that sees nothing

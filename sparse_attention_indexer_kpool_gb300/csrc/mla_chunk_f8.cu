@@ -17,8 +17,9 @@
 //     E5M2's least normal value, by 2^-17 a part, 2^-23 of a weight at the reference in
 //     all.  The sums keep the unrounded fp32 weights.
 // The reference m of a head is kept for u rather than for the bare weight, so that u
-// stays below 2^7 and its parts inside E5M2's range; a row scale counts there as at
-// least 2^-60, which bounds the bare weight as well.  A row whose codes are all zero adds to
+// stays below 2^7 and its parts inside E5M2's range.  Row scales are taken relative to a power
+// of two near those of the first key tile, the base, and count in the reference as at least
+// 2^-80 of it, which bounds the bare weight as well.  A row whose codes are all zero adds to
 // the sums alone: its scale, whatever it is, does not set the reference.
 //
 // Why.  Widening the codes to bf16 in shared memory took 1,960 cycles of conversions
@@ -56,12 +57,18 @@ __host__ __device__ constexpr int cta_threads(int n) {
 }
 constexpr float kRaise8 = 7.f;            // base-2 growth of u that raises a reference
 constexpr float kUp = 256.f;              // weights in E5M2 are scaled by 2^8
-constexpr float kLeastLog = -60.f;
+constexpr float kLeastLog = -80.f;
+// The base lies 2^30 below the largest row scale of a segment's first key tile, so that up to
+// 2^60 above that one and 2^110 below it weights and products stay in range; partials times
+// 2^base do between these two.
+constexpr int kBelow = 30, kBaseMin = -110, kBaseMax = 64;
 constexpr float kLoUp = 16.f;             // of the queries' lo parts
 
 template <int kStages>
 struct Ctl {
-  float m[64], nm[64], alpha[64], l[64], move[64];  // per head; first: read as float4
+  // per head; first: read as float4.  alpha: the square root of a rescale (of weights that may
+  // lie above and below the reference by more than a float's range: taken twice)
+  float m[64], nm[64], alpha[64], l[64], move[64];
   float sq[64];                           // the query rows' scales
   float red[4][64];
   uint64_t full[kStages][4], empty[kStages][4];  // by block of 128 codes
@@ -127,6 +134,10 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
+// 2^x of a whole number
+__device__ __forceinline__ float pow2(int x) {
+  return __uint_as_float((uint32_t)(127 + x) << 23);
+}
 // the leading 3 significant bits (of a NaN: one)
 __device__ __forceinline__ float cut3(float x) {
   return __uint_as_float(__float_as_uint(x) & 0xffe00000u);
@@ -160,7 +171,6 @@ __global__ void __launch_bounds__(256)
   // exponent of the largest magnitude: 2^ex <= top < 2^(ex + 1) (below the normal numbers:
   // theirs, at which the elements are still multiples of 1); 2^(7 - ex) in two factors
   const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -126), half = (7 - ex) >> 1;
-  auto pow2 = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
   const float up0 = pow2(half), up1 = pow2(7 - ex - half);
   const float down = pow2(-half) * pow2(half + ex - 7);  // 2^(ex - 7)
   uint32_t hi[4], lo[4];
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
       }
 #pragma unroll 1
       for (int i = 0; zero && i < 32; ++i) {
-        if ((i & 7) == 0 && !wait_on(&c.full[st][i >> 3], phase_of(tile), dead, wait_ns)) break;
+        if ((i & 7) == 0 && !mbar_test(&c.full[st][i >> 3], phase_of(tile))) return false;
         const uint4 x = *reinterpret_cast<const uint4*>(
             sb + S::kKv + st * kStage + (i >> 3) * kBlock + r * 128 + (((i & 7) ^ (r & 7)) << 4));
         zero = ((x.x | x.y | x.z | x.w) & 0x7f7f7f7fu) == 0u;
@@ -289,7 +299,18 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
       const int heads = min(kN, p.Hm - w.h0 * kN);
       const long long row0 = (long long)w.token * p.Hm + w.h0 * kN;
       if (tid < kN) c.sq[tid] = tid < heads ? __ldg(q_scale + row0 + tid) : 0.f;
+      {  // (c.red: the last segment's sums are read)
+        const float lg = warp_max(fabsf(rs) < INFINITY ? log2f(fabsf(rs)) : -INFINITY);
+        if (hq == 0 && lane == 0) c.red[0][qw] = lg;
+      }
       sync_soft<kSoft>();
+      // the segment's row scales are taken relative to 2^base (as floats: converted in every
+      // tile they cost 15 us of the mixed step)
+      const float top_lg =
+          fmaxf(fmaxf(c.red[0][0], c.red[0][1]), fmaxf(c.red[0][2], c.red[0][3]));
+      const int lowest = (top_lg > -INFINITY ? (int)floorf(top_lg) : 0) - kBelow;
+      const int exponent = min(max(lowest, kBaseMin), kBaseMax);
+      const float base = (float)exponent, unit = kUp * pow2(-exponent);
       for (int v = w.ta; v < w.tb; ++v, ++tiles) {
         const int st = stage_of(tiles), dead_at = tiles & 1;
         const float rs_next = v + 1 < w.tb ? scale_of(w.k, w.b, v + 1) : 0.f;
@@ -309,8 +330,8 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
         }
         // (a hidden key's scale may be anything)
         const float sc = valid ? rs : 0.f, zs = p.zscale * sc;
-        float lg = fmaxf(log2f(fabsf(sc)), kLeastLog);  // in u's reference
-        float up = sc * kUp;
+        float lg = fmaxf(log2f(fabsf(sc)) - base, kLeastLog);  // in u's reference
+        float up = sc * unit;
         const float high_at = kRaise8 - lg;
         float e[kW];
         // z = S * query scale * row scale * softmax scale, S of both parts
@@ -357,11 +378,12 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
           break;
         }
         if (full) {
-          if (adds_nothing(e, sc, st, tiles)) {
+          const bool nothing = high && adds_nothing(e, sc, st, tiles);
+          __syncwarp();
+          if (nothing) {
             lg = kLeastLog;
             up = 0.f;
           }
-          __syncwarp();
           float top[kW];  // of u, relative to the references so far
 #pragma unroll
           for (int i = 0; i < kW; ++i) top[i] = e[i] + lg;
@@ -379,7 +401,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
               if (rel != -INFINITY) move = -rel;
             } else if (rel > kRaise8) {
               c.m[tid] = m_old + rel;
-              a = ex2_fast(-rel);
+              a = ex2_fast(-0.5f * rel);
               move = -rel;
               c.raise = 1;
             }
@@ -397,7 +419,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
         }
         if (full && c.raise) {
 #pragma unroll
-          for (int i = 0; i < kW; ++i) l[i] *= c.alpha[hq * kW + i];
+          for (int i = 0; i < kW; ++i) l[i] = l[i] * c.alpha[hq * kW + i] * c.alpha[hq * kW + i];
         }
         // the weights and their parts (in registers: the last tile's may still be read)
         uint32_t part[3][kW / 4];
@@ -434,7 +456,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
                                 (uint32_t)(i % S::kOParts * kN + hq * kW);
             tmem_ldw<kW>(ta, o);
 #pragma unroll
-            for (int j = 0; j < kW; ++j) o[j] *= c.alpha[hq * kW + j];
+            for (int j = 0; j < kW; ++j) o[j] = o[j] * c.alpha[hq * kW + j] * c.alpha[hq * kW + j];
             tmem_stw<kW>(ta, o);
           }
         }
@@ -489,11 +511,17 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
         c.m[tid] = -INFINITY;
         c.nm[tid] = 0.f;
         if (whole) {
-          c.l[tid] = sum == 0.f ? 0.f : 1.f / (sum * kUp);  // a NaN sum stays one
+          // a NaN sum stays one
+          c.l[tid] = sum == 0.f ? 0.f : 1.f / (sum * kUp) * pow2(exponent);
           if (p.lse && tid < heads) p.lse[row0 + tid] = lse_of(m, sum);
         } else {
+          // relative to its own sum: beside a part of other row scales the references alone
+          // may lie too far apart
+          int ex = 0;
+          const float f = fabsf(sum) < INFINITY ? frexpf(sum, &ex) : sum;
+          c.l[tid] = ldexpf(1.f, exponent - ex);
           const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
-          p.part_ml[slot * kN + tid] = make_float2(m, sum);
+          p.part_ml[slot * kN + tid] = make_float2(m + (float)ex, f);
         }
       }
       sync_soft<kSoft>();
@@ -501,7 +529,7 @@ __global__ void __launch_bounds__(cta_threads(kN), 1)
         store_rows<kN, S::kOParts, S::kOCols>(p, c.l, tl + kOCol, row0, heads, qw, hq, lane);
       else
         store_part<kN, S::kOParts, S::kOCols>(p, 2 * blockIdx.x + (begins ? 1 : 0), tl + kOCol,
-                                              heads, qw, hq, lane);
+                                              heads, qw, hq, lane, c.l);
       tc_fence_before();  // O^T is read: the next segment's P releases it
     }
     if (!ok) hd = Header{-1, -1, 0, 0};

@@ -660,6 +660,42 @@ def test_chunk_e4m3_small_queries(Hm, ps, size):
     check_e4m3(s, at, shift=-110)
 
 
+@pytest.mark.parametrize("Hm,ps", [(64, 64), (16, 64), (32, 64), (64, 5)])
+@pytest.mark.parametrize("lo,hi,zeros", [(-30, 0, 0), (-10, 0, 0), (-62, -58, 0), (-70, -70, 0),
+                                         (-100, -100, 0), (-100, -100, 4), (-115, -80, 0),
+                                         (40, 60, 0), (100, 110, 0), (95, 110, 4)])
+def test_chunk_e4m3_row_scales_of_every_size(Hm, ps, lo, hi, zeros):
+    """Row scales of 2^lo to 2^hi, in every order, with all-zero rows of scale 1 among them;
+    on one CTA's share (700 rows) and on many (9,000)."""
+    for n, n_new in ((700, 3), (9000, 1)):
+        g = torch.Generator(device=DEV).manual_seed(34)
+        zero = list(range(0, n, n // zeros)) if zeros else []
+        rows = torch.randn((n, 512), generator=g, device=DEV)
+        rows[zero] = 0.0
+        lg = lo + (hi - lo) * torch.rand(n, generator=g, device=DEV)
+        scales = torch.exp2(lg)
+        scales[zero] = 1.0
+        q = torch.randn((n_new, Hm, 512), generator=g, device=DEV) * 2.0 ** (-8 - hi)
+        s, at = e4m3_step(rows, scales, Hm=Hm, ps=ps, n_new=n_new, q=q)
+        check_e4m3(s, at, zero, shift=-hi)
+
+
+@pytest.mark.parametrize("Hm,ps", [(64, 64), (16, 64), (32, 64), (64, 5)])
+@pytest.mark.parametrize("first,last,zeros", [(-60, 0, 0), (0, -60, 0), (-100, -100, 300),
+                                              (-20, -100, 40), (60, 0, 130)])
+def test_chunk_e4m3_row_scales_along_the_sequence(Hm, ps, first, last, zeros):
+    """Row scales from 2^first to 2^last, behind ``zeros`` all-zero rows of scale 1, under 300
+    tokens: several tiles of a row one after the other in a CTA."""
+    n = 700
+    g = torch.Generator(device=DEV).manual_seed(36)
+    rows = torch.randn((n, 512), generator=g, device=DEV)
+    scales = torch.exp2(torch.linspace(first, last, n, device=DEV))
+    rows[:zeros], scales[:zeros] = 0.0, 1.0
+    q = torch.randn((300, Hm, 512), generator=g, device=DEV) * 2.0 ** (-8 - max(first, last))
+    s, at = e4m3_step(rows, scales, Hm=Hm, ps=ps, n_new=300, q=q)
+    check_e4m3(s, at, range(zeros), shift=-max(first, last))
+
+
 @pytest.mark.parametrize("n", [1, 3, 200, 9000])
 def test_chunk_e4m3_nothing_but_zero_rows(n):
     """Every logit is 0: out 0 and lse log n, the sum of n ones being exact."""
