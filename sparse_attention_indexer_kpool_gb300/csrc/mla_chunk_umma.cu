@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       for (int v = w.ta; v < w.tb; ++v, ++tiles) {
         const int t = w.k.at(v, r);
         if (!wait_on(&c.s_full, tiles & 1, dead, wait_ns)) c.soft_dead[tiles & 1] = 1;
+        __syncwarp();  // (tcgen05.ld takes a converged warp)
         tc_fence_after();
         float e[kW];
         tmem_ldw<kW>(tl + hq * kW, e);
@@ -305,6 +306,7 @@ __global__ void __launch_bounds__(cta_threads(kSrc), 1)
       }
       if (!wait_on(&c.o_full, segs & 1, dead, wait_ns)) c.soft_dead[tiles & 1] = 1;
       ++segs;
+      __syncwarp();
       tc_fence_after();
       sync_soft<kSoftThreads>();
       if (c.soft_dead[tiles & 1]) {
