@@ -368,9 +368,10 @@ int dsa_paged_append(const void* kv_new, const int32_t* kv_rows, int T, int L, i
  * position t when t <= p and (window == 0 or t > p - window or t < sinks):
  *   z_t = sm_scale * <q_lat[row, h, :], c_t>
  *   out[row, h, :] = sum_t softmax(z)_t * c_t;  lse[row, h] = log(sum_t exp(z_t))
- * Nothing seen gives out = 0 and lse = -inf.  What a token does not see does not
- * reach its output, whatever the cache holds there.  Rows of out and lse behind
- * cu_new[B] are left as they were.  No output may overlap an input.
+ * Nothing seen gives out = 0 and lse = -inf; so do logits that are all -inf, but for
+ * latent columns in which a key seen is not finite (NaN).  What a token does not see
+ * does not reach its output, whatever the cache holds there.  Rows of out and lse
+ * behind cu_new[B] are left as they were.  No output may overlap an input.
  *
  *   q_lat [T, Hm, L] activation dtype; kv as for dsa_mla_paged_decode (seq_lens
  *   counts the new tokens); cu_new [B+1] int32, not decreasing, within [0, T]
@@ -385,6 +386,8 @@ int dsa_paged_append(const void* kv_new, const int32_t* kv_rows, int T, int L, i
  * below 2^-24 of the largest such product of a row that is not all zero, it may be
  * lost to out (not to lse).  The scales of the rows that a token sees, all-zero rows
  * aside, may lie 2^60 apart; out is unspecified for scales further apart than that.
+ * Other pages under bf16 activations with L = 512: sums are held relative to a reference
+ * that weights may pass by 2^20, so that latents above 2^90 in magnitude may overflow.
  * Supported: L multiple of 8 up to 1024 and Hm up to 128 in both dtypes, with
  * pages of any kv_dtype; T * Hm < 2^31, B <= DSA_PLAN_MAX_B.
  * Device faults: DSA_DEV_BAD_PAGE (a visible position past the table or on a page

@@ -281,18 +281,20 @@ namespace {
 // must share their keys (two new tokens of a sequence on average, or more than 64
 // heads), a row must see enough of them to pay for the exchange's start and end (2,048),
 // and every pair must have enough tiles of 64 keys to hide it (64).  The lengths live on
-// the device: the window and the block table's width bound them.
+// the device: T, the window and the block table's width stand for them, so a step
+// whose table is wider than its contexts, or whose T is larger than its tokens, may take
+// pairs where one CTA a row tile were faster, by what the short cases below say.
 // Measured on GB300, pair / single CTA in us (sequences x new tokens, 64 heads; tiles a
-// pair):
-//   context  8,192, 32 x 4: 181 / 196, 16 x 16: 318 / 361, 4 x 256: 1,092 / 1,221
-//   context  4,096, 4 x 8 (13): 50 / 38, 8 x 8 (27): 68 / 59, 1 x 128 (54): 103 / 102,
-//            32 x 4 (54): 111 / 122, 1 x 256 (108): 171 / 178
-//   context  2,048, 16 x 16: 111 / 104, 4 x 256: 330 / 336
-//   context    512, 16 x 16:  61 /  46, 4 x 256: 138 / 114
-//   one sequence, 4 on 65,536 (27): 61 / 61, 8 on 131,072 (108): 157 / 168
-//   window   4,096 of 16,384, 4 x 256: 620 / 662; 2,048: 367 / 367; 512: 177 / 143
-//   context  8,192, 32 x 2: 108 / 109, single tokens 64 x 1: 165 / 111
-//   128 heads, context 8,192, 4 x 4 (27): 63 / 54, 16 x 4 (108): 178 / 207
+// pair), table and T as large as the step:
+//   context  8,192, 32 x 4: 182 / 197, 16 x 16: 321 / 362, 4 x 256: 1,109 / 1,245
+//   context  4,096, 4 x 8 (13): 51 / 37, 8 x 8 (27): 70 / 59, 1 x 128 (54): 105 / 103,
+//            32 x 4 (54): 113 / 123, 1 x 256 (108): 175 / 179
+//   context  2,048, 16 x 16: 118 / 105, 4 x 256: 341 / 339
+//   context    512, 16 x 16:  66 /  45, 4 x 256: 149 / 113
+//   one sequence, 4 on 65,536 (27): 63 / 60, 8 on 131,072 (108): 159 / 169
+//   window   4,096 of 16,384, 4 x 256: 638 / 673; 2,048: 382 / 371; 512: 192 / 142
+//   context  8,192, 32 x 2: 110 / 111, single tokens 64 x 1: 171 / 111
+//   128 heads, context 8,192, 4 x 4 (27): 65 / 55, 16 x 4 (108): 180 / 208
 bool pairs_pay(const ChunkArgs& a) {
   if (a.kv.kv_dtype != DSA_BF16 || (a.Hm <= 64 && a.T < 2ll * a.B)) return false;
   const long long table = (long long)a.kv.max_pages * a.kv.page_size;
@@ -308,7 +310,7 @@ int launch_mla_chunk(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
   if (mla_chunk_umma_ok(a.L, a.dtype, a.kv.kv_dtype)) {
     // E4M3 codes as they are need TMA's boxes of 8 rows; other page sizes are widened
     // (pages of 64, 16 heads, 64 single tokens on 8,192 keys: 65 us, widened 141; 64
-    // heads, 4 x 128 tokens on 4,096 keys: 354 and 495)
+    // heads, 4 x 128 tokens on 4,096 keys: 352 and 516)
     if (a.kv.kv_dtype == DSA_FP8_E4M3 && a.kv.page_size % 8 == 0)
       return launch_mla_chunk_f8(a, workspace, stream);
     return pairs_pay(a) && mla_chunk_pair_ok(a.Hm, a.kv.page_size)

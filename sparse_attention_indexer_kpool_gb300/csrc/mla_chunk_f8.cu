@@ -7,7 +7,7 @@
 // other factor of each product is split into 8-bit parts whose sum it is.
 //   S^T = C q_hi^T + 2^-4 C q_lo^T   E4M3 x E4M3.  A head's query row is scaled by a power
 //     of two to a largest magnitude in [128, 256); hi is the nearest E4M3 value (off by
-//     16 at most), lo that of 16 times the rest.  A bf16 value has 8 significant bits, an
+//     8 at most), lo that of 16 times the rest.  A bf16 value has 8 significant bits, an
 //     E4M3 value 4, so the two are the value itself down to 2^-6 of the scaled row, and
 //     off by at most 2^-14 below: 2^-21 of the row's largest element.  (Beside an element
 //     2^12 times as large, a bf16 element's own rounding is as coarse.)
@@ -29,18 +29,19 @@
 //
 // What bounds it.  64 heads: the products.  S^T is 16 MMAs of 128 x 128 x 32 (both query
 // parts as N, 66 cycles each), O^T 48 of 128 x 64 x 32 (50 cycles, 6 KB of shared memory
-// each), about 4,000 cycles a tile with the next tile's rows through the same port; 4,700
-// measured, 700 more where a reference is raised.  32 heads and fewer: S^T 16 of N = 64 and
+// each), about 4,000 cycles a tile with the next tile's rows through the same port; 5,500
+// by counters, row tiles' ends and raised references included: the rest is the hand-over
+// between the two tiles in flight.  32 heads and fewer: S^T 16 of N = 64 and
 // O^T 16 of N = 96 (the three weight parts beside one another), 1,700 cycles, so the
 // chain load, S^T, softmax, O^T of a tile, two in flight: 4,000 cycles.  16 heads and fewer
 // leave room for a third tile.
-// Measured on GB300: 12 sequences of 1 to 300 new tokens on up to 5,000 keys, 64 heads,
-// 666 us (742 TFLOP/s counted once; one part of the queries after the other: 773); 16
-// heads, 64 single tokens on 4,096 to 16,000 keys in pages of 16, 78 us (334 MB: 4.3
-// TB/s, 0.63 of the measured copy rate; two tiles in flight: 86, and 103 with the parts one
-// after the other).  A softmax
-// thread has half of a tile's heads; a quarter each, on twice the warps, took longer (704
-// us on the former).
+// Measured on GB300 in graphs of calls: 12 sequences of 1 to 300 new tokens on up to 5,000
+// keys, 64 heads, 681 us (726 TFLOP/s counted once; of these, 15 us keep row scales of any size
+// and zero rows right; one part of the queries after the other: 16 % more); 16 heads, 64
+// single tokens on 4,096 to 16,000 keys in pages of 16, 77 us (334 MB: 4.3 TB/s, 0.64 of the
+// measured copy rate; two tiles in flight: 10 % more, and 32 % with the parts one after the
+// other).  A softmax thread has half of a tile's heads; a quarter each, on twice the warps,
+// took 6 % longer on the former.
 #include "mla_chunk.cuh"
 
 namespace dsa {
@@ -789,8 +790,8 @@ size_t mla_chunk_f8_workspace_size(int T, int Hm) {
 }
 
 int launch_mla_chunk_f8(const ChunkArgs& a, void* workspace, cudaStream_t stream) {
-  // (16 heads, 64 single tokens on 8,192 keys: 65 us, as 32 heads 73, as 64 103; 4 x 128
-  // tokens on 4,096 keys: 195, 223 and 334)
+  // (16 heads, 64 single tokens on 8,192 keys: 65 us, as 32 heads 72, as 64 103; 4 x 128
+  // tokens on 4,096 keys: 199, 226 and 330)
   return a.Hm <= 16   ? launch<16>(a, workspace, stream)
          : a.Hm <= 32 ? launch<32>(a, workspace, stream)
                       : launch<64>(a, workspace, stream);

@@ -19,7 +19,7 @@
 // done twice.  What bounds it is the exchange: scores, send, sum, weights, send and PV are
 // a chain of about 9,500 cycles a tile, of which four tiles are on their way at once (what
 // shared memory holds).  Measured on GB300, 64 heads, 2,048 tokens behind 14,336:
-// 3.94 ms, 1,045 TFLOP/s (0.56 of the measured bf16 rate; the single-CTA kernel: 4.53 ms).
+// 4.00 ms, 1,031 TFLOP/s (0.55 of the measured bf16 rate; the single-CTA kernel: 4.62 ms).
 //
 // The two tokens of a pair see the same keys but for the last one and the first of a
 // window.  A key that neither sees is zeroed in shared memory before PV, and so is one that
@@ -881,8 +881,8 @@ int launch_mla_chunk_pair(const ChunkArgs& a, void* workspace, cudaStream_t stre
   static std::atomic<unsigned long long> done{0};
   if (!allow_smem(mla_chunk_pair_kernel, kSmem, done)) return DSA_ERR_CUDA;
   // Not launched beside the end of the kernel before it: pairs that are placed while other
-  // blocks still hold SMs run slower to their end (2,048 tokens behind 14,336: 3.94 ms, and
-  // 4.04 or 4.12 ms beside a kernel of 304 or 1,216 blocks).
+  // blocks still hold SMs run slower to their end (2,048 tokens behind 14,336: 3 % beside a
+  // kernel of 304 blocks, 5 % beside one of 1,216).
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cfg.gridDim = dim3(2 * pairs, 1, 1);

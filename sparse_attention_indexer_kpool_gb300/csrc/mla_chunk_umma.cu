@@ -35,10 +35,13 @@
 // through the same port (1,024 cycles), and the softmax of a tile stands between its two
 // products: rows 128 KB, queries 64 KB and P 16 KB leave no room for a second tile, so
 // the tile is handed on in four column chunks, each refilled as soon as its part of
-// O^T is done.  About 5,500 cycles a tile, of which 4,300 are shared-memory traffic.
-// Measured on GB300, 64 heads: 64 single tokens on 4,096 to 16,000 keys 130 us (667 MB:
-// 5.1 TB/s, 0.76 of the measured copy rate); chunks of 1 to 128 tokens of 16 sequences
-// under a window of 512 and 4 sinks 94 us (430 TFLOP/s); one token on 256 keys 14.6 us.
+// O^T is done.  About 5,500 cycles a tile, of which 4,300 are shared-memory traffic, in long
+// row tiles; a row tile's queries, first rows, first references and end come to 12,500
+// more (five key tiles a row tile: 8,000 cycles each in all, by counters).
+// Measured on GB300 in graphs of calls, 64 heads: 64 single tokens on 4,096 to 16,000 keys
+// 131 us (667 MB: 5.1 TB/s, 0.75 of the measured copy rate); chunks of 1 to 128 tokens of 16
+// sequences under a window of 512 and 4 sinks 94 us (434 TFLOP/s); one token on 256 keys
+// 14.5 us.
 #include "mla_chunk.cuh"
 
 namespace dsa {

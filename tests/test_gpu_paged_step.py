@@ -459,8 +459,9 @@ def test_chunk_infinite_keys(act, Hm, L, width, window, m):
     s = make([n], [m], Hm=Hm, L=L, act=act, kv=act, ps=ps, seed=31, width=width, pad=0)
     d = [7, L - 20]                                     # (one in each half of the columns)
     h = torch.arange(Hm, device=DEV)
-    s["q"][:, :, d[0]] = (s["q"][:, :, d[0]].abs() + 0.5) * torch.where(h % 4 == 1, 1, -1)[:, None].T
-    s["q"][:, :, d[1]] = (s["q"][:, :, d[1]].abs() + 0.5) * torch.where(h % 4 == 2, -1, 1)[:, None].T
+    signs = torch.where(h % 4 == 1, 1, -1), torch.where(h % 4 == 2, -1, 1)
+    for col, sign in zip(d, signs):
+        s["q"][:, :, col] = (s["q"][:, :, col].abs() + 0.5) * sign
     want, want_lse, _ = attend(s, window, 3)
     p = torch.arange(n, device=DEV)
     rows = s["table"][0].long()[p // ps] * ps + p % ps
@@ -583,6 +584,19 @@ def test_chunk_e4m3_queries_with_a_large_element(Hm, ps):
         more = 2.0 ** -21 * s["q"].double().abs().amax(2) * largest * s["sm"]
         ref.check_attend(out, lse, reference(s), BF, 512, rows=torch.arange(live, device=DEV),
                          dz_more=more, out_more=ref.underflow(s["pages"], s["scale"], BF))
+
+
+@pytest.mark.parametrize("act,Hm,L,ps,width", [(BF, 64, 512, 16, 0), (BF, 64, 512, 16, WIDE),
+                                               (BF, 16, 512, 5, 0), (F32, 4, 64, 16, 0)])
+def test_chunk_logits_all_minus_infinity(act, Hm, L, ps, width):
+    """As nothing seen, but for the latent column of the infinity."""
+    s = make([1], [1], Hm=Hm, L=L, act=act, kv=act, ps=ps, seed=37, width=width, pad=0)
+    s["q"][:, :, 5] = -1.0
+    s["pages"][s["table"][0, 0].long() * ps, 5] = math.inf
+    out, lse, st = attend(s)
+    rest = torch.arange(L, device=DEV) != 5
+    assert st == 0 and bool((lse == -math.inf).all()) and bool((out[:, :, rest] == 0).all())
+    assert torch.isnan(out[:, :, 5].float()).all()
 
 
 def e4m3_step(rows, scales=None, Hm=64, ps=64, n_new=3, seed=32, q=None):
