@@ -204,7 +204,7 @@ def _quantise(x, largest):
     m, e = torch.frexp(largest)
     e = torch.where(m <= 0.875, e - 9, e - 8).float()              # 448 = 0.875 * 2^9
     e = torch.where(largest > 0, e.clamp(min=E_MIN), float(E_MIN))
-    return x * torch.exp2(-e)[..., None, None].to(E4M3), e
+    return (x * torch.exp2(-e)[..., None, None]).to(E4M3), e
 
 
 # ------------------------------------------------------------------ one pass
