@@ -445,10 +445,15 @@ def work(case):
 
 
 # ------------------------------------------------------------------ 64 bits
+def _two(e):
+    """2^e in 64 bits, exactly (the 32-bit function is exact at whole numbers)."""
+    return torch.exp2(e.float()).double()
+
+
 def _grid(x):
     """The E4M3 value nearest to x (64 bits; ties to the even code), |x| <= 448."""
     e = (torch.frexp(x)[1] - 1).clamp(min=-6).double()
-    step = torch.exp2(e - 3.0)
+    step = _two(e - 3)
     return torch.round(x / step) * step
 
 
@@ -470,16 +475,16 @@ def exact(case, seed):
                     x = new_rows[at + lo - c:at + hi - c].double().transpose(0, 1)
                     a = x.abs().amax((1, 2))
                     e = torch.ceil(torch.log2(a / 448.0)).clamp(min=E_MIN)
-                    e = torch.where(a > 448.0 * torch.exp2(e), e + 1, e)
-                    e = torch.where(a <= 448.0 * torch.exp2(e - 1), e - 1, e).clamp(min=E_MIN)
+                    e = torch.where(a > 448.0 * _two(e), e + 1, e)
+                    e = torch.where(a <= 448.0 * _two(e - 1), e - 1, e).clamp(min=E_MIN)
                     pg, o = table[b][j], lo - j * ps
                     if o:
-                        before = torch.log2(scale[pg])
+                        before = torch.log2(scale[pg]).round()
                         e = torch.maximum(e, before)
-                        up = torch.exp2(before - e)[:, None, None]
+                        up = _two(before - e)[:, None, None]
                         pages[pg, :, :o] = _grid(pages[pg, :, :o] * up)
-                    pages[pg, :, o:o + hi - lo] = _grid(x / torch.exp2(e)[:, None, None])
-                    scale[pg] = torch.exp2(e)
+                    pages[pg, :, o:o + hi - lo] = _grid(x / _two(e)[:, None, None])
+                    scale[pg] = _two(e)
                 at += n
             return pages, scale
         if sum(new) > 70000:
