@@ -402,6 +402,131 @@ int dsa_mla_paged_chunk(const void* q_lat, const dsa_paged_kv* kv, const int32_t
 size_t dsa_mla_paged_chunk_workspace_size(int T, int Hm, int L, int dtype, int kv_dtype);
 
 /*
+ * A grouped-query layer in the paged serving step: Hq query heads, Hkv heads of
+ * keys and values (Hq a multiple G of Hkv; query head h reads KV head h / G), in a
+ * paged cache of 8-bit codes with a scale for each block of tokens and KV head.
+ * dsa_paged_plan gives its block table and lengths as it does for the latent cache;
+ * dsa_gqa_append writes the step's keys and values, dsa_gqa_attend attends to all
+ * that the new tokens see or, with dsa_gqa_block_scores and dsa_topk_pools before it,
+ * to the blocks selected for each token and KV head; dsa_gqa_read brings rows back.
+ * The pages have no counterpart: their one paged cache holds latent rows (module
+ * glm5next_dsa, Modules, attend).
+ *
+ *   k_pages, v_pages [n_pages, Hkv, page_size, D]  E4M3 codes, 16-byte aligned
+ *   k_scale, v_scale [n_pages, Hkv] fp32: the value of a code c is c * scale, and a
+ *     scale a power of two from 2^-64 to 2^120, as dsa_gqa_append writes it
+ *   block_table [B, max_pages] int32: position t of sequence b is row t % page_size
+ *     of page block_table[b * max_pages + t / page_size]
+ *   seq_lens [B] int32, the step's new tokens included: row cu_new[b] + i of the
+ *     step is position seq_lens[b] - n_b + i, n_b = cu_new[b+1] - cu_new[b]
+ *   cu_new [B+1] int32, not decreasing, within [0, T]
+ * Supported by all four: D a multiple of 16 up to 256, page_size a multiple of 16 up
+ * to 1024, Hq <= 128, n_pages * page_size * Hkv < 2^31, T * Hq < 2^31, B <=
+ * DSA_PLAN_MAX_B, activations bf16 or fp32.  No output may overlap an input or another
+ * output.  Tensors of activations and pages on 16 bytes, everything else on 4 (k_mean
+ * on 16).  Rows behind cu_new[B] are left as they were.  T == 0 is a no-op.
+ * Device faults: DSA_DEV_BAD_PAGE (a position past the table or on a page outside
+ * [0, n_pages): written nowhere, not attended to, no candidate), DSA_DEV_BAD_LENGTH (a
+ * row without a position, cu_new outside [0, T] or decreasing: outputs unspecified
+ * where it decreases).
+ */
+typedef struct dsa_gqa_kv {
+  void* k_pages;
+  void* v_pages;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int n_pages, page_size, max_pages, Hkv, D;
+} dsa_gqa_kv;
+
+/*
+ * dsa_gqa_append - quantise a step's keys and values into the cache.
+ *
+ *   k_new, v_new [T, Hkv, D] activation dtype
+ *   k_mean [n_pages, Hkv, D] bf16 or NULL: the mean key of every complete block
+ * For each block that new tokens fall into, KV head, and keys and values apart:
+ *   a = max |x| over the block's new finite elements
+ *   e = the least exponent >= -64 with a <= 448 * 2^e; at least that of the block's
+ *       scale where tokens before the new ones are in it
+ *   scale = 2^e; codes = x / 2^e, rounded to nearest (a non-finite element becomes the
+ *       NaN code); codes of tokens before the new ones, if the exponent grew from e0:
+ *       their value times 2^(e0 - e), rounded to nearest
+ * A power of two keeps E4M3's relative precision, so that only values below 2^-6 of the
+ * scale are rounded again when it grows.  Where the block's last position is written,
+ * k_mean of its page is the mean of its page_size stored keys, rounded to nearest.
+ * Rows of a block behind the last new token keep their codes (the first token of a
+ * block sets its scale alone, whatever the page held).  Two blocks of a step on the same
+ * page leave it with codes and scale of either.
+ */
+int dsa_gqa_append(const void* k_new, const void* v_new, const int32_t* cu_new, int T, int B,
+                   int dtype, const dsa_gqa_kv* kv, void* k_mean, int32_t* status_dev,
+                   void* stream);
+
+/*
+ * dsa_gqa_read - bring keys and values of the cache back to the activation dtype.
+ *
+ *   cu_out [B+1] int32, not decreasing, within [0, T]: rows cu_out[b] + i of the outputs
+ *   are positions begin[b] + i of sequence b (begin [B] int32, NULL: all zero)
+ *   k_out, v_out [T, Hkv, D]: code * scale, rounded to nearest (exact in fp32, and in bf16
+ *   while it is a normal number)
+ * Positions at or past seq_lens[b] (DSA_DEV_BAD_LENGTH) and positions without a page
+ * (DSA_DEV_BAD_PAGE) are zeros; so are negative ones (DSA_DEV_BAD_LENGTH).
+ */
+int dsa_gqa_read(const dsa_gqa_kv* kv, const int32_t* cu_out, const int32_t* begin, int T, int B,
+                 int dtype, void* k_out, void* v_out, int32_t* status_dev, void* stream);
+
+/*
+ * dsa_gqa_block_scores - how much each new token's query heads look at each block, by
+ * the blocks' mean keys.
+ *
+ * Block j is a candidate of the token at position p when it is complete there,
+ * (j + 1) * page_size - 1 <= p.  Over the candidates, for KV head h and g < G:
+ *   z[g, j] = sm_scale * <q[t, h*G + g, :], k_mean[page of block j, h, :]>
+ *   scores[t, h, j] = sum_g exp(z[g, j]) / sum_j' exp(z[g, j'])
+ * Blocks j <= p / page_size with j < sink_blocks or j > p / page_size - local_blocks get
+ * +inf (local_blocks >= 1: the token's own block is one of them), every other one
+ * -inf, so that dsa_topk_pools over the [T * Hkv, NB] scores takes the former first, in
+ * the order of their numbers, and never the latter.  The pages' own scores (module
+ * glm5next_dsa::tp, "Why the indexer is REPLICATED") are a sum over heads as well.
+ *
+ *   q [T, Hq, D] activation dtype;  k_mean as dsa_gqa_append leaves it
+ *   scores [T, Hkv, NB] fp32, NB >= 1; every entry of a token's row is written; blocks at
+ *   or past NB are no candidates and not forced (DSA_DEV_POOL_RANGE)
+ */
+int dsa_gqa_block_scores(const void* q, const void* k_mean, const int32_t* block_table,
+                         const int32_t* seq_lens, const int32_t* cu_new, int T, int B, int Hq,
+                         int Hkv, int D, int n_pages, int page_size, int max_pages,
+                         int sink_blocks, int local_blocks, float sm_scale, int NB, int dtype,
+                         float* scores, int32_t* status_dev, void* stream);
+
+/*
+ * dsa_gqa_attend - causal attention of the step's new tokens over the cache.
+ *
+ * The token at position p sees position t <= p when (block_ids NULL) window == 0 or
+ * t > p - window or t < sinks, or (block_ids given; window and sinks 0) t's block is
+ * listed for the token and the KV head; a block that is listed twice counts twice,
+ * a negative entry not at all.
+ *   z_t = sm_scale * <q[row, h, :], k_t>;  out[row, h, :] = sum_t softmax(z)_t * v_t
+ *   lse[row, h] = log(sum_t exp(z_t))
+ * Nothing seen gives out = 0 and lse = -inf.  What a token does not see does not reach
+ * its output, whatever the cache holds there.
+ *
+ *   q [T, Hq, D] activation dtype; block_ids [T, Hkv, K] int32 or NULL (K = 0)
+ *   out [T, Hq, D] activation dtype; lse [T, Hq] fp32 (may be NULL)
+ *   workspace: dsa_gqa_attend_workspace_size(...) bytes, 16-byte aligned, no initial
+ *   value; calls in flight at the same time must not share one
+ * The lengths and lists are read on the GPU: a captured call follows them when replayed.
+ * Outputs are deterministic.
+ * Device faults: also DSA_DEV_TIMEOUT (outputs unspecified).
+ */
+int dsa_gqa_attend(const void* q, const dsa_gqa_kv* kv, const int32_t* cu_new,
+                   const int32_t* block_ids, int K, int T, int B, int Hq, int window, int sinks,
+                   float sm_scale, int dtype, void* out, float* lse, void* workspace,
+                   size_t ws_bytes, int32_t* status_dev, void* stream);
+size_t dsa_gqa_attend_workspace_size(int T, int Hq, int Hkv, int D, int dtype);
+
+/*
  * dsa_select - index_scores -> topk_pools -> expand_selection in one call.
  *
  * Source: module glm5next_dsa, Modules, select (the production launcher of the

@@ -38,6 +38,13 @@ class PagedKv(ctypes.Structure):
         (n, c_int) for n in ("n_pages", "page_size", "max_pages", "kv_dtype")]
 
 
+class GqaKv(ctypes.Structure):
+    """dsa_gqa_kv (include/dsa.h), field for field."""
+    _fields_ = [(n, c_void_p) for n in ("k_pages", "v_pages", "k_scale", "v_scale", "block_table",
+                                        "seq_lens")] + [
+        (n, c_int) for n in ("n_pages", "page_size", "max_pages", "Hkv", "D")]
+
+
 # name -> (restype, argtypes); mirrors include/dsa.h
 SIGNATURES = {
     "dsa_kpool_compress": (c_int, [c_void_p] * 6 + [c_float] + [c_void_p] * 3 + [c_int] * 5
@@ -61,6 +68,15 @@ SIGNATURES = {
     "dsa_mla_paged_chunk": (c_int, [c_void_p, ctypes.POINTER(PagedKv), c_void_p] + [c_int] * 6
                             + [c_float, c_int] + [c_void_p] * 3 + [c_size_t] + [c_void_p] * 2),
     "dsa_mla_paged_chunk_workspace_size": (c_size_t, [c_int] * 5),
+    "dsa_gqa_append": (c_int, [c_void_p] * 3 + [c_int] * 3 + [ctypes.POINTER(GqaKv)]
+                       + [c_void_p] * 3),
+    "dsa_gqa_read": (c_int, [ctypes.POINTER(GqaKv)] + [c_void_p] * 2 + [c_int] * 3
+                     + [c_void_p] * 4),
+    "dsa_gqa_block_scores": (c_int, [c_void_p] * 5 + [c_int] * 10 + [c_float] + [c_int] * 2
+                             + [c_void_p] * 3),
+    "dsa_gqa_attend": (c_int, [c_void_p, ctypes.POINTER(GqaKv)] + [c_void_p] * 2 + [c_int] * 6
+                       + [c_float, c_int] + [c_void_p] * 3 + [c_size_t] + [c_void_p] * 2),
+    "dsa_gqa_attend_workspace_size": (c_size_t, [c_int] * 5),
     "dsa_select": (c_int, [c_void_p, c_void_p, c_float, c_void_p, c_int] + [c_void_p] * 6
                    + [c_int] * 9 + [c_void_p] * 4 + [c_size_t] + [c_void_p] * 2),
     "dsa_select_workspace_size": (c_size_t, [c_int, c_int, c_int]),

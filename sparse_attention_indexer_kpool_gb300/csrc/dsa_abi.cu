@@ -203,6 +203,34 @@ int check_chunk(const void* q_lat, const dsa_paged_kv* kv, const int32_t* cu_new
   return DSA_OK;
 }
 
+// The geometry that the grouped-query calls share.
+int check_gqa(int T, int B, int Hq, int Hkv, int D, int n_pages, int page_size, int max_pages,
+              int dtype) {
+  if (T < 0 || B < 0 || Hq < 1 || Hkv < 1 || D < 1 || n_pages < 1 || page_size < 1 ||
+      max_pages < 1 || !dtype_ok(dtype) || Hq % Hkv != 0)
+    return DSA_ERR_INVALID_ARG;
+  if (D % 16 != 0 || D > 256 || page_size % 16 != 0 || page_size > 1024 || Hq > 128 ||
+      B > DSA_PLAN_MAX_B || (long long)T * Hq > 0x7fffffffLL ||
+      (long long)n_pages * page_size > 0x7fffffffLL / Hkv)
+    return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+int check_gqa_kv(const dsa_gqa_kv* kv, const int32_t* cu) {
+  if (!kv->k_pages || !kv->v_pages || !kv->k_scale || !kv->v_scale || !kv->block_table ||
+      !kv->seq_lens || !cu)
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned(kv->k_pages, 16) || !aligned(kv->v_pages, 16) || !aligned(kv->k_scale, 4) ||
+      !aligned(kv->v_scale, 4) || !aligned(kv->block_table, 4) || !aligned(kv->seq_lens, 4) ||
+      !aligned(cu, 4))
+    return DSA_ERR_MISALIGNED;
+  return DSA_OK;
+}
+dsa::GqaKv as_gqa(const dsa_gqa_kv* kv) {
+  return {static_cast<uint8_t*>(kv->k_pages), static_cast<uint8_t*>(kv->v_pages), kv->k_scale,
+          kv->v_scale, kv->block_table, kv->seq_lens, kv->n_pages, kv->page_size, kv->max_pages,
+          kv->Hkv, kv->D};
+}
+
 }  // namespace
 
 namespace dsa {
@@ -521,6 +549,91 @@ int dsa_mla_paged_chunk(const void* q_lat, const dsa_paged_kv* kv, const int32_t
   const dsa::ChunkArgs a{q_lat, pk, cu_new, T, B, Hm, L, window, sinks, sm_scale, dtype, out,
                          lse, status_dev};
   return dsa::launch_mla_chunk(a, workspace, as_stream(stream));
+}
+
+int dsa_gqa_append(const void* k_new, const void* v_new, const int32_t* cu_new, int T, int B,
+                   int dtype, const dsa_gqa_kv* kv, void* k_mean, int32_t* status_dev,
+                   void* stream) {
+  if (!kv) return DSA_ERR_INVALID_ARG;
+  int r = check_gqa(T, B, kv->Hkv, kv->Hkv, kv->D, kv->n_pages, kv->page_size, kv->max_pages,
+                    dtype);
+  if (r != DSA_OK || T == 0 || B == 0) return r;
+  r = check_gqa_kv(kv, cu_new);
+  if (r != DSA_OK) return r;
+  if (!k_new || !v_new) return DSA_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_mean, 16) ||
+      !aligned(status_dev, 4))
+    return DSA_ERR_MISALIGNED;
+  return dsa::launch_gqa_append(k_new, v_new, cu_new, T, B, dtype, as_gqa(kv), k_mean, status_dev,
+                                as_stream(stream));
+}
+
+int dsa_gqa_read(const dsa_gqa_kv* kv, const int32_t* cu_out, const int32_t* begin, int T, int B,
+                 int dtype, void* k_out, void* v_out, int32_t* status_dev, void* stream) {
+  if (!kv) return DSA_ERR_INVALID_ARG;
+  int r = check_gqa(T, B, kv->Hkv, kv->Hkv, kv->D, kv->n_pages, kv->page_size, kv->max_pages,
+                    dtype);
+  if (r != DSA_OK || T == 0 || B == 0) return r;
+  r = check_gqa_kv(kv, cu_out);
+  if (r != DSA_OK) return r;
+  if (!k_out || !v_out) return DSA_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(begin, 4) || !aligned(status_dev, 4))
+    return DSA_ERR_MISALIGNED;
+  return dsa::launch_gqa_read(as_gqa(kv), cu_out, begin, T, B, dtype, k_out, v_out, status_dev,
+                              as_stream(stream));
+}
+
+int dsa_gqa_block_scores(const void* q, const void* k_mean, const int32_t* block_table,
+                         const int32_t* seq_lens, const int32_t* cu_new, int T, int B, int Hq,
+                         int Hkv, int D, int n_pages, int page_size, int max_pages,
+                         int sink_blocks, int local_blocks, float sm_scale, int NB, int dtype,
+                         float* scores, int32_t* status_dev, void* stream) {
+  const int r = check_gqa(T, B, Hq, Hkv, D, n_pages, page_size, max_pages, dtype);
+  if (r != DSA_OK) return r;
+  if (sink_blocks < 0 || local_blocks < 0 || NB < 1 || !isfinite(sm_scale))
+    return DSA_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return DSA_OK;
+  if (!q || !k_mean || !block_table || !seq_lens || !cu_new || !scores) return DSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_mean, 16) || !aligned(block_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(scores, 4) ||
+      !aligned(status_dev, 4))
+    return DSA_ERR_MISALIGNED;
+  const dsa::GqaScoreArgs a{q, static_cast<const __nv_bfloat16*>(k_mean), block_table, seq_lens,
+                            cu_new, T, B, Hq, Hkv, D, n_pages, page_size, max_pages, sink_blocks,
+                            local_blocks, sm_scale, NB, scores, status_dev};
+  return dsa::launch_gqa_scores(a, dtype, as_stream(stream));
+}
+
+size_t dsa_gqa_attend_workspace_size(int T, int Hq, int Hkv, int D, int dtype) {
+  if (T < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0 || !dtype_ok(dtype)) return 0;
+  return dsa::gqa_attend_workspace_size(T, Hq, Hkv, D, dtype);
+}
+
+int dsa_gqa_attend(const void* q, const dsa_gqa_kv* kv, const int32_t* cu_new,
+                   const int32_t* block_ids, int K, int T, int B, int Hq, int window, int sinks,
+                   float sm_scale, int dtype, void* out, float* lse, void* workspace,
+                   size_t ws_bytes, int32_t* status_dev, void* stream) {
+  if (!kv) return DSA_ERR_INVALID_ARG;
+  int r = check_gqa(T, B, Hq, kv->Hkv, kv->D, kv->n_pages, kv->page_size, kv->max_pages, dtype);
+  if (r != DSA_OK) return r;
+  if (window < 0 || sinks < 0 || !isfinite(sm_scale) || K < 0) return DSA_ERR_INVALID_ARG;
+  // a list and a window at once have no meaning here; a list of nothing is no list
+  if ((block_ids != nullptr) != (K > 0) && T > 0) return DSA_ERR_INVALID_ARG;
+  if (K > 0 && (window > 0 || sinks > 0)) return DSA_ERR_INVALID_ARG;
+  if ((long long)K * kv->page_size > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0) return DSA_OK;
+  r = check_gqa_kv(kv, cu_new);
+  if (r != DSA_OK) return r;
+  if (!q || !out) return DSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_ids, 4) ||
+      !aligned(status_dev, 4))
+    return DSA_ERR_MISALIGNED;
+  const size_t need = dsa::gqa_attend_workspace_size(T, Hq, kv->Hkv, kv->D, dtype);
+  if (need > 0 && (!workspace || ws_bytes < need)) return DSA_ERR_WORKSPACE;
+  if (workspace && !aligned(workspace, 16)) return DSA_ERR_MISALIGNED;
+  const dsa::GqaArgs a{q, as_gqa(kv), cu_new, block_ids, K, T, B, Hq, window, sinks, sm_scale,
+                       dtype, out, lse, status_dev};
+  return dsa::launch_gqa_attend(a, workspace, as_stream(stream));
 }
 
 }  // extern "C"

@@ -386,6 +386,43 @@ int launch_mla_chunk_f8(const ChunkArgs& a, void* workspace, cudaStream_t stream
 bool mla_chunk_pair_ok(int Hm, int page_size);
 size_t mla_chunk_pair_workspace_size();
 int launch_mla_chunk_pair(const ChunkArgs& a, void* workspace, cudaStream_t stream);
+// ---- the grouped-query layer of the paged step
+struct GqaKv {  // dsa_gqa_kv after validation
+  uint8_t *k_pages, *v_pages;  // [n_pages, Hkv, page_size, D] E4M3 codes
+  float *k_scale, *v_scale;    // [n_pages, Hkv] powers of two
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* seq_lens;     // [B]
+  int n_pages, page_size, max_pages, Hkv, D;
+};
+int launch_gqa_append(const void* k_new, const void* v_new, const int32_t* cu_new, int T, int B,
+                      int dtype, const GqaKv& kv, void* k_mean, int32_t* status,
+                      cudaStream_t stream);
+int launch_gqa_read(const GqaKv& kv, const int32_t* cu_out, const int32_t* begin, int T, int B,
+                    int dtype, void* k_out, void* v_out, int32_t* status, cudaStream_t stream);
+struct GqaScoreArgs {
+  const void* q;
+  const __nv_bfloat16* k_mean;  // [n_pages, Hkv, D]
+  const int32_t *block_table, *seq_lens, *cu_new;
+  int T, B, Hq, Hkv, D, n_pages, page_size, max_pages, sink_blocks, local_blocks;
+  float sm_scale;
+  int NB;
+  float* scores;  // [T, Hkv, NB]
+  int32_t* status;
+};
+int launch_gqa_scores(const GqaScoreArgs& a, int dtype, cudaStream_t stream);
+struct GqaArgs {
+  const void* q;
+  GqaKv kv;
+  const int32_t *cu_new, *block_ids;  // block_ids [T, Hkv, K] or nullptr
+  int K, T, B, Hq, window, sinks;
+  float sm_scale;
+  int dtype;
+  void* out;
+  float* lse;
+  int32_t* status;
+};
+size_t gqa_attend_workspace_size(int T, int Hq, int Hkv, int D, int dtype);
+int launch_gqa_attend(const GqaArgs& a, void* workspace, cudaStream_t stream);
 }  // namespace dsa
 
 #define DSA_LAUNCH_CHECK()                          \

@@ -308,6 +308,140 @@ def dsa_mla_paged_chunk(q_lat, pages, row_scale, block_table, seq_lens, page_siz
     _check("dsa_mla_paged_chunk", code)
 
 
+def _gqa_codes(t):
+    """Pages of codes: float8_e4m3fn or uint8."""
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"pages must be float8_e4m3fn or uint8 codes, got {t.dtype}")
+    return t.dtype
+
+
+def _gqa_cache(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_new):
+    """A grouped-query cache's geometry, once its tensors' shapes agree."""
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page_size, D]")
+    n_pages, Hkv, page_size, D = k_pages.shape
+    if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0]:
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    B, width = block_table.shape
+    _sizes((k_scale, n_pages * Hkv, "k_scale"), (v_scale, n_pages * Hkv, "v_scale"),
+           (cu_new, B + 1, "cu_new"))
+    return n_pages, Hkv, page_size, D, B, width
+
+
+def dsa_gqa_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_new,
+                   k_mean=None, status=None, stream=None):
+    """Quantise a step's keys and values ``k_new``, ``v_new`` [T, Hkv, D] into the paged cache
+    ``k_pages``, ``v_pages`` [n_pages, Hkv, page_size, D] (float8_e4m3fn or uint8 codes) with
+    ``k_scale``, ``v_scale`` [n_pages, Hkv] fp32; ``k_mean`` [n_pages, Hkv, D] bf16 gets the mean
+    key of every block that becomes complete.  ``seq_lens`` counts the new tokens."""
+    n_pages, Hkv, ps, D, B, width = _gqa_cache(k_pages, v_pages, k_scale, v_scale, block_table,
+                                               seq_lens, cu_new)
+    if k_new.dim() != 3 or k_new.shape[1:] != (Hkv, D) or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [T, Hkv, D]")
+    act, codes = k_new.dtype, _gqa_codes(k_pages)
+    _sizes((k_mean, n_pages * Hkv * D, "k_mean"))
+    dev, st = _device(k_new, stream)
+    kn, vn, kp, vp, ks, vs, table, lens, cu, mean, status = _args(
+        dev, (k_new, act, "k_new"), (v_new, act, "v_new"), (k_pages, codes, "k_pages"),
+        (v_pages, codes, "v_pages"), (k_scale, _F32, "k_scale"), (v_scale, _F32, "v_scale"),
+        (block_table, _I32, "block_table"), (seq_lens, _I32, "seq_lens"), (cu_new, _I32, "cu_new"),
+        (k_mean, torch.bfloat16, "k_mean"), (status, _I32, "status"))
+    kv = _lib.GqaKv(kp, vp, ks, vs, table, lens, n_pages, ps, width, Hkv, D)
+    code = _lib.load().dsa_gqa_append(kn, vn, cu, k_new.shape[0], B, _dtype_tag(k_new),
+                                      ctypes.byref(kv), mean, status, st)
+    _check("dsa_gqa_append", code)
+
+
+def dsa_gqa_read(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_out, k_out, v_out,
+                 begin=None, status=None, stream=None):
+    """Bring rows of the cache back: ``k_out``, ``v_out`` [T, Hkv, D] rows ``cu_out[b]`` .. get
+    positions ``begin[b]`` .. (``begin`` [B] or None: 0) of sequence b."""
+    n_pages, Hkv, ps, D, B, width = _gqa_cache(k_pages, v_pages, k_scale, v_scale, block_table,
+                                               seq_lens, cu_out)
+    if k_out.dim() != 3 or k_out.shape[1:] != (Hkv, D) or v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out must be [T, Hkv, D]")
+    act, codes = k_out.dtype, _gqa_codes(k_pages)
+    _sizes((begin, B, "begin"))
+    dev, st = _device(k_pages, stream)
+    kp, vp, ks, vs, table, lens, cu, first, ko, vo, status = _args(
+        dev, (k_pages, codes, "k_pages"), (v_pages, codes, "v_pages"), (k_scale, _F32, "k_scale"),
+        (v_scale, _F32, "v_scale"), (block_table, _I32, "block_table"),
+        (seq_lens, _I32, "seq_lens"), (cu_out, _I32, "cu_out"), (begin, _I32, "begin"),
+        (k_out, act, "k_out"), (v_out, act, "v_out"), (status, _I32, "status"))
+    kv = _lib.GqaKv(kp, vp, ks, vs, table, lens, n_pages, ps, width, Hkv, D)
+    code = _lib.load().dsa_gqa_read(ctypes.byref(kv), cu, first, k_out.shape[0], B,
+                                    _dtype_tag(k_out), ko, vo, status, st)
+    _check("dsa_gqa_read", code)
+
+
+def dsa_gqa_block_scores(q, k_mean, block_table, seq_lens, page_size, cu_new, sink_blocks,
+                         local_blocks, sm_scale, scores, status=None, stream=None):
+    """``scores`` [T, Hkv, NB] fp32 of the cache's complete blocks for the new tokens' queries
+    ``q`` [T, Hq, D], from the blocks' mean keys ``k_mean`` [n_pages, Hkv, D] bf16: the heads'
+    softmax weights over the blocks, summed over a KV head's group; +inf for the first
+    ``sink_blocks`` and the last ``local_blocks`` blocks.  ``dsa_topk_pools`` over
+    ``scores.view(T * Hkv, NB)`` gives ``dsa_gqa_attend``'s ``block_ids``."""
+    if q.dim() != 3 or k_mean.dim() != 3 or k_mean.shape[2] != q.shape[2]:
+        raise ValueError("q must be [T, Hq, D] and k_mean [n_pages, Hkv, D]")
+    if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0]:
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    T, Hq, D = q.shape
+    n_pages, Hkv, _ = k_mean.shape
+    B, width = block_table.shape
+    if scores.dim() != 3 or scores.shape[:2] != (T, Hkv):
+        raise ValueError("scores must be [T, Hkv, NB]")
+    _sizes((cu_new, B + 1, "cu_new"))
+    dev, st = _device(q, stream)
+    qp, mean, table, lens, cu, sc, status = _args(
+        dev, (q, q.dtype, "q"), (k_mean, torch.bfloat16, "k_mean"),
+        (block_table, _I32, "block_table"), (seq_lens, _I32, "seq_lens"), (cu_new, _I32, "cu_new"),
+        (scores, _F32, "scores"), (status, _I32, "status"))
+    code = _lib.load().dsa_gqa_block_scores(
+        qp, mean, table, lens, cu, T, B, Hq, Hkv, D, n_pages, int(page_size), width,
+        int(sink_blocks), int(local_blocks), float(sm_scale), scores.shape[2], _dtype_tag(q), sc,
+        status, st)
+    _check("dsa_gqa_block_scores", code)
+
+
+def gqa_attend_workspace_bytes(q, k_pages) -> int:
+    T, Hq, D = q.shape
+    return int(_lib.load().dsa_gqa_attend_workspace_size(T, Hq, k_pages.shape[1], D,
+                                                         _dtype_tag(q)))
+
+
+def dsa_gqa_attend(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_new, window,
+                   sinks, sm_scale, out, lse, workspace=None, block_ids=None, status=None,
+                   stream=None):
+    """Causal attention of the step's new tokens ``q`` [T, Hq, D] over the paged 8-bit cache (as
+    for ``dsa_gqa_append``): over all before them (``window`` 0), a sliding window and the first
+    ``sinks`` tokens, or the blocks that ``block_ids`` [T, Hkv, K] lists for each token and KV
+    head (negative: none)."""
+    n_pages, Hkv, ps, D, B, width = _gqa_cache(k_pages, v_pages, k_scale, v_scale, block_table,
+                                               seq_lens, cu_new)
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError("q must be [T, Hq, D]")
+    T, Hq, _ = q.shape
+    K = 0
+    if block_ids is not None:
+        if block_ids.dim() != 3 or block_ids.shape[:2] != (T, Hkv) or block_ids.shape[2] < 1:
+            raise ValueError("block_ids must be [T, Hkv, K], K >= 1")
+        K = block_ids.shape[2]
+    act, codes = q.dtype, _gqa_codes(k_pages)
+    _sizes((out, T * Hq * D, "out"), (lse, T * Hq, "lse"))
+    dev, st = _device(q, stream)
+    qp, kp, vp, ks, vs, table, lens, cu, ids, o, ls, ws, status = _args(
+        dev, (q, act, "q"), (k_pages, codes, "k_pages"), (v_pages, codes, "v_pages"),
+        (k_scale, _F32, "k_scale"), (v_scale, _F32, "v_scale"), (block_table, _I32, "block_table"),
+        (seq_lens, _I32, "seq_lens"), (cu_new, _I32, "cu_new"), (block_ids, _I32, "block_ids"),
+        (out, act, "out"), (lse, _F32, "lse"), (workspace, torch.uint8, "workspace"),
+        (status, _I32, "status"))
+    kv = _lib.GqaKv(kp, vp, ks, vs, table, lens, n_pages, ps, width, Hkv, D)
+    code = _lib.load().dsa_gqa_attend(
+        qp, ctypes.byref(kv), cu, ids, K, T, B, Hq, int(window), int(sinks), float(sm_scale),
+        _dtype_tag(q), o, ls, ws, 0 if workspace is None else workspace.numel(), status, st)
+    _check("dsa_gqa_attend", code)
+
+
 def select_workspace_bytes(Q, P_ld, select_k) -> int:
     return int(_lib.load().dsa_select_workspace_size(Q, P_ld, select_k))
 

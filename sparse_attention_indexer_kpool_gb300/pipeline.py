@@ -11,6 +11,10 @@ tokens their sequences, positions and cache rows, append_step stores their laten
 rows, attend_step attends to all that they see, or select_step and
 attend_selected_step to a selection.  Nothing in it reads the GPU back: a step is
 captured into a graph once and replayed for the next tokens.
+
+``GqaStep`` is the same for the grouped-query layers beside them, over keys and values
+in 8 bits: plan_step as above, append_gqa_step, select_blocks_step where the layer
+attends to selected blocks, attend_gqa_step.
 """
 from __future__ import annotations
 
@@ -19,7 +23,7 @@ from dataclasses import dataclass
 import torch
 
 from . import ops
-from .synth import Batch, PagedCache
+from .synth import Batch, GqaCache, PagedCache
 
 
 @dataclass
@@ -200,12 +204,13 @@ class PagedStep:
         return step
 
 
-def plan_step(cache: PagedCache, step: PagedStep, new_lens, row_base=None, stream=None):
+def plan_step(cache: PagedCache | GqaCache, step: "PagedStep | GqaStep", new_lens, row_base=None,
+              stream=None):
     """The step of ``new_lens`` [B] tokens: lengths, table and free list move on in place."""
     ops.dsa_paged_plan(cache.seq_lens, new_lens, step.free_pages, step.free_begin,
-                       cache.pages.shape[0] // cache.page_size, cache.page_size,
-                       cache.block_table, cache.seq_lens, step.cu_new, step.q_seq, step.q_pos,
-                       step.kv_rows, step.free_begin, row_base,
+                       cache.n_pages, cache.page_size, cache.block_table, cache.seq_lens,
+                       step.cu_new, step.q_seq, step.q_pos, step.kv_rows,
+                       step.free_begin, row_base,
                        None if row_base is None else step.key_rows, step.status, stream)
 
 
@@ -235,3 +240,74 @@ def attend_selected_step(cache: PagedCache, step: PagedStep, q_lat, sm_scale, st
     ops.dsa_mla_paged_decode(q_lat, cache.pages, cache.row_scale, cache.block_table,
                              cache.seq_lens, cache.page_size, step.q_seq, step.token_ids, sm_scale,
                              step.out, step.lse, step.ws_selected, step.status, stream)
+
+
+@dataclass
+class GqaStep:
+    """Buffers of a serving step of up to T new tokens over a ``GqaCache``; layers whose caches
+    share the table and the lengths share the plan."""
+    free_pages: torch.Tensor   # [n_free] int32 pages, taken from free_begin on
+    free_begin: torch.Tensor   # [1] int32
+    cu_new: torch.Tensor       # [B + 1] int32: the plan's token axis
+    q_seq: torch.Tensor        # [T] int32
+    q_pos: torch.Tensor
+    kv_rows: torch.Tensor
+    key_rows: torch.Tensor
+    out: torch.Tensor          # [T, Hq, D]
+    lse: torch.Tensor          # [T, Hq] fp32
+    ws: torch.Tensor | None
+    status: torch.Tensor
+    scores: torch.Tensor | None = None        # [T, Hkv, max_pages] fp32 (alloc with select_k)
+    block_ids: torch.Tensor | None = None     # [T, Hkv, select_k] int32
+    ws_topk: torch.Tensor | None = None
+
+    @staticmethod
+    def alloc(cache: GqaCache, free_pages, T: int, Hq: int, dtype=torch.bfloat16,
+              select_k: int = 0) -> "GqaStep":
+        dev = cache.k_pages.device
+        _, Hkv, _, D = cache.k_pages.shape
+        B, width = cache.block_table.shape
+        i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device=dev)  # noqa: E731
+        out = torch.zeros(T, Hq, D, dtype=dtype, device=dev)
+        ws = ops.gqa_attend_workspace_bytes(out, cache.k_pages)
+        step = GqaStep(
+            free_pages=free_pages, free_begin=i32(1), cu_new=i32(B + 1), q_seq=i32(T),
+            q_pos=i32(T), kv_rows=i32(T), key_rows=i32(T), out=out,
+            lse=torch.zeros(T, Hq, dtype=torch.float32, device=dev),
+            ws=torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None, status=i32(1))
+        if select_k:
+            # rows behind the last token keep what is here: they select nothing
+            step.scores = torch.full((T, Hkv, width), float("-inf"), device=dev)
+            step.block_ids = i32(T, Hkv, select_k)
+            ws_t = ops.topk_workspace_bytes(T * Hkv, width, select_k)
+            step.ws_topk = torch.empty(max(ws_t, 16), dtype=torch.uint8, device=dev)
+        return step
+
+
+def append_gqa_step(cache: GqaCache, step: GqaStep, k_new, v_new, stream=None):
+    """Quantise the step's keys and values ``k_new``, ``v_new`` [T, Hkv, D] into a layer's cache."""
+    ops.dsa_gqa_append(k_new, v_new, cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale,
+                       cache.block_table, cache.seq_lens, step.cu_new, cache.k_mean, step.status,
+                       stream)
+
+
+def select_blocks_step(cache: GqaCache, step: GqaStep, q, sm_scale, sink_blocks=1, local_blocks=1,
+                       stream=None):
+    """``step.block_ids``: the blocks that each of the step's tokens (``q`` [T, Hq, D]) attends
+    to, for each KV head."""
+    ops.dsa_gqa_block_scores(q, cache.k_mean, cache.block_table, cache.seq_lens, cache.page_size,
+                             step.cu_new, sink_blocks, local_blocks, sm_scale, step.scores,
+                             step.status, stream)
+    T, Hkv, width = step.scores.shape
+    ops.dsa_topk_pools(step.scores.view(T * Hkv, width), step.block_ids.shape[2],
+                       step.block_ids.view(T * Hkv, -1), step.ws_topk, stream)
+
+
+def attend_gqa_step(cache: GqaCache, step: GqaStep, q, sm_scale, window=0, sinks=0,
+                    selected=False, stream=None):
+    """Attention of the step's tokens (``q`` [T, Hq, D]) over all that they see, a window, or the
+    blocks of ``select_blocks_step``, into ``step.out``, ``step.lse``."""
+    ops.dsa_gqa_attend(q, cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale,
+                       cache.block_table, cache.seq_lens, step.cu_new, window, sinks, sm_scale,
+                       step.out, step.lse, step.ws, step.block_ids if selected else None,
+                       step.status, stream)

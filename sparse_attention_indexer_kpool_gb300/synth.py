@@ -257,6 +257,42 @@ class PagedCache:
     seq_lens: torch.Tensor       # [B] int32
     page_size: int
 
+    @property
+    def n_pages(self):
+        return self.pages.shape[0] // self.page_size
+
+
+@dataclass
+class GqaCache:
+    """Keys and values of a grouped-query layer in pages of E4M3 codes, one scale for each page
+    and KV head."""
+    k_pages: torch.Tensor        # [n_pages, Hkv, page_size, D] float8_e4m3fn codes
+    v_pages: torch.Tensor
+    k_scale: torch.Tensor        # [n_pages, Hkv] fp32 powers of two
+    v_scale: torch.Tensor
+    k_mean: torch.Tensor         # [n_pages, Hkv, D] bf16: means of complete blocks
+    block_table: torch.Tensor    # [B, max_pages] int32
+    seq_lens: torch.Tensor       # [B] int32
+
+    @property
+    def n_pages(self):
+        return self.k_pages.shape[0]
+
+    @property
+    def page_size(self):
+        return self.k_pages.shape[2]
+
+    @staticmethod
+    def alloc(n_pages, Hkv, page_size, D, B, max_pages, device="cuda") -> "GqaCache":
+        """An empty cache: no sequence holds a page."""
+        codes = lambda: torch.zeros((n_pages, Hkv, page_size, D), dtype=torch.uint8,  # noqa: E731
+                                    device=device).view(torch.float8_e4m3fn)
+        ones = lambda: torch.ones((n_pages, Hkv), device=device)  # noqa: E731
+        return GqaCache(codes(), codes(), ones(), ones(),
+                        torch.zeros((n_pages, Hkv, D), dtype=torch.bfloat16, device=device),
+                        torch.full((B, max_pages), -1, dtype=torch.int32, device=device),
+                        torch.zeros(B, dtype=torch.int32, device=device))
+
 
 def paged_cache(kv, cu_seqlens, page_size: int, *, e4m3=False, seed=0, n_spare=3,
                 extra_blocks=1) -> PagedCache:
