@@ -423,6 +423,10 @@ struct GqaArgs {
 };
 size_t gqa_attend_workspace_size(int T, int Hq, int Hkv, int D, int dtype);
 int launch_gqa_attend(const GqaArgs& a, void* workspace, cudaStream_t stream);
+// its form on the tensor cores for decode tokens and block lists: bf16, head dim 64 or 128
+bool gqa_split_ok(int D, int dtype);
+size_t gqa_split_workspace_size(int Hq, int Hkv, int D);
+int launch_gqa_split(const GqaArgs& a, void* workspace, cudaStream_t stream);
 }  // namespace dsa
 
 #define DSA_LAUNCH_CHECK()                          \

@@ -166,9 +166,12 @@ __global__ void __launch_bounds__(kThreads) gqa_attend_simt_kernel(GqaArgs a) {
 
 }  // namespace
 
-size_t gqa_attend_workspace_size(int, int, int, int, int) { return 0; }
+size_t gqa_attend_workspace_size(int, int Hq, int Hkv, int D, int dtype) {
+  return gqa_split_ok(D, dtype) ? gqa_split_workspace_size(Hq, Hkv, D) : 0;
+}
 
-int launch_gqa_attend(const GqaArgs& a, void*, cudaStream_t stream) {
+int launch_gqa_attend(const GqaArgs& a, void* workspace, cudaStream_t stream) {
+  if (gqa_split_ok(a.kv.D, a.dtype)) return launch_gqa_split(a, workspace, stream);
   const int G = a.Hq / a.kv.Hkv;
   auto kernel =
       a.dtype == DSA_BF16 ? gqa_attend_simt_kernel<__nv_bfloat16> : gqa_attend_simt_kernel<float>;

@@ -1,0 +1,1000 @@
+// Attention of a grouped-query layer over the paged 8-bit cache, for decode tokens and for
+// tokens on selected blocks (bf16 activations, head dim 64 or 128): every warp on its own
+// share of the keys.
+//
+// A row tile is one token, one KV head and up to 8 kN of its query heads.  Per tile of 32
+// keys, with the keys as the rows of the products (16 x 8 x 16, fp16 in, fp32 out):
+//   S^T = C_k Q^T                 the codes of the keys, widened to fp16 (exact)
+//   e = S * (query scale * key scale * softmax scale) + lv - m,  w = 2^e
+//   O^T += C_v^T W^T              the codes of the values, widened likewise
+// Query rows are scaled by a power of two to a largest magnitude in [2^14, 2^15): a bf16
+// element keeps its 8 bits in fp16 down to 2^-28 of the row's largest.  lv is the exponent of the
+// values' scale (a power of two), which so multiplies the weight.  The reference m of a head
+// is that of z + lv, raised when a weight passes it by 2^7; weights are held times 2^8, so
+// that fp16 keeps 11 bits of them down to 2^-22 of the reference and none is off by more than
+// 2^-33 of it.  The sum of a head takes lv off again: it is that of 2^(z - m + B) in fp32, B
+// the lv of the key that set the reference, so that scales as far apart as their exponents
+// go neither overflow it nor lose a weight to it.
+//
+// Why like this.  A decode step reads every key and value once and computes 2 G products for
+// each byte: it is bound by memory, and what counts is bytes on their way and no pause in
+// them.  So no warp waits for another: each has a ring of three 8 KB tiles (32 keys and
+// their values) that TMA fills in the 128-byte swizzle, runs through its share of the
+// batch's tiles, and keeps scores, weights and outputs in registers: an S^T accumulator
+// holds a key's row in four lanes, movmatrix turns it into the second factor of O^T, and
+// a value's 16 bytes are widened in the lane that needs them.  The keys of a tile are taken in
+// an order that keeps both kinds of rows free of bank conflicts.
+// Shares are equal in tiles whatever the lengths; a row tile that two or more warps share
+// leaves partials (fp32) that the join kernel adds in their order.
+#include "gqa.cuh"
+#include "umma.cuh"
+
+#include <cudaTypedefs.h>
+
+namespace dsa {
+namespace {
+
+using namespace gqa;
+
+constexpr int kW = 8, kThreads = 32 * kW;
+constexpr int kKeys = 32;                      // of a tile
+constexpr float kRaise = 15.f;                 // e above which a reference is raised (2^7)
+constexpr int kUp = 8;                         // weights are held times 2^8
+constexpr int kExtra = 1;                      // what a row tile costs beside its tiles, in tiles
+constexpr int kRingBytes = 3 * 2 * kKeys * 128;  // of a warp
+
+struct Header {        // what a warp left for the join
+  int start_tile;      // row tile whose first tiles it holds but not its last (-1: none)
+  int cont_tile;       // row tile that an earlier warp began (-1: none)
+  int cont_some;       // it has a partial of that
+  int cont_ends;       // and its last tiles
+};
+
+struct Params {
+  GqaArgs a;
+  int G, hb;                 // query heads of a KV head, row tiles of those
+  float zscale;              // softmax scale in base 2
+  int cap;                   // positions that the block table has room for
+  int per_block;             // boxes of a block
+  float* part_o;             // [2 workers][8 kN][D]
+  float4* part_ml;           // [2 workers][8 kN]: reference; the sum f 2^z as z and f
+  Header* head;              // [workers]
+};
+
+// ---- the batch as tiles --------------------------------------------------------
+struct Seq {
+  int c0, n, base;           // rows c0 .. c0 + n - 1 of the step; position of the first
+  unsigned u;                // tiles of a row tile, at most, and kExtra
+};
+template <int kR>
+__device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p) {
+  Seq s;
+  s.c0 = min(max(cu0, 0), p.a.T);
+  s.n = max(min(cu1, p.a.T) - s.c0, 0);
+  s.base = len < 0 ? -s.n : len - s.n;  // negative: rows before position 0
+  if (p.a.block_ids) {
+    s.u = (unsigned)(((long long)p.a.K * p.per_block * kR + kKeys - 1) / kKeys);
+  } else {
+    const unsigned all = (unsigned)min(max(len, 0), p.cap);
+    s.u = (all + kKeys - 1) / kKeys;
+    if (p.a.window > 0) {
+      const long long boxes = (p.a.sinks + kR - 1ll) / kR + (kR - 2ll + p.a.window) / kR + 1;
+      const long long most = (boxes * kR + kKeys - 1) / kKeys;
+      if (most < (long long)s.u) s.u = (unsigned)most;
+    }
+  }
+  s.u = max(s.u, 1u) + kExtra;
+  return s;
+}
+
+struct Start {
+  unsigned long long n;      // tiles of the share
+  int b;                     // its first sequence (B: no share)
+  unsigned row, unit;        // row tile of it, tile of that
+};
+
+// A row tile's part of a share.
+template <int kR>
+struct Walk {
+  const Params& p;
+  unsigned long long left;
+  int b;
+  unsigned row, unit;
+  Seq s;
+  int token, h, cb, tile_id, ta, tb, n;     // the segment: tiles [ta, tb) of n
+  int pos, lo, s0, sink_boxes, first, boxes;  // what its token sees
+
+  __device__ __forceinline__ Walk(const Params& pp, const Start& st)
+      : p(pp), left(st.b < pp.a.B ? st.n : 0), b(st.b), row(st.row), unit(st.unit) {
+    if (left > 0) load();
+  }
+  __device__ __forceinline__ void load() {
+    s = seq_of<kR>(__ldg(p.a.cu_new + b), __ldg(p.a.cu_new + b + 1), __ldg(p.a.kv.seq_lens + b),
+                   p);
+  }
+  __device__ __forceinline__ bool next() {
+    if (left == 0) return false;
+    const unsigned per = (unsigned)(p.a.kv.Hkv * p.hb);
+    while (row >= (unsigned)s.n * per) {
+      if (++b >= p.a.B) return false;  // (lengths that changed under the call)
+      load();
+      row = 0;
+    }
+    const unsigned e = left < s.u - unit ? unit + (unsigned)left : s.u;
+    const int i = (int)(row / per), rest = (int)(row - (unsigned)i * per);
+    h = rest / p.hb;
+    cb = rest - h * p.hb;
+    token = s.c0 + i;
+    tile_id = token * (int)per + rest;
+    const int at = s.base + i;
+    if (p.a.block_ids) {
+      pos = at;
+      lo = s0 = 0;
+      sink_boxes = first = 0;
+      boxes = at < 0 ? 0 : p.a.K * p.per_block;
+    } else {
+      pos = min(at, p.cap - 1);
+      lo = p.a.window > 0 ? max(0, max(at, -1) - p.a.window + 1) : 0;
+      s0 = min(min(p.a.sinks, lo), p.cap);
+      first = lo / kR;
+      sink_boxes = min((s0 + kR - 1) / kR, first);
+      boxes = at < 0 ? 0 : sink_boxes + max(pos / kR - first + 1, 0);
+    }
+    n = (boxes * kR + kKeys - 1) / kKeys;
+    ta = share_of(unit, n, s.u);
+    tb = share_of(e, n, s.u);
+    left -= e - unit;
+    unit = e;
+    if (e == s.u) {
+      unit = 0;
+      ++row;
+    }
+    return true;
+  }
+  static __device__ __forceinline__ int share_of(unsigned a, int n, unsigned u) {
+    if (a == 0) return 0;
+    if (a == u) return n;
+    return (int)((unsigned long long)a * (unsigned)n / u);
+  }
+  __device__ __forceinline__ bool sees(int t) const { return t <= pos && (t >= lo || t < s0); }
+};
+
+// The share of worker `me` for each warp of this CTA.  Ends with a barrier.
+template <int kR>
+__device__ __forceinline__ void find_shares(const Params& p, Start* st,
+                                            unsigned long long* scan) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.a.B;
+  const int per = (B + kThreads - 1) / kThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  const unsigned tiles = (unsigned)(p.a.kv.Hkv * p.hb);
+  if (tid < kW) st[tid].b = B;
+  unsigned long long mine = 0;
+  bool odd = false, past = false, falls = false;
+  for (int b = b0; b < b1; ++b) {
+    const int cu0 = p.a.cu_new[b], cu1 = p.a.cu_new[b + 1], len = p.a.kv.seq_lens[b];
+    const Seq s = seq_of<kR>(cu0, cu1, len, p);
+    odd |= cu0 < 0 || cu1 < cu0 || cu1 > p.a.T || (s.n > 0 && s.base < 0);
+    past |= s.n > 0 && len > p.cap;
+    falls |= cu1 < cu0;
+    mine += (unsigned long long)((unsigned)s.n * tiles) * s.u;
+  }
+  if (blockIdx.x == 0) {
+    if (odd) flag(p.a.status, DSA_DEV_BAD_LENGTH);
+    if (past && !p.a.block_ids) flag(p.a.status, DSA_DEV_BAD_PAGE);
+  }
+  unsigned long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) scan[warp] = inc;
+  // rows of several sequences at once (the work would have no bound): nothing is done
+  falls = __syncthreads_or(falls);
+  unsigned long long before = inc - mine, total = 0;
+  for (int w = 0; w < kW; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  if (falls) total = 0;
+  const unsigned workers = gridDim.x * kW;
+  for (int w = 0; w < kW; ++w) {
+    // neighbours in the keys are neighbours in their numbers, and few shares lie on many SMs
+    const unsigned me = (unsigned)w * gridDim.x + blockIdx.x;
+    unsigned long long v0, v1;
+    if (total < workers) {
+      v0 = me < total ? me : total;
+      v1 = me < total ? me + 1 : total;
+    } else {
+      v0 = total * me / workers;
+      v1 = total * (me + 1) / workers;
+    }
+    if (v0 < v1 && v0 >= before && v0 < before + mine) {
+      unsigned long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        const Seq s = seq_of<kR>(p.a.cu_new[b], p.a.cu_new[b + 1], p.a.kv.seq_lens[b], p);
+        const unsigned long long all = (unsigned long long)((unsigned)s.n * tiles) * s.u;
+        if (v0 < at + all) {
+          const unsigned long long off = v0 - at;
+          st[w].b = b;
+          st[w].row = (unsigned)(off / s.u);
+          st[w].unit = (unsigned)(off - (unsigned long long)st[w].row * s.u);
+          st[w].n = v1 - v0;
+          break;
+        }
+        at += all;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// ---- small pieces ----------------------------------------------------------------
+// D[16 x 8] += A[16 x 16] B[16 x 8], fp16 in, fp32 out
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// an 8 x 8 matrix of fp16, a row in four lanes, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// row of a tile that row r of the products holds (r < 8; the other eight follow alike)
+__device__ __forceinline__ int key_of(int r) { return (r & 1) ? r ^ 4 : r; }
+// where the 16-byte chunk c of a row of kD bytes lies in the tile
+template <int kD>
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+  return kD == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// the maximum over the keys of a product's column (lanes of the same t)
+__device__ __forceinline__ float across_keys(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+// x 2^(e - kUp) / f, in steps that stay in range where the result does (0 for f = 0: no sum)
+struct Factor {
+  float inv, a, b;
+  __device__ __forceinline__ Factor(float f, int e) {
+    inv = f == 0.f ? 0.f : 1.f / (f * (float)(1 << kUp));
+    const int third = max(min(e / 3, 126), -126);
+    a = pow2(third);
+    b = pow2(max(min(e - 2 * third, 126), -126));
+  }
+  __device__ __forceinline__ float operator()(float x) const { return x * inv * a * a * b; }
+};
+
+struct Meta {          // of a tile in the ring, by box
+  int pos[2];          // first position (0x7fffffff: no such box)
+  float ks[2];         // keys' scale
+  int ev[2];           // exponent of the values' scale
+};
+template <int kStages>
+struct Ctl {
+  uint64_t full[kW][kStages];
+  Meta meta[kW][kStages];
+  Start start[kW];
+  unsigned long long scan[kW];
+};
+
+template <int kD>
+constexpr int stages() { return kRingBytes / (2 * kKeys * kD); }
+template <int kD>
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)kW * kRingBytes + sizeof(Ctl<stages<kD>()>);
+}
+
+// kD: head dim, kN: blocks of 8 query heads, kR: keys of a TMA box (a divisor of the page)
+template <int kD, int kN, int kR>
+__global__ void __launch_bounds__(kThreads, 1)
+    gqa_split_kernel(const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map, const Params p) {
+  constexpr int kStages = stages<kD>(), kBoxes = kKeys / kR;
+  constexpr int kSteps = kD / 16, kM = kD / 16;   // k steps of S^T, m tiles of O^T
+  constexpr int kTile = kKeys * kD;               // bytes of a tile's keys (its values follow)
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  auto& c = *reinterpret_cast<Ctl<kStages>*>(sb + (size_t)kW * kRingBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const GqaKv& kv = p.a.kv;
+  if (tid < kW * kStages) mbar_init(&c.full[tid / kStages][tid % kStages], 1);
+  if (tid == 0) fence_mbar_init();
+  pdl_wait();
+  pdl_launch_dependents();
+  find_shares<kR>(p, c.start, c.scan);
+  const int worker = warp * gridDim.x + blockIdx.x;
+  const Start& st = c.start[warp];
+  unsigned char* ring = sb + (size_t)warp * kRingBytes;
+  const uint32_t ring_at = smem_u32(ring);
+
+  // ---- the loads, kStages tiles ahead
+  Walk<kR> wl(p, st);
+  bool more = false;
+  int lv = 0, held = 0;                     // next tile; first tile that the lanes hold
+  int row[kBoxes], bpos[kBoxes], bev[kBoxes];
+  float bks[kBoxes];
+  int issued = 0;
+  auto look_up = [&]() {                    // the next 32 tiles, one a lane
+    held = lv;
+#pragma unroll
+    for (int i = 0; i < kBoxes; ++i) {
+      row[i] = -1;
+      bpos[i] = 0x7fffffff;
+      bks[i] = 0.f;
+      bev[i] = 0;
+      const int box = (lv + lane) * kBoxes + i;
+      if (lv + lane >= wl.tb || box >= wl.boxes) continue;
+      long long at;
+      if (p.a.block_ids) {
+        const int j = box / p.per_block;
+        const int id =
+            __ldg(p.a.block_ids + ((long long)wl.token * kv.Hkv + wl.h) * p.a.K + j);
+        at = id < 0 ? -1 : (long long)id * kv.page_size + (box - j * p.per_block) * kR;
+      } else {
+        at = (long long)(box < wl.sink_boxes ? box : wl.first + (box - wl.sink_boxes)) * kR;
+      }
+      if (at < 0 || at > wl.pos) continue;
+      const int blk = (int)at / kv.page_size;
+      const int page =
+          at < p.cap ? __ldg(kv.block_table + (long long)wl.b * kv.max_pages + blk) : -1;
+      if (page < 0 || page >= kv.n_pages) {
+        flag(p.a.status, DSA_DEV_BAD_PAGE);
+        continue;
+      }
+      const int unit = page * kv.Hkv + wl.h;
+      row[i] = unit * kv.page_size + ((int)at - blk * kv.page_size);
+      bpos[i] = (int)at;
+      bks[i] = __ldg(kv.k_scale + unit);
+      bev[i] = exponent_of(__ldg(kv.v_scale + unit));
+    }
+  };
+  auto advance = [&]() {                    // to the next segment with tiles
+    while ((more = wl.next()) && wl.ta == wl.tb) {}
+    if (more) {
+      lv = wl.ta;
+      look_up();
+    }
+  };
+  auto issue = [&]() {
+    if (!more) return;
+    if (lv - held == 32) look_up();
+    const int src = lv - held, s = issued % kStages;
+    if (lane == src) {
+      Meta& m = c.meta[warp][s];
+#pragma unroll
+      for (int i = 0; i < kBoxes; ++i) {
+        m.pos[i] = bpos[i];
+        m.ks[i] = bks[i];
+        m.ev[i] = bev[i];
+      }
+      int boxes = 0;
+#pragma unroll
+      for (int i = 0; i < kBoxes; ++i) boxes += row[i] >= 0;
+      mbar_arrive_expect_tx(&c.full[warp][s], boxes * 2 * kR * kD);
+      unsigned char* dst = ring + s * 2 * kTile;
+#pragma unroll
+      for (int i = 0; i < kBoxes; ++i)
+        if (row[i] >= 0) {
+          tma_load_2d(dst + i * kR * kD, &k_map, 0, row[i], &c.full[warp][s]);
+          tma_load_2d(dst + kTile + i * kR * kD, &v_map, 0, row[i], &c.full[warp][s]);
+        }
+    }
+    __syncwarp();
+    ++issued;
+    if (++lv == wl.tb) advance();
+  };
+  advance();
+#pragma unroll 1
+  for (int s = 0; s < kStages; ++s) issue();
+
+  // ---- the work
+  Walk<kR> w(p, st);
+  Header hd = {-1, -1, 0, 0};
+  int done = 0;
+  bool ok = true;
+  while (ok && w.next()) {
+    const bool some = w.tb > w.ta, whole = w.ta == 0 && w.tb == w.n;
+    const bool begins = some && w.ta == 0 && !whole;
+    if (begins) hd.start_tile = w.tile_id;
+    if (!whole && !begins && hd.cont_tile < 0) {
+      hd.cont_tile = w.tile_id;
+      hd.cont_some = some;
+      hd.cont_ends = w.tb == w.n;
+    }
+    if (!some && !whole) continue;
+    const int head0 = w.cb * 8 * kN, heads = min(8 * kN, p.G - head0);
+    const long long row0 = (long long)w.token * p.a.Hq + w.h * p.G + head0;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + row0 * kD;
+    if (!some) {  // nothing seen
+      for (int i = lane; i < heads * (kD / 8); i += 32)
+        reinterpret_cast<uint4*>(out)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.a.lse)
+        for (int i = lane; i < heads; i += 32) p.a.lse[row0 + i] = -INFINITY;
+      continue;
+    }
+    // the queries: lane (g, t) holds head g's elements 16 t .. and, of 128, 64 + 16 t ..
+    uint32_t q[kN][kSteps][2];
+    float qs[kN][2];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      uint4 x[kD / 64][2];
+      const bool real = n * 8 + g < heads;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.a.q) +
+                                 (row0 + (real ? n * 8 + g : 0)) * kD + 16 * t;
+#pragma unroll
+      for (int i = 0; i < kD / 64; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          x[i][j] = real ? __ldg(reinterpret_cast<const uint4*>(src + 64 * i) + j)
+                         : make_uint4(0u, 0u, 0u, 0u);
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kD / 64; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t u[4] = {x[i][j].x, x[i][j].y, x[i][j].z, x[i][j].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = fabsf(bf16lo(u[k])), b = fabsf(bf16hi(u[k]));
+            if (a < INFINITY) top = fmaxf(top, a);
+            if (b < INFINITY) top = fmaxf(top, b);
+          }
+        }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -126), half = (14 - ex) >> 1;
+      const float up0 = pow2(half), up1 = pow2(14 - ex - half);
+      const float down = pow2(-half) * pow2(half + ex - 14);
+#pragma unroll
+      for (int i = 0; i < kD / 64; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t u[4] = {x[i][j].x, x[i][j].y, x[i][j].z, x[i][j].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // a NaN or an infinity becomes NaN: its head's logits are NaN
+            float a = bf16lo(u[k]) * up0 * up1, b = bf16hi(u[k]) * up0 * up1;
+            a = fabsf(a) < INFINITY ? a : NAN;
+            b = fabsf(b) < INFINITY ? b : NAN;
+            q[n][4 * i + 2 * j + (k >> 1)][k & 1] = pack_f16(a, b);
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        qs[n][j] = __shfl_sync(0xffffffffu, down, (2 * t + j) * 4) * p.zscale;
+    }
+    float o[kM][kN][4], l[kN][2], m[kN][2];
+    int base[kN][2];  // B
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+#pragma unroll
+      for (int i = 0; i < kM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][n][j] = 0.f;
+      l[n][0] = l[n][1] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY;
+      base[n][0] = base[n][1] = 0;
+    }
+    bool unset = true;  // some head here has no reference yet
+
+#pragma unroll 1
+    for (int v = w.ta; v < w.tb; ++v, ++done) {
+      const int s = done % kStages;
+      ok = mbar_wait_bounded(&c.full[warp][s], (unsigned)(done / kStages) & 1u);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const Meta& mt = c.meta[warp][s];
+      const uint32_t kb = ring_at + s * 2 * kTile, vb = kb + kTile;
+      bool all = true;  // every key of the tile is seen
+#pragma unroll
+      for (int i = 0; i < kBoxes; ++i) {
+        const long long p0 = mt.pos[i], p1 = p0 + kR - 1;
+        all = all && p1 <= w.pos && (p0 >= w.lo || p1 < w.s0);
+      }
+      auto seen = [&](int r) -> bool {
+        const int i = kBoxes == 1 ? 0 : r / kR;
+        const long long at = (long long)mt.pos[i] + (kBoxes == 1 ? r : r % kR);
+        return at <= w.pos && (at >= w.lo || at < w.s0);
+      };
+      // S^T: 16 keys at a time
+      float e[2][kN][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[j][n][i] = 0.f;
+        const int r0 = 16 * j + key_of(g);
+#pragma unroll
+        for (int i = 0; i < kD / 64; ++i) {
+          const uint4 x = lds128(kb + chunk_at<kD>(r0, 4 * i + t));
+          const uint4 y = lds128(kb + chunk_at<kD>(r0 + 8, 4 * i + t));
+          const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a0 = codes2_f16(xa[k] & 0xffffu), a2 = codes2_f16(xa[k] >> 16);
+            const uint32_t a1 = codes2_f16(ya[k] & 0xffffu), a3 = codes2_f16(ya[k] >> 16);
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+              mma_f16(e[j][n], a0, a1, a2, a3, q[n][4 * i + k][0], q[n][4 * i + k][1]);
+          }
+        }
+      }
+      // exponents of the weights; columns 2 t and 2 t + 1
+      bool raise = unset;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int box = kBoxes == 1 ? 0 : j;
+        const float ks = mt.ks[box], lv8 = (float)(mt.ev[box] + kUp);
+        const bool see0 = all || seen(16 * j + key_of(g)), see1 = all || seen(16 * j + key_of(g) + 8);
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float mm = m[n][i & 1], ref = mm == -INFINITY ? 0.f : mm;
+            const float x = fmaf(e[j][n][i], qs[n][i & 1] * ks, lv8 - ref);
+            e[j][n][i] = (i < 2 ? see0 : see1) ? x : -INFINITY;
+            raise |= e[j][n][i] > kRaise;
+          }
+      }
+      if (__any_sync(0xffffffffu, raise)) {
+        unset = false;
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float top0 = across_keys(fmaxf(e[0][n][i], e[0][n][i + 2]));
+            const float top1 = across_keys(fmaxf(e[1][n][i], e[1][n][i + 2]));
+            const int lv = mt.ev[kBoxes == 2 && top1 > top0 ? 1 : 0] + kUp;
+            const float rel = fmaxf(top0, top1) - (float)kUp;
+            float move = 0.f;
+            if (m[n][i] == -INFINITY) {  // nothing accumulated for this head yet
+              if (rel != -INFINITY) {
+                m[n][i] = rel;
+                move = -rel;
+                base[n][i] = lv;
+              }
+            } else if (rel > kRaise - (float)kUp) {
+              m[n][i] += rel;
+              move = -rel;
+              // (the square roots, taken twice: weights may lie further apart than a float reaches)
+              const float a = ex2_fast(-0.5f * rel);
+              int to = lv;
+              if ((float)(lv - base[n][i]) - rel > 60.f)
+                to = (int)floorf((float)base[n][i] + rel + 60.f);
+              const float f = ex2_fast(0.5f * ((float)(to - base[n][i]) - rel));
+              base[n][i] = to;
+              l[n][i] = l[n][i] * f * f;
+#pragma unroll
+              for (int k = 0; k < kM; ++k) {
+                o[k][n][i] = o[k][n][i] * a * a;
+                o[k][n][i + 2] = o[k][n][i + 2] * a * a;
+              }
+            }
+            // (an infinite maximum: its key's weight is NaN, as in the formula)
+            e[0][n][i] += move;
+            e[0][n][i + 2] += move;
+            e[1][n][i] += move;
+            e[1][n][i + 2] += move;
+            unset |= m[n][i] == -INFINITY;
+          }
+      }
+      // weights; O^T
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int box = kBoxes == 1 ? 0 : j;
+        const int lv = mt.ev[box] + kUp;
+        uint32_t b[kN][2];
+        bool far = false;  // this box's scale lies far below the reference's
+#pragma unroll
+        for (int n = 0; n < kN; ++n) far |= max(base[n][0], base[n][1]) - lv > 64;
+        far = __any_sync(0xffffffffu, far);
+        if (far) {
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float d = (float)(base[n][i] - lv);
+              float x = e[j][n][i] + d, y = e[j][n][i + 2] + d;
+              if (across_keys(fmaxf(x, y)) > 100.f) {
+                base[n][i] -= 100;
+                l[n][i] *= 0x1p-100f;
+                x -= 100.f;
+                y -= 100.f;
+              }
+              l[n][i] += ex2_fast(x) + ex2_fast(y);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[j][n][i] = ex2_fast(e[j][n][i]);
+          if (!far) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              l[n][i] = fmaf(e[j][n][i] + e[j][n][i + 2], pow2(max(base[n][i] - lv, -126)),
+                             l[n][i]);
+          }
+          b[n][0] = transpose8(pack_f16(e[j][n][0], e[j][n][1]));
+          b[n][1] = transpose8(pack_f16(e[j][n][2], e[j][n][3]));
+        }
+        // the values of four keys: of the products' k = 2 t, 2 t + 1 and eight on
+        const int r0 = 16 * j + key_of(2 * t), r1 = 16 * j + key_of(2 * t + 1);
+        const int rs[4] = {r0, r1, r0 + 8, r1 + 8};
+        if constexpr (kD == 128) {  // lane (g, t): columns 16 g ..
+          uint32_t x[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 y = lds128(vb + chunk_at<kD>(rs[i], g));
+            if (!all && !seen(rs[i])) y = make_uint4(0u, 0u, 0u, 0u);
+            x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t sel = u ? 0x7362u : 0x5140u;
+              const uint32_t a0 = __byte_perm(x[0][k], x[1][k], sel);
+              const uint32_t a1 = __byte_perm(x[0][k + 2], x[1][k + 2], sel);
+              const uint32_t a2 = __byte_perm(x[2][k], x[3][k], sel);
+              const uint32_t a3 = __byte_perm(x[2][k + 2], x[3][k + 2], sel);
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint32_t f0 = codes2_f16(z ? a0 >> 16 : a0 & 0xffffu);
+                const uint32_t f1 = codes2_f16(z ? a1 >> 16 : a1 & 0xffffu);
+                const uint32_t f2 = codes2_f16(z ? a2 >> 16 : a2 & 0xffffu);
+                const uint32_t f3 = codes2_f16(z ? a3 >> 16 : a3 & 0xffffu);
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+                  mma_f16(o[4 * k + 2 * u + z][n], f0, f1, f2, f3, b[n][0], b[n][1]);
+              }
+            }
+        } else {  // columns 8 g ..
+          uint32_t x[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint2 y = lds64(vb + chunk_at<kD>(rs[i], g >> 1) + 8 * (g & 1));
+            if (!all && !seen(rs[i])) y = make_uint2(0u, 0u);
+            x[i][0] = y.x; x[i][1] = y.y;
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t sel = u ? 0x7362u : 0x5140u;
+            const uint32_t a0 = __byte_perm(x[0][0], x[1][0], sel);
+            const uint32_t a1 = __byte_perm(x[0][1], x[1][1], sel);
+            const uint32_t a2 = __byte_perm(x[2][0], x[3][0], sel);
+            const uint32_t a3 = __byte_perm(x[2][1], x[3][1], sel);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t f0 = codes2_f16(z ? a0 >> 16 : a0 & 0xffffu);
+              const uint32_t f1 = codes2_f16(z ? a1 >> 16 : a1 & 0xffffu);
+              const uint32_t f2 = codes2_f16(z ? a2 >> 16 : a2 & 0xffffu);
+              const uint32_t f3 = codes2_f16(z ? a3 >> 16 : a3 & 0xffffu);
+#pragma unroll
+              for (int n = 0; n < kN; ++n)
+                mma_f16(o[2 * u + z][n], f0, f1, f2, f3, b[n][0], b[n][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();  // the tile is read
+      issue();
+    }
+    if (!ok) break;
+
+    // the row tile's end: lane (g, t) holds columns kD / 8 * g .. of heads 2 t and 2 t + 1
+    constexpr int kC = kD / 8;
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float sum = l[n][i];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int col = n * 8 + 2 * t + i;
+        if (col >= heads) continue;
+        float x[kC];
+#pragma unroll
+        for (int k = 0; k < kM; ++k) {
+          x[k] = o[k][n][i];
+          x[kC / 2 + k] = o[k][n][i + 2];
+        }
+        int ex = 0;
+        const float f = fabsf(sum) < INFINITY ? frexpf(sum, &ex) : sum;
+        const float z = m[n][i] + (float)(ex - base[n][i]);  // the sum is f 2^z
+        if (whole) {
+          const Factor by(f, base[n][i] - ex);
+          uint32_t y[kC / 2];
+#pragma unroll
+          for (int k = 0; k < kC / 2; ++k) y[k] = pack_bf16(by(x[2 * k]), by(x[2 * k + 1]));
+          uint4* dst = reinterpret_cast<uint4*>(out + (long long)col * kD + kC * g);
+#pragma unroll
+          for (int k = 0; k < kC / 8; ++k)
+            dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+          if (p.a.lse && g == 0)
+            p.a.lse[row0 + col] = sum == 0.f ? -INFINITY : (z + log2f(f)) / kLog2e;
+        } else {
+          const long long slot = (long long)(2 * worker + (begins ? 1 : 0)) * (8 * kN) + col;
+          float4* dst = reinterpret_cast<float4*>(p.part_o + slot * kD + kC * g);
+#pragma unroll
+          for (int k = 0; k < kC / 4; ++k)
+            dst[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          if (g == 0) p.part_ml[slot] = make_float4(m[n][i], z, f, 0.f);
+        }
+      }
+  }
+  if (!ok) {  // a wait ran out: no copy into this CTA's memory may be in flight at its end
+    for (; done < issued; ++done)
+      mbar_wait_bounded(&c.full[warp][done % kStages], (unsigned)(done / kStages) & 1u);
+    if (lane == 0) flag(p.a.status, DSA_DEV_TIMEOUT);
+    hd = Header{-1, -1, 0, 0};
+  }
+  if (lane == 0) p.head[worker] = hd;
+}
+
+// Join the partials of the row tiles that were split over warps, in their order.  A tile's
+// warps are neighbours in their numbers: every block reads all headers and lists the ones that
+// began a tile.  A piece is one head of such a tile: a warp's where there are many, a block's,
+// each warp a part of the partials, where there are few.
+constexpr int kMaxWorkers = 1280, kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
+struct Joined {
+  float m, z, f, x[4];  // outputs relative to 2^m; the sum f 2^z
+};
+__device__ __forceinline__ Joined nothing() {
+  return Joined{-INFINITY, -INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+}
+__device__ __forceinline__ float finite_or_0(float x) { return x == -INFINITY ? 0.f : x; }
+
+template <int kD, int kN>
+__device__ __forceinline__ Joined join_parts(const Params& p, const Header* heads, int g0, int s0,
+                                             int s1, int col, int lane) {
+  Joined j = nothing();
+#pragma unroll 1
+  for (; s0 < s1; s0 += 32) {
+    const int s = s0 + lane;
+    const bool part = s < s1 && (s == g0 || heads[s].cont_some);
+    const int slot = (s == g0 ? 2 * s + 1 : 2 * s) * 8 * kN + col;
+    float4 ml = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+    if (part) ml = p.part_ml[slot];
+    const bool some = part && ml.z != 0.f;  // (a part that saw no page adds nothing)
+    const float m = fmaxf(j.m, warp_max(some ? ml.x : -INFINITY));
+    const float z = fmaxf(j.z, warp_max(some ? ml.y : -INFINITY));
+    const float ref = finite_or_0(m), zref = finite_or_0(z);
+    // square roots, taken twice; 0 before the first part
+    const float old = ex2_fast(0.5f * (j.m - ref)), zold = ex2_fast(0.5f * (j.z - zref));
+    // (no reference: a NaN sum, which stays one)
+    const float wgt = some ? ex2_fast(ml.x == -INFINITY ? 0.f : 0.5f * (ml.x - ref)) : 0.f;
+    const float zw = some ? ex2_fast(ml.y == -INFINITY ? 0.f : 0.5f * (ml.y - zref)) : 0.f;
+    j.f = j.f * zold * zold + warp_sum(some ? ml.z * zw * zw : 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) j.x[k] = j.x[k] * old * old;
+    j.m = m;
+    j.z = z;
+    unsigned todo = __ballot_sync(0xffffffffu, some);
+    while (todo) {
+      float v[4][4], wv[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {  // four partial rows on their way at once
+        const int i = todo ? __ffs(todo) - 1 : -1;
+        const int sl = __shfl_sync(0xffffffffu, slot, i & 31);
+        wv[u] = __shfl_sync(0xffffffffu, wgt, i & 31);
+        if (i < 0) wv[u] = 0.f;
+        const float* src = p.part_o + (long long)sl * kD + lane * (kD / 32);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[u][k] = 0.f;
+        if (i >= 0) {
+          if constexpr (kD == 128) {
+            const float4 f = __ldcs(reinterpret_cast<const float4*>(src));
+            v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
+          } else {
+            const float2 f = __ldcs(reinterpret_cast<const float2*>(src));
+            v[u][0] = f.x; v[u][1] = f.y;
+          }
+        }
+        todo &= todo - 1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) j.x[k] = fmaf(v[u][k] * wv[u], wv[u], j.x[k]);
+    }
+  }
+  return j;
+}
+template <int kD>
+__device__ __forceinline__ void store_joined(const Params& p, long long row, const Joined& j,
+                                             int lane) {
+  // (m - z: a whole part and a rest below 1)
+  const float d = j.f == 0.f || j.m == -INFINITY ? 0.f : j.m - j.z;
+  const float whole = fabsf(d) < 1000.f ? floorf(d) : 0.f;
+  const Factor by(j.f * ex2_fast(whole - d), (int)whole);
+  float x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = by(j.x[k]);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + row * kD + lane * (kD / 32);
+  if constexpr (kD == 128)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16(x[0], x[1]);
+  if (p.a.lse && lane == 0)
+    p.a.lse[row] = j.f == 0.f ? -INFINITY : (j.z + log2f(j.f)) / kLog2e;
+}
+
+template <int kD, int kN>
+__global__ void __launch_bounds__(kJoinThreads, 2) gqa_join_kernel(const Params p, int workers) {
+  __shared__ __align__(16) Header heads[kMaxWorkers];
+  __shared__ unsigned short begun[kMaxWorkers];
+  __shared__ int n_begun;
+  __shared__ Joined parts[kJoinWarps][32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < workers; i += kJoinThreads)
+    *reinterpret_cast<int4*>(heads + i) = *reinterpret_cast<const int4*>(p.head + i);
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0;
+    for (int s = 0; s < workers; s += 32) {
+      const bool hit = s + lane < workers && heads[s + lane].start_tile >= 0;
+      const unsigned all = __ballot_sync(0xffffffffu, hit);
+      if (hit) begun[n + __popc(all & ((1u << lane) - 1))] = (unsigned short)(s + lane);
+      n += __popc(all);
+    }
+    if (lane == 0) n_begun = n;
+  }
+  __syncthreads();
+  const int cols = min(8 * kN, p.G), pieces = n_begun * cols;
+  const bool wide = pieces <= 2 * (int)gridDim.x;  // a block a piece
+  const int step = wide ? gridDim.x : gridDim.x * kJoinWarps;
+#pragma unroll 1
+  for (int i = wide ? blockIdx.x : warp * gridDim.x + blockIdx.x; i < pieces; i += step) {
+    const int g0 = begun[i / cols], col = i % cols, tile = heads[g0].start_tile;
+    const int rows = p.a.kv.Hkv * p.hb, token = tile / rows, rest = tile - token * rows;
+    const int h = rest / p.hb, head = (rest - h * p.hb) * 8 * kN + col;
+    if (head >= p.G) continue;
+    const long long row = (long long)token * p.a.Hq + h * p.G + head;
+    int n = 1;  // its workers: g0 .. g0 + n - 1
+    for (unsigned stop = 0; !stop;) {
+      const int s = g0 + n + lane;
+      const Header hd = heads[min(s, workers - 1)];
+      const bool mine = s < workers && hd.cont_tile == tile;
+      stop = __ballot_sync(0xffffffffu, !mine || hd.cont_ends);
+      const int k = stop ? __ffs(stop) - 1 : 32;  // before the stopping one
+      n += k + (stop ? __shfl_sync(0xffffffffu, (int)mine, k & 31) : 0);
+    }
+    const int per = wide ? (n + kJoinWarps - 1) / kJoinWarps : n;
+    const int s0 = g0 + (wide ? min(n, warp * per) : 0);
+    const Joined j =
+        join_parts<kD, kN>(p, heads, g0, s0, min(s0 + per, g0 + n), col, lane);
+    if (!wide) {
+      store_joined<kD>(p, row, j, lane);
+      continue;
+    }
+    parts[warp][lane] = j;
+    __syncthreads();
+    if (warp == 0) {
+      Joined all = nothing();
+#pragma unroll
+      for (int u = 0; u < kJoinWarps; ++u) {
+        all.m = fmaxf(all.m, parts[u][lane].m);
+        all.z = fmaxf(all.z, parts[u][lane].z);
+      }
+      const float ref = finite_or_0(all.m), zref = finite_or_0(all.z);
+#pragma unroll
+      for (int u = 0; u < kJoinWarps; ++u) {
+        const Joined& x = parts[u][lane];
+        // (no reference: no part, or a NaN sum, which stays one)
+        const float e = x.m == -INFINITY ? 1.f : ex2_fast(0.5f * (x.m - ref));
+        const float ze = x.z == -INFINITY ? 1.f : ex2_fast(0.5f * (x.z - zref));
+        all.f = fmaf(x.f * ze, ze, all.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) all.x[k] = fmaf(x.x[k] * e, e, all.x[k]);
+      }
+      store_joined<kD>(p, row, all, lane);
+    }
+    __syncthreads();
+  }
+}
+
+// ---- launches ----------------------------------------------------------------------
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+// Rows of D codes (as 2-byte elements), boxes of box_rows of them.
+bool code_map(CUtensorMap* m, const void* base, uint64_t rows, int D, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D / 2, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)D};
+  const cuuint32_t box[2] = {(cuuint32_t)D / 2, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int workers_of() { return num_sms() * kW < kMaxWorkers ? num_sms() * kW : kMaxWorkers; }
+
+template <int kD, int kN, int kR>
+int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
+  Params p = {};
+  p.a = a;
+  p.G = a.Hq / a.kv.Hkv;
+  p.hb = (p.G + 8 * kN - 1) / (8 * kN);
+  p.zscale = a.sm_scale * kLog2e;
+  p.cap = table_cap(a.kv.max_pages, a.kv.page_size);
+  p.per_block = a.kv.page_size / kR;
+  const int grid = workers_of() / kW, workers = grid * kW;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float4*>(p.part_o + (size_t)workers * 2 * 8 * kN * kD);
+  p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)workers * 2 * 8 * kN);
+  CUtensorMap k_map, v_map;
+  const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.Hkv * a.kv.page_size;
+  if (!code_map(&k_map, a.kv.k_pages, rows, kD, kR) ||
+      !code_map(&v_map, a.kv.v_pages, rows, kD, kR))
+    return DSA_ERR_CUDA;
+  auto kernel = gqa_split_kernel<kD, kN, kR>;
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_smem(kernel, smem_bytes<kD>(), done)) return DSA_ERR_CUDA;
+  Launch l(dim3(grid, 1, 1), kThreads, smem_bytes<kD>(), stream);
+  if (launch_kernel(&l.cfg, kernel, k_map, v_map, p) != cudaSuccess) return DSA_ERR_CUDA;
+  Launch j(dim3(2 * num_sms(), 1, 1), kJoinThreads, 0, stream);
+  return launch_kernel(&j.cfg, gqa_join_kernel<kD, kN>, p, workers) == cudaSuccess ? DSA_OK
+                                                                                   : DSA_ERR_CUDA;
+}
+
+template <int kD, int kN>
+int launch_r(const GqaArgs& a, void* workspace, cudaStream_t stream) {
+  return a.kv.page_size % 32 == 0 ? launch<kD, kN, 32>(a, workspace, stream)
+                                  : launch<kD, kN, 16>(a, workspace, stream);
+}
+
+}  // namespace
+
+bool gqa_split_ok(int D, int dtype) { return dtype == DSA_BF16 && (D == 64 || D == 128); }
+
+size_t gqa_split_workspace_size(int Hq, int Hkv, int D) {
+  const size_t cols = Hq / Hkv <= 8 ? 8 : 16;
+  return (size_t)workers_of() * (2 * cols * (D * 4 + 16) + sizeof(Header));
+}
+
+int launch_gqa_split(const GqaArgs& a, void* workspace, cudaStream_t stream) {
+  const bool one = a.Hq / a.kv.Hkv <= 8;
+  if (a.kv.D == 128)
+    return one ? launch_r<128, 1>(a, workspace, stream) : launch_r<128, 2>(a, workspace, stream);
+  return one ? launch_r<64, 1>(a, workspace, stream) : launch_r<64, 2>(a, workspace, stream);
+}
+
+}  // namespace dsa
