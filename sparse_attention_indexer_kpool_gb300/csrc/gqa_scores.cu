@@ -4,7 +4,10 @@
 // with m_g, l_g the maximum and the sum of exp(z - m) over the candidates j < n: two passes
 // over the means, the first for m and l, the second for the sum over the group's heads.
 //
-// Generic kernel (any geometry and type): a CTA a token and KV head, a warp a block.
+// Two kernels: one on the tensor cores (bf16 queries, head dim 64 or 128, groups of up to 32
+// heads), and a generic one (any geometry and type), a CTA a token and KV head, a warp a block.
+#include <cooperative_groups.h>
+
 #include "gqa.cuh"
 
 namespace dsa {
@@ -45,6 +48,7 @@ __device__ __forceinline__ bool forced(const GqaScoreArgs& a, int mine, int j) {
   return j <= mine && (j < a.sink_blocks || (long long)j > (long long)mine - a.local_blocks);
 }
 
+// ---- generic ---------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kThreads) gqa_scores_kernel(GqaScoreArgs a) {
   extern __shared__ float sq[];  // [G][D], then the warps' maxima and sums [kWarps][G] each
@@ -127,10 +131,341 @@ __global__ void __launch_bounds__(kThreads) gqa_scores_kernel(GqaScoreArgs a) {
   }
 }
 
+// ---- tensor cores ------------------------------------------------------------------
+// The means of 16 blocks are the rows of a product, 8 kN (token, head) pairs of one
+// sequence and KV head its columns: z^T = K_mean Q^T, bf16 in, fp32 out.  Lane (g, t) of a warp
+// loads 16-byte pieces t, t + 4, .. of the rows g and g + 8 straight from memory and uses
+// them as they come; the queries' pieces, kept in registers, follow the same order.  A lane
+// then has two columns' z of its rows: it keeps their maximum and sum alone, and only at
+// the end of the first pass do lanes (and warps, and CTAs) exchange them.
+//   kOne: a warp takes such a group and all its blocks; the warps of a CTA take
+//     neighbouring tokens, whose rows they find in L1 (prompt chunks).
+//   otherwise the warps of a cluster's CTAs share the blocks of one token (decode), so
+//     that many SMs read one long context's means.
+// Bound by round trips to the table and the means (decode), by L1's bandwidth (chunks).
+constexpr int kPadG = 32;            // heads of a group, at most
+struct GroupArgs {
+  GqaScoreArgs a;
+  int pad;                           // G up to a power of two
+  int tokens;                        // of a group
+};
+
+template <int kD, int kN, bool kOne>
+__global__ void __launch_bounds__(kThreads)
+    gqa_scores_mma_kernel(const GroupArgs ga) {
+  constexpr int kSteps = kD / 16, kCols = 8 * kN;
+  __shared__ float2 s_part[kWarps][kCols];
+  __shared__ float2 s_cta[kCols];
+  pdl_wait();
+  pdl_launch_dependents();
+  const GqaScoreArgs& a = ga.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int h = blockIdx.y, G = a.Hq / a.Hkv;
+  namespace cg = cooperative_groups;
+  const int splits = kOne ? 1 : (int)cg::this_cluster().num_blocks();
+  const int rank = kOne ? 0 : (int)cg::this_cluster().block_rank();
+  if (blockIdx.x == 0 && h == 0)
+    for (int b = tid; b < a.B; b += kThreads)
+      if (a.cu_new[b] < 0 || a.cu_new[b + 1] < a.cu_new[b] || a.cu_new[b + 1] > a.T)
+        flag(a.status, DSA_DEV_BAD_LENGTH);
+  // the group: slots from floor(cu / tokens) + b on are sequence b's
+  const int slot = kOne ? (int)blockIdx.x * kWarps + warp : (int)blockIdx.x / splits;
+  auto first_slot = [&](int b) { return min(max(a.cu_new[b], 0), a.T) / ga.tokens + b; };
+  int b = 0;
+  for (int hi = a.B; hi - b > 1;) {
+    const int mid = (b + hi) >> 1;
+    if (first_slot(mid) <= slot) b = mid; else hi = mid;
+  }
+  const int c0 = min(max(a.cu_new[b], 0), a.T), n_new = min(a.cu_new[b + 1], a.T) - c0;
+  const int i0 = (slot - first_slot(b)) * ga.tokens;
+  if (i0 < 0 || i0 >= n_new) return;  // (all of a cluster's CTAs alike)
+  const int live = min(ga.tokens, n_new - i0);
+  const long long base = (long long)a.seq_lens[b] - n_new + i0;  // the first token's position
+  auto whole_at = [&](long long pos) {
+    return pos < 0 ? 0 : (int)min((long long)min(a.NB, a.max_pages), (pos + 1) / a.page_size);
+  };
+  const int most = whole_at(base + live - 1);  // candidates of the last token
+  if (h == 0 && rank == 0 && lane == 0 && (kOne || warp == 0)) {
+    if (base < 0) flag(a.status, DSA_DEV_BAD_LENGTH);
+    const long long last = (base + live - 1) / a.page_size;
+    if (base + live > 0 && last >= a.NB) flag(a.status, DSA_DEV_POOL_RANGE);
+    if (base + live > 0 && last >= a.max_pages) flag(a.status, DSA_DEV_BAD_PAGE);
+  }
+
+  // queries: lane (g, t) has column g of every n tile; candidates of columns 2 t, 2 t + 1
+  uint32_t q[kN][kSteps][2];
+  int cand[kN][2];
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    const int col = n * 8 + g, i = col / ga.pad, head = col - i * ga.pad;
+    const bool real = i < live && head < G;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(a.q) +
+        ((long long)(c0 + i0 + (real ? i : 0)) * a.Hq + (long long)h * G + (real ? head : 0)) * kD);
+#pragma unroll
+    for (int k = 0; k < kD / 32; ++k) {
+      const uint4 x = real ? __ldg(src + 4 * k + t) : make_uint4(0u, 0u, 0u, 0u);
+      q[n][2 * k][0] = x.x;
+      q[n][2 * k][1] = x.y;
+      q[n][2 * k + 1][0] = x.z;
+      q[n][2 * k + 1][1] = x.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = n * 8 + 2 * t + j, ic = c / ga.pad;
+      cand[n][j] = ic < live && c - ic * ga.pad < G ? whole_at(base + ic) : 0;
+    }
+  }
+  const float unit = a.sm_scale * kLog2e;
+  const int32_t* table = a.block_table + (long long)b * a.max_pages;
+  const int step = kOne ? 1 : kWarps * splits, first = kOne ? 0 : warp * splits + rank;
+  const int tiles = (most + 15) / 16;
+  // z (base 2) of the tile's blocks j0 + g and j0 + g + 8; -inf where there is no candidate
+  auto page_at = [&](int j) -> int {
+    if (j >= most) return -1;
+    const int page = __ldg(table + j);
+    return page >= 0 && page < a.n_pages ? page : -2;
+  };
+  auto scores_of = [&](int j0, int p0, int p1, float (&z)[kN][4]) {
+    uint4 x[kD / 32], y[kD / 32];
+    const uint4* k0 = reinterpret_cast<const uint4*>(
+        a.k_mean + ((long long)max(p0, 0) * a.Hkv + h) * kD);
+    const uint4* k1 = reinterpret_cast<const uint4*>(
+        a.k_mean + ((long long)max(p1, 0) * a.Hkv + h) * kD);
+#pragma unroll
+    for (int k = 0; k < kD / 32; ++k) {
+      x[k] = p0 >= 0 ? __ldg(k0 + 4 * k + t) : make_uint4(0u, 0u, 0u, 0u);
+      y[k] = p1 >= 0 ? __ldg(k1 + 4 * k + t) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[n][i] = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kD / 32; ++k)
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        mma_bf16_16816(z[n], x[k].x, y[k].x, x[k].y, y[k].y, q[n][2 * k][0], q[n][2 * k][1]);
+        mma_bf16_16816(z[n], x[k].z, y[k].z, x[k].w, y[k].w, q[n][2 * k + 1][0],
+                       q[n][2 * k + 1][1]);
+      }
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        z[n][i] = (i < 2 ? p0 : p1) >= 0 && j0 + g + (i < 2 ? 0 : 8) < cand[n][i & 1]
+                      ? z[n][i] * unit
+                      : -INFINITY;
+  };
+
+  // ---- first pass: maximum and sum of every column
+  float m[kN][2], l[kN][2];
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
+  }
+  bool missing = false;
+  int p0 = page_at(first * 16 + g), p1 = page_at(first * 16 + g + 8);
+#pragma unroll 1
+  for (int v = first; v < tiles; v += step) {
+    const int n0 = page_at((v + step) * 16 + g), n1 = page_at((v + step) * 16 + g + 8);
+    missing |= p0 == -2 || p1 == -2;
+    float z[kN][4];
+    scores_of(v * 16, p0, p1, z);
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float top = fmaxf(z[n][i], z[n][i + 2]);
+        if (top > m[n][i] + 24.f) {  // (a sum of 2^24 times as much still fits)
+          l[n][i] *= ex2_fast(m[n][i] - top);
+          m[n][i] = top;
+        }
+        const float ref = m[n][i] == -INFINITY ? 0.f : m[n][i];
+        l[n][i] += ex2_fast(z[n][i] - ref) + ex2_fast(z[n][i + 2] - ref);
+      }
+    p0 = n0;
+    p1 = n1;
+  }
+  if (missing) flag(a.status, DSA_DEV_BAD_PAGE);
+#pragma unroll
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float top = m[n][i];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = l[n][i] * (m[n][i] == -INFINITY ? 1.f : ex2_fast(m[n][i] - ref));
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      m[n][i] = ref;
+      l[n][i] = sum;
+      if (!kOne && g == 0) s_part[warp][n * 8 + 2 * t + i] = make_float2(top, sum);
+    }
+  if constexpr (!kOne) {
+    __syncthreads();
+    if (tid < kCols) {
+      float top = -INFINITY, sum = 0.f;
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_part[w][tid].x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 x = s_part[w][tid];
+        sum += x.y * (x.x == -INFINITY ? 1.f : ex2_fast(x.x - ref));
+      }
+      s_cta[tid] = make_float2(top, sum);
+    }
+    cg::this_cluster().sync();
+    if (tid < kCols) {
+      float top = -INFINITY, sum = 0.f;
+      for (int r = 0; r < splits; ++r)
+        top = fmaxf(top, cg::this_cluster().map_shared_rank(s_cta, r)[tid].x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      for (int r = 0; r < splits; ++r) {
+        const float2 x = cg::this_cluster().map_shared_rank(s_cta, r)[tid];
+        sum += x.y * (x.x == -INFINITY ? 1.f : ex2_fast(x.x - ref));
+      }
+      s_part[0][tid] = make_float2(ref, sum);
+    }
+    cg::this_cluster().sync();  // (nobody leaves while its sums are read)
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 x = s_part[0][n * 8 + 2 * t + i];
+        m[n][i] = x.x;
+        l[n][i] = x.y;
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = n * 8 + 2 * t + i, ic = c / ga.pad;
+      // (a column that is none adds nothing; without a candidate no weight is looked at)
+      l[n][i] = ic < live && c - ic * ga.pad < G ? 1.f / l[n][i] : 0.f;
+      if (l[n][i] == INFINITY) l[n][i] = 0.f;
+    }
+
+  // ---- second pass: weights, summed over a token's heads
+  p0 = page_at(first * 16 + g);
+  p1 = page_at(first * 16 + g + 8);
+#pragma unroll 1
+  for (int v = first; v < (a.NB + 15) / 16; v += step) {
+    const int n0 = page_at((v + step) * 16 + g), n1 = page_at((v + step) * 16 + g + 8);
+    float z[kN][4];
+    if (v < tiles) {
+      scores_of(v * 16, p0, p1, z);
+    } else {
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[n][i] = -INFINITY;
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[n][i] = ex2_fast(z[n][i] - m[n][i & 1]) * l[n][i & 1];
+    // sums over a token's columns: first of a lane's two, of its neighbours', of n tiles
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      if (ga.pad >= 2) {
+        z[n][0] += z[n][1];
+        z[n][2] += z[n][3];
+      }
+      if (ga.pad >= 4) {
+        z[n][0] += __shfl_xor_sync(0xffffffffu, z[n][0], 1);
+        z[n][2] += __shfl_xor_sync(0xffffffffu, z[n][2], 1);
+      }
+      if (ga.pad >= 8) {
+        z[n][0] += __shfl_xor_sync(0xffffffffu, z[n][0], 2);
+        z[n][2] += __shfl_xor_sync(0xffffffffu, z[n][2], 2);
+      }
+    }
+    if constexpr (kN >= 2)
+      if (ga.pad >= 16) {
+#pragma unroll
+        for (int n = 0; n < kN; n += 2) {
+          z[n][0] += z[n + 1][0];
+          z[n][2] += z[n + 1][2];
+        }
+      }
+    if constexpr (kN >= 4)
+      if (ga.pad >= 32) {
+        z[0][0] += z[2][0];
+        z[0][2] += z[2][2];
+      }
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = n * 8 + 2 * t + i, ic = c / ga.pad;
+        if (ic >= live || c != ic * ga.pad) continue;  // a token's first column writes
+        const long long pos = base + ic;
+        const int mine = pos < 0 ? -1 : (int)(pos / a.page_size);
+        float* out = a.scores + ((long long)(c0 + i0 + ic) * a.Hkv + h) * a.NB;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int j = v * 16 + g + 8 * r, page = r ? p1 : p0;
+          if (j >= a.NB) continue;
+          out[j] = forced(a, mine, j) ? INFINITY
+                   : page >= 0 && j < cand[n][i] ? z[n][2 * r + i]
+                                                 : -INFINITY;
+        }
+      }
+    p0 = n0;
+    p1 = n1;
+  }
+}
+
+template <int kD, int kN, bool kOne>
+int launch_mma(const GroupArgs& ga, int splits, cudaStream_t stream) {
+  const unsigned slots = (unsigned)(ga.a.T / ga.tokens + ga.a.B);
+  const unsigned grid = kOne ? (slots + kWarps - 1) / kWarps : slots * splits;
+  Launch l(dim3(grid, ga.a.Hkv, 1), kThreads, 0, stream);
+  cudaLaunchAttribute attr[2];
+  if (!kOne) {
+    attr[0] = l.attr;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    l.cfg.attrs = attr;
+    l.cfg.numAttrs = 2;
+  }
+  return launch_kernel(&l.cfg, gqa_scores_mma_kernel<kD, kN, kOne>, ga) == cudaSuccess
+             ? DSA_OK
+             : DSA_ERR_CUDA;
+}
+
+template <int kD>
+int launch_groups(const GqaScoreArgs& a, cudaStream_t stream) {
+  GroupArgs ga{a, 1, 1};
+  const int G = a.Hq / a.Hkv;
+  while (ga.pad < G) ga.pad *= 2;
+  // a warp a group where that is work for every SM's warps, with as many tokens as four n
+  // tiles take
+  const long long rows = (long long)a.T * a.Hkv;
+  const int tokens = 32 / ga.pad;
+  if (rows / tokens >= 2ll * num_sms() * kWarps) {
+    ga.tokens = tokens;
+    return launch_mma<kD, 4, true>(ga, 1, stream);
+  }
+  // otherwise CTAs for a token until there are two an SM, each with 64 blocks at least
+  int splits = 1;
+  while (splits < 8 && rows * splits < num_sms() && a.NB >= 128 * splits) splits *= 2;
+  if (ga.pad <= 8) return launch_mma<kD, 1, false>(ga, splits, stream);
+  if (ga.pad <= 16) return launch_mma<kD, 2, false>(ga, splits, stream);
+  return launch_mma<kD, 4, false>(ga, splits, stream);
+}
+
 }  // namespace
 
 int launch_gqa_scores(const GqaScoreArgs& a, int dtype, cudaStream_t stream) {
   const int G = a.Hq / a.Hkv;
+  if (dtype == DSA_BF16 && G <= kPadG && a.D == 128) return launch_groups<128>(a, stream);
+  if (dtype == DSA_BF16 && G <= kPadG && a.D == 64) return launch_groups<64>(a, stream);
   auto kernel = dtype == DSA_BF16 ? gqa_scores_kernel<__nv_bfloat16> : gqa_scores_kernel<float>;
   static std::atomic<unsigned long long> done[2];
   constexpr size_t kMost = (size_t)(kMaxG * 256 + 2 * kWarps * kMaxG) * sizeof(float);
