@@ -427,6 +427,9 @@ int launch_gqa_attend(const GqaArgs& a, void* workspace, cudaStream_t stream);
 bool gqa_split_ok(int D, int dtype);
 size_t gqa_split_workspace_size(int Hq, int Hkv, int D);
 int launch_gqa_split(const GqaArgs& a, void* workspace, cudaStream_t stream);
+// its tcgen05 form for chunks of new tokens (no block lists), the same types
+size_t gqa_chunk_workspace_size(int D);
+int launch_gqa_chunk(const GqaArgs& a, void* workspace, cudaStream_t stream);
 }  // namespace dsa
 
 #define DSA_LAUNCH_CHECK()                          \

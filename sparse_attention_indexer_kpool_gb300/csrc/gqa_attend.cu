@@ -167,11 +167,15 @@ __global__ void __launch_bounds__(kThreads) gqa_attend_simt_kernel(GqaArgs a) {
 }  // namespace
 
 size_t gqa_attend_workspace_size(int, int Hq, int Hkv, int D, int dtype) {
-  return gqa_split_ok(D, dtype) ? gqa_split_workspace_size(Hq, Hkv, D) : 0;
+  if (!gqa_split_ok(D, dtype)) return 0;
+  const size_t one = gqa_split_workspace_size(Hq, Hkv, D), two = gqa_chunk_workspace_size(D);
+  return one > two ? one : two;
 }
 
 int launch_gqa_attend(const GqaArgs& a, void* workspace, cudaStream_t stream) {
-  if (gqa_split_ok(a.kv.D, a.dtype)) return launch_gqa_split(a, workspace, stream);
+  if (gqa_split_ok(a.kv.D, a.dtype))
+    return !a.block_ids && a.T >= 8ll * a.B ? launch_gqa_chunk(a, workspace, stream)
+                                            : launch_gqa_split(a, workspace, stream);
   const int G = a.Hq / a.kv.Hkv;
   auto kernel =
       a.dtype == DSA_BF16 ? gqa_attend_simt_kernel<__nv_bfloat16> : gqa_attend_simt_kernel<float>;

@@ -180,7 +180,8 @@ template <>
 __device__ __forceinline__ void store16<float>(float* p, const float (&x)[16]) {
   float4* o = reinterpret_cast<float4*>(p);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  for (int i = 0; i < 4; ++i)
+    o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
 }
 
 template <typename T>

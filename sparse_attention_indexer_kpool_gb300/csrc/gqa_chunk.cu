@@ -1,0 +1,903 @@
+// Attention of a grouped-query layer over the paged 8-bit cache, for chunks of many new
+// tokens (bf16 activations, head dim 64 or 128): tcgen05 products of 128 query rows and 128
+// keys.
+//
+// A row tile is 128 / G tokens of a sequence with the G query heads of one KV head: up to 128
+// rows.  An item is two of them, A and B, one behind the other; a CTA runs through its equal
+// share of the batch's (item, tile of 128 keys) units.  Per tile, for A and B in turn:
+//   S = Q C_k^T                   fp16 in, fp32 out in tensor memory
+//   e = S * (query scale * key scale * softmax scale) + lv - m,  w = 2^e
+//   O += W C_v                    W as the first factor in tensor memory, where S was
+// with the codes C widened to fp16 (exact), the query rows scaled by a power of two, lv the
+// exponent of the values' scale and m a row's reference, all as in the kernel for decode
+// tokens (weights times 2^8; the sums, of 2^(z - m + B), in fp32).
+//
+// Roles (a thread of the softmax has a whole row, so that no reduction crosses threads):
+//   warps 0 - 3, 4 - 7   softmax of A, of B: S from tensor memory, W back to it
+//   warps 8 - 11         widen the codes into the 128-byte swizzled fp16 tiles
+//   warp 12              TMA of the codes (16 KB of keys, 16 KB of values a tile)
+//   warp 13              the products: O of the last tile, then S of this one, A before B,
+//                        so that the tensor cores have B's while A's softmax runs
+// A row's reference stays until a sum of 16 of its weights passes 2^15 (half of fp16's
+// largest): only then, and at a row's first tile, is a maximum looked for.
+//
+// What no row may see is masked, and its values are zeros in the tile.  Keys that some rows of an
+// item see and others do not (the diagonal, a window's edge) may hold NaN codes in their
+// values: those are zeros in the tile too, and the rows that see them remember which columns
+// they make NaN.
+#include "gqa.cuh"
+#include "gqa_join.cuh"
+#include "mla_chunk.cuh"
+#include "umma.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace gqa;
+using chunk::add2;
+using chunk::fma2;
+using chunk::wait_on;
+
+constexpr int kRows = 128, kKeys = 128, kGroups = kKeys / 16;
+constexpr int kSoft = 256, kWiden = 128;
+constexpr int kWidenWarp = kSoft / 32, kTmaWarp = kWidenWarp + kWiden / 32,
+              kMmaWarp = kTmaWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1), kWarps = kThreads / 32;
+constexpr int kMetas = 4;
+constexpr float kFull = 32768.f;       // a sum of 16 weights above which a reference is raised
+constexpr int kExtra = 2;              // what an item costs beside its tiles, in tiles
+
+struct Params {
+  GqaArgs a;
+  int G, per;          // query heads of a KV head; tokens of a row tile
+  float zscale;        // softmax scale in base 2
+  int cap;             // positions that the block table has room for
+  int box_log;         // keys of a TMA box
+  float* part_o;       // [2 CTAs][2 kRows][D]
+  float4* part_ml;     // [2 CTAs][2 kRows]: reference; the sum f 2^z as z and f
+  Header* head;
+  int drill;
+};
+
+// ---- the batch as units ---------------------------------------------------------
+struct Seq {
+  int c0, n, base;     // rows c0 .. c0 + n - 1 of the step; position of the first
+  unsigned u;          // key tiles of an item, at most, and kExtra
+};
+__device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p) {
+  Seq s;
+  s.c0 = min(max(cu0, 0), p.a.T);
+  s.n = max(min(cu1, p.a.T) - s.c0, 0);
+  s.base = len < 0 ? -s.n : len - s.n;  // negative: rows before position 0
+  const unsigned all = (unsigned)min(max(len, 0), p.cap);
+  s.u = (all + kKeys - 1) / kKeys;
+  if (p.a.window > 0) {
+    const long long R = 1 << p.box_log;
+    const long long span = (long long)p.a.window + 2 * p.per - 1;
+    const long long keys = ((p.a.sinks + R - 1) / R + (R - 2 + span) / R + 1) * R;
+    if ((keys + kKeys - 1) / kKeys < (long long)s.u) s.u = (unsigned)((keys + kKeys - 1) / kKeys);
+  }
+  s.u = max(s.u, 1u) + kExtra;
+  return s;
+}
+__device__ __forceinline__ unsigned items_of(const Seq& s, const Params& p) {
+  return ((unsigned)s.n + 2 * p.per - 1) / (2 * p.per) * p.a.kv.Hkv;
+}
+
+struct Start {
+  unsigned long long n;
+  int b;
+  unsigned item, unit;
+};
+struct Walk {
+  const Params& p;
+  unsigned long long left;
+  int b;
+  unsigned item, unit;
+  Seq s;
+  int token, tokens, h, id, ta, tb, n;        // the segment: tiles [ta, tb) of n
+  int pos0, pos1;                             // positions of its first and last token
+  int lo, s0, first, sink_boxes, boxes;       // the keys that any of them sees
+
+  __device__ __forceinline__ Walk(const Params& pp, const Start& st)
+      : p(pp), left(st.b < pp.a.B ? st.n : 0), b(st.b), item(st.item), unit(st.unit) {
+    if (left > 0) load();
+  }
+  __device__ __forceinline__ void load() {
+    s = seq_of(__ldg(p.a.cu_new + b), __ldg(p.a.cu_new + b + 1), __ldg(p.a.kv.seq_lens + b), p);
+  }
+  __device__ __forceinline__ bool next() {
+    if (left == 0) return false;
+    while (item >= items_of(s, p)) {
+      if (++b >= p.a.B) return false;  // (lengths that changed under the call)
+      load();
+      item = 0;
+    }
+    const unsigned e = left < s.u - unit ? unit + (unsigned)left : s.u;
+    const int Hkv = p.a.kv.Hkv, pair = 2 * p.per, count = (s.n + pair - 1) / pair;
+    const int k = (int)(item / Hkv);
+    h = (int)(item - (unsigned)k * Hkv);
+    // groups are taken from both ends in turn: a share of a long prompt's units is then its
+    // share of the work
+    const int i = ((k & 1) ? count - 1 - (k >> 1) : k >> 1) * pair;
+    token = s.c0 + i;
+    tokens = min(pair, s.n - i);
+    id = token * Hkv + h;
+    pos0 = s.base + i;
+    pos1 = pos0 + tokens - 1;
+    const int end = min(pos1, p.cap - 1);
+    lo = p.a.window > 0 ? max(0, max(pos0, -1) - p.a.window + 1) : 0;
+    s0 = min(min(p.a.sinks, lo), p.cap);
+    first = lo >> p.box_log;
+    sink_boxes = min((s0 + (1 << p.box_log) - 1) >> p.box_log, first);
+    boxes = end < 0 ? 0 : sink_boxes + max((end >> p.box_log) - first + 1, 0);
+    const unsigned per_tile = kKeys >> p.box_log;
+    n = (int)(((unsigned)boxes + per_tile - 1) / per_tile);
+    ta = share_of(unit, n, s.u);
+    tb = share_of(e, n, s.u);
+    left -= e - unit;
+    unit = e;
+    if (e == s.u) {
+      unit = 0;
+      ++item;
+    }
+    return true;
+  }
+  static __device__ __forceinline__ int share_of(unsigned a, int n, unsigned u) {
+    if (a == 0) return 0;
+    if (a == u) return n;
+    return (int)((unsigned long long)a * (unsigned)n / u);
+  }
+};
+
+struct Meta {          // of a key tile, by 16 keys
+  int pos[kGroups];    // first position (0x7fffffff: none)
+  float ks[kGroups];   // keys' scale
+  int ev[kGroups];     // exponent of the values' scale
+  int row[kGroups];    // first cache row
+  uint32_t nan[4];     // keys whose NaN values were taken out of the tile
+  int partial;         // not every row of the item sees every key
+};
+struct Ctl {
+  uint64_t raw_full[2], raw_empty[2];      // codes of keys, of values
+  uint64_t wide_full[2][2], wide_empty[2][2];  // [stage][keys, values]
+  uint64_t s_full[2], p_full[2], o_full[2], q_full[2], q_empty, drain;
+  Meta meta[kMetas];
+  Start start;
+  unsigned long long scan[kWarps];
+  uint32_t tmem;
+  int dead;
+};
+
+template <int kD>
+struct Smem {
+  static constexpr int kAtoms = kD / 64, kAtom = 128 * 128;  // 128 rows of 64 fp16
+  static constexpr int kTile = kAtoms * kAtom, kRaw = kKeys * kD;
+  static constexpr size_t kQ = 0, kWide = 2 * (size_t)kTile;         // [stage][keys, values]
+  static constexpr size_t kCodes = kWide + 4 * (size_t)kTile;
+  static constexpr size_t kCtl = kCodes + 2 * (size_t)kRaw;
+  static constexpr size_t kBytes = 1024 + kCtl + sizeof(Ctl);
+};
+static_assert(Smem<128>::kBytes <= 227 * 1024, "shared memory budget");
+
+// The share of this CTA.  Ends with a barrier.
+__device__ __forceinline__ void find_share(const Params& p, Ctl& c) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.a.B;
+  const int per = (B + kThreads - 1) / kThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  if (tid == 0) c.start.b = B;
+  unsigned long long mine = 0;
+  bool odd = false, past = false, falls = false;
+  for (int b = b0; b < b1; ++b) {
+    const int cu0 = p.a.cu_new[b], cu1 = p.a.cu_new[b + 1], len = p.a.kv.seq_lens[b];
+    const Seq s = seq_of(cu0, cu1, len, p);
+    odd |= cu0 < 0 || cu1 < cu0 || cu1 > p.a.T || (s.n > 0 && s.base < 0);
+    past |= s.n > 0 && len > p.cap;
+    falls |= cu1 < cu0;
+    mine += (unsigned long long)items_of(s, p) * s.u;
+  }
+  if (blockIdx.x == 0) {
+    if (odd) flag(p.a.status, DSA_DEV_BAD_LENGTH);
+    if (past) flag(p.a.status, DSA_DEV_BAD_PAGE);
+  }
+  unsigned long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) c.scan[warp] = inc;
+  // rows of several sequences at once (the work would have no bound): nothing is done
+  falls = __syncthreads_or(falls);
+  unsigned long long before = inc - mine, total = 0, v0, v1;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += c.scan[w];
+    total += c.scan[w];
+  }
+  if (falls) total = 0;
+  const unsigned me = blockIdx.x, workers = gridDim.x;
+  if (total < workers) {
+    v0 = me < total ? me : total;
+    v1 = me < total ? me + 1 : total;
+  } else {
+    v0 = total * me / workers;
+    v1 = total * (me + 1) / workers;
+  }
+  if (v0 < v1 && v0 >= before && v0 < before + mine) {
+    unsigned long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = seq_of(p.a.cu_new[b], p.a.cu_new[b + 1], p.a.kv.seq_lens[b], p);
+      const unsigned long long all = (unsigned long long)items_of(s, p) * s.u;
+      if (v0 < at + all) {
+        const unsigned long long off = v0 - at;
+        c.start.b = b;
+        c.start.item = (unsigned)(off / s.u);
+        c.start.unit = (unsigned)(off - (unsigned long long)c.start.item * s.u);
+        c.start.n = v1 - v0;
+        break;
+      }
+      at += all;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+
+// ---- small pieces -----------------------------------------------------------------
+// Instruction descriptor, kind::f16: fp32 accumulator, fp16 A and B.
+constexpr uint32_t idesc_f16(int m, int n, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(m >> 4) << 24);
+}
+// A from tensor memory; run by a converged warp, one elected lane issues
+__device__ __forceinline__ void umma_f16_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t accumulate) {
+  umma_bf16_elect(d, a, b, idesc, accumulate);  // (the types stand in the descriptor)
+}
+__device__ __forceinline__ void umma_tmem_a_elect(uint32_t d, uint32_t a, uint64_t b,
+                                                  uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// 16 consecutive columns of the warp's 32 TMEM lanes: the load, and the wait behind which its
+// values may be used.
+__device__ __forceinline__ void tmem_ld16_start(uint32_t ta, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(ta));
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+// Store 8 consecutive columns of the warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_st8(uint32_t ta, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+template <int kD>
+__global__ void __launch_bounds__(kThreads, 1)
+    gqa_chunk_kernel(const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map, const Params p) {
+  using S = Smem<kD>;
+  constexpr int kTmem = 512, kOCol = 256;   // S of A at 0, of B at 128; O of A at 256, B at 384
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  unsigned char* sb = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl& c = *reinterpret_cast<Ctl*>(sb + S::kCtl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const GqaKv& kv = p.a.kv;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.raw_full[i], 1);
+      mbar_init(&c.raw_empty[i], kWiden / 32);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&c.wide_full[i][j], kWiden / 32);
+        mbar_init(&c.wide_empty[i][j], 1);
+      }
+      mbar_init(&c.s_full[i], 1);
+      mbar_init(&c.p_full[i], 4);
+      mbar_init(&c.o_full[i], 1);
+      mbar_init(&c.q_full[i], 4);
+    }
+    mbar_init(&c.q_empty, 1);
+    mbar_init(&c.drain, 1);
+    fence_mbar_init();
+    c.dead = 0;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc<kTmem>(&c.tmem);
+    tc_fence_before();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  find_share(p, c);
+  const uint32_t tmem = c.tmem;
+  Walk w(p, c.start);
+  const bool issue = p.drill == 0;  // a failure drill loads and multiplies nothing
+  const unsigned long long wait_ns = p.drill ? kDrillWaitNs : kWaitNs;
+  volatile int* dead = &c.dead;
+
+  if (warp < kWidenWarp) {
+    // ================= softmax: a thread a row of A or B =================
+    const int ab = warp >> 2, r = tid & (kRows - 1);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + ab * 128, to = tmem + lanes + kOCol + ab * 128;
+    const int my = r / p.G, g = r - my * p.G;
+    Header hd = {-1, -1, 0, 0};
+    int tiles = 0, segs = 0;      // key tiles and segments so far
+    int mine = 0, outs = 0;       // those of this row tile
+    bool ok = true;
+    while (ok && w.next()) {
+      const bool some = w.tb > w.ta, whole = w.ta == 0 && w.tb == w.n;
+      const bool begins = some && w.ta == 0 && !whole;
+      if (begins) {
+        hd.start_item = w.id;
+        hd.tokens = w.tokens;
+      }
+      if (!whole && !begins && hd.cont_item < 0) {
+        hd.cont_item = w.id;
+        hd.cont = (some ? 1 : 0) | (w.tb == w.n ? 2 : 0);
+      }
+      if (!some && !whole) continue;
+      const int i = ab * p.per + my;              // this row's token of the item
+      const bool real = my < p.per && i < w.tokens;
+      const bool used = ab == 0 || w.tokens > p.per;
+      const long long row = (long long)(w.token + i) * p.a.Hq + w.h * p.G + g;
+      if (!some) {  // nothing seen
+        if (real) {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + row * kD);
+          for (int k = 0; k < kD / 8; ++k) out[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.a.lse) p.a.lse[row] = -INFINITY;
+        }
+        continue;
+      }
+      // the query row, once the last segment's products with this place are done
+      if (segs > 0 && !wait_on(&c.q_empty, (segs - 1) & 1, dead, wait_ns)) ok = false;
+      ++segs;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (!used) {
+        tiles += w.tb - w.ta;
+        continue;
+      }
+      float qs;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(p.a.q) + (real ? row : 0) * kD);
+        float top = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < kD / 8; ++k) {
+          const uint4 x = __ldg(src + k);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float a = fabsf(bf16lo(u[j])), b = fabsf(bf16hi(u[j]));
+            if (a < INFINITY) top = fmaxf(top, a);
+            if (b < INFINITY) top = fmaxf(top, b);
+          }
+        }
+        const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -126), half = (14 - ex) >> 1;
+        const float up0 = pow2(half), up1 = pow2(14 - ex - half);
+        qs = pow2(-half) * pow2(half + ex - 14) * p.zscale;
+        unsigned char* dst = sb + S::kQ + ab * S::kTile + r * 128;
+#pragma unroll 4
+        for (int k = 0; k < kD / 8; ++k) {
+          const uint4 x = __ldg(src + k);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+          uint32_t y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // a NaN or an infinity becomes NaN: its row's logits are NaN
+            float a = bf16lo(u[j]) * up0 * up1, b = bf16hi(u[j]) * up0 * up1;
+            a = fabsf(a) < INFINITY ? a : NAN;
+            b = fabsf(b) < INFINITY ? b : NAN;
+            y[j] = real ? pack_f16(a, b) : 0u;
+          }
+          *reinterpret_cast<uint4*>(dst + (k >> 3) * S::kAtom + (((k & 7) ^ (r & 7)) << 4)) =
+              make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&c.q_full[ab]);
+
+      const int pos = real ? min(w.pos0 + i, p.cap - 1) : -1;
+      const int lo = p.a.window > 0 ? max(0, max(w.pos0 + i, -1) - p.a.window + 1) : 0;
+      const int s0 = min(p.a.sinks, lo);
+      float m = -INFINITY, l = 0.f;
+      int base = 0;
+      uint32_t bad[kD / 32] = {};  // columns that a NaN value reached by the long way
+#pragma unroll 1
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        ok = wait_on(&c.s_full[ab], mine++ & 1, dead, wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        Meta& mt = c.meta[tiles % kMetas];
+        const bool partial = mt.partial != 0;
+        // exponents of 16 weights, of group q
+        auto exponents = [&](int q, const uint32_t (&s)[16], float (&e)[16]) {
+          const float zs = qs * mt.ks[q];
+          const float off = (float)(mt.ev[q] + kUp) - (m == -INFINITY ? 0.f : m);
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            e[k] = __uint_as_float(s[k]);
+            e[k + 1] = __uint_as_float(s[k + 1]);
+            fma2(e[k], e[k + 1], zs, off, off);
+          }
+          if (partial) {
+            const long long p0 = mt.pos[q];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const long long t = p0 + k;
+              if (!(t <= pos && (t >= lo || t < s0))) e[k] = -INFINITY;
+            }
+          }
+        };
+        // A new reference from the tile's largest exponent, where that lies above the present one;
+        // the row's sum and outputs follow.
+        auto raise = [&]() {
+          float top = -INFINITY;
+          int lv = 0;
+#pragma unroll 1
+          for (int q = 0; q < kGroups; ++q) {
+            uint32_t s[16];
+            float e[16];
+            tmem_ld16_start(ts + q * 16, s);
+            tmem_ld_wait(s);
+            exponents(q, s, e);
+            float t = e[0];
+#pragma unroll
+            for (int k = 1; k < 16; ++k) t = fmaxf(t, e[k]);
+            if (t > top) {
+              top = t;
+              lv = mt.ev[q] + kUp;
+            }
+            __syncwarp();
+          }
+          const float rel = top - (float)kUp;
+          float a = 1.f;
+          if (m == -INFINITY) {  // nothing accumulated for this row yet
+            if (rel != -INFINITY) {
+              m = rel;
+              base = lv;
+            }
+          } else if (rel > 0.f) {
+            m += rel;
+            // (square roots, taken twice: weights may lie further apart than a float reaches)
+            a = ex2_fast(-0.5f * rel);
+            int next = lv;
+            if ((float)(lv - base) - rel > 60.f) next = (int)floorf((float)base + rel + 60.f);
+            const float f = ex2_fast(0.5f * ((float)(next - base) - rel));
+            base = next;
+            l = l * f * f;
+          }
+          if (v > w.ta && __any_sync(0xffffffffu, a != 1.f)) {
+#pragma unroll 1
+            for (int k = 0; k < kD / 16; ++k) {
+              float o[16];
+              tmem_ld16(to + k * 16, o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = o[j] * a * a;
+              chunk::tmem_st16(to + k * 16, o);
+            }
+          }
+        };
+        if (__any_sync(0xffffffffu, m == -INFINITY)) raise();
+        // The weights stay in registers until the scores are no longer needed: where one was too
+        // large, all are taken again after a raise.
+        uint32_t wt[kGroups][8];
+        float sum;
+#pragma unroll 1
+        for (int turn = 0;; ++turn) {
+          bool high = false;
+          sum = 0.f;
+          uint32_t raw[2][16];
+          tmem_ld16_start(ts, raw[0]);
+#pragma unroll
+          for (int q = 0; q < kGroups; ++q) {
+            tmem_ld_wait(raw[q & 1]);
+            if (q + 1 < kGroups) tmem_ld16_start(ts + (q + 1) * 16, raw[(q + 1) & 1]);
+            float e[16];
+            exponents(q, raw[q & 1], e);
+            const int d = base - (mt.ev[q] + kUp);
+            const bool far = __any_sync(0xffffffffu, d > 64);  // a scale far below the reference's
+            if (far) {
+              float top = e[0];
+#pragma unroll
+              for (int k = 1; k < 16; ++k) top = fmaxf(top, e[k]);
+              float by = (float)d;
+              if (top + by > 100.f) {
+                base -= 100;
+                by -= 100.f;
+                l *= 0x1p-100f;
+                sum *= 0x1p-100f;
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) sum += ex2_fast(e[k] + by);
+              __syncwarp();
+            }
+            float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              e[k] = ex2_fast(e[k]);
+              e[k + 1] = ex2_fast(e[k + 1]);
+              add2(a0, a1, e[k], e[k + 1]);
+              wt[q][k / 2] = pack_f16(e[k], e[k + 1]);
+            }
+            high |= a0 + a1 > kFull;
+            if (!far) sum = fmaf(a0 + a1, pow2(max(d, -126)), sum);
+          }
+          if (turn > 0 || !__any_sync(0xffffffffu, high)) break;
+          raise();
+        }
+        l += sum;
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) tmem_st8(ts + q * 8, wt[q]);
+        tmem_st_wait();
+        if (partial) {
+          // (before the weights are handed on: the tile's values stay where they are till then)
+          ok = wait_on(&c.wide_full[tiles & 1][1], (tiles >> 1) & 1, dead, wait_ns);
+          if (ok) {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q)
+#pragma unroll 1
+              for (uint32_t left = mt.nan[q]; left; left &= left - 1) {
+                const int k = q * 32 + __ffs(left) - 1;
+                const long long t = (long long)mt.pos[k >> 4] + (k & 15);
+                if (!(t <= pos && (t >= lo || t < s0))) continue;
+                const uint8_t* codes = kv.v_pages + ((long long)mt.row[k >> 4] + (k & 15)) * kD;
+#pragma unroll 1
+                for (int d = 0; d < kD; ++d)
+                  if ((codes[d] & 0x7f) == 0x7f) {
+#pragma unroll
+                    for (int j = 0; j < kD / 32; ++j)
+                      if (j == (d >> 5)) bad[j] |= 1u << (d & 31);
+                  }
+              }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&c.p_full[ab]);
+      }
+      if (!ok) break;
+
+      // the segment's end
+      ok = wait_on(&c.o_full[ab], outs & 1, dead, wait_ns);
+      ++outs;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      int ex = 0;
+      const float f = fabsf(l) < INFINITY ? frexpf(l, &ex) : l;
+      const float z = m + (float)(ex - base);  // the sum is f 2^z
+      const Factor by(f, base - ex);
+      const int slot = (2 * blockIdx.x + (begins ? 1 : 0)) * (2 * kRows) + ab * kRows + r;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + row * kD;
+      float* part = p.part_o + (long long)slot * kD;
+#pragma unroll
+      for (int k = 0; k < kD / 16; ++k) {
+        float o[16];
+        __syncwarp();
+        tmem_ld16(to + k * 16, o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if ((bad[k / 2] >> ((k & 1) * 16 + j)) & 1u) o[j] = NAN;
+        if (!real) continue;
+        if (whole) {
+          uint32_t y[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = pack_bf16(by(o[2 * j]), by(o[2 * j + 1]));
+          reinterpret_cast<uint4*>(out)[2 * k] = make_uint4(y[0], y[1], y[2], y[3]);
+          reinterpret_cast<uint4*>(out)[2 * k + 1] = make_uint4(y[4], y[5], y[6], y[7]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            reinterpret_cast<float4*>(part)[4 * k + j] =
+                make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      }
+      if (real) {
+        if (!whole)
+          p.part_ml[slot] = make_float4(m, z, f, 0.f);
+        else if (p.a.lse)
+          p.a.lse[row] = l == 0.f ? -INFINITY : (z + log2f(f)) / kLog2e;
+      }
+      tc_fence_before();  // O is read: the next segment's first weights release it
+    }
+    if (!ok) hd = Header{-1, -1, 0, 0};
+    if (tid == 0) p.head[blockIdx.x] = hd;
+  } else if (warp < kTmaWarp) {
+    // ================= widen the codes =================
+    const int ww = warp - kWidenWarp, z = lane >> 3, cc = lane & 3;
+    int tiles = 0;
+    bool ok = issue;
+    while (ok && w.next()) {
+      const int end = min(w.pos1, p.cap - 1);
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        const int st = tiles & 1;
+        Meta& mt = c.meta[tiles % kMetas];
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+          ok = wait_on(&c.raw_full[kind], tiles & 1, dead, wait_ns) &&
+               (tiles < 2 ||
+                wait_on(&c.wide_empty[st][kind], ((tiles >> 1) & 1) ^ 1, dead, wait_ns));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const bool partial = kind == 1 && mt.partial != 0;
+          const unsigned char* raw = sb + S::kCodes + kind * S::kRaw;
+          unsigned char* wide = sb + S::kWide + (2 * st + kind) * S::kTile;
+#pragma unroll 4
+          for (int i = ww; i < 16 * S::kAtoms; i += kWiden / 32) {
+            // eight lanes: four 16-byte pieces of the rows r and r ^ 5, whose places in both
+            // tiles share no bank
+            const int half = i % S::kAtoms;
+            const int r = i / S::kAtoms * 8 + ((lane & 4) ? z ^ 5 : z), ch = half * 4 + cc;
+            uint4 x = *reinterpret_cast<const uint4*>(
+                raw + (kD == 128 ? r * 128 + ((ch ^ (r & 7)) << 4)
+                                 : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)));
+            if (partial) {
+              const long long t = (long long)mt.pos[r >> 4] + (r & 15);
+              if (!(t <= end && (t >= w.lo || t < w.s0))) x = make_uint4(0u, 0u, 0u, 0u);
+              uint32_t any = 0;
+              auto clean = [&](uint32_t u) -> uint32_t {  // without NaN codes
+                const uint32_t n = ((u & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                any |= n;
+                return u & ~((n >> 7) * 0xffu);
+              };
+              x = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
+              if (any) atomicOr(&mt.nan[r >> 5], 1u << (r & 31));
+            }
+            unsigned char* dst = wide + half * S::kAtom + r * 128;
+            *reinterpret_cast<uint4*>(dst + (((2 * cc) ^ (r & 7)) << 4)) =
+                make_uint4(codes2_f16(x.x & 0xffffu), codes2_f16(x.x >> 16),
+                           codes2_f16(x.y & 0xffffu), codes2_f16(x.y >> 16));
+            *reinterpret_cast<uint4*>(dst + (((2 * cc + 1) ^ (r & 7)) << 4)) =
+                make_uint4(codes2_f16(x.z & 0xffffu), codes2_f16(x.z >> 16),
+                           codes2_f16(x.w & 0xffffu), codes2_f16(x.w >> 16));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive1(&c.wide_full[st][kind]);
+            mbar_arrive1(&c.raw_empty[kind]);
+          }
+        }
+        if (!ok) break;
+      }
+    }
+  } else if (warp == kTmaWarp) {
+    // ================= TMA =================
+    const int R = 1 << p.box_log;
+    int tiles = 0, sent = 0;  // sent: copies of tile `tiles` under way (1: keys)
+    bool ok = issue;
+    // group `lane` of tile v: position (0x7fffffff: none) and cache row
+    auto look_up = [&](int v, int& pos, int& row) {
+      pos = 0x7fffffff;
+      row = -1;
+      if (lane >= kGroups || v >= w.tb) return;
+      const unsigned box = (unsigned)v * (unsigned)(kKeys >> p.box_log) +
+                           ((unsigned)(lane * 16) >> p.box_log);
+      if (box >= (unsigned)w.boxes) return;
+      const long long b = (int)box < w.sink_boxes ? (int)box : w.first + ((int)box - w.sink_boxes);
+      const long long at = (b << p.box_log) + ((lane * 16) & (R - 1));
+      if (at > min(w.pos1, p.cap - 1)) return;
+      const int blk = (int)at / kv.page_size;
+      const int page = __ldg(kv.block_table + (long long)w.b * kv.max_pages + blk);
+      if (page < 0 || page >= kv.n_pages) {
+        flag(p.a.status, DSA_DEV_BAD_PAGE);
+        return;
+      }
+      pos = (int)at;
+      row = (page * kv.Hkv + w.h) * kv.page_size + ((int)at - blk * kv.page_size);
+    };
+    while (ok && w.next()) {
+      if (w.ta == w.tb) continue;
+      const int lo1 = p.a.window > 0 ? max(0, max(w.pos1, -1) - p.a.window + 1) : 0;
+      int pos, row;
+      look_up(w.ta, pos, row);
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        float ks = 0.f;
+        int ev = 0;
+        if (row >= 0) {
+          const int unit = row / kv.page_size;
+          ks = __ldg(kv.k_scale + unit);
+          ev = exponent_of(__ldg(kv.v_scale + unit));
+        }
+        int next_pos, next_row;
+        look_up(v + 1, next_pos, next_row);
+        // every row sees every one of the 16 keys
+        const long long last = (long long)pos + 15;
+        const bool full = last <= w.pos0 && (pos >= lo1 || last < p.a.sinks);
+        const bool partial = __any_sync(0xffffffffu, lane < kGroups && !full);
+        const bool box = row >= 0 && ((lane * 16) & (R - 1)) == 0;
+        const unsigned boxes = __ballot_sync(0xffffffffu, box);
+        Meta& mt = c.meta[tiles % kMetas];
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+          ok = tiles == 0 || wait_on(&c.raw_empty[kind], (tiles - 1) & 1, dead, wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (kind == 0) {
+            // (the tile four before this one is done with: its values' place was asked for again
+            // before the last tile's keys were widened)
+            if (lane < kGroups) {
+              mt.pos[lane] = pos;
+              mt.ks[lane] = ks;
+              mt.ev[lane] = ev;
+              mt.row[lane] = row;
+            }
+            if (lane < 4) mt.nan[lane] = 0u;
+            if (lane == 0) mt.partial = partial;
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[kind], __popc(boxes) * R * kD);
+          sent = kind + 1;
+          __syncwarp();
+          if (box)
+            tma_load_2d(sb + S::kCodes + kind * S::kRaw + lane * 16 * kD, kind ? &v_map : &k_map, 0,
+                        row, &c.raw_full[kind]);
+        }
+        if (!ok) break;
+        sent = 0;
+        pos = next_pos;
+        row = next_row;
+      }
+    }
+    // after a give-up: no copy into this CTA's memory may be in flight at its end
+    if (*dead && lane == 0)
+      for (int kind = 0; kind < 2; ++kind) {
+        const int n = tiles + (sent > kind ? 1 : 0);  // copies of this kind so far
+        if (n > 0) mbar_wait_bounded(&c.raw_full[kind], (n - 1) & 1);
+      }
+  } else if (issue) {
+    // ================= the products =================
+    constexpr uint32_t id_s = idesc_f16(kRows, kKeys, false), id_o = idesc_f16(kRows, kD, true);
+    const uint64_t d_q = sw128_desc(smem_u32(sb + S::kQ));
+    const uint64_t d_k = sw128_desc(smem_u32(sb + S::kWide));
+    const uint64_t d_v = umma_desc_sw128(smem_u32(sb + S::kWide) + S::kTile, S::kAtom, 1024);
+    int tiles = 0;
+    int used[2] = {0, 0}, done[2] = {0, 0};  // of A, of B: segments with it, tiles done
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, unsigned parity) {
+      const bool got = wait_on(bar, parity, dead, wait_ns);
+      return __all_sync(0xffffffffu, got) != 0;
+    };
+    // O += W C_v of tile j (of the segment: its first or not) for A or B
+    auto outputs = [&](int ab, int j, bool more) {
+      if (!wait(&c.p_full[ab], done[ab] & 1) ||
+          !wait(&c.wide_full[j & 1][1], (j >> 1) & 1))
+        return false;
+      ++done[ab];
+      tc_fence_after();
+      const uint64_t dv = d_v + (uint32_t)((j & 1) * (2 * S::kTile >> 4));
+#pragma unroll
+      for (int s = 0; s < kKeys / 16; ++s)
+        umma_tmem_a_elect(tmem + kOCol + ab * 128, tmem + ab * 128 + s * 8, dv + (s * 2048 >> 4),
+                          id_o, (s || more) ? 1u : 0u);
+      return true;
+    };
+    auto scores = [&](int ab, int j) {
+      const uint64_t dk = d_k + (uint32_t)((j & 1) * (2 * S::kTile >> 4));
+      const uint64_t dq = d_q + (uint32_t)(ab * (S::kTile >> 4));
+      tc_fence_after();
+#pragma unroll
+      for (int s = 0; s < kD / 16; ++s) {
+        const uint32_t at = ((s >> 2) * S::kAtom + (s & 3) * 32) >> 4;
+        umma_f16_elect(tmem + ab * 128, dq + at, dk + at, id_s, s ? 1u : 0u);
+      }
+      umma_commit_elect(&c.s_full[ab]);
+    };
+    while (ok && w.next()) {
+      if (w.ta == w.tb) continue;
+      const bool two = w.tokens > p.per;
+      ok = wait(&c.q_full[0], used[0] & 1) && (!two || wait(&c.q_full[1], used[1] & 1));
+      if (!ok) break;
+      ++used[0];
+      used[1] += two;
+      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
+        ok = wait(&c.wide_full[tiles & 1][0], (tiles >> 1) & 1);
+        if (!ok) break;
+        for (int ab = 0; ab < (two ? 2 : 1) && ok; ++ab) {
+          if (v > w.ta) ok = outputs(ab, tiles - 1, v - 1 > w.ta);
+          if (ok) scores(ab, tiles);
+        }
+        if (!ok) break;
+        umma_commit_elect(&c.wide_empty[tiles & 1][0]);
+        if (v > w.ta) umma_commit_elect(&c.wide_empty[(tiles - 1) & 1][1]);
+      }
+      if (!ok) break;
+      umma_commit_elect(&c.q_empty);
+      for (int ab = 0; ab < (two ? 2 : 1) && ok; ++ab) {
+        ok = outputs(ab, tiles - 1, w.tb - w.ta > 1);
+        if (ok) umma_commit_elect(&c.o_full[ab]);
+      }
+      if (ok) umma_commit_elect(&c.wide_empty[(tiles - 1) & 1][1]);
+    }
+    if (!ok) {  // drain what was issued before the CTA's memory is given back
+      umma_commit_elect(&c.drain);
+      mbar_wait_bounded(&c.drain, 0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && c.dead) flag(p.a.status, DSA_DEV_TIMEOUT);  // outputs unspecified
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc<kTmem>(tmem);
+  }
+}
+
+// The rows of an item (gqa_join.cuh).
+struct Rows {
+  static constexpr int kRows = 2 * dsa::kRows;
+  int Hq, Hkv, G, per;
+  __device__ __forceinline__ int used() const { return kRows; }
+  __device__ __forceinline__ long long operator()(int item, int tokens, int r) const {
+    const int token = item / Hkv, h = item - token * Hkv;
+    const int ab = r / dsa::kRows, rr = r - ab * dsa::kRows, my = rr / G, i = ab * per + my;
+    return my < per && i < tokens ? (long long)(token + i) * Hq + h * G + (rr - my * G) : -1;
+  }
+};
+
+template <int kD>
+int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
+  const int n_cta = num_sms();
+  Params p = {};
+  p.a = a;
+  p.G = a.Hq / a.kv.Hkv;
+  p.per = kRows / p.G;
+  p.zscale = a.sm_scale * kLog2e;
+  p.cap = table_cap(a.kv.max_pages, a.kv.page_size);
+  p.box_log = chunk::box_log_of(a.kv.page_size);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float4*>(p.part_o + (size_t)n_cta * 4 * kRows * kD);
+  p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)n_cta * 4 * kRows);
+  p.drill = failure_drill();
+  CUtensorMap k_map, v_map;
+  const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.Hkv * a.kv.page_size;
+  if (!code_map(&k_map, a.kv.k_pages, rows, kD, 1u << p.box_log) ||
+      !code_map(&v_map, a.kv.v_pages, rows, kD, 1u << p.box_log))
+    return DSA_ERR_CUDA;
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_smem(gqa_chunk_kernel<kD>, Smem<kD>::kBytes, done)) return DSA_ERR_CUDA;
+  Launch l(dim3(n_cta, 1, 1), kThreads, Smem<kD>::kBytes, stream);
+  if (launch_kernel(&l.cfg, gqa_chunk_kernel<kD>, k_map, v_map, p) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  const JoinArgs j{p.part_o, p.part_ml, p.head, n_cta, static_cast<__nv_bfloat16*>(a.out), a.lse};
+  return launch_join<kD>(j, Rows{a.Hq, a.kv.Hkv, p.G, p.per}, stream);
+}
+
+}  // namespace
+
+size_t gqa_chunk_workspace_size(int D) {
+  return (size_t)num_sms() * (4 * kRows * (D * 4 + 16) + sizeof(Header));
+}
+
+int launch_gqa_chunk(const GqaArgs& a, void* workspace, cudaStream_t stream) {
+  return a.kv.D == 128 ? launch<128>(a, workspace, stream) : launch<64>(a, workspace, stream);
+}
+
+}  // namespace dsa

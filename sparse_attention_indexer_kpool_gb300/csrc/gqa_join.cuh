@@ -1,0 +1,230 @@
+// What the attention kernels of the grouped-query layer share: the tensor maps of the codes, and
+// the join of the partials of items (row tiles) whose tiles were shared out over several
+// workers (warps or CTAs).
+#pragma once
+
+#include "gqa.cuh"
+#include "mla_chunk.cuh"
+
+namespace dsa {
+namespace gqa {
+
+constexpr int kUp = 8;  // weights are held times 2^8, and so are the outputs
+
+struct Header {        // what a worker left
+  int start_item;      // item whose first tiles it holds but not its last (-1: none)
+  int cont_item;       // item that an earlier worker began (-1: none)
+  int cont;            // 1: it has a partial of that, 2: and its last tiles
+  int tokens;          // of start_item, where items differ in them
+};
+
+// x 2^(e - kUp) / f, in steps that stay in range where the result does (0 for f = 0: no sum)
+struct Factor {
+  float inv, a, b;
+  __device__ __forceinline__ Factor(float f, int e) {
+    inv = f == 0.f ? 0.f : 1.f / (f * (float)(1 << kUp));
+    const int third = max(min(e / 3, 126), -126);
+    a = pow2(third);
+    b = pow2(max(min(e - 2 * third, 126), -126));
+  }
+  __device__ __forceinline__ float operator()(float x) const { return x * inv * a * a * b; }
+};
+
+struct JoinArgs {
+  const float* part_o;    // [2 workers][kRows][D], outputs relative to 2^reference
+  const float4* part_ml;  // [2 workers][kRows]: reference; the sum f 2^z as z and f
+  const Header* head;     // [workers]
+  int workers;
+  __nv_bfloat16* out;
+  float* lse;
+};
+
+// Partials are joined in the workers' order.  An item's workers are neighbours in their numbers:
+// every block reads all headers and lists the ones that began an item.  A piece is one row
+// of such an item: a warp's where there are many, a block's, each warp a part of the
+// partials, where there are few.
+constexpr int kMaxWorkers = 1280, kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
+struct Joined {
+  float m, z, f, x[4];  // outputs relative to 2^m; the sum f 2^z
+};
+__device__ __forceinline__ Joined nothing() {
+  return Joined{-INFINITY, -INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+}
+__device__ __forceinline__ float finite_or_0(float x) { return x == -INFINITY ? 0.f : x; }
+
+template <int kD, int kRows>
+__device__ __forceinline__ Joined join_parts(const JoinArgs& p, const Header* heads, int g0,
+                                             int s0, int s1, int r, int lane) {
+  Joined j = nothing();
+#pragma unroll 1
+  for (; s0 < s1; s0 += 32) {
+    const int s = s0 + lane;
+    const bool part = s < s1 && (s == g0 || (heads[s].cont & 1));
+    const int slot = (s == g0 ? 2 * s + 1 : 2 * s) * kRows + r;
+    float4 ml = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+    if (part) ml = p.part_ml[slot];
+    const bool some = part && ml.z != 0.f;  // (a part that saw no page adds nothing)
+    const float m = fmaxf(j.m, warp_max(some ? ml.x : -INFINITY));
+    const float z = fmaxf(j.z, warp_max(some ? ml.y : -INFINITY));
+    const float ref = finite_or_0(m), zref = finite_or_0(z);
+    // square roots, taken twice; 0 before the first part
+    const float old = ex2_fast(0.5f * (j.m - ref)), zold = ex2_fast(0.5f * (j.z - zref));
+    // (no reference: a NaN sum, which stays one)
+    const float wgt = some ? ex2_fast(ml.x == -INFINITY ? 0.f : 0.5f * (ml.x - ref)) : 0.f;
+    const float zw = some ? ex2_fast(ml.y == -INFINITY ? 0.f : 0.5f * (ml.y - zref)) : 0.f;
+    j.f = j.f * zold * zold + warp_sum(some ? ml.z * zw * zw : 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) j.x[k] = j.x[k] * old * old;
+    j.m = m;
+    j.z = z;
+    unsigned todo = __ballot_sync(0xffffffffu, some);
+    while (todo) {
+      float v[4][4], wv[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {  // four partial rows on their way at once
+        const int i = todo ? __ffs(todo) - 1 : -1;
+        const int sl = __shfl_sync(0xffffffffu, slot, i & 31);
+        wv[u] = __shfl_sync(0xffffffffu, wgt, i & 31);
+        if (i < 0) wv[u] = 0.f;
+        const float* src = p.part_o + (long long)sl * kD + lane * (kD / 32);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[u][k] = 0.f;
+        if (i >= 0) {
+          if constexpr (kD == 128) {
+            const float4 f = __ldcs(reinterpret_cast<const float4*>(src));
+            v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
+          } else {
+            const float2 f = __ldcs(reinterpret_cast<const float2*>(src));
+            v[u][0] = f.x; v[u][1] = f.y;
+          }
+        }
+        todo &= todo - 1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) j.x[k] = fmaf(v[u][k] * wv[u], wv[u], j.x[k]);
+    }
+  }
+  return j;
+}
+template <int kD>
+__device__ __forceinline__ void store_joined(const JoinArgs& p, long long row, const Joined& j,
+                                             int lane) {
+  // (m - z: a whole part and a rest below 1)
+  const float d = j.f == 0.f || j.m == -INFINITY ? 0.f : j.m - j.z;
+  const float whole = fabsf(d) < 1000.f ? floorf(d) : 0.f;
+  const Factor by(j.f * ex2_fast(whole - d), (int)whole);
+  float x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = by(j.x[k]);
+  __nv_bfloat16* out = p.out + row * kD + lane * (kD / 32);
+  if constexpr (kD == 128)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16(x[0], x[1]);
+  if (p.lse && lane == 0)
+    p.lse[row] = j.f == 0.f ? -INFINITY : (j.z + log2f(j.f)) / kLog2e;
+}
+
+// Rows: kRows rows of an item, `used` of them in any; the output row of one (-1: none)
+template <int kD, typename Rows>
+__global__ void __launch_bounds__(kJoinThreads, 2)
+    gqa_join_kernel(const JoinArgs p, const Rows rows) {
+  constexpr int kRows = Rows::kRows;
+  const int workers = p.workers;
+  __shared__ __align__(16) Header heads[kMaxWorkers];
+  __shared__ unsigned short begun[kMaxWorkers];
+  __shared__ int n_begun;
+  __shared__ Joined parts[kJoinWarps][32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < workers; i += kJoinThreads)
+    *reinterpret_cast<int4*>(heads + i) = *reinterpret_cast<const int4*>(p.head + i);
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0;
+    for (int s = 0; s < workers; s += 32) {
+      const bool hit = s + lane < workers && heads[s + lane].start_item >= 0;
+      const unsigned all = __ballot_sync(0xffffffffu, hit);
+      if (hit) begun[n + __popc(all & ((1u << lane) - 1))] = (unsigned short)(s + lane);
+      n += __popc(all);
+    }
+    if (lane == 0) n_begun = n;
+  }
+  __syncthreads();
+  const int used = rows.used(), pieces = n_begun * used;
+  const bool wide = pieces <= 2 * (int)gridDim.x;  // a block a piece
+  const int step = wide ? gridDim.x : gridDim.x * kJoinWarps;
+#pragma unroll 1
+  for (int i = wide ? blockIdx.x : warp * gridDim.x + blockIdx.x; i < pieces; i += step) {
+    const int g0 = begun[i / used], r = i % used, item = heads[g0].start_item;
+    const long long row = rows(item, heads[g0].tokens, r);
+    if (row < 0) continue;
+    int n = 1;  // its workers: g0 .. g0 + n - 1
+    for (unsigned stop = 0; !stop;) {
+      const int s = g0 + n + lane;
+      const Header hd = heads[min(s, workers - 1)];
+      const bool mine = s < workers && hd.cont_item == item;
+      stop = __ballot_sync(0xffffffffu, !mine || (hd.cont & 2));
+      const int k = stop ? __ffs(stop) - 1 : 32;  // before the stopping one
+      n += k + (stop ? __shfl_sync(0xffffffffu, (int)mine, k & 31) : 0);
+    }
+    const int per = wide ? (n + kJoinWarps - 1) / kJoinWarps : n;
+    const int s0 = g0 + (wide ? min(n, warp * per) : 0);
+    const Joined j =
+        join_parts<kD, kRows>(p, heads, g0, s0, min(s0 + per, g0 + n), r, lane);
+    if (!wide) {
+      store_joined<kD>(p, row, j, lane);
+      continue;
+    }
+    parts[warp][lane] = j;
+    __syncthreads();
+    if (warp == 0) {
+      Joined all = nothing();
+#pragma unroll
+      for (int u = 0; u < kJoinWarps; ++u) {
+        all.m = fmaxf(all.m, parts[u][lane].m);
+        all.z = fmaxf(all.z, parts[u][lane].z);
+      }
+      const float ref = finite_or_0(all.m), zref = finite_or_0(all.z);
+#pragma unroll
+      for (int u = 0; u < kJoinWarps; ++u) {
+        const Joined& x = parts[u][lane];
+        // (no reference: no part, or a NaN sum, which stays one)
+        const float e = x.m == -INFINITY ? 1.f : ex2_fast(0.5f * (x.m - ref));
+        const float ze = x.z == -INFINITY ? 1.f : ex2_fast(0.5f * (x.z - zref));
+        all.f = fmaf(x.f * ze, ze, all.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) all.x[k] = fmaf(x.x[k] * e, e, all.x[k]);
+      }
+      store_joined<kD>(p, row, all, lane);
+    }
+    __syncthreads();
+  }
+}
+
+// Rows of D codes (as 2-byte elements), boxes of box_rows of them.
+inline bool code_map(CUtensorMap* m, const void* base, uint64_t rows, int D, uint32_t box_rows) {
+  auto fn = chunk::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D / 2, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)D};
+  const cuuint32_t box[2] = {(cuuint32_t)D / 2, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kD, typename Rows>
+int launch_join(const JoinArgs& p, const Rows& rows, cudaStream_t stream) {
+  Launch l(dim3(2 * num_sms(), 1, 1), kJoinThreads, 0, stream);
+  return launch_kernel(&l.cfg, gqa_join_kernel<kD, Rows>, p, rows) == cudaSuccess ? DSA_OK
+                                                                                  : DSA_ERR_CUDA;
+}
+
+}  // namespace gqa
+}  // namespace dsa
