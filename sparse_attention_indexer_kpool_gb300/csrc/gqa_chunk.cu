@@ -19,7 +19,8 @@
 //   warp 13              the products: O of the last tile, then S of this one, A before B,
 //                        so that the tensor cores have B's while A's softmax runs
 // A row's reference stays until a sum of 16 of its weights passes 2^15 (half of fp16's
-// largest): only then, and at a row's first tile, is a maximum looked for.
+// largest): only then, and at a row's first tile, is a maximum looked for.  It is raised by whole
+// numbers, so that the tile's weights that are written already follow exactly.
 //
 // What no row may see is masked, and its values are zeros in the tile.  Keys that some rows of an
 // item see and others do not (the diagonal, a window's edge) may hold NaN codes in their
@@ -42,7 +43,10 @@ constexpr int kRows = 128, kKeys = 128, kGroups = kKeys / 16;
 constexpr int kSoft = 256, kWiden = 128;
 constexpr int kWidenWarp = kSoft / 32, kTmaWarp = kWidenWarp + kWiden / 32,
               kMmaWarp = kTmaWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1), kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;  // (the last two warps idle)
+// Registers: the launch's 128 a thread, moved from the eight other warps to the softmax.
+constexpr int kSoftRegs = 176, kOtherRegs = 80;
+static_assert(kSoftRegs + kOtherRegs == 2 * 128, "what the launch has");
 constexpr int kMetas = 4;
 constexpr float kFull = 32768.f;       // a sum of 16 weights above which a reference is raised
 constexpr int kExtra = 2;              // what an item costs beside its tiles, in tiles
@@ -151,11 +155,12 @@ struct Walk {
 };
 
 struct Meta {          // of a key tile, by 16 keys
-  int pos[kGroups];    // first position (0x7fffffff: none)
-  float ks[kGroups];   // keys' scale
-  int ev[kGroups];     // exponent of the values' scale
+  alignas(16) int pos[kGroups];  // first position (0x7fffffff: none)
+  alignas(16) float ks[kGroups];  // keys' scale
+  alignas(16) int ev[kGroups];    // exponent of the values' scale
   int row[kGroups];    // first cache row
   uint32_t nan[4];     // keys whose NaN values were taken out of the tile
+  int least;           // least exponent of the values' scales
   int partial;         // not every row of the item sees every key
 };
 struct Ctl {
@@ -284,11 +289,34 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
                  "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
                  "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
-// Store 8 consecutive columns of the warp's 32 TMEM lanes.
-__device__ __forceinline__ void tmem_st8(uint32_t ta, const uint32_t (&v)[8]) {
+// The same with 32 columns.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t ta, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(ta));
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+// Store 16 consecutive columns (done behind tmem_st_wait).
+__device__ __forceinline__ void tmem_st16_start(uint32_t ta, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(ta),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
@@ -336,6 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned long long wait_ns = p.drill ? kDrillWaitNs : kWaitNs;
   volatile int* dead = &c.dead;
 
+  // (by whole warpgroups)
+  if (warp < kWidenWarp)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp < kWidenWarp) {
     // ================= softmax: a thread a row of A or B =================
     const int ab = warp >> 2, r = tid & (kRows - 1);
@@ -434,125 +467,170 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         Meta& mt = c.meta[tiles % kMetas];
         const bool partial = mt.partial != 0;
-        // exponents of 16 weights, of group q
-        auto exponents = [&](int q, const uint32_t (&s)[16], float (&e)[16]) {
-          const float zs = qs * mt.ks[q];
-          const float off = (float)(mt.ev[q] + kUp) - (m == -INFINITY ? 0.f : m);
+        // (The code of this loop has to stay small: unrolled over the tile, with the rare paths in
+        // every copy, it waited for instructions more than for anything else.)
+        // exponents of the weights of groups 2 i and 2 i + 1
+        auto exponents = [&](int i, const uint32_t (&s)[32], float (&e)[32]) {
+          const float2 ks = *reinterpret_cast<const float2*>(mt.ks + 2 * i);
+          const int2 lv = *reinterpret_cast<const int2*>(mt.ev + 2 * i);
+          const float ref = (float)kUp - (m == -INFINITY ? 0.f : m);
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            e[k] = __uint_as_float(s[k]);
-            e[k + 1] = __uint_as_float(s[k + 1]);
-            fma2(e[k], e[k + 1], zs, off, off);
-          }
-          if (partial) {
-            const long long p0 = mt.pos[q];
+          for (int h = 0; h < 2; ++h) {
+            const float zs = qs * (h ? ks.y : ks.x), off = (float)(h ? lv.y : lv.x) + ref;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const long long t = p0 + k;
-              if (!(t <= pos && (t >= lo || t < s0))) e[k] = -INFINITY;
+            for (int k = 16 * h; k < 16 * h + 16; k += 2) {
+              e[k] = __uint_as_float(s[k]);
+              e[k + 1] = __uint_as_float(s[k + 1]);
+              fma2(e[k], e[k + 1], zs, off, off);
             }
           }
-        };
-        // A new reference from the tile's largest exponent, where that lies above the present one;
-        // the row's sum and outputs follow.
-        auto raise = [&]() {
-          float top = -INFINITY;
-          int lv = 0;
+          if (partial) {
+            uint32_t see = 0;
 #pragma unroll 1
-          for (int q = 0; q < kGroups; ++q) {
-            uint32_t s[16];
-            float e[16];
-            tmem_ld16_start(ts + q * 16, s);
-            tmem_ld_wait(s);
-            exponents(q, s, e);
-            float t = e[0];
+            for (int h = 0; h < 2; ++h) {  // positions t0 .. t0 + 15: [lo, pos] and [0, s0)
+              const long long t0 = mt.pos[2 * i + h];
+              auto below = [&](long long t) {  // bits of the positions before t
+                const long long n = min(max(t - t0, 0ll), 16ll);
+                return (1u << n) - 1u;
+              };
+              see |= (below((long long)pos + 1) & (~below(lo) | below(s0)) & 0xffffu) << (16 * h);
+            }
 #pragma unroll
-            for (int k = 1; k < 16; ++k) t = fmaxf(t, e[k]);
-            if (t > top) {
-              top = t;
-              lv = mt.ev[q] + kUp;
+            for (int k = 0; k < 32; ++k) e[k] = (see >> k) & 1u ? e[k] : -INFINITY;
+          }
+        };
+        // A row's first reference: its largest exponent in the tile.
+        if (__any_sync(0xffffffffu, m == -INFINITY)) {
+          float top = -INFINITY;
+          int at = 0;
+#pragma unroll 1
+          for (int i = 0; i < kGroups / 2; ++i) {
+            uint32_t s[32];
+            float e[32];
+            tmem_ld32_start(ts + i * 32, s);
+            tmem_ld32_wait(s);
+            exponents(i, s, e);
+            float t0 = e[0], t1 = e[16];
+#pragma unroll
+            for (int k = 1; k < 16; ++k) {
+              t0 = fmaxf(t0, e[k]);
+              t1 = fmaxf(t1, e[16 + k]);
+            }
+            if (fmaxf(t0, t1) > top) {
+              top = fmaxf(t0, t1);
+              at = mt.ev[2 * i + (t1 > t0 ? 1 : 0)] + kUp;
             }
             __syncwarp();
           }
-          const float rel = top - (float)kUp;
-          float a = 1.f;
-          if (m == -INFINITY) {  // nothing accumulated for this row yet
-            if (rel != -INFINITY) {
-              m = rel;
-              base = lv;
+          if (m == -INFINITY && top != -INFINITY) {
+            m = top - (float)kUp;
+            base = at;
+          }
+          __syncwarp();
+        }
+        const bool far = __any_sync(0xffffffffu, base - (mt.least + kUp) > 64);
+        uint32_t s[32];
+        tmem_ld32_start(ts, s);
+#pragma unroll 1
+        for (int i = 0; i < kGroups / 2; ++i) {
+          float e[32], part[2];
+          tmem_ld32_wait(s);
+          exponents(i, s, e);
+          // (the next scores on their way)
+          if (i + 1 < kGroups / 2) tmem_ld32_start(ts + (i + 1) * 32, s);
+          uint32_t wt[16];
+#pragma unroll 1
+          for (bool again = false;; again = true) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+#pragma unroll
+              for (int k = 16 * h; k < 16 * h + 16; k += 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e[k + j] = ex2_fast(e[k + j]);
+                add2(a0, a1, e[k], e[k + 1]);
+                add2(b0, b1, e[k + 2], e[k + 3]);
+                wt[k / 2] = pack_f16(e[k], e[k + 1]);
+                wt[k / 2 + 1] = pack_f16(e[k + 2], e[k + 3]);
+              }
+              part[h] = (a0 + b0) + (a1 + b1);
             }
-          } else if (rel > 0.f) {
-            m += rel;
+            const bool high = fmaxf(part[0], part[1]) > kFull;
+            if (again || !__any_sync(0xffffffffu, high)) break;
+            // A larger reference, by a whole number: what is there already follows exactly (and
+            // an infinite weight stays one).
+            uint32_t x[32];
+            tmem_ld32_start(ts + i * 32, x);
+            tmem_ld32_wait(x);
+            exponents(i, x, e);
+            float top = e[0];
+#pragma unroll
+            for (int k = 1; k < 32; ++k) top = fmaxf(top, e[k]);
+            const float by =
+                high ? fminf(fmaxf(ceilf(top) - (float)kUp, 0.f), 4096.f) : 0.f;
+            m += by;
+            int next = max(mt.ev[2 * i], mt.ev[2 * i + 1]) + kUp;
+            if ((float)(next - base) - by > 60.f) next = (int)floorf((float)base + by + 60.f);
+            if (by == 0.f) next = base;
             // (square roots, taken twice: weights may lie further apart than a float reaches)
-            a = ex2_fast(-0.5f * rel);
-            int next = lv;
-            if ((float)(lv - base) - rel > 60.f) next = (int)floorf((float)base + rel + 60.f);
-            const float f = ex2_fast(0.5f * ((float)(next - base) - rel));
+            const float f = ex2_fast(0.5f * ((float)(next - base) - by)), a = ex2_fast(-0.5f * by);
             base = next;
             l = l * f * f;
-          }
-          if (v > w.ta && __any_sync(0xffffffffu, a != 1.f)) {
+            __syncwarp();
+            if (v > w.ta) {
 #pragma unroll 1
-            for (int k = 0; k < kD / 16; ++k) {
-              float o[16];
-              tmem_ld16(to + k * 16, o);
+              for (int k = 0; k < kD / 16; ++k) {
+                float o[16];
+                tmem_ld16(to + k * 16, o);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = o[j] * a * a;
-              chunk::tmem_st16(to + k * 16, o);
-            }
-          }
-        };
-        if (__any_sync(0xffffffffu, m == -INFINITY)) raise();
-        // The weights stay in registers until the scores are no longer needed: where one was too
-        // large, all are taken again after a raise.
-        uint32_t wt[kGroups][8];
-        float sum;
-#pragma unroll 1
-        for (int turn = 0;; ++turn) {
-          bool high = false;
-          sum = 0.f;
-          uint32_t raw[2][16];
-          tmem_ld16_start(ts, raw[0]);
-#pragma unroll
-          for (int q = 0; q < kGroups; ++q) {
-            tmem_ld_wait(raw[q & 1]);
-            if (q + 1 < kGroups) tmem_ld16_start(ts + (q + 1) * 16, raw[(q + 1) & 1]);
-            float e[16];
-            exponents(q, raw[q & 1], e);
-            const int d = base - (mt.ev[q] + kUp);
-            const bool far = __any_sync(0xffffffffu, d > 64);  // a scale far below the reference's
-            if (far) {
-              float top = e[0];
-#pragma unroll
-              for (int k = 1; k < 16; ++k) top = fmaxf(top, e[k]);
-              float by = (float)d;
-              if (top + by > 100.f) {
-                base -= 100;
-                by -= 100.f;
-                l *= 0x1p-100f;
-                sum *= 0x1p-100f;
+                for (int j = 0; j < 16; ++j) o[j] = o[j] * a * a;
+                chunk::tmem_st16(to + k * 16, o);
               }
-#pragma unroll
-              for (int k = 0; k < 16; ++k) sum += ex2_fast(e[k] + by);
-              __syncwarp();
             }
-            float a0 = 0.f, a1 = 0.f;
+            const float down = by < 30.f ? pow2(-(int)by) : 0.f;  // of fp16
+            const __half2 down2 = __floats2half2_rn(down, down);
+#pragma unroll 1
+            for (int k = 0; k < i; ++k) {
+              uint32_t y[16];
+              tmem_ld16_start(ts + k * 16, y);
+              tmem_ld_wait(y);
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              e[k] = ex2_fast(e[k]);
-              e[k + 1] = ex2_fast(e[k + 1]);
-              add2(a0, a1, e[k], e[k + 1]);
-              wt[q][k / 2] = pack_f16(e[k], e[k + 1]);
+              for (int j = 0; j < 16; ++j) {
+                const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y[j]), down2);
+                y[j] = *reinterpret_cast<const uint32_t*>(&z);
+              }
+              tmem_st16_start(ts + k * 16, y);
+              tmem_st_wait();
             }
-            high |= a0 + a1 > kFull;
-            if (!far) sum = fmaf(a0 + a1, pow2(max(d, -126)), sum);
+            exponents(i, x, e);
           }
-          if (turn > 0 || !__any_sync(0xffffffffu, high)) break;
-          raise();
-        }
-        l += sum;
+          const int2 lv = *reinterpret_cast<const int2*>(mt.ev + 2 * i);
+          if (far) {  // scales far below the reference's: their weights' sum by itself
+            uint32_t x[32];
+            tmem_ld32_start(ts + i * 32, x);
+            tmem_ld32_wait(x);
+            exponents(i, x, e);
+            float top0 = e[0], top1 = e[16];
 #pragma unroll
-        for (int q = 0; q < kGroups; ++q) tmem_st8(ts + q * 8, wt[q]);
+            for (int k = 1; k < 16; ++k) {
+              top0 = fmaxf(top0, e[k]);
+              top1 = fmaxf(top1, e[16 + k]);
+            }
+            if (fmaxf(top0 - (float)lv.x, top1 - (float)lv.y) + (float)(base - kUp) > 100.f) {
+              base -= 100;
+              l *= 0x1p-100f;
+            }
+            const float by0 = (float)(base - kUp - lv.x), by1 = (float)(base - kUp - lv.y);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) l += ex2_fast(e[k] + by0) + ex2_fast(e[16 + k] + by1);
+            __syncwarp();
+          } else {
+            l = fmaf(part[0], pow2(max(base - kUp - lv.x, -126)), l);
+            l = fmaf(part[1], pow2(max(base - kUp - lv.y, -126)), l);
+          }
+          // (where scores lay that are read)
+          tmem_st16_start(ts + i * 16, wt);
+        }
         tmem_st_wait();
         if (partial) {
           // (before the weights are handed on: the tile's values stay where they are till then)
@@ -639,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int v = w.ta; v < w.tb; ++v, ++tiles) {
         const int st = tiles & 1;
         Meta& mt = c.meta[tiles % kMetas];
-#pragma unroll
+#pragma unroll 1
         for (int kind = 0; kind < 2; ++kind) {
           ok = wait_on(&c.raw_full[kind], tiles & 1, dead, wait_ns) &&
                (tiles < 2 ||
@@ -732,6 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long last = (long long)pos + 15;
         const bool full = last <= w.pos0 && (pos >= lo1 || last < p.a.sinks);
         const bool partial = __any_sync(0xffffffffu, lane < kGroups && !full);
+        const int least = __reduce_min_sync(0xffffffffu, row >= 0 ? ev : kExpMax);
         const bool box = row >= 0 && ((lane * 16) & (R - 1)) == 0;
         const unsigned boxes = __ballot_sync(0xffffffffu, box);
         Meta& mt = c.meta[tiles % kMetas];
@@ -750,7 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               mt.row[lane] = row;
             }
             if (lane < 4) mt.nan[lane] = 0u;
-            if (lane == 0) mt.partial = partial;
+            if (lane == 0) {
+              mt.least = least;
+              mt.partial = partial;
+            }
             __syncwarp();
           }
           if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[kind], __popc(boxes) * R * kD);
@@ -772,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = tiles + (sent > kind ? 1 : 0);  // copies of this kind so far
         if (n > 0) mbar_wait_bounded(&c.raw_full[kind], (n - 1) & 1);
       }
-  } else if (issue) {
+  } else if (warp == kMmaWarp && issue) {
     // ================= the products =================
     constexpr uint32_t id_s = idesc_f16(kRows, kKeys, false), id_o = idesc_f16(kRows, kD, true);
     const uint64_t d_q = sw128_desc(smem_u32(sb + S::kQ));
