@@ -10,7 +10,7 @@
 //   O += W C_v                    W as the first factor in tensor memory, where S was
 // with the codes C widened to fp16 (exact), the query rows scaled by a power of two, lv the
 // exponent of the values' scale and m a row's reference, all as in the kernel for decode
-// tokens (weights times 2^8; the sums, of 2^(z - m + B), in fp32).
+// tokens (weights times 2^2; the sums, of 2^(z - m + B), in fp32).
 //
 // Roles (a thread of the softmax has a whole row, so that no reduction crosses threads):
 //   warps 0 - 3, 4 - 7   softmax of A, of B: S from tensor memory, W back to it
@@ -45,7 +45,7 @@ constexpr int kWidenWarp = kSoft / 32, kTmaWarp = kWidenWarp + kWiden / 32,
               kMmaWarp = kTmaWarp + 1;
 constexpr int kThreads = 512, kWarps = kThreads / 32;  // (the last two warps idle)
 // Registers: the launch's 128 a thread, moved from the eight other warps to the softmax.
-constexpr int kSoftRegs = 176, kOtherRegs = 80;
+constexpr int kSoftRegs = 152, kOtherRegs = 104;
 static_assert(kSoftRegs + kOtherRegs == 2 * 128, "what the launch has");
 constexpr int kMetas = 4;
 constexpr float kFull = 32768.f;       // a sum of 16 weights above which a reference is raised
@@ -467,8 +467,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         Meta& mt = c.meta[tiles % kMetas];
         const bool partial = mt.partial != 0;
-        // (The code of this loop has to stay small: unrolled over the tile, with the rare paths in
-        // every copy, it waited for instructions more than for anything else.)
+        // The tile in two code paths: a short one for what most tiles are (every key seen, every
+        // row with a reference that holds, scales not far apart), which leaves off where a weight
+        // is too large, and one for everything, from there on.  (The code has to stay small: with
+        // the rare cases in the common loop, 1.25 ms; with that loop unrolled over the tile, 1.5.)
+        int i = 0;
+        if (!partial && !__any_sync(0xffffffffu, m == -INFINITY || base - (mt.least + kUp) > 64)) {
+          const float ref = (float)kUp - m;
+          uint32_t raw[2][32];
+          tmem_ld32_start(ts, raw[0]);
+#pragma unroll 1
+          for (; i < kGroups / 2; i += 2) {
+            uint32_t wt[2][16];
+            float part[4];
+            const float4 ks = *reinterpret_cast<const float4*>(mt.ks + 2 * i);
+            const int4 lv = *reinterpret_cast<const int4*>(mt.ev + 2 * i);
+            const float zs[4] = {qs * ks.x, qs * ks.y, qs * ks.z, qs * ks.w};
+            const int ev[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              tmem_ld32_wait(raw[j]);
+              if (j == 0) tmem_ld32_start(ts + (i + 1) * 32, raw[1]);
+              else if (i == 0) tmem_ld32_start(ts + 64, raw[0]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float z = zs[2 * j + h], off = (float)ev[2 * j + h] + ref;
+                float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+#pragma unroll
+                for (int k = 16 * h; k < 16 * h + 16; k += 4) {
+                  float e[4];
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) e[u] = __uint_as_float(raw[j][k + u]);
+                  fma2(e[0], e[1], z, off, off);
+                  fma2(e[2], e[3], z, off, off);
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) e[u] = ex2_fast(e[u]);
+                  add2(a0, a1, e[0], e[1]);
+                  add2(b0, b1, e[2], e[3]);
+                  wt[j][k / 2] = pack_f16(e[0], e[1]);
+                  wt[j][k / 2 + 1] = pack_f16(e[2], e[3]);
+                }
+                part[2 * j + h] = (a0 + b0) + (a1 + b1);
+              }
+            }
+            const float high = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+            if (__any_sync(0xffffffffu, high > kFull)) break;
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              l = fmaf(part[h], pow2(max(base - kUp - ev[h], -126)), l);
+            // (where scores lay that are read)
+            tmem_st16_start(ts + i * 16, wt[0]);
+            tmem_st16_start(ts + i * 16 + 16, wt[1]);
+          }
+          // (a load that nobody waited for)
+          if (i == 0) tmem_ld32_wait(raw[0]);
+          tmem_st_wait();
+        }
         // exponents of the weights of groups 2 i and 2 i + 1
         auto exponents = [&](int i, const uint32_t (&s)[32], float (&e)[32]) {
           const float2 ks = *reinterpret_cast<const float2*>(mt.ks + 2 * i);
@@ -500,16 +554,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         // A row's first reference: its largest exponent in the tile.
-        if (__any_sync(0xffffffffu, m == -INFINITY)) {
+        if (i == 0 && __any_sync(0xffffffffu, m == -INFINITY)) {
           float top = -INFINITY;
           int at = 0;
 #pragma unroll 1
-          for (int i = 0; i < kGroups / 2; ++i) {
+          for (int j = 0; j < kGroups / 2; ++j) {
             uint32_t s[32];
             float e[32];
-            tmem_ld32_start(ts + i * 32, s);
+            tmem_ld32_start(ts + j * 32, s);
             tmem_ld32_wait(s);
-            exponents(i, s, e);
+            exponents(j, s, e);
             float t0 = e[0], t1 = e[16];
 #pragma unroll
             for (int k = 1; k < 16; ++k) {
@@ -518,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (fmaxf(t0, t1) > top) {
               top = fmaxf(t0, t1);
-              at = mt.ev[2 * i + (t1 > t0 ? 1 : 0)] + kUp;
+              at = mt.ev[2 * j + (t1 > t0 ? 1 : 0)] + kUp;
             }
             __syncwarp();
           }
@@ -529,15 +583,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         const bool far = __any_sync(0xffffffffu, base - (mt.least + kUp) > 64);
-        uint32_t s[32];
-        tmem_ld32_start(ts, s);
 #pragma unroll 1
-        for (int i = 0; i < kGroups / 2; ++i) {
+        for (; i < kGroups / 2; ++i) {
+          uint32_t s[32];
           float e[32], part[2];
+          tmem_ld32_start(ts + i * 32, s);
           tmem_ld32_wait(s);
           exponents(i, s, e);
-          // (the next scores on their way)
-          if (i + 1 < kGroups / 2) tmem_ld32_start(ts + (i + 1) * 32, s);
           uint32_t wt[16];
 #pragma unroll 1
           for (bool again = false;; again = true) {
@@ -587,8 +639,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 chunk::tmem_st16(to + k * 16, o);
               }
             }
-            const float down = by < 30.f ? pow2(-(int)by) : 0.f;  // of fp16
-            const __half2 down2 = __floats2half2_rn(down, down);
+            tmem_st_wait();  // (the groups' before this one, read back)
+            // (in two steps: 2^15 to 2^-24 is more than fp16 has below 1)
+            const int half = (int)by >> 1, rest = (int)by - half;
+            const __half2 down0 = __float2half2_rn(by < 40.f ? pow2(-half) : 0.f);
+            const __half2 down1 = __float2half2_rn(by < 40.f ? pow2(-rest) : 0.f);
 #pragma unroll 1
             for (int k = 0; k < i; ++k) {
               uint32_t y[16];
@@ -596,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld_wait(y);
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y[j]), down2);
+                const __half2 z = __hmul2(__hmul2(*reinterpret_cast<__half2*>(&y[j]), down0), down1);
                 y[j] = *reinterpret_cast<const uint32_t*>(&z);
               }
               tmem_st16_start(ts + k * 16, y);
@@ -861,18 +916,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t d_k = sw128_desc(smem_u32(sb + S::kWide));
     const uint64_t d_v = umma_desc_sw128(smem_u32(sb + S::kWide) + S::kTile, S::kAtom, 1024);
     int tiles = 0;
-    int used[2] = {0, 0}, done[2] = {0, 0};  // of A, of B: segments with it, tiles done
+    unsigned used_a = 0, used_b = 0, done_a = 0, done_b = 0;  // segments, tiles of A, of B
     bool ok = true;
     auto wait = [&](uint64_t* bar, unsigned parity) {
       const bool got = wait_on(bar, parity, dead, wait_ns);
       return __all_sync(0xffffffffu, got) != 0;
     };
-    // O += W C_v of tile j (of the segment: its first or not) for A or B
-    auto outputs = [&](int ab, int j, bool more) {
-      if (!wait(&c.p_full[ab], done[ab] & 1) ||
-          !wait(&c.wide_full[j & 1][1], (j >> 1) & 1))
+    // O += W C_v of tile j for A or B (a segment's first: O = W C_v)
+    auto outputs = [&](int ab, unsigned& done, int j, bool more) {
+      if (!wait(&c.p_full[ab], done & 1) || !wait(&c.wide_full[j & 1][1], (j >> 1) & 1))
         return false;
-      ++done[ab];
+      ++done;
       tc_fence_after();
       const uint64_t dv = d_v + (uint32_t)((j & 1) * (2 * S::kTile >> 4));
 #pragma unroll
@@ -895,28 +949,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && w.next()) {
       if (w.ta == w.tb) continue;
       const bool two = w.tokens > p.per;
-      ok = wait(&c.q_full[0], used[0] & 1) && (!two || wait(&c.q_full[1], used[1] & 1));
+      ok = wait(&c.q_full[0], used_a & 1) && (!two || wait(&c.q_full[1], used_b & 1));
       if (!ok) break;
-      ++used[0];
-      used[1] += two;
-      for (int v = w.ta; v < w.tb; ++v, ++tiles) {
-        ok = wait(&c.wide_full[tiles & 1][0], (tiles >> 1) & 1);
-        if (!ok) break;
-        for (int ab = 0; ab < (two ? 2 : 1) && ok; ++ab) {
-          if (v > w.ta) ok = outputs(ab, tiles - 1, v - 1 > w.ta);
-          if (ok) scores(ab, tiles);
+      ++used_a;
+      used_b += two;
+      // at v: the outputs of tile v - 1 and the scores of tile v, A's and then B's
+#pragma unroll 1
+      for (int v = w.ta; v <= w.tb; ++v) {
+        const bool first = v == w.ta, end = v == w.tb, more = v - 1 > w.ta;
+        if (!end && !(ok = wait(&c.wide_full[tiles & 1][0], (tiles >> 1) & 1))) break;
+        if (!first && !(ok = outputs(0, done_a, tiles - 1, more))) break;
+        if (end)
+          umma_commit_elect(&c.o_full[0]);
+        else
+          scores(0, tiles);
+        if (two) {
+          if (!first && !(ok = outputs(1, done_b, tiles - 1, more))) break;
+          if (end)
+            umma_commit_elect(&c.o_full[1]);
+          else
+            scores(1, tiles);
         }
-        if (!ok) break;
-        umma_commit_elect(&c.wide_empty[tiles & 1][0]);
-        if (v > w.ta) umma_commit_elect(&c.wide_empty[(tiles - 1) & 1][1]);
+        if (!first) umma_commit_elect(&c.wide_empty[(tiles - 1) & 1][1]);
+        umma_commit_elect(end ? &c.q_empty : &c.wide_empty[tiles & 1][0]);
+        tiles += !end;
       }
-      if (!ok) break;
-      umma_commit_elect(&c.q_empty);
-      for (int ab = 0; ab < (two ? 2 : 1) && ok; ++ab) {
-        ok = outputs(ab, tiles - 1, w.tb - w.ta > 1);
-        if (ok) umma_commit_elect(&c.o_full[ab]);
-      }
-      if (ok) umma_commit_elect(&c.wide_empty[(tiles - 1) & 1][1]);
     }
     if (!ok) {  // drain what was issued before the CTA's memory is given back
       umma_commit_elect(&c.drain);

@@ -10,9 +10,9 @@
 // Query rows are scaled by a power of two to a largest magnitude in [2^14, 2^15): a bf16
 // element keeps its 8 bits in fp16 down to 2^-28 of the row's largest.  lv is the exponent of the
 // values' scale (a power of two), which so multiplies the weight.  The reference m of a head
-// is that of z + lv, raised when a weight passes it by 2^7; weights are held times 2^8, so
-// that fp16 keeps 11 bits of them down to 2^-22 of the reference and none is off by more than
-// 2^-33 of it.  The sum of a head takes lv off again: it is that of 2^(z - m + B) in fp32, B
+// is that of z + lv, raised when a weight passes it by 2^13; weights are held times 2^2, so
+// that fp16 keeps 11 bits of them down to 2^-16 of the reference and none is off by more than
+// 2^-27 of it.  The sum of a head takes lv off again: it is that of 2^(z - m + B) in fp32, B
 // the lv of the key that set the reference, so that scales as far apart as their exponents
 // go neither overflow it nor lose a weight to it.
 //
@@ -38,7 +38,7 @@ using namespace gqa;
 
 constexpr int kW = 8, kThreads = 32 * kW;
 constexpr int kKeys = 32;                      // of a tile
-constexpr float kRaise = 15.f;                 // e above which a reference is raised (2^7)
+constexpr float kRaise = 15.f;                 // e above which a reference is raised
 constexpr int kExtra = 1;                      // what a row tile costs beside its tiles, in tiles
 constexpr int kRingBytes = 3 * 2 * kKeys * 128;  // of a warp
 

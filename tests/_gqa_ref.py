@@ -106,13 +106,15 @@ def scores(q, means, table, lens, cu, ps, sinks, local, sm, NB):
 
 
 def attend(q, kp, ks, vp, vs, table, lens, cu, sm, window=0, sinks=0, ids=None):
-    """out [T, Hq, D], lse [T, Hq], the absolute weighted values [T, Hq, D] and the largest sum
-    of |products| of a logit (for tolerances); rows without a sequence are NaN."""
+    """out [T, Hq, D], lse [T, Hq], and for tolerances the absolute weighted values [T, Hq, D], the
+    number of keys times the largest weight times its value's scale [T, Hq], and the largest sum
+    of |products| of a logit; rows without a sequence are NaN."""
     T, Hq, D = q.shape
     n_pages, Hkv, ps, _ = kp.shape
     G = Hq // Hkv
     out = torch.full((T, Hq, D), math.nan, dtype=torch.float64)
     mass = torch.zeros((T, Hq, D), dtype=torch.float64)
+    top = torch.zeros((T, Hq), dtype=torch.float64)
     lse = torch.full((T, Hq), math.nan, dtype=torch.float64)
     big = 0.0
     for b in range(len(lens)):
@@ -141,4 +143,45 @@ def attend(q, kp, ks, vp, vs, table, lens, cu, sm, window=0, sinks=0, ids=None):
                 w = torch.softmax(z, -1)
                 out[t, hs], lse[t, hs] = w @ v, torch.logsumexp(z, -1)
                 mass[t, hs] = w @ v.abs()
-    return out, lse, mass, big
+                s = torch.stack([vs[table[b][x // ps], h] for x in see])
+                top[t, hs] = (w * s).amax(-1) * len(see)
+    return out, lse, mass, top, big
+
+
+def attend_dense(q, kp, ks, vp, vs, table, lens, cu, sm, window=0, sinks=0):
+    """``attend`` without lists, a sequence and KV head at a time on the tensors' device; every
+    position needs a page."""
+    T, Hq, D = q.shape
+    Hkv, ps = kp.shape[1], kp.shape[2]
+    G, dev = Hq // Hkv, q.device
+    out = torch.full((T, Hq, D), math.nan, dtype=torch.float64, device=dev)
+    lse = torch.full((T, Hq), math.nan, dtype=torch.float64, device=dev)
+    mass, top, big = torch.zeros_like(out), torch.zeros_like(lse), 0.0
+    for b in range(len(lens)):
+        n = cu[b + 1] - cu[b]
+        if n == 0:
+            continue
+        x = torch.arange(lens[b], device=dev)
+        page = torch.tensor(table[b], device=dev)[x // ps]
+        p = lens[b] - n + torch.arange(n, device=dev)
+        see = x[None, :] <= p[:, None]
+        if window:
+            see &= (x[None, :] > p[:, None] - window) | (x[None, :] < sinks)
+        for h in range(Hkv):
+            k = kp[page, h, x % ps] * ks[page, h][:, None]
+            v = vp[page, h, x % ps] * vs[page, h][:, None]
+            bad = torch.isnan(v)
+            qq = q[cu[b]:cu[b + 1], h * G:h * G + G].double()
+            z = torch.einsum("tgd,sd->tgs", qq, k) * sm
+            most = (qq.abs().flatten(0, 1) @ k.abs().T).nan_to_num(0.0).max()
+            big = max(big, float(most) * abs(sm))
+            z = z.masked_fill(~see[:, None, :], -math.inf)
+            w = torch.softmax(z, -1)
+            o = torch.einsum("tgs,sd->tgd", w, v.nan_to_num(0.0))
+            hit = (see.double() @ bad.double()) > 0          # [n, D]
+            rows = slice(cu[b], cu[b + 1]), slice(h * G, h * G + G)
+            out[rows] = o.masked_fill(hit[:, None, :], math.nan)
+            mass[rows] = torch.einsum("tgs,sd->tgd", w, v.nan_to_num(0.0).abs())
+            lse[rows] = torch.logsumexp(z, -1)
+            top[rows] = (w * vs[page, h]).amax(-1) * lens[b]
+    return out, lse, mass, top, big

@@ -327,21 +327,32 @@ def check_attend(c, G, dtype, window=0, sinks=0, K=0, std=2.0, fault=0, ids=None
     compare(c, q, sm, out, lse, dtype, window, sinks, ids)
 
 
-def compare(c, q, sm, out, lse, dtype, window=0, sinks=0, ids=None):
+def compare(c, q, sm, out, lse, dtype, window=0, sinks=0, ids=None, dense=False):
     kp, ks = c.plain("k")
     vp, vs = c.plain("v")
-    want, want_lse, mass, big = ref.attend(q[:c.T], kp, ks, vp, vs, c.table, c.lens, c.cu, sm,
-                                           window, sinks, None if ids is None else ids[:c.T])
+    if dense:
+        want, want_lse, mass, top, big = ref.attend_dense(
+            q[:c.T].to(DEV), kp.to(DEV), ks.to(DEV), vp.to(DEV), vs.to(DEV), c.table, c.lens, c.cu,
+            sm, window, sinks)
+        want, want_lse, mass, top = want.cpu(), want_lse.cpu(), mass.cpu(), top.cpu()
+    else:
+        want, want_lse, mass, top, big = ref.attend(
+            q[:c.T], kp, ks, vp, vs, c.table, c.lens, c.cu, sm, window, sinks,
+            None if ids is None else ids[:c.T])
     out, lse = out[:c.T].double(), lse[:c.T].double()
     n = max(c.lens + [1]) if ids is None else ids.shape[2] * c.ps
     # A logit: D products added in fp32 (in the tensor cores: cut off, two half steps a term),
     # its factors rounded a few times, the reference's taken off.  A weight: 2^z (2^-22), and on
-    # the bf16 path its rounding to fp16 or to two 8-bit parts, 2^-8 of itself at most (and
-    # below 2^-18 of the largest one lost); sums of n.  The output: rounded once.
+    # the bf16 path its rounding to fp16, 2^-8 of itself at most; sums of n.  The output: rounded
+    # once.  fp16 ends: a weight times its value's scale is held times 2^2 of the reference, which
+    # is at most the row's largest such product, in steps of 2^-24, so that it is off by 2^-27 of
+    # the largest at most, times a code of at most 448, for each of n keys.
     dz = big * (2 * c.D * 2.0 ** -24 + 8 * 2.0 ** -24)
     w = 2 * dz + n * 2.0 ** -24 + 2.0 ** -20
     lost = 2.0 ** -8 if dtype == BF else 0.0
     tol = HALF[dtype] * want.abs() + (2 * w + lost) * (mass + want.abs()) + 2.0 ** -126
+    if dtype == BF:
+        tol = tol + 448 * 2.0 ** -27 * top[..., None]
     nan = torch.isnan(want)
     assert torch.equal(torch.isnan(out), nan)
     worst = ((out - want).abs() - tol)[~nan]
@@ -385,6 +396,81 @@ SHAPES = [  # lens, new, Hkv, G, ps, D
 @pytest.mark.parametrize("lens,new,Hkv,G,ps,D", SHAPES)
 def test_attend(lens, new, Hkv, G, ps, D, window, sinks, dtype):
     check_attend(Case(ps + G, lens, new, Hkv, ps, D), G, dtype, window, sinks)
+
+
+def check_dense(c, G, window=0, sinks=0, std=2.0, q=None, sm=None):
+    q = c.normal(c.T + 1, c.Hkv * G, c.D, std=std) if q is None else q
+    sm = 1.0 / math.sqrt(c.D) if sm is None else sm
+    out, lse, st = run_attend(c, q, sm, window, sinks)
+    assert st == 0
+    assert bool((out[c.T:] == 5.0).all()) and bool((lse[c.T:] == 5.0).all())
+    compare(c, q, sm, out, lse, BF, window, sinks, dense=True)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 0), (300, 200), (1, 1), (700, 5)])
+@pytest.mark.parametrize("lens,new,Hkv,G,ps,D", [
+    ([1500], [700], 2, 16, 64, 128), ([900, 40, 1, 400], [300, 40, 1, 129], 1, 8, 32, 128),
+    ([600, 333], [64, 333], 2, 5, 48, 128), ([520], [520], 1, 64, 16, 128),
+    ([300, 1100], [17, 90], 4, 1, 128, 64), ([700], [200], 1, 128, 64, 64),
+    ([2100], [33], 8, 3, 256, 128), ([4000, 3000, 5], [9, 60, 5], 2, 12, 64, 64)])
+def test_attend_chunks(lens, new, Hkv, G, ps, D, window, sinks):
+    check_dense(Case(ps + G, lens, new, Hkv, ps, D), G, window, sinks)
+
+
+@pytest.mark.parametrize("window", [0, 400])
+def test_attend_chunks_rising_logits(window):
+    """Keys that grow along the sequence, so that references are raised again and again, in the
+    middle of a tile and over several of them; and some that fall."""
+    for grow in (8.0, -8.0):
+        c = Case(41, [1300, 700], [200, 90], 1, 16, 128, spread=0)
+        for row, n in zip(c.table, c.lens):
+            blocks = -(-n // 16)
+            for j in range(blocks):
+                c.scale["k"][row[j]] = 2.0 ** (-7 + round(grow * j / blocks))
+        check_dense(c, 16, window)
+    # single keys far above the rest, at every place of a tile
+    c = Case(42, [700], [150], 1, 64, 128, spread=0)
+    for t in range(0, 700, 37):
+        c.codes["k"][c.table[0][t // 64], 0, t % 64] = 0x7e     # 448
+    q = c.normal(c.T + 1, 16, 128).abs()
+    check_dense(c, 16, window, q=q, sm=0.5)
+
+
+def test_attend_chunks_scales_far_apart():
+    for lo, hi in ((-64, 100), (-30, 30), (-64, -64), (40, 100)):
+        c = Case(43, [500, 300], [80, 90], 1, 16, 128)
+        e = torch.randint(0, 2, c.scale["v"].shape, generator=c.g) * (hi - lo) + lo
+        c.scale["v"] = torch.where(torch.isnan(c.scale["v"]), c.scale["v"], torch.exp2(e.float()))
+        c.codes["v"][c.table[0][1], 0] = 0
+        check_dense(c, 8)
+        c.scale["k"] = torch.where(torch.isnan(c.scale["k"]), c.scale["k"], 2.0 ** 2)
+        check_dense(c, 8, std=0.1)
+
+
+def test_attend_chunks_nan():
+    """NaN codes in keys and values at many places, on and beside the diagonal and the window's
+    edge: what sees them is NaN, nothing else."""
+    for window, sinks in ((0, 0), (130, 0), (60, 20)):
+        c = Case(44, [700, 260], [300, 200], 2, 64, 128)
+        rng = random.Random(3)
+        for b, n in enumerate(c.lens):
+            for _ in range(12):
+                t = rng.randrange(n - c.new[b] // 2, n)
+                row = c.codes["v"][c.table[b][t // 64], rng.randrange(2), t % 64]
+                row[rng.randrange(128)] = 0x7f
+            t = n - 20
+            c.codes["k"][c.table[b][t // 64], 1, t % 64, 5] = 0xff
+        c.codes["v"][c.table[0][0], 0, 3, 77] = 0xff
+        q = c.normal(c.T + 1, 16, 128)
+        q[7, 2, 9], q[250, 12, 0] = math.nan, -math.inf
+        out, lse, st = run_attend(c, q, 0.1, window, sinks)
+        assert bool(torch.isnan(out[7, 2]).all()) and bool(torch.isnan(lse[250, 12]).all())
+        q[7, 2], q[250, 12] = 0.0, 0.0
+        clean = run_attend(c, q, 0.1, window, sinks)
+        compare(c, q, 0.1, clean[0], clean[1], BF, window, sinks, dense=True)
+        for t, h in ((7, 2), (250, 12)):
+            out[t, h], lse[t, h] = clean[0][t, h], clean[1][t, h]
+        assert torch.equal(out.nan_to_num(9.0), clean[0].nan_to_num(9.0))
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -629,7 +715,7 @@ def test_step_in_a_graph():
         compare(c, x[2], sm, sa.out.cpu(), sa.lse.cpu(), BF, ids=ids)
         kp, ks = c.plain("k")
         vp, vs = c.plain("v")
-        want, _, mass, big = ref.attend(x[2][:n], kp, ks, vp, vs, c.table, lens, cu, sm)
+        want, _, mass, _, _ = ref.attend(x[2][:n], kp, ks, vp, vs, c.table, lens, cu, sm)
         tol = 2.0 ** -7 * (mass + want.abs()) + 2.0 ** -10
         assert bool(((da.cpu().double()[:n] - want).abs() <= tol).all())
         # the selection: the scores' own top, own and first block always in it

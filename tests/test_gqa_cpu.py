@@ -158,12 +158,12 @@ def test_scores_and_attention_by_hand():
     assert s[0, 0, 0] == math.inf and s[0, 0, 2] == math.inf and s[0, 0, 3] == -math.inf
     kp = torch.tensor([[[[0.0, 0.0], [0.0, 1.0]]], [[[8.0, 8.0], [1.0, 1.0]]]]).double()
     one = torch.ones((2, 1), dtype=torch.float64)
-    out, lse, _, _ = ref.attend(q, kp, one, kp, one, [[0, 1]], [2], [0, 1], 1.0)
+    out, lse, *_ = ref.attend(q, kp, one, kp, one, [[0, 1]], [2], [0, 1], 1.0)
     assert torch.allclose(out[0, 0], torch.tensor([0.0, 0.75]).double(), atol=1e-7)
     assert torch.allclose(lse[0], torch.tensor([4.0, 2.0]).log().double(), atol=1e-7)
-    out, lse, _, _ = ref.attend(q, kp, one, kp, one, [[0, 1]], [2], [0, 1], 1.0,
+    out, lse, *_ = ref.attend(q, kp, one, kp, one, [[0, 1]], [2], [0, 1], 1.0,
                                 ids=torch.tensor([[[0, 0, -1]]]))
     assert torch.allclose(lse[0], torch.tensor([8.0, 4.0]).log().double(), atol=1e-7)
-    out, lse, _, _ = ref.attend(q, kp, one, kp, one, [[0, 1]], [2], [0, 1], 1.0,
+    out, lse, *_ = ref.attend(q, kp, one, kp, one, [[0, 1]], [2], [0, 1], 1.0,
                                 ids=torch.tensor([[[-1, 1, -1]]]))
     assert out.abs().max() == 0 and bool((lse == -math.inf).all())
