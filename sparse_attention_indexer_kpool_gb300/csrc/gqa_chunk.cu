@@ -1026,7 +1026,7 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
   if (launch_kernel(&l.cfg, gqa_chunk_kernel<kD>, k_map, v_map, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   const JoinArgs j{p.part_o, p.part_ml, p.head, n_cta, static_cast<__nv_bfloat16*>(a.out), a.lse};
-  return launch_join<kD>(j, Rows{a.Hq, a.kv.Hkv, p.G, p.per}, stream);
+  return launch_join<kD>(j, Rows{a.Hq, a.kv.Hkv, p.G, p.per}, (long long)a.T * a.kv.Hkv, stream);
 }
 
 }  // namespace

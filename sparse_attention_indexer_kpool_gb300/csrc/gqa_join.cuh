@@ -222,9 +222,12 @@ inline bool code_map(CUtensorMap* m, const void* base, uint64_t rows, int D, uin
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// items: of the step, at most
 template <int kD, typename Rows>
-int launch_join(const JoinArgs& p, const Rows& rows, cudaStream_t stream) {
-  Launch l(dim3(2 * num_sms(), 1, 1), kJoinThreads, 0, stream);
+int launch_join(const JoinArgs& p, const Rows& rows, long long items, cudaStream_t stream) {
+  const long long pieces = (items < p.workers ? items : p.workers) * Rows::kRows;
+  const int grid = pieces < 2 * num_sms() ? (int)pieces : 2 * num_sms();
+  Launch l(dim3(grid, 1, 1), kJoinThreads, 0, stream);
   return launch_kernel(&l.cfg, gqa_join_kernel<kD, Rows>, p, rows) == cudaSuccess ? DSA_OK
                                                                                   : DSA_ERR_CUDA;
 }

@@ -40,6 +40,7 @@ constexpr int kW = 8, kThreads = 32 * kW;
 constexpr int kKeys = 32;                      // of a tile
 constexpr float kRaise = 15.f;                 // e above which a reference is raised
 constexpr int kExtra = 1;                      // what a row tile costs beside its tiles, in tiles
+constexpr int kLeast = 2;                      // tiles of a share, at least
 constexpr int kRingBytes = 3 * 2 * kKeys * 128;  // of a warp
 
 struct Params {
@@ -51,6 +52,7 @@ struct Params {
   float* part_o;             // [2 workers][8 kN][D]
   float4* part_ml;           // [2 workers][8 kN]: reference; the sum f 2^z as z and f
   Header* head;              // [workers]
+  int workers;               // warps that take a share, at most gridDim.x * kW
 };
 
 // ---- the batch as tiles --------------------------------------------------------
@@ -188,18 +190,29 @@ __device__ __forceinline__ void find_shares(const Params& p, Start* st,
     total += scan[w];
   }
   if (falls) total = 0;
-  const unsigned workers = gridDim.x * kW;
-  for (int w = 0; w < kW; ++w) {
+  // the shares' ends, by a thread for each warp
+  if (tid < kW) {
     // neighbours in the keys are neighbours in their numbers, and few shares lie on many SMs
-    const unsigned me = (unsigned)w * gridDim.x + blockIdx.x;
-    unsigned long long v0, v1;
-    if (total < workers) {
-      v0 = me < total ? me : total;
-      v1 = me < total ? me + 1 : total;
-    } else {
-      v0 = total * me / workers;
-      v1 = total * (me + 1) / workers;
+    const unsigned me = (unsigned)tid * gridDim.x + blockIdx.x, workers = (unsigned)p.workers;
+    unsigned long long v0 = 0, v1 = 0;
+    if (me < workers) {
+      if (total < workers) {
+        v0 = me < total ? me : total;
+        v1 = me < total ? me + 1 : total;
+      } else if (total < (1u << 21)) {  // (2,048 workers at most: a product of 32 bits)
+        v0 = (unsigned)total * me / workers;
+        v1 = (unsigned)total * (me + 1) / workers;
+      } else {
+        v0 = total * me / workers;
+        v1 = total * (me + 1) / workers;
+      }
     }
+    st[tid].n = v1 - v0;
+    scan[kW + tid] = v0;
+  }
+  __syncthreads();
+  for (int w = 0; w < kW; ++w) {
+    const unsigned long long v0 = scan[kW + w], v1 = v0 + st[w].n;
     if (v0 < v1 && v0 >= before && v0 < before + mine) {
       unsigned long long at = before;
       for (int b = b0; b < b1; ++b) {
@@ -208,9 +221,8 @@ __device__ __forceinline__ void find_shares(const Params& p, Start* st,
         if (v0 < at + all) {
           const unsigned long long off = v0 - at;
           st[w].b = b;
-          st[w].row = (unsigned)(off / s.u);
+          st[w].row = (unsigned)(off >> 32 ? off / s.u : (unsigned)off / s.u);
           st[w].unit = (unsigned)(off - (unsigned long long)st[w].row * s.u);
-          st[w].n = v1 - v0;
           break;
         }
         at += all;
@@ -275,7 +287,7 @@ struct Ctl {
   uint64_t full[kW][kStages];
   Meta meta[kW][kStages];
   Start start[kW];
-  unsigned long long scan[kW];
+  unsigned long long scan[2 * kW];
 };
 
 template <int kD>
@@ -731,11 +743,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) flag(p.a.status, DSA_DEV_TIMEOUT);
     hd = Header{-1, -1, 0, 0};
   }
-  if (lane == 0) p.head[worker] = hd;
+  if (lane == 0 && worker < p.workers) p.head[worker] = hd;
 }
 
 // ---- launches ----------------------------------------------------------------------
-int workers_of() { return num_sms() * kW < kMaxWorkers ? num_sms() * kW : kMaxWorkers; }
+int workers_of() { return num_sms() * kW < kMaxWorkers ? num_sms() * kW : kMaxWorkers / kW * kW; }
 
 // The heads of a row tile (gqa_join.cuh).
 template <int kN>
@@ -759,7 +771,16 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
   p.zscale = a.sm_scale * kLog2e;
   p.cap = table_cap(a.kv.max_pages, a.kv.page_size);
   p.per_block = a.kv.page_size / kR;
-  const int grid = workers_of() / kW, workers = grid * kW;
+  // Workers: a warp for each kLeast tiles of what the step can hold, all of them at most.
+  const long long row_tiles = (long long)a.T * a.kv.Hkv * p.hb;
+  const long long seen = a.block_ids ? (long long)a.K * a.kv.page_size
+                         : a.window > 0 && (long long)a.window + a.sinks < p.cap
+                             ? (long long)a.window + a.sinks : p.cap;
+  const long long bound = row_tiles * ((seen + kKeys - 1) / kKeys + kExtra);
+  const long long want = (bound + kLeast - 1) / kLeast;
+  const int most = workers_of(), workers = want < most ? (int)want : most;
+  const int grid = workers < num_sms() ? workers : num_sms();
+  p.workers = workers;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float4*>(p.part_o + (size_t)workers * 2 * 8 * kN * kD);
   p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)workers * 2 * 8 * kN);
@@ -774,7 +795,7 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
   Launch l(dim3(grid, 1, 1), kThreads, smem_bytes<kD>(), stream);
   if (launch_kernel(&l.cfg, kernel, k_map, v_map, p) != cudaSuccess) return DSA_ERR_CUDA;
   const JoinArgs j{p.part_o, p.part_ml, p.head, workers, static_cast<__nv_bfloat16*>(a.out), a.lse};
-  return launch_join<kD>(j, Rows<kN>{a.Hq, a.kv.Hkv, p.G, p.hb}, stream);
+  return launch_join<kD>(j, Rows<kN>{a.Hq, a.kv.Hkv, p.G, p.hb}, row_tiles, stream);
 }
 
 template <int kD, int kN>
