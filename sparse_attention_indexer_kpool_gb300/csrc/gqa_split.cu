@@ -18,7 +18,7 @@
 //
 // Why like this.  A decode step reads every key and value once and computes 2 G products for
 // each byte: it is bound by memory, and what counts is bytes on their way and no pause in
-// them.  So no warp waits for another: each has a ring of three 8 KB tiles (32 keys and
+// them.  So no warp waits for another: each has a ring of two 8 KB tiles (32 keys and
 // their values) that TMA fills in the 128-byte swizzle, runs through its share of the
 // batch's tiles, and keeps scores, weights and outputs in registers: an S^T accumulator
 // holds a key's row in four lanes, movmatrix turns it into the second factor of O^T, and
@@ -41,7 +41,7 @@ constexpr int kKeys = 32;                      // of a tile
 constexpr float kRaise = 15.f;                 // e above which a reference is raised
 constexpr int kExtra = 1;                      // what a row tile costs beside its tiles, in tiles
 constexpr int kLeast = 2;                      // tiles of a share, at least
-constexpr int kRingBytes = 3 * 2 * kKeys * 128;  // of a warp
+constexpr int kRingBytes = 2 * 2 * kKeys * 128;  // of a warp
 
 struct Params {
   GqaArgs a;
@@ -508,149 +508,186 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long at = (long long)mt.pos[i] + (kBoxes == 1 ? r : r % kR);
         return at <= w.pos && (at >= w.lo || at < w.s0);
       };
-      // S^T: 16 keys at a time
-      float e[2][kN][4];
+      // The tile, in two forms: a short one for what most are (kPlain: every key seen, every head
+      // with a reference that holds, scales not far apart), which does nothing and says so where a
+      // weight is too large, and one for everything.
+      auto tile = [&](auto form) -> bool {
+        constexpr bool kPlain = decltype(form)::value;
+        // S^T: 16 keys at a time
+        float e[2][kN][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
+          for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[j][n][i] = 0.f;
-        const int r0 = 16 * j + key_of(g);
+            for (int i = 0; i < 4; ++i) e[j][n][i] = 0.f;
+          const int r0 = 16 * j + key_of(g);
 #pragma unroll
-        for (int i = 0; i < kD / 64; ++i) {
-          const uint4 x = lds128(kb + chunk_at<kD>(r0, 4 * i + t));
-          const uint4 y = lds128(kb + chunk_at<kD>(r0 + 8, 4 * i + t));
-          const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
+          for (int i = 0; i < kD / 64; ++i) {
+            const uint4 x = lds128(kb + chunk_at<kD>(r0, 4 * i + t));
+            const uint4 y = lds128(kb + chunk_at<kD>(r0 + 8, 4 * i + t));
+            const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t a0 = codes2_f16(xa[k] & 0xffffu), a2 = codes2_f16(xa[k] >> 16);
-            const uint32_t a1 = codes2_f16(ya[k] & 0xffffu), a3 = codes2_f16(ya[k] >> 16);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a0 = codes2_f16(xa[k] & 0xffffu), a2 = codes2_f16(xa[k] >> 16);
+              const uint32_t a1 = codes2_f16(ya[k] & 0xffffu), a3 = codes2_f16(ya[k] >> 16);
 #pragma unroll
-            for (int n = 0; n < kN; ++n)
-              mma_f16(e[j][n], a0, a1, a2, a3, q[n][4 * i + k][0], q[n][4 * i + k][1]);
+              for (int n = 0; n < kN; ++n)
+                mma_f16(e[j][n], a0, a1, a2, a3, q[n][4 * i + k][0], q[n][4 * i + k][1]);
+            }
           }
         }
-      }
-      // exponents of the weights; columns 2 t and 2 t + 1
-      bool raise = unset;
+        // exponents of the weights; columns 2 t and 2 t + 1
+        bool raise = !kPlain && unset;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int box = kBoxes == 1 ? 0 : j;
-        const float ks = mt.ks[box], lv8 = (float)(mt.ev[box] + kUp);
-        const bool see0 = all || seen(16 * j + key_of(g));
-        const bool see1 = all || seen(16 * j + key_of(g) + 8);
+        for (int j = 0; j < 2; ++j) {
+          const int box = kBoxes == 1 ? 0 : j;
+          const float ks = mt.ks[box], lv8 = (float)(mt.ev[box] + kUp);
+          const bool see0 = kPlain || all || seen(16 * j + key_of(g));
+          const bool see1 = kPlain || all || seen(16 * j + key_of(g) + 8);
+          float top = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
+          for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float mm = m[n][i & 1], ref = mm == -INFINITY ? 0.f : mm;
-            const float x = fmaf(e[j][n][i], qs[n][i & 1] * ks, lv8 - ref);
-            e[j][n][i] = (i < 2 ? see0 : see1) ? x : -INFINITY;
-            raise |= e[j][n][i] > kRaise;
-          }
-      }
-      if (__any_sync(0xffffffffu, raise)) {
-        unset = false;
-#pragma unroll
-        for (int n = 0; n < kN; ++n)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float top0 = across_keys(fmaxf(e[0][n][i], e[0][n][i + 2]));
-            const float top1 = across_keys(fmaxf(e[1][n][i], e[1][n][i + 2]));
-            const int lv = mt.ev[kBoxes == 2 && top1 > top0 ? 1 : 0] + kUp;
-            const float rel = fmaxf(top0, top1) - (float)kUp;
-            float move = 0.f;
-            if (m[n][i] == -INFINITY) {  // nothing accumulated for this head yet
-              if (rel != -INFINITY) {
-                m[n][i] = rel;
-                move = -rel;
-                base[n][i] = lv;
-              }
-            } else if (rel > kRaise - (float)kUp) {
-              m[n][i] += rel;
-              move = -rel;
-              // (the square roots, taken twice: weights may lie further apart than a float reaches)
-              const float a = ex2_fast(-0.5f * rel);
-              int to = lv;
-              if ((float)(lv - base[n][i]) - rel > 60.f)
-                to = (int)floorf((float)base[n][i] + rel + 60.f);
-              const float f = ex2_fast(0.5f * ((float)(to - base[n][i]) - rel));
-              base[n][i] = to;
-              l[n][i] = l[n][i] * f * f;
-#pragma unroll
-              for (int k = 0; k < kM; ++k) {
-                o[k][n][i] = o[k][n][i] * a * a;
-                o[k][n][i + 2] = o[k][n][i + 2] * a * a;
-              }
+            for (int i = 0; i < 4; ++i) {
+              const float mm = m[n][i & 1], ref = !kPlain && mm == -INFINITY ? 0.f : mm;
+              const float x = fmaf(e[j][n][i], qs[n][i & 1] * ks, lv8 - ref);
+              e[j][n][i] = (i < 2 ? see0 : see1) ? x : -INFINITY;
+              top = fmaxf(top, e[j][n][i]);
             }
-            // (an infinite maximum: its key's weight is NaN, as in the formula)
-            e[0][n][i] += move;
-            e[0][n][i + 2] += move;
-            e[1][n][i] += move;
-            e[1][n][i + 2] += move;
-            unset |= m[n][i] == -INFINITY;
-          }
-      }
-      // weights; O^T
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int box = kBoxes == 1 ? 0 : j;
-        const int lv = mt.ev[box] + kUp;
-        uint32_t b[kN][2];
-        bool far = false;  // this box's scale lies far below the reference's
-#pragma unroll
-        for (int n = 0; n < kN; ++n) far |= max(base[n][0], base[n][1]) - lv > 64;
-        far = __any_sync(0xffffffffu, far);
-        if (far) {
+          raise |= top > kRaise;
+        }
+        raise = __any_sync(0xffffffffu, raise);
+        if (kPlain && raise) return false;
+        if (!kPlain && raise) {
+          unset = false;
 #pragma unroll
           for (int n = 0; n < kN; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float d = (float)(base[n][i] - lv);
-              float x = e[j][n][i] + d, y = e[j][n][i + 2] + d;
-              if (across_keys(fmaxf(x, y)) > 100.f) {
-                base[n][i] -= 100;
-                l[n][i] *= 0x1p-100f;
-                x -= 100.f;
-                y -= 100.f;
+              const float top0 = across_keys(fmaxf(e[0][n][i], e[0][n][i + 2]));
+              const float top1 = across_keys(fmaxf(e[1][n][i], e[1][n][i + 2]));
+              const int lv = mt.ev[kBoxes == 2 && top1 > top0 ? 1 : 0] + kUp;
+              const float rel = fmaxf(top0, top1) - (float)kUp;
+              float move = 0.f;
+              if (m[n][i] == -INFINITY) {  // nothing accumulated for this head yet
+                if (rel != -INFINITY) {
+                  m[n][i] = rel;
+                  move = -rel;
+                  base[n][i] = lv;
+                }
+              } else if (rel > kRaise - (float)kUp) {
+                m[n][i] += rel;
+                move = -rel;
+                // (the square roots, taken twice: weights may lie further apart than a float reaches)
+                const float a = ex2_fast(-0.5f * rel);
+                int to = lv;
+                if ((float)(lv - base[n][i]) - rel > 60.f)
+                  to = (int)floorf((float)base[n][i] + rel + 60.f);
+                const float f = ex2_fast(0.5f * ((float)(to - base[n][i]) - rel));
+                base[n][i] = to;
+                l[n][i] = l[n][i] * f * f;
+#pragma unroll
+                for (int k = 0; k < kM; ++k) {
+                  o[k][n][i] = o[k][n][i] * a * a;
+                  o[k][n][i + 2] = o[k][n][i + 2] * a * a;
+                }
               }
-              l[n][i] += ex2_fast(x) + ex2_fast(y);
+              // (an infinite maximum: its key's weight is NaN, as in the formula)
+              e[0][n][i] += move;
+              e[0][n][i + 2] += move;
+              e[1][n][i] += move;
+              e[1][n][i + 2] += move;
+              unset |= m[n][i] == -INFINITY;
             }
         }
+        // weights; O^T
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
+        for (int j = 0; j < 2; ++j) {
+          const int box = kBoxes == 1 ? 0 : j;
+          const int lv = mt.ev[box] + kUp;
+          uint32_t b[kN][2];
+          bool far = false;  // this box's scale lies far below the reference's
+          if (!kPlain) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[j][n][i] = ex2_fast(e[j][n][i]);
-          if (!far) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              l[n][i] = fmaf(e[j][n][i] + e[j][n][i + 2], pow2(max(base[n][i] - lv, -126)),
-                             l[n][i]);
+            for (int n = 0; n < kN; ++n) far |= max(base[n][0], base[n][1]) - lv > 64;
+            far = __any_sync(0xffffffffu, far);
           }
-          b[n][0] = transpose8(pack_f16(e[j][n][0], e[j][n][1]));
-          b[n][1] = transpose8(pack_f16(e[j][n][2], e[j][n][3]));
-        }
-        // the values of four keys: of the products' k = 2 t, 2 t + 1 and eight on
-        const int r0 = 16 * j + key_of(2 * t), r1 = 16 * j + key_of(2 * t + 1);
-        const int rs[4] = {r0, r1, r0 + 8, r1 + 8};
-        if constexpr (kD == 128) {  // lane (g, t): columns 16 g ..
-          uint32_t x[4][4];
+          if (far) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 y = lds128(vb + chunk_at<kD>(rs[i], g));
-            if (!all && !seen(rs[i])) y = make_uint4(0u, 0u, 0u, 0u);
-            x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float d = (float)(base[n][i] - lv);
+                float x = e[j][n][i] + d, y = e[j][n][i + 2] + d;
+                if (across_keys(fmaxf(x, y)) > 100.f) {
+                  base[n][i] -= 100;
+                  l[n][i] *= 0x1p-100f;
+                  x -= 100.f;
+                  y -= 100.f;
+                }
+                l[n][i] += ex2_fast(x) + ex2_fast(y);
+              }
           }
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int n = 0; n < kN; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[j][n][i] = ex2_fast(e[j][n][i]);
+            if (!far) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                l[n][i] = fmaf(e[j][n][i] + e[j][n][i + 2], pow2(max(base[n][i] - lv, -126)),
+                               l[n][i]);
+            }
+            b[n][0] = transpose8(pack_f16(e[j][n][0], e[j][n][1]));
+            b[n][1] = transpose8(pack_f16(e[j][n][2], e[j][n][3]));
+          }
+          // the values of four keys: of the products' k = 2 t, 2 t + 1 and eight on
+          const int r0 = 16 * j + key_of(2 * t), r1 = 16 * j + key_of(2 * t + 1);
+          const int rs[4] = {r0, r1, r0 + 8, r1 + 8};
+          if constexpr (kD == 128) {  // lane (g, t): columns 16 g ..
+            uint32_t x[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 y = lds128(vb + chunk_at<kD>(rs[i], g));
+              if (!kPlain && !all && !seen(rs[i])) y = make_uint4(0u, 0u, 0u, 0u);
+              x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const uint32_t sel = u ? 0x7362u : 0x5140u;
+                const uint32_t a0 = __byte_perm(x[0][k], x[1][k], sel);
+                const uint32_t a1 = __byte_perm(x[0][k + 2], x[1][k + 2], sel);
+                const uint32_t a2 = __byte_perm(x[2][k], x[3][k], sel);
+                const uint32_t a3 = __byte_perm(x[2][k + 2], x[3][k + 2], sel);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const uint32_t f0 = codes2_f16(z ? a0 >> 16 : a0 & 0xffffu);
+                  const uint32_t f1 = codes2_f16(z ? a1 >> 16 : a1 & 0xffffu);
+                  const uint32_t f2 = codes2_f16(z ? a2 >> 16 : a2 & 0xffffu);
+                  const uint32_t f3 = codes2_f16(z ? a3 >> 16 : a3 & 0xffffu);
+#pragma unroll
+                  for (int n = 0; n < kN; ++n)
+                    mma_f16(o[4 * k + 2 * u + z][n], f0, f1, f2, f3, b[n][0], b[n][1]);
+                }
+              }
+          } else {  // columns 8 g ..
+            uint32_t x[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint2 y = lds64(vb + chunk_at<kD>(rs[i], g >> 1) + 8 * (g & 1));
+              if (!kPlain && !all && !seen(rs[i])) y = make_uint2(0u, 0u);
+              x[i][0] = y.x; x[i][1] = y.y;
+            }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const uint32_t sel = u ? 0x7362u : 0x5140u;
-              const uint32_t a0 = __byte_perm(x[0][k], x[1][k], sel);
-              const uint32_t a1 = __byte_perm(x[0][k + 2], x[1][k + 2], sel);
-              const uint32_t a2 = __byte_perm(x[2][k], x[3][k], sel);
-              const uint32_t a3 = __byte_perm(x[2][k + 2], x[3][k + 2], sel);
+              const uint32_t a0 = __byte_perm(x[0][0], x[1][0], sel);
+              const uint32_t a1 = __byte_perm(x[0][1], x[1][1], sel);
+              const uint32_t a2 = __byte_perm(x[2][0], x[3][0], sel);
+              const uint32_t a3 = __byte_perm(x[2][1], x[3][1], sel);
 #pragma unroll
               for (int z = 0; z < 2; ++z) {
                 const uint32_t f0 = codes2_f16(z ? a0 >> 16 : a0 & 0xffffu);
@@ -659,37 +696,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t f3 = codes2_f16(z ? a3 >> 16 : a3 & 0xffffu);
 #pragma unroll
                 for (int n = 0; n < kN; ++n)
-                  mma_f16(o[4 * k + 2 * u + z][n], f0, f1, f2, f3, b[n][0], b[n][1]);
+                  mma_f16(o[2 * u + z][n], f0, f1, f2, f3, b[n][0], b[n][1]);
               }
-            }
-        } else {  // columns 8 g ..
-          uint32_t x[4][2];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint2 y = lds64(vb + chunk_at<kD>(rs[i], g >> 1) + 8 * (g & 1));
-            if (!all && !seen(rs[i])) y = make_uint2(0u, 0u);
-            x[i][0] = y.x; x[i][1] = y.y;
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t sel = u ? 0x7362u : 0x5140u;
-            const uint32_t a0 = __byte_perm(x[0][0], x[1][0], sel);
-            const uint32_t a1 = __byte_perm(x[0][1], x[1][1], sel);
-            const uint32_t a2 = __byte_perm(x[2][0], x[3][0], sel);
-            const uint32_t a3 = __byte_perm(x[2][1], x[3][1], sel);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t f0 = codes2_f16(z ? a0 >> 16 : a0 & 0xffffu);
-              const uint32_t f1 = codes2_f16(z ? a1 >> 16 : a1 & 0xffffu);
-              const uint32_t f2 = codes2_f16(z ? a2 >> 16 : a2 & 0xffffu);
-              const uint32_t f3 = codes2_f16(z ? a3 >> 16 : a3 & 0xffffu);
-#pragma unroll
-              for (int n = 0; n < kN; ++n)
-                mma_f16(o[2 * u + z][n], f0, f1, f2, f3, b[n][0], b[n][1]);
             }
           }
         }
-      }
+        return true;
+      };
+      int far = 0;
+#pragma unroll
+      for (int n = 0; n < kN; ++n) far = max(far, max(base[n][0], base[n][1]));
+      far -= (kBoxes == 1 ? mt.ev[0] : min(mt.ev[0], mt.ev[1])) + kUp;
+      if (__any_sync(0xffffffffu, !all || unset || far > 64) || !tile(std::true_type{}))
+        tile(std::false_type{});
       __syncwarp();  // the tile is read
       issue();
     }
