@@ -308,24 +308,53 @@ def dsa_mla_paged_chunk(q_lat, pages, row_scale, block_table, seq_lens, page_siz
     _check("dsa_mla_paged_chunk", code)
 
 
-def _gqa_codes(t):
-    """Pages of codes: float8_e4m3fn or uint8."""
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-        raise TypeError(f"pages must be float8_e4m3fn or uint8 codes, got {t.dtype}")
-    return t.dtype
+_is_contiguous, _get_device, _data_ptr = (torch.Tensor.is_contiguous, torch.Tensor.get_device,
+                                          torch.Tensor.data_ptr)
+_CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _gqa_cache(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_new):
-    """A grouped-query cache's geometry, once its tensors' shapes agree."""
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+def _pointers(dev, tensors, dtypes):
+    """Pointers of ``tensors``, contiguous and on CUDA device ``dev``; None if one is not, or of
+    another type: ``_args`` then says which.  (The loops over a call's tensors run in C: eleven
+    tensors 2.1 us, 3.0 in ``_args``.)"""
+    try:
+        if ([t.dtype for t in tensors] == dtypes and all(map(_is_contiguous, tensors))
+                and set(map(_get_device, tensors)) == {dev} and dev >= 0):
+            return list(map(_data_ptr, tensors))
+    except (AttributeError, TypeError):
+        pass
+    return None
+
+
+def _gqa_device(t, stream):
+    if stream is None and t.is_cuda:
+        dev = torch._C._cuda_getDevice()
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return _device(t, stream)
+
+
+def _gqa_wrong(dev, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu, *more):
+    """Raise for what ``_pointers`` turned down."""
+    if k_pages.dtype not in _CODES:
+        raise TypeError(f"pages must be float8_e4m3fn or uint8 codes, got {k_pages.dtype}")
+    _args(dev, (k_pages, k_pages.dtype, "k_pages"), (v_pages, k_pages.dtype, "v_pages"),
+          (k_scale, _F32, "k_scale"), (v_scale, _F32, "v_scale"),
+          (block_table, _I32, "block_table"), (seq_lens, _I32, "seq_lens"), (cu, _I32, "cu"), *more)
+    raise ValueError("tensors of the call disagree")
+
+
+def _gqa_shapes(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu):
+    """(n_pages, Hkv, D, B) of a grouped-query cache whose tensors' shapes agree."""
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page_size, D]")
-    n_pages, Hkv, page_size, D = k_pages.shape
+    n_pages, Hkv, _, D = shape
     if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0]:
         raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
-    B, width = block_table.shape
-    _sizes((k_scale, n_pages * Hkv, "k_scale"), (v_scale, n_pages * Hkv, "v_scale"),
-           (cu_new, B + 1, "cu_new"))
-    return n_pages, Hkv, page_size, D, B, width
+    B, n = seq_lens.numel(), n_pages * Hkv
+    if (k_scale.numel(), v_scale.numel(), cu.numel()) != (n, n, B + 1):
+        _sizes((k_scale, n, "k_scale"), (v_scale, n, "v_scale"), (cu, B + 1, "cu_new"))
+    return n_pages, Hkv, D, B
 
 
 def dsa_gqa_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_new,
@@ -334,44 +363,65 @@ def dsa_gqa_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table
     ``k_pages``, ``v_pages`` [n_pages, Hkv, page_size, D] (float8_e4m3fn or uint8 codes) with
     ``k_scale``, ``v_scale`` [n_pages, Hkv] fp32; ``k_mean`` [n_pages, Hkv, D] bf16 gets the mean
     key of every block that becomes complete.  ``seq_lens`` counts the new tokens."""
-    n_pages, Hkv, ps, D, B, width = _gqa_cache(k_pages, v_pages, k_scale, v_scale, block_table,
-                                               seq_lens, cu_new)
-    if k_new.dim() != 3 or k_new.shape[1:] != (Hkv, D) or v_new.shape != k_new.shape:
+    n_pages, Hkv, D, B = _gqa_shapes(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
+                                     cu_new)
+    shape, act = k_new.shape, k_new.dtype
+    if len(shape) != 3 or shape[1] != Hkv or shape[2] != D or v_new.shape != shape:
         raise ValueError("k_new and v_new must be [T, Hkv, D]")
-    act, codes = k_new.dtype, _gqa_codes(k_pages)
-    _sizes((k_mean, n_pages * Hkv * D, "k_mean"))
-    dev, st = _device(k_new, stream)
-    kn, vn, kp, vp, ks, vs, table, lens, cu, mean, status = _args(
-        dev, (k_new, act, "k_new"), (v_new, act, "v_new"), (k_pages, codes, "k_pages"),
-        (v_pages, codes, "v_pages"), (k_scale, _F32, "k_scale"), (v_scale, _F32, "v_scale"),
-        (block_table, _I32, "block_table"), (seq_lens, _I32, "seq_lens"), (cu_new, _I32, "cu_new"),
-        (k_mean, torch.bfloat16, "k_mean"), (status, _I32, "status"))
-    kv = _lib.GqaKv(kp, vp, ks, vs, table, lens, n_pages, ps, width, Hkv, D)
-    code = _lib.load().dsa_gqa_append(kn, vn, cu, k_new.shape[0], B, _dtype_tag(k_new),
-                                      ctypes.byref(kv), mean, status, st)
-    _check("dsa_gqa_append", code)
+    if k_mean is not None and k_mean.numel() != n_pages * Hkv * D:
+        _sizes((k_mean, n_pages * Hkv * D, "k_mean"))
+    dev, st = _gqa_device(k_new, stream)
+    codes = k_pages.dtype
+    tensors = [k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_new, k_new, v_new]
+    dtypes = [codes, codes, _F32, _F32, _I32, _I32, _I32, act, act]
+    if k_mean is not None:
+        tensors.append(k_mean)
+        dtypes.append(torch.bfloat16)
+    if status is not None:
+        tensors.append(status)
+        dtypes.append(_I32)
+    p = _pointers(dev, tensors, dtypes)
+    if p is None or codes not in _CODES:
+        _gqa_wrong(dev, *tensors[:7], (k_new, act, "k_new"), (v_new, act, "v_new"),
+                   (k_mean, torch.bfloat16, "k_mean"), (status, _I32, "status"))
+    kv = _lib.GqaKv(p[0], p[1], p[2], p[3], p[4], p[5], n_pages, k_pages.shape[2],
+                    block_table.shape[1], Hkv, D)
+    code = _lib.load().dsa_gqa_append(
+        p[7], p[8], p[6], shape[0], B, _dtype_tag(k_new), ctypes.byref(kv),
+        None if k_mean is None else p[9], None if status is None else p[-1], st)
+    if code:
+        _check("dsa_gqa_append", code)
 
 
 def dsa_gqa_read(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_out, k_out, v_out,
                  begin=None, status=None, stream=None):
     """Bring rows of the cache back: ``k_out``, ``v_out`` [T, Hkv, D] rows ``cu_out[b]`` .. get
     positions ``begin[b]`` .. (``begin`` [B] or None: 0) of sequence b."""
-    n_pages, Hkv, ps, D, B, width = _gqa_cache(k_pages, v_pages, k_scale, v_scale, block_table,
-                                               seq_lens, cu_out)
-    if k_out.dim() != 3 or k_out.shape[1:] != (Hkv, D) or v_out.shape != k_out.shape:
+    n_pages, Hkv, D, B = _gqa_shapes(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
+                                     cu_out)
+    shape, act = k_out.shape, k_out.dtype
+    if len(shape) != 3 or shape[1] != Hkv or shape[2] != D or v_out.shape != shape:
         raise ValueError("k_out and v_out must be [T, Hkv, D]")
-    act, codes = k_out.dtype, _gqa_codes(k_pages)
     _sizes((begin, B, "begin"))
-    dev, st = _device(k_pages, stream)
-    kp, vp, ks, vs, table, lens, cu, first, ko, vo, status = _args(
-        dev, (k_pages, codes, "k_pages"), (v_pages, codes, "v_pages"), (k_scale, _F32, "k_scale"),
-        (v_scale, _F32, "v_scale"), (block_table, _I32, "block_table"),
-        (seq_lens, _I32, "seq_lens"), (cu_out, _I32, "cu_out"), (begin, _I32, "begin"),
-        (k_out, act, "k_out"), (v_out, act, "v_out"), (status, _I32, "status"))
-    kv = _lib.GqaKv(kp, vp, ks, vs, table, lens, n_pages, ps, width, Hkv, D)
-    code = _lib.load().dsa_gqa_read(ctypes.byref(kv), cu, first, k_out.shape[0], B,
-                                    _dtype_tag(k_out), ko, vo, status, st)
-    _check("dsa_gqa_read", code)
+    dev, st = _gqa_device(k_pages, stream)
+    codes = k_pages.dtype
+    tensors = [k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_out, k_out, v_out]
+    dtypes = [codes, codes, _F32, _F32, _I32, _I32, _I32, act, act]
+    for t in (begin, status):
+        if t is not None:
+            tensors.append(t)
+            dtypes.append(_I32)
+    p = _pointers(dev, tensors, dtypes)
+    if p is None or codes not in _CODES:
+        _gqa_wrong(dev, *tensors[:7], (k_out, act, "k_out"), (v_out, act, "v_out"),
+                   (begin, _I32, "begin"), (status, _I32, "status"))
+    kv = _lib.GqaKv(p[0], p[1], p[2], p[3], p[4], p[5], n_pages, k_pages.shape[2],
+                    block_table.shape[1], Hkv, D)
+    code = _lib.load().dsa_gqa_read(
+        ctypes.byref(kv), p[6], None if begin is None else p[9], shape[0], B, _dtype_tag(k_out),
+        p[7], p[8], None if status is None else p[-1], st)
+    if code:
+        _check("dsa_gqa_read", code)
 
 
 def dsa_gqa_block_scores(q, k_mean, block_table, seq_lens, page_size, cu_new, sink_blocks,
@@ -388,19 +438,28 @@ def dsa_gqa_block_scores(q, k_mean, block_table, seq_lens, page_size, cu_new, si
     T, Hq, D = q.shape
     n_pages, Hkv, _ = k_mean.shape
     B, width = block_table.shape
-    if scores.dim() != 3 or scores.shape[:2] != (T, Hkv):
+    wide = scores.shape
+    if len(wide) != 3 or wide[0] != T or wide[1] != Hkv:
         raise ValueError("scores must be [T, Hkv, NB]")
-    _sizes((cu_new, B + 1, "cu_new"))
-    dev, st = _device(q, stream)
-    qp, mean, table, lens, cu, sc, status = _args(
-        dev, (q, q.dtype, "q"), (k_mean, torch.bfloat16, "k_mean"),
-        (block_table, _I32, "block_table"), (seq_lens, _I32, "seq_lens"), (cu_new, _I32, "cu_new"),
-        (scores, _F32, "scores"), (status, _I32, "status"))
+    if cu_new.numel() != B + 1:
+        _sizes((cu_new, B + 1, "cu_new"))
+    dev, st = _gqa_device(q, stream)
+    tensors = [q, k_mean, block_table, seq_lens, cu_new, scores]
+    dtypes = [q.dtype, torch.bfloat16, _I32, _I32, _I32, _F32]
+    if status is not None:
+        tensors.append(status)
+        dtypes.append(_I32)
+    p = _pointers(dev, tensors, dtypes)
+    if p is None:
+        _args(dev, *zip(tensors, dtypes, ("q", "k_mean", "block_table", "seq_lens", "cu_new",
+                                          "scores", "status")))
+        raise ValueError("tensors of the call disagree")
     code = _lib.load().dsa_gqa_block_scores(
-        qp, mean, table, lens, cu, T, B, Hq, Hkv, D, n_pages, int(page_size), width,
-        int(sink_blocks), int(local_blocks), float(sm_scale), scores.shape[2], _dtype_tag(q), sc,
-        status, st)
-    _check("dsa_gqa_block_scores", code)
+        p[0], p[1], p[2], p[3], p[4], T, B, Hq, Hkv, D, n_pages, int(page_size), width,
+        int(sink_blocks), int(local_blocks), float(sm_scale), wide[2], _dtype_tag(q), p[5],
+        p[6] if status is not None else None, st)
+    if code:
+        _check("dsa_gqa_block_scores", code)
 
 
 def gqa_attend_workspace_bytes(q, k_pages) -> int:
@@ -416,30 +475,59 @@ def dsa_gqa_attend(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
     for ``dsa_gqa_append``): over all before them (``window`` 0), a sliding window and the first
     ``sinks`` tokens, or the blocks that ``block_ids`` [T, Hkv, K] lists for each token and KV
     head (negative: none)."""
-    n_pages, Hkv, ps, D, B, width = _gqa_cache(k_pages, v_pages, k_scale, v_scale, block_table,
-                                               seq_lens, cu_new)
-    if q.dim() != 3 or q.shape[2] != D:
+    n_pages, Hkv, D, B = _gqa_shapes(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
+                                     cu_new)
+    shape, act = q.shape, q.dtype
+    if len(shape) != 3 or shape[2] != D:
         raise ValueError("q must be [T, Hq, D]")
-    T, Hq, _ = q.shape
+    T, Hq, _ = shape
     K = 0
     if block_ids is not None:
-        if block_ids.dim() != 3 or block_ids.shape[:2] != (T, Hkv) or block_ids.shape[2] < 1:
+        listed = block_ids.shape
+        if len(listed) != 3 or listed[0] != T or listed[1] != Hkv or listed[2] < 1:
             raise ValueError("block_ids must be [T, Hkv, K], K >= 1")
-        K = block_ids.shape[2]
-    act, codes = q.dtype, _gqa_codes(k_pages)
-    _sizes((out, T * Hq * D, "out"), (lse, T * Hq, "lse"))
-    dev, st = _device(q, stream)
-    qp, kp, vp, ks, vs, table, lens, cu, ids, o, ls, ws, status = _args(
-        dev, (q, act, "q"), (k_pages, codes, "k_pages"), (v_pages, codes, "v_pages"),
-        (k_scale, _F32, "k_scale"), (v_scale, _F32, "v_scale"), (block_table, _I32, "block_table"),
-        (seq_lens, _I32, "seq_lens"), (cu_new, _I32, "cu_new"), (block_ids, _I32, "block_ids"),
-        (out, act, "out"), (lse, _F32, "lse"), (workspace, torch.uint8, "workspace"),
-        (status, _I32, "status"))
-    kv = _lib.GqaKv(kp, vp, ks, vs, table, lens, n_pages, ps, width, Hkv, D)
+        K = listed[2]
+    if out.numel() != T * Hq * D or (lse is not None and lse.numel() != T * Hq):
+        _sizes((out, T * Hq * D, "out"), (lse, T * Hq, "lse"))
+    dev, st = _gqa_device(q, stream)
+    codes = k_pages.dtype
+    tensors = [k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_new, q, out]
+    dtypes = [codes, codes, _F32, _F32, _I32, _I32, _I32, act, act]
+    if workspace is not None:
+        tensors.append(workspace)
+        dtypes.append(torch.uint8)
+    if lse is not None:
+        tensors.append(lse)
+        dtypes.append(_F32)
+    if block_ids is not None:
+        tensors.append(block_ids)
+        dtypes.append(_I32)
+    if status is not None:
+        tensors.append(status)
+        dtypes.append(_I32)
+    p = _pointers(dev, tensors, dtypes)
+    if p is None or codes not in _CODES:
+        _gqa_wrong(dev, *tensors[:7], (q, act, "q"), (out, act, "out"),
+                   (workspace, torch.uint8, "workspace"), (lse, _F32, "lse"),
+                   (block_ids, _I32, "block_ids"), (status, _I32, "status"))
+    kv = _lib.GqaKv(p[0], p[1], p[2], p[3], p[4], p[5], n_pages, k_pages.shape[2],
+                    block_table.shape[1], Hkv, D)
+    at = 9
+    ws = ls = ids = None
+    ws_bytes = 0
+    if workspace is not None:
+        ws, ws_bytes = p[at], workspace.numel()
+        at += 1
+    if lse is not None:
+        ls = p[at]
+        at += 1
+    if block_ids is not None:
+        ids = p[at]
     code = _lib.load().dsa_gqa_attend(
-        qp, ctypes.byref(kv), cu, ids, K, T, B, Hq, int(window), int(sinks), float(sm_scale),
-        _dtype_tag(q), o, ls, ws, 0 if workspace is None else workspace.numel(), status, st)
-    _check("dsa_gqa_attend", code)
+        p[7], ctypes.byref(kv), p[6], ids, K, T, B, Hq, int(window), int(sinks), float(sm_scale),
+        _dtype_tag(q), p[8], ls, ws, ws_bytes, None if status is None else p[-1], st)
+    if code:
+        _check("dsa_gqa_attend", code)
 
 
 def select_workspace_bytes(Q, P_ld, select_k) -> int:
