@@ -55,6 +55,28 @@ __device__ __forceinline__ Joined nothing() {
 }
 __device__ __forceinline__ float finite_or_0(float x) { return x == -INFINITY ? 0.f : x; }
 
+// a <- a and b together, in this order (nothing: f and x are 0)
+__device__ __forceinline__ void merge(Joined& a, const Joined& b) {
+  const float m = fmaxf(a.m, b.m), z = fmaxf(a.z, b.z);
+  const float ref = finite_or_0(m), zref = finite_or_0(z);
+  // square roots, taken twice (no reference: nothing, or a NaN sum, which stays one)
+  const float wa = a.m == -INFINITY ? 1.f : ex2_fast(0.5f * (a.m - ref));
+  const float wb = b.m == -INFINITY ? 1.f : ex2_fast(0.5f * (b.m - ref));
+  const float za = a.z == -INFINITY ? 1.f : ex2_fast(0.5f * (a.z - zref));
+  const float zb = b.z == -INFINITY ? 1.f : ex2_fast(0.5f * (b.z - zref));
+  a.m = m;
+  a.z = z;
+  a.f = a.f * za * za + b.f * zb * zb;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) a.x[k] = a.x[k] * wa * wa + b.x[k] * wb * wb;
+}
+// a lane's columns of a row
+template <int kD>
+__device__ __forceinline__ void load_part(Joined& j, const float* row, int lane) {
+#pragma unroll
+  for (int k = 0; k < kD / 32; ++k) j.x[k] = row[lane * (kD / 32) + k];
+}
+
 template <int kD, int kRows>
 __device__ __forceinline__ Joined join_parts(const JoinArgs& p, const Header* heads, int g0,
                                              int s0, int s1, int r, int lane) {

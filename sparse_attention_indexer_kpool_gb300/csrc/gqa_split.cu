@@ -26,6 +26,11 @@
 // an order that keeps both kinds of rows free of bank conflicts.
 // Shares are equal in tiles whatever the lengths; a row tile that two or more warps share
 // leaves partials (fp32) that the join kernel adds in their order.
+// Where a step has few row tiles of few keys, a cluster of CTAs takes each (kCluster): its warps
+// share the tiles evenly, and the partials meet in (distributed) shared memory, so that no
+// second kernel follows.
+#include <cooperative_groups.h>
+
 #include "gqa.cuh"
 #include "gqa_join.cuh"
 #include "mla_chunk.cuh"
@@ -41,6 +46,7 @@ constexpr int kKeys = 32;                      // of a tile
 constexpr float kRaise = 15.f;                 // e above which a reference is raised
 constexpr int kExtra = 1;                      // what a row tile costs beside its tiles, in tiles
 constexpr int kLeast = 2;                      // tiles of a share, at least
+constexpr int kMost = 8;                       // tiles of a warp where a cluster takes a row tile
 constexpr int kRingBytes = 2 * 2 * kKeys * 128;  // of a warp
 
 struct Params {
@@ -95,11 +101,13 @@ struct Walk {
   int b;
   unsigned row, unit;
   Seq s;
+  int part, parts;                          // kCluster: this warp's part of every row tile
   int token, h, cb, tile_id, ta, tb, n;     // the segment: tiles [ta, tb) of n
   int pos, lo, s0, sink_boxes, first, boxes;  // what its token sees
 
-  __device__ __forceinline__ Walk(const Params& pp, const Start& st)
-      : p(pp), left(st.b < pp.a.B ? st.n : 0), b(st.b), row(st.row), unit(st.unit) {
+  __device__ __forceinline__ Walk(const Params& pp, const Start& st, int part_, int parts_)
+      : p(pp), left(st.b < pp.a.B ? st.n : 0), b(st.b), row(st.row), unit(st.unit), part(part_),
+        parts(parts_) {
     if (left > 0) load();
   }
   __device__ __forceinline__ void load() {
@@ -135,8 +143,13 @@ struct Walk {
       boxes = at < 0 ? 0 : sink_boxes + max(pos / kR - first + 1, 0);
     }
     n = (boxes * kR + kKeys - 1) / kKeys;
-    ta = share_of(unit, n, s.u);
-    tb = share_of(e, n, s.u);
+    if (parts > 1) {
+      ta = share_of(part, n, parts);
+      tb = share_of(part + 1, n, parts);
+    } else {
+      ta = share_of(unit, n, s.u);
+      tb = share_of(e, n, s.u);
+    }
     left -= e - unit;
     unit = e;
     if (e == s.u) {
@@ -232,6 +245,36 @@ __device__ __forceinline__ void find_shares(const Params& p, Start* st,
   __syncthreads();
 }
 
+// kCluster: the row tile of this cluster, for all its warps; false: there is none (no row of a
+// sequence, or faulty lengths).  Ends with a barrier.
+template <int kR>
+__device__ __forceinline__ bool find_row(const Params& p, Start* st, unsigned tile) {
+  const int tid = threadIdx.x, B = p.a.B, per = p.a.kv.Hkv * p.hb;
+  const int token = (int)(tile / (unsigned)per), rest = (int)tile - token * per;
+  bool odd = false, past = false, falls = false;
+  int below = 0;  // sequences that begin at or before the token
+  for (int b = tid; b < B; b += kThreads) {
+    const int cu0 = p.a.cu_new[b], cu1 = p.a.cu_new[b + 1], len = p.a.kv.seq_lens[b];
+    const Seq s = seq_of<kR>(cu0, cu1, len, p);
+    odd |= cu0 < 0 || cu1 < cu0 || cu1 > p.a.T || (s.n > 0 && s.base < 0);
+    past |= s.n > 0 && len > p.cap;
+    falls |= cu1 < cu0;
+    if (token >= s.c0 && token < s.c0 + s.n) {  // (its owner: one, where cu_new does not fall)
+      st->b = b;
+      st->row = (unsigned)((token - s.c0) * per + rest);
+      st->unit = 0;
+      st->n = s.u;
+      below = 1;
+    }
+  }
+  if (blockIdx.x == 0) {
+    if (odd) flag(p.a.status, DSA_DEV_BAD_LENGTH);
+    if (past && !p.a.block_ids) flag(p.a.status, DSA_DEV_BAD_PAGE);
+  }
+  falls = __syncthreads_or(falls);
+  return __syncthreads_or(below) && !falls;
+}
+
 // ---- small pieces ----------------------------------------------------------------
 // D[16 x 8] += A[16 x 16] B[16 x 8], fp16 in, fp32 out
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -289,16 +332,23 @@ struct Ctl {
   Start start[kW];
   unsigned long long scan[2 * kW];
 };
+// kCluster: a CTA's sums for the others
+template <int kD, int kN>
+struct Shared {
+  float4 ml[kW][8 * kN], cta_ml[8 * kN];   // reference; the sum f 2^z as z and f
+  float cta_x[8 * kN][kD];
+};
 
 template <int kD>
 constexpr int stages() { return kRingBytes / (2 * kKeys * kD); }
-template <int kD>
+template <int kD, int kN, bool kCluster>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)kW * kRingBytes + sizeof(Ctl<stages<kD>()>);
+  return 1024 + (size_t)kW * kRingBytes + sizeof(Ctl<stages<kD>()>) +
+         (kCluster ? 16 + sizeof(Shared<kD, kN>) : 0);
 }
 
 // kD: head dim, kN: blocks of 8 query heads, kR: keys of a TMA box (a divisor of the page)
-template <int kD, int kN, int kR>
+template <int kD, int kN, int kR, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1)
     gqa_split_kernel(const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, const Params p) {
@@ -314,14 +364,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) fence_mbar_init();
   pdl_wait();
   pdl_launch_dependents();
-  find_shares<kR>(p, c.start, c.scan);
-  const int worker = warp * gridDim.x + blockIdx.x;
-  const Start& st = c.start[warp];
+  namespace cg = cooperative_groups;
+  const int ctas = kCluster ? (int)cg::this_cluster().num_blocks() : 1;
+  const int rank = kCluster ? (int)cg::this_cluster().block_rank() : 0;
+  if constexpr (kCluster) {
+    if (!find_row<kR>(p, c.start, blockIdx.x / ctas)) return;  // (all CTAs of the cluster alike)
+  } else {
+    find_shares<kR>(p, c.start, c.scan);
+  }
+  const int worker = kCluster ? rank * kW + warp : warp * gridDim.x + blockIdx.x;
+  const int parts = kCluster ? ctas * kW : 1;
+  const Start& st = c.start[kCluster ? 0 : warp];
+  Shared<kD, kN>* sh = reinterpret_cast<Shared<kD, kN>*>(
+      reinterpret_cast<unsigned char*>(&c) + (sizeof(c) + 15) / 16 * 16);
   unsigned char* ring = sb + (size_t)warp * kRingBytes;
   const uint32_t ring_at = smem_u32(ring);
 
   // ---- the loads, kStages tiles ahead
-  Walk<kR> wl(p, st);
+  Walk<kR> wl(p, st, worker, parts);
   bool more = false;
   int lv = 0, held = 0;                     // next tile; first tile that the lanes hold
   int row[kBoxes], bpos[kBoxes], bev[kBoxes];
@@ -401,13 +461,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int s = 0; s < kStages; ++s) issue();
 
   // ---- the work
-  Walk<kR> w(p, st);
+  Walk<kR> w(p, st, worker, parts);
   Header hd = {-1, -1, 0, 0};
   int done = 0;
   bool ok = true;
   while (ok && w.next()) {
-    const bool some = w.tb > w.ta, whole = w.ta == 0 && w.tb == w.n;
+    const bool some = w.tb > w.ta, whole = !kCluster && w.ta == 0 && w.tb == w.n;
     const bool begins = some && w.ta == 0 && !whole;
+    if (kCluster && !some) break;  // (no part of the row tile)
     if (begins) hd.start_item = w.tile_id;
     if (!whole && !begins && hd.cont_item < 0) {
       hd.cont_item = w.tile_id;
@@ -746,6 +807,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
           if (p.a.lse && g == 0)
             p.a.lse[row0 + col] = sum == 0.f ? -INFINITY : (z + log2f(f)) / kLog2e;
+        } else if (kCluster) {  // to where the ring was: every tile is read
+          float4* dst = reinterpret_cast<float4*>(ring) + (col * kD + kC * g) / 4;
+#pragma unroll
+          for (int k = 0; k < kC / 4; ++k)
+            dst[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          if (g == 0) sh->ml[warp][col] = make_float4(m[n][i], z, f, 0.f);
         } else {
           const long long slot = (long long)(2 * worker + (begins ? 1 : 0)) * (8 * kN) + col;
           float4* dst = reinterpret_cast<float4*>(p.part_o + slot * kD + kC * g);
@@ -762,7 +829,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) flag(p.a.status, DSA_DEV_TIMEOUT);
     hd = Header{-1, -1, 0, 0};
   }
-  if (lane == 0 && worker < p.workers) p.head[worker] = hd;
+  if constexpr (!kCluster) {
+    if (lane == 0 && worker < p.workers) p.head[worker] = hd;
+  } else {
+    // the CTA's warps' partials, a head a warp, then those of the cluster's CTAs
+    const int per = kv.Hkv * p.hb, tile = (int)(blockIdx.x / ctas), token = tile / per;
+    const int rest = tile - token * per, h = rest / p.hb, head0 = (rest - h * p.hb) * 8 * kN;
+    const int heads = min(8 * kN, p.G - head0), mine = max(w.tb - w.ta, 0);
+    static_assert(8 * kN * kD * 4 <= kRingBytes, "a warp's partial takes its ring's place");
+    if (mine == 0)
+      for (int i = lane; i < 8 * kN; i += 32)
+        sh->ml[warp][i] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+    __syncthreads();
+    for (int col = warp; col < heads; col += kW) {
+      Joined j = nothing();
+#pragma unroll
+      for (int i = 0; i < kW; ++i) {
+        const float4 ml = sh->ml[i][col];
+        if (ml.z == 0.f) continue;  // (a warp without a tile, or that saw no page)
+        Joined x{ml.x, ml.y, ml.z, {0.f, 0.f, 0.f, 0.f}};
+        load_part<kD>(x, reinterpret_cast<const float*>(sb + (size_t)i * kRingBytes) + col * kD,
+                      lane);
+        merge(j, x);
+      }
+      if (lane == 0) sh->cta_ml[col] = make_float4(j.m, j.z, j.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kD / 32; ++k) sh->cta_x[col][lane * (kD / 32) + k] = j.x[k];
+    }
+    cg::this_cluster().sync();
+    for (int i = warp; i * ctas + rank < heads; i += kW) {
+      const int col = i * ctas + rank;
+      Joined j = nothing();
+#pragma unroll 4
+      for (int r = 0; r < ctas; ++r) {
+        const Shared<kD, kN>* other = cg::this_cluster().map_shared_rank(sh, r);
+        const float4 ml = other->cta_ml[col];
+        if (ml.z == 0.f) continue;
+        Joined x{ml.x, ml.y, ml.z, {0.f, 0.f, 0.f, 0.f}};
+        load_part<kD>(x, other->cta_x[col], lane);
+        merge(j, x);
+      }
+      const JoinArgs out{nullptr, nullptr, nullptr, 0, static_cast<__nv_bfloat16*>(p.a.out),
+                         p.a.lse};
+      store_joined<kD>(out, (long long)token * p.a.Hq + h * p.G + head0 + col, j, lane);
+    }
+    cg::this_cluster().sync();  // (nobody leaves while its sums are read)
+  }
 }
 
 // ---- launches ----------------------------------------------------------------------
@@ -797,21 +909,40 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
                              ? (long long)a.window + a.sinks : p.cap;
   const long long bound = row_tiles * ((seen + kKeys - 1) / kKeys + kExtra);
   const long long want = (bound + kLeast - 1) / kLeast;
+  CUtensorMap k_map, v_map;
+  const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.Hkv * a.kv.page_size;
+  if (!code_map(&k_map, a.kv.k_pages, rows, kD, kR) ||
+      !code_map(&v_map, a.kv.v_pages, rows, kD, kR))
+    return DSA_ERR_CUDA;
+  // A cluster for a row tile where all of them fit the SMs at once and no warp then has more
+  // than kMost tiles: (measured below)
+  int ctas = 8;
+  while (ctas > 1 && row_tiles * ctas > num_sms()) ctas >>= 1;
+  if (row_tiles * ctas <= num_sms() && (seen + kKeys - 1) / kKeys <= (long long)kMost * kW * ctas) {
+    auto kernel = gqa_split_kernel<kD, kN, kR, true>;
+    constexpr size_t kBytes = smem_bytes<kD, kN, true>();
+    static std::atomic<unsigned long long> done{0};
+    if (!allow_smem(kernel, kBytes, done)) return DSA_ERR_CUDA;
+    Launch l(dim3((unsigned)(row_tiles * ctas), 1, 1), kThreads, kBytes, stream);
+    cudaLaunchAttribute attr[2];
+    attr[0] = l.attr;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    l.cfg.attrs = attr;
+    l.cfg.numAttrs = 2;
+    return launch_kernel(&l.cfg, kernel, k_map, v_map, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  }
   const int most = workers_of(), workers = want < most ? (int)want : most;
   const int grid = workers < num_sms() ? workers : num_sms();
   p.workers = workers;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float4*>(p.part_o + (size_t)workers * 2 * 8 * kN * kD);
   p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)workers * 2 * 8 * kN);
-  CUtensorMap k_map, v_map;
-  const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.Hkv * a.kv.page_size;
-  if (!code_map(&k_map, a.kv.k_pages, rows, kD, kR) ||
-      !code_map(&v_map, a.kv.v_pages, rows, kD, kR))
-    return DSA_ERR_CUDA;
-  auto kernel = gqa_split_kernel<kD, kN, kR>;
+  auto kernel = gqa_split_kernel<kD, kN, kR, false>;
   static std::atomic<unsigned long long> done{0};
-  if (!allow_smem(kernel, smem_bytes<kD>(), done)) return DSA_ERR_CUDA;
-  Launch l(dim3(grid, 1, 1), kThreads, smem_bytes<kD>(), stream);
+  if (!allow_smem(kernel, smem_bytes<kD, kN, false>(), done)) return DSA_ERR_CUDA;
+  Launch l(dim3(grid, 1, 1), kThreads, smem_bytes<kD, kN, false>(), stream);
   if (launch_kernel(&l.cfg, kernel, k_map, v_map, p) != cudaSuccess) return DSA_ERR_CUDA;
   const JoinArgs j{p.part_o, p.part_ml, p.head, workers, static_cast<__nv_bfloat16*>(a.out), a.lse};
   return launch_join<kD>(j, Rows<kN>{a.Hq, a.kv.Hkv, p.G, p.hb}, row_tiles, stream);

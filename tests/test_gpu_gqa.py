@@ -480,6 +480,29 @@ def test_attend_blocks(lens, new, Hkv, G, ps, D, K, dtype):
     check_attend(Case(ps + G, lens, new, Hkv, ps, D), G, dtype, K=K)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
+@pytest.mark.parametrize("lens,new,Hkv,G,ps,D", SHAPES[:8] + [
+    ([5000, 1, 3000, 700], [1, 1, 2, 1], 2, 8, 64, 128), ([9000], [1], 1, 16, 16, 128),
+    ([4000, 2500], [2, 3], 4, 4, 32, 64)])
+def test_attend_by_shares(lens, new, Hkv, G, ps, D, window, sinks):
+    """The same under a table so wide that a step's keys may be many: their tiles are then shared
+    out over all warps and the partials joined by a second kernel."""
+    c = Case(ps + G, lens, new, Hkv, ps, D, width=40_000 // ps)
+    if max(lens) > 2000:
+        check_dense(c, G, window, sinks)
+    else:
+        check_attend(c, G, BF, window, sinks)
+
+
+@pytest.mark.parametrize("K", [40, 300])
+def test_attend_blocks_by_shares(K):
+    """Long lists, and more row tiles than SMs."""
+    c = Case(50, [900, 300, 40], [20, 30, 2], 4, 16, 128)
+    check_attend(c, 8, BF, K=K)
+    c = Case(51, [5000], [1], 2, 16, 128)
+    check_attend(c, 16, BF, K=K)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_attend_blocks_listed_oddly(dtype):
     """The same block twice counts twice; blocks behind the token's own are not seen; past the
@@ -526,8 +549,8 @@ def test_attend_faults(dtype):
 def test_attend_scales_far_apart(K, dtype):
     """Blocks whose scales lie far apart: keys large and small, values at both ends of the range
     of exponents, zero blocks."""
-    for lo, hi in ((-64, 100), (-30, 30), (-64, -64)):
-        c = Case(15, [80, 90], [2, 1], 2, 16, 128)
+    for lo, hi, width in ((-64, 100, 7), (-30, 30, 7), (-64, -64, 7), (-64, 100, 3000)):
+        c = Case(15, [80, 90], [2, 1], 2, 16, 128, width=width)
         used = ~torch.isnan(c.scale["v"])
         e = torch.randint(0, 2, c.scale["v"].shape, generator=c.g) * (hi - lo) + lo
         c.scale["v"] = torch.where(used, torch.exp2(e.float()), c.scale["v"])
