@@ -46,7 +46,14 @@ constexpr int kKeys = 32;                      // of a tile
 constexpr float kRaise = 15.f;                 // e above which a reference is raised
 constexpr int kExtra = 1;                      // what a row tile costs beside its tiles, in tiles
 constexpr int kLeast = 2;                      // tiles of a share, at least
-constexpr int kMost = 8;                       // tiles of a warp where a cluster takes a row tile
+// Tiles of a warp, at most, where a cluster takes a row tile; and where these are three quarters
+// of the SMs.  Measured, cluster / shares in us (sequences x KV heads, 8 query heads each):
+//   1 x 8 on 2,048 keys 11.1 / 14.0, 16,384 (8 tiles) 18.6 / 22.7, 32,768 (16) 26.1 / 25.4
+//   2 x 2 on 2,048 11.1 / 13.1, 16,384 (8) 18.3 / 21.0, 32,768 (16) 26.7 / 24.9
+//   4 x 8 on 8,192 (8) 17.6 / 24.5, 32,768 (32) 49.0 / 57.3, 65,536 (64) 87.7 / 94.3
+//   16 x 8 on 2,048 (8) 16.8 / 27.5, 8,192 (32) 48.2 / 59.9
+// (lengths that differ leave a cluster waiting for its longest: so no more than that)
+constexpr int kMost = 12, kMostFull = 32;
 constexpr int kRingBytes = 2 * 2 * kKeys * 128;  // of a warp
 
 struct Params {
@@ -914,11 +921,11 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
   if (!code_map(&k_map, a.kv.k_pages, rows, kD, kR) ||
       !code_map(&v_map, a.kv.v_pages, rows, kD, kR))
     return DSA_ERR_CUDA;
-  // A cluster for a row tile where all of them fit the SMs at once and no warp then has more
-  // than kMost tiles: (measured below)
+  // a cluster for a row tile where all of them fit the SMs at once
   int ctas = 8;
   while (ctas > 1 && row_tiles * ctas > num_sms()) ctas >>= 1;
-  if (row_tiles * ctas <= num_sms() && (seen + kKeys - 1) / kKeys <= (long long)kMost * kW * ctas) {
+  const long long all = row_tiles * ctas, least = all * 4 >= 3ll * num_sms() ? kMostFull : kMost;
+  if (all <= num_sms() && (seen + kKeys - 1) / kKeys <= least * kW * ctas) {
     auto kernel = gqa_split_kernel<kD, kN, kR, true>;
     constexpr size_t kBytes = smem_bytes<kD, kN, true>();
     static std::atomic<unsigned long long> done{0};
