@@ -49,7 +49,8 @@ constexpr int kSoftRegs = 152, kOtherRegs = 104;
 static_assert(kSoftRegs + kOtherRegs == 2 * 128, "what the launch has");
 constexpr int kMetas = 4;
 constexpr float kFull = 32768.f;       // a sum of 16 weights above which a reference is raised
-constexpr int kExtra = 2;              // what an item costs beside its tiles, in tiles
+// What an item costs, in units: a tile of it, one without rows of B, and an item beside its tiles.
+constexpr int kPairCost = 4, kSingleCost = 3, kExtra = 12;
 
 struct Params {
   GqaArgs a;
@@ -66,7 +67,11 @@ struct Params {
 // ---- the batch as units ---------------------------------------------------------
 struct Seq {
   int c0, n, base;     // rows c0 .. c0 + n - 1 of the step; position of the first
-  unsigned u;          // key tiles of an item, at most, and kExtra
+  unsigned count;      // items of a KV head
+  unsigned u, tail;    // units of an item, of the last of a head
+  __device__ __forceinline__ unsigned long long units() const {  // of a head
+    return count ? (unsigned long long)(count - 1) * u + tail : 0;
+  }
 };
 __device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p) {
   Seq s;
@@ -74,18 +79,19 @@ __device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p
   s.n = max(min(cu1, p.a.T) - s.c0, 0);
   s.base = len < 0 ? -s.n : len - s.n;  // negative: rows before position 0
   const unsigned all = (unsigned)min(max(len, 0), p.cap);
-  s.u = (all + kKeys - 1) / kKeys;
+  unsigned n = (all + kKeys - 1) / kKeys;  // key tiles of an item, at most
   if (p.a.window > 0) {
     const long long R = 1 << p.box_log;
     const long long span = (long long)p.a.window + 2 * p.per - 1;
     const long long keys = ((p.a.sinks + R - 1) / R + (R - 2 + span) / R + 1) * R;
-    if ((keys + kKeys - 1) / kKeys < (long long)s.u) s.u = (unsigned)((keys + kKeys - 1) / kKeys);
+    n = (unsigned)min((long long)n, (keys + kKeys - 1) / kKeys);
   }
-  s.u = max(s.u, 1u) + kExtra;
+  n = max(n, 1u);
+  const unsigned pair = 2 * p.per;
+  s.count = ((unsigned)s.n + pair - 1) / pair;
+  s.u = n * kPairCost + kExtra;
+  s.tail = s.count * pair - (unsigned)s.n >= (unsigned)p.per ? n * kSingleCost + kExtra : s.u;
   return s;
-}
-__device__ __forceinline__ unsigned items_of(const Seq& s, const Params& p) {
-  return ((unsigned)s.n + 2 * p.per - 1) / (2 * p.per) * p.a.kv.Hkv;
 }
 
 struct Start {
@@ -112,18 +118,20 @@ struct Walk {
   }
   __device__ __forceinline__ bool next() {
     if (left == 0) return false;
-    while (item >= items_of(s, p)) {
+    const int Hkv = p.a.kv.Hkv, pair = 2 * p.per;
+    while (item >= s.count * Hkv) {
       if (++b >= p.a.B) return false;  // (lengths that changed under the call)
       load();
       item = 0;
     }
-    const unsigned e = left < s.u - unit ? unit + (unsigned)left : s.u;
-    const int Hkv = p.a.kv.Hkv, pair = 2 * p.per, count = (s.n + pair - 1) / pair;
-    const int k = (int)(item / Hkv);
-    h = (int)(item - (unsigned)k * Hkv);
+    h = (int)(item / s.count);
+    const unsigned k = item - (unsigned)h * s.count;
     // groups are taken from both ends in turn: a share of a long prompt's units is then its
     // share of the work
-    const int i = ((k & 1) ? count - 1 - (k >> 1) : k >> 1) * pair;
+    const unsigned at = (k & 1) ? s.count - 1 - (k >> 1) : k >> 1;
+    const unsigned u = at == s.count - 1 ? s.tail : s.u;
+    const unsigned e = left < u - unit ? unit + (unsigned)left : u;
+    const int i = (int)at * pair;
     token = s.c0 + i;
     tokens = min(pair, s.n - i);
     id = token * Hkv + h;
@@ -137,11 +145,11 @@ struct Walk {
     boxes = end < 0 ? 0 : sink_boxes + max((end >> p.box_log) - first + 1, 0);
     const unsigned per_tile = kKeys >> p.box_log;
     n = (int)(((unsigned)boxes + per_tile - 1) / per_tile);
-    ta = share_of(unit, n, s.u);
-    tb = share_of(e, n, s.u);
+    ta = share_of(unit, n, u);
+    tb = share_of(e, n, u);
     left -= e - unit;
     unit = e;
-    if (e == s.u) {
+    if (e == u) {
       unit = 0;
       ++item;
     }
@@ -166,7 +174,7 @@ struct Meta {          // of a key tile, by 16 keys
 struct Ctl {
   uint64_t raw_full[2], raw_empty[2];      // codes of keys, of values
   uint64_t wide_full[2][2], wide_empty[2][2];  // [stage][keys, values]
-  uint64_t s_full[2], p_full[2], o_full[2], q_full[2], q_empty, drain;
+  uint64_t s_full[2], p_full[2], o_full[2], q_full[2], drain;
   Meta meta[kMetas];
   Start start;
   unsigned long long scan[kWarps];
@@ -198,7 +206,7 @@ __device__ __forceinline__ void find_share(const Params& p, Ctl& c) {
     odd |= cu0 < 0 || cu1 < cu0 || cu1 > p.a.T || (s.n > 0 && s.base < 0);
     past |= s.n > 0 && len > p.cap;
     falls |= cu1 < cu0;
-    mine += (unsigned long long)items_of(s, p) * s.u;
+    mine += s.units() * p.a.kv.Hkv;
   }
   if (blockIdx.x == 0) {
     if (odd) flag(p.a.status, DSA_DEV_BAD_LENGTH);
@@ -231,12 +239,26 @@ __device__ __forceinline__ void find_share(const Params& p, Ctl& c) {
     unsigned long long at = before;
     for (int b = b0; b < b1; ++b) {
       const Seq s = seq_of(p.a.cu_new[b], p.a.cu_new[b + 1], p.a.kv.seq_lens[b], p);
-      const unsigned long long all = (unsigned long long)items_of(s, p) * s.u;
+      const unsigned long long all = s.units() * p.a.kv.Hkv;
       if (v0 < at + all) {
-        const unsigned long long off = v0 - at;
+        unsigned long long off = v0 - at;
         c.start.b = b;
-        c.start.item = (unsigned)(off / s.u);
-        c.start.unit = (unsigned)(off - (unsigned long long)c.start.item * s.u);
+        const unsigned h = (unsigned)(off / s.units());
+        off -= h * s.units();
+        // a head's items: its last group is the second (the first where there is one only)
+        const unsigned last = s.count > 1;
+        unsigned k = 0;
+        if (off >= (unsigned long long)last * s.u) {
+          off -= last * s.u;
+          k = last;
+          if (off >= s.tail) {
+            off -= s.tail;
+            k = last + 1 + (unsigned)(off / s.u);
+            off %= s.u;
+          }
+        }
+        c.start.item = h * s.count + k;
+        c.start.unit = (unsigned)off;
         c.start.n = v1 - v0;
         break;
       }
@@ -319,6 +341,16 @@ __device__ __forceinline__ void tmem_st16_start(uint32_t ta, const uint32_t (&v)
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st32_start(uint32_t ta, const uint32_t (&v)[32]) {
+  uint32_t a[16], b[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    a[i] = v[i];
+    b[i] = v[16 + i];
+  }
+  tmem_st16_start(ta, a);
+  tmem_st16_start(ta + 16, b);
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -346,7 +378,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.o_full[i], 1);
       mbar_init(&c.q_full[i], 4);
     }
-    mbar_init(&c.q_empty, 1);
     mbar_init(&c.drain, 1);
     fence_mbar_init();
     c.dead = 0;
@@ -375,6 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + ab * 128, to = tmem + lanes + kOCol + ab * 128;
     const int my = r / p.G, g = r - my * p.G;
+    // The warp's 32 rows of Q, in pieces of 16 bytes.  Rows come in and go out through it, so that
+    // neighbouring lanes have neighbouring pieces of memory (a row to a lane took 12,000 clocks to
+    // read and 16,000 to write for each item, six times as long).
+    constexpr int kChunks = kD / 8, kAtOnce = 32 / kChunks, kLoads = 32 / kAtOnce;
+    auto piece = [&](int row, int k) {
+      return reinterpret_cast<uint4*>(sb + S::kQ + ab * S::kTile + (k >> 3) * S::kAtom +
+                                      ((r & ~31) + row) * 128 + (((k & 7) ^ (row & 7)) << 4));
+    };
     Header hd = {-1, -1, 0, 0};
     int tiles = 0, segs = 0;      // key tiles and segments so far
     int mine = 0, outs = 0;       // those of this row tile
@@ -394,7 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = ab * p.per + my;              // this row's token of the item
       const bool real = my < p.per && i < w.tokens;
       const bool used = ab == 0 || w.tokens > p.per;
-      const long long row = (long long)(w.token + i) * p.a.Hq + w.h * p.G + g;
+      // the warp's rows are rel rows behind the item's first
+      const long long first_row = (long long)w.token * p.a.Hq + w.h * p.G;
+      const int rel = real ? i * p.a.Hq + g : 0;
+      const long long row = first_row + rel;
       if (!some) {  // nothing seen
         if (real) {
           uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + row * kD);
@@ -403,50 +445,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      // the query row, once the last segment's products with this place are done
-      if (segs > 0 && !wait_on(&c.q_empty, (segs - 1) & 1, dead, wait_ns)) ok = false;
       ++segs;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       if (!used) {
         tiles += w.tb - w.ta;
         continue;
       }
       float qs;
+      const unsigned reals = __ballot_sync(0xffffffffu, real);
       {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(p.a.q) + (real ? row : 0) * kD);
-        float top = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < kD / 8; ++k) {
-          const uint4 x = __ldg(src + k);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        // (this place's last products are done: the outputs of the last segment are out)
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.a.q) + first_row * kD;
+        uint4 x[kLoads];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float a = fabsf(bf16lo(u[j])), b = fabsf(bf16hi(u[j]));
-            if (a < INFINITY) top = fmaxf(top, a);
-            if (b < INFINITY) top = fmaxf(top, b);
+        for (int k = 0; k < kLoads; ++k) {
+          const int in_row = k * kAtOnce + lane / kChunks;
+          const int at = __shfl_sync(0xffffffffu, rel, in_row);
+          x[k] = make_uint4(0u, 0u, 0u, 0u);
+          if ((reals >> in_row) & 1u)
+            x[k] = __ldg(reinterpret_cast<const uint4*>(src + (long long)at * kD) +
+                         lane % kChunks);
+        }
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+          *piece(k * kAtOnce + lane / kChunks, lane % kChunks) = x[k];
+        __syncwarp();
+        // the largest element (of bits whose order is the values')
+        uint32_t top = 0u;
+#pragma unroll 8
+        for (int k = 0; k < kChunks; ++k) {
+          const uint4 y = *piece(lane, k);
+          const uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            top = max(max(top, u[j] & 0x7fff0000u), (u[j] & 0x7fffu) << 16);
+        }
+        const bool odd = top >= 0x7f800000u;  // infinities or NaN: the largest of the others
+        if (odd) {
+          top = 0u;
+#pragma unroll 1
+          for (int k = 0; k < kD; ++k) {
+            const unsigned char* at = reinterpret_cast<const unsigned char*>(piece(lane, k / 8));
+            const uint32_t u = (reinterpret_cast<const uint16_t*>(at)[k % 8] & 0x7fffu) << 16;
+            if (u < 0x7f800000u) top = max(top, u);
           }
         }
-        const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -126), half = (14 - ex) >> 1;
-        const float up0 = pow2(half), up1 = pow2(14 - ex - half);
-        qs = pow2(-half) * pow2(half + ex - 14) * p.zscale;
-        unsigned char* dst = sb + S::kQ + ab * S::kTile + r * 128;
+        const int ex = max((int)(top >> 23) - 127, -126), half = (14 - ex) >> 1;
+        // (a negative scale's sign goes with the query: what scores are multiplied with is
+        // positive, and what is masked may be -infinity before it)
+        const float up0 = copysignf(pow2(half), p.zscale), up1 = pow2(14 - ex - half);
+        qs = pow2(-half) * pow2(half + ex - 14) * fabsf(p.zscale);
 #pragma unroll 4
-        for (int k = 0; k < kD / 8; ++k) {
-          const uint4 x = __ldg(src + k);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-          uint32_t y[4];
+        for (int k = 0; k < kChunks; ++k) {
+          const uint4 y = *piece(lane, k);
+          const uint32_t u[4] = {y.x, y.y, y.z, y.w};
+          uint32_t z[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // a NaN or an infinity becomes NaN: its row's logits are NaN
-            float a = bf16lo(u[j]) * up0 * up1, b = bf16hi(u[j]) * up0 * up1;
-            a = fabsf(a) < INFINITY ? a : NAN;
-            b = fabsf(b) < INFINITY ? b : NAN;
-            y[j] = real ? pack_f16(a, b) : 0u;
+          for (int j = 0; j < 4; ++j)
+            z[j] = pack_f16(bf16lo(u[j]) * up0 * up1, bf16hi(u[j]) * up0 * up1);
+          *piece(lane, k) = make_uint4(z[0], z[1], z[2], z[3]);
+        }
+        if (odd) {  // an infinity becomes NaN too: its row's logits are NaN
+#pragma unroll 1
+          for (int k = 0; k < kD; ++k) {
+            uint16_t* at = reinterpret_cast<uint16_t*>(piece(lane, k / 8)) + k % 8;
+            if ((*at & 0x7fffu) == 0x7c00u) *at = 0x7fffu;
           }
-          *reinterpret_cast<uint4*>(dst + (k >> 3) * S::kAtom + (((k & 7) ^ (r & 7)) << 4)) =
-              make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
       fence_proxy_async_smem();
@@ -467,13 +530,97 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         Meta& mt = c.meta[tiles % kMetas];
         const bool partial = mt.partial != 0;
-        // The tile in two code paths: a short one for what most tiles are (every key seen, every
-        // row with a reference that holds, scales not far apart), which leaves off where a weight
-        // is too large, and one for everything, from there on.  (The code has to stay small: with
-        // the rare cases in the common loop, 1.25 ms; with that loop unrolled over the tile, 1.5.)
+        // What is masked becomes -infinity, a row's first reference the largest exponent of the
+        // tile.
+        const bool begin = __any_sync(0xffffffffu, real && m == -INFINITY);
+        if (partial || begin) {
+          float top = -INFINITY;
+          int at = 0;
+#pragma unroll 1
+          for (int j = 0; j < kGroups / 2; ++j) {
+            uint32_t s[32];
+            tmem_ld32_start(ts + j * 32, s);
+            tmem_ld32_wait(s);
+            if (partial) {
+              uint32_t see = 0;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {  // positions t0 .. t0 + 15: [lo, pos] and [0, s0)
+                const int t0 = mt.pos[2 * j + h];
+                // bits of the positions before t (0 .. 2^31 - 1, as t0 is)
+                auto below = [&](int t) { return (1u << min(max(t - t0, 0), 16)) - 1u; };
+                see |= (below(max(pos + 1, 0)) & (~below(lo) | below(s0)) & 0xffffu) << (16 * h);
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1u ? s[k] : 0xff800000u;
+              tmem_st32_start(ts + j * 32, s);
+            }
+            if (begin) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float t = __uint_as_float(s[16 * h]);
+#pragma unroll
+                for (int k = 1; k < 16; ++k) t = fmaxf(t, __uint_as_float(s[16 * h + k]));
+                const int lv = mt.ev[2 * j + h];
+                t = fmaf(t, fmaxf(qs * mt.ks[2 * j + h], 0x1p-126f), (float)lv);
+                if (t > top) {
+                  top = t;
+                  at = lv + kUp;
+                }
+              }
+            }
+          }
+          if (m == -INFINITY && top != -INFINITY) {
+            m = top;
+            base = at;
+          }
+          tmem_st_wait();
+        }
+        // A larger reference, by a whole number: what is there already follows exactly.
+        auto raise = [&](float by, int next, int cols) {
+          m += by;
+          if ((float)(next - base) - by > 60.f) next = (int)floorf((float)base + by + 60.f);
+          if (by == 0.f) next = base;
+          // (square roots, taken twice: weights may lie further apart than a float reaches)
+          const float f = ex2_fast(0.5f * ((float)(next - base) - by)), a = ex2_fast(-0.5f * by);
+          base = next;
+          l = l * f * f;
+          __syncwarp();
+          if (v > w.ta) {
+#pragma unroll 1
+            for (int k = 0; k < kD / 16; ++k) {
+              float o[16];
+              tmem_ld16(to + k * 16, o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = o[j] * a * a;
+              chunk::tmem_st16(to + k * 16, o);
+            }
+          }
+          tmem_st_wait();  // (the weights before these, read back)
+          // (in two steps: 2^15 to 2^-24 is more than fp16 has below 1)
+          const int half = (int)by >> 1, rest = (int)by - half;
+          const __half2 down0 = __float2half2_rn(by < 40.f ? pow2(-half) : 0.f);
+          const __half2 down1 = __float2half2_rn(by < 40.f ? pow2(-rest) : 0.f);
+#pragma unroll 1
+          for (int k = 0; k < cols; ++k) {
+            uint32_t y[16];
+            tmem_ld16_start(ts + k * 16, y);
+            tmem_ld_wait(y);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const __half2 z = __hmul2(__hmul2(*reinterpret_cast<__half2*>(&y[j]), down0), down1);
+              y[j] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+            tmem_st16_start(ts + k * 16, y);
+            tmem_st_wait();
+          }
+        };
+        // The tile in two code paths: a short one for what most tiles are (scales not far apart,
+        // weights that a float holds), and one for everything, from where that one leaves off.
+        // (The code has to stay small: with the rare cases in the common loop, 1.25 ms; with that
+        // loop unrolled over the tile, 1.5.)
         int i = 0;
-        if (!partial && !__any_sync(0xffffffffu, m == -INFINITY || base - (mt.least + kUp) > 64)) {
-          const float ref = (float)kUp - m;
+        bool far = __any_sync(0xffffffffu, base - (mt.least + kUp) > 64);
+        if (!far) {
           uint32_t raw[2][32];
           tmem_ld32_start(ts, raw[0]);
 #pragma unroll 1
@@ -482,7 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float part[4];
             const float4 ks = *reinterpret_cast<const float4*>(mt.ks + 2 * i);
             const int4 lv = *reinterpret_cast<const int4*>(mt.ev + 2 * i);
-            const float zs[4] = {qs * ks.x, qs * ks.y, qs * ks.z, qs * ks.w};
+            const float zs[4] = {fmaxf(qs * ks.x, 0x1p-126f), fmaxf(qs * ks.y, 0x1p-126f),
+                                 fmaxf(qs * ks.z, 0x1p-126f), fmaxf(qs * ks.w, 0x1p-126f)};
+            const float ref = m == -INFINITY ? -INFINITY : (float)kUp - m;
             const int ev[4] = {lv.x, lv.y, lv.z, lv.w};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -511,7 +660,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const float high = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-            if (__any_sync(0xffffffffu, high > kFull)) break;
+            if (__any_sync(0xffffffffu, high > kFull)) {
+              if (i == 0) tmem_ld32_wait(raw[0]);  // (a load that nobody waited for)
+              far = __any_sync(0xffffffffu, high == INFINITY);
+              if (far) break;
+              // these columns again, with a reference that is the largest sum's
+              const bool up = high > kFull;
+              int next = ev[0];
+#pragma unroll
+              for (int h = 1; h < 4; ++h)
+                if (part[h] == high) next = ev[h];
+              raise(up ? (float)((int)(__float_as_uint(high) >> 23) - 127 - kUp) : 0.f, next + kUp,
+                    i);
+              far = __any_sync(0xffffffffu, base - (mt.least + kUp) > 64);
+              if (far) break;
+              tmem_ld32_start(ts + i * 32, raw[0]);
+              i -= 2;
+              continue;
+            }
 #pragma unroll
             for (int h = 0; h < 4; ++h)
               l = fmaf(part[h], pow2(max(base - kUp - ev[h], -126)), l);
@@ -519,18 +685,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16_start(ts + i * 16, wt[0]);
             tmem_st16_start(ts + i * 16 + 16, wt[1]);
           }
-          // (a load that nobody waited for)
-          if (i == 0) tmem_ld32_wait(raw[0]);
           tmem_st_wait();
         }
         // exponents of the weights of groups 2 i and 2 i + 1
         auto exponents = [&](int i, const uint32_t (&s)[32], float (&e)[32]) {
           const float2 ks = *reinterpret_cast<const float2*>(mt.ks + 2 * i);
           const int2 lv = *reinterpret_cast<const int2*>(mt.ev + 2 * i);
-          const float ref = (float)kUp - (m == -INFINITY ? 0.f : m);
+          const float ref = m == -INFINITY ? -INFINITY : (float)kUp - m;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float zs = qs * (h ? ks.y : ks.x), off = (float)(h ? lv.y : lv.x) + ref;
+            const float zs = fmaxf(qs * (h ? ks.y : ks.x), 0x1p-126f);
+            const float off = (float)(h ? lv.y : lv.x) + ref;
 #pragma unroll
             for (int k = 16 * h; k < 16 * h + 16; k += 2) {
               e[k] = __uint_as_float(s[k]);
@@ -538,51 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               fma2(e[k], e[k + 1], zs, off, off);
             }
           }
-          if (partial) {
-            uint32_t see = 0;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {  // positions t0 .. t0 + 15: [lo, pos] and [0, s0)
-              const long long t0 = mt.pos[2 * i + h];
-              auto below = [&](long long t) {  // bits of the positions before t
-                const long long n = min(max(t - t0, 0ll), 16ll);
-                return (1u << n) - 1u;
-              };
-              see |= (below((long long)pos + 1) & (~below(lo) | below(s0)) & 0xffffu) << (16 * h);
-            }
-#pragma unroll
-            for (int k = 0; k < 32; ++k) e[k] = (see >> k) & 1u ? e[k] : -INFINITY;
-          }
         };
-        // A row's first reference: its largest exponent in the tile.
-        if (i == 0 && __any_sync(0xffffffffu, m == -INFINITY)) {
-          float top = -INFINITY;
-          int at = 0;
-#pragma unroll 1
-          for (int j = 0; j < kGroups / 2; ++j) {
-            uint32_t s[32];
-            float e[32];
-            tmem_ld32_start(ts + j * 32, s);
-            tmem_ld32_wait(s);
-            exponents(j, s, e);
-            float t0 = e[0], t1 = e[16];
-#pragma unroll
-            for (int k = 1; k < 16; ++k) {
-              t0 = fmaxf(t0, e[k]);
-              t1 = fmaxf(t1, e[16 + k]);
-            }
-            if (fmaxf(t0, t1) > top) {
-              top = fmaxf(t0, t1);
-              at = mt.ev[2 * j + (t1 > t0 ? 1 : 0)] + kUp;
-            }
-            __syncwarp();
-          }
-          if (m == -INFINITY && top != -INFINITY) {
-            m = top - (float)kUp;
-            base = at;
-          }
-          __syncwarp();
-        }
-        const bool far = __any_sync(0xffffffffu, base - (mt.least + kUp) > 64);
 #pragma unroll 1
         for (; i < kGroups / 2; ++i) {
           uint32_t s[32];
@@ -609,8 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool high = fmaxf(part[0], part[1]) > kFull;
             if (again || !__any_sync(0xffffffffu, high)) break;
-            // A larger reference, by a whole number: what is there already follows exactly (and
-            // an infinite weight stays one).
+            // (an infinite weight stays one)
             uint32_t x[32];
             tmem_ld32_start(ts + i * 32, x);
             tmem_ld32_wait(x);
@@ -618,48 +738,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             float top = e[0];
 #pragma unroll
             for (int k = 1; k < 32; ++k) top = fmaxf(top, e[k]);
-            const float by =
-                high ? fminf(fmaxf(ceilf(top) - (float)kUp, 0.f), 4096.f) : 0.f;
-            m += by;
-            int next = max(mt.ev[2 * i], mt.ev[2 * i + 1]) + kUp;
-            if ((float)(next - base) - by > 60.f) next = (int)floorf((float)base + by + 60.f);
-            if (by == 0.f) next = base;
-            // (square roots, taken twice: weights may lie further apart than a float reaches)
-            const float f = ex2_fast(0.5f * ((float)(next - base) - by)), a = ex2_fast(-0.5f * by);
-            base = next;
-            l = l * f * f;
-            __syncwarp();
-            if (v > w.ta) {
-#pragma unroll 1
-              for (int k = 0; k < kD / 16; ++k) {
-                float o[16];
-                tmem_ld16(to + k * 16, o);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = o[j] * a * a;
-                chunk::tmem_st16(to + k * 16, o);
-              }
-            }
-            tmem_st_wait();  // (the groups' before this one, read back)
-            // (in two steps: 2^15 to 2^-24 is more than fp16 has below 1)
-            const int half = (int)by >> 1, rest = (int)by - half;
-            const __half2 down0 = __float2half2_rn(by < 40.f ? pow2(-half) : 0.f);
-            const __half2 down1 = __float2half2_rn(by < 40.f ? pow2(-rest) : 0.f);
-#pragma unroll 1
-            for (int k = 0; k < i; ++k) {
-              uint32_t y[16];
-              tmem_ld16_start(ts + k * 16, y);
-              tmem_ld_wait(y);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const __half2 z = __hmul2(__hmul2(*reinterpret_cast<__half2*>(&y[j]), down0), down1);
-                y[j] = *reinterpret_cast<const uint32_t*>(&z);
-              }
-              tmem_st16_start(ts + k * 16, y);
-              tmem_st_wait();
-            }
+            raise(high ? fminf(fmaxf(ceilf(top) - (float)kUp, 0.f), 4096.f) : 0.f,
+                  max(mt.ev[2 * i], mt.ev[2 * i + 1]) + kUp, i);
             exponents(i, x, e);
           }
           const int2 lv = *reinterpret_cast<const int2*>(mt.ev + 2 * i);
+          far = far || __any_sync(0xffffffffu, base - (mt.least + kUp) > 64);
           if (far) {  // scales far below the reference's: their weights' sum by itself
             uint32_t x[32];
             tmem_ld32_start(ts + i * 32, x);
@@ -728,28 +812,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float z = m + (float)(ex - base);  // the sum is f 2^z
       const Factor by(f, base - ex);
       const int slot = (2 * blockIdx.x + (begins ? 1 : 0)) * (2 * kRows) + ab * kRows + r;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + row * kD;
-      float* part = p.part_o + (long long)slot * kD;
-#pragma unroll
-      for (int k = 0; k < kD / 16; ++k) {
-        float o[16];
+      auto outputs = [&](int k, float (&o)[16]) {
         __syncwarp();
         tmem_ld16(to + k * 16, o);
+        uint32_t nans = 0u;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if ((bad[k / 2] >> ((k & 1) * 16 + j)) & 1u) o[j] = NAN;
-        if (!real) continue;
-        if (whole) {
+        for (int j = 0; j < kD / 32; ++j)
+          if (j == (k >> 1)) nans = bad[j];
+        nans = nans >> ((k & 1) * 16) & 0xffffu;
+        if (nans)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if ((nans >> j) & 1u) o[j] = NAN;
+      };
+      if (whole) {
+#pragma unroll 1
+        for (int k = 0; k < kD / 16; ++k) {
+          float o[16];
+          outputs(k, o);
           uint32_t y[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) y[j] = pack_bf16(by(o[2 * j]), by(o[2 * j + 1]));
-          reinterpret_cast<uint4*>(out)[2 * k] = make_uint4(y[0], y[1], y[2], y[3]);
-          reinterpret_cast<uint4*>(out)[2 * k + 1] = make_uint4(y[4], y[5], y[6], y[7]);
-        } else {
+          *piece(lane, 2 * k) = make_uint4(y[0], y[1], y[2], y[3]);
+          *piece(lane, 2 * k + 1) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        __syncwarp();
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + first_row * kD;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            reinterpret_cast<float4*>(part)[4 * k + j] =
-                make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        for (int k = 0; k < kLoads; ++k) {
+          const int to_row = k * kAtOnce + lane / kChunks;
+          const long long at = (long long)__shfl_sync(0xffffffffu, rel, to_row) * kD;
+          if ((reals >> to_row) & 1u)
+            reinterpret_cast<uint4*>(out + at)[lane % kChunks] = *piece(to_row, lane % kChunks);
+        }
+      } else {
+        float* part = p.part_o + (long long)(slot - lane) * kD;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+          for (int k = 0; k < kD / 32; ++k) {
+            float o[16];
+            outputs(half * (kD / 32) + k, o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *piece(lane, 4 * k + j) =
+                  make_uint4(__float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]),
+                             __float_as_uint(o[4 * j + 2]), __float_as_uint(o[4 * j + 3]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < kLoads; ++k) {
+            const int to_row = k * kAtOnce + lane / kChunks;
+            if ((reals >> to_row) & 1u)
+              reinterpret_cast<uint4*>(part + to_row * kD + half * (kD / 2))[lane % kChunks] =
+                  *piece(to_row, lane % kChunks);
+          }
+          __syncwarp();
         }
       }
       if (real) {
@@ -758,6 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (p.a.lse)
           p.a.lse[row] = l == 0.f ? -INFINITY : (z + log2f(f)) / kLog2e;
       }
+      __syncwarp();
       tc_fence_before();  // O is read: the next segment's first weights release it
     }
     if (!ok) hd = Header{-1, -1, 0, 0};
@@ -949,29 +1068,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && w.next()) {
       if (w.ta == w.tb) continue;
       const bool two = w.tokens > p.per;
-      ok = wait(&c.q_full[0], used_a & 1) && (!two || wait(&c.q_full[1], used_b & 1));
-      if (!ok) break;
-      ++used_a;
-      used_b += two;
       // at v: the outputs of tile v - 1 and the scores of tile v, A's and then B's
 #pragma unroll 1
       for (int v = w.ta; v <= w.tb; ++v) {
         const bool first = v == w.ta, end = v == w.tb, more = v - 1 > w.ta;
         if (!end && !(ok = wait(&c.wide_full[tiles & 1][0], (tiles >> 1) & 1))) break;
-        if (!first && !(ok = outputs(0, done_a, tiles - 1, more))) break;
+        if (first ? !(ok = wait(&c.q_full[0], used_a++ & 1))
+                  : !(ok = outputs(0, done_a, tiles - 1, more)))
+          break;
         if (end)
           umma_commit_elect(&c.o_full[0]);
         else
           scores(0, tiles);
         if (two) {
-          if (!first && !(ok = outputs(1, done_b, tiles - 1, more))) break;
+          if (first ? !(ok = wait(&c.q_full[1], used_b++ & 1))
+                    : !(ok = outputs(1, done_b, tiles - 1, more)))
+            break;
           if (end)
             umma_commit_elect(&c.o_full[1]);
           else
             scores(1, tiles);
         }
         if (!first) umma_commit_elect(&c.wide_empty[(tiles - 1) & 1][1]);
-        umma_commit_elect(end ? &c.q_empty : &c.wide_empty[tiles & 1][0]);
+        if (!end) umma_commit_elect(&c.wide_empty[tiles & 1][0]);
         tiles += !end;
       }
     }

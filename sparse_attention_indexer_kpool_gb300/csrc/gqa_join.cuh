@@ -73,8 +73,13 @@ __device__ __forceinline__ void merge(Joined& a, const Joined& b) {
 // a lane's columns of a row
 template <int kD>
 __device__ __forceinline__ void load_part(Joined& j, const float* row, int lane) {
-#pragma unroll
-  for (int k = 0; k < kD / 32; ++k) j.x[k] = row[lane * (kD / 32) + k];
+  if constexpr (kD == 128) {
+    const float4 x = reinterpret_cast<const float4*>(row)[lane];
+    j.x[0] = x.x; j.x[1] = x.y; j.x[2] = x.z; j.x[3] = x.w;
+  } else {
+    const float2 x = reinterpret_cast<const float2*>(row)[lane];
+    j.x[0] = x.x; j.x[1] = x.y;
+  }
 }
 
 template <int kD, int kRows>
@@ -180,14 +185,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
   }
   __syncthreads();
   const int used = rows.used(), pieces = n_begun * used;
-  const bool wide = pieces <= 2 * (int)gridDim.x;  // a block a piece
-  const int step = wide ? gridDim.x : gridDim.x * kJoinWarps;
-#pragma unroll 1
-  for (int i = wide ? blockIdx.x : warp * gridDim.x + blockIdx.x; i < pieces; i += step) {
-    const int g0 = begun[i / used], r = i % used, item = heads[g0].start_item;
-    const long long row = rows(item, heads[g0].tokens, r);
-    if (row < 0) continue;
-    int n = 1;  // its workers: g0 .. g0 + n - 1
+  // workers of the item that g0 began: g0 .. g0 + n - 1
+  auto workers_of = [&](int g0, int item) {
+    int n = 1;
     for (unsigned stop = 0; !stop;) {
       const int s = g0 + n + lane;
       const Header hd = heads[min(s, workers - 1)];
@@ -196,14 +196,73 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       const int k = stop ? __ffs(stop) - 1 : 32;  // before the stopping one
       n += k + (stop ? __shfl_sync(0xffffffffu, (int)mine, k & 31) : 0);
     }
-    const int per = wide ? (n + kJoinWarps - 1) / kJoinWarps : n;
-    const int s0 = g0 + (wide ? min(n, warp * per) : 0);
+    return n;
+  };
+  if (pieces > 2 * (int)gridDim.x) {
+    // A warp two rows at a time: those of an item with few workers (most of a chunk's, whose items
+    // are about as long as a worker's share) with their partials all on their way at once.
+    const int pairs = (used + 1) / 2;
+#pragma unroll 1
+    for (int i = warp * gridDim.x + blockIdx.x; i < n_begun * pairs; i += gridDim.x * kJoinWarps) {
+      const int g0 = begun[i / pairs], r0 = i % pairs * 2, item = heads[g0].start_item;
+      const int n = workers_of(g0, item);
+      long long row[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        row[u] = r0 + u < used ? rows(item, heads[g0].tokens, r0 + u) : -1;
+      Joined j[2];
+      if (n > 4) {
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u)
+          if (row[u] >= 0)
+            store_joined<kD>(p, row[u],
+                             join_parts<kD, kRows>(p, heads, g0, g0, g0 + n, r0 + u, lane), lane);
+        continue;
+      }
+#pragma unroll 1
+      for (int t = 0; t < n; t += 2) {
+        Joined x[2][2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int s = g0 + t + v;
+          const bool part = t + v < n && (t + v == 0 || (heads[s].cont & 1));
+          const int slot = (t + v == 0 ? 2 * s + 1 : 2 * s) * kRows + r0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            x[v][u] = nothing();
+            if (!part || row[u] < 0) continue;
+            const float4 ml = __ldcs(p.part_ml + slot + u);
+            x[v][u].m = ml.x;
+            x[v][u].z = ml.y;
+            x[v][u].f = ml.z;
+            load_part<kD>(x[v][u], p.part_o + (long long)(slot + u) * kD, lane);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (t == 0)
+            j[u] = x[0][u];
+          else
+            merge(j[u], x[0][u]);
+          merge(j[u], x[1][u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (row[u] >= 0) store_joined<kD>(p, row[u], j[u], lane);
+    }
+    return;
+  }
+  // a block a row, each warp a part of the partials
+#pragma unroll 1
+  for (int i = blockIdx.x; i < pieces; i += gridDim.x) {
+    const int g0 = begun[i / used], r = i % used, item = heads[g0].start_item;
+    const long long row = rows(item, heads[g0].tokens, r);
+    if (row < 0) continue;
+    const int n = workers_of(g0, item), per = (n + kJoinWarps - 1) / kJoinWarps;
+    const int s0 = g0 + min(n, warp * per);
     const Joined j =
         join_parts<kD, kRows>(p, heads, g0, s0, min(s0 + per, g0 + n), r, lane);
-    if (!wide) {
-      store_joined<kD>(p, row, j, lane);
-      continue;
-    }
     parts[warp][lane] = j;
     __syncthreads();
     if (warp == 0) {
