@@ -63,9 +63,10 @@ __global__ void __launch_bounds__(kThreads) gqa_attend_simt_kernel(GqaArgs a) {
   const int per = D / 16;
   for (unsigned v0 = 0; v0 < (unsigned)nv; v0 += kTile) {
     __syncthreads();
+    int page = -1;
     if (tid < kTile) {
       const unsigned v = v0 + tid;
-      int page = -1, p = 0;
+      int p = 0;
       if (v < (unsigned)nv) {
         long long x;
         if (ids) {
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) gqa_attend_simt_kernel(GqaArgs a) {
       spage[tid] = page;
       srow[tid] = p % ps;
     }
-    __syncthreads();
+    if (!__syncthreads_or(page >= 0)) continue;  // (a list's -1 entries)
     for (int i = tid; i < kTile * per * 2; i += kThreads) {
       const bool key = i < kTile * per;
       const int j = key ? i : i - kTile * per, r = j / per, d = (j - r * per) * 16;
@@ -173,9 +174,18 @@ size_t gqa_attend_workspace_size(int, int Hq, int Hkv, int D, int dtype) {
 }
 
 int launch_gqa_attend(const GqaArgs& a, void* workspace, cudaStream_t stream) {
-  if (gqa_split_ok(a.kv.D, a.dtype))
-    return !a.block_ids && a.T >= 8ll * a.B ? launch_gqa_chunk(a, workspace, stream)
-                                            : launch_gqa_split(a, workspace, stream);
+  if (gqa_split_ok(a.kv.D, a.dtype)) {
+    // Rows of a sequence together (tcgen05, 128 a tile) or each token's by themselves, in us, by
+    // new tokens of each sequence (8 KV heads of 8 query heads):
+    //   4 sequences on 1,500 keys: 4 tokens 31.4 / 15.8, 8 tokens 32.4 / 35.0, 12 32.4 / 38.0
+    //   16 on 8,000: 4 tokens 150 / 131, 8 153 / 235, 32 180 / 856
+    //   16 on 64: 4 tokens 18.8 / 21.2, 8 18.9 / 24.9, 64 30.6 / 72.5
+    //   16 on 8,000 with one query head a KV head, 2 of them: 4 tokens 53.5 / 39.8, 8 53.9 / 77
+    // and a few short rows, however many a sequence has, by a cluster each (gqa_split.cu).
+    if (a.block_ids || a.T < 8ll * a.B) return launch_gqa_split(a, workspace, stream);
+    const int rc = launch_gqa_split(a, workspace, stream, true);
+    return rc == kElsewhere ? launch_gqa_chunk(a, workspace, stream) : rc;
+  }
   const int G = a.Hq / a.kv.Hkv;
   auto kernel =
       a.dtype == DSA_BF16 ? gqa_attend_simt_kernel<__nv_bfloat16> : gqa_attend_simt_kernel<float>;

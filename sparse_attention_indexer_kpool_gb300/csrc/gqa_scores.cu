@@ -502,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 2) gqa_scores_chunk_kernel(const Gro
     const bool real = i < live && head < G;
     const uint32_t* src = reinterpret_cast<const uint32_t*>(
         static_cast<const __nv_bfloat16*>(a.q) +
-        ((long long)(c0 + (real ? i0 + i : j0)) * a.Hq + (long long)h * G + (real ? head : 0)) * kD);
+        ((long long)(c0 + (real ? i0 + i : j0)) * a.Hq + (long long)h * G + (real ? head : 0)) *
+            kD);
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       q[n][k][0] = real ? __ldg(src + 8 * k + t) : 0u;
@@ -756,10 +757,12 @@ int launch_groups(const GqaScoreArgs& a, cudaStream_t stream) {
   GroupArgs ga{a, 1, 1};
   const int G = a.Hq / a.Hkv;
   while (ga.pad < G) ga.pad *= 2;
-  // tokens together where every SM has a CTA of them
   const long long rows = (long long)a.T * a.Hkv;
   const int n_tiles = ga.pad <= 16 ? 2 : 4, tokens = 8 * n_tiles / ga.pad;
-  if (rows >= (long long)num_sms() * tokens * kWarps) {
+  // Tokens together or a CTA (or several) for each, tables of 48 / 470 blocks, in us: 256 rows
+  // (tokens x KV heads) 9.6 / 34.8 and 7.2 / 10.3, 512 rows 9.7 / 34.8 and 12.8 / 18.4, 1,024 rows
+  // 9.8 / 34.8 and 22.7 / 34.5, 4,096 rows 11.9 / 45.7 and 76 / 116.
+  if (rows >= 7ll * num_sms() || (rows >= 3ll * num_sms() && a.NB <= 128)) {
     ga.tokens = tokens;
     if (ga.pad == 8) return launch_chunk<kD, 2, 8>(ga, stream);
     if (ga.pad == 16) return launch_chunk<kD, 2, 16>(ga, stream);

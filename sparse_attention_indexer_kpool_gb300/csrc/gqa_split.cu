@@ -54,6 +54,10 @@ constexpr int kLeast = 2;                      // tiles of a share, at least
 //   16 x 8 on 2,048 (8) 16.8 / 27.5, 8,192 (32) 48.2 / 59.9
 // (lengths that differ leave a cluster waiting for its longest: so no more than that)
 constexpr int kMost = 12, kMostFull = 32;
+// and where there are tokens enough for the chunk kernel (8 KV heads of 8 query heads, 16 tokens
+// of one sequence, cluster / chunk: on 64 keys 9.4 / 17.5, on 1,500 16.1 / 24.9, on 8,000 (32)
+// 40.6 / 33.5)
+constexpr int kMostTogether = 16;
 constexpr int kRingBytes = 2 * 2 * kKeys * 128;  // of a warp
 
 struct Params {
@@ -647,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               } else if (rel > kRaise - (float)kUp) {
                 m[n][i] += rel;
                 move = -rel;
-                // (the square roots, taken twice: weights may lie further apart than a float reaches)
+                // (square roots, taken twice: weights may lie further apart than a float reaches)
                 const float a = ex2_fast(-0.5f * rel);
                 int to = lv;
                 if ((float)(lv - base[n][i]) - rel > 60.f)
@@ -775,7 +779,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int n = 0; n < kN; ++n) far = max(far, max(base[n][0], base[n][1]));
       far -= (kBoxes == 1 ? mt.ev[0] : min(mt.ev[0], mt.ev[1])) + kUp;
-      if (__any_sync(0xffffffffu, !all || unset || far > 64) || !tile(std::true_type{}))
+      // (nothing there: a list's -1 entries)
+      const bool none = mt.pos[0] == 0x7fffffff && mt.pos[kBoxes - 1] == 0x7fffffff;
+      if ((__any_sync(0xffffffffu, !all || unset || far > 64) || !tile(std::true_type{})) && !none)
         tile(std::false_type{});
       __syncwarp();  // the tile is read
       issue();
@@ -900,8 +906,30 @@ struct Rows {
   }
 };
 
+// Clusters of `ctas` CTAs (one an SM) that the device holds at once.
+template <typename K>
+int clusters_of(K kernel, size_t bytes, int ctas) {
+  static std::atomic<int> held[64][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+  std::atomic<int>& h = held[dev][ctas == 8 ? 3 : ctas == 4 ? 2 : ctas - 1];
+  int n = h.load(std::memory_order_relaxed);
+  if (n) return n - 1;
+  Launch l(dim3(ctas, 1, 1), kThreads, bytes, nullptr);
+  l.attr.id = cudaLaunchAttributeClusterDimension;
+  l.attr.val.clusterDim.x = ctas;
+  l.attr.val.clusterDim.y = l.attr.val.clusterDim.z = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  h.store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// together: only where a cluster takes a row tile and does so in few rounds (kElsewhere if not)
 template <int kD, int kN, int kR>
-int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
+int launch(const GqaArgs& a, void* workspace, cudaStream_t stream, bool together) {
   Params p = {};
   p.a = a;
   p.G = a.Hq / a.kv.Hkv;
@@ -909,28 +937,34 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
   p.zscale = a.sm_scale * kLog2e;
   p.cap = table_cap(a.kv.max_pages, a.kv.page_size);
   p.per_block = a.kv.page_size / kR;
-  // Workers: a warp for each kLeast tiles of what the step can hold, all of them at most.
   const long long row_tiles = (long long)a.T * a.kv.Hkv * p.hb;
   const long long seen = a.block_ids ? (long long)a.K * a.kv.page_size
                          : a.window > 0 && (long long)a.window + a.sinks < p.cap
                              ? (long long)a.window + a.sinks : p.cap;
-  const long long bound = row_tiles * ((seen + kKeys - 1) / kKeys + kExtra);
-  const long long want = (bound + kLeast - 1) / kLeast;
+  // a cluster for a row tile where the device holds all of them at once (16 of 8 CTAs are more
+  // than it does: 17.7 us instead of 9.6 for as many of 4)
+  auto kernel = gqa_split_kernel<kD, kN, kR, true>;
+  constexpr size_t kBytes = smem_bytes<kD, kN, true>();
+  int ctas = 8;
+  if (row_tiles <= num_sms()) {
+    static std::atomic<unsigned long long> done{0};
+    if (!allow_smem(kernel, kBytes, done)) return DSA_ERR_CUDA;
+    while (ctas > 1 && (row_tiles * ctas > num_sms() ||
+                        row_tiles > clusters_of(kernel, kBytes, ctas)))
+      ctas >>= 1;
+  }
+  const long long all = row_tiles * ctas;
+  const int most = together ? kMostTogether : all * 4 >= 3ll * num_sms() ? kMostFull : kMost;
+  const bool cluster =
+      row_tiles <= num_sms() && (seen + kKeys - 1) / kKeys <= (long long)most * kW * ctas;
+  if (together && !cluster) return kElsewhere;
   CUtensorMap k_map, v_map;
   const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.Hkv * a.kv.page_size;
   if (!code_map(&k_map, a.kv.k_pages, rows, kD, kR) ||
       !code_map(&v_map, a.kv.v_pages, rows, kD, kR))
     return DSA_ERR_CUDA;
-  // a cluster for a row tile where all of them fit the SMs at once
-  int ctas = 8;
-  while (ctas > 1 && row_tiles * ctas > num_sms()) ctas >>= 1;
-  const long long all = row_tiles * ctas, least = all * 4 >= 3ll * num_sms() ? kMostFull : kMost;
-  if (all <= num_sms() && (seen + kKeys - 1) / kKeys <= least * kW * ctas) {
-    auto kernel = gqa_split_kernel<kD, kN, kR, true>;
-    constexpr size_t kBytes = smem_bytes<kD, kN, true>();
-    static std::atomic<unsigned long long> done{0};
-    if (!allow_smem(kernel, kBytes, done)) return DSA_ERR_CUDA;
-    Launch l(dim3((unsigned)(row_tiles * ctas), 1, 1), kThreads, kBytes, stream);
+  if (cluster) {
+    Launch l(dim3((unsigned)all, 1, 1), kThreads, kBytes, stream);
     cudaLaunchAttribute attr[2];
     attr[0] = l.attr;
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -940,25 +974,28 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
     l.cfg.numAttrs = 2;
     return launch_kernel(&l.cfg, kernel, k_map, v_map, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
   }
-  const int most = workers_of(), workers = want < most ? (int)want : most;
+  // Workers: a warp for each kLeast tiles of what the step can hold, all of them at most.
+  const long long bound = row_tiles * ((seen + kKeys - 1) / kKeys + kExtra);
+  const long long want = (bound + kLeast - 1) / kLeast;
+  const int limit = workers_of(), workers = want < limit ? (int)want : limit;
   const int grid = workers < num_sms() ? workers : num_sms();
   p.workers = workers;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float4*>(p.part_o + (size_t)workers * 2 * 8 * kN * kD);
   p.head = reinterpret_cast<Header*>(p.part_ml + (size_t)workers * 2 * 8 * kN);
-  auto kernel = gqa_split_kernel<kD, kN, kR, false>;
+  auto shares = gqa_split_kernel<kD, kN, kR, false>;
   static std::atomic<unsigned long long> done{0};
-  if (!allow_smem(kernel, smem_bytes<kD, kN, false>(), done)) return DSA_ERR_CUDA;
+  if (!allow_smem(shares, smem_bytes<kD, kN, false>(), done)) return DSA_ERR_CUDA;
   Launch l(dim3(grid, 1, 1), kThreads, smem_bytes<kD, kN, false>(), stream);
-  if (launch_kernel(&l.cfg, kernel, k_map, v_map, p) != cudaSuccess) return DSA_ERR_CUDA;
+  if (launch_kernel(&l.cfg, shares, k_map, v_map, p) != cudaSuccess) return DSA_ERR_CUDA;
   const JoinArgs j{p.part_o, p.part_ml, p.head, workers, static_cast<__nv_bfloat16*>(a.out), a.lse};
   return launch_join<kD>(j, Rows<kN>{a.Hq, a.kv.Hkv, p.G, p.hb}, row_tiles, stream);
 }
 
 template <int kD, int kN>
-int launch_r(const GqaArgs& a, void* workspace, cudaStream_t stream) {
-  return a.kv.page_size % 32 == 0 ? launch<kD, kN, 32>(a, workspace, stream)
-                                  : launch<kD, kN, 16>(a, workspace, stream);
+int launch_r(const GqaArgs& a, void* workspace, cudaStream_t stream, bool together) {
+  return a.kv.page_size % 32 == 0 ? launch<kD, kN, 32>(a, workspace, stream, together)
+                                  : launch<kD, kN, 16>(a, workspace, stream, together);
 }
 
 }  // namespace
@@ -970,11 +1007,13 @@ size_t gqa_split_workspace_size(int Hq, int Hkv, int D) {
   return (size_t)workers_of() * (2 * cols * (D * 4 + 16) + sizeof(Header));
 }
 
-int launch_gqa_split(const GqaArgs& a, void* workspace, cudaStream_t stream) {
+int launch_gqa_split(const GqaArgs& a, void* workspace, cudaStream_t stream, bool together) {
   const bool one = a.Hq / a.kv.Hkv <= 8;
   if (a.kv.D == 128)
-    return one ? launch_r<128, 1>(a, workspace, stream) : launch_r<128, 2>(a, workspace, stream);
-  return one ? launch_r<64, 1>(a, workspace, stream) : launch_r<64, 2>(a, workspace, stream);
+    return one ? launch_r<128, 1>(a, workspace, stream, together)
+               : launch_r<128, 2>(a, workspace, stream, together);
+  return one ? launch_r<64, 1>(a, workspace, stream, together)
+             : launch_r<64, 2>(a, workspace, stream, together);
 }
 
 }  // namespace dsa
