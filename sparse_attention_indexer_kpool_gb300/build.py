@@ -29,7 +29,7 @@ SOURCES = ["dsa_abi.cu", "kpool_compress.cu", "index_scores.cu", "index_scores_u
            "topk.cu", "mla_decode.cu", "mla_umma.cu", "select_noalloc.cu",
            "indexer_proj.cu", "paged_step.cu", "mla_chunk.cu", "mla_chunk_umma.cu",
            "mla_chunk_pair.cu", "mla_chunk_f8.cu", "gqa_cache.cu", "gqa_scores.cu",
-           "gqa_attend.cu", "gqa_split.cu", "gqa_chunk.cu"]
+           "gqa_scores_chunk.cu", "gqa_attend.cu", "gqa_split.cu", "gqa_chunk.cu"]
 
 
 def _nvcc() -> str:

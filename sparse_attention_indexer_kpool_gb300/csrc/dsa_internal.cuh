@@ -410,6 +410,7 @@ struct GqaScoreArgs {
   int32_t* status;
 };
 int launch_gqa_scores(const GqaScoreArgs& a, int dtype, cudaStream_t stream);
+int launch_gqa_scores_chunk(const GqaScoreArgs& a, cudaStream_t stream);
 struct GqaArgs {
   const void* q;
   GqaKv kv;

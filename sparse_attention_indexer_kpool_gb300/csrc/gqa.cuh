@@ -57,6 +57,11 @@ __host__ __device__ inline int table_cap(int max_pages, int page_size) {
   return n < 0x7fffffffll ? (int)n : 0x7fffffff;
 }
 
+// Block j, forced into the selection of a token whose own block is `mine`.
+__device__ __forceinline__ bool forced(const GqaScoreArgs& a, int mine, int j) {
+  return j <= mine && (j < a.sink_blocks || (long long)j > (long long)mine - a.local_blocks);
+}
+
 struct Launch {  // a launch that may start while the kernel before it ends
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg;

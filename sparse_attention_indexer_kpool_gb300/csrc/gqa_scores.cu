@@ -4,8 +4,9 @@
 // with m_g, l_g the maximum and the sum of exp(z - m) over the candidates j < n: two passes
 // over the means, the first for m and l, the second for the sum over the group's heads.
 //
-// Two kernels: one on the tensor cores (bf16 queries, head dim 64 or 128, groups of up to 32
-// heads), and a generic one (any geometry and type), a CTA a token and KV head, a warp a block.
+// Here: a kernel on the tensor cores for few tokens (bf16 queries, head dim 64 or 128, groups of
+// up to 32 heads), and a generic one (any geometry and type), a CTA a token and KV head, a warp a
+// block.  That for chunks is gqa_scores_chunk.cu.
 #include <cooperative_groups.h>
 
 #include "gqa.cuh"
@@ -43,9 +44,6 @@ __device__ __forceinline__ Row row_of(const GqaScoreArgs& a, int t, bool reports
 __device__ __forceinline__ int page_of(const GqaScoreArgs& a, int b, int j) {
   const int page = a.block_table[(long long)b * a.max_pages + j];
   return page >= 0 && page < a.n_pages ? page : -1;
-}
-__device__ __forceinline__ bool forced(const GqaScoreArgs& a, int mine, int j) {
-  return j <= mine && (j < a.sink_blocks || (long long)j > (long long)mine - a.local_blocks);
 }
 
 // ---- generic ---------------------------------------------------------------------
@@ -144,7 +142,6 @@ constexpr int kPadG = 32;            // heads of a group, at most
 struct GroupArgs {
   GqaScoreArgs a;
   int pad;                           // G up to a power of two
-  int tokens;                        // of a warp (chunks)
 };
 
 // Sums over a token's `pad` columns, left in its first: a lane's two, its neighbours', n tiles.
@@ -442,291 +439,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Prompt chunks: a CTA takes neighbouring tokens of a sequence and one KV head, each warp 32
-// columns of them (32 / G tokens, G up to a power of two), and runs through the means in
-// tiles of 64 blocks that all its warps read from shared memory.  The products, and the two
-// passes, are those above.  Three tiles are in the ring: one in use, two on their way, whose
-// pages were looked up a tile earlier.  A row's 16-byte piece c lies at c ^ (row & 7), so that
-// ldmatrix reads eight rows' pieces without a bank conflict, and hands them over in the order
-// that a product takes them (pieces read by the lanes themselves cost two moves a product).
-constexpr int kBlocks = 64, kRing = 3;
-
-// kPad: G up to a power of two where that is known (0: any)
-template <int kD, int kN, int kPad>
-__global__ void __launch_bounds__(kThreads, 2) gqa_scores_chunk_kernel(const GroupArgs ga) {
-  constexpr int kSteps = kD / 16, kPieces = kD / 8;  // 16-byte pieces of a row
-  constexpr int kCopies = kBlocks * kPieces / kThreads;       // of a thread and tile
-  extern __shared__ __align__(16) unsigned char ring[];       // [kRing][kBlocks][kD] bf16
-  __shared__ uint32_t s_none[kRing][2];                       // blocks of a tile without a page
-  pdl_wait();
-  pdl_launch_dependents();
-  const GqaScoreArgs& a = ga.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y, G = a.Hq / a.Hkv, cta = ga.tokens * kWarps;  // tokens of a CTA
-  if (blockIdx.x == 0 && h == 0)
-    for (int b = tid; b < a.B; b += kThreads)
-      if (a.cu_new[b] < 0 || a.cu_new[b + 1] < a.cu_new[b] || a.cu_new[b + 1] > a.T)
-        flag(a.status, DSA_DEV_BAD_LENGTH);
-  // slots from floor(cu / cta) + b on are sequence b's
-  auto first_slot = [&](int b) { return min(max(a.cu_new[b], 0), a.T) / cta + b; };
-  int b = 0;
-  for (int hi = a.B; hi - b > 1;) {
-    const int mid = (b + hi) >> 1;
-    if (first_slot(mid) <= (int)blockIdx.x) b = mid; else hi = mid;
-  }
-  const int c0 = min(max(a.cu_new[b], 0), a.T), n_new = min(a.cu_new[b + 1], a.T) - c0;
-  const int j0 = ((int)blockIdx.x - first_slot(b)) * cta;  // the CTA's first token
-  if (j0 < 0 || j0 >= n_new) return;
-  const int i0 = j0 + warp * ga.tokens, live = max(0, min(ga.tokens, n_new - i0));
-  const long long base = (long long)a.seq_lens[b] - n_new + i0;  // the first token's position
-  auto whole_at = [&](long long pos) {
-    return pos < 0 ? 0 : (int)min((long long)min(a.NB, a.max_pages), (pos + 1) / a.page_size);
-  };
-  const long long end = (long long)a.seq_lens[b] - n_new + min(j0 + cta, n_new);
-  const int most = whole_at(end - 1);  // candidates of the CTA's last token
-  if (h == 0 && tid == 0) {
-    if (base < 0) flag(a.status, DSA_DEV_BAD_LENGTH);
-    if (end > 0 && (end - 1) / a.page_size >= a.NB) flag(a.status, DSA_DEV_POOL_RANGE);
-    if (end > 0 && (end - 1) / a.page_size >= a.max_pages) flag(a.status, DSA_DEV_BAD_PAGE);
-  }
-  // queries: lane (g, t) has column g of every n tile; candidates of columns 2 t, 2 t + 1
-  uint32_t q[kN][kSteps][2];
-  int cand[kN][2], mine[kN][2];
-  float* out[kN][2];
-  int least = 0x7fffffff;  // candidates that every column has
-  int near = 0x7fffffff;   // the first block that some column's token takes as a near one
-  const int pad = kPad ? kPad : ga.pad, log = 31 - __clz(pad);
-#pragma unroll
-  for (int n = 0; n < kN; ++n) {
-    const int col = n * 8 + g, i = col >> log, head = col & (pad - 1);
-    const bool real = i < live && head < G;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(
-        static_cast<const __nv_bfloat16*>(a.q) +
-        ((long long)(c0 + (real ? i0 + i : j0)) * a.Hq + (long long)h * G + (real ? head : 0)) *
-            kD);
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      q[n][k][0] = real ? __ldg(src + 8 * k + t) : 0u;
-      q[n][k][1] = real ? __ldg(src + 8 * k + 4 + t) : 0u;
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = n * 8 + 2 * t + j, ic = c >> log;
-      const long long pos = base + ic;
-      cand[n][j] = ic < live ? whole_at(pos) : 0;
-      mine[n][j] = ic < live && pos >= 0 ? (int)(pos / a.page_size) : -1;
-      if (ic < live) {
-        least = min(least, cand[n][j]);
-        near = min(near, (int)max((long long)mine[n][j] - a.local_blocks + 1, 0ll));
-      }
-      // a token's first column writes its row
-      out[n][j] = ic < live && (c & (pad - 1)) == 0
-                      ? a.scores + ((long long)(c0 + i0 + ic) * a.Hkv + h) * a.NB + g
-                      : nullptr;
-    }
-  }
-  least = __reduce_min_sync(0xffffffffu, least);
-  near = __reduce_min_sync(0xffffffffu, near);
-  const float unit = a.sm_scale * kLog2e;
-  const int32_t* table = a.block_table + (long long)b * a.max_pages;
-  const int tiles = (most + kBlocks - 1) / kBlocks, all = (a.NB + kBlocks - 1) / kBlocks;
-
-  // ---- the ring: tile v of both passes (2 tiles in all) in slot v % kRing
-  int page[kCopies];  // of the next tile to copy: this thread's rows
-  auto look_up = [&](int v) {
-    const int w = v < tiles ? v : v - tiles;
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const int j = w * kBlocks + (tid + i * kThreads) / kPieces;
-      page[i] = -1;
-      if (v < 2 * tiles && j < most) {
-        const int pg = __ldg(table + j);
-        page[i] = pg >= 0 && pg < a.n_pages ? pg : -2;
-      }
-    }
-  };
-  auto copy = [&](int v) {  // (always a group of copies, if an empty one)
-    if (v < 2 * tiles) {
-      const int s = v % kRing;
-      if (tid < 2) s_none[s][tid] = 0u;  // (nobody reads this slot's now)
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        const int p = tid + i * kThreads, r = p / kPieces, c = p - r * kPieces;
-        const __nv_bfloat16* src =
-            a.k_mean + ((long long)max(page[i], 0) * a.Hkv + h) * kD + c * 8;
-        unsigned char* dst = ring + (((size_t)s * kBlocks + r) * kPieces + (c ^ (r & 7))) * 16;
-        cp_async16(smem_u32(dst), src, page[i] >= 0);
-        if (page[i] == -2) {
-          if (c == 0) atomicOr(&s_none[s][r >> 5], 1u << (r & 31));
-          flag(a.status, DSA_DEV_BAD_PAGE);
-        }
-      }
-    }
-    cp_async_commit();
-  };
-  float ref[kN][2], l[kN][2];  // references (-inf: none yet) and sums of the columns
-#pragma unroll
-  for (int n = 0; n < kN; ++n) {
-    ref[n][0] = ref[n][1] = -INFINITY;
-    l[n][0] = l[n][1] = 0.f;
-  }
-  // products of the blocks 16 i + g, + 8 of the tile in slot s with the queries
-  auto products = [&](int s, int i, float (&z)[kN][4]) {
-    // (lane: row `lane & 15` of the 16, the first or the second piece of a step)
-    const uint32_t at =
-        smem_u32(ring + ((size_t)s * kBlocks + 16 * i + (lane & 15)) * kPieces * 16);
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) z[n][k] = 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      uint32_t x[4];
-      ldmatrix_x4(x[0], x[1], x[2], x[3], at + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4));
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-        mma_bf16_16816(z[n], x[0], x[1], x[2], x[3], q[n][k][0], q[n][k][1]);
-    }
-  };
-  // exponents z unit - ref of the blocks from block0 on; -inf where there is no candidate
-  auto exponents = [&](const float (&z)[kN][4], int block0, uint32_t none, float (&e)[kN][4]) {
-#pragma unroll
-    for (int n = 0; n < kN; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) e[n][k] = fmaf(z[n][k], unit, -ref[n][k & 1]);
-    if (block0 + 16 > least || none) {
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = g + (k < 2 ? 0 : 8);
-          if (block0 + r >= cand[n][k & 1] || ((none >> r) & 1u)) e[n][k] = -INFINITY;
-        }
-    }
-  };
-  look_up(0);
-  copy(0);
-  look_up(1);
-  copy(1);
-  look_up(2);
-  // ---- first pass: maximum and sum of every column
-#pragma unroll 1
-  for (int v = 0; v < tiles; ++v) {
-    cp_async_wait<1>();
-    __syncthreads();  // tile v is there; the slot of tile v + 2 is read
-    copy(v + 2);
-    look_up(v + 3);
-    const int s = v % kRing, rows = min(kBlocks, most - v * kBlocks);
-    const uint32_t none[2] = {s_none[s][0], s_none[s][1]};
-#pragma unroll 1
-    for (int i = 0; i * 16 < rows; ++i) {
-      const int block0 = v * kBlocks + 16 * i;
-      const uint32_t no = (i < 2 ? none[0] : none[1]) >> (16 * (i & 1)) & 0xffffu;
-      float z[kN][4], e[kN][4], top = -INFINITY;
-      products(s, i, z);
-      exponents(z, block0, no, e);
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top = fmaxf(top, e[n][k]);
-      if (top > 24.f) {  // (a sum of 2^24 times as much still fits)
-#pragma unroll
-        for (int n = 0; n < kN; ++n)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            // (without a reference: every candidate's exponent is +inf)
-            const float z0 = e[n][k] == -INFINITY ? -INFINITY : z[n][k] * unit;
-            const float z1 = e[n][k + 2] == -INFINITY ? -INFINITY : z[n][k + 2] * unit;
-            const float to = fmaxf(z0, z1);
-            if (to > ref[n][k] + 24.f) {
-              l[n][k] *= ex2_fast(ref[n][k] - to);
-              ref[n][k] = to;
-            }
-          }
-        exponents(z, block0, no, e);
-      }
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) l[n][k] += ex2_fast(e[n][k]) + ex2_fast(e[n][k + 2]);
-    }
-  }
-#pragma unroll
-  for (int n = 0; n < kN; ++n)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float top = ref[n][k];
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float to = top == -INFINITY ? 0.f : top;
-      float sum = l[n][k] * (ref[n][k] == -INFINITY ? 1.f : ex2_fast(ref[n][k] - to));
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      ref[n][k] = to;
-      // (a column that is none adds nothing; without a candidate no weight is looked at)
-      const int c = n * 8 + 2 * t + k;
-      l[n][k] = (c >> log) < live && (c & (pad - 1)) < G && sum != 0.f ? 1.f / sum : 0.f;
-    }
-  // ---- second pass: weights, summed over a token's heads
-#pragma unroll 1
-  for (int v = 0; v < all; ++v) {
-    const int u = tiles + v, s = u % kRing;
-    if (v < tiles) {
-      cp_async_wait<1>();
-      __syncthreads();
-      copy(u + 2);
-      look_up(u + 3);
-    }
-    uint32_t none[2] = {0u, 0u};
-    if (v < tiles) {
-      none[0] = s_none[s][0];
-      none[1] = s_none[s][1];
-    }
-    const int rows = min(kBlocks, a.NB - v * kBlocks);
-#pragma unroll 1
-    for (int i = 0; i * 16 < rows; ++i) {
-      const int block0 = v * kBlocks + 16 * i;
-      const uint32_t no = (i < 2 ? none[0] : none[1]) >> (16 * (i & 1)) & 0xffffu;
-      float z[kN][4];
-      if (block0 < most) {
-        products(s, i, z);
-        // (columns without a candidate here come to weights that nobody looks at)
-#pragma unroll
-        for (int n = 0; n < kN; ++n)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            z[n][k] = ex2_fast(fmaf(z[n][k], unit, -ref[n][k & 1])) * l[n][k & 1];
-        sum_heads<kN>(z, pad);
-      }
-      // every one a candidate, none forced, none past the rows' end
-      const bool plain = block0 >= a.sink_blocks && block0 + 16 <= min(min(least, near), a.NB) &&
-                         no == 0u;
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (kPad >= 2 && (k == 1 || (n * 8) % kPad != 0)) continue;
-          float* dst = out[n][k];
-          if (dst == nullptr) continue;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int j = block0 + g + 8 * r;
-            float x = z[n][2 * r + k];
-            if (!plain) {
-              if (j >= a.NB) continue;
-              const bool some = j < cand[n][k] && !((no >> (g + 8 * r)) & 1u);
-              x = forced(a, mine[n][k], j) ? INFINITY : some ? x : -INFINITY;
-            }
-            dst[block0 + 8 * r] = x;
-          }
-        }
-    }
-  }
-  cp_async_wait<0>();
-}
-
 template <int kD, int kN>
 int launch_decode(const GroupArgs& ga, int splits, cudaStream_t stream) {
   Launch l(dim3((unsigned)(ga.a.T * splits), ga.a.Hkv, 1), kThreads, 0, stream);
@@ -741,32 +453,17 @@ int launch_decode(const GroupArgs& ga, int splits, cudaStream_t stream) {
                                                                                  : DSA_ERR_CUDA;
 }
 
-template <int kD, int kN, int kPad>
-int launch_chunk(const GroupArgs& ga, cudaStream_t stream) {
-  constexpr size_t kSmem = (size_t)kRing * kBlocks * kD * 2;
-  static std::atomic<unsigned long long> done{0};
-  if (!allow_smem(gqa_scores_chunk_kernel<kD, kN, kPad>, kSmem, done)) return DSA_ERR_CUDA;
-  Launch l(dim3((unsigned)(ga.a.T / (ga.tokens * kWarps) + ga.a.B), ga.a.Hkv, 1), kThreads, kSmem,
-           stream);
-  return launch_kernel(&l.cfg, gqa_scores_chunk_kernel<kD, kN, kPad>, ga) == cudaSuccess ? DSA_OK
-                                                                                   : DSA_ERR_CUDA;
-}
-
 template <int kD>
 int launch_groups(const GqaScoreArgs& a, cudaStream_t stream) {
-  GroupArgs ga{a, 1, 1};
+  GroupArgs ga{a, 1};
   const int G = a.Hq / a.Hkv;
   while (ga.pad < G) ga.pad *= 2;
   const long long rows = (long long)a.T * a.Hkv;
-  const int n_tiles = ga.pad <= 16 ? 2 : 4, tokens = 8 * n_tiles / ga.pad;
   // Tokens together or a CTA (or several) for each, tables of 48 / 470 blocks, in us: 256 rows
   // (tokens x KV heads) 9.6 / 34.8 and 7.2 / 10.3, 512 rows 9.7 / 34.8 and 12.8 / 18.4, 1,024 rows
   // 9.8 / 34.8 and 22.7 / 34.5, 4,096 rows 11.9 / 45.7 and 76 / 116.
   if (rows >= 7ll * num_sms() || (rows >= 3ll * num_sms() && a.NB <= 128)) {
-    ga.tokens = tokens;
-    if (ga.pad == 8) return launch_chunk<kD, 2, 8>(ga, stream);
-    if (ga.pad == 16) return launch_chunk<kD, 2, 16>(ga, stream);
-    return n_tiles == 2 ? launch_chunk<kD, 2, 0>(ga, stream) : launch_chunk<kD, 4, 32>(ga, stream);
+    return launch_gqa_scores_chunk(a, stream);
   }
   // otherwise CTAs for a token until there is one an SM, each with 64 blocks at least
   int splits = 1;
