@@ -493,6 +493,8 @@ int dsa_gqa_read(const dsa_gqa_kv* kv, const int32_t* cu_out, const int32_t* beg
  *   q [T, Hq, D] activation dtype;  k_mean as dsa_gqa_append leaves it
  *   scores [T, Hkv, NB] fp32, NB >= 1; every entry of a token's row is written; blocks at
  *   or past NB are no candidates and not forced (DSA_DEV_POOL_RANGE)
+ * Products, maxima and sums are fp32.
+ * Device faults: also DSA_DEV_TIMEOUT (scores unspecified).
  */
 int dsa_gqa_block_scores(const void* q, const void* k_mean, const int32_t* block_table,
                          const int32_t* seq_lens, const int32_t* cu_new, int T, int B, int Hq,
@@ -517,7 +519,10 @@ int dsa_gqa_block_scores(const void* q, const void* k_mean, const int32_t* block
  *   workspace: dsa_gqa_attend_workspace_size(...) bytes, 16-byte aligned, no initial
  *   value; calls in flight at the same time must not share one
  * The lengths and lists are read on the GPU: a captured call follows them when replayed.
- * Outputs are deterministic.
+ * Outputs are deterministic.  bf16 with D 64 or 128 runs on the tensor cores: codes are
+ * exact there, a query element keeps its 8 bits down to 2^-28 of its row's largest, a
+ * weight is rounded to 11 bits and counts down to 2^-27 of its row's largest; logits,
+ * sums and outputs are fp32, and so is everything of the other types and sizes.
  * Device faults: also DSA_DEV_TIMEOUT (outputs unspecified).
  */
 int dsa_gqa_attend(const void* q, const dsa_gqa_kv* kv, const int32_t* cu_new,

@@ -459,12 +459,12 @@ int launch_groups(const GqaScoreArgs& a, cudaStream_t stream) {
   const int G = a.Hq / a.Hkv;
   while (ga.pad < G) ga.pad *= 2;
   const long long rows = (long long)a.T * a.Hkv;
-  // Tokens together or a CTA (or several) for each, tables of 48 / 470 blocks, in us: 256 rows
-  // (tokens x KV heads) 9.6 / 34.8 and 7.2 / 10.3, 512 rows 9.7 / 34.8 and 12.8 / 18.4, 1,024 rows
-  // 9.8 / 34.8 and 22.7 / 34.5, 4,096 rows 11.9 / 45.7 and 76 / 116.
-  if (rows >= 7ll * num_sms() || (rows >= 3ll * num_sms() && a.NB <= 128)) {
-    return launch_gqa_scores_chunk(a, stream);
-  }
+  // Tokens together (128 columns a CTA) or a CTA (or several) for each, tables of 48 / 470 blocks,
+  // in us, 8 query heads a KV head: 256 rows (tokens x KV heads) 7.9 / 17.7 and 7.4 / 10.4, 512
+  // rows 8.0 / 17.5 and 12.6 / 18.4, 1,024 rows 7.9 / 17.7 and 22.9 / 34.5, 4,096 rows 9.9 / 22.7
+  // and 76 / 116; 512 rows of sequences with one token each 16.7 / 38.3 and 13.6 / 19.6, with two
+  // (1,024 rows) 17.0 / 39.1 and 25.2 / 36.8.
+  if (rows >= 3ll * num_sms() && a.T >= 2ll * a.B) return launch_gqa_scores_chunk(a, stream);
   // otherwise CTAs for a token until there is one an SM, each with 64 blocks at least
   int splits = 1;
   while (splits < 8 && rows * splits < num_sms() && a.NB >= 128 * splits) splits *= 2;

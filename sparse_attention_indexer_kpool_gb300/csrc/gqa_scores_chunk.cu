@@ -14,8 +14,13 @@
 // the last to the first: the last two are still in shared memory.
 //
 // The products of step u + 1 run while step u's numbers are taken, and step u + 2's means are on
-// their way.  Two CTAs an SM.  Bound by the exponentials (two for each column and block), 36 a
-// clock and SM, and by the means' way from L2.
+// their way; two CTAs an SM.  2,048 tokens of 64 query heads on 16,384 keys (256 blocks): 44 us
+// (mma.sync products of 16 x 8, which read each mean again for every 16 columns: 86 us).  The
+// bytes of the scores and the queries take 6 us, the exponentials (two for each column and block,
+// 36 a clock and SM) 6 us: what is left is the instructions around them, by 16 warps an SM, and
+// the start of each CTA.  Without the numbers it is 33 us, without the exponentials alone 43.
+// Not faster: CTAs that stay and take one group of tokens after the other (52 us), a warp for the
+// products alone (52), 16 warps a CTA (70).
 #include "gqa.cuh"
 #include "mla_chunk.cuh"
 #include "umma.cuh"
@@ -92,8 +97,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (j0 < 0 || j0 >= n_new) return;
   const int live = min(kPer, n_new - j0);
   const long long base = (long long)a.seq_lens[b] - n_new + j0, end = base + live;
-  auto whole_at = [&](long long pos) {
-    return pos < 0 ? 0 : (int)min((long long)min(a.NB, a.max_pages), (pos + 1) / a.page_size);
+  const unsigned limit = min(a.NB, a.max_pages), ps = a.page_size;
+  auto whole_at = [&](long long pos) {  // (positions are below 2^31)
+    return pos < 0 ? 0 : (int)min(limit, ((unsigned)pos + 1u) / ps);
   };
   const int most = whole_at(end - 1);  // candidates of the last token; of the first:
   const int least = whole_at(base);
@@ -102,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int i = tid; i < kPer; i += kThreads) {
     const long long pos = base + i;
     c.cand[i] = i < live ? whole_at(pos) : 0;
-    c.mine[i] = i < live && pos >= 0 ? (int)(pos / a.page_size) : -1;
+    c.mine[i] = i < live && pos >= 0 ? (int)((unsigned)pos / ps) : -1;
   }
   if (h == 0 && tid == 0) {
     if (base < 0) flag(a.status, DSA_DEV_BAD_LENGTH);
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int k0 = 0; k0 < 64; k0 += 32) {
         const int col = half * 64 + k0;
         if (col / kPad >= live) break;
-        float z[32], s[kPad == 1 ? 32 : 32 / kPad];
+        float z[32], s[32 / kPad];
         tmem_ld32(ts + (u & 1) * 128 + k0, z);
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
@@ -313,16 +319,22 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
         }
+        constexpr int kTok = 32 / kPad;
+        float* to = out + (col / kPad) * next + j;
+        if (plain && col / kPad + kTok <= live) {
 #pragma unroll
-        for (int i = 0; i < (kPad == 1 ? 32 : 32 / kPad); ++i) {
-          const int tok = col / kPad + i;
-          if (tok >= live) break;
-          float x = s[i];
-          if (!plain) {
-            if (j >= a.NB) continue;
-            x = forced(a, c.mine[tok], j) ? INFINITY : j < c.cand[tok] && !gone ? x : -INFINITY;
+          for (int i = 0; i < kTok; ++i) to[i * next] = s[i];
+        } else if (j < a.NB) {
+#pragma unroll 1
+          for (int i = 0; i < kTok; ++i) {
+            const int tok = col / kPad + i;
+            if (tok >= live) break;
+            float x = s[0];
+#pragma unroll
+            for (int k = 1; k < kTok; ++k) x = k == i ? s[k] : x;
+            to[i * next] =
+                forced(a, c.mine[tok], j) ? INFINITY : j < c.cand[tok] && !gone ? x : -INFINITY;
           }
-          out[tok * next + j] = x;
         }
       }
     }
@@ -338,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
   }
   // blocks that no token has as a candidate
-  for (int i = 0; i < live; ++i)
-    for (int j = n * kBlocks + tid; j < a.NB; j += kThreads)
+  for (int j = n * kBlocks + tid; j < a.NB; j += kThreads)
+    for (int i = 0; i < live; ++i)
       out[i * next + j] = forced(a, c.mine[i], j) ? INFINITY : -INFINITY;
 }
 

@@ -815,3 +815,102 @@ def test_refused_tensors():
     with pytest.raises(ops.DsaError):
         ops.dsa_gqa_attend(q[:, :3].contiguous(), kp, vp, ks, vs, table, lens, cu, 0, 0, 0.1,
                            out[:, :3].contiguous(), lse[:, :3].contiguous(), ws)
+
+
+@pytest.mark.parametrize("lens,new,Hkv,G,ps,D,sinks,local", [
+    ([5000, 3, 0, 2300], [200, 3, 0, 60], 2, 8, 16, 128, 1, 2),
+    ([4200], [460], 1, 1, 16, 128, 0, 0), ([2500, 900], [300, 160], 1, 2, 16, 64, 2, 1),
+    ([700, 700], [100, 60], 3, 4, 16, 64, 0, 1),
+    ([1900, 40], [230, 1], 2, 5, 16, 128, 1, 0), ([3000], [120], 4, 16, 16, 128, 1, 4),
+    ([900], [900], 1, 32, 64, 128, 0, 2), ([2060], [250], 2, 20, 16, 64, 3, 200),
+    ([460], [460], 1, 8, 256, 64, 1, 1)])
+def test_scores_of_chunks(lens, new, Hkv, G, ps, D, sinks, local):
+    check_scores(Case(ps + G, lens, new, Hkv, ps, D), G, BF, sinks, local)
+
+
+def test_scores_of_chunks_narrow_and_faults():
+    c = Case(9, [2300, 700], [200, 30], 2, 16, 64)
+    check_scores(c, 8, BF, 1, 1, NB=133, fault=ops.DEV_POOL_RANGE)
+    check_scores(c, 8, BF, 1, 1, NB=400)
+    check_scores(c, 8, BF, 0, 2, std=60.0)
+    c.table[0][3], c.table[0][130], c.table[1][2] = -9, 10 ** 6, c.n_pages
+    check_scores(c, 8, BF, 0, 1, fault=ops.DEV_BAD_PAGE)
+    c = Case(10, [2300, 700], [200, 30], 2, 16, 64, width=5)
+    check_scores(c, 8, BF, 1, 1, NB=9, fault=ops.DEV_BAD_PAGE | ops.DEV_POOL_RANGE)
+
+
+def test_scores_of_chunks_nan():
+    """A query with a NaN reaches its token's scores of its KV head, a NaN mean the rows that have
+    its block as a candidate."""
+    c = Case(11, [2300, 700], [200, 30], 2, 16, 128)
+    q, means = c.normal(230, 8, 128, std=2.0), c.normal(c.n_pages, 2, 128, std=0.5)
+
+    def scores(q, means):
+        out = torch.empty((230, 2, len(c.table[0])), device=DEV)
+        ops.dsa_gqa_block_scores(q.to(DEV), means.to(DEV), i32(c.table), i32(c.lens), 16,
+                                 i32(c.cu), 1, 1, 0.1, out)
+        return out.cpu()
+    plain = scores(q, means)
+    q[77, 6, 100] = math.nan
+    means[c.table[1][43], 0, 5] = math.nan             # complete with the last 13 tokens or so
+    got = scores(q, means)
+    row = torch.isnan(got)
+    cand = torch.isfinite(plain)
+    want = torch.zeros_like(row)
+    want[77, 1] = cand[77, 1]
+    for t in range(200, 230):
+        if 700 - 230 + t + 1 >= 44 * 16:
+            want[t, 0] = cand[t, 0]
+    assert torch.equal(row, want)
+    assert torch.equal(got[~row], plain[~row])
+
+
+def test_chunks_with_a_negative_scale():
+    """sm_scale < 0 is the negated query's, bit for bit."""
+    c = Case(12, [900, 300], [200, 60], 2, 16, 128)
+    q = c.normal(c.T, 16, 128)
+    one, two = run_attend(c, q, -0.2), run_attend(c, -q, 0.2)
+    assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+    means = c.normal(c.n_pages, 2, 128, std=0.5).to(DEV)
+    out = [torch.empty((c.T, 2, len(c.table[0])), device=DEV) for _ in range(2)]
+    for x, sm, o in ((q, -0.2, out[0]), (-q, 0.2, out[1])):
+        ops.dsa_gqa_block_scores(x.to(DEV), means, i32(c.table), i32(c.lens), 16, i32(c.cu), 1, 1,
+                                 sm, o)
+    assert torch.equal(*out)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_chunks_small_and_zero_queries(D):
+    c = Case(13, [700, 400], [150, 33], 2, 16, D)
+    q = c.normal(c.T + 1, 10, D, std=2.0)
+    q[3], q[40, 2], q[160, 9, 1:] = 0.0, q[40, 2] * 2.0 ** -90, 0.0
+    q[41, 1, ::3] *= 2.0 ** -30
+    check_dense(c, 5, q=q)
+    check_dense(c, 5, 90, 20, q=q)
+
+
+@pytest.mark.parametrize("tokens", [200, 1])
+def test_kernels_give_up_and_recover(tokens):
+    """A wait that runs out ends the call with a flagged status; the context stays usable, and the
+    same call made afterwards gives what it gave before."""
+    c = Case(14, [2300, 700], [tokens, 30], 2, 16, 128)
+    q, means = c.normal(c.T, 16, 128), c.normal(c.n_pages, 2, 128, std=0.5).to(DEV)
+
+    def both():
+        st = i32([0])
+        scores = torch.zeros((c.T, 2, len(c.table[0])), device=DEV)
+        ops.dsa_gqa_block_scores(q.to(DEV), means, i32(c.table), i32(c.lens), 16, i32(c.cu), 1, 1,
+                                 0.1, scores, status=st)
+        out, lse, bits = run_attend(c, q, 0.1)
+        return scores.cpu(), out, lse, bits, st.item()
+    first = both()
+    assert first[3:] == (0, 0)
+    ops.dsa_set_failure_drill(ops.DSA_DRILL_SKIP_ARM)
+    try:
+        _, _, _, bits, st = both()
+    finally:
+        ops.dsa_set_failure_drill(0)
+    if tokens > 1:  # (a decode step's kernels wait for loads alone, which no drill withholds)
+        assert bits == st == ops.DEV_TIMEOUT
+    again = both()
+    assert again[3:] == (0, 0) and all(torch.equal(a, b) for a, b in zip(first[:3], again[:3]))
