@@ -19,8 +19,9 @@
 // the slots from floor(cu / page_size) + 2 b on are its own: a CTA finds its sequence among
 // them with one or two rounds of loads by all its threads (a binary search's dependent loads
 // were half of a decode step's 7.9 us).
-// What bounds it: memory in a chunk, round trips to memory (cu_new, the lengths, the table,
-// then rows and scale) in a decode step.
+// What bounds it: memory in a chunk (65,000 tokens of 8 heads of 128 in bf16 72 us, 5.5 TB/s),
+// round trips to memory (cu_new, the lengths, the table, then rows and scale) in a decode step
+// (64 tokens 6.2 us, 8.1 with cold caches).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -139,13 +140,40 @@ __device__ __forceinline__ bool page_ok(int page, const GqaKv& kv, int32_t* stat
   return ok;
 }
 
+// 32 bytes: at once where the tensor begins on a multiple of them (its rows are multiples).  Two
+// accesses of 16, each with gaps between the lanes, took a read of 59,400 rows from 58 to 66 us.
+__device__ __forceinline__ bool is_wide(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 31) == 0;
+}
+__device__ __forceinline__ void load32(uint4 (&v)[2], const void* p, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x),
+                   "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+                 : "l"(p));
+  } else {
+    v[0] = ld_stream_v4(p);
+    v[1] = ld_stream_v4(static_cast<const uint4*>(p) + 1);
+  }
+}
+__device__ __forceinline__ void store32(void* p, const uint4 (&v)[2], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0].x),
+                 "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z),
+                 "r"(v[1].w)
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = v[0];
+    static_cast<uint4*>(p)[1] = v[1];
+  }
+}
+
 // Sixteen elements as they lie in memory.
 template <typename T> struct Raw16;
 template <> struct Raw16<__nv_bfloat16> {
   uint4 v[2];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    v[0] = ld_stream_v4(p);
-    v[1] = ld_stream_v4(p + 8);
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool wide) {
+    load32(v, p, wide);
   }
   __device__ __forceinline__ void clear() { v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void half(int i, float (&x)[8]) const {
@@ -170,9 +198,14 @@ template <> struct Raw16<__nv_bfloat16> {
 };
 template <> struct Raw16<float> {
   uint4 v[4];
-  __device__ __forceinline__ void load(const float* p) {
+  __device__ __forceinline__ void load(const float* p, bool wide) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ld_stream_v4(p + 4 * i);
+    for (int i = 0; i < 2; ++i) {
+      uint4 w[2];
+      load32(w, p + 8 * i, wide);
+      v[2 * i] = w[0];
+      v[2 * i + 1] = w[1];
+    }
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -219,12 +252,13 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2)
   const int r0 = tid / kRowPieces, c = (tid & (kRowPieces - 1)) * 16;
   const bool mean = kind == 0 && k_mean != nullptr && p.hi == ps;
 
+  const bool wide = is_wide(kind ? v_new : k_new);
   Raw16<T> x[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
     const int r = r0 + i * kStep;
     if (r >= p.lo && r < p.hi)
-      x[i].load(src + (r - p.lo) * pitch + c);
+      x[i].load(src + (r - p.lo) * pitch + c, wide);
     else
       x[i].clear();
   }
@@ -260,13 +294,14 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2)
   if (tid == 0) *scale = pow2(e);
   const bool moves = e > e0 && p.lo > 0;
   const float up = pow2(-e), down = pow2(max(e0 - e, -126));  // (2^-126: all zero by then)
+  uint2 first[kMine];  // codes of the pieces' first halves
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {  // half a piece at a time
+  for (int j = 0; j < 2; ++j) {  // half a piece at a time, written together
     float sum[8] = {};
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int r = r0 + i * kStep;
-      uint2* dst = reinterpret_cast<uint2*>(codes + (long long)r * kD + c) + j;
+      uint2* dst = reinterpret_cast<uint2*>(codes + (long long)r * kD + c);
       float f[8];
       uint2 y;
       if (r >= p.hi) continue;
@@ -279,18 +314,20 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2)
           for (int u = 0; u < 8; ++u) f[u] = fabsf(f[u]) < INFINITY ? f[u] : NAN;
         }
         y = pack8(f);
-        *dst = y;
       } else {  // a row before the new ones
         if (!moves && !mean) continue;
-        y = *dst;
+        y = dst[j];
         if (moves) {
           unpack8(y, f);
 #pragma unroll
           for (int u = 0; u < 8; ++u) f[u] *= down;
           y = pack8(f);
-          *dst = y;
         }
       }
+      if (j == 0)
+        first[i] = y;
+      else if (r >= p.lo || moves)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(first[i].x, first[i].y, y.x, y.y);
       if (mean) {
         unpack8(y, f);
 #pragma unroll
@@ -432,28 +469,38 @@ __global__ void __launch_bounds__(2 * kThreads)
 }
 
 // ---- Read-back ----------------------------------------------------------------
-// value = code * scale.  A CTA takes 32 rows of the outputs, finds their sequences and
+// value = code * scale.  A CTA takes 16 rows of the outputs, finds their sequences and
 // pages once, and walks over their (KV head, 16 codes) pieces: 16 bytes in, 32 or 64 out a
-// thread and step.
-constexpr int kReadRows = 32, kReadThreads = 256;
+// thread and step, two steps' loads at once.  59,400 rows of 8 heads of 128 in bf16: 57.7 us,
+// 6.3 TB/s (one step at a time 65, with 16-byte stores 66; 32 and 64 rows 58 and 59.5); 1,001
+// rows of 4 heads 3.4 us (with 64 rows a CTA 5.4).
+constexpr int kReadRows = 16, kReadThreads = 256;
 
+// wide: 32 bytes at once (p is a multiple of them)
 template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&x)[16]);
+__device__ __forceinline__ void store16(T* p, const float (&x)[16], bool wide);
 template <>
-__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* p, const float (&x)[16]) {
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-  uint4* o = reinterpret_cast<uint4*>(p);
-  o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* p, const float (&x)[16],
+                                                       bool wide) {
+  uint4 w[2];
+  w[0] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                    pack_bf16(x[6], x[7]));
+  w[1] = make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]),
+                    pack_bf16(x[14], x[15]));
+  store32(p, w, wide);
 }
 template <>
-__device__ __forceinline__ void store16<float>(float* p, const float (&x)[16]) {
-  float4* o = reinterpret_cast<float4*>(p);
+__device__ __forceinline__ void store16<float>(float* p, const float (&x)[16], bool wide) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  for (int i = 0; i < 2; ++i) {
+    uint4 w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      w[k] = make_uint4(__float_as_uint(x[8 * i + 4 * k]), __float_as_uint(x[8 * i + 4 * k + 1]),
+                        __float_as_uint(x[8 * i + 4 * k + 2]),
+                        __float_as_uint(x[8 * i + 4 * k + 3]));
+    store32(p + 8 * i, w, wide);
+  }
 }
 
 template <typename T>
@@ -499,29 +546,57 @@ __global__ void __launch_bounds__(kReadThreads)
   const uint8_t* pages = blockIdx.y == 0 ? kv.k_pages : kv.v_pages;
   const float* scales = blockIdx.y == 0 ? kv.k_scale : kv.v_scale;
   T* out = blockIdx.y == 0 ? k_out : v_out;
-  for (int j = tid; j < rows * row; j += kReadThreads) {
-    const int r = j / row, rest = j - r * row, h = rest / per, d = (rest - h * per) * 16;
-    const int page = s_page[r];
-    if (page == -2) continue;
-    float x[16];
-    if (page < 0) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    } else {
-      const long long unit = (long long)page * kv.Hkv + h;
-      const uint4 v = ld_stream_v4(pages + (unit * kv.page_size + s_off[r]) * kv.D + d);
-      const float s = __ldg(scales + unit);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 a = codes2(w[i] & 0xffffu), c = codes2(w[i] >> 16);
-        x[4 * i] = a.x * s;
-        x[4 * i + 1] = a.y * s;
-        x[4 * i + 2] = c.x * s;
-        x[4 * i + 3] = c.y * s;
-      }
+  const bool wide = is_wide(out);
+  // piece `rest` of row r, and how far the thread's next one is; its head by a product (exact:
+  // rest < 2^11, per <= 2^4)
+  const unsigned inv = 65536u / per + 1;
+  const int more_r = kReadThreads / row, more = kReadThreads - more_r * row;
+  int r = tid / row, rest = tid - r * row;
+  auto ahead = [&](int& r, int& rest) {
+    r += more_r;
+    rest += more;
+    if (rest >= row) {
+      rest -= row;
+      ++r;
     }
-    store16<T>(out + ((long long)(t_first + r) * kv.Hkv + h) * kv.D + d, x);
+  };
+  constexpr int kAhead = 2;  // pieces on their way
+#pragma unroll 1
+  while (r < rows) {
+    uint4 v[kAhead];
+    float s[kAhead];
+    int r1 = r, rest1 = rest;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);  // (no page: zeros)
+      s[i] = 0.f;
+      const int page = r1 < rows ? s_page[r1] : -2;
+      if (page >= 0) {
+        const int h = (int)((unsigned)rest1 * inv >> 16);
+        const long long unit = (long long)page * kv.Hkv + h;
+        v[i] = ld_stream_v4(pages + (unit * kv.page_size + s_off[r1]) * kv.D +
+                            (rest1 - h * per) * 16);
+        s[i] = __ldg(scales + unit);
+      }
+      ahead(r1, rest1);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (r < rows && s_page[r] != -2) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        float x[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 a = codes2(w[k] & 0xffffu), c = codes2(w[k] >> 16);
+          x[4 * k] = a.x * s[i];
+          x[4 * k + 1] = a.y * s[i];
+          x[4 * k + 2] = c.x * s[i];
+          x[4 * k + 3] = c.y * s[i];
+        }
+        store16<T>(out + ((long long)(t_first + r) * row + rest) * 16, x, wide);
+      }
+      ahead(r, rest);
+    }
   }
 }
 

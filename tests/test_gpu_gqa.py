@@ -914,3 +914,29 @@ def test_kernels_give_up_and_recover(tokens):
         assert bits == st == ops.DEV_TIMEOUT
     again = both()
     assert again[3:] == (0, 0) and all(torch.equal(a, b) for a, b in zip(first[:3], again[:3]))
+
+
+def offset(x, n):
+    """A copy of x that begins n bytes behind a multiple of 256."""
+    buf = torch.empty(x.numel() * x.element_size() + 256, dtype=torch.uint8, device=DEV)
+    y = buf[n:n + x.numel() * x.element_size()].view(x.dtype).view(x.shape)
+    y.copy_(x)
+    assert y.data_ptr() % 256 == n
+    return y
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,ps,new", [(128, 64, 200), (64, 16, 3), (80, 32, 70)])
+def test_tensors_on_16_bytes(D, ps, new, dtype):
+    """Activations that begin on an odd multiple of 16 bytes, each by itself: the same bits."""
+    c = Case(15, [new + 90, new + 5], [new, new], 2, ps, D)
+    k, v = (c.normal(c.T, 2, D, dtype=dtype).to(DEV) for _ in "kv")
+    want = None
+    for at in ((0, 0), (16, 0), (0, 16), (48, 80)):
+        kp, vp, ks, vs, table, lens, cu = c.put()
+        ops.dsa_gqa_append(offset(k, at[0]), offset(v, at[1]), kp, vp, ks, vs, table, lens, cu)
+        out = [offset(torch.zeros((sum(c.lens), 2, D), dtype=dtype, device=DEV), n) for n in at]
+        ops.dsa_gqa_read(kp, vp, ks, vs, table, lens, i32([0, c.lens[0], sum(c.lens)]), *out)
+        got = [x.clone() for x in (kp.view(torch.uint8), vp.view(torch.uint8), *out)]
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
