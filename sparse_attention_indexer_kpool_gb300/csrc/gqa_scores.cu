@@ -6,7 +6,8 @@
 //
 // Here: a kernel on the tensor cores for few tokens (bf16 queries, head dim 64 or 128, groups of
 // up to 32 heads), and a generic one (any geometry and type), a CTA a token and KV head, a warp a
-// block.  That for chunks is gqa_scores_chunk.cu.
+// block (21 tokens on up to 230 keys, fp32, 9.7 us: latency).  That for chunks is
+// gqa_scores_chunk.cu.
 #include <cooperative_groups.h>
 
 #include "gqa.cuh"
@@ -137,7 +138,9 @@ __global__ void __launch_bounds__(kThreads) gqa_scores_kernel(GqaScoreArgs a) {
 // then has two columns' z of its rows: it keeps their maximum and sum alone, and only at
 // the end of the first pass do lanes (and warps, and CTAs) exchange them.
 // Here (decode) the warps of a cluster's CTAs share the blocks of one token, so that many SMs
-// read one long context's means.  Bound by round trips to the table and the means.
+// read one long context's means.  Bound by round trips to the table and the means: four tokens on
+// 262,144 keys (8 KV heads of 8 query heads of 128) 10.3 us, 15 with cold caches, where the
+// means' 34 MB take 5.
 constexpr int kPadG = 32;            // heads of a group, at most
 struct GroupArgs {
   GqaScoreArgs a;

@@ -29,6 +29,11 @@
 // Where a step has few row tiles of few keys, a cluster of CTAs takes each (kCluster): its warps
 // share the tiles evenly, and the partials meet in (distributed) shared memory, so that no
 // second kernel follows.
+// Measured (head dim 128, join included): 64 tokens on 4,096 to 16,000 keys, 8 KV heads of 8 query
+// heads, 212 us: 6.2 TB/s, memory-bound (the join is 8 of them).  1,024 tokens on 32 blocks of
+// 64 each, 4 KV heads of 16 query heads, 318 us: 2.1 GB of codes out of L2 at 6.7 TB/s, two warps
+// a scheduler, so that an instruction's latency shows.  One token on 256 keys,
+// 8 x 8 heads, 10.4 us: start, lengths, table, scales, one or two tiles, the cluster's exchange.
 #include <cooperative_groups.h>
 
 #include "gqa.cuh"
@@ -992,6 +997,8 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream, bool together
   return launch_join<kD>(j, Rows<kN>{a.Hq, a.kv.Hkv, p.G, p.hb}, row_tiles, stream);
 }
 
+// Boxes of 32 keys, or of 16 where the page is no multiple of 32: 64 decode tokens on 4,096 to
+// 16,000 keys 212.5 / 214.5 us, 1,024 tokens on 32 blocks 319 / 344.
 template <int kD, int kN>
 int launch_r(const GqaArgs& a, void* workspace, cudaStream_t stream, bool together) {
   return a.kv.page_size % 32 == 0 ? launch<kD, kN, 32>(a, workspace, stream, together)
