@@ -491,7 +491,7 @@ int dsa_gqa_read(const dsa_gqa_kv* kv, const int32_t* cu_out, const int32_t* beg
  * glm5next_dsa::tp, "Why the indexer is REPLICATED") are a sum over heads as well.
  *
  *   q [T, Hq, D] activation dtype;  k_mean as dsa_gqa_append leaves it
- *   scores [T, Hkv, NB] fp32, NB >= 1; every entry of a token's row is written; blocks at
+ *   scores [T, Hkv, NB] fp32, 1 <= NB <= 2^27; every entry of a token's row is written; blocks at
  *   or past NB are no candidates and not forced (DSA_DEV_POOL_RANGE)
  * Products, maxima and sums are fp32.
  * Device faults: also DSA_DEV_TIMEOUT (scores unspecified).

@@ -592,6 +592,7 @@ int dsa_gqa_block_scores(const void* q, const void* k_mean, const int32_t* block
   if (r != DSA_OK) return r;
   if (sink_blocks < 0 || local_blocks < 0 || NB < 1 || !isfinite(sm_scale))
     return DSA_ERR_INVALID_ARG;
+  if (NB > 1 << 27) return DSA_ERR_UNSUPPORTED;  // (of 16 tokens each: 2^31 positions)
   if (T == 0 || B == 0) return DSA_OK;
   if (!q || !k_mean || !block_table || !seq_lens || !cu_new || !scores) return DSA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_mean, 16) || !aligned(block_table, 4) ||

@@ -428,7 +428,7 @@ int launch_gqa_attend(const GqaArgs& a, void* workspace, cudaStream_t stream);
 bool gqa_split_ok(int D, int dtype);
 size_t gqa_split_workspace_size(int Hq, int Hkv, int D);
 // together: only where a cluster of CTAs takes a row tile in few rounds; kElsewhere if not
-constexpr int kElsewhere = 1;
+constexpr int kElsewhere = -1;  // (no DSA_ERR_* code)
 int launch_gqa_split(const GqaArgs& a, void* workspace, cudaStream_t stream, bool together = false);
 // its tcgen05 form for chunks of new tokens (no block lists), the same types
 size_t gqa_chunk_workspace_size(int D);

@@ -940,3 +940,57 @@ def test_tensors_on_16_bytes(D, ps, new, dtype):
         got = [x.clone() for x in (kp.view(torch.uint8), vp.view(torch.uint8), *out)]
         want = want or got
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("lens,new", [([700, 300], [150, 60]), ([700, 300], [1, 2])])
+def test_a_scale_of_zero_weighs_all_alike(lens, new):
+    c = Case(16, lens, new, 2, 16, 128)
+    for window, sinks in ((0, 0), (90, 20)):
+        check_dense(c, 8, window, sinks, sm=0.0)
+    means = c.normal(c.n_pages, 2, 128).to(DEV)
+    out = torch.empty((c.T, 2, len(c.table[0])), device=DEV)
+    ops.dsa_gqa_block_scores(c.normal(c.T, 16, 128).to(DEV), means, i32(c.table), i32(c.lens), 16,
+                             i32(c.cu), 0, 1, 0.0, out)
+    got = out.cpu()
+    for b, t in ((0, c.cu[1] - 1), (1, c.T - 1)):
+        n = c.lens[b] // 16 - (c.lens[b] % 16 == 0)     # the own block is forced
+        want = torch.full((2, n), 8.0 / (c.lens[b] // 16))
+        assert torch.allclose(got[t, :, :n], want, rtol=2.0 ** -20, atol=0.0)
+
+
+def test_chunks_in_a_graph_with_other_lengths():
+    """Chunk kernels captured once: replays follow lengths and step boundaries that changed, and a
+    step that shrank to decode tokens."""
+    c = Case(17, [2300, 900], [200, 100], 2, 16, 128)
+    kp, vp, ks, vs, table, lens, cu = c.put()
+    q = c.normal(300, 16, 128).to(DEV)
+    means = c.normal(c.n_pages, 2, 128).to(DEV)
+    out, lse = torch.zeros((300, 16, 128), dtype=BF, device=DEV), torch.zeros((300, 16), device=DEV)
+    scores = torch.zeros((300, 2, len(c.table[0])), device=DEV)
+    ws = torch.empty(ops.gqa_attend_workspace_bytes(q, kp), dtype=torch.uint8, device=DEV)
+
+    def step():
+        ops.dsa_gqa_block_scores(q, means, table, lens, 16, cu, 1, 1, 0.1, scores)
+        ops.dsa_gqa_attend(q, kp, vp, ks, vs, table, lens, cu, 0, 0, 0.1, out, lse, ws)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n, edges in (([2300, 900], [0, 200, 300]), ([2299, 33], [0, 200, 210]),
+                     ([400, 900], [0, 1, 2]), ([2300, 0], [0, 300, 300]), ([17, 900], [0, 0, 300])):
+        lens.copy_(i32(n))
+        cu.copy_(i32(edges))
+        for x in (out, lse, scores):
+            x.fill_(3.0)
+        graph.replay()
+        got = [x.clone() for x in (out, lse, scores)]
+        for x in (out, lse, scores):
+            x.fill_(3.0)
+        step()
+        assert all(torch.equal(a, b) for a, b in zip(got, (out, lse, scores)))
+        assert bool((out[edges[-1]:] == 3.0).all()) and bool((scores[edges[-1]:] == 3.0).all())
+        d = Case.__new__(Case)
+        d.__dict__.update(c.__dict__, lens=n, cu=edges, T=edges[-1],
+                          new=[b - a for a, b in zip(edges, edges[1:])])
+        compare(d, q.cpu(), 0.1, out.cpu(), lse.cpu(), BF, dense=True)

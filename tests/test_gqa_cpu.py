@@ -167,3 +167,8 @@ def test_scores_and_attention_by_hand():
     out, lse, *_ = ref.attend(q, kp, one, kp, one, [[0, 1]], [2], [0, 1], 1.0,
                                 ids=torch.tensor([[[-1, 1, -1]]]))
     assert out.abs().max() == 0 and bool((lse == -math.inf).all())
+
+
+def test_scores_of_more_blocks_than_positions_have(lib):
+    assert scores(lib, NB=(1 << 27) + 1) == ERR["DSA_ERR_UNSUPPORTED"]
+    assert scores(lib, NB=1 << 27, T=0) == 0
