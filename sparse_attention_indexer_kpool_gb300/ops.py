@@ -344,17 +344,19 @@ def _gqa_wrong(dev, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, c
 
 
 def _gqa_shapes(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu):
-    """(n_pages, Hkv, D, B) of a grouped-query cache whose tensors' shapes agree."""
+    """(n_pages, Hkv, page_size, D, B, max_pages) of a grouped-query cache whose tensors' shapes
+    agree."""
     shape = k_pages.shape
     if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page_size, D]")
-    n_pages, Hkv, _, D = shape
-    if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0]:
+    n_pages, Hkv, page_size, D = shape
+    table, B = block_table.shape, seq_lens.numel()
+    if len(table) != 2 or B != table[0]:
         raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
-    B, n = seq_lens.numel(), n_pages * Hkv
+    n = n_pages * Hkv
     if (k_scale.numel(), v_scale.numel(), cu.numel()) != (n, n, B + 1):
         _sizes((k_scale, n, "k_scale"), (v_scale, n, "v_scale"), (cu, B + 1, "cu_new"))
-    return n_pages, Hkv, D, B
+    return n_pages, Hkv, page_size, D, B, table[1]
 
 
 def dsa_gqa_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_new,
@@ -363,8 +365,8 @@ def dsa_gqa_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table
     ``k_pages``, ``v_pages`` [n_pages, Hkv, page_size, D] (float8_e4m3fn or uint8 codes) with
     ``k_scale``, ``v_scale`` [n_pages, Hkv] fp32; ``k_mean`` [n_pages, Hkv, D] bf16 gets the mean
     key of every block that becomes complete.  ``seq_lens`` counts the new tokens."""
-    n_pages, Hkv, D, B = _gqa_shapes(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
-                                     cu_new)
+    n_pages, Hkv, page_size, D, B, width = _gqa_shapes(k_pages, v_pages, k_scale, v_scale,
+                                                       block_table, seq_lens, cu_new)
     shape, act = k_new.shape, k_new.dtype
     if len(shape) != 3 or shape[1] != Hkv or shape[2] != D or v_new.shape != shape:
         raise ValueError("k_new and v_new must be [T, Hkv, D]")
@@ -384,8 +386,7 @@ def dsa_gqa_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table
     if p is None or codes not in _CODES:
         _gqa_wrong(dev, *tensors[:7], (k_new, act, "k_new"), (v_new, act, "v_new"),
                    (k_mean, torch.bfloat16, "k_mean"), (status, _I32, "status"))
-    kv = _lib.GqaKv(p[0], p[1], p[2], p[3], p[4], p[5], n_pages, k_pages.shape[2],
-                    block_table.shape[1], Hkv, D)
+    kv = _lib.GqaKv(p[0], p[1], p[2], p[3], p[4], p[5], n_pages, page_size, width, Hkv, D)
     code = _lib.load().dsa_gqa_append(
         p[7], p[8], p[6], shape[0], B, _dtype_tag(k_new), ctypes.byref(kv),
         None if k_mean is None else p[9], None if status is None else p[-1], st)
@@ -397,26 +398,28 @@ def dsa_gqa_read(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_o
                  begin=None, status=None, stream=None):
     """Bring rows of the cache back: ``k_out``, ``v_out`` [T, Hkv, D] rows ``cu_out[b]`` .. get
     positions ``begin[b]`` .. (``begin`` [B] or None: 0) of sequence b."""
-    n_pages, Hkv, D, B = _gqa_shapes(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
-                                     cu_out)
+    n_pages, Hkv, page_size, D, B, width = _gqa_shapes(k_pages, v_pages, k_scale, v_scale,
+                                                       block_table, seq_lens, cu_out)
     shape, act = k_out.shape, k_out.dtype
     if len(shape) != 3 or shape[1] != Hkv or shape[2] != D or v_out.shape != shape:
         raise ValueError("k_out and v_out must be [T, Hkv, D]")
-    _sizes((begin, B, "begin"))
+    if begin is not None and begin.numel() != B:
+        _sizes((begin, B, "begin"))
     dev, st = _gqa_device(k_pages, stream)
     codes = k_pages.dtype
     tensors = [k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, cu_out, k_out, v_out]
     dtypes = [codes, codes, _F32, _F32, _I32, _I32, _I32, act, act]
-    for t in (begin, status):
-        if t is not None:
-            tensors.append(t)
-            dtypes.append(_I32)
+    if begin is not None:
+        tensors.append(begin)
+        dtypes.append(_I32)
+    if status is not None:
+        tensors.append(status)
+        dtypes.append(_I32)
     p = _pointers(dev, tensors, dtypes)
     if p is None or codes not in _CODES:
         _gqa_wrong(dev, *tensors[:7], (k_out, act, "k_out"), (v_out, act, "v_out"),
                    (begin, _I32, "begin"), (status, _I32, "status"))
-    kv = _lib.GqaKv(p[0], p[1], p[2], p[3], p[4], p[5], n_pages, k_pages.shape[2],
-                    block_table.shape[1], Hkv, D)
+    kv = _lib.GqaKv(p[0], p[1], p[2], p[3], p[4], p[5], n_pages, page_size, width, Hkv, D)
     code = _lib.load().dsa_gqa_read(
         ctypes.byref(kv), p[6], None if begin is None else p[9], shape[0], B, _dtype_tag(k_out),
         p[7], p[8], None if status is None else p[-1], st)
@@ -475,8 +478,8 @@ def dsa_gqa_attend(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
     for ``dsa_gqa_append``): over all before them (``window`` 0), a sliding window and the first
     ``sinks`` tokens, or the blocks that ``block_ids`` [T, Hkv, K] lists for each token and KV
     head (negative: none)."""
-    n_pages, Hkv, D, B = _gqa_shapes(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
-                                     cu_new)
+    n_pages, Hkv, page_size, D, B, width = _gqa_shapes(k_pages, v_pages, k_scale, v_scale,
+                                                       block_table, seq_lens, cu_new)
     shape, act = q.shape, q.dtype
     if len(shape) != 3 or shape[2] != D:
         raise ValueError("q must be [T, Hq, D]")
@@ -510,8 +513,7 @@ def dsa_gqa_attend(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
         _gqa_wrong(dev, *tensors[:7], (q, act, "q"), (out, act, "out"),
                    (workspace, torch.uint8, "workspace"), (lse, _F32, "lse"),
                    (block_ids, _I32, "block_ids"), (status, _I32, "status"))
-    kv = _lib.GqaKv(p[0], p[1], p[2], p[3], p[4], p[5], n_pages, k_pages.shape[2],
-                    block_table.shape[1], Hkv, D)
+    kv = _lib.GqaKv(p[0], p[1], p[2], p[3], p[4], p[5], n_pages, page_size, width, Hkv, D)
     at = 9
     ws = ls = ids = None
     ws_bytes = 0
