@@ -514,7 +514,8 @@ int dsa_gqa_block_scores(const void* q, const void* k_mean, const int32_t* block
  * Nothing seen gives out = 0 and lse = -inf.  What a token does not see does not reach
  * its output, whatever the cache holds there.
  *
- *   q [T, Hq, D] activation dtype; block_ids [T, Hkv, K] int32 or NULL (K = 0)
+ *   q [T, Hq, D] activation dtype; block_ids [T, Hkv, K] int32 or NULL (K = 0), K *
+ *   page_size <= 2^30
  *   out [T, Hq, D] activation dtype; lse [T, Hq] fp32 (may be NULL)
  *   workspace: dsa_gqa_attend_workspace_size(...) bytes, 16-byte aligned, no initial
  *   value; calls in flight at the same time must not share one

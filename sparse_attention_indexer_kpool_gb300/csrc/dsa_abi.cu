@@ -621,7 +621,7 @@ int dsa_gqa_attend(const void* q, const dsa_gqa_kv* kv, const int32_t* cu_new,
   // a list and a window at once have no meaning here; a list of nothing is no list
   if ((block_ids != nullptr) != (K > 0) && T > 0) return DSA_ERR_INVALID_ARG;
   if (K > 0 && (window > 0 || sinks > 0)) return DSA_ERR_INVALID_ARG;
-  if ((long long)K * kv->page_size > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
+  if ((long long)K * kv->page_size > 1LL << 30) return DSA_ERR_UNSUPPORTED;
   if (T == 0 || B == 0) return DSA_OK;
   r = check_gqa_kv(kv, cu_new);
   if (r != DSA_OK) return r;

@@ -54,7 +54,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t) {
 // Positions that the block table has room for.
 __host__ __device__ inline int table_cap(int max_pages, int page_size) {
   const long long n = (long long)max_pages * page_size;
-  return n < 0x7fffffffll ? (int)n : 0x7fffffff;
+  return n < 0x7fffff00ll ? (int)n : 0x7fffff00;  // (and a few tiles more are still below 2^31)
 }
 
 // Block j, forced into the selection of a token whose own block is `mine`.

@@ -198,7 +198,7 @@ struct Smem {
   static constexpr size_t kCtl = kCodes + 2 * (size_t)kRaw;
   static constexpr size_t kBytes = 1024 + kCtl + sizeof(Ctl);
 };
-static_assert(Smem<128>::kBytes <= 227 * 1024, "shared memory budget");
+static_assert(Smem<128>::kBytes <= 227 * 1024, "shared memory of a CTA");
 
 // The share of this CTA.  Ends with a barrier.
 __device__ __forceinline__ void find_share(const Params& p, Ctl& c) {

@@ -172,3 +172,8 @@ def test_scores_and_attention_by_hand():
 def test_scores_of_more_blocks_than_positions_have(lib):
     assert scores(lib, NB=(1 << 27) + 1) == ERR["DSA_ERR_UNSUPPORTED"]
     assert scores(lib, NB=1 << 27, T=0) == 0
+
+
+def test_attend_lists_of_more_rows_than_counted(lib):
+    assert attend(lib, ids=A, K=(1 << 24) + 1) == ERR["DSA_ERR_UNSUPPORTED"]
+    assert attend(lib, ids=A, K=1 << 24, T=0) == 0
