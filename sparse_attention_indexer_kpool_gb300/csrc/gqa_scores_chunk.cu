@@ -39,7 +39,7 @@ constexpr int kThreads = 256, kCols = 128, kBlocks = 128;
 constexpr float kHigh = 16777216.f;
 
 struct Ctl {
-  uint64_t s_full[2];
+  uint64_t s_full[2], drain;
   int page[4][kBlocks];        // of step u in u & 3; -1: no candidate, -2: a bad page
   uint32_t none[8][4];         // candidates without a page, of step u in u & 7
   float2 part[2][kCols];       // reference and sum of a column, by halves of the tiles
@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid == 0) {
     mbar_init(&c.s_full[0], 1);
     mbar_init(&c.s_full[1], 1);
+    mbar_init(&c.drain, 1);
     fence_mbar_init();
     c.dead = 0;
   }
@@ -339,6 +340,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     cp_async_wait<0>();
+    if (!ok && warp == 0) {  // what was issued, before the CTA's memory is given back
+      umma_commit_elect(&c.drain);
+      mbar_wait_bounded(&c.drain, 0);
+    }
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && c.dead) flag(a.status, DSA_DEV_TIMEOUT);  // outputs unspecified
