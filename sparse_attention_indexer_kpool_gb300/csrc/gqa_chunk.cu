@@ -28,7 +28,7 @@
 // they make NaN.
 //
 // Measured (head dim 128, join included): 2,048 tokens behind 14,336 keys, 4 KV heads of 16 query
-// heads, 996 us, 1.03 PFLOP/s.  A tile of A and B takes 3,950 clocks: the products 2,064, a
+// heads, 969 us, 1.06 PFLOP/s.  A tile of A and B takes 3,950 clocks: the products 2,064, a
 // softmax 1,900 (a row's 128 exponentials, its thread's alone) and handing S and W over, of which
 // the two row tiles cover one another's half.  16 sequences of 1 to 250 tokens, window 1,024, 8 KV
 // heads of 4, 87 us: ten tiles an item do not hide its start and end (rows in, first reference,
@@ -56,6 +56,9 @@ constexpr int kSoftRegs = 152, kOtherRegs = 104;
 static_assert(kSoftRegs + kOtherRegs == 2 * 128, "what the launch has");
 constexpr int kMetas = 4;
 constexpr float kFull = 32768.f;       // a sum of 16 weights above which a reference is raised
+// and from which on it is where another row of the warp has to be: the long chunk below 969 us, 974
+// with 1,024, 994 where each row waits for its own (931 if none were raised)
+constexpr float kHigh = 128.f;
 // What an item costs, in units: a tile of it, one without rows of B, and an item beside its tiles.
 constexpr int kPairCost = 4, kSingleCost = 3, kExtra = 12;
 
@@ -671,14 +674,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (i == 0) tmem_ld32_wait(raw[0]);  // (a load that nobody waited for)
               far = __any_sync(0xffffffffu, high == INFINITY);
               if (far) break;
-              // these columns again, with a reference that is the largest sum's
-              const bool up = high > kFull;
+              // These columns again.  Rows with a sum that is high at all go along with those that
+              // have to: to the sum's exponent less 4, so that the largest of its 16 weights is
+              // not below the reference.
+              const bool up = high >= kHigh;
               int next = ev[0];
 #pragma unroll
               for (int h = 1; h < 4; ++h)
                 if (part[h] == high) next = ev[h];
-              raise(up ? (float)((int)(__float_as_uint(high) >> 23) - 127 - kUp) : 0.f, next + kUp,
-                    i);
+              raise(up ? (float)((int)(__float_as_uint(high) >> 23) - 127 - kUp - 4) : 0.f,
+                    next + kUp, i);
               far = __any_sync(0xffffffffu, base - (mt.least + kUp) > 64);
               if (far) break;
               tmem_ld32_start(ts + i * 32, raw[0]);
