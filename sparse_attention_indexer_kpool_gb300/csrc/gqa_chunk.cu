@@ -417,16 +417,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + lanes + ab * 128, to = tmem + lanes + kOCol + ab * 128;
     const int my = r / p.G, g = r - my * p.G;
     // The warp's 32 rows of Q, in pieces of 16 bytes.  Rows come in and go out through it, so that
-    // neighbouring lanes have neighbouring pieces of memory (a row to a lane took 12,000 clocks to
-    // read and 16,000 to write for each item, six times as long).
+    // neighbouring lanes have neighbouring pieces of memory.  (With cold caches an item's take
+    // 4,000 to 8,000 clocks to read and 6,000 to 10,000 to write; a row to a lane 12,000 and
+    // 16,000.)
     constexpr int kChunks = kD / 8, kAtOnce = 32 / kChunks, kLoads = 32 / kAtOnce;
     auto piece = [&](int row, int k) {
       return reinterpret_cast<uint4*>(sb + S::kQ + ab * S::kTile + (k >> 3) * S::kAtom +
                                       ((r & ~31) + row) * 128 + (((k & 7) ^ (row & 7)) << 4));
     };
     Header hd = {-1, -1, 0, 0};
-    int tiles = 0, segs = 0;      // key tiles and segments so far
-    int mine = 0, outs = 0;       // those of this row tile
+    int tiles = 0;                // key tiles so far
+    int mine = 0, outs = 0;       // those of this row tile, its segments
     bool ok = true;
     while (ok && w.next()) {
       const bool some = w.tb > w.ta, whole = w.ta == 0 && w.tb == w.n;
@@ -455,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      ++segs;
       if (!used) {
         tiles += w.tb - w.ta;
         continue;
