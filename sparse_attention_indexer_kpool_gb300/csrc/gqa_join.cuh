@@ -12,8 +12,8 @@ namespace dsa {
 namespace gqa {
 
 // Weights are held times 2^2, and so are the outputs: 2^13 above a head's first reference before it
-// has to be raised (a chunk's 2,048 tokens behind 14,336 keys: 8 bits held and 7 above, 1,133 us,
-// without a raise 969), and 2^-27 of it below.
+// has to be raised (held times 2^8, with 2^7 above, a chunk of 2,048 tokens behind 14,336 keys took
+// 8 % longer), and 2^-27 of it below.
 constexpr int kUp = 2;
 
 struct Header {        // what a worker left
