@@ -51,6 +51,16 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t) {
   return b;
 }
 
+// The rows cu0 .. cu1 - 1 of a step of n_t, as far as the step has them.  (Clamped before anything
+// is subtracted: faulty boundaries may lie 2^32 apart.)
+struct StepRows {
+  int first, n;  // n < 0: cu falls
+};
+__device__ __forceinline__ StepRows rows_between(int cu0, int cu1, int n_t) {
+  const int c0 = min(max(cu0, 0), n_t);
+  return {c0, min(max(cu1, 0), n_t) - c0};
+}
+
 // Positions that the block table has room for.
 __host__ __device__ inline int table_cap(int max_pages, int page_size) {
   const long long n = (long long)max_pages * page_size;

@@ -111,7 +111,8 @@ __device__ __forceinline__ Place find_place(const int32_t* __restrict__ cu_new, 
     cu1 = cu_new[b + 1];
     len = kv.seq_lens[b];
   }
-  const int c0 = min(max(cu0, 0), n_t), n = min(cu1, n_t) - c0;
+  const StepRows mine = rows_between(cu0, cu1, n_t);
+  const int c0 = mine.first, n = mine.n;
   const int i = slot - first_slot(cu0, b);
   if (reports && i == 0 && (cu0 < 0 || cu1 < cu0 || cu1 > n_t)) flag(status, DSA_DEV_BAD_LENGTH);
   if (n <= 0 || i < 0 || len <= 0) return p;
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(kReadThreads)
       const int b = sequence_of(cu_out, B, t);
       const int c0 = max(cu_out[b], 0), c1 = min(cu_out[b + 1], n_t);
       if (t >= c0 && t < c1) {
-        const long long pos = (long long)(t - cu_out[b]) + (begin ? begin[b] : 0);
+        const long long pos = (long long)t - cu_out[b] + (begin ? begin[b] : 0);
         page = -1;
         if (pos < 0 || pos >= kv.seq_lens[b]) {
           flag(status, DSA_DEV_BAD_LENGTH);

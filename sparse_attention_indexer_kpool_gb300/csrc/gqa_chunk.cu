@@ -85,8 +85,9 @@ struct Seq {
 };
 __device__ __forceinline__ Seq seq_of(int cu0, int cu1, int len, const Params& p) {
   Seq s;
-  s.c0 = min(max(cu0, 0), p.a.T);
-  s.n = max(min(cu1, p.a.T) - s.c0, 0);
+  const StepRows rows = rows_between(cu0, cu1, p.a.T);
+  s.c0 = rows.first;
+  s.n = max(rows.n, 0);
   s.base = len < 0 ? -s.n : len - s.n;  // negative: rows before position 0
   const unsigned all = (unsigned)min(max(len, 0), p.cap);
   unsigned n = (all + kKeys - 1) / kKeys;  // key tiles of an item, at most

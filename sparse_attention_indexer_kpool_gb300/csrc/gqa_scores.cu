@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(kThreads)
         flag(a.status, DSA_DEV_BAD_LENGTH);
   const int row = (int)blockIdx.x / splits;  // the token's row of the step
   const int b = sequence_of(a.cu_new, a.B, row);
-  const int c0 = min(max(a.cu_new[b], 0), a.T), n_new = min(a.cu_new[b + 1], a.T) - c0;
+  const StepRows rows = rows_between(a.cu_new[b], a.cu_new[b + 1], a.T);
+  const int c0 = rows.first, n_new = rows.n;
   const int i0 = row - c0;
   if (i0 < 0 || i0 >= n_new) return;  // (all of a cluster's CTAs alike)
   constexpr int live = 1;

@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int mid = (b + hi) >> 1;
     if (first_slot(mid) <= (int)blockIdx.x) b = mid; else hi = mid;
   }
-  const int c0 = min(max(a.cu_new[b], 0), a.T), n_new = min(a.cu_new[b + 1], a.T) - c0;
+  const StepRows rows = rows_between(a.cu_new[b], a.cu_new[b + 1], a.T);
+  const int c0 = rows.first, n_new = rows.n;
   const int j0 = ((int)blockIdx.x - first_slot(b)) * kPer;  // the CTA's first token
   if (j0 < 0 || j0 >= n_new) return;
   const int live = min(kPer, n_new - j0);

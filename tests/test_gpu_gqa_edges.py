@@ -1,0 +1,63 @@
+"""Edges of the grouped-query calls on the GPU: boundaries, lengths, scales and logits at the ends of
+their ranges, what a weight's rounding may cost, more rows than a grid has in y, and waits that run
+out."""
+import math
+
+import pytest
+import torch
+
+from sparse_attention_indexer_kpool_gb300 import ops
+from tests.test_gpu_gqa import BF, DEV, F8, F32, Case, i32
+
+pytestmark = pytest.mark.gpu
+LOW, HIGH = -2 ** 31, 2 ** 31 - 1
+# geometries, new tokens of two sequences and activation types that take each form of the calls
+FORMS = [(2, 8, 16, 128, (200, 90), BF), (8, 8, 16, 64, (3, 2), BF), (2, 8, 64, 128, (40, 90), BF),
+         (1, 4, 32, 80, (30, 9), F32), (2, 8, 1024, 128, (300, 70), BF)]
+
+
+@pytest.mark.parametrize("Hkv,G,ps,D,new,dtype", FORMS)
+def test_boundaries_far_apart(Hkv, G, ps, D, new, dtype):
+    """Boundaries of the token axis that lie 2^31 and more apart are faults like any others:
+    nothing outside the step is read or written, and a sequence whose end lies before its
+    beginning has no rows."""
+    c = Case(60 + D, [new[0] + 50, new[1] + 20], list(new), Hkv, ps, D)
+    T, edge = c.T, new[0]
+    k, v, q = (c.normal(T, h, D, dtype=dtype).to(DEV) for h in (Hkv, Hkv, Hkv * G))
+    means = c.normal(c.n_pages, Hkv, D).to(DEV)
+
+    def run(cu):
+        kp, vp, ks, vs, table, lens, _ = c.put()
+        st = [i32([0]) for _ in range(4)]
+        mean = means.clone()
+        ops.dsa_gqa_append(k, v, kp, vp, ks, vs, table, lens, i32(cu), k_mean=mean, status=st[0])
+        back = [torch.full((T + 4, Hkv, D), 5.0, dtype=dtype, device=DEV) for _ in "kv"]
+        ops.dsa_gqa_read(kp, vp, ks, vs, table, lens, i32(cu), *(x[2:-2] for x in back),
+                         status=st[1])
+        scores = torch.full((T + 4, Hkv, len(c.table[0])), 5.0, device=DEV)
+        ops.dsa_gqa_block_scores(q, means, table, lens, ps, i32(cu), 0, 1, 0.1, scores[2:-2],
+                                 status=st[2])
+        out = torch.full((T + 4, Hkv * G, D), 5.0, dtype=dtype, device=DEV)
+        lse = torch.full((T + 4, Hkv * G), 5.0, device=DEV)
+        ws = torch.empty(max(16, ops.gqa_attend_workspace_bytes(q, kp)), dtype=torch.uint8,
+                         device=DEV)
+        ops.dsa_gqa_attend(q, kp, vp, ks, vs, table, lens, i32(cu), 0, 0, 0.1, out[2:-2],
+                           lse[2:-2], ws, status=st[3])
+        torch.cuda.synchronize()
+        for x in (*back, scores, out, lse):
+            assert bool((x[:2] == 5.0).all()) and bool((x[-2:] == 5.0).all())
+        return ([x.view(torch.uint8) for x in (kp, vp)] + [ks, vs, mean], back, scores, out,
+                [x.item() for x in st])
+    held, back, scores, out, st = run([0, edge, LOW])
+    want = run([0, edge, edge])
+    assert want[4] == [0] * 4 and st[1:] == [ops.DEV_BAD_LENGTH] * 3
+    for x, y in zip(held, want[0]):
+        assert torch.equal(x.nan_to_num(-1.0), y.nan_to_num(-1.0))
+    for x, y in zip([*back, scores], [*want[1], want[2]]):
+        assert torch.equal(x, y)
+    assert bool((out[2 + edge:] == 5.0).all())
+    for cu in ([LOW, edge, HIGH], [HIGH, edge, LOW], [HIGH, LOW, HIGH], [0, HIGH, LOW]):
+        st = run(cu)[4]
+        assert st[1:] == [ops.DEV_BAD_LENGTH] * 3, cu
+    got = run([0, edge, edge])
+    assert got[4] == [0] * 4 and torch.equal(got[3], want[3])
