@@ -81,11 +81,17 @@ struct Lens {                // of up to 2 kThreads - 1 sequences
 };
 // by_token: slots are the step's tokens, and the first of a block in it (the first new one of its
 // sequence, or the block's first) stands for it: fewer slots where tokens are few.
+// One CTA (`first`) reports faulty boundaries and lengths of all sequences: a faulty sequence need
+// not have a slot of its own.
 __device__ __forceinline__ Place find_place(const int32_t* __restrict__ cu_new, int n_t, int B,
                                             const GqaKv& kv, Lens& s, bool by_token,
-                                            int32_t* status, bool reports) {
+                                            int32_t* status, bool first) {
   const int tid = threadIdx.x, ps = kv.page_size, slot = (int)blockIdx.x;
   Place p{false, -1, 0, 0, 0};
+  auto check = [&](int cu0, int cu1, int len) {
+    const int n = rows_between(cu0, cu1, n_t).n;
+    if (cu0 < 0 || cu1 < cu0 || cu1 > n_t || (n > 0 && len < n)) flag(status, DSA_DEV_BAD_LENGTH);
+  };
   auto first_slot = [&](int cu, int b) {
     const int c = min(max(cu, 0), n_t);
     return by_token ? c : c / ps + 2 * b;
@@ -102,6 +108,7 @@ __device__ __forceinline__ Place find_place(const int32_t* __restrict__ cu_new, 
     cu0 = s.cu[b];
     cu1 = s.cu[b + 1];
     len = s.len[b];
+    if (first && tid < B) check(cu, s.cu[tid + 1], s.len[tid]);
   } else {  // first among every `step`th, then among those between (at most 8192 / 256)
     const int step = (B + 2 * kThreads - 1) / (2 * kThreads), i = tid * step;
     b = max(__syncthreads_count(i < B && first_slot(cu_new[i], i) <= slot) - 1, 0) * step;
@@ -110,14 +117,14 @@ __device__ __forceinline__ Place find_place(const int32_t* __restrict__ cu_new, 
     cu0 = cu_new[b];
     cu1 = cu_new[b + 1];
     len = kv.seq_lens[b];
+    if (first)
+      for (int k = tid; k < B; k += 2 * kThreads) check(cu_new[k], cu_new[k + 1], kv.seq_lens[k]);
   }
   const StepRows mine = rows_between(cu0, cu1, n_t);
   const int c0 = mine.first, n = mine.n;
   const int i = slot - first_slot(cu0, b);
-  if (reports && i == 0 && (cu0 < 0 || cu1 < cu0 || cu1 > n_t)) flag(status, DSA_DEV_BAD_LENGTH);
   if (n <= 0 || i < 0 || len <= 0) return p;
   const long long ctx = (long long)len - n;
-  if (ctx < 0 && reports && i == 0) flag(status, DSA_DEV_BAD_LENGTH);
   // (rows before position 0 have no place)
   const int from = (int)max(ctx, 0ll);
   int blk = from / ps + i;
@@ -246,7 +253,8 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 4 : 2)
   pdl_launch_dependents();
   const int all = threadIdx.x, tid = all & (kThreads - 1), kind = all / kThreads;
   const int lane = tid & 31, warp = tid >> 5, h = blockIdx.y, ps = kv.page_size;
-  const Place p = find_place(cu_new, n_t, B, kv, s_lens, false, status, all == 0 && h == 0);
+  const Place p =
+      find_place(cu_new, n_t, B, kv, s_lens, false, status, blockIdx.x == 0 && h == 0);
   if (!p.some) return;
   const long long pitch = (long long)kv.Hkv * kD;
   const T* src = (kind ? v_new : k_new) + (p.t0 * kv.Hkv + h) * kD;
@@ -377,7 +385,8 @@ __global__ void __launch_bounds__(2 * kThreads)
   const int which = blockIdx.y * kTeams + team, h = which >> 1, kind = which & 1;
   const int ps = kv.page_size, D = kv.D;
   const bool reports = threadIdx.x == 0 && blockIdx.y == 0;
-  const Place p = find_place(cu_new, n_t, B, kv, s_lens, kLanes == 32, status, reports);
+  const Place p = find_place(cu_new, n_t, B, kv, s_lens, kLanes == 32, status,
+                             blockIdx.x == 0 && blockIdx.y == 0);
   if (!p.some || !page_ok(p.page, kv, status, reports)) return;
   if (kLanes == 32 && h >= kv.Hkv) return;  // (no barrier follows for single warps)
   const int lo = p.lo, hi = p.hi;

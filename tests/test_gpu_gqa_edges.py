@@ -61,3 +61,42 @@ def test_boundaries_far_apart(Hkv, G, ps, D, new, dtype):
         assert st[1:] == [ops.DEV_BAD_LENGTH] * 3, cu
     got = run([0, edge, edge])
     assert got[4] == [0] * 4 and torch.equal(got[3], want[3])
+
+
+# forms of the append: a warp a token's block, a CTA a block (elements in registers; read twice)
+@pytest.mark.parametrize("T,B,Hkv,ps,D", [
+    (5, 4, 2, 16, 64), (5, 300, 2, 16, 64), (400, 4, 2, 16, 128), (900, 300, 2, 16, 128),
+    (400, 4, 1, 32, 80)])
+def test_append_reports_every_faulty_sequence(T, B, Hkv, ps, D):
+    """Lengths below the new tokens' number, zero and negative ones, and boundaries that fall, are
+    negative or past the step: reported whichever sequence has them, the last included."""
+    kp, vp = (torch.zeros((3, Hkv, ps, D), dtype=torch.uint8, device=DEV).view(F8) for _ in "kv")
+    ks, vs = torch.ones((3, Hkv), device=DEV), torch.ones((3, Hkv), device=DEV)
+    table = torch.full((B, 1), -1, dtype=torch.int32, device=DEV)
+    x = torch.ones((T, Hkv, D), dtype=BF, device=DEV)
+
+    def status(cu, lens):
+        st = i32([0])
+        ops.dsa_gqa_append(x, x, kp, vp, ks, vs, table, i32(lens), i32(cu), status=st)
+        return st.item()
+    part = [0] + [min(T, 2 + i) for i in range(B - 1)] + [T]
+    good = [T + 40] * B
+    assert status(part, good) == ops.DEV_BAD_PAGE           # (no sequence has a page)
+    for b in (0, 1, B - 1):
+        n = part[b + 1] - part[b]
+        for ln in (n - 1, 0, -1, -5, LOW):
+            if n > 0:
+                assert status(part, good[:b] + [ln] + good[b + 1:]) & ops.DEV_BAD_LENGTH, (b, ln)
+        # without new tokens any length is right
+        if b < B - 1:
+            none = [T if i > b + 1 else 0 for i in range(B + 1)]
+            assert status(none, good[:b] + [-3] + good[b + 1:]) == ops.DEV_BAD_PAGE, b
+    for b, edge in ((0, -3), (0, LOW), (B, T + 1), (B, HIGH), (B - 1, T + 5), (2, -1), (B, 0)):
+        cu = list(part)
+        cu[b] = edge
+        assert status(cu, good) & ops.DEV_BAD_LENGTH, (b, edge)
+    # where no slot is the faulty sequence's own
+    for cu in ([0, T - 1, T + 4], [-3, 0, T], [0, T, 2, T], [0, T, T - 1], [T, 0, 0]):
+        cu = cu + [cu[-1]] * (B + 1 - len(cu))
+        assert status(cu, good) & ops.DEV_BAD_LENGTH, cu
+    assert not bool(kp.view(torch.uint8).any()) and not bool(vp.view(torch.uint8).any())
