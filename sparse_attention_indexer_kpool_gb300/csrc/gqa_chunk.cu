@@ -398,8 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   pdl_wait();
-  pdl_launch_dependents();
   find_share(p, c);
+  // behind the barrier that follows the allocation: a dependent kernel's CTA on this SM might
+  // take the tensor memory that this CTA still waits for, and itself wait for this grid
+  pdl_launch_dependents();
   const uint32_t tmem = c.tmem;
   Walk w(p, c.start);
   const bool issue = p.drill == 0;  // a failure drill loads and multiplies nothing

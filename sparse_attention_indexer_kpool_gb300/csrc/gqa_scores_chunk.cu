@@ -80,7 +80,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, G = a.Hq / a.Hkv;
   pdl_wait();
-  pdl_launch_dependents();
   if (blockIdx.x == 0 && h == 0)
     for (int b = tid; b < a.B; b += kThreads)
       if (a.cu_new[b] < 0 || a.cu_new[b + 1] < a.cu_new[b] || a.cu_new[b + 1] > a.T)
@@ -186,6 +185,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int u = 0; u < 3; ++u) keep(u, page_at(u));
     __syncthreads();
+    // behind the barrier that follows the allocation: a dependent kernel's CTA on this SM might
+    // take the tensor memory that this CTA still waits for, and itself wait for this grid
+    pdl_launch_dependents();
     load(0);
     cp_async_commit();
     load(1);

@@ -2,6 +2,8 @@
 and the tests' plain forms on hand-worked values."""
 import ctypes
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -177,3 +179,32 @@ def test_scores_of_more_blocks_than_positions_have(lib):
 def test_attend_lists_of_more_rows_than_counted(lib):
     assert attend(lib, ids=A, K=(1 << 24) + 1) == ERR["DSA_ERR_UNSUPPORTED"]
     assert attend(lib, ids=A, K=1 << 24, T=0) == 0
+
+
+CSRC = os.path.join(os.path.dirname(build.__file__), "csrc")
+
+
+def gqa_kernels():
+    """(file, source from a kernel's __global__ to the next one or the file's end)"""
+    for name in sorted(os.listdir(CSRC)):
+        if name.startswith("gqa"):
+            text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+            for body in text.split("__global__")[1:]:
+                yield name, body
+
+
+def test_dependents_start_behind_the_tensor_memory():
+    """A kernel lets its dependents start behind a barrier that follows its allocation of tensor
+    memory: a dependent's CTA beside one that still waits for its columns could take them, and
+    itself wait for that grid."""
+    found = 0
+    for name, body in gqa_kernels():
+        if "tmem_alloc<" not in body:
+            continue
+        found += 1
+        alloc = body.index("tmem_alloc<")
+        # (find_share ends with a barrier)
+        barrier = re.compile(r"__syncthreads\w*\(|find_share\(p, c\);").search(body, alloc)
+        triggers = [m.start() for m in re.finditer(r"pdl_launch_dependents\(\)", body)]
+        assert triggers and all(t > barrier.start() for t in triggers), name
+    assert found == 2
