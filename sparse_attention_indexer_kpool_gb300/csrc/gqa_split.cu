@@ -377,8 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto& c = *reinterpret_cast<Ctl<kStages>*>(sb + (size_t)kW * kRingBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const GqaKv& kv = p.a.kv;
-  if (tid < kW * kStages) mbar_init(&c.full[tid / kStages][tid % kStages], 1);
-  if (tid == 0) fence_mbar_init();
+  if (tid < kW * kStages) {  // (each thread's fence covers its own)
+    mbar_init(&c.full[tid / kStages][tid % kStages], 1);
+    fence_mbar_init();
+  }
   pdl_wait();
   pdl_launch_dependents();
   namespace cg = cooperative_groups;

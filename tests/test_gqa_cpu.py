@@ -208,3 +208,25 @@ def test_dependents_start_behind_the_tensor_memory():
         triggers = [m.start() for m in re.finditer(r"pdl_launch_dependents\(\)", body)]
         assert triggers and all(t > barrier.start() for t in triggers), name
     assert found == 2
+
+
+def test_barriers_are_fenced_where_they_are_made():
+    """A thread that makes a barrier fences it itself: another thread's fence, or a block-wide
+    barrier, does not show it to the copies that complete on it."""
+    found = 0
+    for name, body in gqa_kernels():
+        opened, inside = [], []          # blocks that are open; (place, condition's block) of each
+        for m in re.finditer(r"[{}]|mbar_init\(&|fence_mbar_init\(\)", body):
+            if m.group() == "{":
+                opened.append(m.start())
+            elif m.group() == "}":
+                opened = opened[:-1]
+            else:
+                under = [at for at in opened if re.search(r"\bif \([^{};]*\) $", body[:at])]
+                inside.append((m.group(), under[-1] if under else None))
+        fenced = {block for what, block in inside if what.startswith("fence")}
+        for what, block in inside:
+            if what.startswith("mbar"):
+                found += 1
+                assert block is not None and block in fenced, name
+    assert found
