@@ -187,7 +187,7 @@ int dsa_index_scores(const void* q, const float* weights, float scale, const voi
  *   scores   [Q, P_ld] fp32;  pool_ids [Q, select_k] int32
  *   workspace: dsa_topk_pools_workspace_size(Q, P_ld, select_k) bytes (currently 0:
  *   the histogram and candidate lists live in shared memory); may be NULL when 0
- * Supported: 1 <= select_k <= DSA_SELECT_K_MAX.
+ * Supported: 1 <= select_k <= DSA_SELECT_K_MAX; any number of rows.
  */
 int dsa_topk_pools(const float* scores, int Q, int P_ld, int select_k, int32_t* pool_ids,
                    void* workspace, size_t ws_bytes, void* stream);

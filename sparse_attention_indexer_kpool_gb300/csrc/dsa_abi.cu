@@ -340,7 +340,6 @@ int dsa_topk_pools(const float* scores, int Q, int P_ld, int select_k, int32_t* 
   if (Q < 0 || P_ld < 1 || select_k < 1) return DSA_ERR_INVALID_ARG;
   if (select_k > DSA_SELECT_K_MAX) return DSA_ERR_UNSUPPORTED;
   if (Q == 0) return DSA_OK;
-  if (Q > 65535) return DSA_ERR_UNSUPPORTED;
   if (!scores || !pool_ids) return DSA_ERR_INVALID_ARG;
   if (!aligned(scores, 4) || !aligned(pool_ids, 4)) return DSA_ERR_MISALIGNED;
   if (ws_bytes < dsa::topk_workspace_size(Q, P_ld, select_k)) return DSA_ERR_WORKSPACE;

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int C = (int)cluster.num_blocks();
-  const int q = blockIdx.y;
+  const int q = (int)(blockIdx.x / (unsigned)C);  // (rows in x: y ends at 65,535)
   const float* row = scores + (long long)q * P_ld;
   const int lo = (int)((long long)P_ld * rank / C);
   const int hi = (int)((long long)P_ld * (rank + 1) / C);
@@ -581,7 +581,7 @@ int launch_select(const float* scores, int Q, int P_ld, int select_k, int32_t* p
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C, Q, 1);
+  cfg.gridDim = dim3((unsigned)C * (unsigned)Q, 1, 1);  // (C > 1 only for rows fewer than SMs)
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;

@@ -3,11 +3,13 @@ their ranges, what a weight's rounding may cost, more rows than a grid has in y,
 out."""
 import math
 
+import math
+
 import pytest
 import torch
 
-from sparse_attention_indexer_kpool_gb300 import ops
-from tests.test_gpu_gqa import BF, DEV, F8, F32, Case, i32
+from sparse_attention_indexer_kpool_gb300 import ops, pipeline, synth
+from tests.test_gpu_gqa import BF, DEV, F8, F32, Case, compare, i32
 
 pytestmark = pytest.mark.gpu
 LOW, HIGH = -2 ** 31, 2 ** 31 - 1
@@ -100,3 +102,57 @@ def test_append_reports_every_faulty_sequence(T, B, Hkv, ps, D):
         cu = cu + [cu[-1]] * (B + 1 - len(cu))
         assert status(cu, good) & ops.DEV_BAD_LENGTH, cu
     assert not bool(kp.view(torch.uint8).any()) and not bool(vp.view(torch.uint8).any())
+
+
+def top_by_sort(scores, K):
+    """Score descending, then the smaller index; -1 for what is no candidate."""
+    Q, P = scores.shape
+    order = torch.sort(scores.nan_to_num(-math.inf, math.inf, -math.inf), dim=1, descending=True,
+                       stable=True)
+    ids = torch.where(order.values > -math.inf, order.indices, -1)[:, :K].to(torch.int32)
+    return torch.nn.functional.pad(ids, (0, max(0, K - P)), value=-1)
+
+
+@pytest.mark.parametrize("Q,P,K", [(65_535, 33, 7), (65_536, 33, 7), (200_001, 20, 32),
+                                   (70_000, 257, 32), (3, 40_000, 100), (152, 70_000, 64)])
+def test_topk_of_many_rows(Q, P, K):
+    g = torch.Generator(device=DEV).manual_seed(Q + P)
+    s = torch.randint(-6, 7, (Q, P), generator=g, device=DEV).float()
+    s[s == -6] = -math.inf
+    s[s == 6] = math.inf
+    s[::5] = torch.randn(s[::5].shape, generator=g, device=DEV)
+    ids = torch.full((Q + 1, K), 77, dtype=torch.int32, device=DEV)
+    ops.dsa_topk_pools(s, K, ids[:Q], None)
+    assert torch.equal(ids[:Q], top_by_sort(s, K))
+    assert bool((ids[Q] == 77).all())
+
+
+def test_blocks_of_a_long_prompt():
+    """9,000 new tokens of 8 KV heads select their blocks: 72,000 rows in one step."""
+    T, Hkv, G, ps, D, K = 9000, 8, 1, 64, 64, 6
+    cache = synth.GqaCache.alloc(150, Hkv, ps, D, 2, 142)
+    step = pipeline.GqaStep.alloc(cache, torch.arange(150, dtype=torch.int32, device=DEV), T,
+                                  Hkv * G, select_k=K)
+    g = torch.Generator().manual_seed(4)
+    k, v, q = (torch.randn((T, Hkv, D), generator=g).to(BF).to(DEV) for _ in "kvq")
+    pipeline.plan_step(cache, step, i32([T - 5, 5]))
+    pipeline.append_gqa_step(cache, step, k, v)
+    pipeline.select_blocks_step(cache, step, q, 0.125)
+    pipeline.attend_gqa_step(cache, step, q, 0.125, selected=True)
+    torch.cuda.synchronize()
+    assert step.status.item() == 0
+    ids = step.block_ids
+    assert torch.equal(ids.view(T * Hkv, K), top_by_sort(step.scores.view(T * Hkv, -1), K))
+    mine = torch.cat([torch.arange(T - 5), torch.arange(5)]).to(DEV) // ps
+    assert bool((ids == mine[:, None, None]).any(2).all()) and bool((ids[..., 0] == 0).all())
+    assert bool((ids <= mine[:, None, None]).all())
+    # the last tokens' attention, from the cache that the step wrote
+    c = Case.__new__(Case)
+    t = torch.arange(T - 9, T)
+    c.__dict__.update(T=4, cu=[0, 4], new=[4], lens=[T - 5], Hkv=Hkv, ps=ps, D=D,
+                      table=cache.block_table[:1].cpu().tolist())
+    c.codes = dict(k=cache.k_pages.cpu().view(torch.uint8),
+                   v=cache.v_pages.cpu().view(torch.uint8))
+    c.scale = dict(k=cache.k_scale.cpu(), v=cache.v_scale.cpu())
+    compare(c, q[t[:4]].cpu(), 0.125, step.out[t[:4]].cpu(), step.lse[t[:4]].cpu(), BF,
+            ids=ids[t[:4]].cpu())
