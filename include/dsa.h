@@ -493,7 +493,8 @@ int dsa_gqa_read(const dsa_gqa_kv* kv, const int32_t* cu_out, const int32_t* beg
  *   q [T, Hq, D] activation dtype;  k_mean as dsa_gqa_append leaves it
  *   scores [T, Hkv, NB] fp32, 1 <= NB <= 2^27; every entry of a token's row is written; blocks at
  *   or past NB are no candidates and not forced (DSA_DEV_POOL_RANGE)
- * Products, maxima and sums are fp32.
+ * Products, maxima and sums are fp32.  A logit of minus infinity weighs nothing; where a
+ * head has no other, neither does the head.
  * Device faults: also DSA_DEV_TIMEOUT (scores unspecified).
  */
 int dsa_gqa_block_scores(const void* q, const void* k_mean, const int32_t* block_table,

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) gqa_scores_kernel(GqaScoreArgs a) {
     const float ref = top == -INFINITY ? 0.f : top;
     for (int w = 0; w < kWarps; ++w) sum += sl[w * G + g] * exp2f(sm[w * G + g] - ref);
     sm[g] = ref;
-    sl[g] = 1.f / sum;
+    sl[g] = sum == 0.f ? 0.f : 1.f / sum;  // (logits of minus infinity alone weigh nothing)
   }
   __syncthreads();
   float* out = a.scores + ((long long)t * a.Hkv + h) * a.NB;

@@ -156,3 +156,42 @@ def test_blocks_of_a_long_prompt():
     c.scale = dict(k=cache.k_scale.cpu(), v=cache.v_scale.cpu())
     compare(c, q[t[:4]].cpu(), 0.125, step.out[t[:4]].cpu(), step.lse[t[:4]].cpu(), BF,
             ids=ids[t[:4]].cpu())
+
+
+@pytest.mark.parametrize("first,low", [(1.0, -math.inf), (2.0 ** 127, -2.0 ** 10)])
+@pytest.mark.parametrize("lens,new,dtype", [([2300, 700], [2, 1], BF), ([2300, 700], [2, 1], F32)])
+@pytest.mark.parametrize("struck", [[5], list(range(40)), list(range(30, 140, 3)),
+                                    list(range(200))])
+def test_scores_with_logits_of_minus_infinity(lens, new, dtype, first, low, struck):
+    """A block whose logit is minus infinity weighs nothing, in every form of the scores, wherever
+    it stands; where there are only such blocks all weigh nothing."""
+    c = Case(80, lens, new, 2, 16, 128)
+    G, sm = 8, 0.1
+    q, means = c.normal(c.T, 16, 128, dtype=dtype), c.normal(c.n_pages, 2, 128, std=0.5)
+    q[..., 0], means[..., 0] = first, 0.0
+    hit = [j for j in struck if j < len(c.table[0]) and c.table[0][j] >= 0]
+    means[[c.table[0][j] for j in hit], :, 0] = low
+    NB = len(c.table[0])
+    out = torch.empty((c.T, 2, NB), device=DEV)
+    st = i32([0])
+    ops.dsa_gqa_block_scores(q.to(DEV), means.to(DEV), i32(c.table), i32(c.lens), 16, i32(c.cu), 0,
+                             0, sm, out, status=st)
+    assert st.item() == 0
+    got = out.cpu().double()
+    qq, mm = q[..., 1:].double().view(c.T, 2, G, 127), means[..., 1:].double()
+    for b in range(2):
+        page = [p for p in c.table[b] if p >= 0]
+        z = torch.einsum("thgd,jhd->thgj", qq[c.cu[b]:c.cu[b + 1]], mm[page]) * sm
+        # of the logits' size, as where all weigh something (the first element adds 0 to them)
+        big = float(torch.einsum("thgd,jhd->thgj", qq.abs(), mm[page].abs()).max()) * sm
+        dz = big * (2 * 128 + 8) * 2.0 ** -24
+        for i in range(new[b]):
+            n = (lens[b] - new[b] + i + 1) // 16
+            x = z[i, :, :, :n].clone()
+            if b == 0:
+                x[..., [j for j in hit if j < n]] = -math.inf
+            want = torch.softmax(x, -1).nan_to_num(0.0).sum(1)      # (all minus infinity: zeros)
+            y = got[c.cu[b] + i]
+            tol = want * (4 * dz + (NB + G) * 2.0 ** -24 + 2.0 ** -20) + 2.0 ** -126
+            assert bool(((y[:, :n] - want).abs() <= tol).all()), (b, i)
+            assert bool((y[:, n:] == -math.inf).all())
