@@ -255,14 +255,24 @@ __global__ void __launch_bounds__(kThreads, 2)
             part = (s[0] + s[1]) + (s[2] + s[3]);
           };
           weigh();
-          if (part > kHigh) {  // (without a reference every candidate's weight is infinite)
-            float top = -INFINITY;
+          // Without a reference every candidate's weight is infinite, or NaN where its logit is
+          // minus infinity: that sets no reference and weighs nothing.
+          if (!(part <= kHigh)) {
+            float top = ref, nan = 0.f;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if ((see >> k) & 1u) top = fmaxf(top, z[k] * unit);
-            sum *= ex2_fast(ref - top);
-            ref = top;
-            weigh();
+              if ((see >> k) & 1u) {
+                const float x = z[k] * unit;
+                top = fmaxf(top, x);
+                nan = x != x ? x : nan;
+              }
+            if (top == -INFINITY) {
+              part = nan;
+            } else {
+              sum *= ex2_fast(ref - top);
+              ref = top;
+              weigh();
+            }
           }
           __syncwarp();
           sum += part;

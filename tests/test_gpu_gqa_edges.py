@@ -159,7 +159,8 @@ def test_blocks_of_a_long_prompt():
 
 
 @pytest.mark.parametrize("first,low", [(1.0, -math.inf), (2.0 ** 127, -2.0 ** 10)])
-@pytest.mark.parametrize("lens,new,dtype", [([2300, 700], [2, 1], BF), ([2300, 700], [2, 1], F32)])
+@pytest.mark.parametrize("lens,new,dtype", [([2300, 700], [200, 30], BF), ([2300, 700], [2, 1], BF),
+                                            ([2300, 700], [2, 1], F32)])
 @pytest.mark.parametrize("struck", [[5], list(range(40)), list(range(30, 140, 3)),
                                     list(range(200))])
 def test_scores_with_logits_of_minus_infinity(lens, new, dtype, first, low, struck):
