@@ -75,6 +75,7 @@ struct Params {
   float4* part_ml;           // [2 workers][8 kN]: reference; the sum f 2^z as z and f
   Header* head;              // [workers]
   int workers;               // warps that take a share, at most gridDim.x * kW
+  int drill;                 // a failure drill loads nothing: the first waits run out
 };
 
 // ---- the batch as tiles --------------------------------------------------------
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!more) return;
     if (lv - held == 32) look_up();
     const int src = lv - held, s = issued % kStages;
-    if (lane == src) {
+    if (lane == src && p.drill == 0) {
       Meta& m = c.meta[warp][s];
 #pragma unroll
       for (int i = 0; i < kBoxes; ++i) {
@@ -484,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Header hd = {-1, -1, 0, 0};
   int done = 0;
   bool ok = true;
+  const unsigned long long wait_ns = p.drill ? kDrillWaitNs : kWaitNs;
   while (ok && w.next()) {
     const bool some = w.tb > w.ta, whole = !kCluster && w.ta == 0 && w.tb == w.n;
     const bool begins = some && w.ta == 0 && !whole;
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int v = w.ta; v < w.tb; ++v, ++done) {
       const int s = done % kStages;
-      ok = mbar_wait_bounded(&c.full[warp][s], (unsigned)(done / kStages) & 1u);
+      ok = mbar_wait_bounded(&c.full[warp][s], (unsigned)(done / kStages) & 1u, wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const Meta& mt = c.meta[warp][s];
@@ -846,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (!ok) {  // a wait ran out: no copy into this CTA's memory may be in flight at its end
     for (; done < issued; ++done)
-      mbar_wait_bounded(&c.full[warp][done % kStages], (unsigned)(done / kStages) & 1u);
+      mbar_wait_bounded(&c.full[warp][done % kStages], (unsigned)(done / kStages) & 1u, wait_ns);
     if (lane == 0) flag(p.a.status, DSA_DEV_TIMEOUT);
     hd = Header{-1, -1, 0, 0};
   }
@@ -858,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rest = tile - token * per, h = rest / p.hb, head0 = (rest - h * p.hb) * 8 * kN;
     const int heads = min(8 * kN, p.G - head0), mine = max(w.tb - w.ta, 0);
     static_assert(8 * kN * kD * 4 <= kRingBytes, "a warp's partial takes its ring's place");
-    if (mine == 0)
+    if (mine == 0 || !ok)  // (after a give-up: no sums of whoever had the memory before)
       for (int i = lane; i < 8 * kN; i += 32)
         sh->ml[warp][i] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
     __syncthreads();
@@ -945,6 +947,7 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream, bool together
   p.zscale = a.sm_scale * kLog2e;
   p.cap = table_cap(a.kv.max_pages, a.kv.page_size);
   p.per_block = a.kv.page_size / kR;
+  p.drill = failure_drill();
   const long long row_tiles = (long long)a.T * a.kv.Hkv * p.hb;
   const long long seen = a.block_ids ? (long long)a.K * a.kv.page_size
                          : a.window > 0 && (long long)a.window + a.sinks < p.cap

@@ -9,7 +9,8 @@ import pytest
 import torch
 
 from sparse_attention_indexer_kpool_gb300 import ops, pipeline, synth
-from tests.test_gpu_gqa import BF, DEV, F8, F32, Case, compare, i32
+from tests.test_gpu_gqa import (BF, DEV, F8, F32, Case, compare, i32, random_ids,
+                                run_attend)
 
 pytestmark = pytest.mark.gpu
 LOW, HIGH = -2 ** 31, 2 ** 31 - 1
@@ -196,3 +197,27 @@ def test_scores_with_logits_of_minus_infinity(lens, new, dtype, first, low, stru
             tol = want * (4 * dz + (NB + G) * 2.0 ** -24 + 2.0 ** -20) + 2.0 ** -126
             assert bool(((y[:, :n] - want).abs() <= tol).all()), (b, i)
             assert bool((y[:, n:] == -math.inf).all())
+
+
+@pytest.mark.parametrize("G", [8, 16])
+@pytest.mark.parametrize("lens,new,width,K", [
+    ([2300, 700], [1, 2], 150, 0),              # a cluster a row tile
+    ([2300, 700], [1, 2], 2500, 0),             # warps on equal shares, and a join
+    ([2300, 700, 90], [60, 40, 9], 150, 20)])   # the same on lists
+def test_decode_attention_gives_up_and_recovers(lens, new, width, K, G):
+    """The waits of the decode attention run out under a drill: the call ends with a flagged
+    status, the context stays usable, and the same call afterwards gives what it gave before."""
+    c = Case(81, lens, new, 2, 16, 128, width=width)
+    q = c.normal(c.T, 2 * G, 128)
+    ids = random_ids(c, K) if K else None
+    first = run_attend(c, q, 0.1, ids=ids)
+    assert first[2] == 0
+    ops.dsa_set_failure_drill(ops.DSA_DRILL_SKIP_ARM)
+    try:
+        for _ in range(2):
+            assert run_attend(c, q, 0.1, ids=ids)[2] == ops.DEV_TIMEOUT
+    finally:
+        ops.dsa_set_failure_drill(0)
+    again = run_attend(c, q, 0.1, ids=ids)
+    assert again[2] == 0
+    assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
