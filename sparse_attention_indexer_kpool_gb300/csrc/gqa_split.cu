@@ -916,9 +916,10 @@ struct Rows {
   }
 };
 
-// Clusters of `ctas` CTAs (one an SM) that the device holds at once.
-template <typename K>
-int clusters_of(K kernel, size_t bytes, int ctas) {
+// Clusters of `ctas` CTAs (one an SM) that the device holds at once; asked once for each kernel (all
+// of them have one type), device and size.
+template <auto kKernel>
+int clusters_of(size_t bytes, int ctas) {
   static std::atomic<int> held[64][4];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
@@ -929,7 +930,7 @@ int clusters_of(K kernel, size_t bytes, int ctas) {
   l.attr.id = cudaLaunchAttributeClusterDimension;
   l.attr.val.clusterDim.x = ctas;
   l.attr.val.clusterDim.y = l.attr.val.clusterDim.z = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, kKernel, &l.cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -961,7 +962,7 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream, bool together
     static std::atomic<unsigned long long> done{0};
     if (!allow_smem(kernel, kBytes, done)) return DSA_ERR_CUDA;
     while (ctas > 1 && (row_tiles * ctas > num_sms() ||
-                        row_tiles > clusters_of(kernel, kBytes, ctas)))
+                        row_tiles > clusters_of<gqa_split_kernel<kD, kN, kR, true>>(kBytes, ctas)))
       ctas >>= 1;
   }
   const long long all = row_tiles * ctas;

@@ -4,6 +4,7 @@ import ctypes
 import math
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -240,3 +241,13 @@ def test_topk_takes_the_rows_of_a_long_prompt(lib):
         assert lib.dsa_topk_pools(None, rows, 64, 32, A, None, 0, None) == ERR["DSA_ERR_INVALID_ARG"]
         assert lib.dsa_topk_pools_workspace_size(rows, 64, 32) == 0
     assert lib.dsa_kernel_launches() == n
+
+
+def test_every_cluster_kernel_asks_for_itself(lib):
+    """How many clusters fit at once is kept for each of the decode kernel's eight cluster forms:
+    they differ in shared memory and registers."""
+    names = subprocess.run(["nm", "-C", os.path.join(build.BUILD, "gqa_split.o")], text=True,
+                           capture_output=True, check=True).stdout
+    kept = re.findall(r"clusters_of<&\(void dsa::\(anonymous namespace\)::gqa_split_kernel"
+                      r"<(\d+, \d+, \d+), true>[^\n]*\)::held$", names, re.M)
+    assert len(set(kept)) == 8
