@@ -6,7 +6,7 @@
 // rows.  An item is two of them, A and B, one behind the other; a CTA runs through its equal
 // share of the batch's (item, tile of 128 keys) units.  Per tile, for A and B in turn:
 //   S = Q C_k^T                   fp16 in, fp32 out in tensor memory
-//   e = S * (query scale * key scale * softmax scale) + lv - m,  w = 2^e
+//   e = S * (query scale * (key scale * softmax scale)) + lv - m,  w = 2^e
 //   O += W C_v                    W as the first factor in tensor memory, where S was
 // with the codes C widened to fp16 (exact), the query rows scaled by a power of two, lv the
 // exponent of the values' scale and m a row's reference, all as in the kernel for decode
@@ -65,7 +65,7 @@ constexpr int kPairCost = 4, kSingleCost = 3, kExtra = 12;
 struct Params {
   GqaArgs a;
   int G, per;          // query heads of a KV head; tokens of a row tile
-  float zscale;        // softmax scale in base 2
+  float zscale;        // softmax scale in base 2, times 2^-14 (see Meta)
   int cap;             // positions that the block table has room for
   int box_log;         // keys of a TMA box
   float* part_o;       // [2 CTAs][2 kRows][D]
@@ -175,7 +175,8 @@ struct Walk {
 
 struct Meta {          // of a key tile, by 16 keys
   alignas(16) int pos[kGroups];  // first position (0x7fffffff: none)
-  alignas(16) float ks[kGroups];  // keys' scale
+  alignas(16) float ks[kGroups];  // keys' scale times the softmax scale's size and 2^-14: what is
+                       // left to a row is the power of two of its largest element, a normal number
   alignas(16) int ev[kGroups];    // exponent of the values' scale
   int row[kGroups];    // first cache row
   uint32_t nan[4];     // keys whose NaN values were taken out of the tile
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (a negative scale's sign goes with the query: what scores are multiplied with is
         // positive, and what is masked may be -infinity before it)
         const float up0 = copysignf(pow2(half), p.zscale), up1 = pow2(14 - ex - half);
-        qs = pow2(-half) * pow2(half + ex - 14) * fabsf(p.zscale);
+        qs = pow2(ex);
 #pragma unroll 4
         for (int k = 0; k < kChunks; ++k) {
           const uint4 y = *piece(lane, k);
@@ -990,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ev = 0;
         if (row >= 0) {
           const int unit = row / kv.page_size;
-          ks = __ldg(kv.k_scale + unit);
+          ks = __ldg(kv.k_scale + unit) * fabsf(p.zscale);
           ev = exponent_of(__ldg(kv.v_scale + unit));
         }
         int next_pos, next_row;
@@ -1142,7 +1143,7 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
   p.a = a;
   p.G = a.Hq / a.kv.Hkv;
   p.per = kRows / p.G;
-  p.zscale = a.sm_scale * kLog2e;
+  p.zscale = a.sm_scale * kLog2e * 0x1p-14f;
   p.cap = table_cap(a.kv.max_pages, a.kv.page_size);
   p.box_log = chunk::box_log_of(a.kv.page_size);
   p.part_o = static_cast<float*>(workspace);

@@ -5,7 +5,7 @@
 // A row tile is one token, one KV head and up to 8 kN of its query heads.  Per tile of 32
 // keys, with the keys as the rows of the products (16 x 8 x 16, fp16 in, fp32 out):
 //   S^T = C_k Q^T                 the codes of the keys, widened to fp16 (exact)
-//   e = S * (query scale * key scale * softmax scale) + lv - m,  w = 2^e
+//   e = S * (query scale * (key scale * softmax scale)) + lv - m,  w = 2^e
 //   O^T += C_v^T W^T              the codes of the values, widened likewise
 // Query rows are scaled by a power of two to a largest magnitude in [2^14, 2^15): a bf16
 // element keeps its 8 bits in fp16 down to 2^-28 of the row's largest.  lv is the exponent of the
@@ -68,7 +68,7 @@ constexpr int kRingBytes = 2 * 2 * kKeys * 128;  // of a warp
 struct Params {
   GqaArgs a;
   int G, hb;                 // query heads of a KV head, row tiles of those
-  float zscale;              // softmax scale in base 2
+  float zscale;              // softmax scale in base 2, times 2^-14 (see Meta)
   int cap;                   // positions that the block table has room for
   int per_block;             // boxes of a block
   float* part_o;             // [2 workers][8 kN][D]
@@ -340,7 +340,8 @@ __device__ __forceinline__ float across_keys(float v) {
 }
 struct Meta {          // of a tile in the ring, by box
   int pos[2];          // first position (0x7fffffff: no such box)
-  float ks[2];         // keys' scale
+  float ks[2];         // keys' scale times the softmax scale and 2^-14: what is left to a query row is
+                       // the power of two of its largest element, a normal number whatever that is
   int ev[2];           // exponent of the values' scale
 };
 template <int kStages>
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int unit = page * kv.Hkv + wl.h;
       row[i] = unit * kv.page_size + ((int)at - blk * kv.page_size);
       bpos[i] = (int)at;
-      bks[i] = __ldg(kv.k_scale + unit);
+      bks[i] = __ldg(kv.k_scale + unit) * p.zscale;
       bev[i] = exponent_of(__ldg(kv.v_scale + unit));
     }
   };
@@ -538,7 +539,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -126), half = (14 - ex) >> 1;
       const float up0 = pow2(half), up1 = pow2(14 - ex - half);
-      const float down = pow2(-half) * pow2(half + ex - 14);
 #pragma unroll
       for (int i = 0; i < kD / 64; ++i)
 #pragma unroll
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        qs[n][j] = __shfl_sync(0xffffffffu, down, (2 * t + j) * 4) * p.zscale;
+        qs[n][j] = __shfl_sync(0xffffffffu, pow2(ex), (2 * t + j) * 4);
     }
     float o[kM][kN][4], l[kN][2], m[kN][2];
     int base[kN][2];  // B
@@ -945,7 +945,7 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream, bool together
   p.a = a;
   p.G = a.Hq / a.kv.Hkv;
   p.hb = (p.G + 8 * kN - 1) / (8 * kN);
-  p.zscale = a.sm_scale * kLog2e;
+  p.zscale = a.sm_scale * kLog2e * 0x1p-14f;
   p.cap = table_cap(a.kv.max_pages, a.kv.page_size);
   p.per_block = a.kv.page_size / kR;
   p.drill = failure_drill();

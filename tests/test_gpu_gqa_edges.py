@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from sparse_attention_indexer_kpool_gb300 import ops, pipeline, synth
+from tests import _gqa_ref as ref
 from tests.test_gpu_gqa import (BF, DEV, F8, F32, Case, compare, i32, random_ids,
                                 run_attend)
 
@@ -221,3 +222,40 @@ def test_decode_attention_gives_up_and_recovers(lens, new, width, K, G):
     again = run_attend(c, q, 0.1, ids=ids)
     assert again[2] == 0
     assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
+PLACES = [  # lens, new, table width, K, type: a cluster a row tile, shares, lists, chunks, generic
+    ([300, 90], [2, 1], None, 0, BF), ([300, 90], [2, 1], 2500, 0, BF),
+    ([300, 90], [40, 30], None, 6, BF), ([300, 90], [40, 30], None, 0, BF),
+    ([120, 40], [3, 2], None, 0, F32)]
+
+
+def check_in_place(c, q, sm, K, dtype):
+    ids = random_ids(c, K) if K else None
+    out, lse, st = run_attend(c, q, sm, ids=ids)
+    assert st == 0
+    compare(c, q, sm, out, lse, dtype, ids=ids)
+
+
+@pytest.mark.parametrize("lens,new,width,K,dtype", PLACES)
+@pytest.mark.parametrize("e_q,lo,hi", [(-17, -64, 11), (-118, -64, 112), (-122, 100, 116),
+                                       (-125, 119, 119), (58, -64, -64)])
+def test_attend_queries_and_key_scales_far_apart(lens, new, width, K, dtype, e_q, lo, hi):
+    """Logits of ordinary size from queries and keys' scales at opposite ends of their ranges, and
+    blocks whose keys are next to nothing beside them."""
+    c = Case(90 + K, lens, new, 2, 16, 128, width=width)
+    e = torch.randint(0, 2, c.scale["k"].shape, generator=c.g) * (hi - lo) + lo
+    c.scale["k"] = torch.where(torch.isnan(c.scale["k"]), c.scale["k"], torch.exp2(e.float()))
+    q = (c.normal(c.T, 16, 128, dtype=F32) * 2.0 ** e_q).to(dtype)
+    check_in_place(c, q, 1.0 / math.sqrt(128), K, dtype)
+
+
+@pytest.mark.parametrize("lens,new,width,K,dtype", PLACES)
+def test_attend_value_scales_at_both_ends(lens, new, width, K, dtype):
+    """Values' scales of 2^-64 and 2^120 side by side (codes up to 112: their values are numbers of
+    the outputs' type)."""
+    c = Case(91 + K, lens, new, 2, 16, 128, width=width)
+    e = torch.randint(0, 2, c.scale["v"].shape, generator=c.g) * 184 - 64
+    c.scale["v"] = torch.where(torch.isnan(c.scale["v"]), c.scale["v"], torch.exp2(e.float()))
+    c.codes["v"] = (ref.values(c.codes["v"]) / 4.0).float().to(F8).view(torch.uint8)
+    check_in_place(c, c.normal(c.T, 16, 128, std=2.0, dtype=dtype), 1.0 / math.sqrt(128), K, dtype)
