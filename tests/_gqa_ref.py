@@ -185,3 +185,23 @@ def attend_dense(q, kp, ks, vp, vs, table, lens, cu, sm, window=0, sinks=0):
             lse[rows] = torch.logsumexp(z, -1)
             top[rows] = (w * vs[page, h]).amax(-1) * lens[b]
     return out, lse, mass, top, big
+
+
+def bound_of_bf16(want, mass, top, big, n, D):
+    """How far the bf16 path's outputs may be from ``attend``'s: a logit is a sum of D products in
+    fp32 (cut off where fp32 rounds: two half steps a term) and a few more roundings; a weight is
+    2^z (2^-22) over a sum of n.  Then the weight's rounding to fp16's 11 bits, 2^-11 of it; where
+    it is below fp16's normal numbers, and where weights that are written are scaled down, 2^-25 of
+    the row's largest at most, a code of at most 448 and n keys; and the output's to bf16, 2^-8."""
+    dz = big * (2 * D + 8) * 2.0 ** -24
+    w = 2 * dz + n * 2.0 ** -24 + 2.0 ** -20
+    return (2.0 ** -8 * want.abs() + 2 * w * (mass + want.abs()) + 2.0 ** -11 * mass
+            + 448 * 2.0 ** -25 * top[..., None] + 2.0 ** -126)
+
+
+def weights_rounded_to(dtype, z, v, s):
+    """Outputs [G, D] of logits ``z`` [G, n], values ``v`` [n, D] of scales ``s`` [n], with weights
+    times scales rounded to ``dtype`` for the products and not for the sum."""
+    w = torch.exp(z - z.amax(-1, keepdim=True))
+    held = 4.0 * w * s / (w * s).amax(-1, keepdim=True)
+    return (held.to(dtype).double() / held.nan_to_num(1.0) * w) @ v / w.sum(-1, keepdim=True)

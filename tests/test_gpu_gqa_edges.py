@@ -259,3 +259,24 @@ def test_attend_value_scales_at_both_ends(lens, new, width, K, dtype):
     c.scale["v"] = torch.where(torch.isnan(c.scale["v"]), c.scale["v"], torch.exp2(e.float()))
     c.codes["v"] = (ref.values(c.codes["v"]) / 4.0).float().to(F8).view(torch.uint8)
     check_in_place(c, c.normal(c.T, 16, 128, std=2.0, dtype=dtype), 1.0 / math.sqrt(128), K, dtype)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,new,width,K", [
+    ([2, 3, 5, 9, 40], [1] * 5, None, 0), ([2, 3, 5, 9, 40], [1] * 5, 2500, 0),
+    ([40, 30, 7], [40, 30, 7], None, 2), ([60, 50], [60, 50], None, 0)])
+def test_weights_have_eleven_bits(lens, new, width, K, D):
+    """Logits next to each other and values that cancel: a weight's own rounding is then most of
+    what an output may be off, and eight bits of it would be too few (the bound's own test)."""
+    c = Case(92 + K, lens, new, 2, 16, D, spread=1, width=width)
+    G, sm = 8, 1.0 / math.sqrt(D)
+    q = c.normal(c.T, 2 * G, D, std=0.02)
+    ids = random_ids(c, K) if K else None
+    out, lse, st = run_attend(c, q, sm, ids=ids)
+    assert st == 0
+    want, _, mass, top, big = ref.attend(q, *c.plain("k"), *c.plain("v"), c.table, c.lens, c.cu, sm,
+                                         ids=ids)
+    n = max(lens) if ids is None else K * 16
+    tol = ref.bound_of_bf16(want, mass, top, big, n, D)
+    assert bool(((out.double() - want).abs() <= tol).all())
+    compare(c, q, sm, out, lse, BF, ids=ids)

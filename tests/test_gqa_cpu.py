@@ -251,3 +251,21 @@ def test_every_cluster_kernel_asks_for_itself(lib):
     kept = re.findall(r"clusters_of<&\(void dsa::\(anonymous namespace\)::gqa_split_kernel"
                       r"<(\d+, \d+, \d+), true>[^\n]*\)::held$", names, re.M)
     assert len(set(kept)) == 8
+
+
+def test_the_bound_of_the_bf16_path_is_that_of_fp16_weights():
+    """The bound that the GPU's attention is held to passes weights rounded to fp16 and none rounded
+    to bf16 (planted here, in the plain form)."""
+    g = torch.Generator().manual_seed(6)
+    for n in (2, 3, 5, 9, 40):
+        z = torch.randn((16, n), generator=g).double() * 0.05
+        s = torch.exp2(torch.randint(-3, 4, (n,), generator=g).double())
+        v = torch.randn((n, 128), generator=g).double() * 100.0 * s[:, None]
+        w = torch.softmax(z, -1)
+        want, mass, top = w @ v, w @ v.abs(), (w * s).amax(-1) * n
+        tol = ref.bound_of_bf16(want, mass, top, 0.2, n, 128)
+        fails = {}
+        for dtype in (torch.float16, torch.bfloat16):
+            out = ref.weights_rounded_to(dtype, z, v, s).to(torch.bfloat16).double()
+            fails[dtype] = int(((out - want).abs() > tol).sum())
+        assert fails[torch.float16] == 0 and fails[torch.bfloat16] > 0, (n, fails)
