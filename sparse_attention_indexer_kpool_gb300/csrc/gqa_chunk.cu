@@ -289,10 +289,6 @@ constexpr uint32_t idesc_f16(int m, int n, bool b_mn) {
          ((uint32_t)(m >> 4) << 24);
 }
 // A from tensor memory; run by a converged warp, one elected lane issues
-__device__ __forceinline__ void umma_f16_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                               uint32_t accumulate) {
-  umma_bf16_elect(d, a, b, idesc, accumulate);  // (the types stand in the descriptor)
-}
 __device__ __forceinline__ void umma_tmem_a_elect(uint32_t d, uint32_t a, uint64_t b,
                                                   uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -1077,7 +1073,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int s = 0; s < kD / 16; ++s) {
         const uint32_t at = ((s >> 2) * S::kAtom + (s & 3) * 32) >> 4;
-        umma_f16_elect(tmem + ab * 128, dq + at, dk + at, id_s, s ? 1u : 0u);
+        // (the types stand in the descriptor)
+        umma_bf16_elect(tmem + ab * 128, dq + at, dk + at, id_s, s ? 1u : 0u);
       }
       umma_commit_elect(&c.s_full[ab]);
     };

@@ -131,13 +131,13 @@ __global__ void __launch_bounds__(kThreads) gqa_scores_kernel(GqaScoreArgs a) {
 }
 
 // ---- tensor cores ------------------------------------------------------------------
-// The means of 16 blocks are the rows of a product, 8 kN (token, head) pairs of one
-// sequence and KV head its columns: z^T = K_mean Q^T, bf16 in, fp32 out.  Lane (g, t) of a warp
+// The means of 16 blocks are the rows of a product, up to 8 kN query heads of a token and KV
+// head its columns: z^T = K_mean Q^T, bf16 in, fp32 out.  Lane (g, t) of a warp
 // loads 16-byte pieces t, t + 4, .. of the rows g and g + 8 straight from memory and uses
 // them as they come; the queries' pieces, kept in registers, follow the same order.  A lane
 // then has two columns' z of its rows: it keeps their maximum and sum alone, and only at
 // the end of the first pass do lanes (and warps, and CTAs) exchange them.
-// Here (decode) the warps of a cluster's CTAs share the blocks of one token, so that many SMs
+// The warps of a cluster's CTAs share the blocks of one token, so that many SMs
 // read one long context's means.  Bound by round trips to the table and the means: four tokens on
 // 262,144 keys (8 KV heads of 8 query heads of 128) 10.3 us, 15 with cold caches, where the
 // means' 34 MB take 5.
@@ -147,7 +147,7 @@ struct GroupArgs {
   int pad;                           // G up to a power of two
 };
 
-// Sums over a token's `pad` columns, left in its first: a lane's two, its neighbours', n tiles.
+// Sums over the token's `pad` columns, left in the first: a lane's two, its neighbours', n tiles.
 template <int kN>
 __device__ __forceinline__ void sum_heads(float (&z)[kN][4], int pad) {
 #pragma unroll
@@ -204,17 +204,14 @@ __global__ void __launch_bounds__(kThreads)
   const int c0 = rows.first, n_new = rows.n;
   const int i0 = row - c0;
   if (i0 < 0 || i0 >= n_new) return;  // (all of a cluster's CTAs alike)
-  constexpr int live = 1;
-  const long long base = (long long)a.seq_lens[b] - n_new + i0;  // the first token's position
-  auto whole_at = [&](long long pos) {
-    return pos < 0 ? 0 : (int)min((long long)min(a.NB, a.max_pages), (pos + 1) / a.page_size);
-  };
-  const int most = whole_at(base + live - 1);  // candidates of the last token
+  const long long pos = (long long)a.seq_lens[b] - n_new + i0;
+  const int most =  // candidates
+      pos < 0 ? 0 : (int)min((long long)min(a.NB, a.max_pages), (pos + 1) / a.page_size);
+  const int mine = pos < 0 ? -1 : (int)(pos / a.page_size);
   if (h == 0 && rank == 0 && tid == 0) {
-    if (base < 0) flag(a.status, DSA_DEV_BAD_LENGTH);
-    const long long last = (base + live - 1) / a.page_size;
-    if (base + live > 0 && last >= a.NB) flag(a.status, DSA_DEV_POOL_RANGE);
-    if (base + live > 0 && last >= a.max_pages) flag(a.status, DSA_DEV_BAD_PAGE);
+    if (pos < 0) flag(a.status, DSA_DEV_BAD_LENGTH);
+    if (mine >= a.NB) flag(a.status, DSA_DEV_POOL_RANGE);
+    if (mine >= a.max_pages) flag(a.status, DSA_DEV_BAD_PAGE);
   }
 
   // queries: lane (g, t) has column g of every n tile; candidates of columns 2 t, 2 t + 1
@@ -222,11 +219,11 @@ __global__ void __launch_bounds__(kThreads)
   int cand[kN][2];
 #pragma unroll
   for (int n = 0; n < kN; ++n) {
-    const int col = n * 8 + g, i = col / ga.pad, head = col - i * ga.pad;
-    const bool real = i < live && head < G;
+    const int head = n * 8 + g;
+    const bool real = head < G;
     const uint4* src = reinterpret_cast<const uint4*>(
         static_cast<const __nv_bfloat16*>(a.q) +
-        ((long long)(c0 + i0 + (real ? i : 0)) * a.Hq + (long long)h * G + (real ? head : 0)) * kD);
+        ((long long)row * a.Hq + (long long)h * G + (real ? head : 0)) * kD);
 #pragma unroll
     for (int k = 0; k < kD / 32; ++k) {
       const uint4 x = real ? __ldg(src + 4 * k + t) : make_uint4(0u, 0u, 0u, 0u);
@@ -236,10 +233,7 @@ __global__ void __launch_bounds__(kThreads)
       q[n][2 * k + 1][1] = x.w;
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = n * 8 + 2 * t + j, ic = c / ga.pad;
-      cand[n][j] = ic < live && c - ic * ga.pad < G ? whole_at(base + ic) : 0;
-    }
+    for (int j = 0; j < 2; ++j) cand[n][j] = n * 8 + 2 * t + j < G ? most : 0;
   }
   const float unit = a.sm_scale * kLog2e;
   const int32_t* table = a.block_table + (long long)b * a.max_pages;
@@ -395,23 +389,20 @@ __global__ void __launch_bounds__(kThreads)
   for (int n = 0; n < kN; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int c = n * 8 + 2 * t + i, ic = c / ga.pad;
       // (a column that is none adds nothing; without a candidate no weight is looked at)
-      l[n][i] = ic < live && c - ic * ga.pad < G ? 1.f / l[n][i] : 0.f;
+      l[n][i] = n * 8 + 2 * t + i < G ? 1.f / l[n][i] : 0.f;
       if (l[n][i] == INFINITY) l[n][i] = 0.f;
     }
 
-  // ---- second pass: weights, summed over a token's heads
-  const long long pos = base;
-  const int mine = pos < 0 ? -1 : (int)(pos / a.page_size);
-  float* out = a.scores + ((long long)(c0 + i0) * a.Hkv + h) * a.NB;
+  // ---- second pass: weights, summed over the token's heads
+  float* out = a.scores + ((long long)row * a.Hkv + h) * a.NB;
   auto write = [&](int v, int p0, int p1, float (&z)[kN][4]) {
 #pragma unroll
     for (int n = 0; n < kN; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) z[n][i] = ex2_fast(z[n][i] - m[n][i & 1]) * l[n][i & 1];
     sum_heads<kN>(z, ga.pad);
-    if (t != 0) return;  // the token's first column writes
+    if (t != 0) return;  // the first column writes
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int j = v * 16 + g + 8 * r, page = r ? p1 : p0;

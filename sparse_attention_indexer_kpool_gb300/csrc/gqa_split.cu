@@ -181,7 +181,6 @@ struct Walk {
     if (a == u) return n;
     return (int)((unsigned long long)a * (unsigned)n / u);
   }
-  __device__ __forceinline__ bool sees(int t) const { return t <= pos && (t >= lo || t < s0); }
 };
 
 // The share of worker `me` for each warp of this CTA.  Ends with a barrier.
