@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int C = (int)cluster.num_blocks();
-  const int q = (int)(blockIdx.x / (unsigned)C);  // (rows in x: y ends at 65,535)
+  // (rows in x: y ends at 65,535)
+  const int q = (int)(C == 1 ? blockIdx.x : blockIdx.x / (unsigned)C);
   const float* row = scores + (long long)q * P_ld;
   const int lo = (int)((long long)P_ld * rank / C);
   const int hi = (int)((long long)P_ld * (rank + 1) / C);
