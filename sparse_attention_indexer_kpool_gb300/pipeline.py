@@ -291,10 +291,16 @@ def append_gqa_step(cache: GqaCache, step: GqaStep, k_new, v_new, stream=None):
                        stream)
 
 
+def _selects(step: GqaStep):
+    if step.block_ids is None:  # (attention without a list would be over everything)
+        raise ValueError("the step has no buffers for a selection: alloc it with select_k")
+
+
 def select_blocks_step(cache: GqaCache, step: GqaStep, q, sm_scale, sink_blocks=1, local_blocks=1,
                        stream=None):
     """``step.block_ids``: the blocks that each of the step's tokens (``q`` [T, Hq, D]) attends
     to, for each KV head."""
+    _selects(step)
     ops.dsa_gqa_block_scores(q, cache.k_mean, cache.block_table, cache.seq_lens, cache.page_size,
                              step.cu_new, sink_blocks, local_blocks, sm_scale, step.scores,
                              step.status, stream)
@@ -307,6 +313,8 @@ def attend_gqa_step(cache: GqaCache, step: GqaStep, q, sm_scale, window=0, sinks
                     selected=False, stream=None):
     """Attention of the step's tokens (``q`` [T, Hq, D]) over all that they see, a window, or the
     blocks of ``select_blocks_step``, into ``step.out``, ``step.lse``."""
+    if selected:
+        _selects(step)
     ops.dsa_gqa_attend(q, cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale,
                        cache.block_table, cache.seq_lens, step.cu_new, window, sinks, sm_scale,
                        step.out, step.lse, step.ws, step.block_ids if selected else None,

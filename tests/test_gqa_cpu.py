@@ -1,6 +1,7 @@
 """The grouped-query entry points refuse what they cannot do, on the host, before any CUDA call;
 and the tests' plain forms on hand-worked values."""
 import ctypes
+import dataclasses
 import math
 import os
 import re
@@ -9,7 +10,7 @@ import subprocess
 import pytest
 import torch
 
-from sparse_attention_indexer_kpool_gb300 import _lib, build
+from sparse_attention_indexer_kpool_gb300 import _lib, build, pipeline
 from tests import _gqa_ref as ref
 from tests.test_abi_cpu import A, ERR, header_define
 
@@ -269,3 +270,14 @@ def test_the_bound_of_the_bf16_path_is_that_of_fp16_weights():
             out = ref.weights_rounded_to(dtype, z, v, s).to(torch.bfloat16).double()
             fails[dtype] = int(((out - want).abs() > tol).sum())
         assert fails[torch.float16] == 0 and fails[torch.bfloat16] > 0, (n, fails)
+
+
+def test_a_step_without_a_selection_is_not_attended_to_densely():
+    """Selected blocks asked of a step that was allocated without a selection: refused, not
+    answered with attention over everything."""
+    kw = {f.name: None for f in dataclasses.fields(pipeline.GqaStep)}
+    step = pipeline.GqaStep(**kw)
+    with pytest.raises(ValueError, match="select_k"):
+        pipeline.attend_gqa_step(None, step, None, 0.1, selected=True)
+    with pytest.raises(ValueError, match="select_k"):
+        pipeline.select_blocks_step(None, step, None, 0.1)
