@@ -457,7 +457,7 @@ typedef struct dsa_gqa_kv {
  * k_mean of its page is the mean of its page_size stored keys, rounded to nearest.
  * Rows of a block behind the last new token keep their codes (the first token of a
  * block sets its scale alone, whatever the page held).  Two blocks of a step on the same
- * page leave it with codes and scale of either.
+ * page leave there a mixture of both: codes of either, and either's scale.
  */
 int dsa_gqa_append(const void* k_new, const void* v_new, const int32_t* cu_new, int T, int B,
                    int dtype, const dsa_gqa_kv* kv, void* k_mean, int32_t* status_dev,
@@ -487,7 +487,8 @@ int dsa_gqa_read(const dsa_gqa_kv* kv, const int32_t* cu_out, const int32_t* beg
  * Blocks j <= p / page_size with j < sink_blocks or j > p / page_size - local_blocks get
  * +inf (local_blocks >= 1: the token's own block is one of them), every other one
  * -inf, so that dsa_topk_pools over the [T * Hkv, NB] scores takes the former first, in
- * the order of their numbers, and never the latter.  The pages' own scores (module
+ * the order of their numbers, and never the latter (with a select_k below sink_blocks +
+ * local_blocks the nearest blocks are not among them).  The pages' own scores (module
  * glm5next_dsa::tp, "Why the indexer is REPLICATED") are a sum over heads as well.
  *
  *   q [T, Hq, D] activation dtype;  k_mean as dsa_gqa_append leaves it

@@ -183,7 +183,10 @@ int launch_gqa_attend(const GqaArgs& a, void* workspace, cudaStream_t stream) {
     //   16 on 8,000: 4 tokens 150 / 131, 8 153 / 235, 32 180 / 856
     //   16 on 64: 4 tokens 18.8 / 21.2, 8 18.9 / 24.9, 64 30.6 / 72.5
     //   16 on 8,000 with one query head a KV head, 2 of them: 4 tokens 53.5 / 39.8, 8 53.9 / 77
-    // and a few short rows, however many a sequence has, by a cluster each (gqa_split.cu).
+    // and a few short rows, however many a sequence has, by a cluster each (gqa_split.cu).  The
+    // sequences of each of these have as many tokens as one another.  The host knows the average
+    // alone: a prompt beside so many decode tokens that it is below eight goes the way of those,
+    // and reads its keys anew for each token (16 x 32 tokens on 8,000: 856 us for 180).
     if (a.block_ids || a.T < 8ll * a.B) return launch_gqa_split(a, workspace, stream);
     const int rc = launch_gqa_split(a, workspace, stream, true);
     return rc == kElsewhere ? launch_gqa_chunk(a, workspace, stream) : rc;

@@ -20,8 +20,9 @@
 // them with one or two rounds of loads by all its threads (a binary search's dependent loads
 // were half of a decode step's 7.9 us).
 // What bounds it: memory in a chunk (65,000 tokens of 8 heads of 128 in bf16 72 us, 5.5 TB/s),
-// round trips to memory (cu_new, the lengths, the table, then rows and scale) in a decode step
-// (64 tokens 6.2 us, 8.1 with cold caches).
+// round trips to memory in a decode step: cu_new, the lengths, the table, then rows and scale
+// (64 sequences with a token each 2.9 us, 3.2 with cold caches) and, where a block becomes
+// complete, its keys for the mean (6.2 to 6.9, 7.1 to 8.5): among 64 tokens one mostly does.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -617,8 +618,8 @@ template <typename T>
 int append(const void* k_new, const void* v_new, const int32_t* cu_new, int n_t, int B,
            const GqaKv& kv, void* k_mean, int32_t* status, cudaStream_t stream) {
   // A warp a token's block where that is no more of them than of blocks, in us, of 64 sequences
-  // with 1 / 2 / 3 / 8 tokens each (8 heads of 128, pages of 64): 2.9 / 3.2 / 5.0 / 6.2, a CTA
-  // a block 5.5 / 5.6 / 5.7 / 5.8.  Elements kept in registers where they fit, of 64 sequences
+  // with 1 / 2 / 3 / 8 tokens each (8 heads of 128, pages of 64, no block becomes complete): 2.9 /
+  // 3.2 / 5.0 / 6.2, a CTA a block 5.5 / 5.6 / 5.7 / 5.8.  Elements kept in registers where they fit, of 64 sequences
   // with 8 / 128 / 512 tokens: 5.8 / 13.4 / 41, read twice 5.3 / 23.8 / 74.
   const int slots = n_t / kv.page_size + 2 * B;
   const bool few = n_t <= slots, block = kv.page_size * kv.D <= 64 * kThreads;

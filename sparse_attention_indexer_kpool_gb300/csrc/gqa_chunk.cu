@@ -28,10 +28,10 @@
 // they make NaN.
 //
 // Measured (head dim 128, join included): 2,048 tokens behind 14,336 keys, 4 KV heads of 16 query
-// heads, 969 us, 1.06 PFLOP/s.  A tile of A and B takes 3,950 clocks: the products 2,064, a
-// softmax 1,900 (a row's 128 exponentials, its thread's alone) and handing S and W over, of which
-// the two row tiles cover one another's half.  16 sequences of 1 to 250 tokens, window 1,024, 8 KV
-// heads of 4, 87 us: ten tiles an item do not hide its start and end (rows in, first reference,
+// heads, 973 us, 1.06 PFLOP/s.  A tile of A and B took 3,950 clocks in a trace of a form that
+// needed 996 us: the products 2,064, a softmax 1,900 (a row's 128 exponentials, its thread's
+// alone) and handing S and W over, of which the two row tiles cover one another's half.  16 sequences of 1 to 250 tokens, window 1,024, 8 KV
+// heads of 4, 85 us: ten tiles an item do not hide its start and end (rows in, first reference,
 // rows out: 14,000 clocks), and an item of up to 32 tokens has no B to run under.
 #include "gqa.cuh"
 #include "gqa_join.cuh"

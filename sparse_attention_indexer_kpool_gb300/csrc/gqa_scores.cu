@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(kThreads) gqa_scores_kernel(GqaScoreArgs a) {
 // the end of the first pass do lanes (and warps, and CTAs) exchange them.
 // The warps of a cluster's CTAs share the blocks of one token, so that many SMs
 // read one long context's means.  Bound by round trips to the table and the means: four tokens on
-// 262,144 keys (8 KV heads of 8 query heads of 128) 10.3 us, 15 with cold caches, where the
-// means' 34 MB take 5.
+// 262,144 keys (8 KV heads of 8 query heads of 128) 9.5 us, 13.8 with cold caches, where the
+// means' 34 MB take 5; with 16 query heads a KV head 10.7.
 constexpr int kPadG = 32;            // heads of a group, at most
 struct GroupArgs {
   GqaScoreArgs a;
@@ -455,10 +455,12 @@ int launch_groups(const GqaScoreArgs& a, cudaStream_t stream) {
   while (ga.pad < G) ga.pad *= 2;
   const long long rows = (long long)a.T * a.Hkv;
   // Tokens together (128 columns a CTA) or a CTA (or several) for each, tables of 48 / 470 blocks,
-  // in us, 8 query heads a KV head: 256 rows (tokens x KV heads) 7.9 / 17.7 and 7.4 / 10.4, 512
-  // rows 8.0 / 17.5 and 12.6 / 18.4, 1,024 rows 7.9 / 17.7 and 22.9 / 34.5, 4,096 rows 9.9 / 22.7
-  // and 76 / 116; 512 rows of sequences with one token each 16.7 / 38.3 and 13.6 / 19.6, with two
-  // (1,024 rows) 17.0 / 39.1 and 25.2 / 36.8.
+  // in us, 8 query heads a KV head: 256 rows (tokens x KV heads) 7.6 / 17.3 and 5.9 / 9.0, 512
+  // rows 7.4 / 17.1 and 10.5 / 16.7, 1,024 rows 7.5 / 17.4 and 19.4 / 31.6, 4,096 rows 9.5 / 21.9
+  // and 66 / 108; 512 rows of sequences with one token each 16.3 / 38.5 and 11.7 / 17.8, with two
+  // (1,024 rows) 16.6 / 39.5 and 21.7 / 33.9.  With 16 query heads a KV head 256 rows 7.1 / 16.1
+  // and 6.4 / 10.2, 512 rows 7.1 / 16.3 and 11.1 / 18.7.  (Equal lengths throughout; T is what the
+  // step has room for, and its sequences may differ: the host knows neither.)
   if (rows >= 3ll * num_sms() && a.T >= 2ll * a.B) return launch_gqa_scores_chunk(a, stream);
   // otherwise CTAs for a token until there is one an SM, each with 64 blocks at least
   int splits = 1;

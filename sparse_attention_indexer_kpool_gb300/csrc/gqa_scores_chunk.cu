@@ -14,7 +14,7 @@
 // the last to the first: the last two are still in shared memory.
 //
 // The products of step u + 1 run while step u's numbers are taken, and step u + 2's means are on
-// their way; two CTAs an SM.  2,048 tokens of 64 query heads on 16,384 keys (256 blocks): 44 us
+// their way; two CTAs an SM.  2,048 tokens of 64 query heads on 16,384 keys (256 blocks): 45 us
 // (mma.sync products of 16 x 8, which read each mean again for every 16 columns: 86 us).  The
 // bytes of the scores and the queries take 6 us, the exponentials (two for each column and block,
 // 36 a clock and SM) 6 us: what is left is the instructions around them, by 16 warps an SM, and

@@ -32,8 +32,9 @@
 // Measured (head dim 128, join included): 64 tokens on 4,096 to 16,000 keys, 8 KV heads of 8 query
 // heads, 212 us: 6.2 TB/s, memory-bound (the join is 8 of them).  1,024 tokens on 32 blocks of
 // 64 each, 4 KV heads of 16 query heads, 318 us: 2.1 GB of codes out of L2 at 6.7 TB/s, two warps
-// a scheduler, so that an instruction's latency shows.  One token on 256 keys,
-// 8 x 8 heads, 10.4 us: start, lengths, table, scales, one or two tiles, the cluster's exchange.
+// a scheduler, so that an instruction's latency shows.  One token on 256 keys, 8 x 8 heads, 10.4
+// us: start, lengths, table, scales, one or two tiles, the cluster's exchange (under a table of 17
+// blocks; under one of 4,096, whose width the host takes for the keys, shares and a join: 15).
 #include <cooperative_groups.h>
 
 #include "gqa.cuh"

@@ -276,7 +276,8 @@ class GqaStep:
             lse=torch.zeros(T, Hq, dtype=torch.float32, device=dev),
             ws=torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None, status=i32(1))
         if select_k:
-            # rows behind the last token keep what is here: they select nothing
+            # (rows behind the last token keep the scores of an earlier step, or these; their
+            # block_ids follow them, and the attention does not look at either)
             step.scores = torch.full((T, Hkv, width), float("-inf"), device=dev)
             step.block_ids = i32(T, Hkv, select_k)
             ws_t = ops.topk_workspace_bytes(T * Hkv, width, select_k)
@@ -299,7 +300,8 @@ def _selects(step: GqaStep):
 def select_blocks_step(cache: GqaCache, step: GqaStep, q, sm_scale, sink_blocks=1, local_blocks=1,
                        stream=None):
     """``step.block_ids``: the blocks that each of the step's tokens (``q`` [T, Hq, D]) attends
-    to, for each KV head."""
+    to, for each KV head; ``select_k`` of the step should not be below ``sink_blocks`` +
+    ``local_blocks``, or the nearest ones are left out."""
     _selects(step)
     ops.dsa_gqa_block_scores(q, cache.k_mean, cache.block_table, cache.seq_lens, cache.page_size,
                              step.cu_new, sink_blocks, local_blocks, sm_scale, step.scores,
