@@ -525,7 +525,8 @@ int dsa_gqa_block_scores(const void* q, const void* k_mean, const int32_t* block
  * Outputs are deterministic.  bf16 with D 64 or 128 runs on the tensor cores: codes are
  * exact there, a query element keeps its 8 bits down to 2^-28 of its row's largest, a
  * weight is rounded to 11 bits and counts down to 2^-27 of its row's largest; logits,
- * sums and outputs are fp32, and so is everything of the other types and sizes.
+ * sums and outputs are fp32, and so is everything of the other types and sizes.  There a
+ * logit is held together with its value's scale: to 2^-24 of the exponent of that, too.
  * Device faults: also DSA_DEV_TIMEOUT (outputs unspecified).
  */
 int dsa_gqa_attend(const void* q, const dsa_gqa_kv* kv, const int32_t* cu_new,

@@ -619,8 +619,8 @@ int append(const void* k_new, const void* v_new, const int32_t* cu_new, int n_t,
            const GqaKv& kv, void* k_mean, int32_t* status, cudaStream_t stream) {
   // A warp a token's block where that is no more of them than of blocks, in us, of 64 sequences
   // with 1 / 2 / 3 / 8 tokens each (8 heads of 128, pages of 64, no block becomes complete): 2.9 /
-  // 3.2 / 5.0 / 6.2, a CTA a block 5.5 / 5.6 / 5.7 / 5.8.  Elements kept in registers where they fit, of 64 sequences
-  // with 8 / 128 / 512 tokens: 5.8 / 13.4 / 41, read twice 5.3 / 23.8 / 74.
+  // 3.2 / 5.0 / 6.2, a CTA a block 5.5 / 5.6 / 5.7 / 5.8.  Elements kept in registers where they
+  // fit, of 64 sequences with 8 / 128 / 512 tokens: 5.8 / 13.4 / 41, read twice 5.3 / 23.8 / 74.
   const int slots = n_t / kv.page_size + 2 * B;
   const bool few = n_t <= slots, block = kv.page_size * kv.D <= 64 * kThreads;
   const dim3 grid = few ? dim3((unsigned)n_t, (unsigned)(2 * kv.Hkv + 7) / 8, 1)

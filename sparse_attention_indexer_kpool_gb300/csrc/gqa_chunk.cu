@@ -30,9 +30,10 @@
 // Measured (head dim 128, join included): 2,048 tokens behind 14,336 keys, 4 KV heads of 16 query
 // heads, 973 us, 1.06 PFLOP/s.  A tile of A and B took 3,950 clocks in a trace of a form that
 // needed 996 us: the products 2,064, a softmax 1,900 (a row's 128 exponentials, its thread's
-// alone) and handing S and W over, of which the two row tiles cover one another's half.  16 sequences of 1 to 250 tokens, window 1,024, 8 KV
-// heads of 4, 85 us: ten tiles an item do not hide its start and end (rows in, first reference,
-// rows out: 14,000 clocks), and an item of up to 32 tokens has no B to run under.
+// alone) and handing S and W over, of which the two row tiles cover one another's half.  16
+// sequences of 1 to 250 tokens, window 1,024, 8 KV heads of 4, 85 us: ten tiles an item do not hide
+// its start and end (rows in, first reference, rows out: 14,000 clocks), and an item of up to 32
+// tokens has no B to run under.
 #include "gqa.cuh"
 #include "gqa_join.cuh"
 #include "mla_chunk.cuh"
@@ -65,7 +66,7 @@ constexpr int kPairCost = 4, kSingleCost = 3, kExtra = 12;
 struct Params {
   GqaArgs a;
   int G, per;          // query heads of a KV head; tokens of a row tile
-  float zscale;        // softmax scale in base 2, times 2^-14 (see Meta)
+  float zscale;        // softmax scale in base 2
   int cap;             // positions that the block table has room for
   int box_log;         // keys of a TMA box
   float* part_o;       // [2 CTAs][2 kRows][D]
@@ -175,8 +176,9 @@ struct Walk {
 
 struct Meta {          // of a key tile, by 16 keys
   alignas(16) int pos[kGroups];  // first position (0x7fffffff: none)
-  alignas(16) float ks[kGroups];  // keys' scale times the softmax scale's size and 2^-14: what is
-                       // left to a row is the power of two of its largest element, a normal number
+  // keys' scale times 2^-14 times the softmax scale's size: what is left to a row is the power of
+  // two of its largest element, always a normal number
+  alignas(16) float ks[kGroups];
   alignas(16) int ev[kGroups];    // exponent of the values' scale
   int row[kGroups];    // first cache row
   uint32_t nan[4];     // keys whose NaN values were taken out of the tile
@@ -987,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ev = 0;
         if (row >= 0) {
           const int unit = row / kv.page_size;
-          ks = __ldg(kv.k_scale + unit) * fabsf(p.zscale);
+          ks = __ldg(kv.k_scale + unit) * 0x1p-14f * fabsf(p.zscale);
           ev = exponent_of(__ldg(kv.v_scale + unit));
         }
         int next_pos, next_row;
@@ -1140,7 +1142,7 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream) {
   p.a = a;
   p.G = a.Hq / a.kv.Hkv;
   p.per = kRows / p.G;
-  p.zscale = a.sm_scale * kLog2e * 0x1p-14f;
+  p.zscale = a.sm_scale * kLog2e;
   p.cap = table_cap(a.kv.max_pages, a.kv.page_size);
   p.box_log = chunk::box_log_of(a.kv.page_size);
   p.part_o = static_cast<float*>(workspace);

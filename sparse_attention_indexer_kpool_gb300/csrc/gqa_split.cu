@@ -69,7 +69,7 @@ constexpr int kRingBytes = 2 * 2 * kKeys * 128;  // of a warp
 struct Params {
   GqaArgs a;
   int G, hb;                 // query heads of a KV head, row tiles of those
-  float zscale;              // softmax scale in base 2, times 2^-14 (see Meta)
+  float zscale;              // softmax scale in base 2
   int cap;                   // positions that the block table has room for
   int per_block;             // boxes of a block
   float* part_o;             // [2 workers][8 kN][D]
@@ -340,8 +340,8 @@ __device__ __forceinline__ float across_keys(float v) {
 }
 struct Meta {          // of a tile in the ring, by box
   int pos[2];          // first position (0x7fffffff: no such box)
-  float ks[2];         // keys' scale times the softmax scale and 2^-14: what is left to a query row is
-                       // the power of two of its largest element, a normal number whatever that is
+  float ks[2];         // keys' scale times 2^-14 times the softmax scale: what is left to a query
+                       // row is the power of two of its largest element, always a normal number
   int ev[2];           // exponent of the values' scale
 };
 template <int kStages>
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int unit = page * kv.Hkv + wl.h;
       row[i] = unit * kv.page_size + ((int)at - blk * kv.page_size);
       bpos[i] = (int)at;
-      bks[i] = __ldg(kv.k_scale + unit) * p.zscale;
+      bks[i] = __ldg(kv.k_scale + unit) * 0x1p-14f * p.zscale;
       bev[i] = exponent_of(__ldg(kv.v_scale + unit));
     }
   };
@@ -916,8 +916,8 @@ struct Rows {
   }
 };
 
-// Clusters of `ctas` CTAs (one an SM) that the device holds at once; asked once for each kernel (all
-// of them have one type), device and size.
+// Clusters of `ctas` CTAs (one an SM) that the device holds at once; asked once for each kernel
+// (all of them have one type), device and size.
 template <auto kKernel>
 int clusters_of(size_t bytes, int ctas) {
   static std::atomic<int> held[64][4];
@@ -945,7 +945,7 @@ int launch(const GqaArgs& a, void* workspace, cudaStream_t stream, bool together
   p.a = a;
   p.G = a.Hq / a.kv.Hkv;
   p.hb = (p.G + 8 * kN - 1) / (8 * kN);
-  p.zscale = a.sm_scale * kLog2e * 0x1p-14f;
+  p.zscale = a.sm_scale * kLog2e;
   p.cap = table_cap(a.kv.max_pages, a.kv.page_size);
   p.per_block = a.kv.page_size / kR;
   p.drill = failure_drill();

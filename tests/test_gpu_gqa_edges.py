@@ -1,6 +1,6 @@
-"""Edges of the grouped-query calls on the GPU: boundaries, lengths, scales and logits at the ends of
-their ranges, what a weight's rounding may cost, more rows than a grid has in y, and waits that run
-out."""
+"""Edges of the grouped-query calls on the GPU: boundaries, lengths, scales and logits at the ends
+of their ranges, what a weight's rounding may cost, more rows than a grid has in y, and waits that
+run out."""
 import math
 
 import math
@@ -280,3 +280,14 @@ def test_weights_have_eleven_bits(lens, new, width, K, D):
     tol = ref.bound_of_bf16(want, mass, top, big, n, D)
     assert bool(((out.double() - want).abs() <= tol).all())
     compare(c, q, sm, out, lse, BF, ids=ids)
+
+
+@pytest.mark.parametrize("lens,new,width,K,dtype", PLACES)
+@pytest.mark.parametrize("e_q,e_k,sm", [(62, 50, 2.0 ** -125), (-64, -50, 2.0 ** 107)])
+def test_attend_softmax_scales_near_the_ends(lens, new, width, K, dtype, e_q, e_k, sm):
+    """Logits of ordinary size by a softmax scale next to fp32's least normal number, or a huge
+    one."""
+    c = Case(93 + K, lens, new, 2, 16, 128, width=width)
+    c.scale["k"] = torch.where(torch.isnan(c.scale["k"]), c.scale["k"], 2.0 ** e_k)
+    q = (c.normal(c.T, 16, 128, dtype=F32) * 2.0 ** e_q).to(dtype)
+    check_in_place(c, q, sm, K, dtype)

@@ -238,8 +238,9 @@ def test_topk_takes_the_rows_of_a_long_prompt(lib):
     """T * Hkv rows of block scores: more than a grid has in y.  (Refused for its pointer, which is
     looked at behind the sizes: nothing is launched.)"""
     n = lib.dsa_kernel_launches()
+    bad = ERR["DSA_ERR_INVALID_ARG"]
     for rows in (65_536, 8 * 65_536, 2 ** 31 - 1):
-        assert lib.dsa_topk_pools(None, rows, 64, 32, A, None, 0, None) == ERR["DSA_ERR_INVALID_ARG"]
+        assert lib.dsa_topk_pools(None, rows, 64, 32, A, None, 0, None) == bad
         assert lib.dsa_topk_pools_workspace_size(rows, 64, 32) == 0
     assert lib.dsa_kernel_launches() == n
 
